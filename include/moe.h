@@ -56,7 +56,8 @@ typedef enum {
   MOE_ERR_DEVICE_ROUTE = 5, /* device flag: a route index outside [0, E) */
   MOE_ERR_TIMEOUT = 6,      /* device flag: a bounded pipeline wait ran out */
   MOE_ERR_ROWS = 7,         /* device flag: group rows exceed the stated bound */
-  MOE_ERR_GATHER = 8        /* device flag: a row_token entry outside [0, T) */
+  MOE_ERR_GATHER = 8,       /* device flag: a row_token entry outside [0, T) */
+  MOE_ERR_TARGET = 9        /* device flag: a target outside [0, vocab) (moe_train.h) */
 } moe_status;
 
 typedef enum { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
@@ -361,8 +362,9 @@ moe_status moe_workspace_init(void *ws, void *stream);
 
 /* Synchronise `stream`, then read and clear the device status word of `ws`:
  * MOE_OK, or the first of MOE_ERR_DEVICE_ROUTE / MOE_ERR_ROWS /
- * MOE_ERR_TIMEOUT / MOE_ERR_GATHER that is set (*bits, if non-NULL, receives
- * every bit: 1 route, 2 rows, 4 timeout, 8 gather). */
+ * MOE_ERR_TIMEOUT / MOE_ERR_GATHER / MOE_ERR_TARGET that is set (*bits, if
+ * non-NULL, receives every bit: 1 route, 2 rows, 4 timeout, 8 gather, 16
+ * target). */
 moe_status moe_get_device_status(void *ws, void *stream, uint32_t *bits);
 
 /* Synchronise `stream`, then read and clear the workspace's count of tokens

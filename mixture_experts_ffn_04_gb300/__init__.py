@@ -25,6 +25,7 @@ LIB_PATH = os.path.join(_HERE, "libmoe.so")
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE = 0, 1, 2, 3
 MOE_ERR_CUDA, MOE_ERR_DEVICE_ROUTE, MOE_ERR_TIMEOUT, MOE_ERR_ROWS = 4, 5, 6, 7
 MOE_ERR_GATHER = 8
+MOE_ERR_TARGET = 9
 MOE_F32, MOE_BF16 = 0, 1
 STAGES = ("residual_setup", "route", "permute", "gate_up", "down", "shared", "combine")
 
@@ -64,6 +65,13 @@ class MoEBackwardInfo(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("fc1", "grad_fc2", "d_fc1", "dx_perm")]
 
 
+class MoECeShape(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("hidden", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("reduction", ctypes.c_int32),
+                ("ignore_index", ctypes.c_int32), ("x_stride", ctypes.c_int64),
+                ("w_stride", ctypes.c_int64)]
+
+
 class MoERouteInfo(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "topk_idx", "topk_w", "gate", "counts", "offsets", "scatter_index", "row_token",
@@ -84,6 +92,7 @@ def lib():
     L = ctypes.CDLL(LIB_PATH)
     P, S, i32, i64, u32, sz = (ctypes.c_void_p, ctypes.POINTER(MoEShape), ctypes.c_int32,
                                ctypes.c_int64, ctypes.c_uint32, ctypes.c_size_t)
+    C = ctypes.POINTER(MoECeShape)
     sig = {
         "moe_topk_pack": (u32, [i32, i32]),
         "moe_topk_unpack": (i32, [u32, ctypes.POINTER(i32), ctypes.POINTER(i32)]),
@@ -125,6 +134,10 @@ def lib():
         "moe_gather_grad": (i32, [S, P, P, P, P, P]),
         "moe_layer_backward": (i32, [S, ctypes.POINTER(MoEWeights), P, P, P,
                                      ctypes.POINTER(MoEExpertGrads), P, sz, P]),
+        # training operators (moe_train.h)
+        "moe_linear_ce_workspace_bytes": (sz, [C]),
+        "moe_linear_ce_forward": (i32, [C, P, P, P, P, P, P, P, sz, P]),
+        "moe_linear_ce_backward": (i32, [C, P, P, P, P, P, P, P, P, sz, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -464,6 +477,62 @@ def grads_for(dw_gate, dw_up, dw_down) -> MoEExpertGrads:
 
 
 # ---------------------------------------------------------------------------
+# training operators (moe_train.h), name for name
+# ---------------------------------------------------------------------------
+MOE_CE_NONE, MOE_CE_SUM, MOE_CE_MEAN = 0, 1, 2
+
+
+def _rows(t: torch.Tensor, rows: int, cols: int, dtype, name: str):
+    """Address and row stride of a [rows, cols] matrix whose rows are contiguous."""
+    if tuple(t.shape) != (rows, cols) or t.dtype != dtype:
+        raise ValueError("%s must be [%d, %d] %s, got %s %s" % (name, rows, cols, dtype,
+                                                                tuple(t.shape), t.dtype))
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError("the rows of %s must be contiguous" % name)
+    return t.data_ptr(), (t.stride(0) if rows > 1 else cols)
+
+
+def _vec(t: torch.Tensor, n: int, dtype, name: str):
+    if t.numel() != n or t.dtype != dtype:
+        raise ValueError("%s must hold %d elements of %s, got %s %s" % (name, n, dtype,
+                                                                        tuple(t.shape), t.dtype))
+    return _p(t)
+
+
+def moe_linear_ce_workspace_bytes(shape: MoECeShape) -> int:
+    return int(lib().moe_linear_ce_workspace_bytes(ctypes.byref(shape)))
+
+
+def moe_linear_ce_forward(shape: MoECeShape, x, w, target, loss, lse, total, ws, stream=None):
+    """x and w may be rows of wider buffers (the strides go into the shape)."""
+    dt = torch.float32 if shape.dtype == MOE_F32 else torch.bfloat16
+    xp, shape.x_stride = _rows(x, shape.tokens, shape.hidden, dt, "x")
+    wp, shape.w_stride = _rows(w, shape.vocab, shape.hidden, dt, "w")
+    f32, T = torch.float32, shape.tokens
+    _check(lib().moe_linear_ce_forward(
+        ctypes.byref(shape), xp, wp, _vec(target, T, torch.int32, "target"),
+        None if loss is None else _vec(loss, T, f32, "loss"),
+        None if lse is None else _vec(lse, T, f32, "lse"),
+        None if total is None else _vec(total, 1, f32, "total"), _p(ws), _nbytes(ws),
+        _stream(stream)), "moe_linear_ce_forward")
+
+
+def moe_linear_ce_backward(shape: MoECeShape, x, w, target, lse, dloss, dx, dw, ws, stream=None):
+    dt = torch.float32 if shape.dtype == MOE_F32 else torch.bfloat16
+    T, H, V = shape.tokens, shape.hidden, shape.vocab
+    xp, shape.x_stride = _rows(x, T, H, dt, "x")
+    wp, shape.w_stride = _rows(w, V, H, dt, "w")
+    n = T if shape.reduction == MOE_CE_NONE else 1
+    _check(lib().moe_linear_ce_backward(
+        ctypes.byref(shape), xp, wp, _vec(target, T, torch.int32, "target"),
+        _vec(lse, T, torch.float32, "lse"),
+        None if dloss is None else _vec(dloss, n, torch.float32, "dloss"),
+        None if dx is None else _vec(dx, T * H, dt, "dx"),
+        None if dw is None else _vec(dw, V * H, dt, "dw"), _p(ws), _nbytes(ws),
+        _stream(stream)), "moe_linear_ce_backward")
+
+
+# ---------------------------------------------------------------------------
 # conveniences over the ABI (allocation through torch, nothing else)
 # ---------------------------------------------------------------------------
 def shape_for(wl, T: Optional[int] = None) -> MoEShape:
@@ -536,6 +605,56 @@ class MoELayer:
 
     def views(self):
         return moe_workspace_views(self.shape, self.ws)
+
+    def device_status(self, stream=None):
+        return moe_get_device_status(self.ws, stream)
+
+
+def _alloc_ws(n: int, device, stream, where: str):
+    if n == 0:
+        raise MoEError(MOE_ERR_INVALID_ARG, where, "invalid shape")
+    ws = torch.empty(n + 256, dtype=torch.uint8, device=device)
+    off = (-ws.data_ptr()) % 256
+    ws = ws[off: off + n]
+    moe_workspace_init(ws, stream)
+    return ws
+
+
+class LinearCrossEntropy:
+    """Softmax cross entropy of x . w^T against target over a vocabulary, and its
+    gradients, without the [tokens, vocab] logits: shape and a workspace over
+    caller tensors.  reduction: "none", "sum" or "mean" (over the tokens whose
+    target is not ignore_index)."""
+
+    def __init__(self, tokens: int, hidden: int, vocab: int, dtype=torch.bfloat16,
+                 reduction: str = "mean", ignore_index: int = -100, device="cuda"):
+        s = MoECeShape()
+        s.tokens, s.hidden, s.vocab, s.dtype = tokens, hidden, vocab, _dtype_code(dtype)
+        s.reduction = {"none": MOE_CE_NONE, "sum": MOE_CE_SUM, "mean": MOE_CE_MEAN}[reduction]
+        s.ignore_index = ignore_index
+        self.shape, self.dtype = s, dtype
+        self.ws = _alloc_ws(moe_linear_ce_workspace_bytes(s), device, None, "LinearCrossEntropy")
+        self.lse = torch.zeros(tokens, dtype=torch.float32, device=device)
+
+    def forward(self, x, w, target, loss=None, total=None, stream=None):
+        """The losses [tokens] ("none") or the reduced loss [1]; self.lse is
+        what the backward needs."""
+        none = self.shape.reduction == MOE_CE_NONE
+        if none and loss is None:
+            loss = torch.empty(self.shape.tokens, dtype=torch.float32, device=x.device)
+        if not none and total is None:
+            total = torch.empty(1, dtype=torch.float32, device=x.device)
+        moe_linear_ce_forward(self.shape, x, w, target, loss, self.lse, total, self.ws, stream)
+        return loss if none else total
+
+    def backward(self, x, w, target, dloss=None, dx=None, dw=None, stream=None):
+        """(dx, dw) after a forward with the same x, w and target."""
+        if dx is None:
+            dx = torch.empty(tuple(x.shape), dtype=x.dtype, device=x.device)
+        if dw is None:
+            dw = torch.empty(tuple(w.shape), dtype=w.dtype, device=w.device)
+        moe_linear_ce_backward(self.shape, x, w, target, self.lse, dloss, dx, dw, self.ws, stream)
+        return dx, dw
 
     def device_status(self, stream=None):
         return moe_get_device_status(self.ws, stream)

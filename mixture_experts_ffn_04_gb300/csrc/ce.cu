@@ -1,0 +1,556 @@
+// ce.cu -- softmax cross entropy of a linear classifier over a vocabulary, and
+// its gradient, without the [tokens, vocab] logits (include/moe_train.h).
+//
+//   z = x W^T,  lse_t = log sum_v exp z_tv,  loss_t = lse_t - z_t,target
+//   d = g (softmax(z) - onehot(target)),  dx = d W,  dW = d^T x
+//
+// The tokens that count are packed into a dense matrix first (one pass over x,
+// small against W and the products), so ignored tokens cost nothing and what
+// their rows hold reaches no sum.  Forward: one GEMM over all of W whose
+// epilogue keeps, per row and 128 columns, a maximum and a sum of exponentials,
+// and a kernel that merges them.  Backward: pieces of the vocabulary; per piece
+// the logits again with d in the epilogue (kept for the piece only), then both
+// gradient products in one launch.  8 T H V flops for loss and gradient, of
+// which 2 T H V recompute the logits.
+#include <algorithm>
+
+#include "../../include/moe_train.h"
+#include "common.cuh"
+#include "internal.h"
+#include "train.h"
+
+namespace moe {
+namespace {
+
+constexpr int64_t kDlogitBytes = 256ll << 20;   // logit gradient of one piece
+constexpr int64_t kPlaneBytes = 512ll << 20;    // bf16 planes of one piece of an fp32 W
+
+struct CeShape {
+  int64_t T, x_ld, w_ld;
+  int H, V, dtype, reduction, ignore, esize, planes;
+};
+
+moe_status decode_ce(const moe_ce_shape* s, CeShape* o, const char** why) {
+  if (!s) { *why = "shape is NULL"; return MOE_ERR_INVALID_ARG; }
+  if (s->dtype != MOE_F32 && s->dtype != MOE_BF16) {
+    *why = "dtype must be MOE_F32 or MOE_BF16";
+    return MOE_ERR_UNSUPPORTED;
+  }
+  if (s->tokens < 0 || s->tokens > (1ll << 28)) {
+    *why = "tokens must be in [0, 2^28]";
+    return MOE_ERR_INVALID_ARG;
+  }
+  if (s->hidden <= 0 || s->hidden % 8) {
+    *why = "hidden must be a positive multiple of 8";
+    return MOE_ERR_INVALID_ARG;
+  }
+  if (s->vocab < 1 || s->vocab > (1 << 30)) {
+    *why = "vocab must be in [1, 2^30]";
+    return MOE_ERR_INVALID_ARG;
+  }
+  if (s->reduction < MOE_CE_NONE || s->reduction > MOE_CE_MEAN) {
+    *why = "reduction must be MOE_CE_NONE, MOE_CE_SUM or MOE_CE_MEAN";
+    return MOE_ERR_INVALID_ARG;
+  }
+  o->x_ld = s->x_stride ? s->x_stride : s->hidden;
+  o->w_ld = s->w_stride ? s->w_stride : s->hidden;
+  if (o->x_ld < s->hidden || o->x_ld % 8 || o->w_ld < s->hidden || o->w_ld % 8 ||
+      o->x_ld >= (1ll << 32) || o->w_ld >= (1ll << 32)) {
+    *why = "x_stride and w_stride must be 0 or at least hidden, and multiples of 8";
+    return MOE_ERR_INVALID_ARG;
+  }
+  o->T = s->tokens;
+  o->H = s->hidden;
+  o->V = s->vocab;
+  o->dtype = s->dtype;
+  o->reduction = s->reduction;
+  o->ignore = s->ignore_index;
+  o->esize = s->dtype == MOE_F32 ? 4 : 2;
+  o->planes = s->dtype == MOE_F32 ? kPlanesF32 : 1;
+  return MOE_OK;
+}
+
+struct CeLayout {
+  int64_t rows_pad, piece, npieces;   // vocabulary columns of a piece
+  int64_t nctr;
+  LinearSplit split;
+  bool dx_direct, dw_direct;
+  size_t flags, meta, ctr, rowmap, inv, tgt, g, lse, zt, loss, xc, wpl, stats, d, dx_part, dw_part, total;
+};
+
+CeLayout layout_ce(const CeShape& s) {
+  CeLayout L;
+  L.rows_pad = std::max<int64_t>(256, (s.T + 255) / 256 * 256);
+  const int64_t vpad = ((int64_t)s.V + 255) / 256 * 256;
+  int64_t piece = kDlogitBytes / (L.rows_pad * 2 * s.planes) / 256 * 256;
+  if (s.planes > 1) piece = std::min(piece, kPlaneBytes / ((int64_t)s.H * 2 * s.planes) / 256 * 256);
+  piece = std::max<int64_t>(piece, 256);
+  L.npieces = (vpad + piece - 1) / piece;
+  // pieces of equal size
+  L.piece = ((vpad + L.npieces - 1) / L.npieces + 255) / 256 * 256;
+  L.npieces = (vpad + L.piece - 1) / L.piece;
+  L.split = linear_grad_split(s.T, L.piece, s.H, s.planes);
+  L.dx_direct = L.npieces == 1 && L.split.dx == 1;
+  L.dw_direct = L.split.dw == 1;
+  L.nctr = 2 * L.npieces;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += (bytes + 255) & ~(size_t)255;
+    return at;
+  };
+  const size_t T = (size_t)L.rows_pad;
+  L.flags = take(256);
+  L.meta = take(256);   // rows that count, the merge's ticket
+  L.ctr = take((size_t)L.nctr * 4);
+  L.rowmap = take(T * 4);
+  L.inv = take(T * 4);
+  L.tgt = take(T * 4);
+  L.g = take(T * 4);
+  L.lse = take(T * 4);
+  L.zt = take(T * 4);
+  L.loss = take(T * 4);
+  L.xc = take((size_t)s.planes * T * s.H * 2);
+  L.wpl = take(s.planes > 1 ? (size_t)s.planes * L.piece * s.H * 2 : 0);
+  const size_t base = off;
+  L.stats = take((size_t)(vpad / 128) * T * 8);
+  const size_t fwd_end = off;
+  off = base;   // the backward's buffers take the forward statistics' place
+  L.d = take((size_t)s.planes * T * L.piece * 2);
+  L.dx_part = take(L.dx_direct ? 0 : (size_t)L.split.dx * T * s.H * 4);
+  L.dw_part = take(L.dw_direct ? 0 : (size_t)L.split.dw * L.piece * s.H * 4);
+  L.total = std::max(off, fwd_end);
+  return L;
+}
+
+struct PrepArgs {
+  const int32_t* target;
+  int64_t T, rows_per_block;
+  int V, ignore, H;
+  const void* x;
+  int64_t x_ld, plane;
+  bf16* xc;
+  int32_t *nrows, *ticket, *ctr, *rowmap, *inv, *tgt;
+  int64_t nctr;
+  uint32_t* flags;
+  // forward: zero the outputs of tokens that do not count
+  float *loss, *lse_out;
+  // backward
+  const float *lse, *dloss;
+  float *g, *lse_c;
+  int reduction;
+  void* dx;   // zero the rows of tokens that do not count (direct dx), or NULL
+};
+
+__device__ __forceinline__ bool counts(int t, int V, int ignore) { return t != ignore && t >= 0 && t < V; }
+
+// Pack the tokens that count: block b takes rows_per_block tokens, counts those
+// before its own (a pass over the targets, which every block reads from L2) and
+// copies its rows -- bf16 as they are, fp32 as three bf16 planes.  Rows from the
+// count up to a multiple of 64 are zeroed: the dW product's last k-block reads
+// them.  Latency-bound at small T; at 8192 x 7168 bound by the copy.
+template <typename T>
+__global__ void __launch_bounds__(256) ce_prep_kernel(const PrepArgs a) {
+  __shared__ int s_before, s_total, s_cnt[256];
+  const int64_t beg = min(a.T, blockIdx.x * a.rows_per_block), end = min(a.T, beg + a.rows_per_block);
+  if (threadIdx.x == 0) s_before = s_total = 0;
+  __syncthreads();
+  int before = 0, total = 0;
+  for (int64_t i = threadIdx.x; i < a.T; i += blockDim.x) {
+    const int c = counts(a.target[i], a.V, a.ignore) ? 1 : 0;
+    total += c;
+    if (i < beg) before += c;
+  }
+  before = __reduce_add_sync(0xffffffffu, before);
+  total = __reduce_add_sync(0xffffffffu, total);
+  if ((threadIdx.x & 31) == 0) {
+    atomicAdd(&s_before, before);   // integers: the order does not matter
+    atomicAdd(&s_total, total);
+  }
+  // place of each of the block's tokens among those that count
+  const int64_t mine = beg + threadIdx.x;
+  int t = a.ignore;
+  if (mine < end) t = a.target[mine];
+  const bool ok = mine < end && counts(t, a.V, a.ignore);
+  if (mine < end && !ok && t != a.ignore) set_flag(a.flags, kFlagTarget);
+  const uint32_t ball = __ballot_sync(0xffffffffu, ok);
+  __shared__ int s_warp[8];
+  if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = __popc(ball);
+  __syncthreads();
+  int pos = s_before;
+  for (int w = 0; w < (threadIdx.x >> 5); ++w) pos += s_warp[w];
+  pos += __popc(ball & ((1u << (threadIdx.x & 31)) - 1u));
+  if (mine < end) {
+    s_cnt[threadIdx.x] = ok ? pos : -1;
+    a.inv[mine] = ok ? pos : -1;
+    if (ok) {
+      a.rowmap[pos] = (int32_t)mine;
+      a.tgt[pos] = t;
+      if (a.g) {
+        float g = 1.0f;
+        if (a.reduction == MOE_CE_NONE) g = a.dloss[mine];
+        else {
+          if (a.dloss) g = a.dloss[0];
+          if (a.reduction == MOE_CE_MEAN) g /= (float)s_total;
+        }
+        a.g[pos] = g;
+        a.lse_c[pos] = a.lse[mine];
+      }
+    } else {
+      if (a.loss) a.loss[mine] = 0.0f;
+      if (a.lse_out) a.lse_out[mine] = 0.0f;
+    }
+  }
+  if (blockIdx.x == 0) {
+    if (threadIdx.x == 0) {
+      *a.nrows = s_total;
+      *a.ticket = 0;
+    }
+    for (int64_t i = threadIdx.x; i < a.nctr; i += blockDim.x) a.ctr[i] = 0;
+  }
+  __syncthreads();
+  // copy the rows: a warp a row
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const T* x = reinterpret_cast<const T*>(a.x);
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const int nv = a.H / 8;
+  for (int r = warp; beg + r < end; r += 8) {
+    const int p = s_cnt[r];
+    if (p < 0) {
+      if (a.dx) {
+        uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<T*>(a.dx) + (beg + r) * (int64_t)a.H);
+        for (int v = lane; v < nv * (int)(sizeof(T) / 2); v += 32) o[v] = zero;
+      }
+      continue;
+    }
+    const T* src = x + (beg + r) * a.x_ld;
+    bf16* dst = a.xc + (int64_t)p * a.H;
+    if (sizeof(T) == 2) {
+#pragma unroll 4
+      for (int v = lane; v < nv; v += 32)
+        reinterpret_cast<uint4*>(dst)[v] = reinterpret_cast<const uint4*>(src)[v];
+    } else {
+      for (int v = lane; v < nv; v += 32) {
+        const float4 u = reinterpret_cast<const float4*>(src)[2 * v];
+        const float4 w = reinterpret_cast<const float4*>(src)[2 * v + 1];
+        float f[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int pl = 0; pl < kPlanesF32; ++pl) {
+          reinterpret_cast<uint4*>(dst + pl * a.plane * a.H)[v] = pack16(f, (const bf16*)nullptr);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float rest = f[e] - __bfloat162float(__float2bfloat16_rn(f[e]));
+            f[e] = isfinite(rest) ? rest : 0.0f;
+          }
+        }
+      }
+    }
+  }
+  const int total_rows = s_total, pad_end = (total_rows + 63) / 64 * 64;
+  const int planes = sizeof(T) == 2 ? 1 : kPlanesF32;
+  for (int r = total_rows + blockIdx.x; r < pad_end; r += gridDim.x)
+    for (int pl = 0; pl < planes; ++pl)
+      for (int v = threadIdx.x; v < nv; v += blockDim.x)
+        reinterpret_cast<uint4*>(a.xc + (pl * a.plane + r) * a.H)[v] = zero;
+}
+
+// Merge the row statistics of all half tiles (lanes: 32 rows, warps: slices of
+// the half tiles): M = max m, S = sum s 2^(m - M), lse = ln 2 (M + log2 S).  The
+// last block adds the rows' losses, in row order, in fp64.
+constexpr int kMergeWarps = 16;
+__global__ void __launch_bounds__(32 * kMergeWarps)
+    ce_merge_kernel(const float2* __restrict__ stats, int64_t rows_pad, int parts,
+                    const float* __restrict__ zt, const int32_t* __restrict__ rowmap,
+                    const int32_t* nrows, int32_t* ticket, float* loss_c, float* loss, float* lse,
+                    float* total, int mean) {
+  const int n = *nrows;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ float2 s_part[kMergeWarps][32];
+  for (int64_t r0 = blockIdx.x * 32ll; r0 < n; r0 += gridDim.x * 32ll) {
+    const int64_t row = r0 + lane;
+    float M = -INFINITY, S = 0.0f;
+    if (row < n) {
+#pragma unroll 4
+      for (int p = warp; p < parts; p += kMergeWarps) {
+        const float2 v = __ldcs(stats + p * rows_pad + row);
+        const float m = fmaxf(M, v.x), mu = m == -INFINITY ? 0.0f : m;
+        S = S * exp2f(M - mu) + v.y * exp2f(v.x - mu);
+        M = m;
+      }
+    }
+    s_part[warp][lane] = make_float2(M, S);
+    __syncthreads();
+    if (warp == 0 && row < n) {
+      for (int w = 1; w < kMergeWarps; ++w) {
+        const float2 v = s_part[w][lane];
+        const float m = fmaxf(M, v.x), mu = m == -INFINITY ? 0.0f : m;
+        S = S * exp2f(M - mu) + v.y * exp2f(v.x - mu);
+        M = m;
+      }
+      const float l = 0.6931471805599453f * (M + log2f(S));
+      const float each = l - zt[row];
+      const int t = rowmap[row];
+      if (lse) lse[t] = l;
+      if (loss) loss[t] = each;
+      loss_c[row] = each;
+    }
+    __syncthreads();
+  }
+  if (!total) return;
+  __shared__ int s_last;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) s_last = atomicAdd(ticket, 1) == (int)gridDim.x - 1;
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  double acc = 0.0;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) acc += (double)__ldcg(loss_c + i);
+  __shared__ double s_sum[kMergeWarps];
+#pragma unroll
+  for (int o = 16; o; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+  if (lane == 0) s_sum[warp] = acc;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double v = 0.0;
+    for (int w = 0; w < kMergeWarps; ++w) v += s_sum[w];
+    if (mean && n > 0) v /= (double)n;
+    *total = (float)v;
+  }
+}
+
+cudaError_t run_prep(const CeShape& s, const CeLayout& L, char* ws, PrepArgs& p, cudaStream_t st) {
+  p.T = s.T;
+  int64_t rpb = (s.T + 1023) / 1024;
+  rpb = (rpb + 31) / 32 * 32;
+  rpb = std::min<int64_t>(std::max<int64_t>(rpb, 32), 256);
+  p.rows_per_block = rpb;
+  p.V = s.V;
+  p.ignore = s.ignore;
+  p.H = s.H;
+  p.x_ld = s.x_ld;
+  p.plane = L.rows_pad;
+  p.xc = reinterpret_cast<bf16*>(ws + L.xc);
+  p.nrows = reinterpret_cast<int32_t*>(ws + L.meta);
+  p.ticket = p.nrows + 1;
+  p.ctr = reinterpret_cast<int32_t*>(ws + L.ctr);
+  p.nctr = L.nctr;
+  p.rowmap = reinterpret_cast<int32_t*>(ws + L.rowmap);
+  p.inv = reinterpret_cast<int32_t*>(ws + L.inv);
+  p.tgt = reinterpret_cast<int32_t*>(ws + L.tgt);
+  p.flags = reinterpret_cast<uint32_t*>(ws);
+  p.reduction = s.reduction;
+  const int64_t blocks = std::max<int64_t>((s.T + rpb - 1) / rpb, 32);
+  if (s.dtype == MOE_F32) ce_prep_kernel<float><<<(unsigned)blocks, 256, 0, st>>>(p);
+  else ce_prep_kernel<bf16><<<(unsigned)blocks, 256, 0, st>>>(p);
+  count_launch();
+  return cudaGetLastError();
+}
+
+// W's columns (vocabulary rows) v0 .. of this piece as a tensor-core operand:
+// the caller's rows, or the piece's planes in the workspace.
+struct Operand {
+  const void* p;
+  int64_t ld, plane, rows, v0;
+};
+cudaError_t piece_operand(const CeShape& s, const CeLayout& L, char* ws, const void* w, int64_t v0,
+                          int64_t vcols, Operand* o, cudaStream_t st) {
+  if (s.planes == 1) {
+    *o = {w, s.w_ld, 0, s.V, v0};
+    return cudaSuccess;
+  }
+  const int64_t have = std::min<int64_t>(vcols, s.V - v0);
+  *o = {ws + L.wpl, s.H, L.piece, vcols, 0};
+  return launch_planes(reinterpret_cast<const float*>(w) + v0 * s.w_ld, s.w_ld, have, vcols, s.H,
+                       ws + L.wpl, L.piece, st);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+#define DECODE_CE(shape, s)                                  \
+  CeShape s;                                                 \
+  do {                                                       \
+    const char* why_ = "";                                   \
+    moe_status st_ = decode_ce(shape, &s, &why_);            \
+    if (st_ != MOE_OK) return ::moe::fail(st_, why_);        \
+  } while (0)
+
+extern "C" size_t moe_linear_ce_workspace_bytes(const moe_ce_shape* shape) {
+  CeShape s;
+  const char* why;
+  if (decode_ce(shape, &s, &why) != MOE_OK) return 0;
+  return layout_ce(s).total;
+}
+
+extern "C" moe_status moe_linear_ce_forward(const moe_ce_shape* shape, const void* x, const void* w,
+                                            const int32_t* target, float* loss, float* lse,
+                                            float* total, void* ws, size_t ws_bytes, void* stream) {
+  reset_launch_count();
+  DECODE_CE(shape, s);
+  if (!w || (s.T > 0 && (!x || !target))) return fail(MOE_ERR_INVALID_ARG, "x, w and target must be non-NULL");
+  if (!loss && !lse && !total) return fail(MOE_ERR_INVALID_ARG, "one of loss, lse and total must be non-NULL");
+  if (s.reduction == MOE_CE_NONE && total)
+    return fail(MOE_ERR_INVALID_ARG, "total must be NULL with MOE_CE_NONE");
+  if (!aligned16(x) || !aligned16(w)) return fail(MOE_ERR_INVALID_ARG, "x and w must be 16-byte aligned");
+  const CeLayout L = layout_ce(s);
+  moe_status e = check_ws(ws, ws_bytes, L.total);
+  if (e != MOE_OK) return e;
+  char* b = static_cast<char*>(ws);
+  cudaStream_t st = (cudaStream_t)stream;
+  PrepArgs p = {};
+  p.target = target;
+  p.x = x;
+  p.loss = loss;
+  p.lse_out = lse;
+  CHECK_CUDA(run_prep(s, L, b, p, st));
+  const int64_t vpad = ((int64_t)s.V + 255) / 256 * 256;
+  // bf16 W is read where it is: one launch over the whole vocabulary
+  const int64_t step = s.planes == 1 ? vpad : L.piece;
+  int64_t c = 0;
+  for (int64_t v0 = 0; v0 < vpad && s.T > 0; v0 += step, ++c) {
+    const int64_t vcols = std::min(step, vpad - v0);
+    Operand o;
+    CHECK_CUDA(piece_operand(s, L, b, w, v0, vcols, &o, st));
+    LogitsArgs a = {};
+    a.planes = s.planes;
+    a.x = b + L.xc;
+    a.x_ld = s.H;
+    a.x_plane = L.rows_pad;
+    a.w = o.p;
+    a.w_ld = o.ld;
+    a.w_plane = o.plane;
+    a.w_rows = o.rows;
+    a.hidden = s.H;
+    a.v0 = v0;
+    a.w_v0 = o.v0;
+    a.vcols = vcols;
+    a.vocab = s.V;
+    a.nrows = p.nrows;
+    a.rows_bound = s.T;
+    a.target = p.tgt;
+    a.ctr = p.ctr + c;
+    a.flags = p.flags;
+    a.stats = reinterpret_cast<float2*>(b + L.stats);
+    a.zt = reinterpret_cast<float*>(b + L.zt);
+    a.rows_pad = L.rows_pad;
+    CHECK_CUDA(launch_linear_logits(a, st));
+  }
+  int64_t blocks = std::min<int64_t>((s.T + 31) / 32, 4096);
+  if (blocks < 1) blocks = 1;
+  ce_merge_kernel<<<(unsigned)blocks, 32 * kMergeWarps, 0, st>>>(
+      reinterpret_cast<const float2*>(b + L.stats), L.rows_pad, (int)(vpad / 128),
+      reinterpret_cast<const float*>(b + L.zt), p.rowmap, p.nrows, p.ticket,
+      reinterpret_cast<float*>(b + L.loss), loss, lse, total, s.reduction == MOE_CE_MEAN);
+  count_launch();
+  CHECK_CUDA(cudaGetLastError());
+  return MOE_OK;
+}
+
+extern "C" moe_status moe_linear_ce_backward(const moe_ce_shape* shape, const void* x, const void* w,
+                                             const int32_t* target, const float* lse,
+                                             const float* dloss, void* dx, void* dw, void* ws,
+                                             size_t ws_bytes, void* stream) {
+  reset_launch_count();
+  DECODE_CE(shape, s);
+  if (!w || (s.T > 0 && (!x || !target || !lse)))
+    return fail(MOE_ERR_INVALID_ARG, "x, w, target and lse must be non-NULL");
+  if (s.reduction == MOE_CE_NONE && !dloss && s.T > 0)
+    return fail(MOE_ERR_INVALID_ARG, "dloss must be non-NULL with MOE_CE_NONE");
+  if (!dw && (!dx && s.T > 0)) return fail(MOE_ERR_INVALID_ARG, "one of dx and dw must be non-NULL");
+  if (!aligned16(x) || !aligned16(w) || !aligned16(dx) || !aligned16(dw))
+    return fail(MOE_ERR_INVALID_ARG, "x, w, dx and dw must be 16-byte aligned");
+  const CeLayout L = layout_ce(s);
+  moe_status e = check_ws(ws, ws_bytes, L.total);
+  if (e != MOE_OK) return e;
+  char* b = static_cast<char*>(ws);
+  cudaStream_t st = (cudaStream_t)stream;
+  PrepArgs p = {};
+  p.target = target;
+  p.x = x;
+  p.lse = lse;
+  p.dloss = dloss;
+  p.g = reinterpret_cast<float*>(b + L.g);
+  p.lse_c = reinterpret_cast<float*>(b + L.lse);
+  p.dx = L.dx_direct ? dx : nullptr;
+  CHECK_CUDA(run_prep(s, L, b, p, st));
+  const int64_t vpad = ((int64_t)s.V + 255) / 256 * 256;
+  int64_t c = 0;
+  for (int64_t v0 = 0; v0 < vpad; v0 += L.piece, ++c) {
+    const int64_t vcols = std::min(L.piece, vpad - v0);
+    const int64_t have = std::min<int64_t>(vcols, s.V - v0);
+    Operand o;
+    CHECK_CUDA(piece_operand(s, L, b, w, v0, vcols, &o, st));
+    LogitsArgs a = {};
+    a.planes = s.planes;
+    a.x = b + L.xc;
+    a.x_ld = s.H;
+    a.x_plane = L.rows_pad;
+    a.w = o.p;
+    a.w_ld = o.ld;
+    a.w_plane = o.plane;
+    a.w_rows = o.rows;
+    a.hidden = s.H;
+    a.v0 = v0;
+    a.w_v0 = o.v0;
+    a.vcols = vcols;
+    a.vocab = s.V;
+    a.nrows = p.nrows;
+    a.rows_bound = s.T;
+    a.target = p.tgt;
+    a.ctr = p.ctr + 2 * c;
+    a.flags = p.flags;
+    a.rows_pad = L.rows_pad;
+    a.gradient = true;
+    a.lse = p.lse_c;
+    a.g = p.g;
+    a.d = b + L.d;
+    a.d_ld = L.piece;
+    CHECK_CUDA(launch_linear_logits(a, st));
+    LinearGradArgs q = {};
+    q.planes = s.planes;
+    q.d = b + L.d;
+    q.d_ld = L.piece;
+    q.d_plane = L.rows_pad;
+    q.x = b + L.xc;
+    q.x_ld = s.H;
+    q.x_plane = L.rows_pad;
+    q.x_rows = L.rows_pad;
+    q.w = o.p;
+    q.w_ld = o.ld;
+    q.w_plane = o.plane;
+    q.w_rows = o.rows;
+    q.hidden = s.H;
+    q.v0 = v0;
+    q.w_v0 = o.v0;
+    q.vcols = vcols;
+    q.vocab = s.V;
+    q.nrows = p.nrows;
+    q.rows_bound = s.T;
+    q.ctr = p.ctr + 2 * c + 1;
+    q.flags = p.flags;
+    q.split = L.split;
+    q.out_f32 = s.dtype == MOE_F32;
+    q.rows_pad = L.rows_pad;
+    q.accumulate = v0 > 0;
+    if (dx && L.dx_direct) {
+      q.dx = dx;
+      q.rowmap = p.rowmap;
+    } else if (dx) {
+      q.dx_part = reinterpret_cast<float*>(b + L.dx_part);
+    }
+    q.dw_pad = L.piece;
+    if (dw && L.dw_direct) q.dw = dw;
+    else if (dw) q.dw_part = reinterpret_cast<float*>(b + L.dw_part);
+    CHECK_CUDA(launch_linear_grad(q, st));
+    if (q.dw_part)
+      CHECK_CUDA(launch_reduce_parts(q.dw_part, L.split.dw, L.piece * s.H, have, s.H, nullptr, nullptr,
+                                     static_cast<char*>(dw) + v0 * s.H * s.esize, q.out_f32, st));
+  }
+  if (dx && !L.dx_direct)
+    CHECK_CUDA(launch_reduce_parts(reinterpret_cast<const float*>(b + L.dx_part), L.split.dx,
+                                   L.rows_pad * s.H, s.T, s.H, p.inv, nullptr, dx, s.dtype == MOE_F32, st));
+  return MOE_OK;
+}

@@ -1,0 +1,907 @@
+// linear_tc.cu -- the dense GEMMs of the training operators on pairs of SMs
+// (tcgen05 cta_group::2): logits z = x W^T with the softmax statistics or the
+// logit gradient in the epilogue, and the two gradient products
+//   dX = D W   (D [rows, V], W [V, H])      K = vocabulary
+//   dW = D^T x (D [rows, V], x [rows, H])   K = rows
+// in one launch over one tile list.
+//
+// A pair of SMs computes 256 x 256 output tiles over 64-wide k-blocks: CTA r
+// keeps rows 128r .. of the A tile and columns 128r .. of the B tile, six
+// 32 KB stages; per k-block an SM reads 32 KB of operands for 512 clocks of
+// MMA.  Operands that are not K-major are read in their stored layout as
+// 64-wide boxes with the 128-byte swizzle (MN-major descriptors), so neither D
+// nor W nor x is ever transposed in memory.  The tile order is dynamic (one
+// counter in global memory): the tiles in progress form one window, and within
+// it groups of kGroupM row tiles pass over the column tiles, so the rows of a
+// group stay in L2 while the other operand streams by once per group.
+//
+// The gradient launch puts the dX tiles (few, long K) before the dW tiles
+// (many, short K): the short ones fill the SMs that the long ones leave idle at
+// their end.  Where tiles are few and long, K is split and the fp32 partial
+// sums are added in split order by a second kernel (no atomics: the result does
+// not depend on the order of the tiles).
+//
+// fp32 operands are three bf16 planes each; a tile's k-loop then runs over the
+// six plane products whose weight is above 2^-24, smallest first, into the same
+// fp32 accumulator.
+//
+// Roles in each CTA: warp 0 TMA producer, warp 1 TMEM and (even CTA) the MMA
+// issuer, warps 2-9 epilogue: two per 32-lane TMEM quarter, one per half of
+// the 256 columns.  Every wait is bounded; a CTA that gives up raises its abort
+// flag, its partner's waits run out in turn, and both meet at the closing
+// cluster barrier before TMEM is released.
+#include <atomic>
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "tc_pair.cuh"
+#include "tcgen05.cuh"
+#include "train.h"
+
+namespace moe {
+namespace tc {
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();   // gemm_tc.cu
+}
+
+namespace lin {
+
+using namespace tc;
+
+constexpr int BM = kLinTile, BN = kLinTile, BMC = BM / 2, BNC = BN / 2, BK = kLinK;
+constexpr int S = 6;
+constexpr int A_BYTES = BMC * BK * 2, B_BYTES = BNC * BK * 2;
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int BOX_BYTES = 64 * BK * 2;
+constexpr int RING_BYTES = S * STAGE_BYTES;
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 32 * (2 + EPI_WARPS);
+constexpr uint32_t TMEM_COLS = 512;
+constexpr int NSLOT = 4;
+constexpr int READERS = 4;          // of a tile slot: odd producer, MMA, two epilogues
+constexpr int BAR_BYTES = 512;
+constexpr int OUT_ROW_BYTES = 80;   // 64 bytes of a chunk's row, padded
+constexpr int OUT_WARP_BYTES = 32 * OUT_ROW_BYTES;
+constexpr int SMEM_BYTES = 1024 + RING_BYTES + BAR_BYTES + EPI_WARPS * OUT_WARP_BYTES;
+static_assert(SMEM_BYTES <= 232448, "shared memory budget of one CTA");
+static_assert((2 * S + 5 + 3 * NSLOT + 1) * 8 + 12 <= BAR_BYTES, "barrier area");
+constexpr int kGroupM = 8;
+
+// kind::f16: D fp32, A and B bf16, M = 256 over the pair, N = 256.
+constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) |
+                           ((uint32_t)(BM >> 4) << 24);
+constexpr uint32_t IDESC_A_MN = 1u << 15, IDESC_B_MN = 1u << 16;
+
+enum Kind { kStats = 0, kDlogit = 1, kGrad = 2 };
+
+struct Args {
+  int hidden, planes;
+  int64_t v0, w_v0, vcols, vocab;
+  const int32_t* nrows;
+  int64_t rows_bound;
+  int32_t* ctr;
+  uint32_t* flags;
+  int64_t x_plane, w_plane, d_plane;
+  const int32_t* target;
+  float2* stats;
+  float* zt;
+  int64_t rows_pad;
+  const float* lse;
+  const float* g;
+  bf16* d;
+  int64_t d_ld;
+  int ks_dx, ks_dw, out_f32;
+  float* dx_part;
+  int accumulate;
+  void* dx;
+  const int32_t* rowmap;
+  const void* dx_add;
+  void* dw;
+  float* dw_part;
+  int64_t dw_pad;
+  int want_dx, want_dw;
+};
+
+__device__ __forceinline__ uint64_t mn_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(BOX_BYTES >> 4) << 16;   // next 64 columns
+  d |= (uint64_t)(1024 >> 4) << 32;        // next 8 k-rows
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// Plane products in ascending weight: (0,2) (2,0) (1,1) (0,1) (1,0) (0,0).
+__device__ __forceinline__ void plane_pair(int planes, int i, int& pa, int& pb) {
+  if (planes == 1) { pa = pb = 0; return; }
+  const int t = i == 0 ? 0x02 : i == 1 ? 0x20 : i == 2 ? 0x11 : i == 3 ? 0x01 : i == 4 ? 0x10 : 0x00;
+  pa = t >> 4;
+  pb = t & 15;
+}
+
+struct Tile {
+  int type;        // 0: logits, 1: dX, 2: dW
+  int mt, nt, sp;
+  int kb0, kb1;    // k-blocks of one plane product
+};
+
+// m-tiles in groups of kGroupM, n-tiles outer within a group.
+__device__ __forceinline__ void order_tile(int64_t t, int MT, int NT, int& mt, int& nt) {
+  const int64_t per = (int64_t)kGroupM * NT;
+  const int grp = (int)(t / per);
+  const int first = grp * kGroupM;
+  const int size = MT - first < kGroupM ? MT - first : kGroupM;
+  const int64_t r = t - grp * per;
+  nt = (int)(r / size);
+  mt = first + (int)(r % size);
+}
+
+template <int KIND>
+struct Plan {
+  int MTr, NTh, NTv, KBv, KBr;
+  int64_t n_dx, total;
+  int64_t rows;
+  __device__ __forceinline__ void init(const Args& a) {
+    rows = a.nrows ? (int64_t)*a.nrows : a.rows_bound;
+    if (rows > a.rows_bound) rows = a.rows_bound;
+    if (rows < 0) rows = 0;
+    MTr = (int)((rows + BM - 1) / BM);
+    NTh = (a.hidden + BN - 1) / BN;
+    NTv = (int)((a.vcols + BN - 1) / BN);
+    KBv = (int)((a.vcols + BK - 1) / BK);
+    KBr = (int)((rows + BK - 1) / BK);
+    n_dx = 0;
+    if (KIND == kGrad) {
+      n_dx = a.want_dx ? (int64_t)MTr * NTh * a.ks_dx : 0;
+      total = n_dx + (a.want_dw ? (int64_t)NTv * NTh * a.ks_dw : 0);
+    } else {
+      total = (int64_t)MTr * NTv;
+    }
+  }
+  __device__ __forceinline__ Tile decode(const Args& a, int64_t t) const {
+    Tile r;
+    if (KIND != kGrad) {
+      r.type = 0;
+      r.sp = 0;
+      order_tile(t, MTr, NTv, r.mt, r.nt);
+      r.kb0 = 0;
+      r.kb1 = (a.hidden + BK - 1) / BK;
+    } else if (t < n_dx) {
+      r.type = 1;
+      r.sp = (int)(t % a.ks_dx);
+      order_tile(t / a.ks_dx, MTr, NTh, r.mt, r.nt);
+      r.kb0 = (int)((int64_t)r.sp * KBv / a.ks_dx);
+      r.kb1 = (int)((int64_t)(r.sp + 1) * KBv / a.ks_dx);
+    } else {
+      t -= n_dx;
+      r.type = 2;
+      r.sp = (int)(t % a.ks_dw);
+      order_tile(t / a.ks_dw, NTv, NTh, r.mt, r.nt);
+      r.kb0 = (int)((int64_t)r.sp * KBr / a.ks_dw);
+      r.kb1 = (int)((int64_t)(r.sp + 1) * KBr / a.ks_dw);
+    }
+    return r;
+  }
+};
+
+__device__ __forceinline__ float ex2(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Write 32 rows x 32 bf16 columns (one row a lane in `packed`) through the
+// warp's staging slice as 16-byte pieces of whole rows.
+__device__ __forceinline__ void store_chunk(unsigned char* stage, int lane, const uint4 (&packed)[4],
+                                            int nvalid, bf16* base, int64_t ld, int ncols) {
+  unsigned char* my_row = stage + lane * OUT_ROW_BYTES;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) reinterpret_cast<uint4*>(my_row)[v] = packed[v];
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int p = lane + 32 * i;
+    const int rr = p >> 2, pc = p & 3;
+    if (rr < nvalid && pc * 8 < ncols)
+      *reinterpret_cast<uint4*>(base + (int64_t)rr * ld + pc * 8) =
+          *reinterpret_cast<const uint4*>(stage + rr * OUT_ROW_BYTES + pc * 16);
+  }
+  __syncwarp();
+}
+
+template <int KIND>
+__global__ void __launch_bounds__(THREADS, 1)
+    linear_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                  const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmDt,
+                  const Args a) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + RING_BYTES);
+  // bars: full[S] empty[S] tfull[2] tempty[2] final tfill[NSLOT] tdrain[NSLOT],
+  // then the tile slots, the epilogue's tile and the scalars
+  volatile int64_t* s_tile = reinterpret_cast<volatile int64_t*>(bars + 2 * S + 5 + 2 * NSLOT);
+  volatile int64_t* s_etile = s_tile + NSLOT;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5 + 3 * NSLOT + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* s_ok = reinterpret_cast<volatile int*>(tmem_slot + 2);
+  unsigned char* s_out = smem + RING_BYTES + BAR_BYTES;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const uint32_t ring = smem_u32(smem);
+  auto full = [&](int s) { return smem_u32(&bars[s]); };
+  auto empty = [&](int s) { return smem_u32(&bars[S + s]); };
+  auto tfull = [&](int b) { return smem_u32(&bars[2 * S + b]); };
+  auto tempty = [&](int b) { return smem_u32(&bars[2 * S + 2 + b]); };
+  const uint32_t final_bar = smem_u32(&bars[2 * S + 4]);
+  auto tfill = [&](int i) { return smem_u32(&bars[2 * S + 5 + i]); };
+  auto tdrain = [&](int i) { return smem_u32(&bars[2 * S + 5 + NSLOT + i]); };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full(s), 1);      // the even CTA's producer (pair's bytes)
+      mbar_init(empty(s), 1);     // the pair's MMA commit
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull(b), 1);
+      mbar_init(tempty(b), 2 * 32 * EPI_WARPS);
+    }
+    mbar_init(final_bar, 1);
+    for (int i = 0; i < NSLOT; ++i) {
+      mbar_init(tfill(i), 1);
+      mbar_init(tdrain(i), READERS);
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  __syncthreads();
+  cluster_sync();   // barriers of both CTAs initialised before any remote arrive
+  if (warp == 1) {
+    tmem_alloc2(smem_u32(tmem_slot), TMEM_COLS);
+    tmem_relinquish2();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  Plan<KIND> plan;
+  plan.init(a);
+  const int nprod = a.planes == 1 ? 1 : 6;
+
+  // Tile n of this pair, or -1 when there is none left (or a wait ran out).
+  // The even CTA's producer takes it, one ahead, from the counter and writes it
+  // to slot n % NSLOT of both CTAs; the other readers read their CTA's slot and
+  // tell the even CTA that they have.
+  int64_t reserve = threadIdx.x == 0 && leader ? (int64_t)atomicAdd(a.ctr, 1) : -1;
+  auto next_tile = [&](int64_t n, bool take) -> int64_t {
+    const int slot = (int)(n % NSLOT);
+    const uint32_t use = (uint32_t)(n / NSLOT);
+    if (take) {
+      if (!wait2(tdrain(slot), (use & 1u) ^ 1u, abort_flag)) return -1;
+      int64_t t = reserve;
+      reserve = (int64_t)atomicAdd(a.ctr, 1);
+      if (t >= plan.total) t = -1;
+      s_tile[slot] = t;
+      const uint32_t remote = map_to_rank(smem_u32((const void*)&s_tile[slot]), 1);
+      asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(remote), "l"(t) : "memory");
+      mbar_arrive(tfill(slot));
+      mbar_arrive_cluster(map_to_rank(tfill(slot), 1));
+      return t;
+    }
+    if (!wait2(tfill(slot), use & 1u, abort_flag)) return -1;
+    const int64_t t = s_tile[slot];
+    mbar_arrive_cluster(map_to_rank(tdrain(slot), 0));
+    return t;
+  };
+
+  if (warp == 0 && lane == 0) {
+    // ---------------- TMA producer ----------------
+    int s = 0;
+    uint32_t ph = 0, issued = 0, par = 0;
+    bool ok = true;
+    for (int64_t n = 0; ok; ++n) {
+      const int64_t tile = next_tile(n, leader);
+      if (tile < 0) break;
+      const Tile t = plan.decode(a, tile);
+      const int arow = t.mt * BM + (int)rank * BMC, bcol = t.nt * BN + (int)rank * BNC;
+      for (int pr = 0; pr < nprod && ok; ++pr) {
+        int pa, pb;
+        plane_pair(a.planes, pr, pa, pb);
+        for (int kb = t.kb0; kb < t.kb1; ++kb) {
+          if (!wait2(empty(s), ph ^ 1u, abort_flag)) { ok = false; break; }
+          const uint32_t sa = ring + s * STAGE_BYTES, sb = sa + A_BYTES;
+          // both CTAs' bytes count on the even CTA's "full" barrier
+          const uint32_t fb = map_to_rank(full(s), 0);
+          if (leader) mbar_expect_tx(full(s), 2 * STAGE_BYTES);
+          const int k = kb * BK;
+          if (KIND != kGrad) {
+            tma_load_2d_pair(sa, &tmX, k, (int)(pa * a.x_plane) + arow, fb);
+            tma_load_2d_pair(sb, &tmW, k, (int)(pb * a.w_plane + a.w_v0) + bcol, fb);
+          } else if (t.type == 1) {
+            tma_load_2d_pair(sa, &tmD, k, (int)(pa * a.d_plane) + arow, fb);
+            const int wr = (int)(pb * a.w_plane + a.w_v0) + k;
+            tma_load_2d_pair(sb, &tmW, bcol, wr, fb);
+            tma_load_2d_pair(sb + BOX_BYTES, &tmW, bcol + 64, wr, fb);
+          } else {
+            const int dr = (int)(pa * a.d_plane) + k, xr = (int)(pb * a.x_plane) + k;
+            tma_load_2d_pair(sa, &tmDt, arow, dr, fb);
+            tma_load_2d_pair(sa + BOX_BYTES, &tmDt, arow + 64, dr, fb);
+            tma_load_2d_pair(sb, &tmX, bcol, xr, fb);
+            tma_load_2d_pair(sb + BOX_BYTES, &tmX, bcol + 64, xr, fb);
+          }
+          issued |= 1u << s;
+          par = (par & ~(1u << s)) | (ph << s);
+          if (++s == S) { s = 0; ph ^= 1u; }
+        }
+      }
+    }
+    if (*abort_flag && leader) {
+      for (int i = 0; i < S; ++i)
+        if (issued & (1u << i)) wait2_quiet(full(i), (par >> i) & 1u);
+    }
+  } else if (warp == 1 && lane == 0 && leader) {
+    // ---------------- even CTA: MMA issuer for the pair ----------------
+    int s = 0, acc = 0;
+    uint32_t ph = 0, aph = 0;
+    bool ok = true;
+    for (int64_t n = 0; ok; ++n) {
+      const int64_t tile = next_tile(n, false);
+      if (tile < 0) break;
+      const Tile t = plan.decode(a, tile);
+      const int steps = (t.kb1 - t.kb0) * nprod;
+      if (steps == 0) continue;   // no rows: the epilogue writes zeros
+      const uint32_t idesc = IDESC | (t.type == 2 ? IDESC_A_MN : 0u) | (t.type != 0 ? IDESC_B_MN : 0u);
+      if (!wait2(tempty(acc), aph ^ 1u, abort_flag)) break;
+      tc_fence_after();
+      const uint32_t d = tmem_base + (uint32_t)acc * BN;
+      for (int i = 0; i < steps; ++i) {
+        if (!wait2(full(s), ph, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t sa = ring + s * STAGE_BYTES, sb = sa + A_BYTES;
+#pragma unroll
+        for (int kk = 0; kk < BK / 16; ++kk) {
+          const uint64_t ad = KIND == kGrad && t.type == 2 ? mn_desc(sa + kk * 2048) : sw128_desc(sa + kk * 32);
+          const uint64_t bd = KIND == kGrad ? mn_desc(sb + kk * 2048) : sw128_desc(sb + kk * 32);
+          mma2(d, ad, bd, idesc, (i | kk) != 0 ? 1u : 0u);
+        }
+        commit2_both(empty(s));
+        if (++s == S) { s = 0; ph ^= 1u; }
+      }
+      if (!ok) break;
+      commit2_both(tfull(acc));
+      acc ^= 1;
+      if (acc == 0) aph ^= 1u;
+    }
+    if (*abort_flag) {
+      commit2_self(final_bar);
+      wait2_quiet(final_bar, 0);
+    }
+  } else if (warp >= 2) {
+    // ---------------- epilogue (warps 2..9, both CTAs) ----------------
+    const int q = warp & 3;                 // TMEM lanes 32q .. 32q+31
+    const int half = (warp - 2) / 4;        // columns 128 half ..
+    const int c_lo = half * (BN / 2), c_hi = c_lo + BN / 2;
+    const int et = threadIdx.x - 64;
+    unsigned char* stage = s_out + (warp - 2) * OUT_WARP_BYTES;
+    auto epi_bar = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(32 * EPI_WARPS) : "memory"); };
+    int acc = 0;
+    uint32_t aph = 0;
+    for (int64_t n = 0;; ++n) {
+      if (et == 0) {
+        const int64_t tl = next_tile(n, false);
+        bool live = tl >= 0;
+        if (live) {
+          const Tile t = plan.decode(a, tl);
+          if (t.kb1 > t.kb0) live = wait2(tfull(acc), aph, abort_flag);
+        }
+        *s_etile = tl;
+        *s_ok = live ? 1 : 0;
+      }
+      epi_bar();
+      const int okv = *s_ok;
+      const int64_t tile = *s_etile;
+      epi_bar();
+      if (!okv) break;
+      const Tile t = plan.decode(a, tile);
+      const bool none = t.kb1 == t.kb0;     // no k-blocks: the product is zero
+      tc_fence_after();
+      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)acc * BN;
+      const int64_t row0 = (int64_t)t.mt * BM + (int64_t)rank * BMC + q * 32;
+      const int64_t row = row0 + lane;
+      if (KIND == kStats) {
+        // running maximum and sum of the row over this half of the tile, in
+        // log2 units: the maximum kept is the rounded z * log2(e), so the
+        // sum's scale and the maximum agree exactly
+        const bool live = row < plan.rows;
+        const int64_t col0 = a.v0 + (int64_t)t.nt * BN;
+        const int tg = live ? a.target[row] : -1;
+        float m = -INFINITY, sum = 0.0f;
+#pragma unroll 1
+        for (int c = c_lo; c < c_hi; c += 32) {
+          uint32_t r[32];
+          tmem_ld32(taddr + c, r);
+          tmem_wait_ld();
+          const int64_t left = a.vocab - (col0 + c);
+          if (left < 32) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j >= left) r[j] = 0xFF800000u;
+          }
+          const int64_t dt = (int64_t)tg - (col0 + c);
+          if (dt >= 0 && dt < 32) {
+            float zt = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j == (int)dt) zt = __uint_as_float(r[j]);
+            a.zt[row] = zt;
+          }
+          float mx = __uint_as_float(r[0]);
+#pragma unroll
+          for (int j = 1; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(r[j]));
+          const float mn = fmaxf(m, mx * kLog2e);
+          const float mu = mn == -INFINITY ? 0.0f : mn;
+          float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            s0 += ex2(fmaf(__uint_as_float(r[j]), kLog2e, -mu));
+            s1 += ex2(fmaf(__uint_as_float(r[j + 1]), kLog2e, -mu));
+          }
+          sum = sum * ex2(m - mu) + (s0 + s1);
+          m = mn;
+        }
+        if (live)
+          a.stats[(2 * (a.v0 / BN + t.nt) + half) * a.rows_pad + row] = make_float2(m, sum);
+      } else if (KIND == kDlogit) {
+        const bool live = row < plan.rows;
+        const int64_t col0 = a.v0 + (int64_t)t.nt * BN;
+        const int tg = live ? a.target[row] : -1;
+        const float l2 = live ? a.lse[row] * kLog2e : 0.0f;
+        const float g = live ? a.g[row] : 0.0f;
+        bf16* drow = a.d + row0 * a.d_ld + (int64_t)t.nt * BN;
+#pragma unroll 1
+        for (int c = c_lo; c < c_hi; c += 32) {
+          uint32_t r[32];
+          tmem_ld32(taddr + c, r);
+          tmem_wait_ld();
+          const int64_t left = a.vocab - (col0 + c);
+          const int64_t dt = (int64_t)tg - (col0 + c);
+          float f[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) f[j] = ex2(fmaf(__uint_as_float(r[j]), kLog2e, -l2));
+          if (dt >= 0 && dt < 32) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j == (int)dt) f[j] -= 1.0f;
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) f[j] = live && j < left ? f[j] * g : 0.0f;
+          for (int p = 0; p < a.planes; ++p) {
+            uint4 pk[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) pk[j] = pack16(f + 8 * j, (const bf16*)nullptr);
+            store_chunk(stage, lane, pk, 32, drow + p * a.d_plane * a.d_ld + c, a.d_ld, 32);
+            if (p + 1 < a.planes) {
+              // what this plane leaves for the next one (0 where it is exact
+              // or not finite)
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                const float rest = f[j] - __bfloat162float(__float2bfloat16_rn(f[j]));
+                f[j] = isfinite(rest) ? rest : 0.0f;
+              }
+            }
+          }
+        }
+      } else {
+        const bool is_dx = t.type == 1;
+        const int64_t rows_out = is_dx ? plan.rows : min(a.vcols, a.vocab - a.v0);
+        const int64_t nv = rows_out - row0;
+        const int nvalid = nv <= 0 ? 0 : (nv >= 32 ? 32 : (int)nv);
+        float* part = is_dx ? a.dx_part : a.dw_part;
+        const int n0 = t.nt * BN;
+        int64_t orow = row;     // where this lane's row goes
+        if (is_dx && a.rowmap) orow = lane < nvalid ? a.rowmap[row] : 0;
+        if (!is_dx) orow = a.v0 + row;
+#pragma unroll 1
+        for (int c = c_lo; c < c_hi && n0 + c < a.hidden; c += 32) {
+          uint32_t r[32];
+          if (none) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) r[j] = 0u;
+          } else {
+            tmem_ld32(taddr + c, r);
+            tmem_wait_ld();
+          }
+          const int ncols = min(32, a.hidden - (n0 + c));   // a multiple of 8
+          if (part != nullptr) {
+            if (lane < nvalid) {
+              float* p = part + ((int64_t)t.sp * (is_dx ? a.rows_pad : a.dw_pad) + row) * a.hidden + n0 + c;
+              const bool add = is_dx && a.accumulate;
+#pragma unroll
+              for (int v = 0; v < 8; ++v) {
+                if (4 * v >= ncols) break;
+                float4 o = make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
+                                       __uint_as_float(r[4 * v + 2]), __uint_as_float(r[4 * v + 3]));
+                if (add) {
+                  const float4 b = reinterpret_cast<const float4*>(p)[v];
+                  o.x += b.x; o.y += b.y; o.z += b.z; o.w += b.w;
+                }
+                reinterpret_cast<float4*>(p)[v] = o;
+              }
+            }
+          } else if (a.out_f32) {
+            if (lane < nvalid) {
+              float* o = reinterpret_cast<float*>(is_dx ? a.dx : a.dw) + orow * a.hidden + n0 + c;
+              const float* ad = is_dx && a.dx_add ? reinterpret_cast<const float*>(a.dx_add) + orow * a.hidden + n0 + c : nullptr;
+#pragma unroll
+              for (int v = 0; v < 8; ++v) {
+                if (4 * v >= ncols) break;
+                float4 f = make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
+                                       __uint_as_float(r[4 * v + 2]), __uint_as_float(r[4 * v + 3]));
+                if (ad) {
+                  const float4 b = reinterpret_cast<const float4*>(ad)[v];
+                  f.x += b.x; f.y += b.y; f.z += b.z; f.w += b.w;
+                }
+                reinterpret_cast<float4*>(o)[v] = f;
+              }
+            }
+          } else {
+            float f[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(r[j]);
+            bf16* out = reinterpret_cast<bf16*>(is_dx ? a.dx : a.dw);
+            uint4 pk[4];
+            // whole-row 16-byte pieces through the staging slice; the row of
+            // lane rr comes by shuffle (a compacted row goes to its token)
+            if (is_dx && a.dx_add) {
+              // coalesced reads of the addend through the same slice
+              const bf16* addp = reinterpret_cast<const bf16*>(a.dx_add);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int p = lane + 32 * i, rr = p >> 2, pc = p & 3;
+                const int64_t ar = __shfl_sync(0xffffffffu, orow, rr);
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (rr < nvalid && pc * 8 < ncols)
+                  v = *reinterpret_cast<const uint4*>(addp + ar * a.hidden + n0 + c + pc * 8);
+                *reinterpret_cast<uint4*>(stage + rr * OUT_ROW_BYTES + pc * 16) = v;
+              }
+              __syncwarp();
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                float b[8];
+                unpack16(reinterpret_cast<const uint4*>(stage + lane * OUT_ROW_BYTES)[j], b, (const bf16*)nullptr);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[8 * j + e] += b[e];
+              }
+              __syncwarp();
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              pk[j] = pack16(f + 8 * j, (const bf16*)nullptr);
+              reinterpret_cast<uint4*>(stage + lane * OUT_ROW_BYTES)[j] = pk[j];
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int p = lane + 32 * i, rr = p >> 2, pc = p & 3;
+              const int64_t wr = __shfl_sync(0xffffffffu, orow, rr);
+              if (rr < nvalid && pc * 8 < ncols)
+                *reinterpret_cast<uint4*>(out + wr * a.hidden + n0 + c + pc * 8) =
+                    *reinterpret_cast<const uint4*>(stage + rr * OUT_ROW_BYTES + pc * 16);
+            }
+            __syncwarp();
+          }
+        }
+      }
+      if (!none) {
+        tc_fence_before();
+        mbar_arrive_cluster(map_to_rank(tempty(acc), 0));
+        acc ^= 1;
+        if (acc == 0) aph ^= 1u;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // no MMA, TMEM load or remote arrive of the pair in flight
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc2(tmem_base, TMEM_COLS);
+  }
+  if (threadIdx.x == 0 && *abort_flag) set_flag(a.flags, kFlagTimeout);
+}
+
+// out[r] = sum over the splits (in order) of part[s][row], + add[r].
+template <typename T>
+__global__ void __launch_bounds__(256) reduce_parts_kernel(const float* __restrict__ part, int splits,
+                                                           int64_t stride, int64_t rows, int hidden,
+                                                           const int32_t* __restrict__ inv,
+                                                           const T* __restrict__ add,
+                                                           T* __restrict__ out) {
+  const int per_row = hidden / 8;
+  const int64_t items = rows * per_row;
+  for (int64_t it = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; it < items;
+       it += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t r = it / per_row;
+    const int j0 = (int)(it - r * per_row) * 8;
+    const int64_t src = inv ? (int64_t)inv[r] : r;
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = 0.0f;
+    if (src >= 0) {
+      for (int s = 0; s < splits; ++s) {
+        const float4* p = reinterpret_cast<const float4*>(part + s * stride + src * hidden + j0);
+        const float4 u = __ldcs(p), v = __ldcs(p + 1);
+        f[0] += u.x; f[1] += u.y; f[2] += u.z; f[3] += u.w;
+        f[4] += v.x; f[5] += v.y; f[6] += v.z; f[7] += v.w;
+      }
+    }
+    constexpr int NV = Vec16<T>::N;
+#pragma unroll
+    for (int h = 0; h < 8 / NV; ++h) {
+      if (add) {
+        float b[8];
+        unpack16(*reinterpret_cast<const uint4*>(add + r * hidden + j0 + h * NV), b, (const T*)nullptr);
+#pragma unroll
+        for (int e = 0; e < NV; ++e) f[h * NV + e] += b[e];
+      }
+      *reinterpret_cast<uint4*>(out + r * hidden + j0 + h * NV) = pack16(f + h * NV, (const T*)nullptr);
+    }
+  }
+}
+
+__device__ __forceinline__ void split3(float v, float& p0, float& p1, float& p2) {
+  p0 = __bfloat162float(__float2bfloat16_rn(v));
+  p1 = v - p0;
+  if (!isfinite(p1)) p1 = 0.0f;
+  const float q1 = __bfloat162float(__float2bfloat16_rn(p1));
+  p2 = p1 - q1;
+  p1 = q1;
+}
+
+__global__ void __launch_bounds__(256) planes_kernel(const float* __restrict__ src, int64_t ld,
+                                                     int64_t rows, int64_t rows_zero, int hidden,
+                                                     bf16* __restrict__ dst, int64_t plane) {
+  const int per_row = hidden / 8;
+  const int64_t items = rows_zero * per_row;
+  for (int64_t it = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; it < items;
+       it += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t r = it / per_row;
+    const int j0 = (int)(it - r * per_row) * 8;
+    float f[3][8];
+    if (r < rows) {
+      const float4 u = *reinterpret_cast<const float4*>(src + r * ld + j0);
+      const float4 v = *reinterpret_cast<const float4*>(src + r * ld + j0 + 4);
+      const float w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) split3(w[e], f[0][e], f[1][e], f[2][e]);
+    } else {
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[p][e] = 0.0f;
+    }
+#pragma unroll
+    for (int p = 0; p < 3; ++p)
+      *reinterpret_cast<uint4*>(dst + (p * plane + r) * hidden + j0) = pack16(f[p], (const bf16*)nullptr);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+// bf16 rows of `width` elements, `ld` apart; box 64 x box_rows, 128-byte swizzle.
+static bool map_rows(CUtensorMap* m, const void* ptr, int64_t rows, int64_t width, int64_t ld, int box_rows) {
+  cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  cuuint32_t es[2] = {1, 1};
+  return encode_fn() != nullptr &&
+         encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, es,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+static std::atomic<int> g_clusters[64];
+
+// Clusters of two CTAs that run at once, and the kernels' shared-memory limit
+// (set once per device; several host threads may come here).
+static cudaError_t prepare_device(int* clusters) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (g_clusters[dev] == 0) {
+    const void* fn[3] = {(const void*)linear_kernel<kStats>, (const void*)linear_kernel<kDlogit>,
+                         (const void*)linear_kernel<kGrad>};
+    int least = 1 << 30;
+    for (const void* f : fn) {
+      e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+      if (e != cudaSuccess) return e;
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 2;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.gridDim = dim3(2);
+      cfg.blockDim = dim3(THREADS);
+      cfg.dynamicSmemBytes = SMEM_BYTES;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int n = 0;
+      e = cudaOccupancyMaxActiveClusters(&n, f, &cfg);
+      if (e != cudaSuccess) return e;
+      if (n < least) least = n;
+    }
+    g_clusters[dev] = least > 0 ? least : -1;
+  }
+  *clusters = g_clusters[dev].load();
+  return *clusters > 0 ? cudaSuccess : cudaErrorNotSupported;
+}
+
+template <int KIND>
+static cudaError_t launch(const CUtensorMap& mX, const CUtensorMap& mW, const CUtensorMap& mD,
+                          const CUtensorMap& mDt, const Args& t, int64_t tiles, cudaStream_t st) {
+  int mc = 0;
+  cudaError_t e = prepare_device(&mc);
+  if (e != cudaSuccess) return e;
+  if (tiles <= 0) return cudaSuccess;
+  const int64_t ncl = tiles < mc ? tiles : mc;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)(2 * ncl));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, linear_kernel<KIND>, mX, mW, mD, mDt, t);
+  if (e != cudaSuccess) return e;
+  count_launch();
+  return cudaGetLastError();
+}
+
+static unsigned elementwise_grid(int64_t items) {
+  int64_t blocks = (items + 255) / 256;
+  const int64_t cap = (int64_t)tc_sm_count() * 16;
+  return (unsigned)(blocks > cap ? cap : blocks);
+}
+
+}  // namespace lin
+
+int linear_clusters() {
+  int mc = 0;
+  return lin::prepare_device(&mc) == cudaSuccess ? mc : 76;
+}
+
+LinearSplit linear_grad_split(int64_t rows, int64_t vocab, int hidden, int planes) {
+  // Tiles long against a pair's share of the work leave SMs idle at the end:
+  // split K until a part is at most a third of that share (at least 8 k-blocks
+  // a part, at most 16 parts, whose fp32 sums the reduction reads back).
+  const int64_t nth = (hidden + 255) / 256, mtr = (rows + 255) / 256, ntv = (vocab + 255) / 256;
+  const int64_t kbv = (vocab + 63) / 64, kbr = (rows + 63) / 64;
+  const int64_t total = mtr * nth * kbv + ntv * nth * kbr;
+  int64_t part = total / (76 * 3);
+  if (part < 8) part = 8;
+  auto splits = [&](int64_t kb) {
+    int64_t s = (kb + part - 1) / part;
+    return (int)(s < 1 ? 1 : (s > 16 ? 16 : s));
+  };
+  (void)planes;
+  return {splits(kbv), splits(kbr)};
+}
+
+cudaError_t launch_linear_logits(const LogitsArgs& a, cudaStream_t st) {
+  using namespace lin;
+  CUtensorMap mX, mW;
+  if (!map_rows(&mX, a.x, a.planes * a.x_plane, a.hidden, a.x_ld, BMC) ||
+      !map_rows(&mW, a.w, (a.planes - 1) * a.w_plane + a.w_rows, a.hidden, a.w_ld, BNC))
+    return cudaErrorInvalidValue;
+  Args t = {};
+  t.hidden = a.hidden;
+  t.planes = a.planes;
+  t.v0 = a.v0;
+  t.w_v0 = a.w_v0;
+  t.vcols = a.vcols;
+  t.vocab = a.vocab;
+  t.nrows = a.nrows;
+  t.rows_bound = a.rows_bound;
+  t.ctr = a.ctr;
+  t.flags = a.flags;
+  t.x_plane = a.x_plane;
+  t.w_plane = a.w_plane;
+  t.d_plane = a.rows_pad;
+  t.target = a.target;
+  t.stats = a.stats;
+  t.zt = a.zt;
+  t.rows_pad = a.rows_pad;
+  t.lse = a.lse;
+  t.g = a.g;
+  t.d = reinterpret_cast<bf16*>(a.d);
+  t.d_ld = a.d_ld;
+  const int64_t tiles = ((a.rows_bound + BM - 1) / BM) * ((a.vcols + BN - 1) / BN);
+  return a.gradient ? launch<kDlogit>(mX, mW, mX, mX, t, tiles, st)
+                    : launch<kStats>(mX, mW, mX, mX, t, tiles, st);
+}
+
+cudaError_t launch_linear_grad(const LinearGradArgs& a, cudaStream_t st) {
+  using namespace lin;
+  CUtensorMap mX, mW, mD, mDt;
+  const int64_t drows = a.planes * a.d_plane;
+  if (!map_rows(&mX, a.x, (a.planes - 1) * a.x_plane + a.x_rows, a.hidden, a.x_ld, BK) ||
+      !map_rows(&mW, a.w, (a.planes - 1) * a.w_plane + a.w_rows, a.hidden, a.w_ld, BK) ||
+      !map_rows(&mD, a.d, drows, a.d_ld, a.d_ld, BMC) || !map_rows(&mDt, a.d, drows, a.d_ld, a.d_ld, BK))
+    return cudaErrorInvalidValue;
+  Args t = {};
+  t.hidden = a.hidden;
+  t.planes = a.planes;
+  t.v0 = a.v0;
+  t.w_v0 = a.w_v0;
+  t.vcols = a.vcols;
+  t.vocab = a.vocab;
+  t.nrows = a.nrows;
+  t.rows_bound = a.rows_bound;
+  t.ctr = a.ctr;
+  t.flags = a.flags;
+  t.x_plane = a.x_plane;
+  t.w_plane = a.w_plane;
+  t.d_plane = a.d_plane;
+  t.rows_pad = a.rows_pad;
+  t.ks_dx = a.split.dx;
+  t.ks_dw = a.split.dw;
+  t.out_f32 = a.out_f32;
+  t.dx_part = a.dx_part;
+  t.accumulate = a.accumulate;
+  t.dx = a.dx;
+  t.rowmap = a.rowmap;
+  t.dx_add = a.dx_add;
+  t.dw = a.dw;
+  t.dw_part = a.dw_part;
+  t.dw_pad = a.dw_pad;
+  t.want_dx = a.dx_part != nullptr || a.dx != nullptr;
+  t.want_dw = a.dw_part != nullptr || a.dw != nullptr;
+  if ((t.want_dx && t.ks_dx > 1 && !a.dx_part) || (t.want_dw && t.ks_dw > 1 && !a.dw_part))
+    return cudaErrorInvalidValue;
+  const int64_t nth = (a.hidden + BN - 1) / BN;
+  const int64_t tiles = (t.want_dx ? ((a.rows_bound + BM - 1) / BM) * nth * t.ks_dx : 0) +
+                        (t.want_dw ? ((a.vcols + BN - 1) / BN) * nth * t.ks_dw : 0);
+  return launch<kGrad>(mX, mW, mD, mDt, t, tiles, st);
+}
+
+cudaError_t launch_reduce_parts(const float* part, int splits, int64_t part_stride, int64_t rows,
+                                int hidden, const int32_t* inv, const void* add, void* out, int out_f32,
+                                cudaStream_t st) {
+  if (rows <= 0) return cudaSuccess;
+  const unsigned grid = lin::elementwise_grid(rows * (hidden / 8));
+  if (out_f32)
+    lin::reduce_parts_kernel<float><<<grid, 256, 0, st>>>(part, splits, part_stride, rows, hidden, inv,
+                                                          reinterpret_cast<const float*>(add),
+                                                          reinterpret_cast<float*>(out));
+  else
+    lin::reduce_parts_kernel<bf16><<<grid, 256, 0, st>>>(part, splits, part_stride, rows, hidden, inv,
+                                                         reinterpret_cast<const bf16*>(add),
+                                                         reinterpret_cast<bf16*>(out));
+  count_launch();
+  return cudaGetLastError();
+}
+
+cudaError_t launch_planes(const float* src, int64_t ld, int64_t rows, int64_t rows_zero, int hidden,
+                          void* dst, int64_t plane, cudaStream_t st) {
+  if (rows_zero <= 0) return cudaSuccess;
+  lin::planes_kernel<<<lin::elementwise_grid(rows_zero * (hidden / 8)), 256, 0, st>>>(
+      src, ld, rows, rows_zero, hidden, reinterpret_cast<bf16*>(dst), plane);
+  count_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace moe

@@ -847,6 +847,7 @@ moe_status moe_get_device_status(void* ws, void* stream, uint32_t* bits) {
   if (v & kFlagRows) return MOE_ERR_ROWS;
   if (v & kFlagTimeout) return MOE_ERR_TIMEOUT;
   if (v & kFlagGather) return MOE_ERR_GATHER;
+  if (v & kFlagTarget) return MOE_ERR_TARGET;
   return MOE_OK;
 }
 
@@ -861,6 +862,7 @@ const char* moe_status_string(moe_status st) {
     case MOE_ERR_TIMEOUT: return "MOE_ERR_TIMEOUT";
     case MOE_ERR_ROWS: return "MOE_ERR_ROWS";
     case MOE_ERR_GATHER: return "MOE_ERR_GATHER";
+    case MOE_ERR_TARGET: return "MOE_ERR_TARGET";
   }
   return "MOE_ERR_UNKNOWN";
 }

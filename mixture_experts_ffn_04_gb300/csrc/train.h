@@ -1,0 +1,105 @@
+// train.h -- host-side plumbing of the training operators (vocabulary cross
+// entropy, router gradient): the dense tensor-core GEMMs they share and the
+// small kernels around them.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace moe {
+
+// fp32 operands go through the bf16 tensor cores as three bf16 planes
+// (x = x0 + x1 + x2, 8 mantissa bits each): planes of one operand are stacked
+// `plane` rows apart in one matrix.
+constexpr int kPlanesF32 = 3;
+
+// K or row tiles of the dense GEMMs: 256 x 256 output tiles, 64-wide k-blocks.
+constexpr int kLinTile = 256, kLinK = 64;
+
+// Work split of the gradient GEMM, the same on every device: rows is the
+// caller's bound (the real count may be smaller).
+struct LinearSplit {
+  int dx, dw;   // K splits of a dX tile (K = vocabulary), a dW tile (K = rows)
+};
+LinearSplit linear_grad_split(int64_t rows, int64_t vocab, int hidden, int planes);
+
+struct LogitsArgs {
+  int planes;              // 1: bf16 operands, kPlanesF32: fp32 in bf16 planes
+  const void* x;           // bf16 [planes * x_plane, x_ld], rows of `hidden`
+  int64_t x_ld, x_plane;
+  const void* w;           // bf16 [planes * w_plane, w_ld]
+  int64_t w_ld, w_plane, w_rows;   // w_rows: rows of one plane that exist
+  int hidden;
+  int64_t v0;              // first vocabulary column of this call; row of w it
+  int64_t w_v0;            // starts at
+  int64_t vcols;           // columns computed (the last ones may pass `vocab`)
+  int64_t vocab;
+  const int32_t* nrows;    // device: rows that count
+  int64_t rows_bound;
+  const int32_t* target;   // [rows] compacted targets
+  int32_t* ctr;            // zeroed tile counter
+  uint32_t* flags;
+  // statistics (gradient == false): (max, sum) of each row over each 128-wide
+  // half tile in log2 units at stats[(2 * tile + half) * rows_pad + row], and
+  // the target's logit
+  float2* stats;
+  float* zt;
+  int64_t rows_pad;
+  // gradient (gradient == true): d = g (exp(z - lse) - [v = target]) in bf16
+  // planes [planes * rows_pad, d_ld], zeros past the rows (to the tile) and
+  // past the vocabulary
+  bool gradient;
+  const float* lse;
+  const float* g;
+  void* d;
+  int64_t d_ld;
+};
+cudaError_t launch_linear_logits(const LogitsArgs& a, cudaStream_t st);
+
+struct LinearGradArgs {
+  int planes;
+  const void* d;           // bf16 [planes * d_plane, d_ld]: d [rows, vcols]
+  int64_t d_ld, d_plane;
+  const void* x;           // bf16 [planes * x_plane, x_ld]; rows past the count
+  int64_t x_ld, x_plane;   // up to a multiple of 64 finite (or past x_rows)
+  int64_t x_rows;
+  const void* w;           // bf16 [planes * w_plane, w_ld]
+  int64_t w_ld, w_plane, w_rows;
+  int hidden;
+  int64_t v0, w_v0, vcols, vocab;
+  const int32_t* nrows;    // device count, or NULL: rows_bound
+  int64_t rows_bound;
+  int32_t* ctr;
+  uint32_t* flags;
+  LinearSplit split;
+  int out_f32;             // type of dx and dw
+  // dx: fp32 partial sums [split.dx][rows_pad][hidden] (added to when
+  // accumulate), or straight to dx rows (row r to rowmap[r]; dx_add added)
+  float* dx_part;
+  int64_t rows_pad;
+  int accumulate;
+  void* dx;
+  const int32_t* rowmap;
+  const void* dx_add;
+  // dw rows v0 .. of [vocab, hidden], or fp32 partials
+  // [split.dw][dw_pad][hidden] of this call's columns
+  void* dw;
+  float* dw_part;
+  int64_t dw_pad;
+};
+cudaError_t launch_linear_grad(const LinearGradArgs& a, cudaStream_t st);
+
+// out[r] = sum of the splits' partial rows (+ add[r]), rounded once; row r of
+// the partials is inv[r] (inv == NULL: r), a negative inv gives a zero row.
+cudaError_t launch_reduce_parts(const float* part, int splits, int64_t part_stride, int64_t rows,
+                                int hidden, const int32_t* inv, const void* add, void* out,
+                                int out_f32, cudaStream_t st);
+
+// Rows of fp32 as bf16 planes (or bf16 rows copied): dst [planes][plane][hidden];
+// rows past `rows` up to `rows_zero` are zeros.
+cudaError_t launch_planes(const float* src, int64_t ld, int64_t rows, int64_t rows_zero, int hidden,
+                          void* dst, int64_t plane, cudaStream_t st);
+
+int linear_clusters();   // clusters of two SMs the device runs at once
+
+}  // namespace moe

@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(256) ce_prep_kernel(const PrepArgs a) {
 // Merge the row statistics of all half tiles (lanes: 32 rows, warps: slices of
 // the half tiles): M = max m, S = sum s 2^(m - M), lse = ln 2 (M + log2 S).  The
 // last block adds the rows' losses, in row order, in fp64.
-constexpr int kMergeWarps = 16;
+constexpr int kMergeWarps = 32;
 __global__ void __launch_bounds__(32 * kMergeWarps)
     ce_merge_kernel(const float2* __restrict__ stats, int64_t rows_pad, int parts,
                     const float* __restrict__ zt, const int32_t* __restrict__ rowmap,
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     const int64_t row = r0 + lane;
     float M = -INFINITY, S = 0.0f;
     if (row < n) {
-#pragma unroll 4
+#pragma unroll 8
       for (int p = warp; p < parts; p += kMergeWarps) {
         const float2 v = __ldcs(stats + p * rows_pad + row);
         const float m = fmaxf(M, v.x), mu = m == -INFINITY ? 0.0f : m;
@@ -321,9 +321,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
 
 cudaError_t run_prep(const CeShape& s, const CeLayout& L, char* ws, PrepArgs& p, cudaStream_t st) {
   p.T = s.T;
-  int64_t rpb = (s.T + 1023) / 1024;
-  rpb = (rpb + 31) / 32 * 32;
-  rpb = std::min<int64_t>(std::max<int64_t>(rpb, 32), 256);
+  // a warp a token up to 8192 tokens, then up to 32
+  int64_t rpb = ((s.T + 1023) / 1024 + 7) / 8 * 8;
+  rpb = std::min<int64_t>(std::max<int64_t>(rpb, 8), 256);
   p.rows_per_block = rpb;
   p.V = s.V;
   p.ignore = s.ignore;

@@ -21,12 +21,20 @@
 // sums are added in split order by a second kernel (no atomics: the result does
 // not depend on the order of the tiles).
 //
+// The tensor cores cut the fp32 accumulator off at each K = 16 step (measured:
+// the loss of one row over H = 2048 came out 4e-6 low in relative terms, as 128
+// truncations predict), so a tile is summed in chunks of k-blocks: each chunk in
+// one of the two TMEM accumulators, the chunks in fp32 registers with rounding to
+// nearest, which frees the accumulator as soon as it is read.  Chunks of 512 for
+// the loss and all fp32 products, 4096 for gradients that are
+// rounded to bf16 anyway.
+//
 // fp32 operands are three bf16 planes each; a tile's k-loop then runs over the
 // six plane products whose weight is above 2^-24, smallest first, into the same
 // fp32 accumulator.
 //
 // Roles in each CTA: warp 0 TMA producer, warp 1 TMEM and (even CTA) the MMA
-// issuer, warps 2-9 epilogue: two per 32-lane TMEM quarter, one per half of
+// issuer, warps 4-11 epilogue: two per 32-lane TMEM quarter, one per half of
 // the 256 columns.  Every wait is bounded; a CTA that gives up raises its abort
 // flag, its partner's waits run out in turn, and both meet at the closing
 // cluster barrier before TMEM is released.
@@ -56,7 +64,12 @@ constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int BOX_BYTES = 64 * BK * 2;
 constexpr int RING_BYTES = S * STAGE_BYTES;
 constexpr int EPI_WARPS = 8;
-constexpr int THREADS = 32 * (2 + EPI_WARPS);
+constexpr int THREADS = 32 * (4 + EPI_WARPS);
+// Registers a thread: 168 at launch (384 threads), then 56 in the role warps'
+// group and 224 in the two epilogue groups, which hold 128 sums each:
+// 56 + 2 * 224 <= 3 * 168.
+constexpr int ROLE_REGS = 56, EPI_REGS = 224;
+static_assert(ROLE_REGS + 2 * EPI_REGS <= 3 * 168, "register pool of the launch");
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int NSLOT = 4;
 constexpr int READERS = 4;          // of a tile slot: odd producer, MMA, two epilogues
@@ -67,6 +80,7 @@ constexpr int SMEM_BYTES = 1024 + RING_BYTES + BAR_BYTES + EPI_WARPS * OUT_WARP_
 static_assert(SMEM_BYTES <= 232448, "shared memory budget of one CTA");
 static_assert((2 * S + 5 + 3 * NSLOT + 1) * 8 + 12 <= BAR_BYTES, "barrier area");
 constexpr int kGroupM = 8;
+constexpr int kChunkExact = 8, kChunkBf16 = 64;   // k-blocks of 64
 
 // kind::f16: D fp32, A and B bf16, M = 256 over the pair, N = 256.
 constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) |
@@ -101,7 +115,34 @@ struct Args {
   float* dw_part;
   int64_t dw_pad;
   int want_dx, want_dw;
+  int chunk;   // k-blocks the tensor cores add up before the fp32 registers do
 };
+
+// Cluster-scope wait that lets the hardware suspend the thread (bounded like
+// wait2): a spinning warp takes issue slots and, under the power cap, clock.
+__device__ __forceinline__ bool wait_cl(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  auto ready = [&]() {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+  };
+  if (ready()) return true;
+  const long long t0 = clock64();
+  while (true) {
+    if (ready()) return true;
+    if (*abort_flag) return false;
+    if (clock64() - t0 > kWaitCycles) {
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
 
 __device__ __forceinline__ uint64_t mn_desc(uint32_t saddr) {
   uint64_t d = 0;
@@ -191,12 +232,21 @@ __device__ __forceinline__ float ex2(float v) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
+// b where i == j, else a: a select that stays one (the compiler would turn a
+// chain of them over an array into an indexed copy in local memory).
+__device__ __forceinline__ float pick(float a, float b, int i, int j) {
+  float r;
+  asm("{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %3, %4;\n\tselp.f32 %0, %2, %1, p;\n\t}\n"
+      : "=f"(r)
+      : "f"(a), "f"(b), "r"(i), "r"(j));
+  return r;
+}
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Write 32 rows x 32 bf16 columns (one row a lane in `packed`) through the
 // warp's staging slice as 16-byte pieces of whole rows.
 __device__ __forceinline__ void store_chunk(unsigned char* stage, int lane, const uint4 (&packed)[4],
-                                            int nvalid, bf16* base, int64_t ld, int ncols) {
+                                            bf16* base, int64_t ld) {
   unsigned char* my_row = stage + lane * OUT_ROW_BYTES;
 #pragma unroll
   for (int v = 0; v < 4; ++v) reinterpret_cast<uint4*>(my_row)[v] = packed[v];
@@ -205,9 +255,8 @@ __device__ __forceinline__ void store_chunk(unsigned char* stage, int lane, cons
   for (int i = 0; i < 4; ++i) {
     const int p = lane + 32 * i;
     const int rr = p >> 2, pc = p & 3;
-    if (rr < nvalid && pc * 8 < ncols)
-      *reinterpret_cast<uint4*>(base + (int64_t)rr * ld + pc * 8) =
-          *reinterpret_cast<const uint4*>(stage + rr * OUT_ROW_BYTES + pc * 16);
+    *reinterpret_cast<uint4*>(base + (int64_t)rr * ld + pc * 8) =
+        *reinterpret_cast<const uint4*>(stage + rr * OUT_ROW_BYTES + pc * 16);
   }
   __syncwarp();
 }
@@ -227,7 +276,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   volatile int64_t* s_etile = s_tile + NSLOT;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5 + 3 * NSLOT + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* s_ok = reinterpret_cast<volatile int*>(tmem_slot + 2);
   unsigned char* s_out = smem + RING_BYTES + BAR_BYTES;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -283,7 +331,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int slot = (int)(n % NSLOT);
     const uint32_t use = (uint32_t)(n / NSLOT);
     if (take) {
-      if (!wait2(tdrain(slot), (use & 1u) ^ 1u, abort_flag)) return -1;
+      if (!wait_cl(tdrain(slot), (use & 1u) ^ 1u, abort_flag)) return -1;
       int64_t t = reserve;
       reserve = (int64_t)atomicAdd(a.ctr, 1);
       if (t >= plan.total) t = -1;
@@ -294,12 +342,14 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_arrive_cluster(map_to_rank(tfill(slot), 1));
       return t;
     }
-    if (!wait2(tfill(slot), use & 1u, abort_flag)) return -1;
+    if (!wait_cl(tfill(slot), use & 1u, abort_flag)) return -1;
     const int64_t t = s_tile[slot];
     mbar_arrive_cluster(map_to_rank(tdrain(slot), 0));
     return t;
   };
 
+  if (warp < 4) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(ROLE_REGS));
   if (warp == 0 && lane == 0) {
     // ---------------- TMA producer ----------------
     int s = 0;
@@ -314,7 +364,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         int pa, pb;
         plane_pair(a.planes, pr, pa, pb);
         for (int kb = t.kb0; kb < t.kb1; ++kb) {
-          if (!wait2(empty(s), ph ^ 1u, abort_flag)) { ok = false; break; }
+          if (!wait_cl(empty(s), ph ^ 1u, abort_flag)) { ok = false; break; }
           const uint32_t sa = ring + s * STAGE_BYTES, sb = sa + A_BYTES;
           // both CTAs' bytes count on the even CTA's "full" barrier
           const uint32_t fb = map_to_rank(full(s), 0);
@@ -354,145 +404,146 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int64_t tile = next_tile(n, false);
       if (tile < 0) break;
       const Tile t = plan.decode(a, tile);
-      const int steps = (t.kb1 - t.kb0) * nprod;
-      if (steps == 0) continue;   // no rows: the epilogue writes zeros
+      const int steps = (t.kb1 - t.kb0) * nprod;   // 0 without rows: the epilogue writes zeros
       const uint32_t idesc = IDESC | (t.type == 2 ? IDESC_A_MN : 0u) | (t.type != 0 ? IDESC_B_MN : 0u);
-      if (!wait2(tempty(acc), aph ^ 1u, abort_flag)) break;
-      tc_fence_after();
-      const uint32_t d = tmem_base + (uint32_t)acc * BN;
-      for (int i = 0; i < steps; ++i) {
-        if (!wait2(full(s), ph, abort_flag)) { ok = false; break; }
+      for (int i0 = 0; i0 < steps && ok; i0 += a.chunk) {
+        const int i1 = min(steps, i0 + a.chunk);
+        if (!wait_cl(tempty(acc), aph ^ 1u, abort_flag)) { ok = false; break; }
         tc_fence_after();
-        const uint32_t sa = ring + s * STAGE_BYTES, sb = sa + A_BYTES;
+        const uint32_t d = tmem_base + (uint32_t)acc * BN;
+        for (int i = i0; i < i1; ++i) {
+          if (!wait_cl(full(s), ph, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t sa = ring + s * STAGE_BYTES, sb = sa + A_BYTES;
 #pragma unroll
-        for (int kk = 0; kk < BK / 16; ++kk) {
-          const uint64_t ad = KIND == kGrad && t.type == 2 ? mn_desc(sa + kk * 2048) : sw128_desc(sa + kk * 32);
-          const uint64_t bd = KIND == kGrad ? mn_desc(sb + kk * 2048) : sw128_desc(sb + kk * 32);
-          mma2(d, ad, bd, idesc, (i | kk) != 0 ? 1u : 0u);
+          for (int kk = 0; kk < BK / 16; ++kk) {
+            const uint64_t ad = KIND == kGrad && t.type == 2 ? mn_desc(sa + kk * 2048) : sw128_desc(sa + kk * 32);
+            const uint64_t bd = KIND == kGrad ? mn_desc(sb + kk * 2048) : sw128_desc(sb + kk * 32);
+            mma2(d, ad, bd, idesc, (i != i0 || kk != 0) ? 1u : 0u);
+          }
+          commit2_both(empty(s));
+          if (++s == S) { s = 0; ph ^= 1u; }
         }
-        commit2_both(empty(s));
-        if (++s == S) { s = 0; ph ^= 1u; }
+        if (!ok) break;
+        commit2_both(tfull(acc));
+        acc ^= 1;
+        if (acc == 0) aph ^= 1u;
       }
-      if (!ok) break;
-      commit2_both(tfull(acc));
-      acc ^= 1;
-      if (acc == 0) aph ^= 1u;
     }
     if (*abort_flag) {
       commit2_self(final_bar);
       wait2_quiet(final_bar, 0);
     }
-  } else if (warp >= 2) {
-    // ---------------- epilogue (warps 2..9, both CTAs) ----------------
+  }
+  } else {
+    // ---------------- epilogue (warps 4..11, both CTAs) ----------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
     const int q = warp & 3;                 // TMEM lanes 32q .. 32q+31
-    const int half = (warp - 2) / 4;        // columns 128 half ..
-    const int c_lo = half * (BN / 2), c_hi = c_lo + BN / 2;
-    const int et = threadIdx.x - 64;
-    unsigned char* stage = s_out + (warp - 2) * OUT_WARP_BYTES;
+    const int half = (warp - 4) / 4;        // columns 128 half ..
+    const int c_lo = half * (BN / 2);
+    const int et = threadIdx.x - 128;
+    unsigned char* stage = s_out + (warp - 4) * OUT_WARP_BYTES;
     auto epi_bar = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(32 * EPI_WARPS) : "memory"); };
     int acc = 0;
     uint32_t aph = 0;
     for (int64_t n = 0;; ++n) {
-      if (et == 0) {
-        const int64_t tl = next_tile(n, false);
-        bool live = tl >= 0;
-        if (live) {
-          const Tile t = plan.decode(a, tl);
-          if (t.kb1 > t.kb0) live = wait2(tfull(acc), aph, abort_flag);
-        }
-        *s_etile = tl;
-        *s_ok = live ? 1 : 0;
-      }
+      if (et == 0) *s_etile = next_tile(n, false);
       epi_bar();
-      const int okv = *s_ok;
       const int64_t tile = *s_etile;
       epi_bar();
-      if (!okv) break;
+      if (tile < 0) break;
       const Tile t = plan.decode(a, tile);
-      const bool none = t.kb1 == t.kb0;     // no k-blocks: the product is zero
-      tc_fence_after();
-      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)acc * BN;
+      const int steps = (t.kb1 - t.kb0) * nprod;
+      // this lane's row of the tile, 128 columns, summed over the chunks
+      float f[BN / 2];
+#pragma unroll
+      for (int j = 0; j < BN / 2; ++j) f[j] = 0.0f;
+      bool ok = true;
+#pragma unroll 1
+      for (int i0 = 0; i0 < steps; i0 += a.chunk) {
+        int w = 1;
+        if (lane == 0) w = wait_cl(tfull(acc), aph, abort_flag) ? 1 : 0;
+        ok = __shfl_sync(0xffffffffu, w, 0);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)acc * BN + c_lo;
+#pragma unroll
+        for (int c = 0; c < BN / 2; c += 32) {
+          uint32_t r[32];
+          tmem_ld32(taddr + c, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) f[c + j] += __uint_as_float(r[j]);
+        }
+        tc_fence_before();
+        mbar_arrive_cluster(map_to_rank(tempty(acc), 0));
+        acc ^= 1;
+        if (acc == 0) aph ^= 1u;
+      }
+      if (!ok) break;
       const int64_t row0 = (int64_t)t.mt * BM + (int64_t)rank * BMC + q * 32;
       const int64_t row = row0 + lane;
       if (KIND == kStats) {
-        // running maximum and sum of the row over this half of the tile, in
-        // log2 units: the maximum kept is the rounded z * log2(e), so the
-        // sum's scale and the maximum agree exactly
+        // maximum and sum of the row over this half of the tile, in log2 units:
+        // the maximum kept is the rounded z * log2(e), so the sum's scale and
+        // the maximum agree exactly
         const bool live = row < plan.rows;
-        const int64_t col0 = a.v0 + (int64_t)t.nt * BN;
-        const int tg = live ? a.target[row] : -1;
-        float m = -INFINITY, sum = 0.0f;
-#pragma unroll 1
-        for (int c = c_lo; c < c_hi; c += 32) {
-          uint32_t r[32];
-          tmem_ld32(taddr + c, r);
-          tmem_wait_ld();
-          const int64_t left = a.vocab - (col0 + c);
-          if (left < 32) {
+        const int64_t col0 = a.v0 + (int64_t)t.nt * BN + c_lo;
+        const int64_t left = a.vocab - col0;
+        if (left < BN / 2) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (j >= left) r[j] = 0xFF800000u;
-          }
-          const int64_t dt = (int64_t)tg - (col0 + c);
-          if (dt >= 0 && dt < 32) {
-            float zt = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (j == (int)dt) zt = __uint_as_float(r[j]);
-            a.zt[row] = zt;
-          }
-          float mx = __uint_as_float(r[0]);
-#pragma unroll
-          for (int j = 1; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(r[j]));
-          const float mn = fmaxf(m, mx * kLog2e);
-          const float mu = mn == -INFINITY ? 0.0f : mn;
-          float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            s0 += ex2(fmaf(__uint_as_float(r[j]), kLog2e, -mu));
-            s1 += ex2(fmaf(__uint_as_float(r[j + 1]), kLog2e, -mu));
-          }
-          sum = sum * ex2(m - mu) + (s0 + s1);
-          m = mn;
+          for (int j = 0; j < BN / 2; ++j)
+            if (j >= left) f[j] = -INFINITY;
         }
+        const int64_t dt = live ? (int64_t)a.target[row] - col0 : -1;
+        if (dt >= 0 && dt < BN / 2) {
+          float zt = 0.0f;
+#pragma unroll
+          for (int j = 0; j < BN / 2; ++j) zt = pick(zt, f[j], (int)dt, j);
+          a.zt[row] = zt;
+        }
+        float m4[4] = {f[0], f[1], f[2], f[3]};
+#pragma unroll
+        for (int j = 4; j < BN / 2; ++j) m4[j & 3] = fmaxf(m4[j & 3], f[j]);
+        const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * kLog2e;
+        const float mu = m == -INFINITY ? 0.0f : m;
+        float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < BN / 2; ++j) s4[j & 3] += ex2(fmaf(f[j], kLog2e, -mu));
         if (live)
-          a.stats[(2 * (a.v0 / BN + t.nt) + half) * a.rows_pad + row] = make_float2(m, sum);
+          a.stats[(2 * (a.v0 / BN + t.nt) + half) * a.rows_pad + row] =
+              make_float2(m, (s4[0] + s4[1]) + (s4[2] + s4[3]));
       } else if (KIND == kDlogit) {
         const bool live = row < plan.rows;
-        const int64_t col0 = a.v0 + (int64_t)t.nt * BN;
-        const int tg = live ? a.target[row] : -1;
+        const int64_t col0 = a.v0 + (int64_t)t.nt * BN + c_lo;
+        const int64_t left = a.vocab - col0;
+        const int64_t dt = live ? (int64_t)a.target[row] - col0 : -1;
         const float l2 = live ? a.lse[row] * kLog2e : 0.0f;
         const float g = live ? a.g[row] : 0.0f;
-        bf16* drow = a.d + row0 * a.d_ld + (int64_t)t.nt * BN;
-#pragma unroll 1
-        for (int c = c_lo; c < c_hi; c += 32) {
-          uint32_t r[32];
-          tmem_ld32(taddr + c, r);
-          tmem_wait_ld();
-          const int64_t left = a.vocab - (col0 + c);
-          const int64_t dt = (int64_t)tg - (col0 + c);
-          float f[32];
+        bf16* drow = a.d + row0 * a.d_ld + (int64_t)t.nt * BN + c_lo;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) f[j] = ex2(fmaf(__uint_as_float(r[j]), kLog2e, -l2));
-          if (dt >= 0 && dt < 32) {
+        for (int j = 0; j < BN / 2; ++j) f[j] = ex2(fmaf(f[j], kLog2e, -l2)) * g;
+        if (dt >= 0 && dt < BN / 2) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (j == (int)dt) f[j] -= 1.0f;
-          }
+          for (int j = 0; j < BN / 2; ++j) f[j] = pick(f[j], f[j] - g, (int)dt, j);
+        }
+        if (!live || left < BN / 2) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) f[j] = live && j < left ? f[j] * g : 0.0f;
+          for (int j = 0; j < BN / 2; ++j) f[j] = live && j < left ? f[j] : 0.0f;
+        }
+#pragma unroll
+        for (int c = 0; c < BN / 2; c += 32) {
           for (int p = 0; p < a.planes; ++p) {
             uint4 pk[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) pk[j] = pack16(f + 8 * j, (const bf16*)nullptr);
-            store_chunk(stage, lane, pk, 32, drow + p * a.d_plane * a.d_ld + c, a.d_ld, 32);
+            for (int j = 0; j < 4; ++j) pk[j] = pack16(f + c + 8 * j, (const bf16*)nullptr);
+            store_chunk(stage, lane, pk, drow + p * a.d_plane * a.d_ld + c, a.d_ld);
             if (p + 1 < a.planes) {
-              // what this plane leaves for the next one (0 where it is exact
-              // or not finite)
+              // what this plane leaves for the next one
 #pragma unroll
               for (int j = 0; j < 32; ++j) {
-                const float rest = f[j] - __bfloat162float(__float2bfloat16_rn(f[j]));
-                f[j] = isfinite(rest) ? rest : 0.0f;
+                const float rest = f[c + j] - __bfloat162float(__float2bfloat16_rn(f[c + j]));
+                f[c + j] = isfinite(rest) ? rest : 0.0f;
               }
             }
           }
@@ -503,63 +554,35 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int64_t nv = rows_out - row0;
         const int nvalid = nv <= 0 ? 0 : (nv >= 32 ? 32 : (int)nv);
         float* part = is_dx ? a.dx_part : a.dw_part;
-        const int n0 = t.nt * BN;
+        const int n0 = t.nt * BN + c_lo;
         int64_t orow = row;     // where this lane's row goes
         if (is_dx && a.rowmap) orow = lane < nvalid ? a.rowmap[row] : 0;
         if (!is_dx) orow = a.v0 + row;
-#pragma unroll 1
-        for (int c = c_lo; c < c_hi && n0 + c < a.hidden; c += 32) {
-          uint32_t r[32];
-          if (none) {
+        float* fout = part ? part + ((int64_t)t.sp * (is_dx ? a.rows_pad : a.dw_pad) + row) * a.hidden
+                           : reinterpret_cast<float*>(is_dx ? a.dx : a.dw) + orow * a.hidden;
+        const float* fadd = part ? (is_dx && a.accumulate ? fout : nullptr)
+                                 : (is_dx && a.dx_add ? reinterpret_cast<const float*>(a.dx_add) + orow * a.hidden : nullptr);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) r[j] = 0u;
-          } else {
-            tmem_ld32(taddr + c, r);
-            tmem_wait_ld();
-          }
+        for (int c = 0; c < BN / 2; c += 32) {
           const int ncols = min(32, a.hidden - (n0 + c));   // a multiple of 8
-          if (part != nullptr) {
+          if (ncols <= 0) break;
+          if (part != nullptr || a.out_f32) {
             if (lane < nvalid) {
-              float* p = part + ((int64_t)t.sp * (is_dx ? a.rows_pad : a.dw_pad) + row) * a.hidden + n0 + c;
-              const bool add = is_dx && a.accumulate;
 #pragma unroll
               for (int v = 0; v < 8; ++v) {
                 if (4 * v >= ncols) break;
-                float4 o = make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
-                                       __uint_as_float(r[4 * v + 2]), __uint_as_float(r[4 * v + 3]));
-                if (add) {
-                  const float4 b = reinterpret_cast<const float4*>(p)[v];
+                float4 o = make_float4(f[c + 4 * v], f[c + 4 * v + 1], f[c + 4 * v + 2], f[c + 4 * v + 3]);
+                if (fadd) {
+                  const float4 b = reinterpret_cast<const float4*>(fadd + n0 + c)[v];
                   o.x += b.x; o.y += b.y; o.z += b.z; o.w += b.w;
                 }
-                reinterpret_cast<float4*>(p)[v] = o;
-              }
-            }
-          } else if (a.out_f32) {
-            if (lane < nvalid) {
-              float* o = reinterpret_cast<float*>(is_dx ? a.dx : a.dw) + orow * a.hidden + n0 + c;
-              const float* ad = is_dx && a.dx_add ? reinterpret_cast<const float*>(a.dx_add) + orow * a.hidden + n0 + c : nullptr;
-#pragma unroll
-              for (int v = 0; v < 8; ++v) {
-                if (4 * v >= ncols) break;
-                float4 f = make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
-                                       __uint_as_float(r[4 * v + 2]), __uint_as_float(r[4 * v + 3]));
-                if (ad) {
-                  const float4 b = reinterpret_cast<const float4*>(ad)[v];
-                  f.x += b.x; f.y += b.y; f.z += b.z; f.w += b.w;
-                }
-                reinterpret_cast<float4*>(o)[v] = f;
+                reinterpret_cast<float4*>(fout + n0 + c)[v] = o;
               }
             }
           } else {
-            float f[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(r[j]);
             bf16* out = reinterpret_cast<bf16*>(is_dx ? a.dx : a.dw);
-            uint4 pk[4];
-            // whole-row 16-byte pieces through the staging slice; the row of
-            // lane rr comes by shuffle (a compacted row goes to its token)
             if (is_dx && a.dx_add) {
-              // coalesced reads of the addend through the same slice
+              // the addend comes in whole-row pieces through the staging slice
               const bf16* addp = reinterpret_cast<const bf16*>(a.dx_add);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
@@ -576,16 +599,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                 float b[8];
                 unpack16(reinterpret_cast<const uint4*>(stage + lane * OUT_ROW_BYTES)[j], b, (const bf16*)nullptr);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[8 * j + e] += b[e];
+                for (int e = 0; e < 8; ++e) f[c + 8 * j + e] += b[e];
               }
               __syncwarp();
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              pk[j] = pack16(f + 8 * j, (const bf16*)nullptr);
-              reinterpret_cast<uint4*>(stage + lane * OUT_ROW_BYTES)[j] = pk[j];
-            }
+            for (int j = 0; j < 4; ++j)
+              reinterpret_cast<uint4*>(stage + lane * OUT_ROW_BYTES)[j] = pack16(f + c + 8 * j, (const bf16*)nullptr);
             __syncwarp();
+            // whole-row 16-byte pieces; a compacted row goes to its token
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int p = lane + 32 * i, rr = p >> 2, pc = p & 3;
@@ -597,12 +619,6 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncwarp();
           }
         }
-      }
-      if (!none) {
-        tc_fence_before();
-        mbar_arrive_cluster(map_to_rank(tempty(acc), 0));
-        acc ^= 1;
-        if (acc == 0) aph ^= 1u;
       }
     }
   }
@@ -829,6 +845,9 @@ cudaError_t launch_linear_logits(const LogitsArgs& a, cudaStream_t st) {
   t.g = a.g;
   t.d = reinterpret_cast<bf16*>(a.d);
   t.d_ld = a.d_ld;
+  // the logit gradient in bf16 takes no harm from the cut-off (about 1e-5 on a
+  // value rounded to 2^-9)
+  t.chunk = a.gradient && a.planes == 1 ? kChunkBf16 : kChunkExact;
   const int64_t tiles = ((a.rows_bound + BM - 1) / BM) * ((a.vcols + BN - 1) / BN);
   return a.gradient ? launch<kDlogit>(mX, mW, mX, mX, t, tiles, st)
                     : launch<kStats>(mX, mW, mX, mX, t, tiles, st);
@@ -860,6 +879,7 @@ cudaError_t launch_linear_grad(const LinearGradArgs& a, cudaStream_t st) {
   t.ks_dx = a.split.dx;
   t.ks_dw = a.split.dw;
   t.out_f32 = a.out_f32;
+  t.chunk = a.out_f32 ? kChunkExact : kChunkBf16;
   t.dx_part = a.dx_part;
   t.accumulate = a.accumulate;
   t.dx = a.dx;

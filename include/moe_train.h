@@ -107,7 +107,7 @@ moe_status moe_router_backward(const moe_shape *shape, const void *x, const void
  * A norm that is not finite thus leaves the gradients as they are, and the
  * caller, who has the norm, skips the step.  Squares are added in fp32 in
  * groups and in fp64 across them, in an order that depends on the list alone; a
- * group whose fp32 sum leaves the safe range is added again in fp64.
+ * group whose fp32 sum leaves the safe range is added again, scaled.
  * ------------------------------------------------------------------------- */
 typedef struct {
   const void *src;    /* device, aligned to its element */

@@ -72,6 +72,16 @@ class MoECeShape(ctypes.Structure):
                 ("w_stride", ctypes.c_int64)]
 
 
+class MoEGradTensor(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("src_dtype", ctypes.c_int32), ("dst_dtype", ctypes.c_int32)]
+
+
+class MoEGradPlan(ctypes.Structure):
+    _fields_ = [("tensors", ctypes.c_int64), ("chunks", ctypes.c_int64),
+                ("chunk_elems", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 class MoERouteInfo(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "topk_idx", "topk_w", "gate", "counts", "offsets", "scatter_index", "row_token",
@@ -138,6 +148,12 @@ def lib():
         "moe_linear_ce_workspace_bytes": (sz, [C]),
         "moe_linear_ce_forward": (i32, [C, P, P, P, P, P, P, P, sz, P]),
         "moe_linear_ce_backward": (i32, [C, P, P, P, P, P, P, P, P, sz, P]),
+        "moe_router_backward_workspace_bytes": (sz, [S]),
+        "moe_router_backward": (i32, [S, P, P, P, P, P, ctypes.c_double, ctypes.c_double, P, P, P,
+                                      P, P, sz, P]),
+        "moe_grad_clip_workspace_bytes": (sz, [P, i64]),
+        "moe_grad_clip_plan": (i32, [P, i64, ctypes.POINTER(MoEGradPlan), P, sz, P]),
+        "moe_grad_clip": (i32, [ctypes.POINTER(MoEGradPlan), ctypes.c_double, P, P, sz, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -532,6 +548,56 @@ def moe_linear_ce_backward(shape: MoECeShape, x, w, target, lse, dloss, dx, dw, 
         _stream(stream)), "moe_linear_ce_backward")
 
 
+def moe_router_backward_workspace_bytes(shape: MoEShape) -> int:
+    return int(lib().moe_router_backward_workspace_bytes(ctypes.byref(shape)))
+
+
+def moe_router_backward(shape: MoEShape, x, w_router, topk_idx, d_topk_w, d_gate, balance_coef,
+                        z_coef, dx_add, dx, dw_router, aux, ws, stream=None):
+    E, k = moe_topk_unpack(shape.topk_shape)
+    T, H, f32 = shape.tokens, shape.hidden, torch.float32
+    dt = f32 if shape.dtype == MOE_F32 else torch.bfloat16
+    rows = E + shape.shared_gate
+
+    def opt(t, n, d, name):
+        return None if t is None else _vec(t, n, d, name)
+
+    _check(lib().moe_router_backward(
+        ctypes.byref(shape), _vec(x, T * H, dt, "x"), _vec(w_router, rows * H, dt, "w_router"),
+        _vec(topk_idx, T * k, torch.int32, "topk_idx"), opt(d_topk_w, T * k, f32, "d_topk_w"),
+        opt(d_gate, T, f32, "d_gate"), balance_coef, z_coef, opt(dx_add, T * H, dt, "dx_add"),
+        _vec(dx, T * H, dt, "dx"), _vec(dw_router, rows * H, dt, "dw_router"),
+        opt(aux, 2, f32, "aux"), _p(ws), _nbytes(ws), _stream(stream)), "moe_router_backward")
+
+
+def grad_tensors(srcs, dsts):
+    """MoEGradTensor array over gradients and destinations (an entry of dsts is
+    None where only the norm counts)."""
+    arr = (MoEGradTensor * len(srcs))()
+    for e, s, d in zip(arr, srcs, dsts):
+        if d is not None and d.numel() != s.numel():
+            raise ValueError("a destination must hold as many elements as its gradient")
+        e.src, e.numel, e.src_dtype = _p(s), s.numel(), _dtype_code(s.dtype)
+        e.dst, e.dst_dtype = _p(d), _dtype_code((s if d is None else d).dtype)
+    return arr
+
+
+def moe_grad_clip_workspace_bytes(tensors) -> int:
+    return int(lib().moe_grad_clip_workspace_bytes(tensors, len(tensors)))
+
+
+def moe_grad_clip_plan(tensors, ws, stream=None) -> MoEGradPlan:
+    plan = MoEGradPlan()
+    _check(lib().moe_grad_clip_plan(tensors, len(tensors), ctypes.byref(plan), _p(ws), _nbytes(ws),
+                                    _stream(stream)), "moe_grad_clip_plan")
+    return plan
+
+
+def moe_grad_clip(plan: MoEGradPlan, max_norm: float, norm, ws, stream=None):
+    _check(lib().moe_grad_clip(ctypes.byref(plan), max_norm, _vec(norm, 1, torch.float32, "norm"),
+                               _p(ws), _nbytes(ws), _stream(stream)), "moe_grad_clip")
+
+
 # ---------------------------------------------------------------------------
 # conveniences over the ABI (allocation through torch, nothing else)
 # ---------------------------------------------------------------------------
@@ -658,3 +724,59 @@ class LinearCrossEntropy:
 
     def device_status(self, stream=None):
         return moe_get_device_status(self.ws, stream)
+
+
+class RouterGrad:
+    """Gradient of the top-k softmax router (with the balance and z losses):
+    shape, coefficients and a workspace over caller tensors."""
+
+    def __init__(self, tokens: int, hidden: int, experts: int, top_k: int, norm_topk: bool = True,
+                 shared_gate: bool = False, dtype=torch.bfloat16, balance_coef: float = 0.0,
+                 z_coef: float = 0.0, device="cuda"):
+        s = MoEShape()
+        s.tokens, s.hidden, s.moe_inter = tokens, hidden, 8   # moe_inter does not count here
+        s.shared_inter = 8 if shared_gate else 0
+        s.topk_shape = moe_topk_pack(experts, top_k)
+        s.shared_gate, s.norm_topk = int(shared_gate), int(norm_topk)
+        s.dtype, s.norm_eps = _dtype_code(dtype), 1e-6
+        self.shape, self.balance_coef, self.z_coef = s, balance_coef, z_coef
+        self.ws = _alloc_ws(moe_router_backward_workspace_bytes(s), device, None, "RouterGrad")
+
+    def backward(self, x, w_router, topk_idx, d_topk_w, d_gate=None, dx_add=None, dx=None,
+                 dw_router=None, aux=None, stream=None):
+        """(dx, dw_router, aux); dx includes dx_add (the experts' dx), aux [2]
+        holds the balance and z losses."""
+        dx = torch.empty_like(x) if dx is None else dx
+        dw_router = torch.empty_like(w_router) if dw_router is None else dw_router
+        if aux is None:
+            aux = torch.empty(2, dtype=torch.float32, device=x.device)
+        moe_router_backward(self.shape, x, w_router, topk_idx, d_topk_w, d_gate, self.balance_coef,
+                            self.z_coef, dx_add, dx, dw_router, aux, self.ws, stream)
+        return dx, dw_router, aux
+
+    def device_status(self, stream=None):
+        return moe_get_device_status(self.ws, stream)
+
+
+class GradClip:
+    """Global norm of a list of gradients, and clipping: in place, or into out
+    (one destination a gradient, fp32 or bf16).  The list's table is made once,
+    here; the tensors must stay where they are."""
+
+    def __init__(self, grads, out=None, stream=None):
+        self.grads, self.out = list(grads), list(grads if out is None else out)
+        if len(self.grads) != len(self.out):
+            raise ValueError("out must have one destination for every gradient")
+        if not self.grads:
+            raise ValueError("the list of gradients is empty")
+        device = self.grads[0].device
+        table = grad_tensors(self.grads, self.out)
+        self.ws = _alloc_ws(moe_grad_clip_workspace_bytes(table), device, stream, "GradClip")
+        self.plan = moe_grad_clip_plan(table, self.ws, stream)
+
+    def clip(self, max_norm: float, norm=None, stream=None):
+        """The norm [1] before clipping."""
+        if norm is None:
+            norm = torch.empty(1, dtype=torch.float32, device=self.ws.device)
+        moe_grad_clip(self.plan, max_norm, norm, self.ws, stream)
+        return norm

@@ -175,6 +175,11 @@ cudaError_t launch_hash_route(const Shape& s, const int32_t* token_ids, const in
                               int64_t vocab, int32_t* idx, float* w, uint32_t* flags,
                               cudaStream_t st);
 
+// Router GEMM into the scratch logits [nsplit][T][ldl] (partial sums over K
+// ranges, to be added in order).
+moe_status router_gemm(const Shape& s, const Layout& L, char* w, const void* x, const void* router,
+                       int* nsplit, cudaStream_t st);
+
 // Split-K factor for a tensor-core fp32-output GEMM of one group (router):
 // enough CTAs to cover the SMs, at most kMaxSplit, at least 4 k-blocks each.
 constexpr int kMaxSplit = 8;

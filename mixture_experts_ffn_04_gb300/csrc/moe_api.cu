@@ -303,6 +303,37 @@ cudaError_t launch_grouped_gemm(const GemmArgs& a, cudaStream_t st) {
   }
 }
 
+// Router GEMM into the scratch logits (split-K partial sums on the tensor
+// cores); returns the number of partials.
+moe_status router_gemm(const Shape& s, const Layout& L, char* w, const void* x, const void* router,
+                       int* nsplit, cudaStream_t st) {
+  float* logits = reinterpret_cast<float*>(w + L.logits);
+  GemmArgs ra;
+  ra.mode = kStoreF32;
+  ra.dtype = s.dtype;
+  ra.A = x;
+  ra.B0 = router;
+  ra.B1 = nullptr;
+  ra.bstride = 0;
+  ra.N = s.ncols;
+  ra.K = s.H;
+  ra.offsets = nullptr;
+  ra.G = 1;
+  ra.single_rows = s.T;
+  ra.rows_bound = s.T;
+  ra.out = logits;
+  ra.ldo = s.ldl;
+  ra.sched = reinterpret_cast<int32_t*>(w + L.sched_router);
+  ra.flags = reinterpret_cast<uint32_t*>(w + L.flags);
+  // On the tensor cores the router is split over K so that its few m-tiles
+  // still cover the SMs; the top-k kernel adds the partial sums in order.
+  ra.ksplit = engine_for(ra) == 2 ? router_split(s.T, s.ncols, s.H) : 1;
+  ra.split_stride = s.T * (int64_t)s.ldl;
+  CHECK_CUDA(launch_grouped_gemm(ra, st));
+  *nsplit = ra.ksplit;
+  return MOE_OK;
+}
+
 }  // namespace moe
 
 using namespace moe;
@@ -374,37 +405,6 @@ moe_status moe_quantize_mxfp8(const void* w, int32_t dtype, int64_t batch, int64
 moe_status moe_workspace_init(void* ws, void* stream) {
   if (!ws) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
   CHECK_CUDA(cudaMemsetAsync(ws, 0, 256, (cudaStream_t)stream));
-  return MOE_OK;
-}
-
-// Router GEMM into the scratch logits (split-K partial sums on the tensor
-// cores); returns the number of partials.
-static moe_status router_gemm(const Shape& s, const Layout& L, char* w, const void* x,
-                              const void* router, int* nsplit, cudaStream_t st) {
-  float* logits = reinterpret_cast<float*>(w + L.logits);
-  GemmArgs ra;
-  ra.mode = kStoreF32;
-  ra.dtype = s.dtype;
-  ra.A = x;
-  ra.B0 = router;
-  ra.B1 = nullptr;
-  ra.bstride = 0;
-  ra.N = s.ncols;
-  ra.K = s.H;
-  ra.offsets = nullptr;
-  ra.G = 1;
-  ra.single_rows = s.T;
-  ra.rows_bound = s.T;
-  ra.out = logits;
-  ra.ldo = s.ldl;
-  ra.sched = reinterpret_cast<int32_t*>(w + L.sched_router);
-  ra.flags = reinterpret_cast<uint32_t*>(w + L.flags);
-  // On the tensor cores the router is split over K so that its few m-tiles
-  // still cover the SMs; the top-k kernel adds the partial sums in order.
-  ra.ksplit = engine_for(ra) == 2 ? router_split(s.T, s.ncols, s.H) : 1;
-  ra.split_stride = s.T * (int64_t)s.ldl;
-  CHECK_CUDA(launch_grouped_gemm(ra, st));
-  *nsplit = ra.ksplit;
   return MOE_OK;
 }
 

@@ -25,6 +25,9 @@ namespace {
 constexpr int64_t kDlogitBytes = 256ll << 20;   // logit gradient of one piece
 constexpr int64_t kPlaneBytes = 512ll << 20;    // bf16 planes of one piece of an fp32 W
 
+// the few-row forward: rows of x, warps a block, blocks an SM, shared memory of x
+constexpr int kSkinnyRows = 4, kSkinnyWarps = 8, kSkinnyPerSm = 2, kSkinnySmem = 112 * 1024;
+
 struct CeShape {
   int64_t T, x_ld, w_ld;
   int H, V, dtype, reduction, ignore, esize, planes;
@@ -75,7 +78,7 @@ struct CeLayout {
   int64_t nctr;
   LinearSplit split;
   bool dx_direct, dw_direct;
-  size_t flags, meta, ctr, rowmap, inv, tgt, g, lse, zt, loss, xc, wpl, stats, d, dx_part, dw_part, total;
+  size_t flags, skinny, meta, ctr, rowmap, inv, tgt, g, lse, zt, loss, xc, wpl, stats, d, dx_part, dw_part, total;
 };
 
 CeLayout layout_ce(const CeShape& s) {
@@ -100,7 +103,8 @@ CeLayout layout_ce(const CeShape& s) {
     return at;
   };
   const size_t T = (size_t)L.rows_pad;
-  L.flags = take(256);
+  L.flags = take(256);   // status word; the few-row kernel's ticket at +32
+  L.skinny = take(s.T <= kSkinnyRows ? (size_t)tc_sm_count() * kSkinnyPerSm * kSkinnyRows * 8 : 0);
   L.meta = take(256);   // rows that count, the merge's ticket
   L.ctr = take((size_t)L.nctr * 4);
   L.rowmap = take(T * 4);
@@ -319,6 +323,174 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   }
 }
 
+// Loss of at most R = 4 rows in one launch: W streams by once, a warp takes NV
+// vocabulary rows at a time (all lanes across the row, 16 bytes a load) against
+// the rows of x in shared memory (fp32), keeps a running maximum and sum per row
+// of x, and the last block merges the blocks.  Bound by HBM: one token against
+// 50257 x 2048 bf16 reads 206 MB.
+struct SkinnyArgs {
+  const void *x, *w;
+  int64_t x_ld, w_ld;
+  const int32_t* target;
+  int T, H, V, ignore, reduction;
+  float *loss, *lse, *total;
+  float2* part;      // [grid][4]
+  float* zt;         // [4]
+  int32_t* ticket;   // 0 between calls
+  uint32_t* flags;
+};
+__device__ __forceinline__ void merge_ms(float& M, float& S, float m, float s) {
+  const float n = fmaxf(M, m), mu = n == -INFINITY ? 0.0f : n;
+  S = S * exp2f(M - mu) + s * exp2f(m - mu);
+  M = n;
+}
+template <typename T, int R, int NV>
+__global__ void __launch_bounds__(32 * kSkinnyWarps) ce_skinny_kernel(const SkinnyArgs a) {
+  extern __shared__ __align__(16) float s_x[];   // [R][H]
+  __shared__ float2 s_ms[kSkinnyWarps][R];
+  __shared__ int s_last;
+  constexpr int N = Vec16<T>::N;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int tg[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    tg[r] = r < a.T ? a.target[r] : a.ignore;
+    if (!counts(tg[r], a.V, a.ignore)) {
+      if (r < a.T && tg[r] != a.ignore && blockIdx.x == 0 && threadIdx.x == 0) set_flag(a.flags, kFlagTarget);
+      tg[r] = -1;
+    }
+    const T* xr = reinterpret_cast<const T*>(a.x) + r * a.x_ld;
+    for (int i = threadIdx.x; i < a.H; i += blockDim.x) s_x[r * a.H + i] = tg[r] >= 0 ? to_f(xr[i]) : 0.0f;
+  }
+  __syncthreads();
+  float M[R], S[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) { M[r] = -INFINITY; S[r] = 0.0f; }
+  const T* w = reinterpret_cast<const T*>(a.w);
+  const int64_t stride = (int64_t)gridDim.x * kSkinnyWarps * NV;
+  for (int64_t v0 = ((int64_t)blockIdx.x * kSkinnyWarps + warp) * NV; v0 < a.V; v0 += stride) {
+    float acc[NV][R];
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int r = 0; r < R; ++r) acc[v][r] = 0.0f;
+    const T* wr[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) wr[v] = w + min(v0 + v, (int64_t)a.V - 1) * a.w_ld;
+#pragma unroll 4
+    for (int i = lane * N; i < a.H; i += 32 * N) {
+      uint4 u[NV];
+#pragma unroll
+      for (int v = 0; v < NV; ++v) u[v] = __ldcs(reinterpret_cast<const uint4*>(wr[v] + i));
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        float f[N];
+        unpack16(u[v], f, (const T*)nullptr);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int e = 0; e < N; e += 4) {
+            const float4 xv = *reinterpret_cast<const float4*>(s_x + r * a.H + i + e);
+            acc[v][r] = fmaf(f[e], xv.x, acc[v][r]);
+            acc[v][r] = fmaf(f[e + 1], xv.y, acc[v][r]);
+            acc[v][r] = fmaf(f[e + 2], xv.z, acc[v][r]);
+            acc[v][r] = fmaf(f[e + 3], xv.w, acc[v][r]);
+          }
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float z = acc[v][r];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        if (v0 + v < a.V) {
+          if (lane == 0 && tg[r] == (int)(v0 + v)) a.zt[r] = z;
+          merge_ms(M[r], S[r], z * 1.4426950408889634f, 1.0f);
+        }
+      }
+  }
+  if (lane == 0)
+#pragma unroll
+    for (int r = 0; r < R; ++r) s_ms[warp][r] = make_float2(M[r], S[r]);
+  __syncthreads();
+  if (threadIdx.x < R) {
+    float m = -INFINITY, s = 0.0f;
+    for (int k = 0; k < kSkinnyWarps; ++k) merge_ms(m, s, s_ms[k][threadIdx.x].x, s_ms[k][threadIdx.x].y);
+    a.part[blockIdx.x * kSkinnyRows + threadIdx.x] = make_float2(m, s);
+  }
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) s_last = atomicAdd(a.ticket, 1) == (int)gridDim.x - 1;
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  __shared__ float s_loss[R];
+  if (warp < R) {
+    const int r = warp;
+    float m = -INFINITY, s = 0.0f;
+    for (int b = lane; b < (int)gridDim.x; b += 32) {
+      const float2 p = __ldcg(a.part + b * kSkinnyRows + r);
+      merge_ms(m, s, p.x, p.y);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
+      merge_ms(m, s, m2, s2);
+    }
+    if (lane == 0 && r < a.T) {
+      const bool ok = counts(a.target[r], a.V, a.ignore);
+      const float l = ok ? 0.6931471805599453f * (m + log2f(s)) : 0.0f;
+      const float each = ok ? l - __ldcg(a.zt + r) : 0.0f;
+      if (a.lse) a.lse[r] = l;
+      if (a.loss) a.loss[r] = each;
+      s_loss[r] = each;
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    if (a.total) {
+      double t = 0.0;
+      int n = 0;
+      for (int r = 0; r < a.T; ++r)
+        if (counts(a.target[r], a.V, a.ignore)) {
+          t += (double)s_loss[r];
+          ++n;
+        }
+      if (a.reduction == MOE_CE_MEAN && n > 0) t /= (double)n;
+      *a.total = (float)t;
+    }
+    *a.ticket = 0;
+  }
+}
+
+template <typename T>
+cudaError_t launch_skinny(const SkinnyArgs& a, cudaStream_t st) {
+  const int rows = a.T <= 1 ? 1 : a.T <= 2 ? 2 : 4;
+  const size_t smem = (size_t)rows * a.H * 4;
+  auto go = [&](auto kernel, int nv) {
+    if (smem > 40 * 1024) {
+      cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      if (e != cudaSuccess) return e;
+    }
+    const int64_t want = ((int64_t)a.V + kSkinnyWarps * nv - 1) / (kSkinnyWarps * nv);
+    const int64_t blocks = std::min<int64_t>(want, (int64_t)tc_sm_count() * kSkinnyPerSm);
+    kernel<<<(unsigned)blocks, 32 * kSkinnyWarps, smem, st>>>(a);
+    count_launch();
+    return cudaGetLastError();
+  };
+  if (rows == 1) return go(ce_skinny_kernel<T, 1, 2>, 2);
+  if (rows == 2) return go(ce_skinny_kernel<T, 2, 2>, 2);
+  return go(ce_skinny_kernel<T, 4, 4>, 4);
+}
+
+// Up to four rows stream W once on the CUDA cores; above, the tensor cores'
+// tiles (which do the work of 256 rows whatever T is) are faster.
+bool skinny_ok(const CeShape& s) {
+  return s.T >= 1 && s.T <= kSkinnyRows && (size_t)(s.T <= 2 ? s.T : 4) * s.H * 4 <= (size_t)kSkinnySmem;
+}
+
 cudaError_t run_prep(const CeShape& s, const CeLayout& L, char* ws, PrepArgs& p, cudaStream_t st) {
   p.T = s.T;
   // a warp a token up to 8192 tokens, then up to 32
@@ -400,6 +572,28 @@ extern "C" moe_status moe_linear_ce_forward(const moe_ce_shape* shape, const voi
   if (e != MOE_OK) return e;
   char* b = static_cast<char*>(ws);
   cudaStream_t st = (cudaStream_t)stream;
+  if (skinny_ok(s)) {
+    SkinnyArgs k = {};
+    k.x = x;
+    k.w = w;
+    k.x_ld = s.x_ld;
+    k.w_ld = s.w_ld;
+    k.target = target;
+    k.T = (int)s.T;
+    k.H = s.H;
+    k.V = s.V;
+    k.ignore = s.ignore;
+    k.reduction = s.reduction;
+    k.loss = loss;
+    k.lse = lse;
+    k.total = total;
+    k.part = reinterpret_cast<float2*>(b + L.skinny);
+    k.zt = reinterpret_cast<float*>(b + L.zt);
+    k.flags = reinterpret_cast<uint32_t*>(b);
+    k.ticket = reinterpret_cast<int32_t*>(b) + 8;
+    CHECK_CUDA(s.dtype == MOE_F32 ? launch_skinny<float>(k, st) : launch_skinny<bf16>(k, st));
+    return MOE_OK;
+  }
   PrepArgs p = {};
   p.target = target;
   p.x = x;

@@ -10,8 +10,8 @@
 // the scaling pass downwards: what the norm pass read last is still in L2 when
 // the scaling pass starts.
 //
-// Each chunk's squares are added in fp32 (at most kChunk / 256 in a row in one
-// thread) and its sum goes to the workspace; the last block to finish adds the
+// Each chunk's squares are added in fp32 (at most 64 in a row in each of
+// four sums of a thread) and its sum goes to the workspace; the last block to finish adds the
 // chunks in fp64 in chunk order (no atomics on the sums, so the norm is the same
 // in every run).  A chunk whose fp32 sum overflowed, or is small enough for
 // squares to have underflowed, is added again with its values scaled by a power
@@ -26,7 +26,10 @@
 namespace moe {
 namespace {
 
-constexpr int kChunk = 16384;   // elements
+// Elements of a chunk: the power of two that gives about eight chunks an SM, so
+// that a small list covers the GPU and a large one spends little on table
+// look-ups and block sums.
+constexpr int kChunkMin = 2048, kChunkMax = 65536;
 constexpr int kThreads = 256;
 
 struct Entry {
@@ -46,10 +49,11 @@ __global__ void table_kernel(const __grid_constant__ Batch b, int n, Entry* tabl
   if ((int)threadIdx.x < n) table[at + threadIdx.x] = b.e[threadIdx.x];
 }
 // chunk -> tensor
-__global__ void __launch_bounds__(256) chunks_kernel(const Entry* table, int64_t tensors, int32_t* owner) {
+__global__ void __launch_bounds__(256) chunks_kernel(const Entry* table, int64_t tensors, int32_t* owner,
+                                                      int64_t chunk) {
   for (int64_t t = blockIdx.x; t < tensors; t += gridDim.x) {
     const Entry e = table[t];
-    const int64_t n = (e.numel + kChunk - 1) / kChunk;
+    const int64_t n = (e.numel + chunk - 1) / chunk;
     for (int64_t c = threadIdx.x; c < n; c += blockDim.x) owner[e.first + c] = (int32_t)t;
   }
 }
@@ -60,15 +64,16 @@ struct Span {
   int64_t n;
   int sd, dd;
 };
-__device__ __forceinline__ Span span_of(const Entry* table, const int32_t* owner, int64_t c) {
+__device__ __forceinline__ Span span_of(const Entry* table, const int32_t* owner, int64_t c,
+                                           int64_t chunk) {
   const Entry e = table[owner[c]];
-  const int64_t at = (c - e.first) * kChunk;
+  const int64_t at = (c - e.first) * chunk;
   Span s;
   s.sd = e.src_dtype;
   s.dd = e.dst_dtype;
   s.src = reinterpret_cast<const char*>(e.src) + at * (s.sd == MOE_F32 ? 4 : 2);
   s.dst = e.dst ? reinterpret_cast<char*>(e.dst) + at * (s.dd == MOE_F32 ? 4 : 2) : nullptr;
-  s.n = e.numel - at < kChunk ? e.numel - at : kChunk;
+  s.n = e.numel - at < chunk ? e.numel - at : chunk;
   return s;
 }
 
@@ -145,12 +150,12 @@ struct Head {   // the workspace's first bytes
 
 __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const Entry* table, const int32_t* owner,
                                                              int64_t chunks, double* sums, Head* head,
-                                                             double max_norm, float* norm) {
+                                                             double max_norm, float* norm, int64_t chunk) {
   __shared__ float sh[kThreads / 32];
   __shared__ double shd[kThreads / 32];
   __shared__ int s_last;
   for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const Span s = span_of(table, owner, c);
+    const Span s = span_of(table, owner, c, chunk);
     auto squares = [&](float scale) {
       return (double)block_sum(s.sd == MOE_F32 ? chunk_squares<float>(s, scale) : chunk_squares<bf16>(s, scale), sh);
     };
@@ -235,10 +240,11 @@ __device__ __forceinline__ void scale_chunk(const Span& s, float coef) {
 }
 
 __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const Entry* table, const int32_t* owner,
-                                                              int64_t chunks, const Head* head) {
+                                                              int64_t chunks, const Head* head,
+                                                              int64_t chunk) {
   const float coef = head->coef;
   for (int64_t i = blockIdx.x; i < chunks; i += gridDim.x) {
-    const Span s = span_of(table, owner, chunks - 1 - i);
+    const Span s = span_of(table, owner, chunks - 1 - i, chunk);
     if (s.dst == nullptr || (coef == 1.0f && s.dst == s.src)) continue;
     if (s.sd == MOE_F32) {
       if (s.dd == MOE_F32) scale_chunk<float, float>(s, coef);
@@ -269,12 +275,12 @@ ClipLayout layout_clip(int64_t tensors, int64_t chunks) {
   return L;
 }
 
-moe_status check_list(const moe_grad_tensor* t, int64_t n, int64_t* chunks, const char** why) {
+moe_status check_list(const moe_grad_tensor* t, int64_t n, int64_t* chunks, int* chunk, const char** why) {
   if (n < 0 || n > 0x7fffffff || (n > 0 && !t)) {
     *why = "tensors must be an array of n >= 0 entries";
     return MOE_ERR_INVALID_ARG;
   }
-  int64_t c = 0;
+  int64_t c = 0, all = 0;
   for (int64_t i = 0; i < n; ++i) {
     for (int32_t d : {t[i].src_dtype, t[i].dst_dtype})
       if (d != MOE_F32 && d != MOE_BF16) {
@@ -294,8 +300,11 @@ moe_status check_list(const moe_grad_tensor* t, int64_t n, int64_t* chunks, cons
       *why = "in-place clipping keeps the type";
       return MOE_ERR_INVALID_ARG;
     }
-    c += (t[i].numel + kChunk - 1) / kChunk;
+    all += t[i].numel;
   }
+  *chunk = kChunkMin;
+  while (*chunk < kChunkMax && all / *chunk > 8 * 152) *chunk *= 2;
+  for (int64_t i = 0; i < n; ++i) c += (t[i].numel + *chunk - 1) / *chunk;
   if (c > 0x7fffffff) {
     *why = "the list is too long";
     return MOE_ERR_UNSUPPORTED;
@@ -316,8 +325,9 @@ using namespace moe;
 
 extern "C" size_t moe_grad_clip_workspace_bytes(const moe_grad_tensor* tensors, int64_t n) {
   int64_t chunks;
+  int chunk;
   const char* why;
-  if (check_list(tensors, n, &chunks, &why) != MOE_OK) return 0;
+  if (check_list(tensors, n, &chunks, &chunk, &why) != MOE_OK) return 0;
   return layout_clip(n, chunks).total;
 }
 
@@ -325,8 +335,9 @@ extern "C" moe_status moe_grad_clip_plan(const moe_grad_tensor* tensors, int64_t
                                          void* ws, size_t ws_bytes, void* stream) {
   reset_launch_count();
   int64_t chunks = 0;
+  int chunk = 0;
   const char* why = "";
-  moe_status e = check_list(tensors, n, &chunks, &why);
+  moe_status e = check_list(tensors, n, &chunks, &chunk, &why);
   if (e != MOE_OK) return fail(e, why);
   if (!plan) return fail(MOE_ERR_INVALID_ARG, "plan must be non-NULL");
   const ClipLayout L = layout_clip(n, chunks);
@@ -343,25 +354,26 @@ extern "C" moe_status moe_grad_clip_plan(const moe_grad_tensor* tensors, int64_t
     for (int i = 0; i < m; ++i) {
       const moe_grad_tensor& t = tensors[at + i];
       batch.e[i] = {t.src, t.dst, t.numel, t.src_dtype, t.dst_dtype, first};
-      first += (t.numel + kChunk - 1) / kChunk;
+      first += (t.numel + chunk - 1) / chunk;
     }
     table_kernel<<<1, kBatch, 0, st>>>(batch, m, table, at);
     count_launch();
     CHECK_CUDA(cudaGetLastError());
   }
   if (chunks > 0) {
-    chunks_kernel<<<clip_grid(n, 8), 256, 0, st>>>(table, n, reinterpret_cast<int32_t*>(b + L.owner));
+    chunks_kernel<<<clip_grid(n, 8), 256, 0, st>>>(table, n, reinterpret_cast<int32_t*>(b + L.owner),
+                                                   chunk);
     count_launch();
     CHECK_CUDA(cudaGetLastError());
   }
-  *plan = {n, chunks, kChunk, 0};
+  *plan = {n, chunks, chunk, 0};
   return MOE_OK;
 }
 
 extern "C" moe_status moe_grad_clip(const moe_grad_plan* plan, double max_norm, float* norm, void* ws,
                                     size_t ws_bytes, void* stream) {
   reset_launch_count();
-  if (!plan || plan->chunk_elems != kChunk || plan->tensors < 0 || plan->chunks < 0)
+  if (!plan || plan->chunk_elems < kChunkMin || plan->chunk_elems > kChunkMax || plan->tensors < 0 || plan->chunks < 0)
     return fail(MOE_ERR_INVALID_ARG, "plan was not made by moe_grad_clip_plan");
   if (!norm) return fail(MOE_ERR_INVALID_ARG, "norm must be non-NULL");
   if (!(max_norm > 0.0)) return fail(MOE_ERR_INVALID_ARG, "max_norm must be positive");
@@ -374,11 +386,13 @@ extern "C" moe_status moe_grad_clip(const moe_grad_plan* plan, double max_norm, 
   const int32_t* owner = reinterpret_cast<const int32_t*>(b + L.owner);
   Head* head = reinterpret_cast<Head*>(b + L.head);
   grad_norm_kernel<<<clip_grid(plan->chunks, 8), kThreads, 0, st>>>(
-      table, owner, plan->chunks, reinterpret_cast<double*>(b + L.sums), head, max_norm, norm);
+      table, owner, plan->chunks, reinterpret_cast<double*>(b + L.sums), head, max_norm, norm,
+      plan->chunk_elems);
   count_launch();
   CHECK_CUDA(cudaGetLastError());
   if (plan->chunks > 0 && std::isfinite(max_norm)) {
-    grad_scale_kernel<<<clip_grid(plan->chunks, 8), kThreads, 0, st>>>(table, owner, plan->chunks, head);
+    grad_scale_kernel<<<clip_grid(plan->chunks, 8), kThreads, 0, st>>>(table, owner, plan->chunks, head,
+                                                                         plan->chunk_elems);
     count_launch();
     CHECK_CUDA(cudaGetLastError());
   }

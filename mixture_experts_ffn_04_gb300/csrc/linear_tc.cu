@@ -72,13 +72,13 @@ constexpr int ROLE_REGS = 56, EPI_REGS = 224;
 static_assert(ROLE_REGS + 2 * EPI_REGS <= 3 * 168, "register pool of the launch");
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int NSLOT = 4;
-constexpr int READERS = 4;          // of a tile slot: odd producer, MMA, two epilogues
+constexpr int READERS = 2 + 2 * EPI_WARPS;   // of a tile slot: odd producer, MMA, epilogue warps
 constexpr int BAR_BYTES = 512;
 constexpr int OUT_ROW_BYTES = 80;   // 64 bytes of a chunk's row, padded
 constexpr int OUT_WARP_BYTES = 32 * OUT_ROW_BYTES;
 constexpr int SMEM_BYTES = 1024 + RING_BYTES + BAR_BYTES + EPI_WARPS * OUT_WARP_BYTES;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget of one CTA");
-static_assert((2 * S + 5 + 3 * NSLOT + 1) * 8 + 12 <= BAR_BYTES, "barrier area");
+static_assert((2 * S + 5 + 3 * NSLOT) * 8 + 8 <= BAR_BYTES, "barrier area");
 constexpr int kGroupM = 8;
 constexpr int kChunkExact = 8, kChunkBf16 = 64;   // k-blocks of 64
 
@@ -142,6 +142,13 @@ __device__ __forceinline__ bool wait_cl(uint32_t bar, uint32_t parity, volatile 
       return false;
     }
   }
+}
+
+// Arrival without a memory fence: for barriers that only say "this slot or
+// accumulator has been read".  A releasing arrival waits for the thread's own
+// global stores, which here are the previous tile's output.
+__device__ __forceinline__ void arrive_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 __device__ __forceinline__ uint64_t mn_desc(uint32_t saddr) {
@@ -271,10 +278,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + RING_BYTES);
   // bars: full[S] empty[S] tfull[2] tempty[2] final tfill[NSLOT] tdrain[NSLOT],
-  // then the tile slots, the epilogue's tile and the scalars
+  // then the tile slots and the scalars
   volatile int64_t* s_tile = reinterpret_cast<volatile int64_t*>(bars + 2 * S + 5 + 2 * NSLOT);
-  volatile int64_t* s_etile = s_tile + NSLOT;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5 + 3 * NSLOT + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5 + 3 * NSLOT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   unsigned char* s_out = smem + RING_BYTES + BAR_BYTES;
 
@@ -297,7 +303,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull(b), 1);
-      mbar_init(tempty(b), 2 * 32 * EPI_WARPS);
+      mbar_init(tempty(b), 2 * EPI_WARPS);
     }
     mbar_init(final_bar, 1);
     for (int i = 0; i < NSLOT; ++i) {
@@ -344,7 +350,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     if (!wait_cl(tfill(slot), use & 1u, abort_flag)) return -1;
     const int64_t t = s_tile[slot];
-    mbar_arrive_cluster(map_to_rank(tdrain(slot), 0));
+    // the slot has been read (the branch needs the value) when the arrival goes
+    if (t != INT64_MIN) arrive_relaxed(map_to_rank(tdrain(slot), 0));
     return t;
   };
 
@@ -441,23 +448,83 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int q = warp & 3;                 // TMEM lanes 32q .. 32q+31
     const int half = (warp - 4) / 4;        // columns 128 half ..
     const int c_lo = half * (BN / 2);
-    const int et = threadIdx.x - 128;
     unsigned char* stage = s_out + (warp - 4) * OUT_WARP_BYTES;
-    auto epi_bar = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(32 * EPI_WARPS) : "memory"); };
     int acc = 0;
     uint32_t aph = 0;
     for (int64_t n = 0;; ++n) {
-      if (et == 0) *s_etile = next_tile(n, false);
-      epi_bar();
-      const int64_t tile = *s_etile;
-      epi_bar();
+      // each warp takes the tile for itself: no barrier among the warps
+      int64_t tile = -1;
+      if (lane == 0) tile = next_tile(n, false);
+      tile = __shfl_sync(0xffffffffu, tile, 0);
       if (tile < 0) break;
       const Tile t = plan.decode(a, tile);
       const int steps = (t.kb1 - t.kb0) * nprod;
-      // this lane's row of the tile, 128 columns, summed over the chunks
+      const int64_t row0 = (int64_t)t.mt * BM + (int64_t)rank * BMC + q * 32;
+      const int64_t row = row0 + lane;
+      // this lane's row of the tile, 128 columns, summed over the chunks;
+      // gradients start from what they are added to, read while the tile's MMAs
+      // run
       float f[BN / 2];
 #pragma unroll
       for (int j = 0; j < BN / 2; ++j) f[j] = 0.0f;
+      const bool is_dx = t.type == 1;
+      const int n0 = t.nt * BN + c_lo;
+      int nvalid = 0;
+      int64_t orow = row;     // where this lane's row goes
+      float* fout = nullptr;
+      if (KIND == kGrad) {
+        const int64_t nv = (is_dx ? plan.rows : min(a.vcols, a.vocab - a.v0)) - row0;
+        nvalid = nv <= 0 ? 0 : (nv >= 32 ? 32 : (int)nv);
+        float* part = is_dx ? a.dx_part : a.dw_part;
+        if (is_dx && a.rowmap) orow = lane < nvalid ? a.rowmap[row] : 0;
+        if (!is_dx) orow = a.v0 + row;
+        const float* fadd = nullptr;
+        if (part != nullptr) {
+          fout = part + ((int64_t)t.sp * (is_dx ? a.rows_pad : a.dw_pad) + row) * a.hidden;
+          if (is_dx && a.accumulate) fadd = fout;
+        } else if (a.out_f32) {
+          fout = reinterpret_cast<float*>(is_dx ? a.dx : a.dw) + orow * a.hidden;
+          if (is_dx && a.dx_add) fadd = reinterpret_cast<const float*>(a.dx_add) + orow * a.hidden;
+        }
+        if (fadd != nullptr && lane < nvalid) {
+#pragma unroll
+          for (int v = 0; v < BN / 8; ++v)
+            if (n0 + 4 * v < a.hidden) {
+              const float4 b = reinterpret_cast<const float4*>(fadd + n0)[v];
+              f[4 * v] = b.x;
+              f[4 * v + 1] = b.y;
+              f[4 * v + 2] = b.z;
+              f[4 * v + 3] = b.w;
+            }
+        }
+        if (is_dx && fout == nullptr && a.dx_add) {
+          // bf16: whole-row 16-byte pieces through the staging slice
+          const bf16* addp = reinterpret_cast<const bf16*>(a.dx_add);
+#pragma unroll
+          for (int c = 0; c < BN / 2; c += 32) {
+            uint4 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int p = lane + 32 * i, rr = p >> 2, pc = p & 3;
+              const int64_t ar = a.rowmap ? __shfl_sync(0xffffffffu, orow, rr) : row0 + rr;
+              v[i] = make_uint4(0, 0, 0, 0);
+              if (rr < nvalid && n0 + c + pc * 8 < a.hidden)
+                v[i] = *reinterpret_cast<const uint4*>(addp + ar * a.hidden + n0 + c + pc * 8);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int p = lane + 32 * i, rr = p >> 2, pc = p & 3;
+              *reinterpret_cast<uint4*>(stage + rr * OUT_ROW_BYTES + pc * 16) = v[i];
+            }
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              unpack16(reinterpret_cast<const uint4*>(stage + lane * OUT_ROW_BYTES)[j], f + c + 8 * j,
+                       (const bf16*)nullptr);
+            __syncwarp();
+          }
+        }
+      }
       bool ok = true;
 #pragma unroll 1
       for (int i0 = 0; i0 < steps; i0 += a.chunk) {
@@ -476,13 +543,12 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int j = 0; j < 32; ++j) f[c + j] += __uint_as_float(r[j]);
         }
         tc_fence_before();
-        mbar_arrive_cluster(map_to_rank(tempty(acc), 0));
+        __syncwarp();
+        if (lane == 0) arrive_relaxed(map_to_rank(tempty(acc), 0));
         acc ^= 1;
         if (acc == 0) aph ^= 1u;
       }
       if (!ok) break;
-      const int64_t row0 = (int64_t)t.mt * BM + (int64_t)rank * BMC + q * 32;
-      const int64_t row = row0 + lane;
       if (KIND == kStats) {
         // maximum and sum of the row over this half of the tile, in log2 units:
         // the maximum kept is the rounded z * log2(e), so the sum's scale and
@@ -549,60 +615,20 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
       } else {
-        const bool is_dx = t.type == 1;
-        const int64_t rows_out = is_dx ? plan.rows : min(a.vcols, a.vocab - a.v0);
-        const int64_t nv = rows_out - row0;
-        const int nvalid = nv <= 0 ? 0 : (nv >= 32 ? 32 : (int)nv);
-        float* part = is_dx ? a.dx_part : a.dw_part;
-        const int n0 = t.nt * BN + c_lo;
-        int64_t orow = row;     // where this lane's row goes
-        if (is_dx && a.rowmap) orow = lane < nvalid ? a.rowmap[row] : 0;
-        if (!is_dx) orow = a.v0 + row;
-        float* fout = part ? part + ((int64_t)t.sp * (is_dx ? a.rows_pad : a.dw_pad) + row) * a.hidden
-                           : reinterpret_cast<float*>(is_dx ? a.dx : a.dw) + orow * a.hidden;
-        const float* fadd = part ? (is_dx && a.accumulate ? fout : nullptr)
-                                 : (is_dx && a.dx_add ? reinterpret_cast<const float*>(a.dx_add) + orow * a.hidden : nullptr);
 #pragma unroll
         for (int c = 0; c < BN / 2; c += 32) {
           const int ncols = min(32, a.hidden - (n0 + c));   // a multiple of 8
           if (ncols <= 0) break;
-          if (part != nullptr || a.out_f32) {
+          if (fout != nullptr) {
             if (lane < nvalid) {
 #pragma unroll
-              for (int v = 0; v < 8; ++v) {
-                if (4 * v >= ncols) break;
-                float4 o = make_float4(f[c + 4 * v], f[c + 4 * v + 1], f[c + 4 * v + 2], f[c + 4 * v + 3]);
-                if (fadd) {
-                  const float4 b = reinterpret_cast<const float4*>(fadd + n0 + c)[v];
-                  o.x += b.x; o.y += b.y; o.z += b.z; o.w += b.w;
-                }
-                reinterpret_cast<float4*>(fout + n0 + c)[v] = o;
-              }
+              for (int v = 0; v < 8; ++v)
+                if (4 * v < ncols)
+                  reinterpret_cast<float4*>(fout + n0 + c)[v] =
+                      make_float4(f[c + 4 * v], f[c + 4 * v + 1], f[c + 4 * v + 2], f[c + 4 * v + 3]);
             }
           } else {
             bf16* out = reinterpret_cast<bf16*>(is_dx ? a.dx : a.dw);
-            if (is_dx && a.dx_add) {
-              // the addend comes in whole-row pieces through the staging slice
-              const bf16* addp = reinterpret_cast<const bf16*>(a.dx_add);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int p = lane + 32 * i, rr = p >> 2, pc = p & 3;
-                const int64_t ar = __shfl_sync(0xffffffffu, orow, rr);
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (rr < nvalid && pc * 8 < ncols)
-                  v = *reinterpret_cast<const uint4*>(addp + ar * a.hidden + n0 + c + pc * 8);
-                *reinterpret_cast<uint4*>(stage + rr * OUT_ROW_BYTES + pc * 16) = v;
-              }
-              __syncwarp();
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                float b[8];
-                unpack16(reinterpret_cast<const uint4*>(stage + lane * OUT_ROW_BYTES)[j], b, (const bf16*)nullptr);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[c + 8 * j + e] += b[e];
-              }
-              __syncwarp();
-            }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               reinterpret_cast<uint4*>(stage + lane * OUT_ROW_BYTES)[j] = pack16(f + c + 8 * j, (const bf16*)nullptr);
@@ -611,7 +637,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int p = lane + 32 * i, rr = p >> 2, pc = p & 3;
-              const int64_t wr = __shfl_sync(0xffffffffu, orow, rr);
+              const int64_t wr = is_dx && a.rowmap ? __shfl_sync(0xffffffffu, orow, rr)
+                                                   : (is_dx ? 0 : a.v0) + row0 + rr;
               if (rr < nvalid && pc * 8 < ncols)
                 *reinterpret_cast<uint4*>(out + wr * a.hidden + n0 + c + pc * 8) =
                     *reinterpret_cast<const uint4*>(stage + rr * OUT_ROW_BYTES + pc * 16);

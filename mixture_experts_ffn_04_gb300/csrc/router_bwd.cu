@@ -73,8 +73,178 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// A warp a token; z and the slots' contributions of its token in shared memory
-// (2 ncols floats a warp), so any E fits.
+// The losses: block sums in fp64, the last block adds the blocks in order.
+__device__ void finish_aux(const DzArgs& a, double sum_pn, double sum_l2) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  __shared__ double s_d[8][2];
+  __shared__ int s_last;
+  if (lane == 0) {
+    s_d[warp][0] = sum_pn;
+    s_d[warp][1] = sum_l2;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double x = 0.0, y = 0.0;
+    for (int w = 0; w < warps; ++w) {
+      x += s_d[w][0];
+      y += s_d[w][1];
+    }
+    a.part[2 * blockIdx.x] = x;
+    a.part[2 * blockIdx.x + 1] = y;
+    __threadfence();
+    s_last = atomicAdd(a.ticket, 1) == (int)gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!s_last || warp != 0) return;
+  __threadfence();
+  double x = 0.0, y = 0.0;
+  for (int i = lane; i < (int)gridDim.x; i += 32) {
+    x += __ldcg(a.part + 2 * i);
+    y += __ldcg(a.part + 2 * i + 1);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    x += __shfl_xor_sync(0xffffffffu, x, o);
+    y += __shfl_xor_sync(0xffffffffu, y, o);
+  }
+  if (lane == 0) {
+    a.aux[0] = (float)(x * a.balance);
+    a.aux[1] = (float)(y * a.zmean);
+  }
+}
+
+// A warp a token, up to 64 * NP router columns and 32 slots: the token's logits
+// in registers (columns 64 j + 2 lane, + 1), its slots one a lane, loaded with
+// the logits; only the gather at the slots' experts and the scatter of their
+// terms go through shared memory.  Bound by the logits' latency at few tokens, at
+// 8192 x 256 by issue (three exponentials a column were two too many: p is
+// kept).
+template <int NP>
+__global__ void __launch_bounds__(256) router_dz_small_kernel(const DzArgs a) {
+  extern __shared__ float s_f[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  float* row = s_f + (size_t)warp * 64 * NP;
+  float cnt[2 * NP];
+#pragma unroll
+  for (int j = 0; j < 2 * NP; ++j) {
+    const int e = 64 * (j / 2) + 2 * lane + (j & 1);
+    cnt[j] = a.counts && e < a.E ? (float)a.counts[e] : 0.0f;
+  }
+  double sum_pn = 0.0, sum_l2 = 0.0;
+  for (int64_t t = blockIdx.x * (int64_t)warps + warp; t < a.rows; t += (int64_t)gridDim.x * warps) {
+    if (t >= a.T) {   // rows the weight gradient's last k-block reads
+      for (int p = 0; p < a.planes; ++p)
+        for (int e = lane; e < a.ld; e += 32) a.dz[(p * a.plane + t) * a.ld + e] = __float2bfloat16_rn(0.0f);
+      continue;
+    }
+    int slot = -1;
+    float D = 0.0f;
+    if (a.d_w && lane < a.k) {
+      slot = a.idx[t * a.k + lane];
+      D = a.d_w[t * a.k + lane];
+    }
+    if (slot >= a.E) slot = -1;
+    const float dg = a.gate ? a.d_gate[t] : 0.0f;
+    float z[2 * NP];
+#pragma unroll
+    for (int j = 0; j < 2 * NP; ++j) z[j] = 0.0f;
+    for (int s = 0; s < a.nsplit; ++s) {
+      const float* l = a.logits + s * a.split_stride + t * a.ldl + 2 * lane;
+#pragma unroll
+      for (int j = 0; j < NP; ++j)
+        if (64 * j + 2 * lane < a.ncols) {
+          const float2 v = *reinterpret_cast<const float2*>(l + 64 * j);   // ldl is a multiple of 4
+          z[2 * j] += v.x;
+          z[2 * j + 1] += v.y;
+        }
+    }
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 2 * NP; ++j) {
+      const int e = 64 * (j / 2) + 2 * lane + (j & 1);
+      if (e < a.E) m = fmaxf(m, z[j]);
+      row[e] = z[j];
+    }
+    __syncwarp();
+    m = warp_max(m);
+    float p[2 * NP], sum = 0.0f, pn = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 2 * NP; ++j) {
+      const int e = 64 * (j / 2) + 2 * lane + (j & 1);
+      p[j] = e < a.E ? expf(z[j] - m) : 0.0f;
+      sum += p[j];
+      pn = fmaf(p[j], cnt[j], pn);
+    }
+    sum = warp_sum(sum);
+    pn = warp_sum(pn) / sum;
+    const float inv = 1.0f / sum, lse = m + logf(sum);
+    sum_pn += (double)pn;
+    sum_l2 += (double)lse * lse;
+    const float zs = slot >= 0 ? row[slot] : -INFINITY;
+    __syncwarp();
+    float w, dot = 0.0f, add = 0.0f;
+    if (a.d_w) {
+      float top = m, den = sum;
+      if (a.norm) {
+        top = warp_max(zs);
+        den = warp_sum(slot >= 0 ? expf(zs - top) : 0.0f);
+      }
+      w = slot >= 0 ? expf(zs - top) / den : 0.0f;
+      dot = warp_sum(w * D);
+      add = a.norm ? w * (D - dot) : w * D;
+      if (slot < 0) add = 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < NP; ++j) *reinterpret_cast<float2*>(row + 64 * j + 2 * lane) = make_float2(0.0f, 0.0f);
+    __syncwarp();
+    if (a.d_w) {
+      // repeated routes add up in slot order
+      const uint32_t same = __match_any_sync(0xffffffffu, slot);
+      const bool dup = slot >= 0 && __popc(same) > 1;
+      if (slot >= 0 && !dup) row[slot] = add;
+      uint32_t left = __ballot_sync(0xffffffffu, dup);
+      while (left) {
+        const int s = __ffs(left) - 1;
+        left &= left - 1;
+        if (lane == s) row[slot] += add;
+        __syncwarp();
+      }
+      __syncwarp();
+    }
+    const float base = (a.norm ? 0.0f : -dot) + a.cz2 * lse - a.cb * pn;
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      const int e = 64 * j + 2 * lane;
+      if (e >= a.ld) continue;
+      const float2 c = *reinterpret_cast<const float2*>(row + e);
+      float v[2] = {c.x, c.y};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (e + h < a.E) {
+          v[h] += p[2 * j + h] * inv * (base + a.cb * cnt[2 * j + h]);
+        } else if (e + h < a.ncols) {
+          const float s = 1.0f / (1.0f + expf(-z[2 * j + h]));
+          v[h] = dg * s * (1.0f - s);
+        } else {
+          v[h] = 0.0f;
+        }
+      }
+      for (int pl = 0; pl < a.planes; ++pl) {
+        *reinterpret_cast<uint32_t*>(a.dz + (pl * a.plane + t) * a.ld + e) = pack_bf16x2(v[0], v[1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          v[h] -= __bfloat162float(__float2bfloat16_rn(v[h]));
+          if (!isfinite(v[h])) v[h] = 0.0f;
+        }
+      }
+    }
+    __syncwarp();
+  }
+  if (a.aux) finish_aux(a, sum_pn, sum_l2);
+}
+
+// Any number of columns and slots: a warp a token; z and the slots'
+// contributions of its token in shared memory (2 ncols floats a warp).
 __global__ void __launch_bounds__(256) router_dz_kernel(const DzArgs a) {
   extern __shared__ float s_f[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
@@ -163,45 +333,7 @@ __global__ void __launch_bounds__(256) router_dz_kernel(const DzArgs a) {
     }
     __syncwarp();
   }
-  if (!a.aux) return;
-  // the losses: block sums in fp64, the last block adds the blocks in order
-  __shared__ double s_d[8][2];
-  __shared__ int s_last;
-  if (lane == 0) {
-    s_d[warp][0] = sum_pn;
-    s_d[warp][1] = sum_l2;
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    double x = 0.0, y = 0.0;
-    for (int w = 0; w < warps; ++w) {
-      x += s_d[w][0];
-      y += s_d[w][1];
-    }
-    a.part[2 * blockIdx.x] = x;
-    a.part[2 * blockIdx.x + 1] = y;
-    __threadfence();
-    s_last = atomicAdd(a.ticket, 1) == (int)gridDim.x - 1;
-  }
-  __syncthreads();
-  if (!s_last) return;
-  __threadfence();
-  double x = 0.0, y = 0.0;
-  for (int i = lane; warp == 0 && i < (int)gridDim.x; i += 32) {
-    x += __ldcg(a.part + 2 * i);
-    y += __ldcg(a.part + 2 * i + 1);
-  }
-  if (warp == 0) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      x += __shfl_xor_sync(0xffffffffu, x, o);
-      y += __shfl_xor_sync(0xffffffffu, y, o);
-    }
-    if (lane == 0) {
-      a.aux[0] = (float)(x * a.balance);
-      a.aux[1] = (float)(y * a.zmean);
-    }
-  }
+  if (a.aux) finish_aux(a, sum_pn, sum_l2);
 }
 
 constexpr int kDzBlocks = 2048;
@@ -324,13 +456,24 @@ extern "C" moe_status moe_router_backward(const moe_shape* shape, const void* x,
   d.aux = aux;
   d.balance = cb;
   d.zmean = z_coef / (double)s.T;
-  const size_t per_warp = 2 * (size_t)s.ncols * 4;
-  const int warps = (int)std::max<size_t>(1, std::min<size_t>(8, 200 * 1024 / per_warp));
-  if (per_warp * warps > 48 * 1024)
-    CHECK_CUDA(cudaFuncSetAttribute(router_dz_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)(per_warp * warps)));
-  const int64_t blocks = std::min<int64_t>((d.rows + warps - 1) / warps, kDzBlocks);
-  router_dz_kernel<<<(unsigned)blocks, 32 * warps, per_warp * warps, st>>>(d);
+  if (s.k <= 32 && s.ncols <= 512) {
+    const int np = s.ncols <= 64 ? 1 : s.ncols <= 128 ? 2 : s.ncols <= 256 ? 4 : 8;
+    const int warps = 4;
+    const unsigned blocks = (unsigned)std::min<int64_t>((d.rows + warps - 1) / warps, kDzBlocks);
+    const size_t smem = (size_t)warps * 64 * np * 4;
+    if (np == 1) router_dz_small_kernel<1><<<blocks, 32 * warps, smem, st>>>(d);
+    else if (np == 2) router_dz_small_kernel<2><<<blocks, 32 * warps, smem, st>>>(d);
+    else if (np == 4) router_dz_small_kernel<4><<<blocks, 32 * warps, smem, st>>>(d);
+    else router_dz_small_kernel<8><<<blocks, 32 * warps, smem, st>>>(d);
+  } else {
+    const size_t per_warp = 2 * (size_t)s.ncols * 4;
+    const int warps = (int)std::max<size_t>(1, std::min<size_t>(8, 200 * 1024 / per_warp));
+    if (per_warp * warps > 48 * 1024)
+      CHECK_CUDA(cudaFuncSetAttribute(router_dz_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      (int)(per_warp * warps)));
+    const int64_t blocks = std::min<int64_t>((d.rows + warps - 1) / warps, kDzBlocks);
+    router_dz_kernel<<<(unsigned)blocks, 32 * warps, per_warp * warps, st>>>(d);
+  }
   count_launch();
   CHECK_CUDA(cudaGetLastError());
   LinearGradArgs q = {};

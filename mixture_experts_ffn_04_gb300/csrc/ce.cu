@@ -26,7 +26,7 @@ constexpr int64_t kDlogitBytes = 256ll << 20;   // logit gradient of one piece
 constexpr int64_t kPlaneBytes = 512ll << 20;    // bf16 planes of one piece of an fp32 W
 
 // the few-row forward: rows of x, warps a block, blocks an SM, shared memory of x
-constexpr int kSkinnyRows = 4, kSkinnyWarps = 8, kSkinnyPerSm = 2, kSkinnySmem = 112 * 1024;
+constexpr int kSkinnyRows = 4, kSkinnyWarps = 8, kSkinnyPerSm = 4, kSkinnySmem = 112 * 1024;
 
 struct CeShape {
   int64_t T, x_ld, w_ld;
@@ -54,6 +54,10 @@ moe_status decode_ce(const moe_ce_shape* s, CeShape* o, const char** why) {
   if (s->reduction < MOE_CE_NONE || s->reduction > MOE_CE_MEAN) {
     *why = "reduction must be MOE_CE_NONE, MOE_CE_SUM or MOE_CE_MEAN";
     return MOE_ERR_INVALID_ARG;
+  }
+  if ((double)s->tokens * s->vocab >= (double)(1ll << 46)) {
+    *why = "tokens * vocab must be below 2^46";
+    return MOE_ERR_UNSUPPORTED;
   }
   o->x_ld = s->x_stride ? s->x_stride : s->hidden;
   o->w_ld = s->w_stride ? s->w_stride : s->hidden;
@@ -156,6 +160,8 @@ __device__ __forceinline__ bool counts(int t, int V, int ignore) { return t != i
 template <typename T>
 __global__ void __launch_bounds__(256) ce_prep_kernel(const PrepArgs a) {
   __shared__ int s_before, s_total, s_cnt[256];
+  pdl_trigger();
+  pdl_wait();
   const int64_t beg = min(a.T, blockIdx.x * a.rows_per_block), end = min(a.T, beg + a.rows_per_block);
   if (threadIdx.x == 0) s_before = s_total = 0;
   __syncthreads();
@@ -267,6 +273,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
                     const float* __restrict__ zt, const int32_t* __restrict__ rowmap,
                     const int32_t* nrows, int32_t* ticket, float* loss_c, float* loss, float* lse,
                     float* total, int mean) {
+  pdl_trigger();
+  pdl_wait();
   const int n = *nrows;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   __shared__ float2 s_part[kMergeWarps][32];
@@ -345,7 +353,9 @@ __device__ __forceinline__ void merge_ms(float& M, float& S, float m, float s) {
   M = n;
 }
 template <typename T, int R, int NV>
-__global__ void __launch_bounds__(32 * kSkinnyWarps) ce_skinny_kernel(const SkinnyArgs a) {
+__global__ void __launch_bounds__(32 * kSkinnyWarps, R <= 2 ? kSkinnyPerSm : 2) ce_skinny_kernel(const SkinnyArgs a) {
+  pdl_trigger();
+  pdl_wait();
   extern __shared__ __align__(16) float s_x[];   // [R][H]
   __shared__ float2 s_ms[kSkinnyWarps][R];
   __shared__ int s_last;
@@ -367,8 +377,10 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps) ce_skinny_kernel(const Skin
 #pragma unroll
   for (int r = 0; r < R; ++r) { M[r] = -INFINITY; S[r] = 0.0f; }
   const T* w = reinterpret_cast<const T*>(a.w);
-  const int64_t stride = (int64_t)gridDim.x * kSkinnyWarps * NV;
-  for (int64_t v0 = ((int64_t)blockIdx.x * kSkinnyWarps + warp) * NV; v0 < a.V; v0 += stride) {
+  // a contiguous range of rows a warp: every warp has the same number, but one
+  const int64_t all = (int64_t)gridDim.x * kSkinnyWarps, me = (int64_t)blockIdx.x * kSkinnyWarps + warp;
+  const int64_t vend = a.V * (me + 1) / all;
+  for (int64_t v0 = a.V * me / all; v0 < vend; v0 += NV) {
     float acc[NV][R];
 #pragma unroll
     for (int v = 0; v < NV; ++v)
@@ -376,7 +388,7 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps) ce_skinny_kernel(const Skin
       for (int r = 0; r < R; ++r) acc[v][r] = 0.0f;
     const T* wr[NV];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) wr[v] = w + min(v0 + v, (int64_t)a.V - 1) * a.w_ld;
+    for (int v = 0; v < NV; ++v) wr[v] = w + min(v0 + v, vend - 1) * a.w_ld;
 #pragma unroll 4
     for (int i = lane * N; i < a.H; i += 32 * N) {
       uint4 u[NV];
@@ -405,7 +417,7 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps) ce_skinny_kernel(const Skin
         float z = acc[v][r];
 #pragma unroll
         for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-        if (v0 + v < a.V) {
+        if (v0 + v < vend) {
           if (lane == 0 && tg[r] == (int)(v0 + v)) a.zt[r] = z;
           merge_ms(M[r], S[r], z * 1.4426950408889634f, 1.0f);
         }
@@ -475,10 +487,10 @@ cudaError_t launch_skinny(const SkinnyArgs& a, cudaStream_t st) {
       if (e != cudaSuccess) return e;
     }
     const int64_t want = ((int64_t)a.V + kSkinnyWarps * nv - 1) / (kSkinnyWarps * nv);
-    const int64_t blocks = std::min<int64_t>(want, (int64_t)tc_sm_count() * kSkinnyPerSm);
-    kernel<<<(unsigned)blocks, 32 * kSkinnyWarps, smem, st>>>(a);
-    count_launch();
-    return cudaGetLastError();
+    // four blocks an SM with up to two rows of x, else two, if x fits so often
+    const int per = (int)std::max<size_t>(1, std::min<size_t>(rows <= 2 ? kSkinnyPerSm : 2, 220 * 1024 / (smem + 1024)));
+    const int64_t blocks = std::min<int64_t>(want, (int64_t)tc_sm_count() * per);
+    return launch_after(kernel, (unsigned)blocks, 32 * kSkinnyWarps, smem, st, 1, a);
   };
   if (rows == 1) return go(ce_skinny_kernel<T, 1, 2>, 2);
   if (rows == 2) return go(ce_skinny_kernel<T, 2, 2>, 2);
@@ -513,10 +525,8 @@ cudaError_t run_prep(const CeShape& s, const CeLayout& L, char* ws, PrepArgs& p,
   p.flags = reinterpret_cast<uint32_t*>(ws);
   p.reduction = s.reduction;
   const int64_t blocks = std::max<int64_t>((s.T + rpb - 1) / rpb, 32);
-  if (s.dtype == MOE_F32) ce_prep_kernel<float><<<(unsigned)blocks, 256, 0, st>>>(p);
-  else ce_prep_kernel<bf16><<<(unsigned)blocks, 256, 0, st>>>(p);
-  count_launch();
-  return cudaGetLastError();
+  return launch_after(s.dtype == MOE_F32 ? ce_prep_kernel<float> : ce_prep_kernel<bf16>, (unsigned)blocks, 256, 0,
+                      st, 1, p);
 }
 
 // W's columns (vocabulary rows) v0 .. of this piece as a tensor-core operand:
@@ -634,12 +644,11 @@ extern "C" moe_status moe_linear_ce_forward(const moe_ce_shape* shape, const voi
   }
   int64_t blocks = std::min<int64_t>((s.T + 31) / 32, 4096);
   if (blocks < 1) blocks = 1;
-  ce_merge_kernel<<<(unsigned)blocks, 32 * kMergeWarps, 0, st>>>(
-      reinterpret_cast<const float2*>(b + L.stats), L.rows_pad, (int)(vpad / 128),
-      reinterpret_cast<const float*>(b + L.zt), p.rowmap, p.nrows, p.ticket,
-      reinterpret_cast<float*>(b + L.loss), loss, lse, total, s.reduction == MOE_CE_MEAN);
-  count_launch();
-  CHECK_CUDA(cudaGetLastError());
+  CHECK_CUDA(launch_after(ce_merge_kernel, (unsigned)blocks, 32 * kMergeWarps, 0, st, 1,
+                          reinterpret_cast<const float2*>(b + L.stats), L.rows_pad, (int)(vpad / 128),
+                          reinterpret_cast<const float*>(b + L.zt), p.rowmap, p.nrows, p.ticket,
+                          reinterpret_cast<float*>(b + L.loss), loss, lse, total,
+                          s.reduction == MOE_CE_MEAN ? 1 : 0));
   return MOE_OK;
 }
 

@@ -22,6 +22,7 @@
 #include "../../include/moe_train.h"
 #include "common.cuh"
 #include "internal.h"
+#include "train.h"
 
 namespace moe {
 namespace {
@@ -29,7 +30,7 @@ namespace {
 // Elements of a chunk: the power of two that gives about eight chunks an SM, so
 // that a small list covers the GPU and a large one spends little on table
 // look-ups and block sums.
-constexpr int kChunkMin = 2048, kChunkMax = 65536;
+constexpr int kChunkMin = 2048, kChunkMax = 32768;
 constexpr int kThreads = 256;
 
 struct Entry {
@@ -146,15 +147,23 @@ struct Head {   // the workspace's first bytes
   uint32_t flags;
   int32_t ticket;
   float coef;
+  int32_t next;   // norm pass: chunks handed out beyond the blocks' first ones
 };
 
-__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const Entry* table, const int32_t* owner,
+constexpr int kNormPerSm = 6;   // resident blocks: one wave
+__global__ void __launch_bounds__(kThreads, kNormPerSm) grad_norm_kernel(const Entry* table, const int32_t* owner,
                                                              int64_t chunks, double* sums, Head* head,
                                                              double max_norm, float* norm, int64_t chunk) {
   __shared__ float sh[kThreads / 32];
   __shared__ double shd[kThreads / 32];
   __shared__ int s_last;
-  for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+  pdl_trigger();
+  pdl_wait();
+  // chunks of a ragged list differ in size: the next one is claimed while this
+  // one is added up
+  __shared__ int64_t s_next;
+  for (int64_t c = blockIdx.x; c < chunks;) {
+    if (threadIdx.x == 0) s_next = (int64_t)gridDim.x + atomicAdd(&head->next, 1);
     const Span s = span_of(table, owner, c, chunk);
     auto squares = [&](float scale) {
       return (double)block_sum(s.sd == MOE_F32 ? chunk_squares<float>(s, scale) : chunk_squares<bf16>(s, scale), sh);
@@ -167,6 +176,8 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const Entry* table,
     if (!(sum >= 1e-28)) sum = squares(0x1p80f) * 0x1p-160;
     else if (!(sum <= 1e38)) sum = squares(0x1p-96f) * 0x1p192;
     if (threadIdx.x == 0) sums[c] = sum;
+    c = s_next;        // written before block_sum's barriers
+    __syncthreads();
   }
   __threadfence();
   __syncthreads();
@@ -187,6 +198,7 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const Entry* table,
     *norm = (float)n;
     head->coef = coef;
     head->ticket = 0;
+    head->next = 0;
   }
 }
 
@@ -242,6 +254,8 @@ __device__ __forceinline__ void scale_chunk(const Span& s, float coef) {
 __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const Entry* table, const int32_t* owner,
                                                               int64_t chunks, const Head* head,
                                                               int64_t chunk) {
+  pdl_trigger();
+  pdl_wait();
   const float coef = head->coef;
   for (int64_t i = blockIdx.x; i < chunks; i += gridDim.x) {
     const Span s = span_of(table, owner, chunks - 1 - i, chunk);
@@ -385,16 +399,11 @@ extern "C" moe_status moe_grad_clip(const moe_grad_plan* plan, double max_norm, 
   const Entry* table = reinterpret_cast<const Entry*>(b + L.table);
   const int32_t* owner = reinterpret_cast<const int32_t*>(b + L.owner);
   Head* head = reinterpret_cast<Head*>(b + L.head);
-  grad_norm_kernel<<<clip_grid(plan->chunks, 8), kThreads, 0, st>>>(
-      table, owner, plan->chunks, reinterpret_cast<double*>(b + L.sums), head, max_norm, norm,
-      plan->chunk_elems);
-  count_launch();
-  CHECK_CUDA(cudaGetLastError());
-  if (plan->chunks > 0 && std::isfinite(max_norm)) {
-    grad_scale_kernel<<<clip_grid(plan->chunks, 8), kThreads, 0, st>>>(table, owner, plan->chunks, head,
-                                                                         plan->chunk_elems);
-    count_launch();
-    CHECK_CUDA(cudaGetLastError());
-  }
+  CHECK_CUDA(launch_after(grad_norm_kernel, clip_grid(plan->chunks, kNormPerSm), kThreads, 0, st, 1, table, owner,
+                          plan->chunks, reinterpret_cast<double*>(b + L.sums), head, max_norm, norm,
+                          (int64_t)plan->chunk_elems));
+  if (plan->chunks > 0 && std::isfinite(max_norm))
+    CHECK_CUDA(launch_after(grad_scale_kernel, clip_grid(plan->chunks, 16), kThreads, 0, st, 1, table, owner,
+                            plan->chunks, (const Head*)head, (int64_t)plan->chunk_elems));
   return MOE_OK;
 }

@@ -78,7 +78,7 @@ constexpr int OUT_ROW_BYTES = 80;   // 64 bytes of a chunk's row, padded
 constexpr int OUT_WARP_BYTES = 32 * OUT_ROW_BYTES;
 constexpr int SMEM_BYTES = 1024 + RING_BYTES + BAR_BYTES + EPI_WARPS * OUT_WARP_BYTES;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget of one CTA");
-static_assert((2 * S + 5 + 3 * NSLOT) * 8 + 8 <= BAR_BYTES, "barrier area");
+static_assert((2 * S + 5 + 2 * NSLOT) * 8 + 8 + NSLOT * 32 <= BAR_BYTES, "barrier area");
 constexpr int kGroupM = 8;
 constexpr int kChunkExact = 8, kChunkBf16 = 64;   // k-blocks of 64
 
@@ -169,27 +169,28 @@ __device__ __forceinline__ void plane_pair(int planes, int i, int& pa, int& pb) 
   pb = t & 15;
 }
 
-struct Tile {
-  int type;        // 0: logits, 1: dX, 2: dW
+// A tile as it stands in a slot: decoded once, by the taker (the divisions cost
+// every reader about 1900 clocks a tile otherwise, a third of a short tile).
+struct __align__(16) Tile {
+  int type;        // 0: logits, 1: dX, 2: dW; -1: no tile left
   int mt, nt, sp;
   int kb0, kb1;    // k-blocks of one plane product
+  int pad[2];
 };
 
 // m-tiles in groups of kGroupM, n-tiles outer within a group.
-__device__ __forceinline__ void order_tile(int64_t t, int MT, int NT, int& mt, int& nt) {
-  const int64_t per = (int64_t)kGroupM * NT;
-  const int grp = (int)(t / per);
-  const int first = grp * kGroupM;
-  const int size = MT - first < kGroupM ? MT - first : kGroupM;
-  const int64_t r = t - grp * per;
+__device__ __forceinline__ void order_tile(uint32_t t, uint32_t MT, uint32_t NT, int& mt, int& nt) {
+  const uint32_t per = kGroupM * NT, grp = t / per, first = grp * kGroupM;
+  const uint32_t size = MT - first < (uint32_t)kGroupM ? MT - first : (uint32_t)kGroupM;
+  const uint32_t r = t - grp * per;
   nt = (int)(r / size);
-  mt = first + (int)(r % size);
+  mt = (int)(first + r % size);
 }
 
 template <int KIND>
 struct Plan {
   int MTr, NTh, NTv, KBv, KBr;
-  int64_t n_dx, total;
+  uint32_t n_dx, total;   // tiles (the launcher bounds them by 2^31)
   int64_t rows;
   __device__ __forceinline__ void init(const Args& a) {
     rows = a.nrows ? (int64_t)*a.nrows : a.rows_bound;
@@ -202,34 +203,35 @@ struct Plan {
     KBr = (int)((rows + BK - 1) / BK);
     n_dx = 0;
     if (KIND == kGrad) {
-      n_dx = a.want_dx ? (int64_t)MTr * NTh * a.ks_dx : 0;
-      total = n_dx + (a.want_dw ? (int64_t)NTv * NTh * a.ks_dw : 0);
+      n_dx = a.want_dx ? (uint32_t)MTr * NTh * a.ks_dx : 0u;
+      total = n_dx + (a.want_dw ? (uint32_t)NTv * NTh * a.ks_dw : 0u);
     } else {
-      total = (int64_t)MTr * NTv;
+      total = (uint32_t)MTr * NTv;
     }
   }
-  __device__ __forceinline__ Tile decode(const Args& a, int64_t t) const {
+  __device__ __forceinline__ Tile decode(const Args& a, uint32_t t) const {
     Tile r;
+    r.sp = 0;
     if (KIND != kGrad) {
       r.type = 0;
-      r.sp = 0;
       order_tile(t, MTr, NTv, r.mt, r.nt);
       r.kb0 = 0;
       r.kb1 = (a.hidden + BK - 1) / BK;
-    } else if (t < n_dx) {
-      r.type = 1;
-      r.sp = (int)(t % a.ks_dx);
-      order_tile(t / a.ks_dx, MTr, NTh, r.mt, r.nt);
-      r.kb0 = (int)((int64_t)r.sp * KBv / a.ks_dx);
-      r.kb1 = (int)((int64_t)(r.sp + 1) * KBv / a.ks_dx);
-    } else {
-      t -= n_dx;
-      r.type = 2;
-      r.sp = (int)(t % a.ks_dw);
-      order_tile(t / a.ks_dw, NTv, NTh, r.mt, r.nt);
-      r.kb0 = (int)((int64_t)r.sp * KBr / a.ks_dw);
-      r.kb1 = (int)((int64_t)(r.sp + 1) * KBr / a.ks_dw);
+      return r;
     }
+    const bool dx = t < n_dx;
+    if (!dx) t -= n_dx;
+    r.type = dx ? 1 : 2;
+    const uint32_t ks = dx ? a.ks_dx : a.ks_dw, kb = dx ? KBv : KBr;
+    if (ks > 1) {
+      r.sp = (int)(t % ks);
+      t /= ks;
+    }
+    order_tile(t, dx ? MTr : NTv, NTh, r.mt, r.nt);
+    // the first kb % ks parts take one k-block more
+    const uint32_t each = kb / ks, more = kb % ks;
+    r.kb0 = (int)(r.sp * each + min((uint32_t)r.sp, more));
+    r.kb1 = r.kb0 + (int)(each + ((uint32_t)r.sp < more ? 1u : 0u));
     return r;
   }
 };
@@ -279,11 +281,13 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + RING_BYTES);
   // bars: full[S] empty[S] tfull[2] tempty[2] final tfill[NSLOT] tdrain[NSLOT],
   // then the tile slots and the scalars
-  volatile int64_t* s_tile = reinterpret_cast<volatile int64_t*>(bars + 2 * S + 5 + 2 * NSLOT);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5 + 3 * NSLOT);
+  static_assert(sizeof(Tile) == 32, "a slot is two 16-byte pieces");
+  unsigned char* s_slots = smem + RING_BYTES + BAR_BYTES - NSLOT * sizeof(Tile);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5 + 2 * NSLOT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   unsigned char* s_out = smem + RING_BYTES + BAR_BYTES;
 
+  pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
@@ -324,34 +328,55 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();   // barriers, TMEM and descriptors are set up under the kernel before
   Plan<KIND> plan;
   plan.init(a);
   const int nprod = a.planes == 1 ? 1 : 6;
 
-  // Tile n of this pair, or -1 when there is none left (or a wait ran out).
-  // The even CTA's producer takes it, one ahead, from the counter and writes it
-  // to slot n % NSLOT of both CTAs; the other readers read their CTA's slot and
-  // tell the even CTA that they have.
-  int64_t reserve = threadIdx.x == 0 && leader ? (int64_t)atomicAdd(a.ctr, 1) : -1;
-  auto next_tile = [&](int64_t n, bool take) -> int64_t {
-    const int slot = (int)(n % NSLOT);
-    const uint32_t use = (uint32_t)(n / NSLOT);
-    if (take) {
-      if (!wait_cl(tdrain(slot), (use & 1u) ^ 1u, abort_flag)) return -1;
-      int64_t t = reserve;
-      reserve = (int64_t)atomicAdd(a.ctr, 1);
-      if (t >= plan.total) t = -1;
-      s_tile[slot] = t;
-      const uint32_t remote = map_to_rank(smem_u32((const void*)&s_tile[slot]), 1);
-      asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(remote), "l"(t) : "memory");
-      mbar_arrive(tfill(slot));
-      mbar_arrive_cluster(map_to_rank(tfill(slot), 1));
-      return t;
+  // Tile n of this pair (type -1 when there is none left, or a wait ran out).
+  // The even CTA's producer takes it, one ahead, from the counter, decodes it and
+  // writes it to slot n % NSLOT of both CTAs; the other readers read their CTA's
+  // slot and tell the even CTA that they have.
+  uint32_t reserve = threadIdx.x == 0 && leader ? (uint32_t)atomicAdd(a.ctr, 1) : 0u;
+  auto take_tile = [&](int n) -> Tile {
+    const int slot = n % NSLOT;
+    const uint32_t use = (uint32_t)n / NSLOT;
+    Tile t;
+    t.type = -1;
+    if (!wait_cl(tdrain(slot), (use & 1u) ^ 1u, abort_flag)) return t;
+    const uint32_t id = reserve;
+    if (id < plan.total) {
+      reserve = (uint32_t)atomicAdd(a.ctr, 1);
+      t = plan.decode(a, id);
     }
-    if (!wait_cl(tfill(slot), use & 1u, abort_flag)) return -1;
-    const int64_t t = s_tile[slot];
-    // the slot has been read (the branch needs the value) when the arrival goes
-    if (t != INT64_MIN) arrive_relaxed(map_to_rank(tdrain(slot), 0));
+    const uint32_t mine = smem_u32(s_slots + slot * sizeof(Tile)), other = map_to_rank(mine, 1);
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mine), "r"(t.type), "r"(t.mt), "r"(t.nt),
+                 "r"(t.sp)
+                 : "memory");
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(mine + 16), "r"(t.kb0), "r"(t.kb1) : "memory");
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(other), "r"(t.type), "r"(t.mt),
+                 "r"(t.nt), "r"(t.sp)
+                 : "memory");
+    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(other + 16), "r"(t.kb0), "r"(t.kb1)
+                 : "memory");
+    mbar_arrive(tfill(slot));
+    mbar_arrive_cluster(map_to_rank(tfill(slot), 1));
+    return t;
+  };
+  auto read_tile = [&](int n) -> Tile {
+    const int slot = n % NSLOT;
+    const uint32_t use = (uint32_t)n / NSLOT;
+    Tile t;
+    t.type = -1;
+    if (!wait_cl(tfill(slot), use & 1u, abort_flag)) return t;
+    const uint32_t mine = smem_u32(s_slots + slot * sizeof(Tile));
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(t.type), "=r"(t.mt), "=r"(t.nt), "=r"(t.sp)
+                 : "r"(mine)
+                 : "memory");
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(t.kb0), "=r"(t.kb1) : "r"(mine + 16) : "memory");
+    // the slot has been read (the branch needs the values) when the arrival goes
+    if ((t.type ^ t.mt ^ t.nt ^ t.sp ^ t.kb0 ^ t.kb1) != INT32_MIN) arrive_relaxed(map_to_rank(tdrain(slot), 0));
     return t;
   };
 
@@ -362,10 +387,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     int s = 0;
     uint32_t ph = 0, issued = 0, par = 0;
     bool ok = true;
-    for (int64_t n = 0; ok; ++n) {
-      const int64_t tile = next_tile(n, leader);
-      if (tile < 0) break;
-      const Tile t = plan.decode(a, tile);
+    for (int n = 0; ok; ++n) {
+      const Tile t = leader ? take_tile(n) : read_tile(n);
+      if (t.type < 0) break;
       const int arow = t.mt * BM + (int)rank * BMC, bcol = t.nt * BN + (int)rank * BNC;
       for (int pr = 0; pr < nprod && ok; ++pr) {
         int pa, pb;
@@ -407,10 +431,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     int s = 0, acc = 0;
     uint32_t ph = 0, aph = 0;
     bool ok = true;
-    for (int64_t n = 0; ok; ++n) {
-      const int64_t tile = next_tile(n, false);
-      if (tile < 0) break;
-      const Tile t = plan.decode(a, tile);
+    for (int n = 0; ok; ++n) {
+      const Tile t = read_tile(n);
+      if (t.type < 0) break;
       const int steps = (t.kb1 - t.kb0) * nprod;   // 0 without rows: the epilogue writes zeros
       const uint32_t idesc = IDESC | (t.type == 2 ? IDESC_A_MN : 0u) | (t.type != 0 ? IDESC_B_MN : 0u);
       for (int i0 = 0; i0 < steps && ok; i0 += a.chunk) {
@@ -451,13 +474,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     unsigned char* stage = s_out + (warp - 4) * OUT_WARP_BYTES;
     int acc = 0;
     uint32_t aph = 0;
-    for (int64_t n = 0;; ++n) {
+    for (int n = 0;; ++n) {
       // each warp takes the tile for itself: no barrier among the warps
-      int64_t tile = -1;
-      if (lane == 0) tile = next_tile(n, false);
-      tile = __shfl_sync(0xffffffffu, tile, 0);
-      if (tile < 0) break;
-      const Tile t = plan.decode(a, tile);
+      Tile t;
+      if (lane == 0) t = read_tile(n);
+      t.type = __shfl_sync(0xffffffffu, t.type, 0);
+      t.mt = __shfl_sync(0xffffffffu, t.mt, 0);
+      t.nt = __shfl_sync(0xffffffffu, t.nt, 0);
+      t.sp = __shfl_sync(0xffffffffu, t.sp, 0);
+      t.kb0 = __shfl_sync(0xffffffffu, t.kb0, 0);
+      t.kb1 = __shfl_sync(0xffffffffu, t.kb1, 0);
+      if (t.type < 0) break;
       const int steps = (t.kb1 - t.kb0) * nprod;
       const int64_t row0 = (int64_t)t.mt * BM + (int64_t)rank * BMC + q * 32;
       const int64_t row = row0 + lane;
@@ -470,14 +497,22 @@ __global__ void __launch_bounds__(THREADS, 1)
       const bool is_dx = t.type == 1;
       const int n0 = t.nt * BN + c_lo;
       int nvalid = 0;
-      int64_t orow = row;     // where this lane's row goes
+      // bf16 output goes in 16-byte pieces of whole rows: this lane's are piece
+      // lane & 3 of rows (lane >> 2) + 8 i, at these element offsets; -1: no row
+      int64_t poff[4] = {-1, -1, -1, -1};
       float* fout = nullptr;
       if (KIND == kGrad) {
         const int64_t nv = (is_dx ? plan.rows : min(a.vcols, a.vocab - a.v0)) - row0;
         nvalid = nv <= 0 ? 0 : (nv >= 32 ? 32 : (int)nv);
         float* part = is_dx ? a.dx_part : a.dw_part;
+        int64_t orow = is_dx ? row : a.v0 + row;     // where this lane's row goes
         if (is_dx && a.rowmap) orow = lane < nvalid ? a.rowmap[row] : 0;
-        if (!is_dx) orow = a.v0 + row;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = (lane >> 2) + 8 * i;
+          const int64_t o = __shfl_sync(0xffffffffu, orow, rr);
+          if (rr < nvalid) poff[i] = o * a.hidden + n0 + (lane & 3) * 8;
+        }
         const float* fadd = nullptr;
         if (part != nullptr) {
           fout = part + ((int64_t)t.sp * (is_dx ? a.rows_pad : a.dw_pad) + row) * a.hidden;
@@ -500,21 +535,22 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (is_dx && fout == nullptr && a.dx_add) {
           // bf16: whole-row 16-byte pieces through the staging slice
           const bf16* addp = reinterpret_cast<const bf16*>(a.dx_add);
+          // (all loads before the first use: one latency a tile)
+          uint4 v[BN / 64][4];
 #pragma unroll
-          for (int c = 0; c < BN / 2; c += 32) {
-            uint4 v[4];
+          for (int c = 0; c < BN / 2; c += 32)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int p = lane + 32 * i, rr = p >> 2, pc = p & 3;
-              const int64_t ar = a.rowmap ? __shfl_sync(0xffffffffu, orow, rr) : row0 + rr;
-              v[i] = make_uint4(0, 0, 0, 0);
-              if (rr < nvalid && n0 + c + pc * 8 < a.hidden)
-                v[i] = *reinterpret_cast<const uint4*>(addp + ar * a.hidden + n0 + c + pc * 8);
+              v[c / 32][i] = make_uint4(0, 0, 0, 0);
+              if (poff[i] >= 0 && n0 + c + (lane & 3) * 8 < a.hidden)
+                v[c / 32][i] = *reinterpret_cast<const uint4*>(addp + poff[i] + c);
             }
 #pragma unroll
+          for (int c = 0; c < BN / 2; c += 32) {
+#pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int p = lane + 32 * i, rr = p >> 2, pc = p & 3;
-              *reinterpret_cast<uint4*>(stage + rr * OUT_ROW_BYTES + pc * 16) = v[i];
+              *reinterpret_cast<uint4*>(stage + rr * OUT_ROW_BYTES + pc * 16) = v[c / 32][i];
             }
             __syncwarp();
 #pragma unroll
@@ -535,12 +571,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_after();
         const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)acc * BN + c_lo;
 #pragma unroll
-        for (int c = 0; c < BN / 2; c += 32) {
-          uint32_t r[32];
-          tmem_ld32(taddr + c, r);
+        for (int c = 0; c < BN / 2; c += 64) {
+          uint32_t r0[32], r1[32];
+          tmem_ld32(taddr + c, r0);
+          tmem_ld32(taddr + c + 32, r1);
           tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) f[c + j] += __uint_as_float(r[j]);
+          for (int j = 0; j < 32; ++j) {
+            f[c + j] += __uint_as_float(r0[j]);
+            f[c + 32 + j] += __uint_as_float(r1[j]);
+          }
         }
         tc_fence_before();
         __syncwarp();
@@ -636,11 +676,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             // whole-row 16-byte pieces; a compacted row goes to its token
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int p = lane + 32 * i, rr = p >> 2, pc = p & 3;
-              const int64_t wr = is_dx && a.rowmap ? __shfl_sync(0xffffffffu, orow, rr)
-                                                   : (is_dx ? 0 : a.v0) + row0 + rr;
-              if (rr < nvalid && pc * 8 < ncols)
-                *reinterpret_cast<uint4*>(out + wr * a.hidden + n0 + c + pc * 8) =
+              const int rr = (lane >> 2) + 8 * i, pc = lane & 3;
+              if (poff[i] >= 0 && pc * 8 < ncols)
+                *reinterpret_cast<uint4*>(out + poff[i] + c) =
                     *reinterpret_cast<const uint4*>(stage + rr * OUT_ROW_BYTES + pc * 16);
             }
             __syncwarp();
@@ -667,6 +705,8 @@ __global__ void __launch_bounds__(256) reduce_parts_kernel(const float* __restri
                                                            const int32_t* __restrict__ inv,
                                                            const T* __restrict__ add,
                                                            T* __restrict__ out) {
+  pdl_trigger();
+  pdl_wait();
   const int per_row = hidden / 8;
   const int64_t items = rows * per_row;
   for (int64_t it = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; it < items;
@@ -711,6 +751,8 @@ __device__ __forceinline__ void split3(float v, float& p0, float& p1, float& p2)
 __global__ void __launch_bounds__(256) planes_kernel(const float* __restrict__ src, int64_t ld,
                                                      int64_t rows, int64_t rows_zero, int hidden,
                                                      bf16* __restrict__ dst, int64_t plane) {
+  pdl_trigger();
+  pdl_wait();
   const int per_row = hidden / 8;
   const int64_t items = rows_zero * per_row;
   for (int64_t it = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; it < items;
@@ -796,18 +838,21 @@ static cudaError_t launch(const CUtensorMap& mX, const CUtensorMap& mW, const CU
   cudaError_t e = prepare_device(&mc);
   if (e != cudaSuccess) return e;
   if (tiles <= 0) return cudaSuccess;
+  if (tiles >= (1ll << 31) - 4 * mc) return cudaErrorInvalidValue;
   const int64_t ncl = tiles < mc ? tiles : mc;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3((unsigned)(2 * ncl));
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = SMEM_BYTES;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, linear_kernel<KIND>, mX, mW, mD, mDt, t);
   if (e != cudaSuccess) return e;
   count_launch();
@@ -931,24 +976,17 @@ cudaError_t launch_reduce_parts(const float* part, int splits, int64_t part_stri
   if (rows <= 0) return cudaSuccess;
   const unsigned grid = lin::elementwise_grid(rows * (hidden / 8));
   if (out_f32)
-    lin::reduce_parts_kernel<float><<<grid, 256, 0, st>>>(part, splits, part_stride, rows, hidden, inv,
-                                                          reinterpret_cast<const float*>(add),
-                                                          reinterpret_cast<float*>(out));
-  else
-    lin::reduce_parts_kernel<bf16><<<grid, 256, 0, st>>>(part, splits, part_stride, rows, hidden, inv,
-                                                         reinterpret_cast<const bf16*>(add),
-                                                         reinterpret_cast<bf16*>(out));
-  count_launch();
-  return cudaGetLastError();
+    return launch_after(lin::reduce_parts_kernel<float>, grid, 256, 0, st, 1, part, splits, part_stride, rows,
+                        hidden, inv, reinterpret_cast<const float*>(add), reinterpret_cast<float*>(out));
+  return launch_after(lin::reduce_parts_kernel<bf16>, grid, 256, 0, st, 1, part, splits, part_stride, rows,
+                      hidden, inv, reinterpret_cast<const bf16*>(add), reinterpret_cast<bf16*>(out));
 }
 
 cudaError_t launch_planes(const float* src, int64_t ld, int64_t rows, int64_t rows_zero, int hidden,
                           void* dst, int64_t plane, cudaStream_t st) {
   if (rows_zero <= 0) return cudaSuccess;
-  lin::planes_kernel<<<lin::elementwise_grid(rows_zero * (hidden / 8)), 256, 0, st>>>(
-      src, ld, rows, rows_zero, hidden, reinterpret_cast<bf16*>(dst), plane);
-  count_launch();
-  return cudaGetLastError();
+  return launch_after(lin::planes_kernel, lin::elementwise_grid(rows_zero * (hidden / 8)), 256, 0, st, 1, src, ld,
+                      rows, rows_zero, hidden, reinterpret_cast<bf16*>(dst), plane);
 }
 
 }  // namespace moe

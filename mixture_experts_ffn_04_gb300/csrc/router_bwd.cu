@@ -15,6 +15,8 @@
 #include <algorithm>
 #include <cmath>
 
+#include <cooperative_groups.h>
+
 #include "../../include/moe_train.h"
 #include "common.cuh"
 #include "internal.h"
@@ -45,10 +47,19 @@ struct DzArgs {
   double balance, zmean;   // scales of the sums of pn and lse^2
 };
 
-// Slots routed to each expert (integers: the order does not matter).
-__global__ void __launch_bounds__(256) route_hist_kernel(const int32_t* __restrict__ idx, int64_t n,
-                                                         int E, int32_t* counts, uint32_t* flags) {
+// Slots routed to each expert (integers: the order does not matter), by one
+// cluster: each block counts its part in shared memory, then adds up its share of
+// the experts over the blocks.  Nothing has to be zero before.  One block takes
+// 18 us for 32768 slots (shared-memory atomics), eight 5.  meta: the ticket and
+// the tile counter, zeroed here.
+constexpr int kHistCluster = 8, kHistOneBlock = 4096;
+__global__ void __launch_bounds__(1024) route_hist_kernel(const int32_t* __restrict__ idx, int64_t n,
+                                                          int E, int32_t* counts, int32_t* meta,
+                                                          uint32_t* flags) {
   extern __shared__ int32_t s_h[];
+  pdl_trigger();
+  pdl_wait();
+  if (blockIdx.x == 0 && threadIdx.x < 2) meta[threadIdx.x] = 0;
   for (int e = threadIdx.x; e < E; e += blockDim.x) s_h[e] = 0;
   __syncthreads();
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n;
@@ -57,9 +68,19 @@ __global__ void __launch_bounds__(256) route_hist_kernel(const int32_t* __restri
     if (e >= 0 && e < E) atomicAdd(&s_h[e], 1);
     else set_flag(flags, kFlagRoute);
   }
-  __syncthreads();
-  for (int e = threadIdx.x; e < E; e += blockDim.x)
-    if (s_h[e]) atomicAdd(&counts[e], s_h[e]);
+  if (gridDim.x == 1) {
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += blockDim.x) counts[e] = s_h[e];
+    return;
+  }
+  cooperative_groups::cluster_group cl = cooperative_groups::this_cluster();
+  cl.sync();
+  for (int e = blockIdx.x * blockDim.x + threadIdx.x; e < E; e += gridDim.x * blockDim.x) {
+    int c = 0;
+    for (int r = 0; r < kHistCluster; ++r) c += *cl.map_shared_rank(s_h + e, r);
+    counts[e] = c;
+  }
+  cl.sync();   // the blocks' shared memory stays until all have read it
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -71,6 +92,14 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+
+// e^v by the hardware's 2^x: a few ulp for the arguments near 0 that carry the
+// weight, |v| 2^-24 more for the others.
+__device__ __forceinline__ float exp_of(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v * 1.4426950408889634f));
+  return r;
 }
 
 // The losses: block sums in fp64, the last block adds the blocks in order.
@@ -122,6 +151,8 @@ __device__ void finish_aux(const DzArgs& a, double sum_pn, double sum_l2) {
 template <int NP>
 __global__ void __launch_bounds__(256) router_dz_small_kernel(const DzArgs a) {
   extern __shared__ float s_f[];
+  pdl_trigger();
+  pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   float* row = s_f + (size_t)warp * 64 * NP;
   float cnt[2 * NP];
@@ -130,7 +161,10 @@ __global__ void __launch_bounds__(256) router_dz_small_kernel(const DzArgs a) {
     const int e = 64 * (j / 2) + 2 * lane + (j & 1);
     cnt[j] = a.counts && e < a.E ? (float)a.counts[e] : 0.0f;
   }
+  // (fp64 arithmetic is slow on this GPU: a few tokens' terms first add up in fp32)
   double sum_pn = 0.0, sum_l2 = 0.0;
+  float few_pn = 0.0f, few_l2 = 0.0f;
+  int few = 0;
   for (int64_t t = blockIdx.x * (int64_t)warps + warp; t < a.rows; t += (int64_t)gridDim.x * warps) {
     if (t >= a.T) {   // rows the weight gradient's last k-block reads
       for (int p = 0; p < a.planes; ++p)
@@ -148,6 +182,7 @@ __global__ void __launch_bounds__(256) router_dz_small_kernel(const DzArgs a) {
     float z[2 * NP];
 #pragma unroll
     for (int j = 0; j < 2 * NP; ++j) z[j] = 0.0f;
+#pragma unroll 4
     for (int s = 0; s < a.nsplit; ++s) {
       const float* l = a.logits + s * a.split_stride + t * a.ldl + 2 * lane;
 #pragma unroll
@@ -171,15 +206,21 @@ __global__ void __launch_bounds__(256) router_dz_small_kernel(const DzArgs a) {
 #pragma unroll
     for (int j = 0; j < 2 * NP; ++j) {
       const int e = 64 * (j / 2) + 2 * lane + (j & 1);
-      p[j] = e < a.E ? expf(z[j] - m) : 0.0f;
+      p[j] = e < a.E ? exp_of(z[j] - m) : 0.0f;
       sum += p[j];
       pn = fmaf(p[j], cnt[j], pn);
     }
     sum = warp_sum(sum);
     pn = warp_sum(pn) / sum;
     const float inv = 1.0f / sum, lse = m + logf(sum);
-    sum_pn += (double)pn;
-    sum_l2 += (double)lse * lse;
+    few_pn += pn;
+    few_l2 = fmaf(lse, lse, few_l2);
+    if (++few == 8) {
+      sum_pn += (double)few_pn;
+      sum_l2 += (double)few_l2;
+      few_pn = few_l2 = 0.0f;
+      few = 0;
+    }
     const float zs = slot >= 0 ? row[slot] : -INFINITY;
     __syncwarp();
     float w, dot = 0.0f, add = 0.0f;
@@ -187,9 +228,9 @@ __global__ void __launch_bounds__(256) router_dz_small_kernel(const DzArgs a) {
       float top = m, den = sum;
       if (a.norm) {
         top = warp_max(zs);
-        den = warp_sum(slot >= 0 ? expf(zs - top) : 0.0f);
+        den = warp_sum(slot >= 0 ? exp_of(zs - top) : 0.0f);
       }
-      w = slot >= 0 ? expf(zs - top) / den : 0.0f;
+      w = slot >= 0 ? exp_of(zs - top) / den : 0.0f;
       dot = warp_sum(w * D);
       add = a.norm ? w * (D - dot) : w * D;
       if (slot < 0) add = 0.0f;
@@ -223,7 +264,7 @@ __global__ void __launch_bounds__(256) router_dz_small_kernel(const DzArgs a) {
         if (e + h < a.E) {
           v[h] += p[2 * j + h] * inv * (base + a.cb * cnt[2 * j + h]);
         } else if (e + h < a.ncols) {
-          const float s = 1.0f / (1.0f + expf(-z[2 * j + h]));
+          const float s = 1.0f / (1.0f + exp_of(-z[2 * j + h]));
           v[h] = dg * s * (1.0f - s);
         } else {
           v[h] = 0.0f;
@@ -240,13 +281,15 @@ __global__ void __launch_bounds__(256) router_dz_small_kernel(const DzArgs a) {
     }
     __syncwarp();
   }
-  if (a.aux) finish_aux(a, sum_pn, sum_l2);
+  if (a.aux) finish_aux(a, sum_pn + (double)few_pn, sum_l2 + (double)few_l2);
 }
 
 // Any number of columns and slots: a warp a token; z and the slots'
 // contributions of its token in shared memory (2 ncols floats a warp).
 __global__ void __launch_bounds__(256) router_dz_kernel(const DzArgs a) {
   extern __shared__ float s_f[];
+  pdl_trigger();
+  pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   float* z = s_f + (size_t)warp * 2 * a.ncols;
   float* acc = z + a.ncols;
@@ -345,7 +388,6 @@ struct RbLayout {
   LinearSplit split;
   bool dx_direct, dw_direct;
   size_t meta, counts, part, dz, xpl, wpl, dx_part, dw_part, total;
-  size_t meta_bytes;
 };
 RbLayout layout_rb(const Shape& s) {
   RbLayout R;
@@ -362,9 +404,8 @@ RbLayout layout_rb(const Shape& s) {
     off += (bytes + 255) & ~(size_t)255;
     return at;
   };
-  R.meta = take(256);   // ticket, tile counter; zeroed with the counts
+  R.meta = take(256);   // ticket, tile counter
   R.counts = take((size_t)s.E * 4);
-  R.meta_bytes = off - R.meta;
   R.part = take((size_t)kDzBlocks * 16);
   R.dz = take((size_t)R.planes * R.rows_pad * R.cols_pad * 2);
   R.xpl = take(R.planes > 1 ? (size_t)R.planes * R.rows_pad * s.H * 2 : 0);
@@ -416,15 +457,13 @@ extern "C" moe_status moe_router_backward(const moe_shape* shape, const void* x,
   uint32_t* flags = reinterpret_cast<uint32_t*>(b);
   int32_t* meta = reinterpret_cast<int32_t*>(b + R.meta);
   int32_t* counts = reinterpret_cast<int32_t*>(b + R.counts);
-  CHECK_CUDA(cudaMemsetAsync(meta, 0, R.meta_bytes, st));
   const int64_t slots = s.T * s.k;
-  const unsigned hb = (unsigned)std::min<int64_t>((slots + 1023) / 1024, 256);
+  const unsigned hb = slots <= kHistOneBlock ? 1u : (unsigned)kHistCluster;
   // (the pass that finds routes out of range, so it runs in any case)
   if ((size_t)s.E * 4 > 48 * 1024)
     CHECK_CUDA(cudaFuncSetAttribute(route_hist_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, s.E * 4));
-  route_hist_kernel<<<hb, 256, (size_t)s.E * 4, st>>>(topk_idx, slots, s.E, counts, flags);
-  count_launch();
-  CHECK_CUDA(cudaGetLastError());
+  CHECK_CUDA(launch_after(route_hist_kernel, hb, 1024, (size_t)s.E * 4, st, hb, topk_idx, slots, s.E, counts,
+                          meta, flags));
   int nsplit = 1;
   e = router_gemm(s, R.L, b, x, w_router, &nsplit, st);
   if (e != MOE_OK) return e;
@@ -461,10 +500,9 @@ extern "C" moe_status moe_router_backward(const moe_shape* shape, const void* x,
     const int warps = 4;
     const unsigned blocks = (unsigned)std::min<int64_t>((d.rows + warps - 1) / warps, kDzBlocks);
     const size_t smem = (size_t)warps * 64 * np * 4;
-    if (np == 1) router_dz_small_kernel<1><<<blocks, 32 * warps, smem, st>>>(d);
-    else if (np == 2) router_dz_small_kernel<2><<<blocks, 32 * warps, smem, st>>>(d);
-    else if (np == 4) router_dz_small_kernel<4><<<blocks, 32 * warps, smem, st>>>(d);
-    else router_dz_small_kernel<8><<<blocks, 32 * warps, smem, st>>>(d);
+    auto kernel = np == 1 ? router_dz_small_kernel<1> : np == 2 ? router_dz_small_kernel<2>
+                : np == 4 ? router_dz_small_kernel<4> : router_dz_small_kernel<8>;
+    CHECK_CUDA(launch_after(kernel, blocks, 32 * warps, smem, st, 1, d));
   } else {
     const size_t per_warp = 2 * (size_t)s.ncols * 4;
     const int warps = (int)std::max<size_t>(1, std::min<size_t>(8, 200 * 1024 / per_warp));
@@ -472,10 +510,8 @@ extern "C" moe_status moe_router_backward(const moe_shape* shape, const void* x,
       CHECK_CUDA(cudaFuncSetAttribute(router_dz_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       (int)(per_warp * warps)));
     const int64_t blocks = std::min<int64_t>((d.rows + warps - 1) / warps, kDzBlocks);
-    router_dz_kernel<<<(unsigned)blocks, 32 * warps, per_warp * warps, st>>>(d);
+    CHECK_CUDA(launch_after(router_dz_kernel, (unsigned)blocks, 32 * warps, per_warp * warps, st, 1, d));
   }
-  count_launch();
-  CHECK_CUDA(cudaGetLastError());
   LinearGradArgs q = {};
   q.planes = R.planes;
   q.d = b + R.dz;

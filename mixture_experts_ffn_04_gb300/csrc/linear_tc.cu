@@ -6,7 +6,7 @@
 // in one launch over one tile list.
 //
 // A pair of SMs computes 256 x 256 output tiles over 64-wide k-blocks: CTA r
-// keeps rows 128r .. of the A tile and columns 128r .. of the B tile, six
+// keeps rows 128r .. of the A tile and columns 128r .. of the B tile, seven
 // 32 KB stages; per k-block an SM reads 32 KB of operands for 512 clocks of
 // MMA.  Operands that are not K-major are read in their stored layout as
 // 64-wide boxes with the 128-byte swizzle (MN-major descriptors), so neither D
@@ -58,7 +58,7 @@ namespace lin {
 using namespace tc;
 
 constexpr int BM = kLinTile, BN = kLinTile, BMC = BM / 2, BNC = BN / 2, BK = kLinK;
-constexpr int S = 6;
+constexpr int S = 7;
 constexpr int A_BYTES = BMC * BK * 2, B_BYTES = BNC * BK * 2;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int BOX_BYTES = 64 * BK * 2;
@@ -74,9 +74,7 @@ constexpr uint32_t TMEM_COLS = 512;
 constexpr int NSLOT = 4;
 constexpr int READERS = 2 + 2 * EPI_WARPS;   // of a tile slot: odd producer, MMA, epilogue warps
 constexpr int BAR_BYTES = 512;
-constexpr int OUT_ROW_BYTES = 80;   // 64 bytes of a chunk's row, padded
-constexpr int OUT_WARP_BYTES = 32 * OUT_ROW_BYTES;
-constexpr int SMEM_BYTES = 1024 + RING_BYTES + BAR_BYTES + EPI_WARPS * OUT_WARP_BYTES;
+constexpr int SMEM_BYTES = 1024 + RING_BYTES + BAR_BYTES;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget of one CTA");
 static_assert((2 * S + 5 + 2 * NSLOT) * 8 + 8 + NSLOT * 32 <= BAR_BYTES, "barrier area");
 constexpr int kGroupM = 8;
@@ -115,6 +113,7 @@ struct Args {
   float* dw_part;
   int64_t dw_pad;
   int want_dx, want_dw;
+  int wide_dx, wide_dw;   // rows of dx (and dx_add), of dw on 32-byte boundaries
   int chunk;   // k-blocks the tensor cores add up before the fp32 registers do
 };
 
@@ -252,22 +251,51 @@ __device__ __forceinline__ float pick(float a, float b, int i, int j) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Write 32 rows x 32 bf16 columns (one row a lane in `packed`) through the
-// warp's staging slice as 16-byte pieces of whole rows.
-__device__ __forceinline__ void store_chunk(unsigned char* stage, int lane, const uint4 (&packed)[4],
-                                            bf16* base, int64_t ld) {
-  unsigned char* my_row = stage + lane * OUT_ROW_BYTES;
-#pragma unroll
-  for (int v = 0; v < 4; ++v) reinterpret_cast<uint4*>(my_row)[v] = packed[v];
-  __syncwarp();
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int p = lane + 32 * i;
-    const int rr = p >> 2, pc = p & 3;
-    *reinterpret_cast<uint4*>(base + (int64_t)rr * ld + pc * 8) =
-        *reinterpret_cast<const uint4*>(stage + rr * OUT_ROW_BYTES + pc * 16);
+// Global accesses of the epilogue: a lane owns a row and moves it in 32-byte
+// sectors, straight between registers and memory.  (Through a staging slice in
+// shared memory, whole rows at a time, a 256 x 256 bf16 tile took 4000 clocks to
+// store: the MMAs' operand reads hold the shared memory's bandwidth.)  Rows that
+// are only 16-byte aligned go in halves.
+struct Sector {
+  uint32_t v[8];
+};
+__device__ __forceinline__ Sector load_sector(const void* p, bool wide, bool second) {
+  Sector s;
+  if (wide) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(s.v[0]), "=r"(s.v[1]), "=r"(s.v[2]), "=r"(s.v[3]), "=r"(s.v[4]), "=r"(s.v[5]),
+                   "=r"(s.v[6]), "=r"(s.v[7])
+                 : "l"(p)
+                 : "memory");
+  } else {
+    const uint4 a = reinterpret_cast<const uint4*>(p)[0];
+    const uint4 b = second ? reinterpret_cast<const uint4*>(p)[1] : make_uint4(0, 0, 0, 0);
+    s = {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
   }
-  __syncwarp();
+  return s;
+}
+__device__ __forceinline__ void store_sector(void* p, const Sector& s, bool wide, bool second) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(s.v[0]), "r"(s.v[1]),
+                 "r"(s.v[2]), "r"(s.v[3]), "r"(s.v[4]), "r"(s.v[5]), "r"(s.v[6]), "r"(s.v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(s.v[0], s.v[1], s.v[2], s.v[3]);
+    if (second) reinterpret_cast<uint4*>(p)[1] = make_uint4(s.v[4], s.v[5], s.v[6], s.v[7]);
+  }
+}
+// 16 values as bf16, 8 as fp32.
+__device__ __forceinline__ Sector pack_bf16(const float* f) {
+  Sector s;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s.v[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+  return s;
+}
+__device__ __forceinline__ Sector pack_f32(const float* f) {
+  Sector s;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s.v[i] = __float_as_uint(f[i]);
+  return s;
 }
 
 template <int KIND>
@@ -285,7 +313,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   unsigned char* s_slots = smem + RING_BYTES + BAR_BYTES - NSLOT * sizeof(Tile);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5 + 2 * NSLOT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  unsigned char* s_out = smem + RING_BYTES + BAR_BYTES;
 
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -363,18 +390,23 @@ __global__ void __launch_bounds__(THREADS, 1)
     mbar_arrive_cluster(map_to_rank(tfill(slot), 1));
     return t;
   };
-  auto read_tile = [&](int n) -> Tile {
-    const int slot = n % NSLOT;
-    const uint32_t use = (uint32_t)n / NSLOT;
+  auto load_slot = [&](int slot) -> Tile {
     Tile t;
-    t.type = -1;
-    if (!wait_cl(tfill(slot), use & 1u, abort_flag)) return t;
     const uint32_t mine = smem_u32(s_slots + slot * sizeof(Tile));
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(t.type), "=r"(t.mt), "=r"(t.nt), "=r"(t.sp)
                  : "r"(mine)
                  : "memory");
     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(t.kb0), "=r"(t.kb1) : "r"(mine + 16) : "memory");
+    return t;
+  };
+  auto read_tile = [&](int n) -> Tile {
+    const int slot = n % NSLOT;
+    const uint32_t use = (uint32_t)n / NSLOT;
+    Tile t;
+    t.type = -1;
+    if (!wait_cl(tfill(slot), use & 1u, abort_flag)) return t;
+    t = load_slot(slot);
     // the slot has been read (the branch needs the values) when the arrival goes
     if ((t.type ^ t.mt ^ t.nt ^ t.sp ^ t.kb0 ^ t.kb1) != INT32_MIN) arrive_relaxed(map_to_rank(tdrain(slot), 0));
     return t;
@@ -471,19 +503,20 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int q = warp & 3;                 // TMEM lanes 32q .. 32q+31
     const int half = (warp - 4) / 4;        // columns 128 half ..
     const int c_lo = half * (BN / 2);
-    unsigned char* stage = s_out + (warp - 4) * OUT_WARP_BYTES;
     int acc = 0;
     uint32_t aph = 0;
     for (int n = 0;; ++n) {
       // each warp takes the tile for itself: no barrier among the warps
       Tile t;
-      if (lane == 0) t = read_tile(n);
-      t.type = __shfl_sync(0xffffffffu, t.type, 0);
-      t.mt = __shfl_sync(0xffffffffu, t.mt, 0);
-      t.nt = __shfl_sync(0xffffffffu, t.nt, 0);
-      t.sp = __shfl_sync(0xffffffffu, t.sp, 0);
-      t.kb0 = __shfl_sync(0xffffffffu, t.kb0, 0);
-      t.kb1 = __shfl_sync(0xffffffffu, t.kb1, 0);
+      {
+        const int slot = n % NSLOT;
+        int w = 0;
+        if (lane == 0) w = wait_cl(tfill(slot), ((uint32_t)n / NSLOT) & 1u, abort_flag) ? 1 : 0;
+        if (!__shfl_sync(0xffffffffu, w, 0)) break;
+        t = load_slot(slot);
+        __syncwarp();
+        if (lane == 0) arrive_relaxed(map_to_rank(tdrain(slot), 0));
+      }
       if (t.type < 0) break;
       const int steps = (t.kb1 - t.kb0) * nprod;
       const int64_t row0 = (int64_t)t.mt * BM + (int64_t)rank * BMC + q * 32;
@@ -497,68 +530,53 @@ __global__ void __launch_bounds__(THREADS, 1)
       const bool is_dx = t.type == 1;
       const int n0 = t.nt * BN + c_lo;
       int nvalid = 0;
-      // bf16 output goes in 16-byte pieces of whole rows: this lane's are piece
-      // lane & 3 of rows (lane >> 2) + 8 i, at these element offsets; -1: no row
-      int64_t poff[4] = {-1, -1, -1, -1};
-      float* fout = nullptr;
+      float* fout = nullptr;   // this lane's row of the output: fp32, or bf16
+      bf16* hout = nullptr;
+      bool wide = true;        // its sectors are aligned
       if (KIND == kGrad) {
         const int64_t nv = (is_dx ? plan.rows : min(a.vcols, a.vocab - a.v0)) - row0;
         nvalid = nv <= 0 ? 0 : (nv >= 32 ? 32 : (int)nv);
         float* part = is_dx ? a.dx_part : a.dw_part;
-        int64_t orow = is_dx ? row : a.v0 + row;     // where this lane's row goes
+        int64_t orow = is_dx ? row : a.v0 + row;
         if (is_dx && a.rowmap) orow = lane < nvalid ? a.rowmap[row] : 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rr = (lane >> 2) + 8 * i;
-          const int64_t o = __shfl_sync(0xffffffffu, orow, rr);
-          if (rr < nvalid) poff[i] = o * a.hidden + n0 + (lane & 3) * 8;
-        }
         const float* fadd = nullptr;
+        const bf16* hadd = nullptr;
         if (part != nullptr) {
-          fout = part + ((int64_t)t.sp * (is_dx ? a.rows_pad : a.dw_pad) + row) * a.hidden;
+          fout = part + ((int64_t)t.sp * (is_dx ? a.rows_pad : a.dw_pad) + row) * a.hidden + n0;
           if (is_dx && a.accumulate) fadd = fout;
         } else if (a.out_f32) {
-          fout = reinterpret_cast<float*>(is_dx ? a.dx : a.dw) + orow * a.hidden;
-          if (is_dx && a.dx_add) fadd = reinterpret_cast<const float*>(a.dx_add) + orow * a.hidden;
+          fout = reinterpret_cast<float*>(is_dx ? a.dx : a.dw) + orow * a.hidden + n0;
+          if (is_dx && a.dx_add) fadd = reinterpret_cast<const float*>(a.dx_add) + orow * a.hidden + n0;
+          wide = is_dx ? a.wide_dx : a.wide_dw;
+        } else {
+          hout = reinterpret_cast<bf16*>(is_dx ? a.dx : a.dw) + orow * a.hidden + n0;
+          if (is_dx && a.dx_add) hadd = reinterpret_cast<const bf16*>(a.dx_add) + orow * a.hidden + n0;
+          wide = is_dx ? a.wide_dx : a.wide_dw;
         }
+        // (all loads before the first use: one latency a tile; hidden is a
+        // multiple of 8)
         if (fadd != nullptr && lane < nvalid) {
 #pragma unroll
-          for (int v = 0; v < BN / 8; ++v)
-            if (n0 + 4 * v < a.hidden) {
-              const float4 b = reinterpret_cast<const float4*>(fadd + n0)[v];
-              f[4 * v] = b.x;
-              f[4 * v + 1] = b.y;
-              f[4 * v + 2] = b.z;
-              f[4 * v + 3] = b.w;
+          for (int c = 0; c < BN / 2; c += 8)
+            if (n0 + c < a.hidden) {
+              const Sector v = load_sector(fadd + c, wide, true);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) f[c + j] = __uint_as_float(v.v[j]);
             }
         }
-        if (is_dx && fout == nullptr && a.dx_add) {
-          // bf16: whole-row 16-byte pieces through the staging slice
-          const bf16* addp = reinterpret_cast<const bf16*>(a.dx_add);
-          // (all loads before the first use: one latency a tile)
-          uint4 v[BN / 64][4];
+        if (hadd != nullptr && lane < nvalid) {
+          Sector v[BN / 32];
 #pragma unroll
-          for (int c = 0; c < BN / 2; c += 32)
+          for (int c = 0; c < BN / 2; c += 16)
+            if (n0 + c < a.hidden) v[c / 16] = load_sector(hadd + c, wide && n0 + c + 16 <= a.hidden, n0 + c + 16 <= a.hidden);
+            else v[c / 16] = {};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              v[c / 32][i] = make_uint4(0, 0, 0, 0);
-              if (poff[i] >= 0 && n0 + c + (lane & 3) * 8 < a.hidden)
-                v[c / 32][i] = *reinterpret_cast<const uint4*>(addp + poff[i] + c);
+          for (int c = 0; c < BN / 2; c += 16)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              f[c + 2 * j] = __uint_as_float(v[c / 16].v[j] << 16);
+              f[c + 2 * j + 1] = __uint_as_float(v[c / 16].v[j] & 0xFFFF0000u);
             }
-#pragma unroll
-          for (int c = 0; c < BN / 2; c += 32) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int p = lane + 32 * i, rr = p >> 2, pc = p & 3;
-              *reinterpret_cast<uint4*>(stage + rr * OUT_ROW_BYTES + pc * 16) = v[c / 32][i];
-            }
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              unpack16(reinterpret_cast<const uint4*>(stage + lane * OUT_ROW_BYTES)[j], f + c + 8 * j,
-                       (const bf16*)nullptr);
-            __syncwarp();
-          }
         }
       }
       bool ok = true;
@@ -626,7 +644,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int64_t dt = live ? (int64_t)a.target[row] - col0 : -1;
         const float l2 = live ? a.lse[row] * kLog2e : 0.0f;
         const float g = live ? a.g[row] : 0.0f;
-        bf16* drow = a.d + row0 * a.d_ld + (int64_t)t.nt * BN + c_lo;
+        bf16* drow = a.d + row * a.d_ld + (int64_t)t.nt * BN + c_lo;
 #pragma unroll
         for (int j = 0; j < BN / 2; ++j) f[j] = ex2(fmaf(f[j], kLog2e, -l2)) * g;
         if (dt >= 0 && dt < BN / 2) {
@@ -638,51 +656,29 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int j = 0; j < BN / 2; ++j) f[j] = live && j < left ? f[j] : 0.0f;
         }
 #pragma unroll
-        for (int c = 0; c < BN / 2; c += 32) {
+        for (int c = 0; c < BN / 2; c += 16) {
           for (int p = 0; p < a.planes; ++p) {
-            uint4 pk[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) pk[j] = pack16(f + c + 8 * j, (const bf16*)nullptr);
-            store_chunk(stage, lane, pk, drow + p * a.d_plane * a.d_ld + c, a.d_ld);
+            store_sector(drow + p * a.d_plane * a.d_ld + c, pack_bf16(f + c), true, true);
             if (p + 1 < a.planes) {
               // what this plane leaves for the next one
 #pragma unroll
-              for (int j = 0; j < 32; ++j) {
+              for (int j = 0; j < 16; ++j) {
                 const float rest = f[c + j] - __bfloat162float(__float2bfloat16_rn(f[c + j]));
                 f[c + j] = isfinite(rest) ? rest : 0.0f;
               }
             }
           }
         }
-      } else {
+      } else if (lane < nvalid) {
+        if (fout != nullptr) {
 #pragma unroll
-        for (int c = 0; c < BN / 2; c += 32) {
-          const int ncols = min(32, a.hidden - (n0 + c));   // a multiple of 8
-          if (ncols <= 0) break;
-          if (fout != nullptr) {
-            if (lane < nvalid) {
+          for (int c = 0; c < BN / 2; c += 8)
+            if (n0 + c < a.hidden) store_sector(fout + c, pack_f32(f + c), wide, true);
+        } else {
 #pragma unroll
-              for (int v = 0; v < 8; ++v)
-                if (4 * v < ncols)
-                  reinterpret_cast<float4*>(fout + n0 + c)[v] =
-                      make_float4(f[c + 4 * v], f[c + 4 * v + 1], f[c + 4 * v + 2], f[c + 4 * v + 3]);
-            }
-          } else {
-            bf16* out = reinterpret_cast<bf16*>(is_dx ? a.dx : a.dw);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              reinterpret_cast<uint4*>(stage + lane * OUT_ROW_BYTES)[j] = pack16(f + c + 8 * j, (const bf16*)nullptr);
-            __syncwarp();
-            // whole-row 16-byte pieces; a compacted row goes to its token
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int rr = (lane >> 2) + 8 * i, pc = lane & 3;
-              if (poff[i] >= 0 && pc * 8 < ncols)
-                *reinterpret_cast<uint4*>(out + poff[i] + c) =
-                    *reinterpret_cast<const uint4*>(stage + rr * OUT_ROW_BYTES + pc * 16);
-            }
-            __syncwarp();
-          }
+          for (int c = 0; c < BN / 2; c += 16)
+            if (n0 + c < a.hidden)
+              store_sector(hout + c, pack_bf16(f + c), wide && n0 + c + 16 <= a.hidden, n0 + c + 16 <= a.hidden);
         }
       }
     }
@@ -960,6 +956,10 @@ cudaError_t launch_linear_grad(const LinearGradArgs& a, cudaStream_t st) {
   t.dw = a.dw;
   t.dw_part = a.dw_part;
   t.dw_pad = a.dw_pad;
+  auto aligned32 = [](const void* p) { return ((uintptr_t)p & 31u) == 0; };
+  const bool rows32 = a.hidden * (a.out_f32 ? 4 : 2) % 32 == 0;
+  t.wide_dx = rows32 && aligned32(a.dx) && aligned32(a.dx_add);
+  t.wide_dw = rows32 && aligned32(a.dw);
   t.want_dx = a.dx_part != nullptr || a.dx != nullptr;
   t.want_dw = a.dw_part != nullptr || a.dw != nullptr;
   if ((t.want_dx && t.ks_dx > 1 && !a.dx_part) || (t.want_dw && t.ks_dw > 1 && !a.dw_part))

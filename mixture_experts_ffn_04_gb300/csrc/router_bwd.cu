@@ -498,7 +498,8 @@ extern "C" moe_status moe_router_backward(const moe_shape* shape, const void* x,
   if (s.k <= 32 && s.ncols <= 512) {
     const int np = s.ncols <= 64 ? 1 : s.ncols <= 128 ? 2 : s.ncols <= 256 ? 4 : 8;
     const int warps = 4;
-    const unsigned blocks = (unsigned)std::min<int64_t>((d.rows + warps - 1) / warps, kDzBlocks);
+    // one wave (64 to 80 registers: at least six blocks an SM)
+    const unsigned blocks = (unsigned)std::min<int64_t>((d.rows + warps - 1) / warps, 6 * tc_sm_count());
     const size_t smem = (size_t)warps * 64 * np * 4;
     auto kernel = np == 1 ? router_dz_small_kernel<1> : np == 2 ? router_dz_small_kernel<2>
                 : np == 4 ? router_dz_small_kernel<4> : router_dz_small_kernel<8>;

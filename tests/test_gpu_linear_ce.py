@@ -238,3 +238,19 @@ def test_repeatable_other_stream_and_graph():
     graph.replay()
     c = check(x, w, t, torch.bfloat16)
     assert torch.equal(a, c[1]) and torch.equal(b[0], c[2]) and torch.equal(b[1], c[3])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_outputs_on_16_byte_boundaries(dtype):
+    """dx and dw that start 16 bytes past a 32-byte boundary."""
+    T, H, V = 200, 256, 700
+    x, w, t = make(T, H, V, dtype, ignored=0.2, seed=4)
+    op, loss, dx, dw = check(x, w, t, dtype)
+    o = 16 // x.element_size()
+    bx = torch.full((T * H + 2 * o,), 3.0, device="cuda", dtype=dtype)
+    bw = torch.full((V * H + 2 * o,), 3.0, device="cuda", dtype=dtype)
+    vx, vw = bx[o: o + T * H].view(T, H), bw[o: o + V * H].view(V, H)
+    op.backward(x, w, t, dx=vx, dw=vw)
+    assert torch.equal(vx, dx) and torch.equal(vw, dw)
+    for b in (bx, bw):
+        assert (b[:o] == 3).all() and (b[-o:] == 3).all()

@@ -6,7 +6,7 @@
 // in one launch over one tile list.
 //
 // A pair of SMs computes 256 x 256 output tiles over 64-wide k-blocks: CTA r
-// keeps rows 128r .. of the A tile and columns 128r .. of the B tile, seven
+// keeps rows 128r .. of the A tile and columns 128r .. of the B tile, six
 // 32 KB stages; per k-block an SM reads 32 KB of operands for 512 clocks of
 // MMA.  Operands that are not K-major are read in their stored layout as
 // 64-wide boxes with the 128-byte swizzle (MN-major descriptors), so neither D
@@ -58,7 +58,7 @@ namespace lin {
 using namespace tc;
 
 constexpr int BM = kLinTile, BN = kLinTile, BMC = BM / 2, BNC = BN / 2, BK = kLinK;
-constexpr int S = 7;
+constexpr int S = 6;
 constexpr int A_BYTES = BMC * BK * 2, B_BYTES = BNC * BK * 2;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int BOX_BYTES = 64 * BK * 2;
@@ -72,9 +72,10 @@ constexpr int ROLE_REGS = 56, EPI_REGS = 224;
 static_assert(ROLE_REGS + 2 * EPI_REGS <= 3 * 168, "register pool of the launch");
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int NSLOT = 4;
-constexpr int READERS = 2 + 2 * EPI_WARPS;   // of a tile slot: odd producer, MMA, epilogue warps
+constexpr int READERS = 4 + 2 * EPI_WARPS;   // of a tile slot: odd producer, MMA, prefetch and epilogue warps
 constexpr int BAR_BYTES = 512;
-constexpr int SMEM_BYTES = 1024 + RING_BYTES + BAR_BYTES;
+constexpr int STAGE_WARP = 4096;   // output staging of an epilogue warp: 32 rows of 128 bytes
+constexpr int SMEM_BYTES = 1024 + RING_BYTES + EPI_WARPS * STAGE_WARP + BAR_BYTES;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget of one CTA");
 static_assert((2 * S + 5 + 2 * NSLOT) * 8 + 8 + NSLOT * 32 <= BAR_BYTES, "barrier area");
 constexpr int kGroupM = 8;
@@ -113,7 +114,7 @@ struct Args {
   float* dw_part;
   int64_t dw_pad;
   int want_dx, want_dw;
-  int wide_dx, wide_dw;   // rows of dx (and dx_add), of dw on 32-byte boundaries
+  int wide_dx;   // rows of dx and dx_add on 32-byte boundaries
   int chunk;   // k-blocks the tensor cores add up before the fp32 registers do
 };
 
@@ -251,11 +252,42 @@ __device__ __forceinline__ float pick(float a, float b, int i, int j) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Global accesses of the epilogue: a lane owns a row and moves it in 32-byte
-// sectors, straight between registers and memory.  (Through a staging slice in
-// shared memory, whole rows at a time, a 256 x 256 bf16 tile took 4000 clocks to
-// store: the MMAs' operand reads hold the shared memory's bandwidth.)  Rows that
-// are only 16-byte aligned go in halves.
+// Output goes through a warp's staging slice (32 rows of 128 bytes, 128-byte
+// swizzle: conflict-free 16-byte pieces) and out by TMA, one box a slice: with a
+// lane storing its own row instead, every instruction touches 32 lines, and a
+// 256 x 256 bf16 tile took the SM about 6000 clocks.  add: the box is added to
+// what is there (fp32).
+__device__ __forceinline__ void put_piece(uint32_t stage, int lane, int j, uint4 v) {
+  const uint32_t at = stage + lane * 128 + ((j ^ (lane & 7)) << 4);
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ void stage_free(int lane) {
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  __syncwarp();
+}
+__device__ __forceinline__ void stage_out(const CUtensorMap* map, uint32_t stage, int lane, int col, int row,
+                                          bool add) {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+  if (lane == 0) {
+    if (add)
+      asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                       reinterpret_cast<uint64_t>(map)),
+                   "r"(col), "r"(row), "r"(stage)
+                   : "memory");
+    else
+      asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                       reinterpret_cast<uint64_t>(map)),
+                   "r"(col), "r"(row), "r"(stage)
+                   : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+}
+
+// The addend of dX, and rows of dX that go to their tokens, are moved by the
+// lane that owns the row, in 32-byte sectors (rows that are only 16-byte aligned
+// in halves).
 struct Sector {
   uint32_t v[8];
 };
@@ -302,15 +334,17 @@ template <int KIND>
 __global__ void __launch_bounds__(THREADS, 1)
     linear_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                   const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmDt,
+                  const __grid_constant__ CUtensorMap tmOx, const __grid_constant__ CUtensorMap tmOw,
                   const Args a) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + RING_BYTES);
+  unsigned char* s_out = smem + RING_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_out + EPI_WARPS * STAGE_WARP);
   // bars: full[S] empty[S] tfull[2] tempty[2] final tfill[NSLOT] tdrain[NSLOT],
   // then the tile slots and the scalars
   static_assert(sizeof(Tile) == 32, "a slot is two 16-byte pieces");
-  unsigned char* s_slots = smem + RING_BYTES + BAR_BYTES - NSLOT * sizeof(Tile);
+  unsigned char* s_slots = reinterpret_cast<unsigned char*>(bars) + BAR_BYTES - NSLOT * sizeof(Tile);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5 + 2 * NSLOT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -496,6 +530,36 @@ __global__ void __launch_bounds__(THREADS, 1)
       commit2_self(final_bar);
       wait2_quiet(final_bar, 0);
     }
+  } else if (warp == 2) {
+    // ---------------- L2 prefetch of dX's addend ----------------
+    // a tile or two ahead of the epilogue, which otherwise waits a DRAM latency
+    // for every tile
+    const int esz = a.out_f32 ? 4 : 2;
+    for (int n = 0;; ++n) {
+      Tile t;
+      {
+        const int slot = n % NSLOT;
+        int w = 0;
+        if (lane == 0) w = wait_cl(tfill(slot), ((uint32_t)n / NSLOT) & 1u, abort_flag) ? 1 : 0;
+        if (!__shfl_sync(0xffffffffu, w, 0)) break;
+        t = load_slot(slot);
+        __syncwarp();
+        if (lane == 0) arrive_relaxed(map_to_rank(tdrain(slot), 0));
+      }
+      if (t.type < 0) break;
+      if (KIND == kGrad && t.type == 1 && a.dx_add != nullptr) {
+        const int n0 = t.nt * BN;
+        const uint32_t bytes = (uint32_t)min(BN, a.hidden - n0) * esz;   // hidden: a multiple of 8
+        for (int r = lane; r < BMC; r += 32) {
+          const int64_t row = (int64_t)t.mt * BM + (int64_t)rank * BMC + r;
+          if (row < plan.rows)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                             reinterpret_cast<const char*>(a.dx_add) + (row * a.hidden + n0) * esz),
+                         "r"(bytes)
+                         : "memory");
+        }
+      }
+    }
   }
   } else {
     // ---------------- epilogue (warps 4..11, both CTAs) ----------------
@@ -503,6 +567,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int q = warp & 3;                 // TMEM lanes 32q .. 32q+31
     const int half = (warp - 4) / 4;        // columns 128 half ..
     const int c_lo = half * (BN / 2);
+    const uint32_t stage = smem_u32(s_out + (warp - 4) * STAGE_WARP);
     int acc = 0;
     uint32_t aph = 0;
     for (int n = 0;; ++n) {
@@ -530,28 +595,24 @@ __global__ void __launch_bounds__(THREADS, 1)
       const bool is_dx = t.type == 1;
       const int n0 = t.nt * BN + c_lo;
       int nvalid = 0;
-      float* fout = nullptr;   // this lane's row of the output: fp32, or bf16
-      bf16* hout = nullptr;
+      bf16* hout = nullptr;    // rows of dX that go to their tokens: this lane's
+      float* fout = nullptr;
       bool wide = true;        // its sectors are aligned
       if (KIND == kGrad) {
         const int64_t nv = (is_dx ? plan.rows : min(a.vcols, a.vocab - a.v0)) - row0;
         nvalid = nv <= 0 ? 0 : (nv >= 32 ? 32 : (int)nv);
-        float* part = is_dx ? a.dx_part : a.dw_part;
-        int64_t orow = is_dx ? row : a.v0 + row;
-        if (is_dx && a.rowmap) orow = lane < nvalid ? a.rowmap[row] : 0;
         const float* fadd = nullptr;
         const bf16* hadd = nullptr;
-        if (part != nullptr) {
-          fout = part + ((int64_t)t.sp * (is_dx ? a.rows_pad : a.dw_pad) + row) * a.hidden + n0;
-          if (is_dx && a.accumulate) fadd = fout;
-        } else if (a.out_f32) {
-          fout = reinterpret_cast<float*>(is_dx ? a.dx : a.dw) + orow * a.hidden + n0;
-          if (is_dx && a.dx_add) fadd = reinterpret_cast<const float*>(a.dx_add) + orow * a.hidden + n0;
-          wide = is_dx ? a.wide_dx : a.wide_dw;
-        } else {
-          hout = reinterpret_cast<bf16*>(is_dx ? a.dx : a.dw) + orow * a.hidden + n0;
-          if (is_dx && a.dx_add) hadd = reinterpret_cast<const bf16*>(a.dx_add) + orow * a.hidden + n0;
-          wide = is_dx ? a.wide_dx : a.wide_dw;
+        if (is_dx && a.dx_part == nullptr) {
+          wide = a.wide_dx;
+          if (a.rowmap) {
+            const int64_t orow = lane < nvalid ? a.rowmap[row] : 0;
+            if (a.out_f32) fout = reinterpret_cast<float*>(a.dx) + orow * a.hidden + n0;
+            else hout = reinterpret_cast<bf16*>(a.dx) + orow * a.hidden + n0;
+          } else if (a.dx_add) {
+            if (a.out_f32) fadd = reinterpret_cast<const float*>(a.dx_add) + row * a.hidden + n0;
+            else hadd = reinterpret_cast<const bf16*>(a.dx_add) + row * a.hidden + n0;
+          }
         }
         // (all loads before the first use: one latency a tile; hidden is a
         // multiple of 8)
@@ -644,7 +705,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int64_t dt = live ? (int64_t)a.target[row] - col0 : -1;
         const float l2 = live ? a.lse[row] * kLog2e : 0.0f;
         const float g = live ? a.g[row] : 0.0f;
-        bf16* drow = a.d + row * a.d_ld + (int64_t)t.nt * BN + c_lo;
 #pragma unroll
         for (int j = 0; j < BN / 2; ++j) f[j] = ex2(fmaf(f[j], kLog2e, -l2)) * g;
         if (dt >= 0 && dt < BN / 2) {
@@ -656,32 +716,60 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int j = 0; j < BN / 2; ++j) f[j] = live && j < left ? f[j] : 0.0f;
         }
 #pragma unroll
-        for (int c = 0; c < BN / 2; c += 16) {
+        for (int c = 0; c < BN / 2; c += 64) {
           for (int p = 0; p < a.planes; ++p) {
-            store_sector(drow + p * a.d_plane * a.d_ld + c, pack_bf16(f + c), true, true);
+            stage_free(lane);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) put_piece(stage, lane, j, pack16(f + c + 8 * j, (const bf16*)nullptr));
+            stage_out(&tmOx, stage, lane, t.nt * BN + c_lo + c, (int)(p * a.d_plane + row0), false);
             if (p + 1 < a.planes) {
               // what this plane leaves for the next one
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
+              for (int j = 0; j < 64; ++j) {
                 const float rest = f[c + j] - __bfloat162float(__float2bfloat16_rn(f[c + j]));
                 f[c + j] = isfinite(rest) ? rest : 0.0f;
               }
             }
           }
         }
-      } else if (lane < nvalid) {
+      } else if (nvalid > 0) {
+        const bool part = is_dx ? a.dx_part != nullptr : a.dw_part != nullptr;
+        const CUtensorMap* map = is_dx ? &tmOx : &tmOw;
         if (fout != nullptr) {
 #pragma unroll
           for (int c = 0; c < BN / 2; c += 8)
-            if (n0 + c < a.hidden) store_sector(fout + c, pack_f32(f + c), wide, true);
-        } else {
+            if (n0 + c < a.hidden && lane < nvalid) store_sector(fout + c, pack_f32(f + c), wide, true);
+        } else if (hout != nullptr) {
 #pragma unroll
           for (int c = 0; c < BN / 2; c += 16)
-            if (n0 + c < a.hidden)
+            if (n0 + c < a.hidden && lane < nvalid)
               store_sector(hout + c, pack_bf16(f + c), wide && n0 + c + 16 <= a.hidden, n0 + c + 16 <= a.hidden);
+        } else if (part || a.out_f32) {
+          const int orow = (int)((part ? (int64_t)t.sp * (is_dx ? a.rows_pad : a.dw_pad) : is_dx ? 0 : a.v0) + row0);
+#pragma unroll
+          for (int c = 0; c < BN / 2; c += 32)
+            if (n0 + c < a.hidden) {
+              stage_free(lane);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) put_piece(stage, lane, j, pack16(f + c + 4 * j, (const float*)nullptr));
+              stage_out(map, stage, lane, n0 + c, orow, part && is_dx && a.accumulate);
+            }
+        } else {
+          const int orow = (int)((is_dx ? 0 : a.v0) + row0);
+#pragma unroll
+          for (int c = 0; c < BN / 2; c += 64)
+            if (n0 + c < a.hidden) {
+              stage_free(lane);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) put_piece(stage, lane, j, pack16(f + c + 8 * j, (const bf16*)nullptr));
+              stage_out(map, stage, lane, n0 + c, orow, false);
+            }
         }
       }
     }
+    // the staging slices and what left them outlive the block's last tile
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
   }
 
   tc_fence_before();
@@ -790,6 +878,19 @@ static bool map_rows(CUtensorMap* m, const void* ptr, int64_t rows, int64_t widt
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Output boxes: 32 rows of 128 bytes (64 bf16 or 32 fp32 columns).
+static bool map_out(CUtensorMap* m, void* ptr, int64_t rows, int64_t width, bool f32) {
+  const int esz = f32 ? 4 : 2;
+  cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)width * esz};
+  cuuint32_t box[2] = {(cuuint32_t)(128 / esz), 32};
+  cuuint32_t es[2] = {1, 1};
+  return encode_fn() != nullptr &&
+         encode_fn()(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ptr, dims,
+                     strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 static std::atomic<int> g_clusters[64];
 
 // Clusters of two CTAs that run at once, and the kernels' shared-memory limit
@@ -829,7 +930,8 @@ static cudaError_t prepare_device(int* clusters) {
 
 template <int KIND>
 static cudaError_t launch(const CUtensorMap& mX, const CUtensorMap& mW, const CUtensorMap& mD,
-                          const CUtensorMap& mDt, const Args& t, int64_t tiles, cudaStream_t st) {
+                          const CUtensorMap& mDt, const CUtensorMap& mOx, const CUtensorMap& mOw, const Args& t,
+                          int64_t tiles, cudaStream_t st) {
   int mc = 0;
   cudaError_t e = prepare_device(&mc);
   if (e != cudaSuccess) return e;
@@ -849,7 +951,7 @@ static cudaError_t launch(const CUtensorMap& mX, const CUtensorMap& mW, const CU
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, linear_kernel<KIND>, mX, mW, mD, mDt, t);
+  e = cudaLaunchKernelEx(&cfg, linear_kernel<KIND>, mX, mW, mD, mDt, mOx, mOw, t);
   if (e != cudaSuccess) return e;
   count_launch();
   return cudaGetLastError();
@@ -917,8 +1019,10 @@ cudaError_t launch_linear_logits(const LogitsArgs& a, cudaStream_t st) {
   // value rounded to 2^-9)
   t.chunk = a.gradient && a.planes == 1 ? kChunkBf16 : kChunkExact;
   const int64_t tiles = ((a.rows_bound + BM - 1) / BM) * ((a.vcols + BN - 1) / BN);
-  return a.gradient ? launch<kDlogit>(mX, mW, mX, mX, t, tiles, st)
-                    : launch<kStats>(mX, mW, mX, mX, t, tiles, st);
+  if (!a.gradient) return launch<kStats>(mX, mW, mX, mX, mX, mX, t, tiles, st);
+  CUtensorMap mO;
+  if (!map_out(&mO, a.d, a.planes * a.rows_pad, a.d_ld, false)) return cudaErrorInvalidValue;
+  return launch<kDlogit>(mX, mW, mX, mX, mO, mO, t, tiles, st);
 }
 
 cudaError_t launch_linear_grad(const LinearGradArgs& a, cudaStream_t st) {
@@ -957,17 +1061,23 @@ cudaError_t launch_linear_grad(const LinearGradArgs& a, cudaStream_t st) {
   t.dw_part = a.dw_part;
   t.dw_pad = a.dw_pad;
   auto aligned32 = [](const void* p) { return ((uintptr_t)p & 31u) == 0; };
-  const bool rows32 = a.hidden * (a.out_f32 ? 4 : 2) % 32 == 0;
-  t.wide_dx = rows32 && aligned32(a.dx) && aligned32(a.dx_add);
-  t.wide_dw = rows32 && aligned32(a.dw);
+  t.wide_dx = a.hidden * (a.out_f32 ? 4 : 2) % 32 == 0 && aligned32(a.dx) && aligned32(a.dx_add);
   t.want_dx = a.dx_part != nullptr || a.dx != nullptr;
   t.want_dw = a.dw_part != nullptr || a.dw != nullptr;
+  if (a.rowmap && a.dx_add) return cudaErrorInvalidValue;
   if ((t.want_dx && t.ks_dx > 1 && !a.dx_part) || (t.want_dw && t.ks_dw > 1 && !a.dw_part))
     return cudaErrorInvalidValue;
   const int64_t nth = (a.hidden + BN - 1) / BN;
   const int64_t tiles = (t.want_dx ? ((a.rows_bound + BM - 1) / BM) * nth * t.ks_dx : 0) +
                         (t.want_dw ? ((a.vcols + BN - 1) / BN) * nth * t.ks_dw : 0);
-  return launch<kGrad>(mX, mW, mD, mDt, t, tiles, st);
+  CUtensorMap mOx = mX, mOw = mX;   // not used where nothing is stored by box
+  if (t.want_dx && (a.dx_part ? !map_out(&mOx, a.dx_part, a.split.dx * a.rows_pad, a.hidden, true)
+                              : !map_out(&mOx, a.dx, a.rows_bound > 0 ? a.rows_bound : 1, a.hidden, a.out_f32)))
+    return cudaErrorInvalidValue;
+  if (t.want_dw && (a.dw_part ? !map_out(&mOw, a.dw_part, a.split.dw * a.dw_pad, a.hidden, true)
+                              : !map_out(&mOw, a.dw, a.vocab, a.hidden, a.out_f32)))
+    return cudaErrorInvalidValue;
+  return launch<kGrad>(mX, mW, mD, mDt, mOx, mOw, t, tiles, st);
 }
 
 cudaError_t launch_reduce_parts(const float* part, int splits, int64_t part_stride, int64_t rows,

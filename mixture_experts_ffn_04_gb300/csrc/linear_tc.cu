@@ -15,9 +15,9 @@
 // it groups of kGroupM row tiles pass over the column tiles, so the rows of a
 // group stay in L2 while the other operand streams by once per group.
 //
-// The gradient launch puts the dX tiles (few, long K) before the dW tiles
-// (many, short K): the short ones fill the SMs that the long ones leave idle at
-// their end.  Where tiles are few and long, K is split and the fp32 partial
+// The gradient launch puts the tiles with the longer K first (dX, K = vocabulary,
+// unless the rows are more): the short ones run beside them and fill the SMs that
+// the long ones leave idle at their end.  Where tiles are few and long, K is split and the fp32 partial
 // sums are added in split order by a second kernel (no atomics: the result does
 // not depend on the order of the tiles).
 //
@@ -190,7 +190,8 @@ __device__ __forceinline__ void order_tile(uint32_t t, uint32_t MT, uint32_t NT,
 template <int KIND>
 struct Plan {
   int MTr, NTh, NTv, KBv, KBr;
-  uint32_t n_dx, total;   // tiles (the launcher bounds them by 2^31)
+  uint32_t n_dx, n_dw, total;   // tiles (the launcher bounds them by 2^31)
+  bool dw_first;                // the longer parts come first
   int64_t rows;
   __device__ __forceinline__ void init(const Args& a) {
     rows = a.nrows ? (int64_t)*a.nrows : a.rows_bound;
@@ -204,7 +205,9 @@ struct Plan {
     n_dx = 0;
     if (KIND == kGrad) {
       n_dx = a.want_dx ? (uint32_t)MTr * NTh * a.ks_dx : 0u;
-      total = n_dx + (a.want_dw ? (uint32_t)NTv * NTh * a.ks_dw : 0u);
+      n_dw = a.want_dw ? (uint32_t)NTv * NTh * a.ks_dw : 0u;
+      total = n_dx + n_dw;
+      dw_first = KBr / a.ks_dw > KBv / a.ks_dx;
     } else {
       total = (uint32_t)MTr * NTv;
     }
@@ -219,8 +222,9 @@ struct Plan {
       r.kb1 = (a.hidden + BK - 1) / BK;
       return r;
     }
-    const bool dx = t < n_dx;
-    if (!dx) t -= n_dx;
+    const uint32_t lead = dw_first ? n_dw : n_dx;
+    const bool dx = (t < lead) != dw_first;
+    if (t >= lead) t -= lead;
     r.type = dx ? 1 : 2;
     const uint32_t ks = dx ? a.ks_dx : a.ks_dw, kb = dx ? KBv : KBr;
     if (ks > 1) {
@@ -379,6 +383,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
+  __syncwarp();
   __syncthreads();
   cluster_sync();   // barriers of both CTAs initialised before any remote arrive
   if (warp == 1) {
@@ -772,8 +777,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
   }
 
+  __syncwarp();     // the barriers below are for whole warps: roles end lane by lane
   tc_fence_before();
   __syncthreads();
+  __syncwarp();
   cluster_sync();   // no MMA, TMEM load or remote arrive of the pair in flight
   if (warp == 1) {
     tc_fence_after();
@@ -971,13 +978,16 @@ int linear_clusters() {
 }
 
 LinearSplit linear_grad_split(int64_t rows, int64_t vocab, int hidden, int planes) {
-  // Tiles long against a pair's share of the work leave SMs idle at the end:
-  // split K until a part is at most a third of that share (at least 8 k-blocks
-  // a part, at most 16 parts, whose fp32 sums the reduction reads back).
+  // A part longer than a pair's share of the work would leave the other SMs idle
+  // at the end: split K until it is at most nine tenths of that share (at least 8
+  // k-blocks a part, at most 16 parts, whose fp32 sums the reduction reads back).
+  // Not shorter: the long parts start first and run beside the short tiles, so
+  // that the reads of one kind overlap the writes of the other (HBM takes 4.1
+  // TB/s of writes alone, 6.8 of both).
   const int64_t nth = (hidden + 255) / 256, mtr = (rows + 255) / 256, ntv = (vocab + 255) / 256;
   const int64_t kbv = (vocab + 63) / 64, kbr = (rows + 63) / 64;
   const int64_t total = mtr * nth * kbv + ntv * nth * kbr;
-  int64_t part = total / (76 * 3);
+  int64_t part = total * 9 / (76 * 10);
   if (part < 8) part = 8;
   auto splits = [&](int64_t kb) {
     int64_t s = (kb + part - 1) / part;

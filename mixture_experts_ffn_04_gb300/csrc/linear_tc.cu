@@ -29,9 +29,10 @@
 // the loss and all fp32 products, 4096 for gradients that are
 // rounded to bf16 anyway.
 //
-// fp32 operands are three bf16 planes each; a tile's k-loop then runs over the
-// six plane products whose weight is above 2^-24, smallest first, into the same
-// fp32 accumulator.
+// fp32 operands come in planes (train.h).  Three bf16 planes: a tile's k-loop runs
+// over the six plane products whose weight is above 2^-24, smallest first.  Two
+// fp16 planes: the two cross products first, then, after their sum in the
+// registers is scaled by 2^-11, the product of the high planes; half the MMAs.
 //
 // Roles in each CTA: warp 0 TMA producer, warp 1 TMEM and (even CTA) the MMA
 // issuer, warps 4-11 epilogue: two per 32-lane TMEM quarter, one per half of
@@ -81,15 +82,17 @@ static_assert((2 * S + 5 + 2 * NSLOT) * 8 + 8 + NSLOT * 32 <= BAR_BYTES, "barrie
 constexpr int kGroupM = 8;
 constexpr int kChunkExact = 8, kChunkBf16 = 64;   // k-blocks of 64
 
-// kind::f16: D fp32, A and B bf16, M = 256 over the pair, N = 256.
-constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) |
-                           ((uint32_t)(BM >> 4) << 24);
+// kind::f16: D fp32, A and B fp16 (IDESC_BF16: both bf16), M = 256 over the pair,
+// N = 256.
+constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+constexpr uint32_t IDESC_BF16 = (1u << 7) | (1u << 10);
 constexpr uint32_t IDESC_A_MN = 1u << 15, IDESC_B_MN = 1u << 16;
 
 enum Kind { kStats = 0, kDlogit = 1, kGrad = 2 };
 
 struct Args {
   int hidden, planes;
+  const float* scale;
   int64_t v0, w_v0, vcols, vocab;
   const int32_t* nrows;
   int64_t rows_bound;
@@ -161,9 +164,11 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t saddr) {
   return d;
 }
 
-// Plane products in ascending weight: (0,2) (2,0) (1,1) (0,1) (1,0) (0,0).
+// Plane products in ascending weight: (0,2) (2,0) (1,1) (0,1) (1,0) (0,0); of two
+// planes the last three.
 __device__ __forceinline__ void plane_pair(int planes, int i, int& pa, int& pb) {
   if (planes == 1) { pa = pb = 0; return; }
+  if (planes == 2) i += 3;
   const int t = i == 0 ? 0x02 : i == 1 ? 0x20 : i == 2 ? 0x11 : i == 3 ? 0x01 : i == 4 ? 0x10 : 0x00;
   pa = t >> 4;
   pb = t & 15;
@@ -397,7 +402,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   pdl_wait();   // barriers, TMEM and descriptors are set up under the kernel before
   Plan<KIND> plan;
   plan.init(a);
-  const int nprod = a.planes == 1 ? 1 : 6;
+  const int nprod = a.planes == 1 ? 1 : a.planes == kPlanesHalf ? 3 : 6;
+  // steps of the fp16 cross products, which are summed and scaled by themselves
+  const int ncross = a.planes == kPlanesHalf ? 2 : 0;
 
   // Tile n of this pair (type -1 when there is none left, or a wait ran out).
   // The even CTA's producer takes it, one ahead, from the counter, decodes it and
@@ -506,9 +513,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       const Tile t = read_tile(n);
       if (t.type < 0) break;
       const int steps = (t.kb1 - t.kb0) * nprod;   // 0 without rows: the epilogue writes zeros
-      const uint32_t idesc = IDESC | (t.type == 2 ? IDESC_A_MN : 0u) | (t.type != 0 ? IDESC_B_MN : 0u);
-      for (int i0 = 0; i0 < steps && ok; i0 += a.chunk) {
-        const int i1 = min(steps, i0 + a.chunk);
+      const int cross = (t.kb1 - t.kb0) * ncross;
+      const uint32_t idesc = IDESC | (a.planes == kPlanesHalf ? 0u : IDESC_BF16) |
+                             (t.type == 2 ? IDESC_A_MN : 0u) | (t.type != 0 ? IDESC_B_MN : 0u);
+      for (int i0 = 0, i1; i0 < steps && ok; i0 = i1) {
+        i1 = min(i0 < cross ? cross : steps, i0 + a.chunk);
         if (!wait_cl(tempty(acc), aph ^ 1u, abort_flag)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d = tmem_base + (uint32_t)acc * BN;
@@ -646,8 +655,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
       bool ok = true;
+      const int cross = (t.kb1 - t.kb0) * ncross;
 #pragma unroll 1
-      for (int i0 = 0; i0 < steps; i0 += a.chunk) {
+      for (int i0 = 0, i1; i0 < steps; i0 = i1) {
+        i1 = min(i0 < cross ? cross : steps, i0 + a.chunk);
+        if (i0 == cross && cross > 0) {
+#pragma unroll
+          for (int j = 0; j < BN / 2; ++j) f[j] *= 1.0f / kHalfLow;
+        }
         int w = 1;
         if (lane == 0) w = wait_cl(tfull(acc), aph, abort_flag) ? 1 : 0;
         ok = __shfl_sync(0xffffffffu, w, 0);
@@ -673,6 +688,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (acc == 0) aph ^= 1u;
       }
       if (!ok) break;
+      if (a.planes == kPlanesHalf) {
+        // the operands' scales, powers of two (two factors: their product may
+        // leave the range)
+        const float r0 = pow2_recip(a.scale[is_dx || KIND != kGrad ? 1 : 0]);
+        const float r1 = pow2_recip(a.scale[KIND != kGrad ? 0 : 2]);
+#pragma unroll
+        for (int j = 0; j < BN / 2; ++j) f[j] = f[j] * r0 * r1;
+      }
       if (KIND == kStats) {
         // maximum and sum of the row over this half of the tile, in log2 units:
         // the maximum kept is the rounded z * log2(e), so the sum's scale and
@@ -720,21 +743,30 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int j = 0; j < BN / 2; ++j) f[j] = live && j < left ? f[j] : 0.0f;
         }
+        if (a.planes == 1) {
 #pragma unroll
-        for (int c = 0; c < BN / 2; c += 64) {
-          for (int p = 0; p < a.planes; ++p) {
+          for (int c = 0; c < BN / 2; c += 64) {
             stage_free(lane);
 #pragma unroll
             for (int j = 0; j < 8; ++j) put_piece(stage, lane, j, pack16(f + c + 8 * j, (const bf16*)nullptr));
-            stage_out(&tmOx, stage, lane, t.nt * BN + c_lo + c, (int)(p * a.d_plane + row0), false);
-            if (p + 1 < a.planes) {
-              // what this plane leaves for the next one
+            stage_out(&tmOx, stage, lane, t.nt * BN + c_lo + c, (int)row0, false);
+          }
+        } else {
+          const float sd = a.scale[2];
 #pragma unroll
-              for (int j = 0; j < 64; ++j) {
-                const float rest = f[c + j] - __bfloat162float(__float2bfloat16_rn(f[c + j]));
-                f[c + j] = isfinite(rest) ? rest : 0.0f;
-              }
-            }
+          for (int c = 0; c < BN / 2; c += 64) {
+#pragma unroll
+            for (int j = 0; j < 64; ++j) f[c + j] *= sd;
+            stage_free(lane);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) put_piece(stage, lane, j, pack_half8(f + c + 8 * j));
+            stage_out(&tmOx, stage, lane, t.nt * BN + c_lo + c, (int)row0, false);
+#pragma unroll
+            for (int j = 0; j < 64; ++j) f[c + j] = half_rest(f[c + j]);
+            stage_free(lane);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) put_piece(stage, lane, j, pack_half8(f + c + 8 * j));
+            stage_out(&tmOx, stage, lane, t.nt * BN + c_lo + c, (int)(a.d_plane + row0), false);
           }
         }
       } else if (nvalid > 0) {
@@ -866,6 +898,35 @@ __global__ void __launch_bounds__(256) planes_kernel(const float* __restrict__ s
 #pragma unroll
     for (int p = 0; p < 3; ++p)
       *reinterpret_cast<uint4*>(dst + (p * plane + r) * hidden + j0) = pack16(f[p], (const bf16*)nullptr);
+  }
+}
+
+__global__ void __launch_bounds__(256) halves_kernel(const float* __restrict__ src, int64_t ld,
+                                                     int64_t rows, int64_t rows_zero, int hidden,
+                                                     uint16_t* __restrict__ dst, int64_t plane,
+                                                     const uint32_t* __restrict__ max) {
+  pdl_trigger();
+  pdl_wait();
+  const float s = pow2_scale(*max);
+  const int per_row = hidden / 8;
+  const int64_t items = rows_zero * per_row;
+  for (int64_t it = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; it < items;
+       it += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t r = it / per_row;
+    const int j0 = (int)(it - r * per_row) * 8;
+    float f[8], l[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = 0.0f;
+    if (r < rows) {
+      const float4 u = __ldcs(reinterpret_cast<const float4*>(src + r * ld + j0));
+      const float4 v = __ldcs(reinterpret_cast<const float4*>(src + r * ld + j0 + 4));
+      f[0] = u.x * s; f[1] = u.y * s; f[2] = u.z * s; f[3] = u.w * s;
+      f[4] = v.x * s; f[5] = v.y * s; f[6] = v.z * s; f[7] = v.w * s;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) l[e] = half_rest(f[e]);
+    *reinterpret_cast<uint4*>(dst + r * hidden + j0) = pack_half8(f);
+    *reinterpret_cast<uint4*>(dst + (plane + r) * hidden + j0) = pack_half8(l);
   }
 }
 
@@ -1006,6 +1067,7 @@ cudaError_t launch_linear_logits(const LogitsArgs& a, cudaStream_t st) {
   Args t = {};
   t.hidden = a.hidden;
   t.planes = a.planes;
+  t.scale = a.scale;
   t.v0 = a.v0;
   t.w_v0 = a.w_v0;
   t.vcols = a.vcols;
@@ -1046,6 +1108,7 @@ cudaError_t launch_linear_grad(const LinearGradArgs& a, cudaStream_t st) {
   Args t = {};
   t.hidden = a.hidden;
   t.planes = a.planes;
+  t.scale = a.scale;
   t.v0 = a.v0;
   t.w_v0 = a.w_v0;
   t.vcols = a.vcols;
@@ -1074,7 +1137,7 @@ cudaError_t launch_linear_grad(const LinearGradArgs& a, cudaStream_t st) {
   t.wide_dx = a.hidden * (a.out_f32 ? 4 : 2) % 32 == 0 && aligned32(a.dx) && aligned32(a.dx_add);
   t.want_dx = a.dx_part != nullptr || a.dx != nullptr;
   t.want_dw = a.dw_part != nullptr || a.dw != nullptr;
-  if (a.rowmap && a.dx_add) return cudaErrorInvalidValue;
+  if (a.dx_add && (a.rowmap || a.planes == kPlanesHalf)) return cudaErrorInvalidValue;
   if ((t.want_dx && t.ks_dx > 1 && !a.dx_part) || (t.want_dw && t.ks_dw > 1 && !a.dw_part))
     return cudaErrorInvalidValue;
   const int64_t nth = (a.hidden + BN - 1) / BN;
@@ -1107,6 +1170,13 @@ cudaError_t launch_planes(const float* src, int64_t ld, int64_t rows, int64_t ro
   if (rows_zero <= 0) return cudaSuccess;
   return launch_after(lin::planes_kernel, lin::elementwise_grid(rows_zero * (hidden / 8)), 256, 0, st, 1, src, ld,
                       rows, rows_zero, hidden, reinterpret_cast<bf16*>(dst), plane);
+}
+
+cudaError_t launch_halves(const float* src, int64_t ld, int64_t rows, int64_t rows_zero, int hidden,
+                          void* dst, int64_t plane, const uint32_t* max, cudaStream_t st) {
+  if (rows_zero <= 0) return cudaSuccess;
+  return launch_after(lin::halves_kernel, lin::elementwise_grid(rows_zero * (hidden / 8)), 256, 0, st, 1, src, ld,
+                      rows, rows_zero, hidden, reinterpret_cast<uint16_t*>(dst), plane, max);
 }
 
 }  // namespace moe

@@ -3,6 +3,9 @@
 // small kernels around them.
 #pragma once
 
+#ifdef __CUDACC__
+#include <cuda_fp16.h>
+#endif
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -43,10 +46,43 @@ cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned block, si
 }
 #endif
 
-// fp32 operands go through the bf16 tensor cores as three bf16 planes
-// (x = x0 + x1 + x2, 8 mantissa bits each): planes of one operand are stacked
-// `plane` rows apart in one matrix.
-constexpr int kPlanesF32 = 3;
+// fp32 operands go through the 16-bit tensor cores in planes, stacked `plane`
+// rows apart in one matrix:
+//  * three bf16 planes, x = x0 + x1 + x2 (8 mantissa bits each), any range, six
+//    products;
+//  * two fp16 planes, x s = h + l 2^-11 with one power of two s for the matrix
+//    that brings its largest finite value to [2^14, 2^15): 22 mantissa bits down
+//    to 2^-29 of the largest, three products.
+constexpr int kPlanesF32 = 3, kPlanesHalf = 2;
+
+#ifdef __CUDACC__
+constexpr float kHalfLow = 2048.0f;   // scale of the low plane against the high one
+// The power of two for a largest absolute value, given as its bits (a value that
+// is not finite or zero: 1), and its reciprocal.
+__device__ __forceinline__ float pow2_scale(uint32_t bits) {
+  if (bits == 0u || bits >= 0x7F800000u) return 1.0f;
+  int s = 14 - ilogbf(__uint_as_float(bits));
+  s = s > 126 ? 126 : (s < -126 ? -126 : s);
+  return __uint_as_float((uint32_t)(s + 127) << 23);
+}
+__device__ __forceinline__ float pow2_recip(float s) {
+  return __uint_as_float((254u << 23) - __float_as_uint(s));
+}
+// What the high plane leaves for the low one (0 where it is not finite).
+__device__ __forceinline__ float half_rest(float v) {
+  const float r = (v - __half2float(__float2half_rn(v))) * kHalfLow;
+  return isfinite(r) ? r : 0.0f;
+}
+__device__ __forceinline__ uint4 pack_half8(const float* f) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+#endif
 
 // K or row tiles of the dense GEMMs: 256 x 256 output tiles, 64-wide k-blocks.
 constexpr int kLinTile = 256, kLinK = 64;
@@ -59,7 +95,8 @@ struct LinearSplit {
 LinearSplit linear_grad_split(int64_t rows, int64_t vocab, int hidden, int planes);
 
 struct LogitsArgs {
-  int planes;              // 1: bf16 operands, kPlanesF32: fp32 in bf16 planes
+  int planes;              // 1: bf16 operands, kPlanesHalf: fp32 in fp16 planes
+  const float* scale;      // kPlanesHalf: device, the scales of x, w and d
   const void* x;           // bf16 [planes * x_plane, x_ld], rows of `hidden`
   int64_t x_ld, x_plane;
   const void* w;           // bf16 [planes * w_plane, w_ld]
@@ -92,7 +129,8 @@ struct LogitsArgs {
 cudaError_t launch_linear_logits(const LogitsArgs& a, cudaStream_t st);
 
 struct LinearGradArgs {
-  int planes;
+  int planes;              // 1, kPlanesHalf or kPlanesF32
+  const float* scale;      // kPlanesHalf: device, the scales of x, w and d
   const void* d;           // bf16 [planes * d_plane, d_ld]: d [rows, vcols]
   int64_t d_ld, d_plane;
   const void* x;           // bf16 [planes * x_plane, x_ld]; rows past the count
@@ -134,6 +172,11 @@ cudaError_t launch_reduce_parts(const float* part, int splits, int64_t part_stri
 // rows past `rows` up to `rows_zero` are zeros.
 cudaError_t launch_planes(const float* src, int64_t ld, int64_t rows, int64_t rows_zero, int hidden,
                           void* dst, int64_t plane, cudaStream_t st);
+
+// The same as two fp16 planes; max: device, the bits of the matrix's largest
+// finite absolute value.
+cudaError_t launch_halves(const float* src, int64_t ld, int64_t rows, int64_t rows_zero, int hidden,
+                          void* dst, int64_t plane, const uint32_t* max, cudaStream_t st);
 
 int linear_clusters();   // clusters of two SMs the device runs at once
 

@@ -254,3 +254,34 @@ def test_outputs_on_16_byte_boundaries(dtype):
     assert torch.equal(vx, dx) and torch.equal(vw, dw)
     for b in (bx, bw):
         assert (b[:o] == 3).all() and (b[-o:] == 3).all()
+
+
+@pytest.mark.parametrize("a,b", [(1e-12, 1e12), (1e15, 1e-15), (2.0 ** -60, 2.0 ** 60)])
+def test_fp32_of_any_magnitude(a, b):
+    """The fp16 planes of fp32 inputs follow the matrices' own magnitudes."""
+    T, H, V = 150, 128, 500
+    x, w, t = make(T, H, V, torch.float32, ignored=0.2, seed=6)
+    check(x * a, w * b, t, torch.float32)
+    dl = torch.rand(T, device="cuda") * a
+    check(x, w, t, torch.float32, "none", dl)
+
+
+def test_fp32_rows_of_different_magnitude():
+    """Rows of x, rows of w and the tokens' weights over six decades each: every
+    row of dx and dw is as exact as its own magnitude allows (22 bits down to
+    2^-29 of the largest)."""
+    T, H, V = 120, 64, 300
+    x, w, t = make(T, H, V, torch.float32, seed=8)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    ten = lambda n: 10.0 ** (-6.0 * torch.rand(n, generator=g, device="cuda"))
+    x, w, dl = x * ten(T)[:, None], w * ten(V)[:, None], ten(T)
+    op, loss, dx, dw = check(x, w, t, torch.float32, "none", dl)
+    _, _, rdx, rdw, zb = reference(x, w, t, "none", dl, V)
+    tol = 2.0 ** -21 + 4 * zb + 16 * F
+    for got, want in ((dx, rdx), (dw, rdw)):
+        # a row's terms cancel (each token's weight is p - 1 at its target): the
+        # bound is on the row's own norm where it is not below its largest term
+        err = (got.double() - want).norm(dim=1)
+        size = want.norm(dim=1)
+        assert (err <= 16 * tol * torch.maximum(size, 2.0 ** -20 * size.max())).all()

@@ -563,14 +563,18 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (t.type < 0) break;
       if (KIND == kGrad && t.type == 1 && a.dx_add != nullptr) {
         const int n0 = t.nt * BN;
-        const uint32_t bytes = (uint32_t)min(BN, a.hidden - n0) * esz;   // hidden: a multiple of 8
+        // Line by line, not by cp.async.bulk.prefetch.L2: with that, one row an
+        // instruction, this warp of one block once in some hundred launches did not
+        // come back from it, and the launch never ended (found by progress counters
+        // in host memory; 380,000 launches of this form ran through).
+        const int lines = (min(BN, a.hidden - n0) * esz + 127) / 128;
         for (int r = lane; r < BMC; r += 32) {
           const int64_t row = (int64_t)t.mt * BM + (int64_t)rank * BMC + r;
-          if (row < plan.rows)
-            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
-                             reinterpret_cast<const char*>(a.dx_add) + (row * a.hidden + n0) * esz),
-                         "r"(bytes)
-                         : "memory");
+          if (row < plan.rows) {
+            const char* p = reinterpret_cast<const char*>(a.dx_add) + (row * a.hidden + n0) * esz;
+            for (int l = 0; l < lines; ++l)
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(p + l * 128) : "memory");
+          }
         }
       }
     }

@@ -3,7 +3,8 @@
 // logit gradient in the epilogue, and the two gradient products
 //   dX = D W   (D [rows, V], W [V, H])      K = vocabulary
 //   dW = D^T x (D [rows, V], x [rows, H])   K = rows
-// in one launch over one tile list.
+// in one launch over one tile list; and the plain product x W^T in fp32 (a
+// router's logits).
 //
 // A pair of SMs computes 256 x 256 output tiles over 64-wide k-blocks: CTA r
 // keeps rows 128r .. of the A tile and columns 128r .. of the B tile, six
@@ -88,7 +89,7 @@ constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)
 constexpr uint32_t IDESC_BF16 = (1u << 7) | (1u << 10);
 constexpr uint32_t IDESC_A_MN = 1u << 15, IDESC_B_MN = 1u << 16;
 
-enum Kind { kStats = 0, kDlogit = 1, kGrad = 2 };
+enum Kind { kStats = 0, kDlogit = 1, kGrad = 2, kProduct = 3 };
 
 struct Args {
   int hidden, planes;
@@ -168,7 +169,8 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t saddr) {
 // planes the last three.
 __device__ __forceinline__ void plane_pair(int planes, int i, int& pa, int& pb) {
   if (planes == 1) { pa = pb = 0; return; }
-  if (planes == 2) i += 3;
+  if (planes == kPlanesD2) { pa = 1 - i; pb = 0; return; }
+  if (planes == kPlanesHalf) i += 3;
   const int t = i == 0 ? 0x02 : i == 1 ? 0x20 : i == 2 ? 0x11 : i == 3 ? 0x01 : i == 4 ? 0x10 : 0x00;
   pa = t >> 4;
   pb = t & 15;
@@ -214,7 +216,7 @@ struct Plan {
       total = n_dx + n_dw;
       dw_first = KBr / a.ks_dw > KBv / a.ks_dx;
     } else {
-      total = (uint32_t)MTr * NTv;
+      total = (uint32_t)MTr * NTv * (KIND == kProduct ? a.ks_dx : 1);
     }
   }
   __device__ __forceinline__ Tile decode(const Args& a, uint32_t t) const {
@@ -222,9 +224,13 @@ struct Plan {
     r.sp = 0;
     if (KIND != kGrad) {
       r.type = 0;
+      const uint32_t kb = (a.hidden + BK - 1) / BK, ks = KIND == kProduct ? a.ks_dx : 1;
+      if (ks > 1) {
+        r.sp = (int)(t % ks);
+        t /= ks;
+      }
       order_tile(t, MTr, NTv, r.mt, r.nt);
-      r.kb0 = 0;
-      r.kb1 = (a.hidden + BK - 1) / BK;
+      part_range(kb, ks, r);
       return r;
     }
     const uint32_t lead = dw_first ? n_dw : n_dx;
@@ -237,11 +243,14 @@ struct Plan {
       t /= ks;
     }
     order_tile(t, dx ? MTr : NTv, NTh, r.mt, r.nt);
-    // the first kb % ks parts take one k-block more
+    part_range(kb, ks, r);
+    return r;
+  }
+  // the first kb % ks parts take one k-block more
+  static __device__ __forceinline__ void part_range(uint32_t kb, uint32_t ks, Tile& r) {
     const uint32_t each = kb / ks, more = kb % ks;
     r.kb0 = (int)(r.sp * each + min((uint32_t)r.sp, more));
     r.kb1 = r.kb0 + (int)(each + ((uint32_t)r.sp < more ? 1u : 0u));
-    return r;
   }
 };
 
@@ -402,7 +411,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   pdl_wait();   // barriers, TMEM and descriptors are set up under the kernel before
   Plan<KIND> plan;
   plan.init(a);
-  const int nprod = a.planes == 1 ? 1 : a.planes == kPlanesHalf ? 3 : 6;
+  const int nprod = a.planes == 1 ? 1 : a.planes == kPlanesD2 ? 2 : a.planes == kPlanesHalf ? 3 : 6;
   // steps of the fp16 cross products, which are summed and scaled by themselves
   const int ncross = a.planes == kPlanesHalf ? 2 : 0;
 
@@ -479,7 +488,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           const uint32_t fb = map_to_rank(full(s), 0);
           if (leader) mbar_expect_tx(full(s), 2 * STAGE_BYTES);
           const int k = kb * BK;
-          if (KIND != kGrad) {
+          if (KIND != kGrad) {   // (kProduct: one plane)
             tma_load_2d_pair(sa, &tmX, k, (int)(pa * a.x_plane) + arow, fb);
             tma_load_2d_pair(sb, &tmW, k, (int)(pb * a.w_plane + a.w_v0) + bcol, fb);
           } else if (t.type == 1) {
@@ -773,6 +782,16 @@ __global__ void __launch_bounds__(THREADS, 1)
             stage_out(&tmOx, stage, lane, t.nt * BN + c_lo + c, (int)(a.d_plane + row0), false);
           }
         }
+      } else if (KIND == kProduct) {
+        const int orow = (int)((int64_t)t.sp * a.rows_pad + row0);
+#pragma unroll
+        for (int c = 0; c < BN / 2; c += 32)
+          if (n0 + c < a.vcols && row0 < plan.rows) {
+            stage_free(lane);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) put_piece(stage, lane, j, pack16(f + c + 4 * j, (const float*)nullptr));
+            stage_out(&tmOx, stage, lane, n0 + c, orow, false);
+          }
       } else if (nvalid > 0) {
         const bool part = is_dx ? a.dx_part != nullptr : a.dw_part != nullptr;
         const CUtensorMap* map = is_dx ? &tmOx : &tmOw;
@@ -973,8 +992,8 @@ static cudaError_t prepare_device(int* clusters) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (g_clusters[dev] == 0) {
-    const void* fn[3] = {(const void*)linear_kernel<kStats>, (const void*)linear_kernel<kDlogit>,
-                         (const void*)linear_kernel<kGrad>};
+    const void* fn[4] = {(const void*)linear_kernel<kStats>, (const void*)linear_kernel<kDlogit>,
+                         (const void*)linear_kernel<kGrad>, (const void*)linear_kernel<kProduct>};
     int least = 1 << 30;
     for (const void* f : fn) {
       e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
@@ -1101,12 +1120,43 @@ cudaError_t launch_linear_logits(const LogitsArgs& a, cudaStream_t st) {
   return launch<kDlogit>(mX, mW, mX, mX, mO, mO, t, tiles, st);
 }
 
+int linear_product_split(int64_t rows, int64_t cols, int hidden) {
+  // few tiles: as many parts of K as the 76 pairs of SMs take in one round, at
+  // least 4 k-blocks each, at most 8 (the reader adds them up)
+  const int64_t tiles = ((rows + 255) / 256) * ((cols + 255) / 256), kb = (hidden + 63) / 64;
+  int64_t s = tiles > 0 ? 76 / tiles : 1;
+  s = s < kb / 4 ? s : kb / 4;
+  return (int)(s < 1 ? 1 : (s > 8 ? 8 : s));
+}
+
+cudaError_t launch_linear_product(const ProductArgs& a, cudaStream_t st) {
+  using namespace lin;
+  CUtensorMap mX, mW, mO;
+  if (!map_rows(&mX, a.x, a.rows, a.hidden, a.x_ld, BMC) || !map_rows(&mW, a.w, a.cols, a.hidden, a.w_ld, BNC) ||
+      !map_out(&mO, a.part, a.split * a.rows_pad, a.ld, true))
+    return cudaErrorInvalidValue;
+  Args t = {};
+  t.hidden = a.hidden;
+  t.planes = 1;
+  t.vcols = a.ld;
+  t.vocab = a.cols;
+  t.rows_bound = a.rows;
+  t.ctr = a.ctr;
+  t.flags = a.flags;
+  t.rows_pad = a.rows_pad;
+  t.ks_dx = a.split;
+  t.chunk = kChunkExact;
+  const int64_t tiles = ((a.rows + BM - 1) / BM) * ((a.ld + BN - 1) / BN) * a.split;
+  return launch<kProduct>(mX, mW, mX, mX, mO, mO, t, tiles, st);
+}
+
 cudaError_t launch_linear_grad(const LinearGradArgs& a, cudaStream_t st) {
   using namespace lin;
   CUtensorMap mX, mW, mD, mDt;
-  const int64_t drows = a.planes * a.d_plane;
-  if (!map_rows(&mX, a.x, (a.planes - 1) * a.x_plane + a.x_rows, a.hidden, a.x_ld, BK) ||
-      !map_rows(&mW, a.w, (a.planes - 1) * a.w_plane + a.w_rows, a.hidden, a.w_ld, BK) ||
+  const int64_t drows = (a.planes == kPlanesD2 ? 2 : a.planes) * a.d_plane;
+  const int64_t more = a.planes == kPlanesD2 ? 0 : a.planes - 1;   // planes of x and w after the first
+  if (!map_rows(&mX, a.x, more * a.x_plane + a.x_rows, a.hidden, a.x_ld, BK) ||
+      !map_rows(&mW, a.w, more * a.w_plane + a.w_rows, a.hidden, a.w_ld, BK) ||
       !map_rows(&mD, a.d, drows, a.d_ld, a.d_ld, BMC) || !map_rows(&mDt, a.d, drows, a.d_ld, a.d_ld, BK))
     return cudaErrorInvalidValue;
   Args t = {};

@@ -1,16 +1,20 @@
 // router_bwd.cu -- gradient of the top-k softmax router with its load-balance
 // and z losses (include/moe_train.h).
 //
-// The logits come from the forward's router GEMM again (2 T H E flops, against
-// the 4 T H E of the two gradient products).  One warp a token then turns them
-// into the gradient of the logits:
+// The logits are computed again (2 T H E flops, against the 4 T H E of the two
+// gradient products): bf16 on the pairs of SMs, summed in chunks of K (the
+// truncation of one long tensor-core sum shows in the z loss), fp32 by the
+// forward's router GEMM.  One warp a token then turns them into the gradient of
+// the logits:
 //   dz_te = [norm]  sum_s [idx_s = e] w_s (D_s - dot)        w: softmax over the k
 //           [full]  sum_s [idx_s = e] w_s D_s - p_te dot     w_s = p at idx_s
 //           + p_te (cb (n_e - sum_j n_j p_tj) + 2 c_z / T lse_t)
 // with dot = sum_s w_s D_s, D = d_topk_w, cb = balance_coef E / (T^2 k), and the
-// gate column d_gate s (1 - s).  All of it in fp32; dz is rounded to bf16 (fp32
-// layers: three bf16 planes) as the operand of the gradient products, which run
-// as one launch on the tensor cores: dx = dz W_r (+ dx_add) and dW_r = dz^T x.
+// gate column d_gate s (1 - s).  All of it in fp32.  dz goes into the gradient
+// products dx = dz W_r (+ dx_add) and dW_r = dz^T x, one launch on the tensor
+// cores, as two bf16 planes (fp32 layers: three): one plane would add its rounding
+// to that of the results (dW_r 2.5e-3 off instead of 1.7e-3), and the MMAs are not
+// what bounds them.
 // What bounds it: HBM, x once for each product, dx_add and dx once.
 #include <algorithm>
 #include <cmath>
@@ -36,7 +40,7 @@ struct DzArgs {
   const float* d_gate;
   const int32_t* counts;
   float cb, cz2;       // balance_coef E / (T^2 k), 2 z_coef / T
-  int planes;
+  int planes;          // of dz
   bf16* dz;            // [planes][plane][ld]
   int64_t plane;
   int ld;
@@ -51,7 +55,7 @@ struct DzArgs {
 // cluster: each block counts its part in shared memory, then adds up its share of
 // the experts over the blocks.  Nothing has to be zero before.  One block takes
 // 18 us for 32768 slots (shared-memory atomics), eight 5.  meta: the ticket and
-// the tile counter, zeroed here.
+// the two tile counters, zeroed here.
 constexpr int kHistCluster = 8, kHistOneBlock = 4096;
 __global__ void __launch_bounds__(1024) route_hist_kernel(const int32_t* __restrict__ idx, int64_t n,
                                                           int E, int32_t* counts, int32_t* meta,
@@ -59,7 +63,7 @@ __global__ void __launch_bounds__(1024) route_hist_kernel(const int32_t* __restr
   extern __shared__ int32_t s_h[];
   pdl_trigger();
   pdl_wait();
-  if (blockIdx.x == 0 && threadIdx.x < 2) meta[threadIdx.x] = 0;
+  if (blockIdx.x == 0 && threadIdx.x < 3) meta[threadIdx.x] = 0;
   for (int e = threadIdx.x; e < E; e += blockDim.x) s_h[e] = 0;
   __syncthreads();
   for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n;
@@ -384,17 +388,19 @@ constexpr int kDzBlocks = 2048;
 struct RbLayout {
   Layout L;
   int64_t rows_pad, cols_pad;
-  int planes;
+  int planes, dz_planes, zsplit;
   LinearSplit split;
   bool dx_direct, dw_direct;
-  size_t meta, counts, part, dz, xpl, wpl, dx_part, dw_part, total;
+  size_t meta, counts, part, z, dz, xpl, wpl, dx_part, dw_part, total;
 };
 RbLayout layout_rb(const Shape& s) {
   RbLayout R;
   R.L = layout_for(s);
   R.rows_pad = std::max<int64_t>(256, (s.T + 255) / 256 * 256);
   R.cols_pad = ((int64_t)s.ncols + 63) / 64 * 64;
-  R.planes = s.dtype == MOE_F32 ? kPlanesF32 : 1;
+  R.planes = s.dtype == MOE_F32 ? kPlanesF32 : kPlanesD2;
+  R.dz_planes = s.dtype == MOE_F32 ? kPlanesF32 : 2;
+  R.zsplit = linear_product_split(s.T, R.cols_pad, s.H);
   R.split = linear_grad_split(s.T, R.cols_pad, s.H, R.planes);
   R.dx_direct = R.split.dx == 1;
   R.dw_direct = R.split.dw == 1;
@@ -404,12 +410,13 @@ RbLayout layout_rb(const Shape& s) {
     off += (bytes + 255) & ~(size_t)255;
     return at;
   };
-  R.meta = take(256);   // ticket, tile counter
+  R.meta = take(256);   // ticket, tile counters
   R.counts = take((size_t)s.E * 4);
   R.part = take((size_t)kDzBlocks * 16);
-  R.dz = take((size_t)R.planes * R.rows_pad * R.cols_pad * 2);
-  R.xpl = take(R.planes > 1 ? (size_t)R.planes * R.rows_pad * s.H * 2 : 0);
-  R.wpl = take(R.planes > 1 ? (size_t)R.planes * R.cols_pad * s.H * 2 : 0);
+  R.z = take(s.dtype == MOE_F32 ? 0 : (size_t)R.zsplit * R.rows_pad * R.cols_pad * 4);
+  R.dz = take((size_t)R.dz_planes * R.rows_pad * R.cols_pad * 2);
+  R.xpl = take(s.dtype == MOE_F32 ? (size_t)R.planes * R.rows_pad * s.H * 2 : 0);
+  R.wpl = take(s.dtype == MOE_F32 ? (size_t)R.planes * R.cols_pad * s.H * 2 : 0);
   R.dx_part = take(R.dx_direct ? 0 : (size_t)R.split.dx * R.rows_pad * s.H * 4);
   const size_t dw_rows = ((size_t)s.ncols + 255) / 256 * 256;
   R.dw_part = take(R.dw_direct ? 0 : (size_t)R.split.dw * dw_rows * s.H * 4);
@@ -464,14 +471,36 @@ extern "C" moe_status moe_router_backward(const moe_shape* shape, const void* x,
     CHECK_CUDA(cudaFuncSetAttribute(route_hist_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, s.E * 4));
   CHECK_CUDA(launch_after(route_hist_kernel, hb, 1024, (size_t)s.E * 4, st, hb, topk_idx, slots, s.E, counts,
                           meta, flags));
-  int nsplit = 1;
-  e = router_gemm(s, R.L, b, x, w_router, &nsplit, st);
-  if (e != MOE_OK) return e;
   DzArgs d = {};
-  d.logits = reinterpret_cast<const float*>(b + R.L.logits);
-  d.split_stride = s.T * (int64_t)s.ldl;
-  d.nsplit = nsplit;
-  d.ldl = s.ldl;
+  if (s.dtype == MOE_F32) {
+    int nsplit = 1;
+    e = router_gemm(s, R.L, b, x, w_router, &nsplit, st);
+    if (e != MOE_OK) return e;
+    d.logits = reinterpret_cast<const float*>(b + R.L.logits);
+    d.split_stride = s.T * (int64_t)s.ldl;
+    d.nsplit = nsplit;
+    d.ldl = s.ldl;
+  } else {
+    ProductArgs z = {};
+    z.x = x;
+    z.x_ld = s.H;
+    z.rows = s.T;
+    z.w = w_router;
+    z.w_ld = s.H;
+    z.cols = s.ncols;
+    z.hidden = s.H;
+    z.split = R.zsplit;
+    z.ctr = meta + 2;
+    z.flags = flags;
+    z.part = reinterpret_cast<float*>(b + R.z);
+    z.rows_pad = R.rows_pad;
+    z.ld = R.cols_pad;
+    CHECK_CUDA(launch_linear_product(z, st));
+    d.logits = z.part;
+    d.split_stride = R.rows_pad * R.cols_pad;
+    d.nsplit = R.zsplit;
+    d.ldl = (int)R.cols_pad;
+  }
   d.T = s.T;
   d.E = s.E;
   d.k = s.k;
@@ -485,7 +514,7 @@ extern "C" moe_status moe_router_backward(const moe_shape* shape, const void* x,
   const double cb = balance_coef * s.E / ((double)s.T * (double)s.T * s.k);
   d.cb = (float)cb;
   d.cz2 = (float)(2.0 * z_coef / (double)s.T);
-  d.planes = R.planes;
+  d.planes = R.dz_planes;
   d.dz = reinterpret_cast<bf16*>(b + R.dz);
   d.plane = R.rows_pad;
   d.ld = (int)R.cols_pad;
@@ -524,7 +553,7 @@ extern "C" moe_status moe_router_backward(const moe_shape* shape, const void* x,
   q.w = w_router;
   q.w_ld = s.H;
   q.w_rows = s.ncols;
-  if (R.planes > 1) {
+  if (s.dtype == MOE_F32) {
     CHECK_CUDA(launch_planes(static_cast<const float*>(x), s.H, s.T, d.rows, s.H, b + R.xpl, R.rows_pad, st));
     CHECK_CUDA(launch_planes(static_cast<const float*>(w_router), s.H, s.ncols, R.cols_pad, s.H, b + R.wpl,
                              R.cols_pad, st));

@@ -53,7 +53,9 @@ cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned block, si
 //  * two fp16 planes, x s = h + l 2^-11 with one power of two s for the matrix
 //    that brings its largest finite value to [2^14, 2^15): 22 mantissa bits down
 //    to 2^-29 of the largest, three products.
-constexpr int kPlanesF32 = 3, kPlanesHalf = 2;
+// bf16 gradients can keep D in two bf16 planes against one of x and w (two
+// products): D's rounding, half of the gradients' error, then vanishes.
+constexpr int kPlanesF32 = 3, kPlanesHalf = 2, kPlanesD2 = 4;
 
 #ifdef __CUDACC__
 constexpr float kHalfLow = 2048.0f;   // scale of the low plane against the high one
@@ -128,8 +130,24 @@ struct LogitsArgs {
 };
 cudaError_t launch_linear_logits(const LogitsArgs& a, cudaStream_t st);
 
+// z = x W^T of bf16 operands in fp32, K in `split` parts: part[s][rows_pad][ld] (ld a
+// multiple of 64), to be added in order.
+struct ProductArgs {
+  const void* x;           // bf16 [rows, x_ld]
+  int64_t x_ld, rows;
+  const void* w;           // bf16 [cols, w_ld]
+  int64_t w_ld, cols;
+  int hidden, split;
+  int32_t* ctr;            // zeroed tile counter
+  uint32_t* flags;
+  float* part;
+  int64_t rows_pad, ld;
+};
+int linear_product_split(int64_t rows, int64_t cols, int hidden);
+cudaError_t launch_linear_product(const ProductArgs& a, cudaStream_t st);
+
 struct LinearGradArgs {
-  int planes;              // 1, kPlanesHalf or kPlanesF32
+  int planes;              // 1, kPlanesD2, kPlanesHalf or kPlanesF32
   const float* scale;      // kPlanesHalf: device, the scales of x, w and d
   const void* d;           // bf16 [planes * d_plane, d_ld]: d [rows, vcols]
   int64_t d_ld, d_plane;

@@ -118,6 +118,7 @@ struct Args {
   float* dw_part;
   int64_t dw_pad;
   int want_dx, want_dw;
+  int wide_in;   // x and w in maps of 64-wide column blocks (hidden a multiple of 64)
   int wide_dx;   // rows of dx and dx_add on 32-byte boundaries
   int chunk;   // k-blocks the tensor cores add up before the fp32 registers do
 };
@@ -494,14 +495,21 @@ __global__ void __launch_bounds__(THREADS, 1)
           } else if (t.type == 1) {
             tma_load_2d_pair(sa, &tmD, k, (int)(pa * a.d_plane) + arow, fb);
             const int wr = (int)(pb * a.w_plane + a.w_v0) + k;
-            tma_load_2d_pair(sb, &tmW, bcol, wr, fb);
-            tma_load_2d_pair(sb + BOX_BYTES, &tmW, bcol + 64, wr, fb);
+            if (a.wide_in) {
+              tma_load_3d_pair(sb, &tmW, 0, wr, bcol / 64, fb);
+            } else {
+              tma_load_2d_pair(sb, &tmW, bcol, wr, fb);
+              tma_load_2d_pair(sb + BOX_BYTES, &tmW, bcol + 64, wr, fb);
+            }
           } else {
             const int dr = (int)(pa * a.d_plane) + k, xr = (int)(pb * a.x_plane) + k;
-            tma_load_2d_pair(sa, &tmDt, arow, dr, fb);
-            tma_load_2d_pair(sa + BOX_BYTES, &tmDt, arow + 64, dr, fb);
-            tma_load_2d_pair(sb, &tmX, bcol, xr, fb);
-            tma_load_2d_pair(sb + BOX_BYTES, &tmX, bcol + 64, xr, fb);
+            tma_load_3d_pair(sa, &tmDt, 0, dr, arow / 64, fb);
+            if (a.wide_in) {
+              tma_load_3d_pair(sb, &tmX, 0, xr, bcol / 64, fb);
+            } else {
+              tma_load_2d_pair(sb, &tmX, bcol, xr, fb);
+              tma_load_2d_pair(sb + BOX_BYTES, &tmX, bcol + 64, xr, fb);
+            }
           }
           issued |= 1u << s;
           par = (par & ~(1u << s)) | (ph << s);
@@ -969,6 +977,19 @@ static bool map_rows(CUtensorMap* m, const void* ptr, int64_t rows, int64_t widt
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same rows as {64, rows, width / 64}: one box of 64 rows brings two 64-wide
+// column blocks, as the MN-major operand wants them (width a multiple of 64).
+static bool map_blocks(CUtensorMap* m, const void* ptr, int64_t rows, int64_t width, int64_t ld) {
+  cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)(width / 64)};
+  cuuint64_t strides[2] = {(cuuint64_t)ld * 2, 128};
+  cuuint32_t box[3] = {64, BK, 2};
+  cuuint32_t es[3] = {1, 1, 1};
+  return encode_fn() != nullptr &&
+         encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, es,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Output boxes: 32 rows of 128 bytes (64 bf16 or 32 fp32 columns).
 static bool map_out(CUtensorMap* m, void* ptr, int64_t rows, int64_t width, bool f32) {
   const int esz = f32 ? 4 : 2;
@@ -1155,9 +1176,12 @@ cudaError_t launch_linear_grad(const LinearGradArgs& a, cudaStream_t st) {
   CUtensorMap mX, mW, mD, mDt;
   const int64_t drows = (a.planes == kPlanesD2 ? 2 : a.planes) * a.d_plane;
   const int64_t more = a.planes == kPlanesD2 ? 0 : a.planes - 1;   // planes of x and w after the first
-  if (!map_rows(&mX, a.x, more * a.x_plane + a.x_rows, a.hidden, a.x_ld, BK) ||
-      !map_rows(&mW, a.w, more * a.w_plane + a.w_rows, a.hidden, a.w_ld, BK) ||
-      !map_rows(&mD, a.d, drows, a.d_ld, a.d_ld, BMC) || !map_rows(&mDt, a.d, drows, a.d_ld, a.d_ld, BK))
+  const int64_t xrows = more * a.x_plane + a.x_rows, wrows = more * a.w_plane + a.w_rows;
+  const bool wide = a.hidden % 64 == 0;
+  if (a.d_ld % 64 || !map_rows(&mD, a.d, drows, a.d_ld, a.d_ld, BMC) || !map_blocks(&mDt, a.d, drows, a.d_ld, a.d_ld))
+    return cudaErrorInvalidValue;
+  if (wide ? !map_blocks(&mX, a.x, xrows, a.hidden, a.x_ld) || !map_blocks(&mW, a.w, wrows, a.hidden, a.w_ld)
+           : !map_rows(&mX, a.x, xrows, a.hidden, a.x_ld, BK) || !map_rows(&mW, a.w, wrows, a.hidden, a.w_ld, BK))
     return cudaErrorInvalidValue;
   Args t = {};
   t.hidden = a.hidden;
@@ -1177,6 +1201,7 @@ cudaError_t launch_linear_grad(const LinearGradArgs& a, cudaStream_t st) {
   t.rows_pad = a.rows_pad;
   t.ks_dx = a.split.dx;
   t.ks_dw = a.split.dw;
+  t.wide_in = wide;
   t.out_f32 = a.out_f32;
   t.chunk = a.out_f32 ? kChunkExact : kChunkBf16;
   t.dx_part = a.dx_part;

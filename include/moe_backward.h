@@ -29,7 +29,8 @@
  * sizes: the launch bound is the scattered row count T*k, never T, so a
  * group larger than T (duplicate routes) is never truncated.  The router, a
  * shared expert and the input RMSNorm are dense layers around this op: their
- * gradients are the caller's (d_topk_w is what a router's backward needs).
+ * gradients are the caller's (d_topk_w is what a router's backward needs:
+ * moe_router_backward in moe_train.h).
  *
  * Precision: bf16 operands, fp32 accumulation, each output rounded once to
  * the activation type (d_topk_w fp32); the fp32 layer runs in fp32 on the

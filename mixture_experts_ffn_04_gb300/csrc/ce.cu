@@ -12,6 +12,10 @@
 // the logits again with d in the epilogue (kept for the piece only), then both
 // gradient products in one launch.  8 T H V flops for loss and gradient, of
 // which 2 T H V recompute the logits.
+//
+// Measured (bf16): T = 4096, H = 2048, V = 131072 loss and gradient 5.5 ms, 1.6
+// PFLOP/s under the power cap (0.92 of the sustained matrix-product rate); of its
+// launches packing, merging and adding up dx take 60 us.
 #include <algorithm>
 
 #include "../../include/moe_train.h"
@@ -22,7 +26,10 @@
 namespace moe {
 namespace {
 
-constexpr int64_t kDlogitBytes = 256ll << 20;   // logit gradient of one piece
+// Logit gradient of one piece.  T = 4096, V = 131072 (loss and gradient): pieces of
+// 64 MiB 5768 us, 128 5613, 256 5525, 512 5478, all in one (1 GiB) 5446: each piece
+// costs a launch pair's tail, and larger ones only memory.
+constexpr int64_t kDlogitBytes = 512ll << 20;
 constexpr int64_t kPlaneBytes = 512ll << 20;    // fp16 planes of one piece of an fp32 W
 
 // the few-row forward: rows of x, warps a block, blocks an SM, shared memory of x
@@ -326,6 +333,7 @@ __global__ void __launch_bounds__(256) ce_max_kernel(const float* __restrict__ x
 // Merge the row statistics of all half tiles (lanes: 32 rows, warps: slices of
 // the half tiles): M = max m, S = sum s 2^(m - M), lse = ln 2 (M + log2 S).  The
 // last block adds the rows' losses, in row order, in fp64.
+// (T = 4096, V = 131072: 34 MB of statistics in 20 us, bound by their latency.)
 constexpr int kMergeWarps = 32;
 __global__ void __launch_bounds__(32 * kMergeWarps)
     ce_merge_kernel(const float2* __restrict__ stats, int64_t rows_pad, int parts,
@@ -394,7 +402,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
 // vocabulary rows at a time (all lanes across the row, 16 bytes a load) against
 // the rows of x in shared memory (fp32), keeps a running maximum and sum per row
 // of x, and the last block merges the blocks.  Bound by HBM: one token against
-// 50257 x 2048 bf16 reads 206 MB.
+// 50257 x 2048 bf16 reads 206 MB in 38 us, 5.4 TB/s (0.80 of the copy); with two
+// blocks an SM instead of four it took 63 (too few loads in flight).
 struct SkinnyArgs {
   const void *x, *w;
   int64_t x_ld, w_ld;
@@ -552,14 +561,21 @@ cudaError_t launch_skinny(const SkinnyArgs& a, cudaStream_t st) {
     return launch_after(kernel, (unsigned)blocks, 32 * kSkinnyWarps, smem, st, 1, a);
   };
   if (rows == 1) return go(ce_skinny_kernel<T, 1, 2>, 2);
-  if (rows == 2) return go(ce_skinny_kernel<T, 2, 2>, 2);
-  return go(ce_skinny_kernel<T, 4, 4>, 4);
+  if constexpr (sizeof(T) == 4) {
+    if (rows == 4) return go(ce_skinny_kernel<T, 4, 4>, 4);
+  }
+  return go(ce_skinny_kernel<T, 2, 2>, 2);
 }
 
-// Up to four rows stream W once on the CUDA cores; above, the tensor cores'
-// tiles (which do the work of 256 rows whatever T is) are faster.
+// The few-row kernel against the tensor cores' tiles (which do the work of 256 rows
+// whatever T is), us at H = 2048, V = 50257 and H = 7168, V = 32768:
+//   bf16  T = 1: 38 / 59, 78 / 114   T = 2: 47 / 60, 98 / 114   T = 4: 59 / 59, 135 / 115
+//   fp32  T = 1: 67 / 328, 148 / 731                            T = 4: 77 / 329, 206 / 730
+// (fp32 W goes through its maximum and its planes first): two rows in bf16, four in
+// fp32.
 bool skinny_ok(const CeShape& s) {
-  return s.T >= 1 && s.T <= kSkinnyRows && (size_t)(s.T <= 2 ? s.T : 4) * s.H * 4 <= (size_t)kSkinnySmem;
+  const int64_t most = s.dtype == MOE_F32 ? kSkinnyRows : 2;
+  return s.T >= 1 && s.T <= most && (size_t)(s.T <= 2 ? s.T : 4) * s.H * 4 <= (size_t)kSkinnySmem;
 }
 
 cudaError_t run_prep(const CeShape& s, const CeLayout& L, char* ws, PrepArgs& p, const void* w,

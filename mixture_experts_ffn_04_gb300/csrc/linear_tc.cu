@@ -35,8 +35,14 @@
 // fp16 planes: the two cross products first, then, after their sum in the
 // registers is scaled by 2^-11, the product of the high planes; half the MMAs.
 //
+// Measured under a full clock: statistics 1.71 PFLOP/s (T = 4096, H = 2048, V =
+// 131072), the logit gradient 1.76, the gradient products 1.87, against 1.91 for the
+// library's matrix product; back to back under the power cap 1.56-1.6 against 1.73.
+// What bounds them is the MMA rate and the cap; tiles with few k-blocks (dW of few
+// rows, dX of a router) are bound by their output.
+//
 // Roles in each CTA: warp 0 TMA producer, warp 1 TMEM and (even CTA) the MMA
-// issuer, warps 4-11 epilogue: two per 32-lane TMEM quarter, one per half of
+// issuer, warp 2 the L2 prefetch of dX's addend, warps 4-11 epilogue: two per 32-lane TMEM quarter, one per half of
 // the 256 columns.  Every wait is bounded; a CTA that gives up raises its abort
 // flag, its partner's waits run out in turn, and both meet at the closing
 // cluster barrier before TMEM is released.

@@ -556,7 +556,7 @@ def moe_router_backward_workspace_bytes(shape: MoEShape) -> int:
 
 def moe_router_backward(shape: MoEShape, x, w_router, topk_idx, d_topk_w, d_gate, balance_coef,
                         z_coef, dx_add, dx, dw_router, aux, ws, stream=None):
-    E, k = moe_topk_unpack(shape.topk_shape)
+    E, k = shape.topk_shape >> 8, shape.topk_shape & 255   # moe_topk_unpack's fields
     T, H, f32 = shape.tokens, shape.hidden, torch.float32
     dt = f32 if shape.dtype == MOE_F32 else torch.bfloat16
     rows = E + shape.shared_gate
@@ -691,7 +691,8 @@ def _alloc_ws(n: int, device, stream, where: str):
 class LinearCrossEntropy:
     """Softmax cross entropy of x . w^T against target over a vocabulary, and its
     gradients, without the [tokens, vocab] logits: shape and a workspace over
-    caller tensors.  reduction: "none", "sum" or "mean" (over the tokens whose
+    caller tensors.  x [tokens, hidden] and w [vocab, hidden] in bf16 or fp32 may
+    be rows of wider buffers; target is int32 [tokens].  reduction: "none", "sum" or "mean" (over the tokens whose
     target is not ignore_index)."""
 
     def __init__(self, tokens: int, hidden: int, vocab: int, dtype=torch.bfloat16,

@@ -285,3 +285,50 @@ def test_fp32_rows_of_different_magnitude():
         err = (got.double() - want).norm(dim=1)
         size = want.norm(dim=1)
         assert (err <= 16 * tol * torch.maximum(size, 2.0 ** -20 * size.max())).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_many_tokens(dtype):
+    """Several tokens a warp in the packing; dW's rows (K) split in parts."""
+    T, H, V = 40001, 64, 300
+    x, w, t = make(T, H, V, dtype, ignored=0.3, seed=12)
+    check(x, w, t, dtype)
+
+
+@pytest.mark.parametrize("T,V", [(263001, 70), (70, 263001)])
+def test_offsets_past_31_bits(T, V):
+    """x and dx, or w and dw, of more than 2^31 elements: the first and last rows
+    against float64 on those rows."""
+    H = 8200
+    g = torch.Generator(device="cuda")
+    g.manual_seed(0)
+    x = torch.randn((T, H), generator=g, device="cuda", dtype=torch.bfloat16)
+    w = torch.randn((V, H), generator=g, device="cuda", dtype=torch.bfloat16).mul_(H ** -0.5)
+    t = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    t[-3], t[1] = V - 1, IGNORE
+    op = m.LinearCrossEntropy(T, H, V, reduction="none", ignore_index=IGNORE)
+    dl = torch.rand(T, generator=g, device="cuda")
+    loss = op.forward(x, w, t)
+    dx, dw = op.backward(x, w, t, dl)
+    keep = (t != IGNORE).float()
+    if V < T:   # a few rows of dx
+        rows = torch.tensor([0, 1, 2, 131072, T - 3, T - 1], device="cuda")
+        z = x[rows].double() @ w.double().t()
+        lse = torch.logsumexp(z, 1) * keep[rows]
+        p = torch.softmax(z, 1)
+        p[torch.arange(len(rows)), t[rows].long().clamp(min=0)] -= 1.0
+        want = (p * (dl * keep)[rows, None].double()) @ w.double()
+        got = dx[rows]
+        assert ((op.lse[rows].double() - lse).abs() <= 1e-4).all()
+    else:       # a few rows of dw: p of those columns needs every column's lse
+        cols = torch.tensor([0, 1, 131072, V - 2, V - 1], device="cuda")
+        z = torch.cat([x.double() @ c.double().t() for c in w.split(32768)], 1)
+        lse = torch.logsumexp(z, 1)
+        assert ((op.lse.double() - lse * keep).abs() <= 1e-4).all()
+        p = torch.exp(z[:, cols] - lse[:, None]) - (t.long()[:, None] == cols[None]).double()
+        want = (p * (dl * keep)[:, None].double()).t() @ x.double()
+        got = dw[cols]
+    err = (got.double() - want).norm(dim=1) / want.norm(dim=1).clamp(min=1e-30)
+    # two roundings of bf16 and, on sums of few terms, what the logits' fp32 sums
+    # leave (1e-4 on a probability)
+    assert (err <= 2 * U[torch.bfloat16] + 1e-3).all(), err

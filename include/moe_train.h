@@ -4,8 +4,9 @@
  * gradient of the router (with its balance and z losses), and the global
  * gradient norm with clipping.  Conventions (device pointers owned by the
  * caller, asynchronous calls on `stream`, host-side validation, workspace and
- * device status word) are those of moe.h; outputs must not overlap inputs
- * unless a declaration says so.
+ * device status word) are those of moe.h, moe_workspace_init before a
+ * workspace's first use included; outputs must not overlap inputs unless a
+ * declaration says so.
  */
 #ifndef MOE_TRAIN_H_
 #define MOE_TRAIN_H_

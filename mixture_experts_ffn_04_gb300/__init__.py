@@ -783,3 +783,6 @@ class GradClip:
             norm = torch.empty(1, dtype=torch.float32, device=self.ws.device)
         moe_grad_clip(self.plan, max_norm, norm, self.ws, stream)
         return norm
+
+    def device_status(self, stream=None):
+        return moe_get_device_status(self.ws, stream)

@@ -42,6 +42,9 @@ struct DzArgs {
   const float* d_w;
   const float* d_gate;
   const int32_t* counts;
+  int32_t *zctr, *gctr;  // tile counters of the logits and of the gradient launch
+  uint32_t* flags;     // few slots (counts == NULL with `count`): each block counts
+  int count;           // the slots itself, and flags the routes out of range
   float cb, cz2;       // balance_coef E / (T^2 k), 2 z_coef / T
   int planes;          // of dz
   bf16* dz;            // [planes][plane][ld]
@@ -59,7 +62,7 @@ struct DzArgs {
 // the experts over the blocks.  Nothing has to be zero before.  One block takes
 // 18 us for 32768 slots (shared-memory atomics), eight 5.  meta: the ticket and
 // the two tile counters, zeroed here.
-constexpr int kHistCluster = 8, kHistOneBlock = 4096;
+constexpr int kHistCluster = 8, kHistOneBlock = 4096, kFewSlots = 1024;
 __global__ void __launch_bounds__(1024) route_hist_kernel(const int32_t* __restrict__ idx, int64_t n,
                                                           int E, int32_t* counts, int32_t* meta,
                                                           uint32_t* flags) {
@@ -146,6 +149,7 @@ __device__ void finish_aux(const DzArgs& a, double sum_pn, double sum_l2) {
   if (lane == 0) {
     a.aux[0] = (float)(x * a.balance);
     a.aux[1] = (float)(y * a.zmean);
+    *a.ticket = 0;
   }
 }
 
@@ -161,12 +165,30 @@ __global__ void __launch_bounds__(256) router_dz_small_kernel(const DzArgs a) {
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   float* row = s_f + (size_t)warp * 64 * NP;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *a.gctr = 0;                    // the next launch's
+    if (a.zctr) *a.zctr = 0;        // the next call's: the logits are done
+  }
   float cnt[2 * NP];
+#pragma unroll
+  for (int j = 0; j < 2 * NP; ++j) cnt[j] = 0.0f;
+  if (a.count) {
+    int* h = reinterpret_cast<int*>(s_f);   // (before the rows need the space)
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) h[e] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < (int)a.T * a.k; i += blockDim.x) {
+      const int e = a.idx[i];
+      if (e >= 0 && e < a.E) atomicAdd(&h[e], 1);   // integers: the order does not matter
+      else if (blockIdx.x == 0) set_flag(a.flags, kFlagRoute);
+    }
+    __syncthreads();
+  }
 #pragma unroll
   for (int j = 0; j < 2 * NP; ++j) {
     const int e = 64 * (j / 2) + 2 * lane + (j & 1);
-    cnt[j] = a.counts && e < a.E ? (float)a.counts[e] : 0.0f;
+    if (e < a.E) cnt[j] = a.count ? (float)reinterpret_cast<const int*>(s_f)[e] : a.counts ? (float)a.counts[e] : 0.0f;
   }
+  if (a.count) __syncthreads();
   // (fp64 arithmetic is slow on this GPU: a few tokens' terms first add up in fp32)
   double sum_pn = 0.0, sum_l2 = 0.0;
   float few_pn = 0.0f, few_l2 = 0.0f;
@@ -393,7 +415,7 @@ struct RbLayout {
   int planes, dz_planes, zsplit;
   LinearSplit split;
   bool dx_direct, dw_direct;
-  size_t meta, counts, part, z, dz, xpl, wpl, dx_part, dw_part, total;
+  size_t counts, part, z, dz, xpl, wpl, dx_part, dw_part, total;
 };
 RbLayout layout_rb(const Shape& s) {
   RbLayout R;
@@ -412,7 +434,6 @@ RbLayout layout_rb(const Shape& s) {
     off += (bytes + 255) & ~(size_t)255;
     return at;
   };
-  R.meta = take(256);   // ticket, tile counters
   R.counts = take((size_t)s.E * 4);
   R.part = take((size_t)kDzBlocks * 16);
   R.z = take(s.dtype == MOE_F32 ? 0 : (size_t)R.zsplit * R.rows_pad * R.cols_pad * 4);
@@ -464,15 +485,23 @@ extern "C" moe_status moe_router_backward(const moe_shape* shape, const void* x,
     return MOE_OK;
   }
   uint32_t* flags = reinterpret_cast<uint32_t*>(b);
-  int32_t* meta = reinterpret_cast<int32_t*>(b + R.meta);
+  // ticket and tile counters, in the status word's block: zero from the workspace's
+  // initialisation on, and zeroed again by their last reader or the histogram
+  int32_t* meta = reinterpret_cast<int32_t*>(b) + 16;
   int32_t* counts = reinterpret_cast<int32_t*>(b + R.counts);
   const int64_t slots = s.T * s.k;
-  const unsigned hb = slots <= kHistOneBlock ? 1u : (unsigned)kHistCluster;
-  // (the pass that finds routes out of range, so it runs in any case)
-  if ((size_t)s.E * 4 > 48 * 1024)
-    CHECK_CUDA(cudaFuncSetAttribute(route_hist_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, s.E * 4));
-  CHECK_CUDA(launch_after(route_hist_kernel, hb, 1024, (size_t)s.E * 4, st, hb, topk_idx, slots, s.E, counts,
-                          meta, flags));
+  // Few slots: every block of the small dz kernel counts them for itself, which
+  // takes less than a launch does (T = 64, k = 4: 25 us a call, by the histogram
+  // kernel 27 to 30).  The counters then have to be zero: dz zeroes them.
+  const bool small = s.k <= 32 && s.ncols <= 512, few = small && slots <= kFewSlots;
+  if (!few) {
+    const unsigned hb = slots <= kHistOneBlock ? 1u : (unsigned)kHistCluster;
+    // (the pass that finds routes out of range, so it runs in any case)
+    if ((size_t)s.E * 4 > 48 * 1024)
+      CHECK_CUDA(cudaFuncSetAttribute(route_hist_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, s.E * 4));
+    CHECK_CUDA(launch_after(route_hist_kernel, hb, 1024, (size_t)s.E * 4, st, hb, topk_idx, slots, s.E, counts,
+                            meta, flags));
+  }
   DzArgs d = {};
   if (s.dtype == MOE_F32) {
     int nsplit = 1;
@@ -512,7 +541,11 @@ extern "C" moe_status moe_router_backward(const moe_shape* shape, const void* x,
   d.idx = topk_idx;
   d.d_w = d_topk_w;
   d.d_gate = d_gate;
-  d.counts = balance_coef > 0.0 ? counts : nullptr;
+  d.counts = balance_coef > 0.0 && !few ? counts : nullptr;
+  d.count = few;
+  d.flags = flags;
+  d.gctr = meta + 1;
+  d.zctr = s.dtype == MOE_F32 ? nullptr : meta + 2;
   const double cb = balance_coef * s.E / ((double)s.T * (double)s.T * s.k);
   d.cb = (float)cb;
   d.cz2 = (float)(2.0 * z_coef / (double)s.T);
@@ -526,7 +559,7 @@ extern "C" moe_status moe_router_backward(const moe_shape* shape, const void* x,
   d.aux = aux;
   d.balance = cb;
   d.zmean = z_coef / (double)s.T;
-  if (s.k <= 32 && s.ncols <= 512) {
+  if (small) {
     const int np = s.ncols <= 64 ? 1 : s.ncols <= 128 ? 2 : s.ncols <= 256 ? 4 : 8;
     const int warps = 4;
     // one wave (64 to 80 registers: at least six blocks an SM)

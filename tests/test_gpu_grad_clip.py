@@ -154,3 +154,21 @@ def test_more_elements_than_a_launch_has_threads():
     want = torch.tensor(2.0 ** -10 * (16.0 / (norm + 1e-6)), dtype=torch.float64)
     for part in (g[:5], g[-5:], g[1 << 29: (1 << 29) + 5]):
         assert ((part.double().cpu() - want).abs() <= 2.0 ** -8 * want).all()
+
+
+@pytest.mark.parametrize("n", [2048 * 600, 2048 * 1216, 2048 * 1217, 2048 * 2433])
+def test_around_the_chunk_sizes(n):
+    """Lists just below and above the limits at which the chunks double, repeated:
+    the counters are ready for the next call."""
+    grads = make([(n - 5000, FP), (4990, BF), (10, FP)], seed=3)
+    outs = [torch.empty_like(g) for g in grads]
+    norm, coef = reference(grads, 1.0)
+    op = m.GradClip(grads, out=outs)
+    for clip in (norm * 0.5, norm * 0.25, norm * 3.0):
+        got = float(op.clip(clip))
+        assert abs(got - norm) <= 64 * F * norm
+        c = min(1.0, clip / (norm + 1e-6))
+        for g, o in zip(grads, outs):
+            want = g.double() * c
+            assert ((o.double() - want).abs() <= (67 * F + U[o.dtype]) * want.abs() + 2.0 ** -133).all()
+    assert op.device_status() == (m.MOE_OK, 0)

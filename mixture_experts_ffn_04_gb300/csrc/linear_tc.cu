@@ -85,7 +85,7 @@ constexpr int BAR_BYTES = 512;
 constexpr int STAGE_WARP = 4096;   // output staging of an epilogue warp: 32 rows of 128 bytes
 constexpr int SMEM_BYTES = 1024 + RING_BYTES + EPI_WARPS * STAGE_WARP + BAR_BYTES;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget of one CTA");
-static_assert((2 * S + 5 + 2 * NSLOT) * 8 + 8 + NSLOT * 32 <= BAR_BYTES, "barrier area");
+static_assert((2 * S + 5 + 2 * NSLOT + EPI_WARPS) * 8 + 8 + NSLOT * 32 <= BAR_BYTES, "barrier area");
 constexpr int kGroupM = 8;
 constexpr int kChunkExact = 8, kChunkBf16 = 64;   // k-blocks of 64
 
@@ -125,7 +125,7 @@ struct Args {
   int64_t dw_pad;
   int want_dx, want_dw;
   int wide_in;   // x and w in maps of 64-wide column blocks (hidden a multiple of 64)
-  int wide_dx;   // rows of dx and dx_add on 32-byte boundaries
+  int wide_dx;   // rows of dx on 32-byte boundaries
   int chunk;   // k-blocks the tensor cores add up before the fp32 registers do
 };
 
@@ -310,27 +310,22 @@ __device__ __forceinline__ void stage_out(const CUtensorMap* map, uint32_t stage
   }
 }
 
-// The addend of dX, and rows of dX that go to their tokens, are moved by the
-// lane that owns the row, in 32-byte sectors (rows that are only 16-byte aligned
-// in halves).
+// A piece of the warp's slice back: 16 bytes j of this lane's row.
+__device__ __forceinline__ uint4 get_piece(uint32_t stage, int lane, int j) {
+  const uint32_t at = stage + lane * 128 + ((j ^ (lane & 7)) << 4);
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+
+// Rows of dX that go to their tokens are stored by the lane that owns the row, in
+// 32-byte sectors (rows that are only 16-byte aligned in halves).
 struct Sector {
   uint32_t v[8];
 };
-__device__ __forceinline__ Sector load_sector(const void* p, bool wide, bool second) {
-  Sector s;
-  if (wide) {
-    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(s.v[0]), "=r"(s.v[1]), "=r"(s.v[2]), "=r"(s.v[3]), "=r"(s.v[4]), "=r"(s.v[5]),
-                   "=r"(s.v[6]), "=r"(s.v[7])
-                 : "l"(p)
-                 : "memory");
-  } else {
-    const uint4 a = reinterpret_cast<const uint4*>(p)[0];
-    const uint4 b = second ? reinterpret_cast<const uint4*>(p)[1] : make_uint4(0, 0, 0, 0);
-    s = {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
-  }
-  return s;
-}
 __device__ __forceinline__ void store_sector(void* p, const Sector& s, bool wide, bool second) {
   if (wide) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(s.v[0]), "r"(s.v[1]),
@@ -360,17 +355,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     linear_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                   const __grid_constant__ CUtensorMap tmD, const __grid_constant__ CUtensorMap tmDt,
                   const __grid_constant__ CUtensorMap tmOx, const __grid_constant__ CUtensorMap tmOw,
-                  const Args a) {
+                  const __grid_constant__ CUtensorMap tmAdd, const Args a) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   unsigned char* s_out = smem + RING_BYTES;
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_out + EPI_WARPS * STAGE_WARP);
-  // bars: full[S] empty[S] tfull[2] tempty[2] final tfill[NSLOT] tdrain[NSLOT],
-  // then the tile slots and the scalars
+  // bars: full[S] empty[S] tfull[2] tempty[2] final tfill[NSLOT] tdrain[NSLOT]
+  // addend[EPI_WARPS], then the scalars and the tile slots
   static_assert(sizeof(Tile) == 32, "a slot is two 16-byte pieces");
   unsigned char* s_slots = reinterpret_cast<unsigned char*>(bars) + BAR_BYTES - NSLOT * sizeof(Tile);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5 + 2 * NSLOT);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5 + 2 * NSLOT + EPI_WARPS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   pdl_trigger();
@@ -384,6 +379,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto tempty = [&](int b) { return smem_u32(&bars[2 * S + 2 + b]); };
   const uint32_t final_bar = smem_u32(&bars[2 * S + 4]);
   auto tfill = [&](int i) { return smem_u32(&bars[2 * S + 5 + i]); };
+  auto addend = [&](int w) { return smem_u32(&bars[2 * S + 5 + 2 * NSLOT + w]); };
   auto tdrain = [&](int i) { return smem_u32(&bars[2 * S + 5 + NSLOT + i]); };
 
   if (threadIdx.x == 0) {
@@ -400,6 +396,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(tfill(i), 1);
       mbar_init(tdrain(i), READERS);
     }
+    for (int w = 0; w < EPI_WARPS; ++w) mbar_init(addend(w), 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -485,10 +482,16 @@ __global__ void __launch_bounds__(THREADS, 1)
       const Tile t = leader ? take_tile(n) : read_tile(n);
       if (t.type < 0) break;
       const int arow = t.mt * BM + (int)rank * BMC, bcol = t.nt * BN + (int)rank * BNC;
-      for (int pr = 0; pr < nprod && ok; ++pr) {
-        int pa, pb;
-        plane_pair(a.planes, pr, pa, pb);
-        for (int kb = t.kb0; kb < t.kb1; ++kb) {
+      // Plane products one after the other; D's two planes side by side at each
+      // k-block, so that the other operand's block comes from L2 the second time (a
+      // router's dW otherwise reads x twice from memory).
+      const bool paired = a.planes == kPlanesD2;
+      const int outer = paired ? 1 : nprod, inner = paired ? nprod : 1;
+      for (int po = 0; po < outer && ok; ++po) {
+        for (int j = t.kb0 * inner; j < t.kb1 * inner; ++j) {
+          int pa, pb;
+          plane_pair(a.planes, paired ? j & 1 : po, pa, pb);
+          const int kb = paired ? j >> 1 : j;
           if (!wait_cl(empty(s), ph ^ 1u, abort_flag)) { ok = false; break; }
           const uint32_t sa = ring + s * STAGE_BYTES, sb = sa + A_BYTES;
           // both CTAs' bytes count on the even CTA's "full" barrier
@@ -610,7 +613,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int c_lo = half * (BN / 2);
     const uint32_t stage = smem_u32(s_out + (warp - 4) * STAGE_WARP);
     int acc = 0;
-    uint32_t aph = 0;
+    uint32_t aph = 0, add_ph = 0;
     for (int n = 0;; ++n) {
       // each warp takes the tile for itself: no barrier among the warps
       Tile t;
@@ -639,48 +642,45 @@ __global__ void __launch_bounds__(THREADS, 1)
       bf16* hout = nullptr;    // rows of dX that go to their tokens: this lane's
       float* fout = nullptr;
       bool wide = true;        // its sectors are aligned
+      bool fit = true;
       if (KIND == kGrad) {
         const int64_t nv = (is_dx ? plan.rows : min(a.vcols, a.vocab - a.v0)) - row0;
         nvalid = nv <= 0 ? 0 : (nv >= 32 ? 32 : (int)nv);
-        const float* fadd = nullptr;
-        const bf16* hadd = nullptr;
         if (is_dx && a.dx_part == nullptr) {
           wide = a.wide_dx;
           if (a.rowmap) {
             const int64_t orow = lane < nvalid ? a.rowmap[row] : 0;
             if (a.out_f32) fout = reinterpret_cast<float*>(a.dx) + orow * a.hidden + n0;
             else hout = reinterpret_cast<bf16*>(a.dx) + orow * a.hidden + n0;
-          } else if (a.dx_add) {
-            if (a.out_f32) fadd = reinterpret_cast<const float*>(a.dx_add) + row * a.hidden + n0;
-            else hadd = reinterpret_cast<const bf16*>(a.dx_add) + row * a.hidden + n0;
+          } else if (a.dx_add != nullptr && nvalid > 0) {
+            // the addend by boxes through the slice, like the output (by the lanes'
+            // own loads, 32 lines an instruction: 1 % slower at T = 8192)
+            const int step = a.out_f32 ? 32 : 64;
+#pragma unroll
+            for (int c = 0; c < BN / 2; c += 32) {
+              if (c % step != 0 || n0 + c >= a.hidden) continue;
+              stage_free(lane);
+              if (lane == 0) {
+                mbar_expect_tx(addend(warp - 4), STAGE_WARP);
+                tma_load_2d(stage, &tmAdd, n0 + c, (int)row0, addend(warp - 4));
+              }
+              int w = 1;
+              if (lane == 0) w = wait_cl(addend(warp - 4), add_ph, abort_flag) ? 1 : 0;
+              add_ph ^= 1u;
+              if (!__shfl_sync(0xffffffffu, w, 0)) { fit = false; break; }
+              if (a.out_f32) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) unpack16(get_piece(stage, lane, j), f + c + 4 * j, (const float*)nullptr);
+              } else if (c % 64 == 0) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) unpack16(get_piece(stage, lane, j), f + c + 8 * j, (const bf16*)nullptr);
+              }
+              __syncwarp();
+            }
           }
         }
-        // (all loads before the first use: one latency a tile; hidden is a
-        // multiple of 8)
-        if (fadd != nullptr && lane < nvalid) {
-#pragma unroll
-          for (int c = 0; c < BN / 2; c += 8)
-            if (n0 + c < a.hidden) {
-              const Sector v = load_sector(fadd + c, wide, true);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) f[c + j] = __uint_as_float(v.v[j]);
-            }
-        }
-        if (hadd != nullptr && lane < nvalid) {
-          Sector v[BN / 32];
-#pragma unroll
-          for (int c = 0; c < BN / 2; c += 16)
-            if (n0 + c < a.hidden) v[c / 16] = load_sector(hadd + c, wide && n0 + c + 16 <= a.hidden, n0 + c + 16 <= a.hidden);
-            else v[c / 16] = {};
-#pragma unroll
-          for (int c = 0; c < BN / 2; c += 16)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              f[c + 2 * j] = __uint_as_float(v[c / 16].v[j] << 16);
-              f[c + 2 * j + 1] = __uint_as_float(v[c / 16].v[j] & 0xFFFF0000u);
-            }
-        }
       }
+      if (!fit) break;
       bool ok = true;
       const int cross = (t.kb1 - t.kb0) * ncross;
 #pragma unroll 1
@@ -1048,8 +1048,8 @@ static cudaError_t prepare_device(int* clusters) {
 
 template <int KIND>
 static cudaError_t launch(const CUtensorMap& mX, const CUtensorMap& mW, const CUtensorMap& mD,
-                          const CUtensorMap& mDt, const CUtensorMap& mOx, const CUtensorMap& mOw, const Args& t,
-                          int64_t tiles, cudaStream_t st) {
+                          const CUtensorMap& mDt, const CUtensorMap& mOx, const CUtensorMap& mOw,
+                          const CUtensorMap& mAdd, const Args& t, int64_t tiles, cudaStream_t st) {
   int mc = 0;
   cudaError_t e = prepare_device(&mc);
   if (e != cudaSuccess) return e;
@@ -1069,7 +1069,7 @@ static cudaError_t launch(const CUtensorMap& mX, const CUtensorMap& mW, const CU
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, linear_kernel<KIND>, mX, mW, mD, mDt, mOx, mOw, t);
+  e = cudaLaunchKernelEx(&cfg, linear_kernel<KIND>, mX, mW, mD, mDt, mOx, mOw, mAdd, t);
   if (e != cudaSuccess) return e;
   count_launch();
   return cudaGetLastError();
@@ -1141,10 +1141,10 @@ cudaError_t launch_linear_logits(const LogitsArgs& a, cudaStream_t st) {
   // value rounded to 2^-9)
   t.chunk = a.gradient && a.planes == 1 ? kChunkBf16 : kChunkExact;
   const int64_t tiles = ((a.rows_bound + BM - 1) / BM) * ((a.vcols + BN - 1) / BN);
-  if (!a.gradient) return launch<kStats>(mX, mW, mX, mX, mX, mX, t, tiles, st);
+  if (!a.gradient) return launch<kStats>(mX, mW, mX, mX, mX, mX, mX, t, tiles, st);
   CUtensorMap mO;
   if (!map_out(&mO, a.d, a.planes * a.rows_pad, a.d_ld, false)) return cudaErrorInvalidValue;
-  return launch<kDlogit>(mX, mW, mX, mX, mO, mO, t, tiles, st);
+  return launch<kDlogit>(mX, mW, mX, mX, mO, mO, mO, t, tiles, st);
 }
 
 int linear_product_split(int64_t rows, int64_t cols, int hidden) {
@@ -1174,7 +1174,7 @@ cudaError_t launch_linear_product(const ProductArgs& a, cudaStream_t st) {
   t.ks_dx = a.split;
   t.chunk = kChunkExact;
   const int64_t tiles = ((a.rows + BM - 1) / BM) * ((a.ld + BN - 1) / BN) * a.split;
-  return launch<kProduct>(mX, mW, mX, mX, mO, mO, t, tiles, st);
+  return launch<kProduct>(mX, mW, mX, mX, mO, mO, mO, t, tiles, st);
 }
 
 cudaError_t launch_linear_grad(const LinearGradArgs& a, cudaStream_t st) {
@@ -1219,7 +1219,7 @@ cudaError_t launch_linear_grad(const LinearGradArgs& a, cudaStream_t st) {
   t.dw_part = a.dw_part;
   t.dw_pad = a.dw_pad;
   auto aligned32 = [](const void* p) { return ((uintptr_t)p & 31u) == 0; };
-  t.wide_dx = a.hidden * (a.out_f32 ? 4 : 2) % 32 == 0 && aligned32(a.dx) && aligned32(a.dx_add);
+  t.wide_dx = a.hidden * (a.out_f32 ? 4 : 2) % 32 == 0 && aligned32(a.dx);
   t.want_dx = a.dx_part != nullptr || a.dx != nullptr;
   t.want_dw = a.dw_part != nullptr || a.dw != nullptr;
   if (a.dx_add && (a.rowmap || a.planes == kPlanesHalf)) return cudaErrorInvalidValue;
@@ -1228,14 +1228,16 @@ cudaError_t launch_linear_grad(const LinearGradArgs& a, cudaStream_t st) {
   const int64_t nth = (a.hidden + BN - 1) / BN;
   const int64_t tiles = (t.want_dx ? ((a.rows_bound + BM - 1) / BM) * nth * t.ks_dx : 0) +
                         (t.want_dw ? ((a.vcols + BN - 1) / BN) * nth * t.ks_dw : 0);
-  CUtensorMap mOx = mX, mOw = mX;   // not used where nothing is stored by box
+  CUtensorMap mOx = mX, mOw = mX, mAdd = mX;   // not used where nothing goes by box
+  if (a.dx_add && !a.dx_part && !map_out(&mAdd, const_cast<void*>(a.dx_add), a.rows_bound > 0 ? a.rows_bound : 1, a.hidden, a.out_f32))
+    return cudaErrorInvalidValue;
   if (t.want_dx && (a.dx_part ? !map_out(&mOx, a.dx_part, a.split.dx * a.rows_pad, a.hidden, true)
                               : !map_out(&mOx, a.dx, a.rows_bound > 0 ? a.rows_bound : 1, a.hidden, a.out_f32)))
     return cudaErrorInvalidValue;
   if (t.want_dw && (a.dw_part ? !map_out(&mOw, a.dw_part, a.split.dw * a.dw_pad, a.hidden, true)
                               : !map_out(&mOw, a.dw, a.vocab, a.hidden, a.out_f32)))
     return cudaErrorInvalidValue;
-  return launch<kGrad>(mX, mW, mD, mDt, mOx, mOw, t, tiles, st);
+  return launch<kGrad>(mX, mW, mD, mDt, mOx, mOw, mAdd, t, tiles, st);
 }
 
 cudaError_t launch_reduce_parts(const float* part, int splits, int64_t part_stride, int64_t rows,

@@ -16,9 +16,9 @@
 // to that of the results (dW_r 2.5e-3 off instead of 1.7e-3), and the MMAs are not
 // what bounds them.
 // What bounds it: HBM, x once for each product, dx_add and dx once; at few tokens
-// the five launches.  T = 8192, H = 7168, E = 256: 179 us, of which the gradient
-// launch takes 110 (360 MB in and out, half of HBM's rate), the logits 32, dz 20,
-// the histogram 8, the reduction of dW_r's parts 6.
+// the launches.  T = 8192, H = 7168, E = 256: 173 us, of which the gradient launch
+// takes 103 (360 MB in and out, half of HBM's rate), the logits 31, dz 20, the
+// histogram 8, the reduction of dW_r's parts 6.
 #include <algorithm>
 #include <cmath>
 

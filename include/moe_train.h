@@ -55,20 +55,23 @@ typedef struct {
 size_t moe_linear_ce_workspace_bytes(const moe_ce_shape *shape);
 
 /* x [T, H], w [V, H] (16-byte aligned), target [T] int32.  Outputs (fp32):
- * loss [T] (may be NULL), lse [T] (may be NULL; the backward reads it),
+ * loss [T] (may be NULL), lse [T] (may be NULL), stats [T, 4] (may be NULL; the
+ * backward reads it: M, the row's largest z log2 e, S = sum_v 2^(z log2 e - M), R the
+ * same without the target, 0; from lse, rounded at its magnitude, probabilities near
+ * 1 would lose digits; 16-byte aligned),
  * total [1] (the reduced loss; NULL with MOE_CE_NONE, else may be NULL). */
 moe_status moe_linear_ce_forward(const moe_ce_shape *shape, const void *x, const void *w,
-                                 const int32_t *target, float *loss, float *lse, float *total,
-                                 void *ws, size_t ws_bytes, void *stream);
+                                 const int32_t *target, float *loss, float *lse, float *stats,
+                                 float *total, void *ws, size_t ws_bytes, void *stream);
 
 /* Gradients of the reduced loss, g_t = d objective / d loss_t:
- *   d_tv = g_t (exp(z_tv - lse_t) - [v = target_t]);  dx = d w;  dw = d^T x
- * lse as the forward wrote it for the same x and w.  dloss: MOE_CE_NONE: [T]
+ *   d_tv = g_t (exp(z_tv - lse_t) - [v = target_t]), at the target -g_t R / S;  dx = d w;  dw = d^T x
+ * stats as the forward wrote it for the same x and w.  dloss: MOE_CE_NONE: [T]
  * (needed); otherwise [1], the gradient of the total, or NULL for 1.
  * dx [T, H], dw [V, H], contiguous; either may be NULL (not computed).  Both
  * are overwritten. */
 moe_status moe_linear_ce_backward(const moe_ce_shape *shape, const void *x, const void *w,
-                                  const int32_t *target, const float *lse, const float *dloss,
+                                  const int32_t *target, const float *stats, const float *dloss,
                                   void *dx, void *dw, void *ws, size_t ws_bytes, void *stream);
 
 /* ---------------------------------------------------------------------------

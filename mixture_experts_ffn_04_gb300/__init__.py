@@ -146,7 +146,7 @@ def lib():
                                      ctypes.POINTER(MoEExpertGrads), P, sz, P]),
         # training operators (moe_train.h)
         "moe_linear_ce_workspace_bytes": (sz, [C]),
-        "moe_linear_ce_forward": (i32, [C, P, P, P, P, P, P, P, sz, P]),
+        "moe_linear_ce_forward": (i32, [C, P, P, P, P, P, P, P, P, sz, P]),
         "moe_linear_ce_backward": (i32, [C, P, P, P, P, P, P, P, P, sz, P]),
         "moe_router_backward_workspace_bytes": (sz, [S]),
         "moe_router_backward": (i32, [S, P, P, P, P, P, ctypes.c_double, ctypes.c_double, P, P, P,
@@ -521,7 +521,8 @@ def moe_linear_ce_workspace_bytes(shape: MoECeShape) -> int:
     return int(lib().moe_linear_ce_workspace_bytes(ctypes.byref(shape)))
 
 
-def moe_linear_ce_forward(shape: MoECeShape, x, w, target, loss, lse, total, ws, stream=None):
+def moe_linear_ce_forward(shape: MoECeShape, x, w, target, loss, lse, stats, total, ws,
+                          stream=None):
     """x and w may be rows of wider buffers (the strides go into the shape)."""
     dt = torch.float32 if shape.dtype == MOE_F32 else torch.bfloat16
     xp, shape.x_stride = _rows(x, shape.tokens, shape.hidden, dt, "x")
@@ -531,11 +532,13 @@ def moe_linear_ce_forward(shape: MoECeShape, x, w, target, loss, lse, total, ws,
         ctypes.byref(shape), xp, wp, _vec(target, T, torch.int32, "target"),
         None if loss is None else _vec(loss, T, f32, "loss"),
         None if lse is None else _vec(lse, T, f32, "lse"),
+        None if stats is None else _vec(stats, 4 * T, f32, "stats"),
         None if total is None else _vec(total, 1, f32, "total"), _p(ws), _nbytes(ws),
         _stream(stream)), "moe_linear_ce_forward")
 
 
-def moe_linear_ce_backward(shape: MoECeShape, x, w, target, lse, dloss, dx, dw, ws, stream=None):
+def moe_linear_ce_backward(shape: MoECeShape, x, w, target, stats, dloss, dx, dw, ws,
+                           stream=None):
     dt = torch.float32 if shape.dtype == MOE_F32 else torch.bfloat16
     T, H, V = shape.tokens, shape.hidden, shape.vocab
     xp, shape.x_stride = _rows(x, T, H, dt, "x")
@@ -543,7 +546,7 @@ def moe_linear_ce_backward(shape: MoECeShape, x, w, target, lse, dloss, dx, dw, 
     n = T if shape.reduction == MOE_CE_NONE else 1
     _check(lib().moe_linear_ce_backward(
         ctypes.byref(shape), xp, wp, _vec(target, T, torch.int32, "target"),
-        _vec(lse, T, torch.float32, "lse"),
+        _vec(stats, 4 * T, torch.float32, "stats"),
         None if dloss is None else _vec(dloss, n, torch.float32, "dloss"),
         None if dx is None else _vec(dx, T * H, dt, "dx"),
         None if dw is None else _vec(dw, V * H, dt, "dw"), _p(ws), _nbytes(ws),
@@ -704,16 +707,18 @@ class LinearCrossEntropy:
         self.shape, self.dtype = s, dtype
         self.ws = _alloc_ws(moe_linear_ce_workspace_bytes(s), device, None, "LinearCrossEntropy")
         self.lse = torch.zeros(tokens, dtype=torch.float32, device=device)
+        self.stats = torch.zeros((tokens, 4), dtype=torch.float32, device=device)
 
     def forward(self, x, w, target, loss=None, total=None, stream=None):
-        """The losses [tokens] ("none") or the reduced loss [1]; self.lse is
+        """The losses [tokens] ("none") or the reduced loss [1]; self.stats is
         what the backward needs."""
         none = self.shape.reduction == MOE_CE_NONE
         if none and loss is None:
             loss = torch.empty(self.shape.tokens, dtype=torch.float32, device=x.device)
         if not none and total is None:
             total = torch.empty(1, dtype=torch.float32, device=x.device)
-        moe_linear_ce_forward(self.shape, x, w, target, loss, self.lse, total, self.ws, stream)
+        moe_linear_ce_forward(self.shape, x, w, target, loss, self.lse, self.stats, total,
+                              self.ws, stream)
         return loss if none else total
 
     def backward(self, x, w, target, dloss=None, dx=None, dw=None, stream=None):
@@ -722,7 +727,7 @@ class LinearCrossEntropy:
             dx = torch.empty(tuple(x.shape), dtype=x.dtype, device=x.device)
         if dw is None:
             dw = torch.empty(tuple(w.shape), dtype=w.dtype, device=w.device)
-        moe_linear_ce_backward(self.shape, x, w, target, self.lse, dloss, dx, dw, self.ws, stream)
+        moe_linear_ce_backward(self.shape, x, w, target, self.stats, dloss, dx, dw, self.ws, stream)
         return dx, dw
 
     def device_status(self, stream=None):

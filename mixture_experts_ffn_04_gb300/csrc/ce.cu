@@ -89,7 +89,7 @@ struct CeLayout {
   int64_t nctr;
   LinearSplit split;
   bool dx_direct, dw_direct;
-  size_t flags, skinny, meta, ctr, rowmap, inv, tgt, g, lse, zt, loss, xc, wpl, stats, d, dx_part, dw_part, total;
+  size_t flags, skinny, meta, ctr, rowmap, inv, tgt, g, rowstat, zt, loss, xc, wpl, stats, d, dx_part, dw_part, total;
 };
 
 CeLayout layout_ce(const CeShape& s) {
@@ -122,7 +122,7 @@ CeLayout layout_ce(const CeShape& s) {
   L.inv = take(T * 4);
   L.tgt = take(T * 4);
   L.g = take(T * 4);
-  L.lse = take(T * 4);
+  L.rowstat = take(T * 16);
   L.zt = take(T * 4);
   L.loss = take(T * 4);
   L.xc = take((size_t)s.planes * T * s.H * 2);
@@ -150,9 +150,12 @@ struct PrepArgs {
   uint32_t* flags;
   // forward: zero the outputs of tokens that do not count
   float *loss, *lse_out;
+  float4* stats_out;
   // backward
-  const float *lse, *dloss;
-  float *g, *lse_c;
+  const float4* rowstat;
+  const float* dloss;
+  float* g;
+  float4* rowstat_c;
   int reduction;
   void* dx;   // zero the rows of tokens that do not count (direct dx), or NULL
   // fp32: the bits of the largest finite |x| of tokens that count, |w| and (none
@@ -215,11 +218,12 @@ __global__ void __launch_bounds__(256) ce_prep_kernel(const PrepArgs a) {
           if (a.reduction == MOE_CE_MEAN) g /= (float)s_total;
         }
         a.g[pos] = g;
-        a.lse_c[pos] = a.lse[mine];
+        a.rowstat_c[pos] = a.rowstat[mine];
       }
     } else {
       if (a.loss) a.loss[mine] = 0.0f;
       if (a.lse_out) a.lse_out[mine] = 0.0f;
+      if (a.stats_out) a.stats_out[mine] = make_float4(0.0f, 1.0f, 0.0f, 0.0f);
     }
   }
   if (blockIdx.x == 0) {
@@ -330,8 +334,28 @@ __global__ void __launch_bounds__(256) ce_max_kernel(const float* __restrict__ x
   }
 }
 
+// A row from the maximum m and sum of exponentials of its other columns (log2
+// units) and its target's logit:  M = the larger of m and z_t log2 e, R = the others'
+// sum under M, S = R + 2^(z_t log2 e - M);  loss = ln(S / e_t) = log1p(R / e_t).
+// With the target apart neither the loss nor the gradient p_t - 1 = -R / S of a
+// nearly certain target loses digits to 1 or to lse.
+struct RowStat {
+  float4 stat;   // M, S, R, 0
+  float lse, loss;
+};
+__device__ __forceinline__ RowStat finish_row(float m, float s, float zt) {
+  const float log2e = 1.4426950408889634f, ln2 = 0.6931471805599453f;
+  const float M = fmaxf(m, zt * log2e), Mu = M == -INFINITY ? 0.0f : M;
+  const float R = s * exp2f(m - Mu), et = exp2f(fmaf(zt, log2e, -Mu)), S = R + et;
+  RowStat r;
+  r.stat = make_float4(Mu, S, R, 0.0f);
+  r.lse = ln2 * (Mu + log2f(S));
+  r.loss = R <= et ? log1pf(R / et) : fmaf(ln2, fmaf(-zt, log2e, Mu), logf(S));
+  return r;
+}
+
 // Merge the row statistics of all half tiles (lanes: 32 rows, warps: slices of
-// the half tiles): M = max m, S = sum s 2^(m - M), lse = ln 2 (M + log2 S).  The
+// the half tiles): the other columns' maximum and sum, then the row (above).  The
 // last block adds the rows' losses, in row order, in fp64.
 // (T = 4096, V = 131072: 34 MB of statistics in 20 us, bound by their latency.)
 constexpr int kMergeWarps = 32;
@@ -339,7 +363,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     ce_merge_kernel(const float2* __restrict__ stats, int64_t rows_pad, int parts,
                     const float* __restrict__ zt, const int32_t* __restrict__ rowmap,
                     const int32_t* nrows, int32_t* ticket, float* loss_c, float* loss, float* lse,
-                    float* total, int mean) {
+                    float4* rowstat, float* total, int mean) {
   pdl_trigger();
   pdl_wait();
   const int n = *nrows;
@@ -366,10 +390,11 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
         S = S * exp2f(M - mu) + v.y * exp2f(v.x - mu);
         M = m;
       }
-      const float l = 0.6931471805599453f * (M + log2f(S));
-      const float each = l - zt[row];
+      const RowStat r = finish_row(M, S, zt[row]);
+      const float each = r.loss;
       const int t = rowmap[row];
-      if (lse) lse[t] = l;
+      if (lse) lse[t] = r.lse;
+      if (rowstat) rowstat[t] = r.stat;
       if (loss) loss[t] = each;
       loss_c[row] = each;
     }
@@ -410,6 +435,7 @@ struct SkinnyArgs {
   const int32_t* target;
   int T, H, V, ignore, reduction;
   float *loss, *lse, *total;
+  float4* rowstat;   // [T] or NULL
   float2* part;      // [grid][4]
   float* zt;         // [4]
   int32_t* ticket;   // 0 between calls
@@ -486,8 +512,8 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps, R <= 2 ? kSkinnyPerSm : 2) 
 #pragma unroll
         for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
         if (v0 + v < vend) {
-          if (lane == 0 && tg[r] == (int)(v0 + v)) a.zt[r] = z;
-          merge_ms(M[r], S[r], z * 1.4426950408889634f, 1.0f);
+          if (tg[r] != (int)(v0 + v)) merge_ms(M[r], S[r], z * 1.4426950408889634f, 1.0f);
+          else if (lane == 0) a.zt[r] = z;   // the target is merged by itself
         }
       }
   }
@@ -521,9 +547,11 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps, R <= 2 ? kSkinnyPerSm : 2) 
     }
     if (lane == 0 && r < a.T) {
       const bool ok = counts(a.target[r], a.V, a.ignore);
-      const float l = ok ? 0.6931471805599453f * (m + log2f(s)) : 0.0f;
-      const float each = ok ? l - __ldcg(a.zt + r) : 0.0f;
-      if (a.lse) a.lse[r] = l;
+      RowStat q = {make_float4(0.0f, 1.0f, 0.0f, 0.0f), 0.0f, 0.0f};
+      if (ok) q = finish_row(m, s, __ldcg(a.zt + r));
+      const float each = q.loss;
+      if (a.lse) a.lse[r] = q.lse;
+      if (a.rowstat) a.rowstat[r] = q.stat;
       if (a.loss) a.loss[r] = each;
       s_loss[r] = each;
     }
@@ -657,12 +685,14 @@ extern "C" size_t moe_linear_ce_workspace_bytes(const moe_ce_shape* shape) {
 }
 
 extern "C" moe_status moe_linear_ce_forward(const moe_ce_shape* shape, const void* x, const void* w,
-                                            const int32_t* target, float* loss, float* lse,
+                                            const int32_t* target, float* loss, float* lse, float* stats,
                                             float* total, void* ws, size_t ws_bytes, void* stream) {
   reset_launch_count();
   DECODE_CE(shape, s);
   if (!w || (s.T > 0 && (!x || !target))) return fail(MOE_ERR_INVALID_ARG, "x, w and target must be non-NULL");
-  if (!loss && !lse && !total) return fail(MOE_ERR_INVALID_ARG, "one of loss, lse and total must be non-NULL");
+  if (!loss && !lse && !stats && !total)
+    return fail(MOE_ERR_INVALID_ARG, "one of loss, lse, stats and total must be non-NULL");
+  if (!aligned16(stats)) return fail(MOE_ERR_INVALID_ARG, "stats must be 16-byte aligned");
   if (s.reduction == MOE_CE_NONE && total)
     return fail(MOE_ERR_INVALID_ARG, "total must be NULL with MOE_CE_NONE");
   if (!aligned16(x) || !aligned16(w)) return fail(MOE_ERR_INVALID_ARG, "x and w must be 16-byte aligned");
@@ -685,6 +715,7 @@ extern "C" moe_status moe_linear_ce_forward(const moe_ce_shape* shape, const voi
     k.reduction = s.reduction;
     k.loss = loss;
     k.lse = lse;
+    k.rowstat = reinterpret_cast<float4*>(stats);
     k.total = total;
     k.part = reinterpret_cast<float2*>(b + L.skinny);
     k.zt = reinterpret_cast<float*>(b + L.zt);
@@ -698,6 +729,7 @@ extern "C" moe_status moe_linear_ce_forward(const moe_ce_shape* shape, const voi
   p.x = x;
   p.loss = loss;
   p.lse_out = lse;
+  p.stats_out = reinterpret_cast<float4*>(stats);
   CHECK_CUDA(run_prep(s, L, b, p, w, st));
   const int64_t vpad = ((int64_t)s.V + 255) / 256 * 256;
   // bf16 W is read where it is: one launch over the whole vocabulary
@@ -737,19 +769,21 @@ extern "C" moe_status moe_linear_ce_forward(const moe_ce_shape* shape, const voi
   CHECK_CUDA(launch_after(ce_merge_kernel, (unsigned)blocks, 32 * kMergeWarps, 0, st, 1,
                           reinterpret_cast<const float2*>(b + L.stats), L.rows_pad, (int)(vpad / 128),
                           reinterpret_cast<const float*>(b + L.zt), p.rowmap, p.nrows, p.ticket,
-                          reinterpret_cast<float*>(b + L.loss), loss, lse, total,
+                          reinterpret_cast<float*>(b + L.loss), loss, lse,
+                          reinterpret_cast<float4*>(stats), total,
                           s.reduction == MOE_CE_MEAN ? 1 : 0));
   return MOE_OK;
 }
 
 extern "C" moe_status moe_linear_ce_backward(const moe_ce_shape* shape, const void* x, const void* w,
-                                             const int32_t* target, const float* lse,
+                                             const int32_t* target, const float* stats,
                                              const float* dloss, void* dx, void* dw, void* ws,
                                              size_t ws_bytes, void* stream) {
   reset_launch_count();
   DECODE_CE(shape, s);
-  if (!w || (s.T > 0 && (!x || !target || !lse)))
-    return fail(MOE_ERR_INVALID_ARG, "x, w, target and lse must be non-NULL");
+  if (!w || (s.T > 0 && (!x || !target || !stats)))
+    return fail(MOE_ERR_INVALID_ARG, "x, w, target and stats must be non-NULL");
+  if (!aligned16(stats)) return fail(MOE_ERR_INVALID_ARG, "stats must be 16-byte aligned");
   if (s.reduction == MOE_CE_NONE && !dloss && s.T > 0)
     return fail(MOE_ERR_INVALID_ARG, "dloss must be non-NULL with MOE_CE_NONE");
   if (!dw && (!dx && s.T > 0)) return fail(MOE_ERR_INVALID_ARG, "one of dx and dw must be non-NULL");
@@ -763,10 +797,10 @@ extern "C" moe_status moe_linear_ce_backward(const moe_ce_shape* shape, const vo
   PrepArgs p = {};
   p.target = target;
   p.x = x;
-  p.lse = lse;
+  p.rowstat = reinterpret_cast<const float4*>(stats);
   p.dloss = dloss;
   p.g = reinterpret_cast<float*>(b + L.g);
-  p.lse_c = reinterpret_cast<float*>(b + L.lse);
+  p.rowstat_c = reinterpret_cast<float4*>(b + L.rowstat);
   p.dx = L.dx_direct ? dx : nullptr;
   CHECK_CUDA(run_prep(s, L, b, p, w, st));
   const int64_t vpad = ((int64_t)s.V + 255) / 256 * 256;
@@ -798,7 +832,7 @@ extern "C" moe_status moe_linear_ce_backward(const moe_ce_shape* shape, const vo
     a.flags = p.flags;
     a.rows_pad = L.rows_pad;
     a.gradient = true;
-    a.lse = p.lse_c;
+    a.rowstat = p.rowstat_c;
     a.g = p.g;
     a.d = b + L.d;
     a.d_ld = L.piece;

@@ -110,7 +110,7 @@ struct Args {
   float2* stats;
   float* zt;
   int64_t rows_pad;
-  const float* lse;
+  const float4* rowstat;
   const float* g;
   bf16* d;
   int64_t d_ld;
@@ -739,7 +739,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (dt >= 0 && dt < BN / 2) {
           float zt = 0.0f;
 #pragma unroll
-          for (int j = 0; j < BN / 2; ++j) zt = pick(zt, f[j], (int)dt, j);
+          for (int j = 0; j < BN / 2; ++j) {
+            zt = pick(zt, f[j], (int)dt, j);
+            f[j] = pick(f[j], -INFINITY, (int)dt, j);   // the target is merged by itself
+          }
           a.zt[row] = zt;
         }
         float m4[4] = {f[0], f[1], f[2], f[3]};
@@ -758,13 +761,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int64_t col0 = a.v0 + (int64_t)t.nt * BN + c_lo;
         const int64_t left = a.vocab - col0;
         const int64_t dt = live ? (int64_t)a.target[row] - col0 : -1;
-        const float l2 = live ? a.lse[row] * kLog2e : 0.0f;
-        const float g = live ? a.g[row] : 0.0f;
+        const float4 ms = live ? a.rowstat[row] : make_float4(0.0f, 1.0f, 0.0f, 0.0f);
+        const float gs = live ? a.g[row] / ms.y : 0.0f;
 #pragma unroll
-        for (int j = 0; j < BN / 2; ++j) f[j] = ex2(fmaf(f[j], kLog2e, -l2)) * g;
+        for (int j = 0; j < BN / 2; ++j) f[j] = ex2(fmaf(f[j], kLog2e, -ms.x)) * gs;
         if (dt >= 0 && dt < BN / 2) {
 #pragma unroll
-          for (int j = 0; j < BN / 2; ++j) f[j] = pick(f[j], f[j] - g, (int)dt, j);
+          for (int j = 0; j < BN / 2; ++j) f[j] = pick(f[j], -gs * ms.z, (int)dt, j);
         }
         if (!live || left < BN / 2) {
 #pragma unroll
@@ -1133,7 +1136,7 @@ cudaError_t launch_linear_logits(const LogitsArgs& a, cudaStream_t st) {
   t.stats = a.stats;
   t.zt = a.zt;
   t.rows_pad = a.rows_pad;
-  t.lse = a.lse;
+  t.rowstat = a.rowstat;
   t.g = a.g;
   t.d = reinterpret_cast<bf16*>(a.d);
   t.d_ld = a.d_ld;

@@ -114,16 +114,16 @@ struct LogitsArgs {
   int32_t* ctr;            // zeroed tile counter
   uint32_t* flags;
   // statistics (gradient == false): (max, sum) of each row over each 128-wide
-  // half tile in log2 units at stats[(2 * tile + half) * rows_pad + row], and
+  // half tile without its target, in log2 units at stats[(2 * tile + half) * rows_pad + row], and
   // the target's logit
   float2* stats;
   float* zt;
   int64_t rows_pad;
-  // gradient (gradient == true): d = g (exp(z - lse) - [v = target]) in bf16
+  // gradient (gradient == true): d = g 2^(z log2 e - M) / S, at the target -g R / S, in bf16
   // planes [planes * rows_pad, d_ld], zeros past the rows (to the tile) and
   // past the vocabulary
   bool gradient;
-  const float* lse;
+  const float4* rowstat;   // (M, S, R, -) of the compacted rows
   const float* g;
   void* d;
   int64_t d_ld;

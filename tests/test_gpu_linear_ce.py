@@ -190,8 +190,8 @@ def test_one_of_the_gradients():
     x, w, t = make(130, 128, 900, torch.bfloat16)
     op, loss, dx, dw = check(x, w, t, torch.bfloat16)
     a, b = torch.empty_like(dx), torch.empty_like(dw)
-    m.moe_linear_ce_backward(op.shape, x, w, t, op.lse, None, a, None, op.ws)
-    m.moe_linear_ce_backward(op.shape, x, w, t, op.lse, None, None, b, op.ws)
+    m.moe_linear_ce_backward(op.shape, x, w, t, op.stats, None, a, None, op.ws)
+    m.moe_linear_ce_backward(op.shape, x, w, t, op.stats, None, None, b, op.ws)
     assert torch.equal(a, dx) and torch.equal(b, dw)
 
 
@@ -332,3 +332,26 @@ def test_offsets_past_31_bits(T, V):
     # two roundings of bf16 and, on sums of few terms, what the logits' fp32 sums
     # leave (1e-4 on a probability)
     assert (err <= 2 * U[torch.bfloat16] + 1e-3).all(), err
+
+
+@pytest.mark.parametrize("T", [2, 60])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_nearly_certain_targets(T, dtype):
+    """Targets whose probability is 1 - 1e-2 .. 1 - 1e-5 (logits 20 above the rest):
+    the loss and d = p - 1 keep their digits although lse is near 24.  The bound is
+    relative: the chunked fp32 sums' error of the logits' difference (zb, absolute)
+    plus a few f, against a loss and a gradient of size 1 - p."""
+    H, V = 64, 400
+    x, w, t = make(T, H, V, dtype, seed=9)
+    x = torch.nn.functional.normalize(w[t.long()].float(), dim=1) * 22
+    x = x.to(dtype)
+    op = m.LinearCrossEntropy(T, H, V, dtype=dtype, reduction="sum", ignore_index=IGNORE)
+    loss = op.forward(x, w, t)
+    dx, dw = op.backward(x, w, t)
+    out, lse, rdx, rdw, zb = reference(x, w, t, "sum", None, V)
+    assert abs(float(loss) - float(out)) <= (2 * zb + 64 * F) * T
+    tol = 2 * U[dtype] + 4 * zb + 16 * F
+    # each token's row of dx is (p - 1) w_t + ...: size 1 - p, error 8 f + zb (1 - p)
+    size = rdx.norm(dim=1)
+    err = (dx.double() - rdx).norm(dim=1)
+    assert (err <= tol * size + 8 * F * float(w.double().norm(dim=1).max())).all()

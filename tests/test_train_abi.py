@@ -48,7 +48,7 @@ BAD_CE = [(dict(tokens=-1), "tokens"), (dict(hidden=0), "hidden"), (dict(hidden=
 def test_ce_shapes_rejected(m, kw, word):
     s = ce_shape(m, **kw)
     assert m.moe_linear_ce_workspace_bytes(s) == 0
-    for st in (m.lib().moe_linear_ce_forward(ctypes.byref(s), 16, 16, 16, 16, 16, 16, 256, 1 << 40, None),
+    for st in (m.lib().moe_linear_ce_forward(ctypes.byref(s), 16, 16, 16, 16, 16, 16, 16, 256, 1 << 40, None),
                m.lib().moe_linear_ce_backward(ctypes.byref(s), 16, 16, 16, 16, 16, 16, 16, 256, 1 << 40, None)):
         assert st in (m.MOE_ERR_INVALID_ARG, m.MOE_ERR_UNSUPPORTED)
         assert word in m.moe_last_error()
@@ -60,24 +60,26 @@ def test_ce_arguments_rejected(m):
     ref, n = ctypes.byref(s), m.moe_linear_ce_workspace_bytes(s)
     assert n > 0
     inv, wse = m.MOE_ERR_INVALID_ARG, m.MOE_ERR_WORKSPACE
-    assert f(None, 16, 16, 16, 16, 16, 16, 256, n, None) == inv
+    assert f(None, 16, 16, 16, 16, 16, 16, 16, 256, n, None) == inv
     for hole in range(3):
         a = [16, 16, 16]
         a[hole] = None
-        assert f(ref, *a, 16, 16, 16, 256, n, None) == inv
+        assert f(ref, *a, 16, 16, 16, 16, 256, n, None) == inv
         assert b(ref, *a, 16, 16, 16, 16, 256, n, None) == inv
-    assert f(ref, 16, 16, 16, None, None, None, 256, n, None) == inv
-    assert f(ref, 8, 16, 16, 16, 16, 16, 256, n, None) == inv
-    assert f(ref, 16, 24, 16, 16, 16, 16, 256, n, None) == inv
-    assert f(ref, 16, 16, 16, 16, 16, 16, None, n, None) == wse
-    assert f(ref, 16, 16, 16, 16, 16, 16, 128, n, None) == wse
-    assert f(ref, 16, 16, 16, 16, 16, 16, 256, n - 1, None) == wse
+    assert f(ref, 16, 16, 16, None, None, None, None, 256, n, None) == inv
+    assert f(ref, 16, 16, 16, 16, 16, 4, 16, 256, n, None) == inv
+    assert f(ref, 8, 16, 16, 16, 16, 16, 16, 256, n, None) == inv
+    assert f(ref, 16, 24, 16, 16, 16, 16, 16, 256, n, None) == inv
+    assert f(ref, 16, 16, 16, 16, 16, 16, 16, None, n, None) == wse
+    assert f(ref, 16, 16, 16, 16, 16, 16, 16, 128, n, None) == wse
+    assert f(ref, 16, 16, 16, 16, 16, 16, 16, 256, n - 1, None) == wse
     assert b(ref, 16, 16, 16, None, 16, 16, 16, 256, n, None) == inv
+    assert b(ref, 16, 16, 16, 4, 16, 16, 16, 256, n, None) == inv
     assert b(ref, 16, 16, 16, 16, 16, None, None, 256, n, None) == inv
     assert b(ref, 16, 16, 16, 16, 16, 8, 16, 256, n, None) == inv
     assert b(ref, 16, 16, 16, 16, 16, 16, 16, 256, n - 1, None) == wse
     none = ce_shape(m, reduction=m.MOE_CE_NONE)
-    assert f(ctypes.byref(none), 16, 16, 16, 16, 16, 16, 256, n, None) == inv
+    assert f(ctypes.byref(none), 16, 16, 16, 16, 16, 16, 16, 256, n, None) == inv
     assert b(ctypes.byref(none), 16, 16, 16, 16, None, 16, 16, 256, n, None) == inv
 
 
@@ -85,13 +87,13 @@ def test_ce_binding_checks_tensors(m):
     s = ce_shape(m)
     x, w = torch.zeros(64, 256, dtype=torch.bfloat16), torch.zeros(1000, 256, dtype=torch.bfloat16)
     t, ws = torch.zeros(64, dtype=torch.int32), torch.zeros(16, dtype=torch.uint8)
-    lse, tot = torch.zeros(64), torch.zeros(1)
+    lse, st, tot = torch.zeros(64), torch.zeros(64, 4), torch.zeros(1)
     for bad in (dict(x=x.float()), dict(x=x[:63]), dict(w=w[:, :248]), dict(t=t.long()), dict(t=t[:5]),
-                dict(lse=lse[:3]), dict(tot=torch.zeros(2)), dict(x=x.t().contiguous().t())):
-        a = dict(x=x, w=w, t=t, lse=lse, tot=tot)
+                dict(lse=lse[:3]), dict(st=lse), dict(tot=torch.zeros(2)), dict(x=x.t().contiguous().t())):
+        a = dict(x=x, w=w, t=t, lse=lse, st=st, tot=tot)
         a.update(bad)
         with pytest.raises(ValueError):
-            m.moe_linear_ce_forward(s, a["x"], a["w"], a["t"], None, a["lse"], a["tot"], ws, stream=0)
+            m.moe_linear_ce_forward(s, a["x"], a["w"], a["t"], None, a["lse"], a["st"], a["tot"], ws, stream=0)
 
 
 def test_router_arguments_rejected(m):

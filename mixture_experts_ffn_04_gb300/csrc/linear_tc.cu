@@ -488,9 +488,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       const bool paired = a.planes == kPlanesD2;
       const int outer = paired ? 1 : nprod, inner = paired ? nprod : 1;
       for (int po = 0; po < outer && ok; ++po) {
+        int pa, pb;
+        plane_pair(a.planes, po, pa, pb);
         for (int j = t.kb0 * inner; j < t.kb1 * inner; ++j) {
-          int pa, pb;
-          plane_pair(a.planes, paired ? j & 1 : po, pa, pb);
+          if (paired) pa = 1 - (j & 1);   // pb stays 0
           const int kb = paired ? j >> 1 : j;
           if (!wait_cl(empty(s), ph ^ 1u, abort_flag)) { ok = false; break; }
           const uint32_t sa = ring + s * STAGE_BYTES, sb = sa + A_BYTES;

@@ -475,61 +475,73 @@ __global__ void __launch_bounds__(THREADS, 1)
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(ROLE_REGS));
   if (warp == 0 && lane == 0) {
     // ---------------- TMA producer ----------------
+    // A k-block has 512 clocks of MMA: what does not change within a tile is
+    // computed before it, and each kind of tile has a loop of its own.
     int s = 0;
-    uint32_t ph = 0, issued = 0, par = 0;
+    uint32_t ph = 0, issued = 0;
     bool ok = true;
+    const uint32_t full0 = map_to_rank(full(0), 0);   // the even CTA's "full" barriers
+    const bool paired = a.planes == kPlanesD2;
+    const int outer = paired ? 1 : nprod;
     for (int n = 0; ok; ++n) {
       const Tile t = leader ? take_tile(n) : read_tile(n);
       if (t.type < 0) break;
       const int arow = t.mt * BM + (int)rank * BMC, bcol = t.nt * BN + (int)rank * BNC;
+      // one stage: both CTAs' bytes count on the even CTA's barrier
+      auto stage_load = [&](auto&& load) -> bool {
+        if (!wait_cl(empty(s), ph ^ 1u, abort_flag)) return false;
+        const uint32_t sa = ring + s * STAGE_BYTES;
+        if (leader) mbar_expect_tx(full(s), 2 * STAGE_BYTES);
+        load(sa, sa + A_BYTES, full0 + 8u * s);
+        ++issued;
+        if (++s == S) { s = 0; ph ^= 1u; }
+        return true;
+      };
       // Plane products one after the other; D's two planes side by side at each
       // k-block, so that the other operand's block comes from L2 the second time (a
       // router's dW otherwise reads x twice from memory).
-      const bool paired = a.planes == kPlanesD2;
-      const int outer = paired ? 1 : nprod, inner = paired ? nprod : 1;
       for (int po = 0; po < outer && ok; ++po) {
         int pa, pb;
         plane_pair(a.planes, po, pa, pb);
-        for (int j = t.kb0 * inner; j < t.kb1 * inner; ++j) {
-          if (paired) pa = 1 - (j & 1);   // pb stays 0
-          const int kb = paired ? j >> 1 : j;
-          if (!wait_cl(empty(s), ph ^ 1u, abort_flag)) { ok = false; break; }
-          const uint32_t sa = ring + s * STAGE_BYTES, sb = sa + A_BYTES;
-          // both CTAs' bytes count on the even CTA's "full" barrier
-          const uint32_t fb = map_to_rank(full(s), 0);
-          if (leader) mbar_expect_tx(full(s), 2 * STAGE_BYTES);
-          const int k = kb * BK;
-          if (KIND != kGrad) {   // (kProduct: one plane)
-            tma_load_2d_pair(sa, &tmX, k, (int)(pa * a.x_plane) + arow, fb);
-            tma_load_2d_pair(sb, &tmW, k, (int)(pb * a.w_plane + a.w_v0) + bcol, fb);
-          } else if (t.type == 1) {
-            tma_load_2d_pair(sa, &tmD, k, (int)(pa * a.d_plane) + arow, fb);
-            const int wr = (int)(pb * a.w_plane + a.w_v0) + k;
-            if (a.wide_in) {
-              tma_load_3d_pair(sb, &tmW, 0, wr, bcol / 64, fb);
-            } else {
-              tma_load_2d_pair(sb, &tmW, bcol, wr, fb);
-              tma_load_2d_pair(sb + BOX_BYTES, &tmW, bcol + 64, wr, fb);
-            }
-          } else {
-            const int dr = (int)(pa * a.d_plane) + k, xr = (int)(pb * a.x_plane) + k;
-            tma_load_3d_pair(sa, &tmDt, 0, dr, arow / 64, fb);
-            if (a.wide_in) {
-              tma_load_3d_pair(sb, &tmX, 0, xr, bcol / 64, fb);
-            } else {
-              tma_load_2d_pair(sb, &tmX, bcol, xr, fb);
-              tma_load_2d_pair(sb + BOX_BYTES, &tmX, bcol + 64, xr, fb);
-            }
-          }
-          issued |= 1u << s;
-          par = (par & ~(1u << s)) | (ph << s);
-          if (++s == S) { s = 0; ph ^= 1u; }
+        const int d0 = (int)(pa * a.d_plane), d1 = paired ? 0 : d0;   // paired: plane 1, then 0
+        const int w0 = (int)(pb * a.w_plane + a.w_v0), x0 = (int)((KIND == kGrad ? pb : pa) * a.x_plane);
+        if (KIND != kGrad) {   // (kProduct: one plane)
+          for (int k = t.kb0 * BK; k < t.kb1 * BK && ok; k += BK)
+            ok = stage_load([&](uint32_t sa, uint32_t sb, uint32_t fb) {
+              tma_load_2d_pair(sa, &tmX, k, x0 + arow, fb);
+              tma_load_2d_pair(sb, &tmW, k, w0 + bcol, fb);
+            });
+        } else if (t.type == 1) {
+          for (int k = t.kb0 * BK; k < t.kb1 * BK && ok; k += BK)
+            for (int d = d0, h = 0; h <= (int)paired && ok; ++h, d = d1)
+              ok = stage_load([&](uint32_t sa, uint32_t sb, uint32_t fb) {
+                tma_load_2d_pair(sa, &tmD, k, d + arow, fb);
+                if (a.wide_in) {
+                  tma_load_3d_pair(sb, &tmW, 0, w0 + k, bcol / 64, fb);
+                } else {
+                  tma_load_2d_pair(sb, &tmW, bcol, w0 + k, fb);
+                  tma_load_2d_pair(sb + BOX_BYTES, &tmW, bcol + 64, w0 + k, fb);
+                }
+              });
+        } else {
+          for (int k = t.kb0 * BK; k < t.kb1 * BK && ok; k += BK)
+            for (int d = d0, h = 0; h <= (int)paired && ok; ++h, d = d1)
+              ok = stage_load([&](uint32_t sa, uint32_t sb, uint32_t fb) {
+                tma_load_3d_pair(sa, &tmDt, 0, d + k, arow / 64, fb);
+                if (a.wide_in) {
+                  tma_load_3d_pair(sb, &tmX, 0, x0 + k, bcol / 64, fb);
+                } else {
+                  tma_load_2d_pair(sb, &tmX, bcol, x0 + k, fb);
+                  tma_load_2d_pair(sb + BOX_BYTES, &tmX, bcol + 64, x0 + k, fb);
+                }
+              });
         }
       }
     }
     if (*abort_flag && leader) {
-      for (int i = 0; i < S; ++i)
-        if (issued & (1u << i)) wait2_quiet(full(i), (par >> i) & 1u);
+      // loads still in flight land before the pair goes away
+      for (uint32_t i = issued > (uint32_t)S ? issued - S : 0u; i < issued; ++i)
+        wait2_quiet(full((int)(i % S)), (i / S) & 1u);
     }
   } else if (warp == 1 && lane == 0 && leader) {
     // ---------------- even CTA: MMA issuer for the pair ----------------

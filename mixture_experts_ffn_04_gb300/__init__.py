@@ -501,12 +501,16 @@ MOE_CE_NONE, MOE_CE_SUM, MOE_CE_MEAN = 0, 1, 2
 
 
 def _rows(t: torch.Tensor, rows: int, cols: int, dtype, name: str):
-    """Address and row stride of a [rows, cols] matrix whose rows are contiguous."""
+    """Address and row stride of a [rows, cols] matrix whose rows are contiguous and
+    apart (a broadcast row's stride 0 would mean "dense" to the library)."""
     if tuple(t.shape) != (rows, cols) or t.dtype != dtype:
         raise ValueError("%s must be [%d, %d] %s, got %s %s" % (name, rows, cols, dtype,
                                                                 tuple(t.shape), t.dtype))
     if cols > 1 and t.stride(1) != 1:
         raise ValueError("the rows of %s must be contiguous" % name)
+    if rows > 1 and t.stride(0) < cols:
+        raise ValueError("the rows of %s share memory (row stride %d for %d columns): pass a copy, "
+                         "for example %s.contiguous()" % (name, t.stride(0), cols, name))
     return t.data_ptr(), (t.stride(0) if rows > 1 else cols)
 
 

@@ -355,7 +355,8 @@ moe_status moe_layer_forward_traced(const moe_shape *shape, const moe_weights *w
                                     const float *routes_w, void *y, void *ws, size_t ws_bytes,
                                     void *stream, void *const *stage_events);
 
-/* Zero the device status word of a new workspace (asynchronous on `stream`).
+/* Zero the first 256 bytes of a new workspace, its device status word and the
+ * counters beside it (asynchronous on `stream`).
  * Call once before the first use of a workspace; status bits then accumulate
  * until moe_get_device_status reads and clears them. */
 moe_status moe_workspace_init(void *ws, void *stream);

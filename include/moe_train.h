@@ -6,7 +6,10 @@
  * caller, asynchronous calls on `stream`, host-side validation, workspace and
  * device status word) are those of moe.h, moe_workspace_init before a
  * workspace's first use included; outputs must not overlap inputs unless a
- * declaration says so.
+ * declaration says so.  One workspace serves calls of any shapes and operators in
+ * turn.  Its first 256 bytes outlive a call: the status word, and counters that
+ * are zero between calls.  A call that reported MOE_ERR_CUDA may have left them
+ * otherwise: moe_workspace_init before the next one.
  */
 #ifndef MOE_TRAIN_H_
 #define MOE_TRAIN_H_
@@ -50,8 +53,8 @@ typedef struct {
   int64_t w_stride;     /* the same for w */
 } moe_ce_shape;
 
-/* Workspace of the two calls below (0 for an invalid shape).  Nothing in it is
- * kept from one call for the next but the status word. */
+/* Workspace of the two calls below (0 for an invalid shape).  Nothing of a call's
+ * results or inputs is kept in it for the next. */
 size_t moe_linear_ce_workspace_bytes(const moe_ce_shape *shape);
 
 /* x [T, H], w [V, H] (16-byte aligned), target [T] int32.  Outputs (fp32):

@@ -61,7 +61,7 @@ struct DzArgs {
 // cluster: each block counts its part in shared memory, then adds up its share of
 // the experts over the blocks.  Nothing has to be zero before.  One block takes
 // 18 us for 32768 slots (shared-memory atomics), eight 5.  meta: the ticket and
-// the two tile counters, zeroed here.
+// the two tile counters, zeroed here too (after a call that ended early).
 constexpr int kHistCluster = 8, kHistOneBlock = 4096, kFewSlots = 1024;
 __global__ void __launch_bounds__(1024) route_hist_kernel(const int32_t* __restrict__ idx, int64_t n,
                                                           int E, int32_t* counts, int32_t* meta,
@@ -110,6 +110,16 @@ __device__ __forceinline__ float exp_of(float v) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v * 1.4426950408889634f));
   return r;
+}
+
+// Every dz kernel zeroes the tile counters of the gradient launch that follows it and
+// of the logits' launch, which is done: a call of few slots, of whatever shape, finds
+// zeros in them without a launch of its own for that.
+__device__ __forceinline__ void reset_counters(const DzArgs& a) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *a.gctr = 0;
+    if (a.zctr) *a.zctr = 0;
+  }
 }
 
 // The losses: block sums in fp64, the last block adds the blocks in order.
@@ -165,10 +175,7 @@ __global__ void __launch_bounds__(256) router_dz_small_kernel(const DzArgs a) {
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   float* row = s_f + (size_t)warp * 64 * NP;
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    *a.gctr = 0;                    // the next launch's
-    if (a.zctr) *a.zctr = 0;        // the next call's: the logits are done
-  }
+  reset_counters(a);
   float cnt[2 * NP];
 #pragma unroll
   for (int j = 0; j < 2 * NP; ++j) cnt[j] = 0.0f;
@@ -319,6 +326,7 @@ __global__ void __launch_bounds__(256) router_dz_kernel(const DzArgs a) {
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  reset_counters(a);
   float* z = s_f + (size_t)warp * 2 * a.ncols;
   float* acc = z + a.ncols;
   double sum_pn = 0.0, sum_l2 = 0.0;
@@ -486,7 +494,9 @@ extern "C" moe_status moe_router_backward(const moe_shape* shape, const void* x,
   }
   uint32_t* flags = reinterpret_cast<uint32_t*>(b);
   // ticket and tile counters, in the status word's block: zero from the workspace's
-  // initialisation on, and zeroed again by their last reader or the histogram
+  // initialisation on; the ticket's last reader and each call's dz kernel (the
+  // histogram too, for calls that have it) leave zeros for the next call, whose shape
+  // may be another
   int32_t* meta = reinterpret_cast<int32_t*>(b) + 16;
   int32_t* counts = reinterpret_cast<int32_t*>(b + R.counts);
   const int64_t slots = s.T * s.k;

@@ -1,0 +1,123 @@
+"""The training operators where their state, ranges and inputs are unusual: one
+workspace for several shapes, logits far from zero, fp32 matrices whose rows and
+columns differ by more than half precision can hold, dropped routes with any value
+in their slots, very many tokens, lists given as generators, outputs made on
+another stream.
+
+Bounds (derived).  f = 2^-24, u = f or 2^-8 (bf16).
+ * logits: zb = 8 sqrt(H) f max|x| max|w| + 16 f max|z|, the bound of a product in
+   fp32, over the columns that are not masked (a masked column's probability is
+   exactly 0 on both sides).  lse and loss: 2 zb + 8 f |lse|.
+ * gradients: 2 u (the operand's and the result's rounding) + 4 zb (the
+   probabilities' relative error) + 16 f, relative, of the matrix or row named.
+"""
+import math
+
+import pytest
+import torch
+
+import mixture_experts_ffn_04_gb300 as m
+from mixture_experts_ffn_04_gb300 import workloads as W
+
+pytestmark = pytest.mark.gpu
+IGNORE = -100
+F = 2.0 ** -24
+BF, FP = torch.bfloat16, torch.float32
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def make(T, H, V, seed):
+    g = gen(seed)
+    x = torch.randn((T, H), generator=g, device="cuda")
+    w = torch.randn((V, H), generator=g, device="cuda") / math.sqrt(H)
+    t = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    return x, w, t, torch.rand(T, generator=g, device="cuda") + 0.5
+
+
+# ---------------------------------------------------------------------------
+# one workspace for several shapes and operators
+# ---------------------------------------------------------------------------
+def router_shape(T, H, E, k, dtype=BF):
+    s = m.MoEShape()
+    s.tokens, s.hidden, s.moe_inter, s.topk_shape = T, H, 8, m.moe_topk_pack(E, k)
+    s.norm_topk, s.dtype, s.norm_eps = 1, m.MOE_F32 if dtype == FP else m.MOE_BF16, 1e-6
+    return s
+
+
+def workspace(n):
+    ws = torch.empty(n + 256, dtype=torch.uint8, device="cuda")
+    ws.fill_(0xFF)   # NaN in whatever is read without having been written
+    off = (-ws.data_ptr()) % 256
+    ws = ws[off: off + n]
+    m.moe_workspace_init(ws)
+    return ws
+
+
+def router_call(shape, ws, dtype, seed):
+    T, H = shape.tokens, shape.hidden
+    E, k = m.moe_topk_unpack(shape.topk_shape)
+    g = gen(seed)
+    x = torch.randn((T, H), generator=g, device="cuda").to(dtype)
+    w = (torch.randn((E, H), generator=g, device="cuda") / math.sqrt(H)).to(dtype)
+    idx = torch.randint(0, E, (T, k), generator=g, device="cuda").to(torch.int32)
+    d_w = torch.randn((T, k), generator=g, device="cuda")
+    dx, dw, aux = torch.empty_like(x), torch.empty_like(w), torch.empty(2, device="cuda")
+    m.moe_router_backward(shape, x, w, idx, d_w, None, 0.02, 0.003, None, dx, dw, aux, ws)
+    return dx, dw, aux
+
+
+def ce_call(T, H, V, dtype, ws, seed):
+    s = m.MoECeShape()
+    s.tokens, s.hidden, s.vocab, s.dtype = T, H, V, m.MOE_F32 if dtype == FP else m.MOE_BF16
+    s.reduction, s.ignore_index = m.MOE_CE_MEAN, IGNORE
+    x, w, t, _ = make(T, H, V, seed)
+    x, w = x.to(dtype), w.to(dtype)
+    stats, total = torch.empty((T, 4), device="cuda"), torch.empty(1, device="cuda")
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    ws = workspace(m.moe_linear_ce_workspace_bytes(s)) if ws is None else ws
+    m.moe_linear_ce_forward(s, x, w, t, None, None, stats, total, ws)
+    m.moe_linear_ce_backward(s, x, w, t, stats, None, dx, dw, ws)
+    return total, dx, dw
+
+
+# the kernels of a router call depend on its columns, slots and type: wide, few
+# slots, many slots, many slots a token
+ROUTERS = [(300, 128, 700, 5, BF), (64, 256, 60, 4, BF), (257, 64, 32, 40, BF), (16, 1024, 16, 2, BF),
+           (600, 256, 64, 8, BF), (64, 128, 600, 3, FP), (64, 256, 60, 4, FP), (40, 512, 8, 1, BF)]
+
+
+def test_one_workspace_for_routers_of_any_shape():
+    shapes = [router_shape(*r) for r in ROUTERS]
+    ws = workspace(max(m.moe_router_backward_workspace_bytes(s) for s in shapes))
+    fresh = [router_call(s, workspace(m.moe_router_backward_workspace_bytes(s)), r[4], i)
+             for i, (s, r) in enumerate(zip(shapes, ROUTERS))]
+    order = [0, 1, 2, 3, 0, 3, 5, 1, 4, 2, 7, 6, 0, 7, 5, 3, 1]
+    for i in order:
+        got = router_call(shapes[i], ws, ROUTERS[i][4], i)
+        for a, b in zip(got, fresh[i]):
+            assert torch.isfinite(a.float()).all(), i
+            assert torch.equal(a, b), i
+    assert m.moe_get_device_status(ws)[0] == m.MOE_OK
+
+
+def test_one_workspace_for_the_layer_and_the_training_operators():
+    wl = W.small(W.QWEN3_30B_A3B, T=64, H=256, I=128, E=16, k=2)
+    dev = W.make_inputs(wl, seed=0, device="cuda")
+    layer = m.MoELayer(wl, dev)
+    shapes = [router_shape(*r) for r in ROUTERS[:4]]
+    ces = [(1, 256, 900, BF), (300, 128, 2000, BF), (3, 64, 500, FP), (70, 64, 500, FP)]
+    n = max([layer.ws.numel()] + [m.moe_router_backward_workspace_bytes(s) for s in shapes] + [64 << 20])
+    y = layer.forward(dev["x"])
+    ce = [ce_call(*c, None, i) for i, c in enumerate(ces)]
+    ro = [router_call(s, workspace(m.moe_router_backward_workspace_bytes(s)), BF, i) for i, s in enumerate(shapes)]
+    layer.ws = workspace(n)
+    for i in [0, 1, 2, 3, 0, 1, 3, 2]:
+        assert torch.equal(layer.forward(dev["x"]), y)
+        assert all(torch.equal(a, b) for a, b in zip(ce_call(*ces[i], layer.ws, i), ce[i])), i
+        assert all(torch.equal(a, b) for a, b in zip(router_call(shapes[i], layer.ws, BF, i), ro[i])), i
+    assert layer.device_status()[0] == m.MOE_OK

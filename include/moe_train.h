@@ -59,9 +59,9 @@ size_t moe_linear_ce_workspace_bytes(const moe_ce_shape *shape);
 
 /* x [T, H], w [V, H] (16-byte aligned), target [T] int32.  Outputs (fp32):
  * loss [T] (may be NULL), lse [T] (may be NULL), stats [T, 4] (may be NULL; the
- * backward reads it: M, the row's largest z log2 e, S = sum_v 2^(z log2 e - M), R the
- * same without the target, 0; from lse, rounded at its magnitude, probabilities near
- * 1 would lose digits; 16-byte aligned),
+ * backward reads it: M, the row's largest z, S = sum_v e^(z - M), R the same without
+ * the target, 0; from lse, rounded at its magnitude, probabilities near 1 would lose
+ * digits; 16-byte aligned),
  * total [1] (the reduced loss; NULL with MOE_CE_NONE, else may be NULL). */
 moe_status moe_linear_ce_forward(const moe_ce_shape *shape, const void *x, const void *w,
                                  const int32_t *target, float *loss, float *lse, float *stats,

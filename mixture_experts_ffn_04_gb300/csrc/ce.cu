@@ -334,23 +334,30 @@ __global__ void __launch_bounds__(256) ce_max_kernel(const float* __restrict__ x
   }
 }
 
-// A row from the maximum m and sum of exponentials of its other columns (log2
-// units) and its target's logit:  M = the larger of m and z_t log2 e, R = the others'
-// sum under M, S = R + 2^(z_t log2 e - M);  loss = ln(S / e_t) = log1p(R / e_t).
-// With the target apart neither the loss nor the gradient p_t - 1 = -R / S of a
-// nearly certain target loses digits to 1 or to lse.
+// Maximum M and sum of exponentials S joined with another pair's.
+__device__ __forceinline__ void merge_ms(float& M, float& S, float m, float s) {
+  const float log2e = 1.4426950408889634f, n = fmaxf(M, m), mu = n == -INFINITY ? 0.0f : n;
+  S = S * exp2f((M - mu) * log2e) + s * exp2f((m - mu) * log2e);
+  M = n;
+}
+
+// A row from the maximum m and sum of exponentials of its other columns and its
+// target's logit:  M = the larger of m and z_t, R = the others' sum under M, S = R +
+// e^(z_t - M);  loss = ln(S / e_t) = log1p(R / e_t).  With the target apart neither
+// the loss nor the gradient p_t - 1 = -R / S of a nearly certain target loses digits
+// to 1 or to lse.
 struct RowStat {
   float4 stat;   // M, S, R, 0
   float lse, loss;
 };
 __device__ __forceinline__ RowStat finish_row(float m, float s, float zt) {
-  const float log2e = 1.4426950408889634f, ln2 = 0.6931471805599453f;
-  const float M = fmaxf(m, zt * log2e), Mu = M == -INFINITY ? 0.0f : M;
-  const float R = s * exp2f(m - Mu), et = exp2f(fmaf(zt, log2e, -Mu)), S = R + et;
+  const float log2e = 1.4426950408889634f;
+  const float M = fmaxf(m, zt), Mu = M == -INFINITY ? 0.0f : M;
+  const float R = s * exp2f((m - Mu) * log2e), et = exp2f((zt - Mu) * log2e), S = R + et;
   RowStat r;
   r.stat = make_float4(Mu, S, R, 0.0f);
-  r.lse = ln2 * (Mu + log2f(S));
-  r.loss = R <= et ? log1pf(R / et) : fmaf(ln2, fmaf(-zt, log2e, Mu), logf(S));
+  r.lse = Mu + logf(S);
+  r.loss = R <= et ? log1pf(R / et) : (Mu - zt) + logf(S);
   return r;
 }
 
@@ -376,9 +383,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
 #pragma unroll 8
       for (int p = warp; p < parts; p += kMergeWarps) {
         const float2 v = __ldcs(stats + p * rows_pad + row);
-        const float m = fmaxf(M, v.x), mu = m == -INFINITY ? 0.0f : m;
-        S = S * exp2f(M - mu) + v.y * exp2f(v.x - mu);
-        M = m;
+        merge_ms(M, S, v.x, v.y);
       }
     }
     s_part[warp][lane] = make_float2(M, S);
@@ -386,9 +391,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     if (warp == 0 && row < n) {
       for (int w = 1; w < kMergeWarps; ++w) {
         const float2 v = s_part[w][lane];
-        const float m = fmaxf(M, v.x), mu = m == -INFINITY ? 0.0f : m;
-        S = S * exp2f(M - mu) + v.y * exp2f(v.x - mu);
-        M = m;
+        merge_ms(M, S, v.x, v.y);
       }
       const RowStat r = finish_row(M, S, zt[row]);
       const float each = r.loss;
@@ -441,11 +444,6 @@ struct SkinnyArgs {
   int32_t* ticket;   // 0 between calls
   uint32_t* flags;
 };
-__device__ __forceinline__ void merge_ms(float& M, float& S, float m, float s) {
-  const float n = fmaxf(M, m), mu = n == -INFINITY ? 0.0f : n;
-  S = S * exp2f(M - mu) + s * exp2f(m - mu);
-  M = n;
-}
 template <typename T, int R, int NV>
 __global__ void __launch_bounds__(32 * kSkinnyWarps, R <= 2 ? kSkinnyPerSm : 2) ce_skinny_kernel(const SkinnyArgs a) {
   pdl_trigger();
@@ -512,7 +510,7 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps, R <= 2 ? kSkinnyPerSm : 2) 
 #pragma unroll
         for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
         if (v0 + v < vend) {
-          if (tg[r] != (int)(v0 + v)) merge_ms(M[r], S[r], z * 1.4426950408889634f, 1.0f);
+          if (tg[r] != (int)(v0 + v)) merge_ms(M[r], S[r], z, 1.0f);
           else if (lane == 0) a.zt[r] = z;   // the target is merged by itself
         }
       }

@@ -737,9 +737,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int j = 0; j < BN / 2; ++j) f[j] = f[j] * r0 * r1;
       }
       if (KIND == kStats) {
-        // maximum and sum of the row over this half of the tile, in log2 units:
-        // the maximum kept is the rounded z * log2(e), so the sum's scale and
-        // the maximum agree exactly
+        // maximum of the row over this half of the tile and the sum of e^(z - maximum).
+        // The difference is taken before the factor log2 e: a half tile of masked
+        // columns has a maximum of -1e10 and more, whose product with log2 e is
+        // rounded by more than exponents can be.
         const bool live = row < plan.rows;
         const int64_t col0 = a.v0 + (int64_t)t.nt * BN + c_lo;
         const int64_t left = a.vocab - col0;
@@ -761,11 +762,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         float m4[4] = {f[0], f[1], f[2], f[3]};
 #pragma unroll
         for (int j = 4; j < BN / 2; ++j) m4[j & 3] = fmaxf(m4[j & 3], f[j]);
-        const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * kLog2e;
+        const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         const float mu = m == -INFINITY ? 0.0f : m;
         float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int j = 0; j < BN / 2; ++j) s4[j & 3] += ex2(fmaf(f[j], kLog2e, -mu));
+        for (int j = 0; j < BN / 2; ++j) s4[j & 3] += ex2((f[j] - mu) * kLog2e);
         if (live)
           a.stats[(2 * (a.v0 / BN + t.nt) + half) * a.rows_pad + row] =
               make_float2(m, (s4[0] + s4[1]) + (s4[2] + s4[3]));
@@ -777,7 +778,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float4 ms = live ? a.rowstat[row] : make_float4(0.0f, 1.0f, 0.0f, 0.0f);
         const float gs = live ? a.g[row] / ms.y : 0.0f;
 #pragma unroll
-        for (int j = 0; j < BN / 2; ++j) f[j] = ex2(fmaf(f[j], kLog2e, -ms.x)) * gs;
+        for (int j = 0; j < BN / 2; ++j) f[j] = ex2((f[j] - ms.x) * kLog2e) * gs;
         if (dt >= 0 && dt < BN / 2) {
 #pragma unroll
           for (int j = 0; j < BN / 2; ++j) f[j] = pick(f[j], -gs * ms.z, (int)dt, j);

@@ -113,13 +113,13 @@ struct LogitsArgs {
   const int32_t* target;   // [rows] compacted targets
   int32_t* ctr;            // zeroed tile counter
   uint32_t* flags;
-  // statistics (gradient == false): (max, sum) of each row over each 128-wide
-  // half tile without its target, in log2 units at stats[(2 * tile + half) * rows_pad + row], and
-  // the target's logit
+  // statistics (gradient == false): (max, sum of e^(z - max)) of each row over each
+  // 128-wide half tile without its target, at stats[(2 * tile + half) * rows_pad +
+  // row], and the target's logit
   float2* stats;
   float* zt;
   int64_t rows_pad;
-  // gradient (gradient == true): d = g 2^(z log2 e - M) / S, at the target -g R / S, in bf16
+  // gradient (gradient == true): d = g e^(z - M) / S, at the target -g R / S, in bf16
   // planes [planes * rows_pad, d_ld], zeros past the rows (to the tile) and
   // past the vocabulary
   bool gradient;

@@ -40,6 +40,47 @@ def make(T, H, V, seed):
 
 
 # ---------------------------------------------------------------------------
+# logits far from zero
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("value", [1e4, 1e8, 1e12, 1e25])
+@pytest.mark.parametrize("T", [2, 60, 300])
+@pytest.mark.parametrize("dtype", [BF])
+def test_masked_half_tiles(T, value, dtype):
+    """All of 128 and of 256 neighbouring columns at logits of -value (a padded
+    vocabulary): the exponentials of such a group's own differences from its
+    maximum must not leave the range."""
+    H, V = 64, 1000
+    x, w, t, dl = make(T, H, V, 34)
+    x, w = x.to(dtype), w.to(dtype)
+    x[:, 3] = 1.0
+    columns = torch.ones(V, dtype=torch.bool, device="cuda")
+    columns[128:256] = False
+    columns[512:768] = False
+    w[~columns, 3] = -value
+    keep = columns.nonzero().flatten()
+    t = keep[t.long() % len(keep)].to(torch.int32)
+    op = m.LinearCrossEntropy(T, H, V, dtype=dtype, reduction="none", ignore_index=IGNORE)
+    loss = op.forward(x, w, t)
+    dx, dw = op.backward(x, w, t, dl)
+    z = x.double() @ w[keep].double().t()
+    at = torch.cumsum(columns.long(), 0)[t.long()] - 1
+    one = torch.nn.functional.one_hot(at, len(keep)).double()
+    lse = torch.logsumexp(z, 1)
+    zb = 8 * math.sqrt(H) * F * float(x.double().norm(dim=1).max() * w[keep].double().norm(dim=1).max())
+    zb += 16 * F * float(z.abs().max())
+    tol = 2 * zb + 8 * F * float(lse.abs().max())
+    assert float((op.lse.double() - lse).abs().max()) <= tol
+    assert float((loss.double() - (lse - (z * one).sum(1))).abs().max()) <= tol
+    d = (torch.softmax(z, 1) - one) * dl.double()[:, None]
+    gt = (2.0 ** -7 if dtype == BF else 2 * F) + 4 * zb + 16 * F
+    want = d @ w[keep].double()
+    assert float((dx.double() - want).norm()) <= gt * float(want.norm())
+    want = d.t() @ x.double()
+    assert float((dw[keep].double() - want).norm()) <= gt * float(want.norm())
+    assert (dw[~columns] == 0).all()
+
+
+# ---------------------------------------------------------------------------
 # one workspace for several shapes and operators
 # ---------------------------------------------------------------------------
 def router_shape(T, H, E, k, dtype=BF):

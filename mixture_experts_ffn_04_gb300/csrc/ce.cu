@@ -106,7 +106,7 @@ CeLayout layout_ce(const CeShape& s) {
   L.split = linear_grad_split(s.T, L.piece, s.H, s.planes);
   L.dx_direct = L.npieces == 1 && L.split.dx == 1;
   L.dw_direct = L.split.dw == 1;
-  L.nctr = 2 * L.npieces;
+  L.nctr = 3 * L.npieces;   // statistics, logit gradient, gradients of each piece
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -394,12 +394,11 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
         merge_ms(M, S, v.x, v.y);
       }
       const RowStat r = finish_row(M, S, zt[row]);
-      const float each = r.loss;
-      const int t = rowmap[row];
+      const int64_t t = rowmap ? rowmap[row] : row;   // NULL: the rows stay packed
       if (lse) lse[t] = r.lse;
       if (rowstat) rowstat[t] = r.stat;
-      if (loss) loss[t] = each;
-      loss_c[row] = each;
+      if (loss) loss[t] = r.loss;
+      loss_c[row] = r.loss;
     }
     __syncthreads();
   }
@@ -662,6 +661,54 @@ cudaError_t piece_operand(const CeShape& s, const CeLayout& L, char* ws, const v
                        ws + L.wpl, L.piece, reinterpret_cast<const uint32_t*>(ws + L.meta + 32) + 1, st);
 }
 
+// Statistics of the packed rows over the whole vocabulary, and their merge into the
+// rows' results (rowmap: by token; NULL: packed).
+cudaError_t run_stats(const CeShape& s, const CeLayout& L, char* b, const PrepArgs& p, const void* w,
+                      const int32_t* rowmap, float* loss, float* lse, float4* rowstat, float* total,
+                      cudaStream_t st) {
+  const int64_t vpad = ((int64_t)s.V + 255) / 256 * 256;
+  // bf16 W is read where it is: one launch over the whole vocabulary
+  const int64_t step = s.planes == 1 ? vpad : L.piece;
+  int64_t c = 0;
+  for (int64_t v0 = 0; v0 < vpad && s.T > 0; v0 += step, ++c) {
+    const int64_t vcols = std::min(step, vpad - v0);
+    Operand o;
+    cudaError_t e = piece_operand(s, L, b, w, v0, vcols, &o, st);
+    if (e != cudaSuccess) return e;
+    LogitsArgs a = {};
+    a.planes = s.planes;
+    a.scale = p.scales;
+    a.x = b + L.xc;
+    a.x_ld = s.H;
+    a.x_plane = L.rows_pad;
+    a.w = o.p;
+    a.w_ld = o.ld;
+    a.w_plane = o.plane;
+    a.w_rows = o.rows;
+    a.hidden = s.H;
+    a.v0 = v0;
+    a.w_v0 = o.v0;
+    a.vcols = vcols;
+    a.vocab = s.V;
+    a.nrows = p.nrows;
+    a.rows_bound = s.T;
+    a.target = p.tgt;
+    a.ctr = p.ctr + c;
+    a.flags = p.flags;
+    a.stats = reinterpret_cast<float2*>(b + L.stats);
+    a.zt = reinterpret_cast<float*>(b + L.zt);
+    a.rows_pad = L.rows_pad;
+    e = launch_linear_logits(a, st);
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((s.T + 31) / 32, 4096));
+  return launch_after(ce_merge_kernel, (unsigned)blocks, 32 * kMergeWarps, 0, st, 1,
+                      reinterpret_cast<const float2*>(b + L.stats), L.rows_pad, (int)(vpad / 128),
+                      reinterpret_cast<const float*>(b + L.zt), rowmap, p.nrows, p.ticket,
+                      reinterpret_cast<float*>(b + L.loss), loss, lse, rowstat, total,
+                      s.reduction == MOE_CE_MEAN ? 1 : 0);
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -729,47 +776,7 @@ extern "C" moe_status moe_linear_ce_forward(const moe_ce_shape* shape, const voi
   p.lse_out = lse;
   p.stats_out = reinterpret_cast<float4*>(stats);
   CHECK_CUDA(run_prep(s, L, b, p, w, st));
-  const int64_t vpad = ((int64_t)s.V + 255) / 256 * 256;
-  // bf16 W is read where it is: one launch over the whole vocabulary
-  const int64_t step = s.planes == 1 ? vpad : L.piece;
-  int64_t c = 0;
-  for (int64_t v0 = 0; v0 < vpad && s.T > 0; v0 += step, ++c) {
-    const int64_t vcols = std::min(step, vpad - v0);
-    Operand o;
-    CHECK_CUDA(piece_operand(s, L, b, w, v0, vcols, &o, st));
-    LogitsArgs a = {};
-    a.planes = s.planes;
-    a.scale = p.scales;
-    a.x = b + L.xc;
-    a.x_ld = s.H;
-    a.x_plane = L.rows_pad;
-    a.w = o.p;
-    a.w_ld = o.ld;
-    a.w_plane = o.plane;
-    a.w_rows = o.rows;
-    a.hidden = s.H;
-    a.v0 = v0;
-    a.w_v0 = o.v0;
-    a.vcols = vcols;
-    a.vocab = s.V;
-    a.nrows = p.nrows;
-    a.rows_bound = s.T;
-    a.target = p.tgt;
-    a.ctr = p.ctr + c;
-    a.flags = p.flags;
-    a.stats = reinterpret_cast<float2*>(b + L.stats);
-    a.zt = reinterpret_cast<float*>(b + L.zt);
-    a.rows_pad = L.rows_pad;
-    CHECK_CUDA(launch_linear_logits(a, st));
-  }
-  int64_t blocks = std::min<int64_t>((s.T + 31) / 32, 4096);
-  if (blocks < 1) blocks = 1;
-  CHECK_CUDA(launch_after(ce_merge_kernel, (unsigned)blocks, 32 * kMergeWarps, 0, st, 1,
-                          reinterpret_cast<const float2*>(b + L.stats), L.rows_pad, (int)(vpad / 128),
-                          reinterpret_cast<const float*>(b + L.zt), p.rowmap, p.nrows, p.ticket,
-                          reinterpret_cast<float*>(b + L.loss), loss, lse,
-                          reinterpret_cast<float4*>(stats), total,
-                          s.reduction == MOE_CE_MEAN ? 1 : 0));
+  CHECK_CUDA(run_stats(s, L, b, p, w, p.rowmap, loss, lse, reinterpret_cast<float4*>(stats), total, st));
   return MOE_OK;
 }
 
@@ -801,6 +808,9 @@ extern "C" moe_status moe_linear_ce_backward(const moe_ce_shape* shape, const vo
   p.rowstat_c = reinterpret_cast<float4*>(b + L.rowstat);
   p.dx = L.dx_direct ? dx : nullptr;
   CHECK_CUDA(run_prep(s, L, b, p, w, st));
+  // The few-row forward adds up its logits in an order of its own, so its statistics
+  // are not those of the tiles below: they are taken again.
+  if (skinny_ok(s)) CHECK_CUDA(run_stats(s, L, b, p, w, nullptr, nullptr, nullptr, p.rowstat_c, nullptr, st));
   const int64_t vpad = ((int64_t)s.V + 255) / 256 * 256;
   int64_t c = 0;
   for (int64_t v0 = 0; v0 < vpad; v0 += L.piece, ++c) {
@@ -826,7 +836,7 @@ extern "C" moe_status moe_linear_ce_backward(const moe_ce_shape* shape, const vo
     a.nrows = p.nrows;
     a.rows_bound = s.T;
     a.target = p.tgt;
-    a.ctr = p.ctr + 2 * c;
+    a.ctr = p.ctr + L.npieces + 2 * c;
     a.flags = p.flags;
     a.rows_pad = L.rows_pad;
     a.gradient = true;
@@ -856,7 +866,7 @@ extern "C" moe_status moe_linear_ce_backward(const moe_ce_shape* shape, const vo
     q.vocab = s.V;
     q.nrows = p.nrows;
     q.rows_bound = s.T;
-    q.ctr = p.ctr + 2 * c + 1;
+    q.ctr = p.ctr + L.npieces + 2 * c + 1;
     q.flags = p.flags;
     q.split = L.split;
     q.out_f32 = s.dtype == MOE_F32;

@@ -27,8 +27,7 @@
 // truncations predict), so a tile is summed in chunks of k-blocks: each chunk in
 // one of the two TMEM accumulators, the chunks in fp32 registers with rounding to
 // nearest, which frees the accumulator as soon as it is read.  Chunks of 512 for
-// the loss and all fp32 products, 4096 for gradients that are
-// rounded to bf16 anyway.
+// logits and all fp32 products, 4096 for gradients that are rounded to bf16 anyway.
 //
 // fp32 operands come in planes (train.h).  Three bf16 planes: a tile's k-loop runs
 // over the six plane products whose weight is above 2^-24, smallest first.  Two
@@ -1154,9 +1153,10 @@ cudaError_t launch_linear_logits(const LogitsArgs& a, cudaStream_t st) {
   t.g = a.g;
   t.d = reinterpret_cast<bf16*>(a.d);
   t.d_ld = a.d_ld;
-  // the logit gradient in bf16 takes no harm from the cut-off (about 1e-5 on a
-  // value rounded to 2^-9)
-  t.chunk = a.gradient && a.planes == 1 ? kChunkBf16 : kChunkExact;
+  // the same chunks for the gradient's logits as for the statistics: with chunks of
+  // their own (4096 of K) they differed from them by 1e-5 of their size, which at
+  // logits of 1e4 is a third of a probability
+  t.chunk = kChunkExact;
   const int64_t tiles = ((a.rows_bound + BM - 1) / BM) * ((a.vcols + BN - 1) / BN);
   if (!a.gradient) return launch<kStats>(mX, mW, mX, mX, mX, mX, mX, t, tiles, st);
   CUtensorMap mO;

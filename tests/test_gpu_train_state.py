@@ -80,6 +80,38 @@ def test_masked_half_tiles(T, value, dtype):
     assert (dw[~columns] == 0).all()
 
 
+@pytest.mark.parametrize("value", [300.0, 1e4, 1e8, 1e12, 1e25])
+@pytest.mark.parametrize("T", [2, 60, 300])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_huge_logits(T, value, dtype):
+    """Rows of x of norm value sqrt(H): every probability is 0 or 1 where the two
+    largest logits are further apart than the sums' error."""
+    H, V = 2048, 500
+    x, w, t, dl = make(T, H, V, 35)
+    x, w = (x * value).to(dtype), w.to(dtype)
+    op = m.LinearCrossEntropy(T, H, V, dtype=dtype, reduction="none", ignore_index=IGNORE)
+    loss = op.forward(x, w, t)
+    dx, dw = op.backward(x, w, t, dl)
+    z = x.double() @ w.double().t()
+    one = torch.nn.functional.one_hot(t.long(), V).double()
+    lse = torch.logsumexp(z, 1)
+    zb = 8 * math.sqrt(H) * F * (x.double().norm(dim=1) * float(w.double().norm(dim=1).max()))
+    zb += 16 * F * z.abs().amax(dim=1)
+    tol = 2 * zb + 8 * F * lse.abs()
+    assert ((op.lse.double() - lse).abs() <= tol).all()
+    assert ((loss.double() - (lse - (z * one).sum(1))).abs() <= tol).all()
+    assert torch.isfinite(dx.float()).all() and torch.isfinite(dw.float()).all()
+    top = z.topk(2, dim=1).values
+    sure = (top[:, 0] - top[:, 1]) > 2 * zb + 100.0
+    sure &= z.argmax(dim=1) != t          # (p - 1 of a certain target is 0)
+    assert T < 60 or int(sure.sum()) >= T // 20
+    d = (torch.softmax(z, 1) - one) * dl.double()[:, None]
+    want = (d @ w.double())[sure]
+    gt = (2.0 ** -7 if dtype == BF else 2 * F) + 16 * F
+    err = (dx[sure].double() - want).norm(dim=1)
+    assert (err <= gt * want.norm(dim=1)).all()
+
+
 # ---------------------------------------------------------------------------
 # one workspace for several shapes and operators
 # ---------------------------------------------------------------------------

@@ -32,12 +32,11 @@ extern "C" {
  * MOE_ERR_TARGET on the device.
  *   MOE_CE_NONE: the losses of the tokens;  MOE_CE_SUM: their sum;
  *   MOE_CE_MEAN: the sum over the number of tokens that count (0 when none).
- * Precision: bf16 inputs on the tensor cores with fp32 sums; fp32 inputs as two
- * fp16 planes under one power of two for each matrix (22 mantissa bits for values
- * down to 2^-29 of the matrix's largest finite one, fewer below), fp32 sums;
- * statistics in fp32; the gradient of the logits is rounded to bf16 (fp32: to two
- * planes) as the operand of the two gradient products; dx and dw are rounded
- * once.
+ * Precision: bf16 inputs on the tensor cores with fp32 sums; fp32 inputs as three
+ * bf16 planes each (all 24 mantissa bits, any finite magnitude; an infinite element
+ * may give NaN where fp32 arithmetic gives an infinity), fp32 sums; statistics in
+ * fp32; the gradient of the logits is rounded to bf16 (fp32: to three planes) as the
+ * operand of the two gradient products; dx and dw are rounded once.
  * ------------------------------------------------------------------------- */
 typedef enum { MOE_CE_NONE = 0, MOE_CE_SUM = 1, MOE_CE_MEAN = 2 } moe_ce_reduction;
 

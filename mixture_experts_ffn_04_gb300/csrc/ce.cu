@@ -30,7 +30,7 @@ namespace {
 // 64 MiB 5768 us, 128 5613, 256 5525, 512 5478, all in one (1 GiB) 5446: each piece
 // costs a launch pair's tail, and larger ones only memory.
 constexpr int64_t kDlogitBytes = 512ll << 20;
-constexpr int64_t kPlaneBytes = 512ll << 20;    // fp16 planes of one piece of an fp32 W
+constexpr int64_t kPlaneBytes = 512ll << 20;    // planes of one piece of an fp32 W
 
 // the few-row forward: rows of x, warps a block, blocks an SM, shared memory of x
 constexpr int kSkinnyRows = 4, kSkinnyWarps = 8, kSkinnyPerSm = 4, kSkinnySmem = 112 * 1024;
@@ -80,7 +80,7 @@ moe_status decode_ce(const moe_ce_shape* s, CeShape* o, const char** why) {
   o->reduction = s->reduction;
   o->ignore = s->ignore_index;
   o->esize = s->dtype == MOE_F32 ? 4 : 2;
-  o->planes = s->dtype == MOE_F32 ? kPlanesHalf : 1;
+  o->planes = s->dtype == MOE_F32 ? kPlanesF32 : 1;
   return MOE_OK;
 }
 
@@ -116,7 +116,7 @@ CeLayout layout_ce(const CeShape& s) {
   const size_t T = (size_t)L.rows_pad;
   L.flags = take(256);   // status word; the few-row kernel's ticket at +32
   L.skinny = take(s.T <= kSkinnyRows ? (size_t)tc_sm_count() * kSkinnyPerSm * kSkinnyRows * 8 : 0);
-  L.meta = take(256);   // rows that count, the merge's ticket; +32 maxima (bits), +64 scales
+  L.meta = take(256);   // rows that count, the merge's ticket
   L.ctr = take((size_t)L.nctr * 4);
   L.rowmap = take(T * 4);
   L.inv = take(T * 4);
@@ -158,17 +158,13 @@ struct PrepArgs {
   float4* rowstat_c;
   int reduction;
   void* dx;   // zero the rows of tokens that do not count (direct dx), or NULL
-  // fp32: the bits of the largest finite |x| of tokens that count, |w| and (none
-  // reduced) |dloss|; the scales of the planes of x, w and d
-  const uint32_t* maxima;
-  float* scales;
 };
 
 __device__ __forceinline__ bool counts(int t, int V, int ignore) { return t != ignore && t >= 0 && t < V; }
 
 // Pack the tokens that count: block b takes rows_per_block tokens, counts those
 // before its own (a pass over the targets, which every block reads from L2) and
-// copies its rows -- bf16 as they are, fp32 as two fp16 planes.  Rows from the
+// copies its rows -- bf16 as they are, fp32 as planes.  Rows from the
 // count up to a multiple of 64 are zeroed: the dW product's last k-block reads
 // them.  Latency-bound at small T; at 8192 x 7168 bound by the copy.
 template <typename T>
@@ -230,17 +226,6 @@ __global__ void __launch_bounds__(256) ce_prep_kernel(const PrepArgs a) {
     if (threadIdx.x == 0) {
       *a.nrows = s_total;
       *a.ticket = 0;
-      if (sizeof(T) == 4) {
-        a.scales[0] = pow2_scale(a.maxima[0]);
-        a.scales[1] = pow2_scale(a.maxima[1]);
-        uint32_t d = a.maxima[2];
-        if (a.g && a.reduction != MOE_CE_NONE) {
-          float g = a.dloss ? a.dloss[0] : 1.0f;
-          if (a.reduction == MOE_CE_MEAN && s_total > 0) g /= (float)s_total;
-          d = __float_as_uint(fabsf(g));
-        }
-        a.scales[2] = pow2_scale(d);
-      }
     }
     for (int64_t i = threadIdx.x; i < a.nctr; i += blockDim.x) a.ctr[i] = 0;
   }
@@ -248,7 +233,6 @@ __global__ void __launch_bounds__(256) ce_prep_kernel(const PrepArgs a) {
   // copy the rows: a warp a row
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const T* x = reinterpret_cast<const T*>(a.x);
-  const float scale = sizeof(T) == 4 ? pow2_scale(a.maxima[0]) : 1.0f;
   const uint4 zero = make_uint4(0, 0, 0, 0);
   const int nv = a.H / 8;
   for (int r = warp; beg + r < end; r += 8) {
@@ -272,66 +256,21 @@ __global__ void __launch_bounds__(256) ce_prep_kernel(const PrepArgs a) {
         const float4 w = reinterpret_cast<const float4*>(src)[2 * v + 1];
         float f[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= scale;
-        reinterpret_cast<uint4*>(dst)[v] = pack_half8(f);
+        for (int pl = 0; pl < kPlanesF32; ++pl) {
+          float q[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = half_rest(f[e]);
-        reinterpret_cast<uint4*>(dst + a.plane * a.H)[v] = pack_half8(f);
+          for (int e = 0; e < 8; ++e) q[e] = take_plane(f[e]);
+          reinterpret_cast<uint4*>(dst + pl * a.plane * a.H)[v] = pack16(q, (const bf16*)nullptr);
+        }
       }
     }
   }
   const int total_rows = s_total, pad_end = (total_rows + 63) / 64 * 64;
-  const int planes = sizeof(T) == 2 ? 1 : kPlanesHalf;
+  const int planes = sizeof(T) == 2 ? 1 : kPlanesF32;
   for (int r = total_rows + blockIdx.x; r < pad_end; r += gridDim.x)
     for (int pl = 0; pl < planes; ++pl)
       for (int v = threadIdx.x; v < nv; v += blockDim.x)
         reinterpret_cast<uint4*>(a.xc + (pl * a.plane + r) * a.H)[v] = zero;
-}
-
-// Largest finite absolute values, as bits: of the rows of x that count, of w, and
-// of dloss where it is per token (its rows that count).  A warp a row; bound by
-// the read of w.
-__global__ void __launch_bounds__(256) ce_max_kernel(const float* __restrict__ x, int64_t x_ld, int64_t T,
-                                                     const float* __restrict__ w, int64_t w_ld, int V, int H,
-                                                     const int32_t* __restrict__ target, int ignore,
-                                                     const float* __restrict__ dloss, uint32_t* maxima) {
-  pdl_trigger();
-  pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
-  uint32_t mx = 0, mw = 0, md = 0;
-  auto take = [](uint32_t& m, float v) {
-    const uint32_t b = __float_as_uint(fabsf(v));
-    if (b < 0x7F800000u && b > m) m = b;
-  };
-  for (int64_t r = blockIdx.x * (int64_t)(blockDim.x >> 5) + (threadIdx.x >> 5); r < T + V; r += warps) {
-    const bool of_x = r < T;
-    if (of_x && !counts(target[r], V, ignore)) continue;
-    const float4* p = reinterpret_cast<const float4*>(of_x ? x + r * x_ld : w + (r - T) * w_ld);
-    uint32_t m = 0;
-#pragma unroll 4
-    for (int i = lane; i < H / 4; i += 32) {
-      const float4 v = p[i];
-      take(m, v.x);
-      take(m, v.y);
-      take(m, v.z);
-      take(m, v.w);
-    }
-    if (of_x) {
-      mx = max(mx, m);
-      if (dloss && lane == 0) take(md, dloss[r]);
-    } else {
-      mw = max(mw, m);
-    }
-  }
-  mx = __reduce_max_sync(0xffffffffu, mx);
-  mw = __reduce_max_sync(0xffffffffu, mw);
-  md = __reduce_max_sync(0xffffffffu, md);
-  if (lane == 0) {
-    if (mx) atomicMax(maxima, mx);
-    if (mw) atomicMax(maxima + 1, mw);
-    if (md) atomicMax(maxima + 2, md);
-  }
 }
 
 // Maximum M and sum of exponentials S joined with another pair's.
@@ -596,28 +535,14 @@ cudaError_t launch_skinny(const SkinnyArgs& a, cudaStream_t st) {
 // whatever T is), us at H = 2048, V = 50257 and H = 7168, V = 32768:
 //   bf16  T = 1: 38 / 59, 78 / 114   T = 2: 47 / 60, 98 / 114   T = 4: 59 / 59, 135 / 115
 //   fp32  T = 1: 67 / 328, 148 / 731                            T = 4: 77 / 329, 206 / 730
-// (fp32 W goes through its maximum and its planes first): two rows in bf16, four in
+// (fp32 W goes through its planes first): two rows in bf16, four in
 // fp32.
 bool skinny_ok(const CeShape& s) {
   const int64_t most = s.dtype == MOE_F32 ? kSkinnyRows : 2;
   return s.T >= 1 && s.T <= most && (size_t)(s.T <= 2 ? s.T : 4) * s.H * 4 <= (size_t)kSkinnySmem;
 }
 
-cudaError_t run_prep(const CeShape& s, const CeLayout& L, char* ws, PrepArgs& p, const void* w,
-                     cudaStream_t st) {
-  if (s.dtype == MOE_F32) {
-    uint32_t* maxima = reinterpret_cast<uint32_t*>(ws + L.meta + 32);
-    cudaError_t e = cudaMemsetAsync(maxima, 0, 12, st);
-    if (e != cudaSuccess) return e;
-    const int64_t rows = s.T + s.V;
-    const unsigned blocks = (unsigned)std::min<int64_t>((rows + 7) / 8, 8 * tc_sm_count());
-    e = launch_after(ce_max_kernel, blocks, 256, 0, st, 1, reinterpret_cast<const float*>(p.x), s.x_ld, s.T,
-                     reinterpret_cast<const float*>(w), s.w_ld, s.V, s.H, p.target, s.ignore,
-                     s.reduction == MOE_CE_NONE ? p.dloss : nullptr, maxima);
-    if (e != cudaSuccess) return e;
-    p.maxima = maxima;
-    p.scales = reinterpret_cast<float*>(ws + L.meta + 64);
-  }
+cudaError_t run_prep(const CeShape& s, const CeLayout& L, char* ws, PrepArgs& p, cudaStream_t st) {
   p.T = s.T;
   // a warp a token up to 8192 tokens, then up to 32
   int64_t rpb = ((s.T + 1023) / 1024 + 7) / 8 * 8;
@@ -657,8 +582,8 @@ cudaError_t piece_operand(const CeShape& s, const CeLayout& L, char* ws, const v
   }
   const int64_t have = std::min<int64_t>(vcols, s.V - v0);
   *o = {ws + L.wpl, s.H, L.piece, vcols, 0};
-  return launch_halves(reinterpret_cast<const float*>(w) + v0 * s.w_ld, s.w_ld, have, vcols, s.H,
-                       ws + L.wpl, L.piece, reinterpret_cast<const uint32_t*>(ws + L.meta + 32) + 1, st);
+  return launch_planes(reinterpret_cast<const float*>(w) + v0 * s.w_ld, s.w_ld, have, vcols, s.H,
+                       ws + L.wpl, L.piece, st);
 }
 
 // Statistics of the packed rows over the whole vocabulary, and their merge into the
@@ -677,7 +602,6 @@ cudaError_t run_stats(const CeShape& s, const CeLayout& L, char* b, const PrepAr
     if (e != cudaSuccess) return e;
     LogitsArgs a = {};
     a.planes = s.planes;
-    a.scale = p.scales;
     a.x = b + L.xc;
     a.x_ld = s.H;
     a.x_plane = L.rows_pad;
@@ -775,7 +699,7 @@ extern "C" moe_status moe_linear_ce_forward(const moe_ce_shape* shape, const voi
   p.loss = loss;
   p.lse_out = lse;
   p.stats_out = reinterpret_cast<float4*>(stats);
-  CHECK_CUDA(run_prep(s, L, b, p, w, st));
+  CHECK_CUDA(run_prep(s, L, b, p, st));
   CHECK_CUDA(run_stats(s, L, b, p, w, p.rowmap, loss, lse, reinterpret_cast<float4*>(stats), total, st));
   return MOE_OK;
 }
@@ -807,7 +731,7 @@ extern "C" moe_status moe_linear_ce_backward(const moe_ce_shape* shape, const vo
   p.g = reinterpret_cast<float*>(b + L.g);
   p.rowstat_c = reinterpret_cast<float4*>(b + L.rowstat);
   p.dx = L.dx_direct ? dx : nullptr;
-  CHECK_CUDA(run_prep(s, L, b, p, w, st));
+  CHECK_CUDA(run_prep(s, L, b, p, st));
   // The few-row forward adds up its logits in an order of its own, so its statistics
   // are not those of the tiles below: they are taken again.
   if (skinny_ok(s)) CHECK_CUDA(run_stats(s, L, b, p, w, nullptr, nullptr, nullptr, p.rowstat_c, nullptr, st));
@@ -820,7 +744,6 @@ extern "C" moe_status moe_linear_ce_backward(const moe_ce_shape* shape, const vo
     CHECK_CUDA(piece_operand(s, L, b, w, v0, vcols, &o, st));
     LogitsArgs a = {};
     a.planes = s.planes;
-    a.scale = p.scales;
     a.x = b + L.xc;
     a.x_ld = s.H;
     a.x_plane = L.rows_pad;
@@ -847,7 +770,6 @@ extern "C" moe_status moe_linear_ce_backward(const moe_ce_shape* shape, const vo
     CHECK_CUDA(launch_linear_logits(a, st));
     LinearGradArgs q = {};
     q.planes = s.planes;
-    q.scale = p.scales;
     q.d = b + L.d;
     q.d_ld = L.piece;
     q.d_plane = L.rows_pad;

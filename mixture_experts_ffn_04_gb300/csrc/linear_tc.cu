@@ -29,10 +29,8 @@
 // nearest, which frees the accumulator as soon as it is read.  Chunks of 512 for
 // logits and all fp32 products, 4096 for gradients that are rounded to bf16 anyway.
 //
-// fp32 operands come in planes (train.h).  Three bf16 planes: a tile's k-loop runs
-// over the six plane products whose weight is above 2^-24, smallest first.  Two
-// fp16 planes: the two cross products first, then, after their sum in the
-// registers is scaled by 2^-11, the product of the high planes; half the MMAs.
+// fp32 operands come in three bf16 planes (train.h): a tile's k-loop runs over the
+// six plane products whose weight is above 2^-24, smallest first.
 //
 // Measured under a full clock: statistics 1.71 PFLOP/s (T = 4096, H = 2048, V =
 // 131072), the logit gradient 1.76, the gradient products 1.87, against 1.91 for the
@@ -88,17 +86,15 @@ static_assert((2 * S + 5 + 2 * NSLOT + EPI_WARPS) * 8 + 8 + NSLOT * 32 <= BAR_BY
 constexpr int kGroupM = 8;
 constexpr int kChunkExact = 8, kChunkBf16 = 64;   // k-blocks of 64
 
-// kind::f16: D fp32, A and B fp16 (IDESC_BF16: both bf16), M = 256 over the pair,
-// N = 256.
-constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
-constexpr uint32_t IDESC_BF16 = (1u << 7) | (1u << 10);
+// kind::f16: D fp32, A and B bf16, M = 256 over the pair, N = 256.
+constexpr uint32_t IDESC = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) |
+                           ((uint32_t)(BM >> 4) << 24);
 constexpr uint32_t IDESC_A_MN = 1u << 15, IDESC_B_MN = 1u << 16;
 
 enum Kind { kStats = 0, kDlogit = 1, kGrad = 2, kProduct = 3 };
 
 struct Args {
   int hidden, planes;
-  const float* scale;
   int64_t v0, w_v0, vcols, vocab;
   const int32_t* nrows;
   int64_t rows_bound;
@@ -171,12 +167,10 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t saddr) {
   return d;
 }
 
-// Plane products in ascending weight: (0,2) (2,0) (1,1) (0,1) (1,0) (0,0); of two
-// planes the last three.
+// Plane products in ascending weight: (0,2) (2,0) (1,1) (0,1) (1,0) (0,0).
 __device__ __forceinline__ void plane_pair(int planes, int i, int& pa, int& pb) {
   if (planes == 1) { pa = pb = 0; return; }
   if (planes == kPlanesD2) { pa = 1 - i; pb = 0; return; }
-  if (planes == kPlanesHalf) i += 3;
   const int t = i == 0 ? 0x02 : i == 1 ? 0x20 : i == 2 ? 0x11 : i == 3 ? 0x01 : i == 4 ? 0x10 : 0x00;
   pa = t >> 4;
   pb = t & 15;
@@ -414,9 +408,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   pdl_wait();   // barriers, TMEM and descriptors are set up under the kernel before
   Plan<KIND> plan;
   plan.init(a);
-  const int nprod = a.planes == 1 ? 1 : a.planes == kPlanesD2 ? 2 : a.planes == kPlanesHalf ? 3 : 6;
-  // steps of the fp16 cross products, which are summed and scaled by themselves
-  const int ncross = a.planes == kPlanesHalf ? 2 : 0;
+  const int nprod = a.planes == 1 ? 1 : a.planes == kPlanesD2 ? 2 : 6;
 
   // Tile n of this pair (type -1 when there is none left, or a wait ran out).
   // The even CTA's producer takes it, one ahead, from the counter, decodes it and
@@ -551,11 +543,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       const Tile t = read_tile(n);
       if (t.type < 0) break;
       const int steps = (t.kb1 - t.kb0) * nprod;   // 0 without rows: the epilogue writes zeros
-      const int cross = (t.kb1 - t.kb0) * ncross;
-      const uint32_t idesc = IDESC | (a.planes == kPlanesHalf ? 0u : IDESC_BF16) |
-                             (t.type == 2 ? IDESC_A_MN : 0u) | (t.type != 0 ? IDESC_B_MN : 0u);
-      for (int i0 = 0, i1; i0 < steps && ok; i0 = i1) {
-        i1 = min(i0 < cross ? cross : steps, i0 + a.chunk);
+      const uint32_t idesc = IDESC | (t.type == 2 ? IDESC_A_MN : 0u) | (t.type != 0 ? IDESC_B_MN : 0u);
+      for (int i0 = 0; i0 < steps && ok; i0 += a.chunk) {
+        const int i1 = min(steps, i0 + a.chunk);
         if (!wait_cl(tempty(acc), aph ^ 1u, abort_flag)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d = tmem_base + (uint32_t)acc * BN;
@@ -694,14 +684,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       if (!fit) break;
       bool ok = true;
-      const int cross = (t.kb1 - t.kb0) * ncross;
 #pragma unroll 1
-      for (int i0 = 0, i1; i0 < steps; i0 = i1) {
-        i1 = min(i0 < cross ? cross : steps, i0 + a.chunk);
-        if (i0 == cross && cross > 0) {
-#pragma unroll
-          for (int j = 0; j < BN / 2; ++j) f[j] *= 1.0f / kHalfLow;
-        }
+      for (int i0 = 0; i0 < steps; i0 += a.chunk) {
         int w = 1;
         if (lane == 0) w = wait_cl(tfull(acc), aph, abort_flag) ? 1 : 0;
         ok = __shfl_sync(0xffffffffu, w, 0);
@@ -727,14 +711,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (acc == 0) aph ^= 1u;
       }
       if (!ok) break;
-      if (a.planes == kPlanesHalf) {
-        // the operands' scales, powers of two (two factors: their product may
-        // leave the range)
-        const float r0 = pow2_recip(a.scale[is_dx || KIND != kGrad ? 1 : 0]);
-        const float r1 = pow2_recip(a.scale[KIND != kGrad ? 0 : 2]);
-#pragma unroll
-        for (int j = 0; j < BN / 2; ++j) f[j] = f[j] * r0 * r1;
-      }
       if (KIND == kStats) {
         // maximum of the row over this half of the tile and the sum of e^(z - maximum).
         // The difference is taken before the factor log2 e: a half tile of masked
@@ -786,30 +762,19 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int j = 0; j < BN / 2; ++j) f[j] = live && j < left ? f[j] : 0.0f;
         }
-        if (a.planes == 1) {
 #pragma unroll
-          for (int c = 0; c < BN / 2; c += 64) {
+        for (int c = 0; c < BN / 2; c += 64) {
+          for (int pl = 0; pl < a.planes; ++pl) {
             stage_free(lane);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) put_piece(stage, lane, j, pack16(f + c + 8 * j, (const bf16*)nullptr));
-            stage_out(&tmOx, stage, lane, t.nt * BN + c_lo + c, (int)row0, false);
-          }
-        } else {
-          const float sd = a.scale[2];
+            for (int j = 0; j < 8; ++j) {
+              float q[8];
 #pragma unroll
-          for (int c = 0; c < BN / 2; c += 64) {
-#pragma unroll
-            for (int j = 0; j < 64; ++j) f[c + j] *= sd;
-            stage_free(lane);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) put_piece(stage, lane, j, pack_half8(f + c + 8 * j));
-            stage_out(&tmOx, stage, lane, t.nt * BN + c_lo + c, (int)row0, false);
-#pragma unroll
-            for (int j = 0; j < 64; ++j) f[c + j] = half_rest(f[c + j]);
-            stage_free(lane);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) put_piece(stage, lane, j, pack_half8(f + c + 8 * j));
-            stage_out(&tmOx, stage, lane, t.nt * BN + c_lo + c, (int)(a.d_plane + row0), false);
+              for (int e = 0; e < 8; ++e)
+                q[e] = pl + 1 < a.planes ? take_plane(f[c + 8 * j + e]) : f[c + 8 * j + e];
+              put_piece(stage, lane, j, pack16(q, (const bf16*)nullptr));
+            }
+            stage_out(&tmOx, stage, lane, t.nt * BN + c_lo + c, (int)(pl * a.d_plane + row0), false);
           }
         }
       } else if (KIND == kProduct) {
@@ -915,15 +880,6 @@ __global__ void __launch_bounds__(256) reduce_parts_kernel(const float* __restri
   }
 }
 
-__device__ __forceinline__ void split3(float v, float& p0, float& p1, float& p2) {
-  p0 = __bfloat162float(__float2bfloat16_rn(v));
-  p1 = v - p0;
-  if (!isfinite(p1)) p1 = 0.0f;
-  const float q1 = __bfloat162float(__float2bfloat16_rn(p1));
-  p2 = p1 - q1;
-  p1 = q1;
-}
-
 __global__ void __launch_bounds__(256) planes_kernel(const float* __restrict__ src, int64_t ld,
                                                      int64_t rows, int64_t rows_zero, int hidden,
                                                      bf16* __restrict__ dst, int64_t plane) {
@@ -941,7 +897,11 @@ __global__ void __launch_bounds__(256) planes_kernel(const float* __restrict__ s
       const float4 v = *reinterpret_cast<const float4*>(src + r * ld + j0 + 4);
       const float w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) split3(w[e], f[0][e], f[1][e], f[2][e]);
+      for (int e = 0; e < 8; ++e) {
+        float v = w[e];
+#pragma unroll
+        for (int p = 0; p < 3; ++p) f[p][e] = take_plane(v);
+      }
     } else {
 #pragma unroll
       for (int p = 0; p < 3; ++p)
@@ -951,35 +911,6 @@ __global__ void __launch_bounds__(256) planes_kernel(const float* __restrict__ s
 #pragma unroll
     for (int p = 0; p < 3; ++p)
       *reinterpret_cast<uint4*>(dst + (p * plane + r) * hidden + j0) = pack16(f[p], (const bf16*)nullptr);
-  }
-}
-
-__global__ void __launch_bounds__(256) halves_kernel(const float* __restrict__ src, int64_t ld,
-                                                     int64_t rows, int64_t rows_zero, int hidden,
-                                                     uint16_t* __restrict__ dst, int64_t plane,
-                                                     const uint32_t* __restrict__ max) {
-  pdl_trigger();
-  pdl_wait();
-  const float s = pow2_scale(*max);
-  const int per_row = hidden / 8;
-  const int64_t items = rows_zero * per_row;
-  for (int64_t it = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; it < items;
-       it += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t r = it / per_row;
-    const int j0 = (int)(it - r * per_row) * 8;
-    float f[8], l[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = 0.0f;
-    if (r < rows) {
-      const float4 u = __ldcs(reinterpret_cast<const float4*>(src + r * ld + j0));
-      const float4 v = __ldcs(reinterpret_cast<const float4*>(src + r * ld + j0 + 4));
-      f[0] = u.x * s; f[1] = u.y * s; f[2] = u.z * s; f[3] = u.w * s;
-      f[4] = v.x * s; f[5] = v.y * s; f[6] = v.z * s; f[7] = v.w * s;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) l[e] = half_rest(f[e]);
-    *reinterpret_cast<uint4*>(dst + r * hidden + j0) = pack_half8(f);
-    *reinterpret_cast<uint4*>(dst + (plane + r) * hidden + j0) = pack_half8(l);
   }
 }
 
@@ -1133,7 +1064,6 @@ cudaError_t launch_linear_logits(const LogitsArgs& a, cudaStream_t st) {
   Args t = {};
   t.hidden = a.hidden;
   t.planes = a.planes;
-  t.scale = a.scale;
   t.v0 = a.v0;
   t.w_v0 = a.w_v0;
   t.vcols = a.vcols;
@@ -1209,7 +1139,6 @@ cudaError_t launch_linear_grad(const LinearGradArgs& a, cudaStream_t st) {
   Args t = {};
   t.hidden = a.hidden;
   t.planes = a.planes;
-  t.scale = a.scale;
   t.v0 = a.v0;
   t.w_v0 = a.w_v0;
   t.vcols = a.vcols;
@@ -1239,7 +1168,7 @@ cudaError_t launch_linear_grad(const LinearGradArgs& a, cudaStream_t st) {
   t.wide_dx = a.hidden * (a.out_f32 ? 4 : 2) % 32 == 0 && aligned32(a.dx);
   t.want_dx = a.dx_part != nullptr || a.dx != nullptr;
   t.want_dw = a.dw_part != nullptr || a.dw != nullptr;
-  if (a.dx_add && (a.rowmap || a.planes == kPlanesHalf)) return cudaErrorInvalidValue;
+  if (a.dx_add && a.rowmap) return cudaErrorInvalidValue;
   if ((t.want_dx && t.ks_dx > 1 && !a.dx_part) || (t.want_dw && t.ks_dw > 1 && !a.dw_part))
     return cudaErrorInvalidValue;
   const int64_t nth = (a.hidden + BN - 1) / BN;
@@ -1274,13 +1203,6 @@ cudaError_t launch_planes(const float* src, int64_t ld, int64_t rows, int64_t ro
   if (rows_zero <= 0) return cudaSuccess;
   return launch_after(lin::planes_kernel, lin::elementwise_grid(rows_zero * (hidden / 8)), 256, 0, st, 1, src, ld,
                       rows, rows_zero, hidden, reinterpret_cast<bf16*>(dst), plane);
-}
-
-cudaError_t launch_halves(const float* src, int64_t ld, int64_t rows, int64_t rows_zero, int hidden,
-                          void* dst, int64_t plane, const uint32_t* max, cudaStream_t st) {
-  if (rows_zero <= 0) return cudaSuccess;
-  return launch_after(lin::halves_kernel, lin::elementwise_grid(rows_zero * (hidden / 8)), 256, 0, st, 1, src, ld,
-                      rows, rows_zero, hidden, reinterpret_cast<uint16_t*>(dst), plane, max);
 }
 
 }  // namespace moe

@@ -3,12 +3,12 @@
 // small kernels around them.
 #pragma once
 
-#ifdef __CUDACC__
-#include <cuda_fp16.h>
-#endif
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#ifdef __CUDACC__
+#include "common.cuh"
+#endif
 #include "internal.h"
 
 namespace moe {
@@ -46,43 +46,27 @@ cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned block, si
 }
 #endif
 
-// fp32 operands go through the 16-bit tensor cores in planes, stacked `plane`
-// rows apart in one matrix:
-//  * three bf16 planes, x = x0 + x1 + x2 (8 mantissa bits each), any range, six
-//    products;
-//  * two fp16 planes, x s = h + l 2^-11 with one power of two s for the matrix
-//    that brings its largest finite value to [2^14, 2^15): 22 mantissa bits down
-//    to 2^-29 of the largest, three products.
+// fp32 operands go through the bf16 tensor cores as three bf16 planes, x = x0 + x1 +
+// x2 exactly (8 mantissa bits each, the range of fp32), stacked `plane` rows apart in
+// one matrix; a product takes the six plane products above 2^-24.  Not two fp16 planes
+// under a scale for the matrix, which need half the products: values 2^-50 below the
+// matrix's largest vanish in them, which a masked row of 1e15, a rare column's
+// gradient or a large feature that meets zeros does to all the rest, whatever the
+// scale is taken over.
 // bf16 gradients can keep D in two bf16 planes against one of x and w (two
 // products): D's rounding, half of the gradients' error, then vanishes.
-constexpr int kPlanesF32 = 3, kPlanesHalf = 2, kPlanesD2 = 4;
+constexpr int kPlanesF32 = 3, kPlanesD2 = 4;
 
 #ifdef __CUDACC__
-constexpr float kHalfLow = 2048.0f;   // scale of the low plane against the high one
-// The power of two for a largest absolute value, given as its bits (a value that
-// is not finite or zero: 1), and its reciprocal.
-__device__ __forceinline__ float pow2_scale(uint32_t bits) {
-  if (bits == 0u || bits >= 0x7F800000u) return 1.0f;
-  int s = 14 - ilogbf(__uint_as_float(bits));
-  s = s > 126 ? 126 : (s < -126 ? -126 : s);
-  return __uint_as_float((uint32_t)(s + 127) << 23);
-}
-__device__ __forceinline__ float pow2_recip(float s) {
-  return __uint_as_float((254u << 23) - __float_as_uint(s));
-}
-// What the high plane leaves for the low one (0 where it is not finite).
-__device__ __forceinline__ float half_rest(float v) {
-  const float r = (v - __half2float(__float2half_rn(v))) * kHalfLow;
-  return isfinite(r) ? r : 0.0f;
-}
-__device__ __forceinline__ uint4 pack_half8(const float* f) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+// The next plane of v, which keeps the rest (none where the plane is not finite).  A
+// finite value that would round to infinity takes the largest bf16 value instead:
+// infinity times a zero on the other side would be NaN.
+__device__ __forceinline__ float take_plane(float& v) {
+  float p = __bfloat162float(__float2bfloat16_rn(v));
+  if (fabsf(p) == INFINITY && fabsf(v) != INFINITY) p = copysignf(__uint_as_float(0x7F7F0000u), v);
+  const float r = v - p;
+  v = isfinite(r) ? r : 0.0f;
+  return p;
 }
 #endif
 
@@ -97,8 +81,7 @@ struct LinearSplit {
 LinearSplit linear_grad_split(int64_t rows, int64_t vocab, int hidden, int planes);
 
 struct LogitsArgs {
-  int planes;              // 1: bf16 operands, kPlanesHalf: fp32 in fp16 planes
-  const float* scale;      // kPlanesHalf: device, the scales of x, w and d
+  int planes;              // 1: bf16 operands, kPlanesF32: fp32 in planes
   const void* x;           // bf16 [planes * x_plane, x_ld], rows of `hidden`
   int64_t x_ld, x_plane;
   const void* w;           // bf16 [planes * w_plane, w_ld]
@@ -147,8 +130,7 @@ int linear_product_split(int64_t rows, int64_t cols, int hidden);
 cudaError_t launch_linear_product(const ProductArgs& a, cudaStream_t st);
 
 struct LinearGradArgs {
-  int planes;              // 1, kPlanesD2, kPlanesHalf or kPlanesF32
-  const float* scale;      // kPlanesHalf: device, the scales of x, w and d
+  int planes;              // 1, kPlanesD2 or kPlanesF32
   const void* d;           // bf16 [planes * d_plane, d_ld]: d [rows, vcols]
   int64_t d_ld, d_plane;
   const void* x;           // bf16 [planes * x_plane, x_ld]; rows past the count
@@ -186,15 +168,10 @@ cudaError_t launch_reduce_parts(const float* part, int splits, int64_t part_stri
                                 int hidden, const int32_t* inv, const void* add, void* out,
                                 int out_f32, cudaStream_t st);
 
-// Rows of fp32 as bf16 planes (or bf16 rows copied): dst [planes][plane][hidden];
-// rows past `rows` up to `rows_zero` are zeros.
+// Rows of fp32 as three bf16 planes: dst [3][plane][hidden]; rows past `rows` up to
+// `rows_zero` are zeros.
 cudaError_t launch_planes(const float* src, int64_t ld, int64_t rows, int64_t rows_zero, int hidden,
                           void* dst, int64_t plane, cudaStream_t st);
-
-// The same as two fp16 planes; max: device, the bits of the matrix's largest
-// finite absolute value.
-cudaError_t launch_halves(const float* src, int64_t ld, int64_t rows, int64_t rows_zero, int hidden,
-                          void* dst, int64_t plane, const uint32_t* max, cudaStream_t st);
 
 int linear_clusters();   // clusters of two SMs the device runs at once
 

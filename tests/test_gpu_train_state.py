@@ -40,11 +40,106 @@ def make(T, H, V, seed):
 
 
 # ---------------------------------------------------------------------------
+# cross entropy in fp32: magnitudes that differ within a matrix
+# ---------------------------------------------------------------------------
+def compare(x, w, t, dl, columns, rows):
+    """Loss, lse, dx and dw with weights per token; `columns` of w are not masked,
+    `rows` of x have ordinary logits."""
+    T, H = x.shape
+    V = w.shape[0]
+    op = m.LinearCrossEntropy(T, H, V, dtype=FP, reduction="none", ignore_index=IGNORE)
+    loss = op.forward(x, w, t)
+    dx, dw = op.backward(x, w, t, dl)
+    xd, wd = x[rows].double(), w[columns].double()
+    z = xd @ wd.t()
+    at = torch.full((V,), -1, device="cuda")
+    at[columns] = torch.arange(len(columns), device="cuda")
+    tt = at[t[rows].long()]
+    assert (tt >= 0).all()
+    one = torch.nn.functional.one_hot(tt, len(columns)).double()
+    lse = torch.logsumexp(z, 1)
+    d = (torch.softmax(z, 1) - one) * dl[rows].double()[:, None]
+    # entries that meet zeros on the other side add nothing to a logit
+    live = (wd != 0).any(0), (xd != 0).any(0)
+    zb = 8 * math.sqrt(H) * F * float((xd * live[0]).norm(dim=1).max() * (wd * live[1]).norm(dim=1).max())
+    zb += 16 * F * float(z.abs().max())
+    tol = 2 * zb + 8 * F * float(lse.abs().max())
+    assert float((op.lse[rows].double() - lse).abs().max()) <= tol
+    assert float((loss[rows].double() - (lse - (z * one).sum(1))).abs().max()) <= tol
+    gt = 2 * F + 4 * zb + 16 * F
+    assert torch.isfinite(dx[rows]).all() and torch.isfinite(dw).all()
+    return d, dx, dw, xd, wd, gt
+
+
+@pytest.mark.parametrize("value", [1e9, 1e15, 1e30, -torch.finfo(FP).min])
+@pytest.mark.parametrize("T", [2, 5, 60, 300])
+def test_fp32_masked_rows_of_w(T, value):
+    """Rows of w that send their column's logit to -value through one feature."""
+    H, V = 72, 700
+    x, w, t, dl = make(T, H, V, 31)
+    x[:, 3] = 1.0
+    columns = torch.ones(V, dtype=torch.bool, device="cuda")
+    columns[torch.tensor([0, 100, 101, 255, 256, 699], device="cuda")] = False
+    columns[384:512] = False         # all the columns of a half tile
+    w[~columns] = 0.0
+    w[~columns, 3] = -value
+    columns = columns.nonzero().flatten()
+    t = columns[t.long() % len(columns)].to(torch.int32)
+    rows = torch.arange(T, device="cuda")
+    d, dx, dw, xd, wd, gt = compare(x, w, t, dl, columns, rows)
+    want = d @ wd
+    assert float((dx.double() - want).norm()) <= gt * float(want.norm())
+    want = d.t() @ xd
+    assert float((dw[columns].double() - want).norm()) <= gt * float(want.norm())
+    gone = torch.ones(V, dtype=torch.bool, device="cuda")
+    gone[columns] = False
+    assert (dw[gone] == 0).all()
+
+
+@pytest.mark.parametrize("value", [1e9, 1e15, 1e30])
+@pytest.mark.parametrize("T", [5, 130])
+def test_fp32_row_and_feature_of_x_far_above_the_rest(T, value):
+    """A token of huge magnitude that is not learned from (weight 0), and a huge
+    feature that no row of w reads: the other tokens keep their digits."""
+    H, V = 136, 515
+    x, w, t, dl = make(T, H, V, 32)
+    x[3] *= value
+    dl[3] = 0.0
+    x[:, 7] = value
+    w[:, 7] = 0.0
+    rows = torch.arange(T, device="cuda") != 3
+    rows = rows.nonzero().flatten()
+    d, dx, dw, xd, wd, gt = compare(x, w, t, dl, torch.arange(V, device="cuda"), rows)
+    want = d @ wd
+    assert float((dx[rows].double() - want).norm()) <= gt * float(want.norm())
+    assert (dx[3] == 0).all()
+    # the huge feature's own gradients are huge: the others by themselves
+    keep = torch.arange(H, device="cuda") != 7
+    want = (d.t() @ xd)[:, keep]
+    assert float((dw[:, keep].double() - want).norm()) <= gt * float(want.norm())
+
+
+def test_fp32_gradient_of_rare_columns():
+    """A column whose probability is about 1e-13 at every token: its row of dw has
+    all its digits, not those that are left next to 1."""
+    T, H, V = 64, 64, 300
+    x, w, t, dl = make(T, H, V, 33)
+    x[:, 5] = 1.0
+    w[200, 5] -= 30.0
+    t[t == 200] = 7
+    rows = torch.arange(T, device="cuda")
+    d, dx, dw, xd, wd, gt = compare(x, w, t, dl, torch.arange(V, device="cuda"), rows)
+    want = (d.t() @ xd)[200]
+    assert 0 < float(want.norm()) < 1e-9
+    assert float((dw[200].double() - want).norm()) <= gt * float(d[:, 200].norm() * torch.linalg.matrix_norm(xd, 2))
+
+
+# ---------------------------------------------------------------------------
 # logits far from zero
 # ---------------------------------------------------------------------------
 @pytest.mark.parametrize("value", [1e4, 1e8, 1e12, 1e25])
 @pytest.mark.parametrize("T", [2, 60, 300])
-@pytest.mark.parametrize("dtype", [BF])
+@pytest.mark.parametrize("dtype", [BF, FP])
 def test_masked_half_tiles(T, value, dtype):
     """All of 128 and of 256 neighbouring columns at logits of -value (a padded
     vocabulary): the exponentials of such a group's own differences from its

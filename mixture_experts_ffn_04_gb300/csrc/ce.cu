@@ -106,7 +106,7 @@ CeLayout layout_ce(const CeShape& s) {
   L.split = linear_grad_split(s.T, L.piece, s.H, s.planes);
   L.dx_direct = L.npieces == 1 && L.split.dx == 1;
   L.dw_direct = L.split.dw == 1;
-  L.nctr = 3 * L.npieces;   // statistics, logit gradient, gradients of each piece
+  L.nctr = 2 * L.npieces;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -333,11 +333,12 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
         merge_ms(M, S, v.x, v.y);
       }
       const RowStat r = finish_row(M, S, zt[row]);
-      const int64_t t = rowmap ? rowmap[row] : row;   // NULL: the rows stay packed
+      const float each = r.loss;
+      const int t = rowmap[row];
       if (lse) lse[t] = r.lse;
       if (rowstat) rowstat[t] = r.stat;
-      if (loss) loss[t] = r.loss;
-      loss_c[row] = r.loss;
+      if (loss) loss[t] = each;
+      loss_c[row] = each;
     }
     __syncthreads();
   }
@@ -364,12 +365,76 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   }
 }
 
-// Loss of at most R = 4 rows in one launch: W streams by once, a warp takes NV
-// vocabulary rows at a time (all lanes across the row, 16 bytes a load) against
-// the rows of x in shared memory (fp32), keeps a running maximum and sum per row
-// of x, and the last block merges the blocks.  Bound by HBM: one token against
-// 50257 x 2048 bf16 reads 206 MB in 38 us, 5.4 TB/s (0.80 of the copy); with two
-// blocks an SM instead of four it took 63 (too few loads in flight).
+// The logits of at most four rows against vocabulary rows v .. vend: a warp takes NV
+// rows of W at a time (all lanes across the row, 16 bytes a load) against the rows of
+// x in shared memory (fp32).  Forward and backward both call it: the same sums in the
+// same order, so the backward's logits are those of the statistics.
+template <typename T, int R, int NV, typename F>
+__device__ __forceinline__ void skinny_logits(const T* w, int64_t w_ld, const float* s_x, int H, int64_t v,
+                                              int64_t vend, F&& take) {
+  constexpr int N = Vec16<T>::N;
+  const int lane = threadIdx.x & 31;
+  for (; v < vend; v += NV) {
+    float acc[NV][R];
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+      for (int r = 0; r < R; ++r) acc[k][r] = 0.0f;
+    const T* wr[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) wr[k] = w + min(v + k, vend - 1) * w_ld;
+#pragma unroll 4
+    for (int i = lane * N; i < H; i += 32 * N) {
+      uint4 u[NV];
+#pragma unroll
+      for (int k = 0; k < NV; ++k) u[k] = __ldcs(reinterpret_cast<const uint4*>(wr[k] + i));
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        float f[N];
+        unpack16(u[k], f, (const T*)nullptr);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int e = 0; e < N; e += 4) {
+            const float4 xv = *reinterpret_cast<const float4*>(s_x + r * H + i + e);
+            acc[k][r] = fmaf(f[e], xv.x, acc[k][r]);
+            acc[k][r] = fmaf(f[e + 1], xv.y, acc[k][r]);
+            acc[k][r] = fmaf(f[e + 2], xv.z, acc[k][r]);
+            acc[k][r] = fmaf(f[e + 3], xv.w, acc[k][r]);
+          }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float z = acc[k][r];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        if (v + k < vend) take(v + k, r, z);
+      }
+  }
+}
+
+// A row's target, or -1 where it does not count, and its x into shared memory (zeros
+// where it does not count, whatever x holds).
+template <typename T, int R>
+__device__ __forceinline__ void skinny_rows(const T* x, int64_t x_ld, const int32_t* target, int rows, int H,
+                                            int V, int ignore, float* s_x, int* tg) {
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    tg[r] = r < rows ? target[r] : ignore;
+    if (!counts(tg[r], V, ignore)) tg[r] = -1;
+    const T* xr = x + r * x_ld;
+    for (int i = threadIdx.x; i < H; i += blockDim.x) s_x[r * H + i] = tg[r] >= 0 ? to_f(xr[i]) : 0.0f;
+  }
+  __syncthreads();
+}
+
+// Loss of at most R = 4 rows in one launch: W streams by once, a running maximum and
+// sum per row of x, and the last block merges the blocks.  Bound by HBM: one token
+// against 50257 x 2048 bf16 reads 206 MB in 38 us, 5.4 TB/s (0.80 of the copy); with
+// two blocks an SM instead of four it took 63 (too few loads in flight).
 struct SkinnyArgs {
   const void *x, *w;
   int64_t x_ld, w_ld;
@@ -389,70 +454,23 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps, R <= 2 ? kSkinnyPerSm : 2) 
   extern __shared__ __align__(16) float s_x[];   // [R][H]
   __shared__ float2 s_ms[kSkinnyWarps][R];
   __shared__ int s_last;
-  constexpr int N = Vec16<T>::N;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int tg[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    tg[r] = r < a.T ? a.target[r] : a.ignore;
-    if (!counts(tg[r], a.V, a.ignore)) {
-      if (r < a.T && tg[r] != a.ignore && blockIdx.x == 0 && threadIdx.x == 0) set_flag(a.flags, kFlagTarget);
-      tg[r] = -1;
-    }
-    const T* xr = reinterpret_cast<const T*>(a.x) + r * a.x_ld;
-    for (int i = threadIdx.x; i < a.H; i += blockDim.x) s_x[r * a.H + i] = tg[r] >= 0 ? to_f(xr[i]) : 0.0f;
+  skinny_rows<T, R>(reinterpret_cast<const T*>(a.x), a.x_ld, a.target, a.T, a.H, a.V, a.ignore, s_x, tg);
+  if (blockIdx.x == 0 && (int)threadIdx.x < a.T) {
+    const int t = a.target[threadIdx.x];
+    if (t != a.ignore && !counts(t, a.V, a.ignore)) set_flag(a.flags, kFlagTarget);
   }
-  __syncthreads();
   float M[R], S[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) { M[r] = -INFINITY; S[r] = 0.0f; }
-  const T* w = reinterpret_cast<const T*>(a.w);
   // a contiguous range of rows a warp: every warp has the same number, but one
   const int64_t all = (int64_t)gridDim.x * kSkinnyWarps, me = (int64_t)blockIdx.x * kSkinnyWarps + warp;
-  const int64_t vend = a.V * (me + 1) / all;
-  for (int64_t v0 = a.V * me / all; v0 < vend; v0 += NV) {
-    float acc[NV][R];
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-#pragma unroll
-      for (int r = 0; r < R; ++r) acc[v][r] = 0.0f;
-    const T* wr[NV];
-#pragma unroll
-    for (int v = 0; v < NV; ++v) wr[v] = w + min(v0 + v, vend - 1) * a.w_ld;
-#pragma unroll 4
-    for (int i = lane * N; i < a.H; i += 32 * N) {
-      uint4 u[NV];
-#pragma unroll
-      for (int v = 0; v < NV; ++v) u[v] = __ldcs(reinterpret_cast<const uint4*>(wr[v] + i));
-#pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        float f[N];
-        unpack16(u[v], f, (const T*)nullptr);
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int e = 0; e < N; e += 4) {
-            const float4 xv = *reinterpret_cast<const float4*>(s_x + r * a.H + i + e);
-            acc[v][r] = fmaf(f[e], xv.x, acc[v][r]);
-            acc[v][r] = fmaf(f[e + 1], xv.y, acc[v][r]);
-            acc[v][r] = fmaf(f[e + 2], xv.z, acc[v][r]);
-            acc[v][r] = fmaf(f[e + 3], xv.w, acc[v][r]);
-          }
-      }
-    }
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float z = acc[v][r];
-#pragma unroll
-        for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-        if (v0 + v < vend) {
-          if (tg[r] != (int)(v0 + v)) merge_ms(M[r], S[r], z, 1.0f);
-          else if (lane == 0) a.zt[r] = z;   // the target is merged by itself
-        }
-      }
-  }
+  skinny_logits<T, R, NV>(reinterpret_cast<const T*>(a.w), a.w_ld, s_x, a.H, a.V * me / all,
+                          a.V * (me + 1) / all, [&](int64_t v, int r, float z) {
+                            if (tg[r] != (int)v) merge_ms(M[r], S[r], z, 1.0f);
+                            else if (lane == 0) a.zt[r] = z;   // the target is merged by itself
+                          });
   if (lane == 0)
 #pragma unroll
     for (int r = 0; r < R; ++r) s_ms[warp][r] = make_float2(M[r], S[r]);
@@ -509,26 +527,93 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps, R <= 2 ? kSkinnyPerSm : 2) 
   }
 }
 
+// The logit gradient of few rows, in the place of the tiles' (whose logits, added up in
+// another order, differ from the statistics by their rounding: at logits of 1e5 that is
+// a probability's whole size).  d [planes][plane][d_ld] of columns v0 .. v0 + vcols; row
+// of d: the token's place among those that count.  The rows up to 64, which the dW
+// product's k-block reads, and the columns past the vocabulary are zeroed.
+struct SkinnyGradArgs {
+  const void *x, *w;
+  int64_t x_ld, w_ld;
+  const int32_t* target;
+  int T, H, V, ignore, planes;
+  const float4* rowstat;   // [T]
+  const float* g;          // of the rows that count
+  int64_t v0, vcols, plane, d_ld;
+  bf16* d;
+};
+template <typename T, int R, int NV>
+__global__ void __launch_bounds__(32 * kSkinnyWarps, R <= 2 ? kSkinnyPerSm : 2)
+    ce_skinny_grad_kernel(const SkinnyGradArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  extern __shared__ __align__(16) float s_x[];   // [R][H]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int tg[R], n = 0, pos[R];
+  skinny_rows<T, R>(reinterpret_cast<const T*>(a.x), a.x_ld, a.target, a.T, a.H, a.V, a.ignore, s_x, tg);
+  float M[R], gs[R], gt[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    pos[r] = n;
+    if (tg[r] < 0) continue;
+    const float4 ms = a.rowstat[r];
+    M[r] = ms.x;
+    gs[r] = a.g[n++] / ms.y;
+    gt[r] = -gs[r] * ms.z;
+  }
+  auto put = [&](int row, int64_t c, float v) {
+    for (int p = 0; p < a.planes; ++p) a.d[(p * a.plane + row) * a.d_ld + c] = __float2bfloat16_rn(take_plane(v));
+  };
+  const int64_t have = min(a.vcols, a.V - a.v0);
+  const int64_t all = (int64_t)gridDim.x * kSkinnyWarps, me = (int64_t)blockIdx.x * kSkinnyWarps + warp;
+  skinny_logits<T, R, NV>(reinterpret_cast<const T*>(a.w) + a.v0 * a.w_ld, a.w_ld, s_x, a.H, have * me / all,
+                          have * (me + 1) / all, [&](int64_t c, int r, float z) {
+                            if (lane != 0 || tg[r] < 0) return;
+                            const float e = exp2f((z - M[r]) * 1.4426950408889634f) * gs[r];
+                            put(pos[r], c, a.v0 + c == tg[r] ? gt[r] : e);
+                          });
+  const int64_t tid = blockIdx.x * (int64_t)blockDim.x + threadIdx.x, step = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t i = tid; i < n * (a.vcols - have); i += step) put((int)(i % n), have + i / n, 0.0f);
+  const int64_t per = a.vcols / 8;   // 16-byte pieces of a row (vcols: a multiple of 256)
+  for (int64_t i = tid; i < a.planes * (64 - n) * per; i += step) {
+    const int64_t row = i / per;
+    const int64_t at = (row / (64 - n)) * a.plane + n + row % (64 - n);
+    *reinterpret_cast<uint4*>(a.d + at * a.d_ld + (i % per) * 8) = make_uint4(0, 0, 0, 0);
+  }
+}
+
+// Both few-row kernels: `vocab` rows of W, T rows of x.
+template <typename Args>
+cudaError_t launch_few(void (*kernel)(Args), int nv, int rows, int H, int64_t vocab, const Args& a,
+                       cudaStream_t st) {
+  const size_t smem = (size_t)rows * H * 4;
+  if (smem > 40 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t want = (vocab + kSkinnyWarps * nv - 1) / (kSkinnyWarps * nv);
+  // four blocks an SM with up to two rows of x, else two, if x fits so often
+  const int per = (int)std::max<size_t>(1, std::min<size_t>(rows <= 2 ? kSkinnyPerSm : 2, 220 * 1024 / (smem + 1024)));
+  const int64_t blocks = std::min<int64_t>(want, (int64_t)tc_sm_count() * per);
+  return launch_after(kernel, (unsigned)blocks, 32 * kSkinnyWarps, smem, st, 1, a);
+}
+
 template <typename T>
 cudaError_t launch_skinny(const SkinnyArgs& a, cudaStream_t st) {
-  const int rows = a.T <= 1 ? 1 : a.T <= 2 ? 2 : 4;
-  const size_t smem = (size_t)rows * a.H * 4;
-  auto go = [&](auto kernel, int nv) {
-    if (smem > 40 * 1024) {
-      cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-      if (e != cudaSuccess) return e;
-    }
-    const int64_t want = ((int64_t)a.V + kSkinnyWarps * nv - 1) / (kSkinnyWarps * nv);
-    // four blocks an SM with up to two rows of x, else two, if x fits so often
-    const int per = (int)std::max<size_t>(1, std::min<size_t>(rows <= 2 ? kSkinnyPerSm : 2, 220 * 1024 / (smem + 1024)));
-    const int64_t blocks = std::min<int64_t>(want, (int64_t)tc_sm_count() * per);
-    return launch_after(kernel, (unsigned)blocks, 32 * kSkinnyWarps, smem, st, 1, a);
-  };
-  if (rows == 1) return go(ce_skinny_kernel<T, 1, 2>, 2);
+  if (a.T <= 1) return launch_few(ce_skinny_kernel<T, 1, 2>, 2, 1, a.H, a.V, a, st);
   if constexpr (sizeof(T) == 4) {
-    if (rows == 4) return go(ce_skinny_kernel<T, 4, 4>, 4);
+    if (a.T > 2) return launch_few(ce_skinny_kernel<T, 4, 4>, 4, 4, a.H, a.V, a, st);
   }
-  return go(ce_skinny_kernel<T, 2, 2>, 2);
+  return launch_few(ce_skinny_kernel<T, 2, 2>, 2, 2, a.H, a.V, a, st);
+}
+template <typename T>
+cudaError_t launch_skinny_grad(const SkinnyGradArgs& a, cudaStream_t st) {
+  const int64_t have = std::min<int64_t>(a.vcols, a.V - a.v0);
+  if (a.T <= 1) return launch_few(ce_skinny_grad_kernel<T, 1, 2>, 2, 1, a.H, have, a, st);
+  if constexpr (sizeof(T) == 4) {
+    if (a.T > 2) return launch_few(ce_skinny_grad_kernel<T, 4, 4>, 4, 4, a.H, have, a, st);
+  }
+  return launch_few(ce_skinny_grad_kernel<T, 2, 2>, 2, 2, a.H, have, a, st);
 }
 
 // The few-row kernel against the tensor cores' tiles (which do the work of 256 rows
@@ -584,53 +669,6 @@ cudaError_t piece_operand(const CeShape& s, const CeLayout& L, char* ws, const v
   *o = {ws + L.wpl, s.H, L.piece, vcols, 0};
   return launch_planes(reinterpret_cast<const float*>(w) + v0 * s.w_ld, s.w_ld, have, vcols, s.H,
                        ws + L.wpl, L.piece, st);
-}
-
-// Statistics of the packed rows over the whole vocabulary, and their merge into the
-// rows' results (rowmap: by token; NULL: packed).
-cudaError_t run_stats(const CeShape& s, const CeLayout& L, char* b, const PrepArgs& p, const void* w,
-                      const int32_t* rowmap, float* loss, float* lse, float4* rowstat, float* total,
-                      cudaStream_t st) {
-  const int64_t vpad = ((int64_t)s.V + 255) / 256 * 256;
-  // bf16 W is read where it is: one launch over the whole vocabulary
-  const int64_t step = s.planes == 1 ? vpad : L.piece;
-  int64_t c = 0;
-  for (int64_t v0 = 0; v0 < vpad && s.T > 0; v0 += step, ++c) {
-    const int64_t vcols = std::min(step, vpad - v0);
-    Operand o;
-    cudaError_t e = piece_operand(s, L, b, w, v0, vcols, &o, st);
-    if (e != cudaSuccess) return e;
-    LogitsArgs a = {};
-    a.planes = s.planes;
-    a.x = b + L.xc;
-    a.x_ld = s.H;
-    a.x_plane = L.rows_pad;
-    a.w = o.p;
-    a.w_ld = o.ld;
-    a.w_plane = o.plane;
-    a.w_rows = o.rows;
-    a.hidden = s.H;
-    a.v0 = v0;
-    a.w_v0 = o.v0;
-    a.vcols = vcols;
-    a.vocab = s.V;
-    a.nrows = p.nrows;
-    a.rows_bound = s.T;
-    a.target = p.tgt;
-    a.ctr = p.ctr + c;
-    a.flags = p.flags;
-    a.stats = reinterpret_cast<float2*>(b + L.stats);
-    a.zt = reinterpret_cast<float*>(b + L.zt);
-    a.rows_pad = L.rows_pad;
-    e = launch_linear_logits(a, st);
-    if (e != cudaSuccess) return e;
-  }
-  const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((s.T + 31) / 32, 4096));
-  return launch_after(ce_merge_kernel, (unsigned)blocks, 32 * kMergeWarps, 0, st, 1,
-                      reinterpret_cast<const float2*>(b + L.stats), L.rows_pad, (int)(vpad / 128),
-                      reinterpret_cast<const float*>(b + L.zt), rowmap, p.nrows, p.ticket,
-                      reinterpret_cast<float*>(b + L.loss), loss, lse, rowstat, total,
-                      s.reduction == MOE_CE_MEAN ? 1 : 0);
 }
 
 }  // namespace
@@ -700,7 +738,46 @@ extern "C" moe_status moe_linear_ce_forward(const moe_ce_shape* shape, const voi
   p.lse_out = lse;
   p.stats_out = reinterpret_cast<float4*>(stats);
   CHECK_CUDA(run_prep(s, L, b, p, st));
-  CHECK_CUDA(run_stats(s, L, b, p, w, p.rowmap, loss, lse, reinterpret_cast<float4*>(stats), total, st));
+  const int64_t vpad = ((int64_t)s.V + 255) / 256 * 256;
+  // bf16 W is read where it is: one launch over the whole vocabulary
+  const int64_t step = s.planes == 1 ? vpad : L.piece;
+  int64_t c = 0;
+  for (int64_t v0 = 0; v0 < vpad && s.T > 0; v0 += step, ++c) {
+    const int64_t vcols = std::min(step, vpad - v0);
+    Operand o;
+    CHECK_CUDA(piece_operand(s, L, b, w, v0, vcols, &o, st));
+    LogitsArgs a = {};
+    a.planes = s.planes;
+    a.x = b + L.xc;
+    a.x_ld = s.H;
+    a.x_plane = L.rows_pad;
+    a.w = o.p;
+    a.w_ld = o.ld;
+    a.w_plane = o.plane;
+    a.w_rows = o.rows;
+    a.hidden = s.H;
+    a.v0 = v0;
+    a.w_v0 = o.v0;
+    a.vcols = vcols;
+    a.vocab = s.V;
+    a.nrows = p.nrows;
+    a.rows_bound = s.T;
+    a.target = p.tgt;
+    a.ctr = p.ctr + c;
+    a.flags = p.flags;
+    a.stats = reinterpret_cast<float2*>(b + L.stats);
+    a.zt = reinterpret_cast<float*>(b + L.zt);
+    a.rows_pad = L.rows_pad;
+    CHECK_CUDA(launch_linear_logits(a, st));
+  }
+  int64_t blocks = std::min<int64_t>((s.T + 31) / 32, 4096);
+  if (blocks < 1) blocks = 1;
+  CHECK_CUDA(launch_after(ce_merge_kernel, (unsigned)blocks, 32 * kMergeWarps, 0, st, 1,
+                          reinterpret_cast<const float2*>(b + L.stats), L.rows_pad, (int)(vpad / 128),
+                          reinterpret_cast<const float*>(b + L.zt), p.rowmap, p.nrows, p.ticket,
+                          reinterpret_cast<float*>(b + L.loss), loss, lse,
+                          reinterpret_cast<float4*>(stats), total,
+                          s.reduction == MOE_CE_MEAN ? 1 : 0));
   return MOE_OK;
 }
 
@@ -732,9 +809,6 @@ extern "C" moe_status moe_linear_ce_backward(const moe_ce_shape* shape, const vo
   p.rowstat_c = reinterpret_cast<float4*>(b + L.rowstat);
   p.dx = L.dx_direct ? dx : nullptr;
   CHECK_CUDA(run_prep(s, L, b, p, st));
-  // The few-row forward adds up its logits in an order of its own, so its statistics
-  // are not those of the tiles below: they are taken again.
-  if (skinny_ok(s)) CHECK_CUDA(run_stats(s, L, b, p, w, nullptr, nullptr, nullptr, p.rowstat_c, nullptr, st));
   const int64_t vpad = ((int64_t)s.V + 255) / 256 * 256;
   int64_t c = 0;
   for (int64_t v0 = 0; v0 < vpad; v0 += L.piece, ++c) {
@@ -742,32 +816,54 @@ extern "C" moe_status moe_linear_ce_backward(const moe_ce_shape* shape, const vo
     const int64_t have = std::min<int64_t>(vcols, s.V - v0);
     Operand o;
     CHECK_CUDA(piece_operand(s, L, b, w, v0, vcols, &o, st));
-    LogitsArgs a = {};
-    a.planes = s.planes;
-    a.x = b + L.xc;
-    a.x_ld = s.H;
-    a.x_plane = L.rows_pad;
-    a.w = o.p;
-    a.w_ld = o.ld;
-    a.w_plane = o.plane;
-    a.w_rows = o.rows;
-    a.hidden = s.H;
-    a.v0 = v0;
-    a.w_v0 = o.v0;
-    a.vcols = vcols;
-    a.vocab = s.V;
-    a.nrows = p.nrows;
-    a.rows_bound = s.T;
-    a.target = p.tgt;
-    a.ctr = p.ctr + L.npieces + 2 * c;
-    a.flags = p.flags;
-    a.rows_pad = L.rows_pad;
-    a.gradient = true;
-    a.rowstat = p.rowstat_c;
-    a.g = p.g;
-    a.d = b + L.d;
-    a.d_ld = L.piece;
-    CHECK_CUDA(launch_linear_logits(a, st));
+    if (skinny_ok(s)) {
+      SkinnyGradArgs k = {};
+      k.x = x;
+      k.w = w;
+      k.x_ld = s.x_ld;
+      k.w_ld = s.w_ld;
+      k.target = target;
+      k.T = (int)s.T;
+      k.H = s.H;
+      k.V = s.V;
+      k.ignore = s.ignore;
+      k.planes = s.planes;
+      k.rowstat = p.rowstat;
+      k.g = p.g;
+      k.v0 = v0;
+      k.vcols = vcols;
+      k.plane = L.rows_pad;
+      k.d_ld = L.piece;
+      k.d = reinterpret_cast<bf16*>(b + L.d);
+      CHECK_CUDA(s.dtype == MOE_F32 ? launch_skinny_grad<float>(k, st) : launch_skinny_grad<bf16>(k, st));
+    } else {
+      LogitsArgs a = {};
+      a.planes = s.planes;
+      a.x = b + L.xc;
+      a.x_ld = s.H;
+      a.x_plane = L.rows_pad;
+      a.w = o.p;
+      a.w_ld = o.ld;
+      a.w_plane = o.plane;
+      a.w_rows = o.rows;
+      a.hidden = s.H;
+      a.v0 = v0;
+      a.w_v0 = o.v0;
+      a.vcols = vcols;
+      a.vocab = s.V;
+      a.nrows = p.nrows;
+      a.rows_bound = s.T;
+      a.target = p.tgt;
+      a.ctr = p.ctr + 2 * c;
+      a.flags = p.flags;
+      a.rows_pad = L.rows_pad;
+      a.gradient = true;
+      a.rowstat = p.rowstat_c;
+      a.g = p.g;
+      a.d = b + L.d;
+      a.d_ld = L.piece;
+      CHECK_CUDA(launch_linear_logits(a, st));
+    }
     LinearGradArgs q = {};
     q.planes = s.planes;
     q.d = b + L.d;
@@ -788,7 +884,7 @@ extern "C" moe_status moe_linear_ce_backward(const moe_ce_shape* shape, const vo
     q.vocab = s.V;
     q.nrows = p.nrows;
     q.rows_bound = s.T;
-    q.ctr = p.ctr + L.npieces + 2 * c + 1;
+    q.ctr = p.ctr + 2 * c + 1;
     q.flags = p.flags;
     q.split = L.split;
     q.out_f32 = s.dtype == MOE_F32;

@@ -119,6 +119,28 @@ def test_fp32_row_and_feature_of_x_far_above_the_rest(T, value):
     assert float((dw[:, keep].double() - want).norm()) <= gt * float(want.norm())
 
 
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5])
+def test_fp32_few_rows_over_several_pieces(T):
+    """Up to four rows have kernels of their own in both directions; w's planes take
+    more than one piece here; one of the tokens does not count."""
+    H, V = 4096, 30001
+    x, w, t, dl = make(T, H, V, 37)
+    t[T - 1] = 29999
+    if T > 1:
+        t[0] = IGNORE
+        x[0] = math.nan
+        rows = torch.arange(1, T, device="cuda")
+    else:
+        rows = torch.arange(1, device="cuda")
+    d, dx, dw, xd, wd, gt = compare(x, w, t, dl, torch.arange(V, device="cuda"), rows)
+    want = d @ wd
+    assert float((dx[rows].double() - want).norm()) <= gt * float(want.norm())
+    want = d.t() @ xd
+    assert float((dw.double() - want).norm()) <= gt * float(want.norm())
+    if T > 1:
+        assert (dx[0] == 0).all()
+
+
 def test_fp32_gradient_of_rare_columns():
     """A column whose probability is about 1e-13 at every token: its row of dw has
     all its digits, not those that are left next to 1."""

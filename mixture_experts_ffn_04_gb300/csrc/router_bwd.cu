@@ -212,7 +212,10 @@ __global__ void __launch_bounds__(256) router_dz_small_kernel(const DzArgs a) {
       slot = a.idx[t * a.k + lane];
       D = a.d_w[t * a.k + lane];
     }
-    if (slot >= a.E) slot = -1;
+    if (slot < 0 || slot >= a.E) {   // dropped: whatever d_w holds there
+      slot = -1;
+      D = 0.0f;
+    }
     const float dg = a.gate ? a.d_gate[t] : 0.0f;
     float z[2 * NP];
 #pragma unroll

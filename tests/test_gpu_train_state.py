@@ -311,3 +311,30 @@ def test_one_workspace_for_the_layer_and_the_training_operators():
         assert all(torch.equal(a, b) for a, b in zip(ce_call(*ces[i], layer.ws, i), ce[i])), i
         assert all(torch.equal(a, b) for a, b in zip(router_call(shapes[i], layer.ws, BF, i), ro[i])), i
     assert layer.device_status()[0] == m.MOE_OK
+
+
+# ---------------------------------------------------------------------------
+# dropped routes
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("E,k", [(16, 3), (16, 33), (700, 3)])
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_a_dropped_route_may_hold_any_gradient(E, k, norm, bad):
+    """k = 3 and E = 16 take the kernel for few columns, the others the general one."""
+    T, H = 90, 128
+    g = gen(5)
+    x = torch.randn((T, H), generator=g, device="cuda").bfloat16()
+    w = (torch.randn((E, H), generator=g, device="cuda") / math.sqrt(H)).bfloat16()
+    idx = torch.randint(0, E, (T, k), generator=g, device="cuda").to(torch.int32)
+    d_w = torch.randn((T, k), generator=g, device="cuda")
+    idx[4, 1], idx[7, 0], idx[9], idx[80, 2] = E, -1, -7, 2 ** 31 - 1
+    gone = (idx < 0) | (idx >= E)
+    out = []
+    for v in (0.0, bad):
+        d_w[gone] = v
+        op = m.RouterGrad(T, H, E, k, norm_topk=norm, balance_coef=0.01, z_coef=0.001)
+        out.append(op.backward(x, w, idx, d_w))
+        assert op.device_status()[0] == m.MOE_ERR_DEVICE_ROUTE
+    for a, b in zip(*out):
+        assert torch.isfinite(b.float()).all()
+        assert torch.equal(a, b)

@@ -521,6 +521,17 @@ def _vec(t: torch.Tensor, n: int, dtype, name: str):
     return _p(t)
 
 
+def _on_device(ws: torch.Tensor, **tensors):
+    """The workspace is device memory, and the tensors lie where it does: an address
+    of another memory must not reach a kernel."""
+    if ws is None or not ws.is_cuda:
+        raise ValueError("the workspace must be a CUDA tensor, got %s" % (ws if ws is None else ws.device))
+    at = ws.get_device()
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != at:
+            raise ValueError("%s is on %s, the workspace on %s" % (name, t.device, ws.device))
+
+
 def moe_linear_ce_workspace_bytes(shape: MoECeShape) -> int:
     return int(lib().moe_linear_ce_workspace_bytes(ctypes.byref(shape)))
 
@@ -532,13 +543,14 @@ def moe_linear_ce_forward(shape: MoECeShape, x, w, target, loss, lse, stats, tot
     xp, shape.x_stride = _rows(x, shape.tokens, shape.hidden, dt, "x")
     wp, shape.w_stride = _rows(w, shape.vocab, shape.hidden, dt, "w")
     f32, T = torch.float32, shape.tokens
-    _check(lib().moe_linear_ce_forward(
-        ctypes.byref(shape), xp, wp, _vec(target, T, torch.int32, "target"),
-        None if loss is None else _vec(loss, T, f32, "loss"),
-        None if lse is None else _vec(lse, T, f32, "lse"),
-        None if stats is None else _vec(stats, 4 * T, f32, "stats"),
-        None if total is None else _vec(total, 1, f32, "total"), _p(ws), _nbytes(ws),
-        _stream(stream)), "moe_linear_ce_forward")
+    args = (_vec(target, T, torch.int32, "target"),
+            None if loss is None else _vec(loss, T, f32, "loss"),
+            None if lse is None else _vec(lse, T, f32, "lse"),
+            None if stats is None else _vec(stats, 4 * T, f32, "stats"),
+            None if total is None else _vec(total, 1, f32, "total"))
+    _on_device(ws, x=x, w=w, target=target, loss=loss, lse=lse, stats=stats, total=total)
+    _check(lib().moe_linear_ce_forward(ctypes.byref(shape), xp, wp, *args, _p(ws), _nbytes(ws),
+                                       _stream(stream)), "moe_linear_ce_forward")
 
 
 def moe_linear_ce_backward(shape: MoECeShape, x, w, target, stats, dloss, dx, dw, ws,
@@ -548,13 +560,13 @@ def moe_linear_ce_backward(shape: MoECeShape, x, w, target, stats, dloss, dx, dw
     xp, shape.x_stride = _rows(x, T, H, dt, "x")
     wp, shape.w_stride = _rows(w, V, H, dt, "w")
     n = T if shape.reduction == MOE_CE_NONE else 1
-    _check(lib().moe_linear_ce_backward(
-        ctypes.byref(shape), xp, wp, _vec(target, T, torch.int32, "target"),
-        _vec(stats, 4 * T, torch.float32, "stats"),
-        None if dloss is None else _vec(dloss, n, torch.float32, "dloss"),
-        None if dx is None else _vec(dx, T * H, dt, "dx"),
-        None if dw is None else _vec(dw, V * H, dt, "dw"), _p(ws), _nbytes(ws),
-        _stream(stream)), "moe_linear_ce_backward")
+    args = (_vec(target, T, torch.int32, "target"), _vec(stats, 4 * T, torch.float32, "stats"),
+            None if dloss is None else _vec(dloss, n, torch.float32, "dloss"),
+            None if dx is None else _vec(dx, T * H, dt, "dx"),
+            None if dw is None else _vec(dw, V * H, dt, "dw"))
+    _on_device(ws, x=x, w=w, target=target, stats=stats, dloss=dloss, dx=dx, dw=dw)
+    _check(lib().moe_linear_ce_backward(ctypes.byref(shape), xp, wp, *args, _p(ws), _nbytes(ws),
+                                        _stream(stream)), "moe_linear_ce_backward")
 
 
 def moe_router_backward_workspace_bytes(shape: MoEShape) -> int:
@@ -571,12 +583,15 @@ def moe_router_backward(shape: MoEShape, x, w_router, topk_idx, d_topk_w, d_gate
     def opt(t, n, d, name):
         return None if t is None else _vec(t, n, d, name)
 
-    _check(lib().moe_router_backward(
-        ctypes.byref(shape), _vec(x, T * H, dt, "x"), _vec(w_router, rows * H, dt, "w_router"),
-        _vec(topk_idx, T * k, torch.int32, "topk_idx"), opt(d_topk_w, T * k, f32, "d_topk_w"),
-        opt(d_gate, T, f32, "d_gate"), balance_coef, z_coef, opt(dx_add, T * H, dt, "dx_add"),
-        _vec(dx, T * H, dt, "dx"), _vec(dw_router, rows * H, dt, "dw_router"),
-        opt(aux, 2, f32, "aux"), _p(ws), _nbytes(ws), _stream(stream)), "moe_router_backward")
+    args = (_vec(x, T * H, dt, "x"), _vec(w_router, rows * H, dt, "w_router"),
+            _vec(topk_idx, T * k, torch.int32, "topk_idx"), opt(d_topk_w, T * k, f32, "d_topk_w"),
+            opt(d_gate, T, f32, "d_gate"), balance_coef, z_coef, opt(dx_add, T * H, dt, "dx_add"),
+            _vec(dx, T * H, dt, "dx"), _vec(dw_router, rows * H, dt, "dw_router"),
+            opt(aux, 2, f32, "aux"))
+    _on_device(ws, x=x, w_router=w_router, topk_idx=topk_idx, d_topk_w=d_topk_w, d_gate=d_gate,
+               dx_add=dx_add, dx=dx, dw_router=dw_router, aux=aux)
+    _check(lib().moe_router_backward(ctypes.byref(shape), *args, _p(ws), _nbytes(ws),
+                                     _stream(stream)), "moe_router_backward")
 
 
 def grad_tensors(srcs, dsts):
@@ -586,6 +601,8 @@ def grad_tensors(srcs, dsts):
     for e, s, d in zip(arr, srcs, dsts):
         if d is not None and d.numel() != s.numel():
             raise ValueError("a destination must hold as many elements as its gradient")
+        if not s.is_cuda or (d is not None and d.device != s.device) or s.device != srcs[0].device:
+            raise ValueError("gradients and destinations must be on one CUDA device")
         e.src, e.numel, e.src_dtype = _p(s), s.numel(), _dtype_code(s.dtype)
         e.dst, e.dst_dtype = _p(d), _dtype_code((s if d is None else d).dtype)
     return arr
@@ -603,8 +620,10 @@ def moe_grad_clip_plan(tensors, ws, stream=None) -> MoEGradPlan:
 
 
 def moe_grad_clip(plan: MoEGradPlan, max_norm: float, norm, ws, stream=None):
-    _check(lib().moe_grad_clip(ctypes.byref(plan), max_norm, _vec(norm, 1, torch.float32, "norm"),
-                               _p(ws), _nbytes(ws), _stream(stream)), "moe_grad_clip")
+    at = _vec(norm, 1, torch.float32, "norm")
+    _on_device(ws, norm=norm)
+    _check(lib().moe_grad_clip(ctypes.byref(plan), max_norm, at, _p(ws), _nbytes(ws),
+                               _stream(stream)), "moe_grad_clip")
 
 
 # ---------------------------------------------------------------------------

@@ -55,3 +55,44 @@ def test_one_row_has_any_stride(m, name):
         b = dict(a)
         b[name] = torch.zeros(16 * H, dtype=a[name].dtype).as_strided((1, H), (stride, 1))
         assert m._rows(b[name], 1, H, torch.bfloat16, name)[1] == H
+
+
+def router_args(m, T=32, H=64, E=8, k=2):
+    s = m.MoEShape()
+    s.tokens, s.hidden, s.moe_inter, s.topk_shape = T, H, 8, m.moe_topk_pack(E, k)
+    s.norm_topk, s.dtype, s.norm_eps = 1, m.MOE_BF16, 1e-6
+    x = torch.zeros(T, H, dtype=torch.bfloat16)
+    w = torch.zeros(E, H, dtype=torch.bfloat16)
+    n = m.moe_router_backward_workspace_bytes(s)
+    return s, [x, w, torch.zeros(T, k, dtype=torch.int32), torch.zeros(T, k), None, 0.1, 0.1, None,
+               torch.zeros_like(x), torch.zeros_like(w), torch.zeros(2), torch.zeros(n, dtype=torch.uint8)]
+
+
+def test_host_memory_is_refused(m):
+    """Addresses of host tensors must not reach a kernel: with a host workspace, and
+    with a host tensor beside a workspace on a device."""
+    s, a = ce_args(m)
+    a["ws"] = torch.zeros(m.moe_linear_ce_workspace_bytes(s), dtype=torch.uint8)
+    for call in (ce_forward, ce_backward):
+        with pytest.raises(ValueError, match="workspace must be a CUDA tensor"):
+            call(m, s, a)
+    s, r = router_args(m)
+    with pytest.raises(ValueError, match="workspace must be a CUDA tensor"):
+        m.moe_router_backward(s, *r, stream=0)
+    plan = m.MoEGradPlan()
+    plan.tensors, plan.chunks, plan.chunk_elems = 1, 1, 2048
+    with pytest.raises(ValueError, match="workspace must be a CUDA tensor"):
+        m.moe_grad_clip(plan, 1.0, torch.zeros(1), torch.zeros(4096, dtype=torch.uint8), stream=0)
+    with pytest.raises(ValueError, match="one CUDA device"):
+        m.GradClip([torch.zeros(4)])
+
+    class DeviceBytes:   # what a workspace on a GPU answers
+        is_cuda, device = True, torch.device("cuda", 0)
+
+        def get_device(self):
+            return 0
+
+    for name in ("x", "w", "dx", "stats"):
+        with pytest.raises(ValueError, match="%s is on cpu" % name):
+            m._on_device(DeviceBytes(), **{name: torch.zeros(3)})
+    m._on_device(DeviceBytes(), dloss=None)

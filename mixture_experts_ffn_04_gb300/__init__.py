@@ -795,7 +795,8 @@ class GradClip:
     here; the tensors must stay where they are."""
 
     def __init__(self, grads, out=None, stream=None):
-        self.grads, self.out = list(grads), list(grads if out is None else out)
+        self.grads = list(grads)   # once: it may be a generator
+        self.out = list(self.grads if out is None else out)
         if len(self.grads) != len(self.out):
             raise ValueError("out must have one destination for every gradient")
         if not self.grads:

@@ -338,3 +338,16 @@ def test_a_dropped_route_may_hold_any_gradient(E, k, norm, bad):
     for a, b in zip(*out):
         assert torch.isfinite(b.float()).all()
         assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------------------
+# the Python classes
+# ---------------------------------------------------------------------------
+def test_clip_of_a_generator():
+    grads = [torch.randn(1000, device="cuda") for _ in range(3)]
+    want = math.sqrt(sum(float(g.double().square().sum()) for g in grads))
+    op = m.GradClip(g for g in grads)
+    keep = [g.clone() for g in grads]
+    assert abs(float(op.clip(1.0)) - want) <= 64 * F * want
+    for g, k in zip(grads, keep):
+        assert torch.allclose(g, k / want, rtol=1e-5, atol=0)

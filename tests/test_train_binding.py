@@ -96,3 +96,13 @@ def test_host_memory_is_refused(m):
         with pytest.raises(ValueError, match="%s is on cpu" % name):
             m._on_device(DeviceBytes(), **{name: torch.zeros(3)})
     m._on_device(DeviceBytes(), dloss=None)
+
+
+def test_lists_of_gradients_may_be_generators(m):
+    """The refusal is that of the tensors (on the host here), not of the list."""
+    with pytest.raises(ValueError, match="one CUDA device"):
+        m.GradClip(torch.zeros(4) for _ in range(3))
+    with pytest.raises(ValueError, match="one CUDA device"):
+        m.GradClip((torch.zeros(4) for _ in range(3)), out=(torch.zeros(4) for _ in range(3)))
+    with pytest.raises(ValueError, match="empty"):
+        m.GradClip(torch.zeros(4) for _ in range(0))

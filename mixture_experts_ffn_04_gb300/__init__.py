@@ -704,10 +704,21 @@ class MoELayer:
         return moe_get_device_status(self.ws, stream)
 
 
+def _empty(stream, shape, dtype, device):
+    """Memory of the stream that writes it: a block that another stream has freed may
+    still be in use there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _alloc_ws(n: int, device, stream, where: str):
     if n == 0:
         raise MoEError(MOE_ERR_INVALID_ARG, where, "invalid shape")
-    ws = torch.empty(n + 256, dtype=torch.uint8, device=device)
+    ws = _empty(stream, n + 256, torch.uint8, device)
     off = (-ws.data_ptr()) % 256
     ws = ws[off: off + n]
     moe_workspace_init(ws, stream)
@@ -718,8 +729,10 @@ class LinearCrossEntropy:
     """Softmax cross entropy of x . w^T against target over a vocabulary, and its
     gradients, without the [tokens, vocab] logits: shape and a workspace over
     caller tensors.  x [tokens, hidden] and w [vocab, hidden] in bf16 or fp32 may
-    be rows of wider buffers; target is int32 [tokens].  reduction: "none", "sum" or "mean" (over the tokens whose
-    target is not ignore_index)."""
+    be rows of wider buffers; target is int32 [tokens].  reduction: "none", "sum" or
+    "mean" (over the tokens whose target is not ignore_index).  The workspace is made on
+    the current stream, which another one has to wait for before its first call; outputs
+    that a call makes belong to the stream it is given."""
 
     def __init__(self, tokens: int, hidden: int, vocab: int, dtype=torch.bfloat16,
                  reduction: str = "mean", ignore_index: int = -100, device="cuda"):
@@ -737,9 +750,9 @@ class LinearCrossEntropy:
         what the backward needs."""
         none = self.shape.reduction == MOE_CE_NONE
         if none and loss is None:
-            loss = torch.empty(self.shape.tokens, dtype=torch.float32, device=x.device)
+            loss = _empty(stream, self.shape.tokens, torch.float32, x.device)
         if not none and total is None:
-            total = torch.empty(1, dtype=torch.float32, device=x.device)
+            total = _empty(stream, 1, torch.float32, x.device)
         moe_linear_ce_forward(self.shape, x, w, target, loss, self.lse, self.stats, total,
                               self.ws, stream)
         return loss if none else total
@@ -747,9 +760,9 @@ class LinearCrossEntropy:
     def backward(self, x, w, target, dloss=None, dx=None, dw=None, stream=None):
         """(dx, dw) after a forward with the same x, w and target."""
         if dx is None:
-            dx = torch.empty(tuple(x.shape), dtype=x.dtype, device=x.device)
+            dx = _empty(stream, x.shape, x.dtype, x.device)
         if dw is None:
-            dw = torch.empty(tuple(w.shape), dtype=w.dtype, device=w.device)
+            dw = _empty(stream, w.shape, w.dtype, w.device)
         moe_linear_ce_backward(self.shape, x, w, target, self.stats, dloss, dx, dw, self.ws, stream)
         return dx, dw
 
@@ -759,7 +772,8 @@ class LinearCrossEntropy:
 
 class RouterGrad:
     """Gradient of the top-k softmax router (with the balance and z losses):
-    shape, coefficients and a workspace over caller tensors."""
+    shape, coefficients and a workspace over caller tensors.  Streams as in
+    LinearCrossEntropy."""
 
     def __init__(self, tokens: int, hidden: int, experts: int, top_k: int, norm_topk: bool = True,
                  shared_gate: bool = False, dtype=torch.bfloat16, balance_coef: float = 0.0,
@@ -777,10 +791,11 @@ class RouterGrad:
                  dw_router=None, aux=None, stream=None):
         """(dx, dw_router, aux); dx includes dx_add (the experts' dx), aux [2]
         holds the balance and z losses."""
-        dx = torch.empty_like(x) if dx is None else dx
-        dw_router = torch.empty_like(w_router) if dw_router is None else dw_router
+        dx = _empty(stream, x.shape, x.dtype, x.device) if dx is None else dx
+        if dw_router is None:
+            dw_router = _empty(stream, w_router.shape, w_router.dtype, w_router.device)
         if aux is None:
-            aux = torch.empty(2, dtype=torch.float32, device=x.device)
+            aux = _empty(stream, 2, torch.float32, x.device)
         moe_router_backward(self.shape, x, w_router, topk_idx, d_topk_w, d_gate, self.balance_coef,
                             self.z_coef, dx_add, dx, dw_router, aux, self.ws, stream)
         return dx, dw_router, aux
@@ -809,7 +824,7 @@ class GradClip:
     def clip(self, max_norm: float, norm=None, stream=None):
         """The norm [1] before clipping."""
         if norm is None:
-            norm = torch.empty(1, dtype=torch.float32, device=self.ws.device)
+            norm = _empty(stream, 1, torch.float32, self.ws.device)
         moe_grad_clip(self.plan, max_norm, norm, self.ws, stream)
         return norm
 

@@ -351,3 +351,39 @@ def test_clip_of_a_generator():
     assert abs(float(op.clip(1.0)) - want) <= 64 * F * want
     for g, k in zip(grads, keep):
         assert torch.allclose(g, k / want, rtol=1e-5, atol=0)
+
+
+def test_outputs_are_made_on_the_stream_that_writes_them():
+    """A block that the current stream has just freed may still be in use there, so
+    an output for another stream must not come from it."""
+    T, H, V, E, k = 512, 512, 2048, 16, 2
+    x, w, t, _ = make(T, H, V, 3)
+    x, w = x.bfloat16(), w.bfloat16()
+    wr = w[:E].contiguous()
+    idx = torch.randint(0, E, (T, k), device="cuda").to(torch.int32)
+    d_w = torch.randn((T, k), device="cuda")
+    ce = m.LinearCrossEntropy(T, H, V, reduction="none")
+    ro = m.RouterGrad(T, H, E, k)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def freed(numel, dtype):
+        b = torch.empty(numel, dtype=dtype, device="cuda")
+        return b.data_ptr()
+
+    calls = [(T, FP, lambda s: ce.forward(x, w, t, stream=s)),
+             (V * H, BF, lambda s: ce.backward(x, w, t, d_w[:, 0].contiguous(), stream=s)[1]),
+             (T * H, BF, lambda s: ro.backward(x, wr, idx, d_w, stream=s)[0])]
+    for numel, dtype, call in calls:
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        at = freed(numel, dtype)
+        assert freed(numel, dtype) == at        # the current stream takes it again
+        for s in (side, side.cuda_stream):
+            out = call(s)
+            torch.cuda.synchronize()
+            assert not at <= out.data_ptr() < at + numel * out.element_size()
+            del out
+    layer_ws = m.GradClip([d_w], stream=side)
+    torch.cuda.synchronize()
+    assert float(layer_ws.clip(math.inf, stream=side)) > 0

@@ -174,11 +174,16 @@ def _p(t: Optional[torch.Tensor]):
     return t.data_ptr()
 
 
+# The current stream's handle without the Stream object that torch.cuda makes around
+# it (6 us of a small call); not part of torch's public interface, so it may be absent.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
-        # the current stream's handle; torch.cuda.current_stream() makes a Stream
-        # object around it, 6 us of a small call
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        if _raw_stream is None:
+            return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return stream

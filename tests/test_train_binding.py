@@ -106,3 +106,16 @@ def test_lists_of_gradients_may_be_generators(m):
         m.GradClip((torch.zeros(4) for _ in range(3)), out=(torch.zeros(4) for _ in range(3)))
     with pytest.raises(ValueError, match="empty"):
         m.GradClip(torch.zeros(4) for _ in range(0))
+
+
+def test_the_current_stream_without_torch_internals(m, monkeypatch):
+    """The handle comes from torch's public interface where the shorter way is absent."""
+    class Current:
+        cuda_stream = 1234
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Current)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 5)
+    monkeypatch.setattr(m, "_raw_stream", None)
+    assert m._stream(None) == 1234
+    monkeypatch.setattr(m, "_raw_stream", lambda device: 100 + device)
+    assert m._stream(None) == 105
+    assert m._stream(17) == 17

@@ -32,6 +32,9 @@ namespace {
 constexpr int64_t kDlogitBytes = 512ll << 20;
 constexpr int64_t kPlaneBytes = 512ll << 20;    // planes of one piece of an fp32 W
 
+// packing: tokens of a tile, most blocks
+constexpr int kPackTile = 256, kPackBlocks = 1024;
+
 // the few-row forward: rows of x, warps a block, blocks an SM, shared memory of x
 constexpr int kSkinnyRows = 4, kSkinnyWarps = 8, kSkinnyPerSm = 4, kSkinnySmem = 112 * 1024;
 
@@ -89,7 +92,7 @@ struct CeLayout {
   int64_t nctr;
   LinearSplit split;
   bool dx_direct, dw_direct;
-  size_t flags, skinny, meta, ctr, rowmap, inv, tgt, g, rowstat, zt, loss, xc, wpl, stats, d, dx_part, dw_part, total;
+  size_t flags, skinny, meta, ctr, count, rowmap, inv, tgt, g, rowstat, zt, loss, xc, wpl, stats, d, dx_part, dw_part, total;
 };
 
 CeLayout layout_ce(const CeShape& s) {
@@ -118,6 +121,7 @@ CeLayout layout_ce(const CeShape& s) {
   L.skinny = take(s.T <= kSkinnyRows ? (size_t)tc_sm_count() * kSkinnyPerSm * kSkinnyRows * 8 : 0);
   L.meta = take(256);   // rows that count, the merge's ticket
   L.ctr = take((size_t)L.nctr * 4);
+  L.count = take(kPackBlocks * 4);
   L.rowmap = take(T * 4);
   L.inv = take(T * 4);
   L.tgt = take(T * 4);
@@ -140,6 +144,7 @@ CeLayout layout_ce(const CeShape& s) {
 
 struct PrepArgs {
   const int32_t* target;
+  const int32_t* count;   // of each block's tokens, or NULL
   int64_t T, rows_per_block;
   int V, ignore, H;
   const void* x;
@@ -162,24 +167,52 @@ struct PrepArgs {
 
 __device__ __forceinline__ bool counts(int t, int V, int ignore) { return t != ignore && t >= 0 && t < V; }
 
+// Tokens that count in each block's range, for lists whose blocks take more than one
+// tile of tokens (kPackTile): with every block counting for itself, as below, the reads
+// grow with the square of the tokens.
+__global__ void __launch_bounds__(kPackTile) ce_count_kernel(const int32_t* __restrict__ target, int64_t T,
+                                                             int64_t rows_per_block, int V, int ignore,
+                                                             int32_t* count) {
+  __shared__ int s_sum;
+  pdl_trigger();
+  pdl_wait();
+  const int64_t beg = min(T, blockIdx.x * rows_per_block), end = min(T, beg + rows_per_block);
+  if (threadIdx.x == 0) s_sum = 0;
+  __syncthreads();
+  int c = 0;
+  for (int64_t i = beg + threadIdx.x; i < end; i += blockDim.x) c += counts(target[i], V, ignore) ? 1 : 0;
+  c = __reduce_add_sync(0xffffffffu, c);
+  if ((threadIdx.x & 31) == 0) atomicAdd(&s_sum, c);   // integers: the order does not matter
+  __syncthreads();
+  if (threadIdx.x == 0) count[blockIdx.x] = s_sum;
+}
+
 // Pack the tokens that count: block b takes rows_per_block tokens, counts those
-// before its own (a pass over the targets, which every block reads from L2) and
-// copies its rows -- bf16 as they are, fp32 as planes.  Rows from the
-// count up to a multiple of 64 are zeroed: the dW product's last k-block reads
-// them.  Latency-bound at small T; at 8192 x 7168 bound by the copy.
+// before its own (a pass over the targets, which every block reads from L2; over the
+// blocks' counts where there are any) and copies its rows -- bf16 as they are, fp32 as
+// planes.  Rows from the count up to a multiple of 64 are zeroed: the dW product's last
+// k-block reads them.  Latency-bound at small T; at 8192 x 7168 bound by the copy.
 template <typename T>
-__global__ void __launch_bounds__(256) ce_prep_kernel(const PrepArgs a) {
-  __shared__ int s_before, s_total, s_cnt[256];
+__global__ void __launch_bounds__(kPackTile) ce_prep_kernel(const PrepArgs a) {
+  __shared__ int s_before, s_total, s_cnt[kPackTile], s_warp[kPackTile / 32];
   pdl_trigger();
   pdl_wait();
   const int64_t beg = min(a.T, blockIdx.x * a.rows_per_block), end = min(a.T, beg + a.rows_per_block);
   if (threadIdx.x == 0) s_before = s_total = 0;
   __syncthreads();
   int before = 0, total = 0;
-  for (int64_t i = threadIdx.x; i < a.T; i += blockDim.x) {
-    const int c = counts(a.target[i], a.V, a.ignore) ? 1 : 0;
-    total += c;
-    if (i < beg) before += c;
+  if (a.count) {
+    for (int i = threadIdx.x; i < (int)gridDim.x; i += blockDim.x) {
+      const int c = a.count[i];
+      total += c;
+      if (i < (int)blockIdx.x) before += c;
+    }
+  } else {
+    for (int64_t i = threadIdx.x; i < a.T; i += blockDim.x) {
+      const int c = counts(a.target[i], a.V, a.ignore) ? 1 : 0;
+      total += c;
+      if (i < beg) before += c;
+    }
   }
   before = __reduce_add_sync(0xffffffffu, before);
   total = __reduce_add_sync(0xffffffffu, total);
@@ -187,41 +220,7 @@ __global__ void __launch_bounds__(256) ce_prep_kernel(const PrepArgs a) {
     atomicAdd(&s_before, before);   // integers: the order does not matter
     atomicAdd(&s_total, total);
   }
-  // place of each of the block's tokens among those that count
-  const int64_t mine = beg + threadIdx.x;
-  int t = a.ignore;
-  if (mine < end) t = a.target[mine];
-  const bool ok = mine < end && counts(t, a.V, a.ignore);
-  if (mine < end && !ok && t != a.ignore) set_flag(a.flags, kFlagTarget);
-  const uint32_t ball = __ballot_sync(0xffffffffu, ok);
-  __shared__ int s_warp[8];
-  if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = __popc(ball);
   __syncthreads();
-  int pos = s_before;
-  for (int w = 0; w < (threadIdx.x >> 5); ++w) pos += s_warp[w];
-  pos += __popc(ball & ((1u << (threadIdx.x & 31)) - 1u));
-  if (mine < end) {
-    s_cnt[threadIdx.x] = ok ? pos : -1;
-    a.inv[mine] = ok ? pos : -1;
-    if (ok) {
-      a.rowmap[pos] = (int32_t)mine;
-      a.tgt[pos] = t;
-      if (a.g) {
-        float g = 1.0f;
-        if (a.reduction == MOE_CE_NONE) g = a.dloss[mine];
-        else {
-          if (a.dloss) g = a.dloss[0];
-          if (a.reduction == MOE_CE_MEAN) g /= (float)s_total;
-        }
-        a.g[pos] = g;
-        a.rowstat_c[pos] = a.rowstat[mine];
-      }
-    } else {
-      if (a.loss) a.loss[mine] = 0.0f;
-      if (a.lse_out) a.lse_out[mine] = 0.0f;
-      if (a.stats_out) a.stats_out[mine] = make_float4(0.0f, 1.0f, 0.0f, 0.0f);
-    }
-  }
   if (blockIdx.x == 0) {
     if (threadIdx.x == 0) {
       *a.nrows = s_total;
@@ -229,41 +228,82 @@ __global__ void __launch_bounds__(256) ce_prep_kernel(const PrepArgs a) {
     }
     for (int64_t i = threadIdx.x; i < a.nctr; i += blockDim.x) a.ctr[i] = 0;
   }
-  __syncthreads();
-  // copy the rows: a warp a row
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const T* x = reinterpret_cast<const T*>(a.x);
   const uint4 zero = make_uint4(0, 0, 0, 0);
   const int nv = a.H / 8;
-  for (int r = warp; beg + r < end; r += 8) {
-    const int p = s_cnt[r];
-    if (p < 0) {
-      if (a.dx) {
-        uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<T*>(a.dx) + (beg + r) * (int64_t)a.H);
-        for (int v = lane; v < nv * (int)(sizeof(T) / 2); v += 32) o[v] = zero;
-      }
-      continue;
+  int base = s_before;
+  for (int64_t tile = beg; tile < end; tile += kPackTile) {
+    // place of each of the tile's tokens among those that count
+    const int64_t mine = tile + threadIdx.x;
+    int t = a.ignore;
+    if (mine < end) t = a.target[mine];
+    const bool ok = mine < end && counts(t, a.V, a.ignore);
+    if (mine < end && !ok && t != a.ignore) set_flag(a.flags, kFlagTarget);
+    const uint32_t ball = __ballot_sync(0xffffffffu, ok);
+    if (lane == 0) s_warp[warp] = __popc(ball);
+    __syncthreads();
+    int pos = base;
+    for (int w = 0; w < kPackTile / 32; ++w) {
+      if (w < warp) pos += s_warp[w];
+      base += s_warp[w];
     }
-    const T* src = x + (beg + r) * a.x_ld;
-    bf16* dst = a.xc + (int64_t)p * a.H;
-    if (sizeof(T) == 2) {
+    pos += __popc(ball & ((1u << lane) - 1u));
+    if (mine < end) {
+      s_cnt[threadIdx.x] = ok ? pos : -1;
+      a.inv[mine] = ok ? pos : -1;
+      if (ok) {
+        a.rowmap[pos] = (int32_t)mine;
+        a.tgt[pos] = t;
+        if (a.g) {
+          float g = 1.0f;
+          if (a.reduction == MOE_CE_NONE) g = a.dloss[mine];
+          else {
+            if (a.dloss) g = a.dloss[0];
+            if (a.reduction == MOE_CE_MEAN) g /= (float)s_total;
+          }
+          a.g[pos] = g;
+          a.rowstat_c[pos] = a.rowstat[mine];
+        }
+      } else {
+        if (a.loss) a.loss[mine] = 0.0f;
+        if (a.lse_out) a.lse_out[mine] = 0.0f;
+        if (a.stats_out) a.stats_out[mine] = make_float4(0.0f, 1.0f, 0.0f, 0.0f);
+      }
+    }
+    __syncthreads();
+    // copy the rows: a warp a row
+    for (int r = warp; r < kPackTile && tile + r < end; r += kPackTile / 32) {
+      const int p = s_cnt[r];
+      if (p < 0) {
+        if (a.dx) {
+          uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<T*>(a.dx) + (tile + r) * (int64_t)a.H);
+          for (int v = lane; v < nv * (int)(sizeof(T) / 2); v += 32) o[v] = zero;
+        }
+        continue;
+      }
+      const T* src = x + (tile + r) * a.x_ld;
+      bf16* dst = a.xc + (int64_t)p * a.H;
+      if (sizeof(T) == 2) {
 #pragma unroll 4
-      for (int v = lane; v < nv; v += 32)
-        reinterpret_cast<uint4*>(dst)[v] = reinterpret_cast<const uint4*>(src)[v];
-    } else {
-      for (int v = lane; v < nv; v += 32) {
-        const float4 u = reinterpret_cast<const float4*>(src)[2 * v];
-        const float4 w = reinterpret_cast<const float4*>(src)[2 * v + 1];
-        float f[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+        for (int v = lane; v < nv; v += 32)
+          reinterpret_cast<uint4*>(dst)[v] = reinterpret_cast<const uint4*>(src)[v];
+      } else {
+        for (int v = lane; v < nv; v += 32) {
+          const float4 u = reinterpret_cast<const float4*>(src)[2 * v];
+          const float4 w = reinterpret_cast<const float4*>(src)[2 * v + 1];
+          float f[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int pl = 0; pl < kPlanesF32; ++pl) {
-          float q[8];
+          for (int pl = 0; pl < kPlanesF32; ++pl) {
+            float q[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) q[e] = take_plane(f[e]);
-          reinterpret_cast<uint4*>(dst + pl * a.plane * a.H)[v] = pack16(q, (const bf16*)nullptr);
+            for (int e = 0; e < 8; ++e) q[e] = take_plane(f[e]);
+            reinterpret_cast<uint4*>(dst + pl * a.plane * a.H)[v] = pack16(q, (const bf16*)nullptr);
+          }
         }
       }
     }
+    __syncthreads();   // s_warp and s_cnt are the next tile's
   }
   const int total_rows = s_total, pad_end = (total_rows + 63) / 64 * 64;
   const int planes = sizeof(T) == 2 ? 1 : kPlanesF32;
@@ -629,9 +669,17 @@ bool skinny_ok(const CeShape& s) {
 
 cudaError_t run_prep(const CeShape& s, const CeLayout& L, char* ws, PrepArgs& p, cudaStream_t st) {
   p.T = s.T;
-  // a warp a token up to 8192 tokens, then up to 32
-  int64_t rpb = ((s.T + 1023) / 1024 + 7) / 8 * 8;
-  rpb = std::min<int64_t>(std::max<int64_t>(rpb, 8), 256);
+  // a warp a token up to 8192 tokens, then more; whole tiles above 2^18 tokens
+  int64_t rpb = std::max<int64_t>(((s.T + kPackBlocks - 1) / kPackBlocks + 7) / 8 * 8, 8);
+  if (rpb > kPackTile) rpb = (rpb + kPackTile - 1) / kPackTile * kPackTile;
+  const int64_t blocks = std::max<int64_t>((s.T + rpb - 1) / rpb, 32);
+  if (rpb > kPackTile) {
+    int32_t* count = reinterpret_cast<int32_t*>(ws + L.count);
+    const cudaError_t e = launch_after(ce_count_kernel, (unsigned)blocks, kPackTile, 0, st, 1, p.target, s.T, rpb,
+                                       s.V, s.ignore, count);
+    if (e != cudaSuccess) return e;
+    p.count = count;
+  }
   p.rows_per_block = rpb;
   p.V = s.V;
   p.ignore = s.ignore;
@@ -648,9 +696,8 @@ cudaError_t run_prep(const CeShape& s, const CeLayout& L, char* ws, PrepArgs& p,
   p.tgt = reinterpret_cast<int32_t*>(ws + L.tgt);
   p.flags = reinterpret_cast<uint32_t*>(ws);
   p.reduction = s.reduction;
-  const int64_t blocks = std::max<int64_t>((s.T + rpb - 1) / rpb, 32);
-  return launch_after(s.dtype == MOE_F32 ? ce_prep_kernel<float> : ce_prep_kernel<bf16>, (unsigned)blocks, 256, 0,
-                      st, 1, p);
+  return launch_after(s.dtype == MOE_F32 ? ce_prep_kernel<float> : ce_prep_kernel<bf16>, (unsigned)blocks,
+                      kPackTile, 0, st, 1, p);
 }
 
 // W's columns (vocabulary rows) v0 .. of this piece as a tensor-core operand:

@@ -341,6 +341,59 @@ def test_a_dropped_route_may_hold_any_gradient(E, k, norm, bad):
 
 
 # ---------------------------------------------------------------------------
+# very many tokens
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_packing_of_several_hundred_thousand_tokens(dtype):
+    """Above 2^18 tokens: losses per token, and dx and dw, against float64.  bf16
+    gradients: 2^-8 twice; the fp32 sums over the rows (586 chunks of 512, in each 32
+    truncated steps) add at worst 650 f, 2^-14."""
+    T, H, V = 300011, 16, 40
+    x, w, t, dl = make(T, H, V, 41)
+    x, w = x.to(dtype), w.to(dtype)
+    t[torch.rand(T, generator=gen(2), device="cuda") < 0.3] = IGNORE
+    t[:300] = IGNORE
+    t[-1] = 3
+    op = m.LinearCrossEntropy(T, H, V, dtype=dtype, reduction="none", ignore_index=IGNORE)
+    loss = op.forward(x, w, t)
+    dx, dw = op.backward(x, w, t, dl)
+    ok = t != IGNORE
+    z = x.double() @ w.double().t()
+    one = torch.nn.functional.one_hot(t.long().clamp(min=0), V).double()
+    lse = torch.logsumexp(z, 1)
+    want = (lse - (z * one).sum(1)) * ok
+    zb = 8 * math.sqrt(H) * F * float(x.double().norm(dim=1).max() * w.double().norm(dim=1).max())
+    zb += 16 * F * float(z.abs().max())
+    assert float((loss.double() - want).abs().max()) <= 2 * zb + 8 * F * float(lse.abs().max())
+    d = (torch.softmax(z, 1) - one) * (dl * ok).double()[:, None]
+    tol = (2.0 ** -7 if dtype == BF else 2 * F) + 4 * zb + 16 * F + 2.0 ** -14
+    for got, ref in ((dx, d @ w.double()), (dw, d.t() @ x.double())):
+        assert float((got.double() - ref).norm()) <= tol * float(ref.norm())
+    assert (dx[~ok] == 0).all()
+
+
+def test_packing_time_grows_with_the_tokens():
+    """Eight times the tokens cost about eight times the time (the packing must not
+    count every token in every block): at most sixteen are allowed."""
+    def time(T):
+        x = torch.randn((T, 8), device="cuda").bfloat16()
+        w = torch.randn((2, 8), device="cuda").bfloat16()
+        t = torch.zeros(T, device="cuda", dtype=torch.int32)
+        op = m.LinearCrossEntropy(T, 8, 2, reduction="sum")
+        total = torch.empty(1, device="cuda")
+        best = math.inf
+        for _ in range(6):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            op.forward(x, w, t, total=total)
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best
+    assert time(1 << 22) <= 16 * time(1 << 19)
+
+
+# ---------------------------------------------------------------------------
 # the Python classes
 # ---------------------------------------------------------------------------
 def test_clip_of_a_generator():

@@ -40,9 +40,11 @@
 //
 // Roles in each CTA: warp 0 TMA producer, warp 1 TMEM and (even CTA) the MMA
 // issuer, warp 2 the L2 prefetch of dX's addend, warps 4-11 epilogue: two per 32-lane TMEM quarter, one per half of
-// the 256 columns.  Every wait is bounded; a CTA that gives up raises its abort
-// flag, its partner's waits run out in turn, and both meet at the closing
-// cluster barrier before TMEM is released.
+// the 256 columns.  Every wait on an mbarrier is bounded; a CTA that gives up raises
+// its abort flag, its partner's waits run out in turn, copies and MMAs in flight are
+// waited for, again with a limit, and both meet at the closing cluster barrier before
+// TMEM is released.  Not bounded are the closing barriers themselves, which every warp
+// reaches from whatever it was doing, and the waits for a warp's own output boxes.
 #include <atomic>
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -83,6 +85,7 @@ constexpr int STAGE_WARP = 4096;   // output staging of an epilogue warp: 32 row
 constexpr int SMEM_BYTES = 1024 + RING_BYTES + EPI_WARPS * STAGE_WARP + BAR_BYTES;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget of one CTA");
 static_assert((2 * S + 5 + 2 * NSLOT + EPI_WARPS) * 8 + 8 + NSLOT * 32 <= BAR_BYTES, "barrier area");
+constexpr long long kDrainCycles = 1 << 21;   // about a millisecond
 constexpr int kGroupM = 8;
 constexpr int kChunkExact = 8, kChunkBf16 = 64;   // k-blocks of 64
 
@@ -529,10 +532,17 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
     }
-    if (*abort_flag && leader) {
-      // loads still in flight land before the pair goes away
-      for (uint32_t i = issued > (uint32_t)S ? issued - S : 0u; i < issued; ++i)
-        wait2_quiet(full((int)(i % S)), (i / S) & 1u);
+    if (*abort_flag) {
+      // Loads still in flight land before the pair goes away.  The odd CTA's count on
+      // the even CTA's barriers, which may have stopped expecting them: it waits a
+      // thousand times a load's latency instead.
+      if (leader) {
+        for (uint32_t i = issued > (uint32_t)S ? issued - S : 0u; i < issued; ++i)
+          wait2_quiet(full((int)(i % S)), (i / S) & 1u);
+      } else {
+        const long long t0 = clock64();
+        while (clock64() - t0 < kDrainCycles) {}
+      }
     }
   } else if (warp == 1 && lane == 0 && leader) {
     // ---------------- even CTA: MMA issuer for the pair ----------------
@@ -667,7 +677,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tma_load_2d(stage, &tmAdd, n0 + c, (int)row0, addend(warp - 4));
               }
               int w = 1;
-              if (lane == 0) w = wait_cl(addend(warp - 4), add_ph, abort_flag) ? 1 : 0;
+              if (lane == 0) {
+                w = wait_cl(addend(warp - 4), add_ph, abort_flag) ? 1 : 0;
+                // given up (perhaps for another warp's wait): the box still lands first
+                if (!w) wait2_quiet(addend(warp - 4), add_ph);
+              }
               add_ph ^= 1u;
               if (!__shfl_sync(0xffffffffu, w, 0)) { fit = false; break; }
               if (a.out_f32) {

@@ -106,7 +106,7 @@ CeLayout layout_ce(const CeShape& s) {
   // pieces of equal size
   L.piece = ((vpad + L.npieces - 1) / L.npieces + 255) / 256 * 256;
   L.npieces = (vpad + L.piece - 1) / L.piece;
-  L.split = linear_grad_split(s.T, L.piece, s.H, s.planes);
+  L.split = linear_grad_split(s.T, L.piece, s.H);
   L.dx_direct = L.npieces == 1 && L.split.dx == 1;
   L.dw_direct = L.split.dw == 1;
   L.nctr = 2 * L.npieces;

@@ -110,15 +110,12 @@ struct Args {
   int64_t rows_pad;
   const float4* rowstat;
   const float* g;
-  bf16* d;
-  int64_t d_ld;
   int ks_dx, ks_dw, out_f32;
   float* dx_part;
   int accumulate;
   void* dx;
   const int32_t* rowmap;
   const void* dx_add;
-  void* dw;
   float* dw_part;
   int64_t dw_pad;
   int want_dx, want_dw;
@@ -1044,12 +1041,7 @@ static unsigned elementwise_grid(int64_t items) {
 
 }  // namespace lin
 
-int linear_clusters() {
-  int mc = 0;
-  return lin::prepare_device(&mc) == cudaSuccess ? mc : 76;
-}
-
-LinearSplit linear_grad_split(int64_t rows, int64_t vocab, int hidden, int planes) {
+LinearSplit linear_grad_split(int64_t rows, int64_t vocab, int hidden) {
   // A part longer than a pair's share of the work would leave the other SMs idle
   // at the end: split K until it is at most nine tenths of that share (at least 8
   // k-blocks a part, at most 16 parts, whose fp32 sums the reduction reads back).
@@ -1065,7 +1057,6 @@ LinearSplit linear_grad_split(int64_t rows, int64_t vocab, int hidden, int plane
     int64_t s = (kb + part - 1) / part;
     return (int)(s < 1 ? 1 : (s > 16 ? 16 : s));
   };
-  (void)planes;
   return {splits(kbv), splits(kbr)};
 }
 
@@ -1095,8 +1086,6 @@ cudaError_t launch_linear_logits(const LogitsArgs& a, cudaStream_t st) {
   t.rows_pad = a.rows_pad;
   t.rowstat = a.rowstat;
   t.g = a.g;
-  t.d = reinterpret_cast<bf16*>(a.d);
-  t.d_ld = a.d_ld;
   // the same chunks for the gradient's logits as for the statistics: with chunks of
   // their own (4096 of K) they differed from them by 1e-5 of their size, which at
   // logits of 1e4 is a third of a probability
@@ -1175,7 +1164,6 @@ cudaError_t launch_linear_grad(const LinearGradArgs& a, cudaStream_t st) {
   t.dx = a.dx;
   t.rowmap = a.rowmap;
   t.dx_add = a.dx_add;
-  t.dw = a.dw;
   t.dw_part = a.dw_part;
   t.dw_pad = a.dw_pad;
   auto aligned32 = [](const void* p) { return ((uintptr_t)p & 31u) == 0; };

@@ -436,7 +436,7 @@ RbLayout layout_rb(const Shape& s) {
   R.planes = s.dtype == MOE_F32 ? kPlanesF32 : kPlanesD2;
   R.dz_planes = s.dtype == MOE_F32 ? kPlanesF32 : 2;
   R.zsplit = linear_product_split(s.T, R.cols_pad, s.H);
-  R.split = linear_grad_split(s.T, R.cols_pad, s.H, R.planes);
+  R.split = linear_grad_split(s.T, R.cols_pad, s.H);
   R.dx_direct = R.split.dx == 1;
   R.dw_direct = R.split.dw == 1;
   size_t off = R.L.scratch_end;

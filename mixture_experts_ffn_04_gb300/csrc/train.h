@@ -78,7 +78,7 @@ constexpr int kLinTile = 256, kLinK = 64;
 struct LinearSplit {
   int dx, dw;   // K splits of a dX tile (K = vocabulary), a dW tile (K = rows)
 };
-LinearSplit linear_grad_split(int64_t rows, int64_t vocab, int hidden, int planes);
+LinearSplit linear_grad_split(int64_t rows, int64_t vocab, int hidden);
 
 struct LogitsArgs {
   int planes;              // 1: bf16 operands, kPlanesF32: fp32 in planes
@@ -172,7 +172,5 @@ cudaError_t launch_reduce_parts(const float* part, int splits, int64_t part_stri
 // `rows_zero` are zeros.
 cudaError_t launch_planes(const float* src, int64_t ld, int64_t rows, int64_t rows_zero, int hidden,
                           void* dst, int64_t plane, cudaStream_t st);
-
-int linear_clusters();   // clusters of two SMs the device runs at once
 
 }  // namespace moe

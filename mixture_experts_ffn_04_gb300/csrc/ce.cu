@@ -32,8 +32,8 @@ namespace {
 constexpr int64_t kDlogitBytes = 512ll << 20;
 constexpr int64_t kPlaneBytes = 512ll << 20;    // planes of one piece of an fp32 W
 
-// packing: tokens of a tile, most blocks
-constexpr int kPackTile = 256, kPackBlocks = 1024;
+// packing: tokens of a tile, most blocks, tokens up to which each block counts for itself
+constexpr int kPackTile = 256, kPackBlocks = 1024, kPackSelf = 4096;
 
 // the few-row forward: rows of x, warps a block, blocks an SM, shared memory of x
 constexpr int kSkinnyRows = 4, kSkinnyWarps = 8, kSkinnyPerSm = 4, kSkinnySmem = 112 * 1024;
@@ -167,9 +167,11 @@ struct PrepArgs {
 
 __device__ __forceinline__ bool counts(int t, int V, int ignore) { return t != ignore && t >= 0 && t < V; }
 
-// Tokens that count in each block's range, for lists whose blocks take more than one
-// tile of tokens (kPackTile): with every block counting for itself, as below, the reads
-// grow with the square of the tokens.
+// Tokens that count in each block's range, for more than kPackSelf tokens: with every
+// block counting all of them, as below, the reads grow with the square of the tokens.
+// Packing and a two-column loss at H = 8, counted here against each block for itself:
+// T = 4096 25.2 / 25.1 us, 8192 27 / 33, 65536 92 / 140, 262144 287 / 486; H = 1024:
+// 36 / 35, 35 / 37, 157 / 196, 560 / 734.
 __global__ void __launch_bounds__(kPackTile) ce_count_kernel(const int32_t* __restrict__ target, int64_t T,
                                                              int64_t rows_per_block, int V, int ignore,
                                                              int32_t* count) {
@@ -658,10 +660,9 @@ cudaError_t launch_skinny_grad(const SkinnyGradArgs& a, cudaStream_t st) {
 
 // The few-row kernel against the tensor cores' tiles (which do the work of 256 rows
 // whatever T is), us at H = 2048, V = 50257 and H = 7168, V = 32768:
-//   bf16  T = 1: 38 / 59, 78 / 114   T = 2: 47 / 60, 98 / 114   T = 4: 59 / 59, 135 / 115
-//   fp32  T = 1: 67 / 328, 148 / 731                            T = 4: 77 / 329, 206 / 730
-// (fp32 W goes through its planes first): two rows in bf16, four in
-// fp32.
+//   bf16  T = 1: 38 / 64, 79 / 120   T = 2: 48 / 64, 99 / 120   T = 4: 59 / 64, 135 / 120
+//   fp32  T = 1: 71 / 485, 149 / 1124                           T = 4: 83 / 485, 209 / 1124
+// (fp32 W goes through its planes first): two rows in bf16, four in fp32.
 bool skinny_ok(const CeShape& s) {
   const int64_t most = s.dtype == MOE_F32 ? kSkinnyRows : 2;
   return s.T >= 1 && s.T <= most && (size_t)(s.T <= 2 ? s.T : 4) * s.H * 4 <= (size_t)kSkinnySmem;
@@ -673,7 +674,7 @@ cudaError_t run_prep(const CeShape& s, const CeLayout& L, char* ws, PrepArgs& p,
   int64_t rpb = std::max<int64_t>(((s.T + kPackBlocks - 1) / kPackBlocks + 7) / 8 * 8, 8);
   if (rpb > kPackTile) rpb = (rpb + kPackTile - 1) / kPackTile * kPackTile;
   const int64_t blocks = std::max<int64_t>((s.T + rpb - 1) / rpb, 32);
-  if (rpb > kPackTile) {
+  if (s.T > kPackSelf) {
     int32_t* count = reinterpret_cast<int32_t*>(ws + L.count);
     const cudaError_t e = launch_after(ce_count_kernel, (unsigned)blocks, kPackTile, 0, st, 1, p.target, s.T, rpb,
                                        s.V, s.ignore, count);

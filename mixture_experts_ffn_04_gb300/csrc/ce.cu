@@ -13,9 +13,16 @@
 // gradient products in one launch.  8 T H V flops for loss and gradient, of
 // which 2 T H V recompute the logits.
 //
-// Measured (bf16): T = 4096, H = 2048, V = 131072 loss and gradient 5.5 ms, 1.6
-// PFLOP/s under the power cap (0.92 of the sustained matrix-product rate); of its
-// launches packing, merging and adding up dx take 60 us.
+// Up to two rows (fp32: 32) the logits are not tiles' work but a pass over W, forward
+// and backward; the gradient products are the same.
+//
+// Every exponential is of a difference from a maximum, and the backward's logits are
+// added up exactly as the forward's: probabilities stay in [0, 1] whatever the logits'
+// size.
+//
+// Measured (bf16): T = 4096, H = 2048, V = 131072 loss and gradient 5.66 to 5.84 ms
+// from GPU to GPU, 1.5-1.55 PFLOP/s under the power cap (0.9 of the sustained
+// matrix-product rate); of its launches packing, merging and adding up dx take 55 us.
 #include <algorithm>
 
 #include "../../include/moe_train.h"
@@ -26,17 +33,21 @@
 namespace moe {
 namespace {
 
-// Logit gradient of one piece.  T = 4096, V = 131072 (loss and gradient): pieces of
-// 64 MiB 5768 us, 128 5613, 256 5525, 512 5478, all in one (1 GiB) 5446: each piece
-// costs a launch pair's tail, and larger ones only memory.
+// Logit gradient of one piece.  T = 4096, V = 131072 (loss and gradient; one GPU, the
+// gradient's logits then in chunks of 4096, 2 % faster than now): pieces of 64 MiB 5768
+// us, 128 5613, 256 5525, 512 5478, all in one (1 GiB) 5446: each piece costs a launch
+// pair's tail, and larger ones only memory.
 constexpr int64_t kDlogitBytes = 512ll << 20;
-constexpr int64_t kPlaneBytes = 512ll << 20;    // planes of one piece of an fp32 W
+// Planes of one piece of an fp32 W.  T = 64, H = 2048, V = 50257: pieces of 512 MiB
+// (two of them, four rounds of tiles) 494 us the loss and 1337 with the gradient, of 768
+// (one, three rounds) 417 and 1158.
+constexpr int64_t kPlaneBytes = 768ll << 20;
 
 // packing: tokens of a tile, most blocks, tokens up to which each block counts for itself
 constexpr int kPackTile = 256, kPackBlocks = 1024, kPackSelf = 4096;
 
-// the few-row forward: rows of x, warps a block, blocks an SM, shared memory of x
-constexpr int kSkinnyRows = 4, kSkinnyWarps = 8, kSkinnyPerSm = 4, kSkinnySmem = 112 * 1024;
+// the few-row kernels: most rows of x, blocks an SM, shared memory of x
+constexpr int kSkinnyRows = 32, kSkinnyPerSm = 4, kSkinnySmem = 220 * 1024;
 
 struct CeShape {
   int64_t T, x_ld, w_ld;
@@ -118,7 +129,7 @@ CeLayout layout_ce(const CeShape& s) {
   };
   const size_t T = (size_t)L.rows_pad;
   L.flags = take(256);   // status word; the few-row kernel's ticket at +32
-  L.skinny = take(s.T <= kSkinnyRows ? (size_t)tc_sm_count() * kSkinnyPerSm * kSkinnyRows * 8 : 0);
+  L.skinny = take(s.T <= kSkinnyRows ? (size_t)tc_sm_count() * kSkinnyPerSm * s.T * 8 : 0);
   L.meta = take(256);   // rows that count, the merge's ticket
   L.ctr = take((size_t)L.nctr * 4);
   L.count = take(kPackBlocks * 4);
@@ -407,13 +418,15 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   }
 }
 
-// The logits of at most four rows against vocabulary rows v .. vend: a warp takes NV
-// rows of W at a time (all lanes across the row, 16 bytes a load) against the rows of
-// x in shared memory (fp32).  Forward and backward both call it: the same sums in the
-// same order, so the backward's logits are those of the statistics.
+// The logits of R rows against vocabulary rows v .. vend: a warp takes NV rows of W at a
+// time (all lanes across the row, 16 bytes a load) against the rows of x in shared
+// memory (fp32); lane k R + r is handed the logit of row k and x row r.  Forward and
+// backward both call it: the same sums in the same order, whatever R and NV are, so the
+// backward's logits are those of the statistics.
 template <typename T, int R, int NV, typename F>
 __device__ __forceinline__ void skinny_logits(const T* w, int64_t w_ld, const float* s_x, int H, int64_t v,
                                               int64_t vend, F&& take) {
+  static_assert(NV * R <= 32, "a lane a logit");
   constexpr int N = Vec16<T>::N;
   const int lane = threadIdx.x & 31;
   for (; v < vend; v += NV) {
@@ -446,6 +459,7 @@ __device__ __forceinline__ void skinny_logits(const T* w, int64_t w_ld, const fl
           }
       }
     }
+    float mine = 0.0f;
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
@@ -453,30 +467,38 @@ __device__ __forceinline__ void skinny_logits(const T* w, int64_t w_ld, const fl
         float z = acc[k][r];
 #pragma unroll
         for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-        if (v + k < vend) take(v + k, r, z);
+        if (lane == k * R + r) mine = z;
       }
+    if (lane < NV * R && v + lane / R < vend) take(v + lane / R, mine);
   }
 }
 
-// A row's target, or -1 where it does not count, and its x into shared memory (zeros
-// where it does not count, whatever x holds).
+// Warps a block: more where a block's rows of x leave room for one or two blocks an SM.
+template <int R>
+constexpr int kFewWarps = R <= 8 ? 8 : 16;
+template <int R>
+constexpr int kFewBlocks = R <= 2 ? kSkinnyPerSm : R <= 8 ? 2 : 1;
+
+// x of rows first .. first + R into shared memory (zeros where a row does not count,
+// whatever x holds).
 template <typename T, int R>
-__device__ __forceinline__ void skinny_rows(const T* x, int64_t x_ld, const int32_t* target, int rows, int H,
-                                            int V, int ignore, float* s_x, int* tg) {
+__device__ __forceinline__ void skinny_rows(const T* x, int64_t x_ld, const int32_t* target, int first, int rows,
+                                            int H, int V, int ignore, float* s_x) {
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    tg[r] = r < rows ? target[r] : ignore;
-    if (!counts(tg[r], V, ignore)) tg[r] = -1;
-    const T* xr = x + r * x_ld;
-    for (int i = threadIdx.x; i < H; i += blockDim.x) s_x[r * H + i] = tg[r] >= 0 ? to_f(xr[i]) : 0.0f;
+    const bool ok = first + r < rows && counts(target[first + r], V, ignore);
+    const T* xr = x + (first + r) * x_ld;
+    for (int i = threadIdx.x; i < H; i += blockDim.x) s_x[r * H + i] = ok ? to_f(xr[i]) : 0.0f;
   }
   __syncthreads();
 }
 
-// Loss of at most R = 4 rows in one launch: W streams by once, a running maximum and
-// sum per row of x, and the last block merges the blocks.  Bound by HBM: one token
-// against 50257 x 2048 bf16 reads 206 MB in 38 us, 5.4 TB/s (0.80 of the copy); with
-// two blocks an SM instead of four it took 63 (too few loads in flight).
+// Loss of few rows in one launch: W streams by, a running maximum and sum per row of x,
+// and the last block merges the blocks.  More than R rows go in groups of R, whose
+// blocks of the same part of W are neighbours, so that it comes from HBM once.  Bound by
+// HBM up to R = 4: one token against 50257 x 2048 bf16 reads 206 MB in 38 us, 5.4 TB/s
+// (0.80 of the copy); with two blocks an SM instead of four it took 63 (too few loads in
+// flight).  From R = 8 on by the FMAs and the reads of x from shared memory.
 struct SkinnyArgs {
   const void *x, *w;
   int64_t x_ld, w_ld;
@@ -484,43 +506,48 @@ struct SkinnyArgs {
   int T, H, V, ignore, reduction;
   float *loss, *lse, *total;
   float4* rowstat;   // [T] or NULL
-  float2* part;      // [grid][4]
-  float* zt;         // [4]
+  int groups;        // of R rows
+  float2* part;      // [grid / groups][T]
+  float* zt;         // [T]
   int32_t* ticket;   // 0 between calls
   uint32_t* flags;
 };
 template <typename T, int R, int NV>
-__global__ void __launch_bounds__(32 * kSkinnyWarps, R <= 2 ? kSkinnyPerSm : 2) ce_skinny_kernel(const SkinnyArgs a) {
+__global__ void __launch_bounds__(32 * kFewWarps<R>, kFewBlocks<R>) ce_skinny_kernel(const SkinnyArgs a) {
   pdl_trigger();
   pdl_wait();
+  constexpr int W = kFewWarps<R>;
   extern __shared__ __align__(16) float s_x[];   // [R][H]
-  __shared__ float2 s_ms[kSkinnyWarps][R];
+  __shared__ float2 s_ms[W][R];
+  __shared__ float s_loss[kSkinnyRows];
   __shared__ int s_last;
+  const int first = blockIdx.x % a.groups * R, block = blockIdx.x / a.groups, blocks = gridDim.x / a.groups;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int tg[R];
-  skinny_rows<T, R>(reinterpret_cast<const T*>(a.x), a.x_ld, a.target, a.T, a.H, a.V, a.ignore, s_x, tg);
+  skinny_rows<T, R>(reinterpret_cast<const T*>(a.x), a.x_ld, a.target, first, a.T, a.H, a.V, a.ignore, s_x);
   if (blockIdx.x == 0 && (int)threadIdx.x < a.T) {
     const int t = a.target[threadIdx.x];
     if (t != a.ignore && !counts(t, a.V, a.ignore)) set_flag(a.flags, kFlagTarget);
   }
-  float M[R], S[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) { M[r] = -INFINITY; S[r] = 0.0f; }
+  const int row = first + lane % R, target = row < a.T ? a.target[row] : -1;
+  float M = -INFINITY, S = 0.0f;
   // a contiguous range of rows a warp: every warp has the same number, but one
-  const int64_t all = (int64_t)gridDim.x * kSkinnyWarps, me = (int64_t)blockIdx.x * kSkinnyWarps + warp;
+  const int64_t all = (int64_t)blocks * W, me = (int64_t)block * W + warp;
   skinny_logits<T, R, NV>(reinterpret_cast<const T*>(a.w), a.w_ld, s_x, a.H, a.V * me / all,
-                          a.V * (me + 1) / all, [&](int64_t v, int r, float z) {
-                            if (tg[r] != (int)v) merge_ms(M[r], S[r], z, 1.0f);
-                            else if (lane == 0) a.zt[r] = z;   // the target is merged by itself
+                          a.V * (me + 1) / all, [&](int64_t v, float z) {
+                            if (target != (int)v) merge_ms(M, S, z, 1.0f);
+                            else a.zt[row] = z;   // the target is merged by itself
                           });
-  if (lane == 0)
 #pragma unroll
-    for (int r = 0; r < R; ++r) s_ms[warp][r] = make_float2(M[r], S[r]);
+  for (int o = R; o < NV * R; o <<= 1) {
+    const float m2 = __shfl_xor_sync(0xffffffffu, M, o), s2 = __shfl_xor_sync(0xffffffffu, S, o);
+    merge_ms(M, S, m2, s2);
+  }
+  if (lane < R) s_ms[warp][lane] = make_float2(M, S);
   __syncthreads();
-  if (threadIdx.x < R) {
+  if (threadIdx.x < R && first + (int)threadIdx.x < a.T) {
     float m = -INFINITY, s = 0.0f;
-    for (int k = 0; k < kSkinnyWarps; ++k) merge_ms(m, s, s_ms[k][threadIdx.x].x, s_ms[k][threadIdx.x].y);
-    a.part[blockIdx.x * kSkinnyRows + threadIdx.x] = make_float2(m, s);
+    for (int k = 0; k < W; ++k) merge_ms(m, s, s_ms[k][threadIdx.x].x, s_ms[k][threadIdx.x].y);
+    a.part[block * a.T + first + threadIdx.x] = make_float2(m, s);
   }
   __threadfence();
   __syncthreads();
@@ -528,12 +555,10 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps, R <= 2 ? kSkinnyPerSm : 2) 
   __syncthreads();
   if (!s_last) return;
   __threadfence();
-  __shared__ float s_loss[R];
-  if (warp < R) {
-    const int r = warp;
+  for (int r = warp; r < a.T; r += W) {
     float m = -INFINITY, s = 0.0f;
-    for (int b = lane; b < (int)gridDim.x; b += 32) {
-      const float2 p = __ldcg(a.part + b * kSkinnyRows + r);
+    for (int b = lane; b < blocks; b += 32) {
+      const float2 p = __ldcg(a.part + b * a.T + r);
       merge_ms(m, s, p.x, p.y);
     }
 #pragma unroll
@@ -541,15 +566,14 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps, R <= 2 ? kSkinnyPerSm : 2) 
       const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
       merge_ms(m, s, m2, s2);
     }
-    if (lane == 0 && r < a.T) {
+    if (lane == 0) {
       const bool ok = counts(a.target[r], a.V, a.ignore);
       RowStat q = {make_float4(0.0f, 1.0f, 0.0f, 0.0f), 0.0f, 0.0f};
       if (ok) q = finish_row(m, s, __ldcg(a.zt + r));
-      const float each = q.loss;
       if (a.lse) a.lse[r] = q.lse;
       if (a.rowstat) a.rowstat[r] = q.stat;
-      if (a.loss) a.loss[r] = each;
-      s_loss[r] = each;
+      if (a.loss) a.loss[r] = q.loss;
+      s_loss[r] = q.loss;
     }
   }
   __syncthreads();
@@ -578,41 +602,48 @@ struct SkinnyGradArgs {
   const void *x, *w;
   int64_t x_ld, w_ld;
   const int32_t* target;
-  int T, H, V, ignore, planes;
+  int T, H, V, ignore, planes, groups;
   const float4* rowstat;   // [T]
   const float* g;          // of the rows that count
   int64_t v0, vcols, plane, d_ld;
   bf16* d;
 };
 template <typename T, int R, int NV>
-__global__ void __launch_bounds__(32 * kSkinnyWarps, R <= 2 ? kSkinnyPerSm : 2)
+__global__ void __launch_bounds__(32 * kFewWarps<R>, kFewBlocks<R>)
     ce_skinny_grad_kernel(const SkinnyGradArgs a) {
   pdl_trigger();
   pdl_wait();
+  constexpr int W = kFewWarps<R>;
   extern __shared__ __align__(16) float s_x[];   // [R][H]
+  const int first = blockIdx.x % a.groups * R, block = blockIdx.x / a.groups, blocks = gridDim.x / a.groups;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int tg[R], n = 0, pos[R];
-  skinny_rows<T, R>(reinterpret_cast<const T*>(a.x), a.x_ld, a.target, a.T, a.H, a.V, a.ignore, s_x, tg);
-  float M[R], gs[R], gt[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    pos[r] = n;
-    if (tg[r] < 0) continue;
-    const float4 ms = a.rowstat[r];
-    M[r] = ms.x;
-    gs[r] = a.g[n++] / ms.y;
-    gt[r] = -gs[r] * ms.z;
+  // this lane's row: its place among those that count (-1: it does not)
+  const int row = first + lane % R;
+  int n = 0, pos = -1;
+  for (int r = 0; r < a.T; ++r) {
+    const bool ok = counts(a.target[r], a.V, a.ignore);
+    if (ok && r == row) pos = n;
+    n += ok ? 1 : 0;
   }
+  float4 ms = make_float4(0.0f, 1.0f, 0.0f, 0.0f);
+  float gs = 0.0f;
+  int target = -1;
+  if (pos >= 0) {
+    ms = a.rowstat[row];
+    gs = a.g[pos] / ms.y;
+    target = a.target[row];
+  }
+  skinny_rows<T, R>(reinterpret_cast<const T*>(a.x), a.x_ld, a.target, first, a.T, a.H, a.V, a.ignore, s_x);
   auto put = [&](int row, int64_t c, float v) {
     for (int p = 0; p < a.planes; ++p) a.d[(p * a.plane + row) * a.d_ld + c] = __float2bfloat16_rn(take_plane(v));
   };
   const int64_t have = min(a.vcols, a.V - a.v0);
-  const int64_t all = (int64_t)gridDim.x * kSkinnyWarps, me = (int64_t)blockIdx.x * kSkinnyWarps + warp;
+  const int64_t all = (int64_t)blocks * W, me = (int64_t)block * W + warp;
   skinny_logits<T, R, NV>(reinterpret_cast<const T*>(a.w) + a.v0 * a.w_ld, a.w_ld, s_x, a.H, have * me / all,
-                          have * (me + 1) / all, [&](int64_t c, int r, float z) {
-                            if (lane != 0 || tg[r] < 0) return;
-                            const float e = exp2f((z - M[r]) * 1.4426950408889634f) * gs[r];
-                            put(pos[r], c, a.v0 + c == tg[r] ? gt[r] : e);
+                          have * (me + 1) / all, [&](int64_t c, float z) {
+                            if (pos < 0) return;
+                            const float e = exp2f((z - ms.x) * 1.4426950408889634f) * gs;
+                            put(pos, c, a.v0 + c == target ? -gs * ms.z : e);
                           });
   const int64_t tid = blockIdx.x * (int64_t)blockDim.x + threadIdx.x, step = (int64_t)gridDim.x * blockDim.x;
   for (int64_t i = tid; i < n * (a.vcols - have); i += step) put((int)(i % n), have + i / n, 0.0f);
@@ -624,48 +655,70 @@ __global__ void __launch_bounds__(32 * kSkinnyWarps, R <= 2 ? kSkinnyPerSm : 2)
   }
 }
 
-// Both few-row kernels: `vocab` rows of W, T rows of x.
-template <typename Args>
-cudaError_t launch_few(void (*kernel)(Args), int nv, int rows, int H, int64_t vocab, const Args& a,
-                       cudaStream_t st) {
-  const size_t smem = (size_t)rows * H * 4;
+// Rows of x a block holds.
+int skinny_group(const CeShape& s) {
+  if (s.T <= 2) return (int)s.T;   // (all of bf16's)
+  int r = s.T <= 4 ? 4 : s.T <= 8 ? 8 : 16;
+  while (r > 4 && (size_t)r * s.H * 4 > (size_t)kSkinnySmem) r /= 2;
+  return r;
+}
+
+// Both few-row kernels: R rows of x a block, `vocab` rows of W.
+template <int R, int NV, typename Args>
+cudaError_t launch_few(void (*kernel)(Args), int64_t vocab, Args a, cudaStream_t st) {
+  constexpr int W = kFewWarps<R>;
+  const size_t smem = (size_t)R * a.H * 4;
   if (smem > 40 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  const int64_t want = (vocab + kSkinnyWarps * nv - 1) / (kSkinnyWarps * nv);
-  // four blocks an SM with up to two rows of x, else two, if x fits so often
-  const int per = (int)std::max<size_t>(1, std::min<size_t>(rows <= 2 ? kSkinnyPerSm : 2, 220 * 1024 / (smem + 1024)));
-  const int64_t blocks = std::min<int64_t>(want, (int64_t)tc_sm_count() * per);
-  return launch_after(kernel, (unsigned)blocks, 32 * kSkinnyWarps, smem, st, 1, a);
+  a.groups = (a.T + R - 1) / R;
+  const int64_t want = (vocab + W * NV - 1) / (W * NV);
+  // as many blocks an SM as the kernel is compiled for, if x fits so often
+  const int per = (int)std::max<size_t>(1, std::min<size_t>(kFewBlocks<R>, 220 * 1024 / (smem + 1024)));
+  const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(want, (int64_t)tc_sm_count() * per / a.groups));
+  return launch_after(kernel, (unsigned)(parts * a.groups), 32 * W, smem, st, 1, a);
 }
-
-template <typename T>
-cudaError_t launch_skinny(const SkinnyArgs& a, cudaStream_t st) {
-  if (a.T <= 1) return launch_few(ce_skinny_kernel<T, 1, 2>, 2, 1, a.H, a.V, a, st);
-  if constexpr (sizeof(T) == 4) {
-    if (a.T > 2) return launch_few(ce_skinny_kernel<T, 4, 4>, 4, 4, a.H, a.V, a, st);
+cudaError_t launch_skinny(const CeShape& s, const SkinnyArgs& a, cudaStream_t st) {
+  const bool f = s.dtype == MOE_F32;
+  switch (skinny_group(s)) {
+    case 1: return launch_few<1, 2>(f ? ce_skinny_kernel<float, 1, 2> : ce_skinny_kernel<bf16, 1, 2>, s.V, a, st);
+    case 2: return launch_few<2, 2>(f ? ce_skinny_kernel<float, 2, 2> : ce_skinny_kernel<bf16, 2, 2>, s.V, a, st);
+    case 4: return launch_few<4, 4>(ce_skinny_kernel<float, 4, 4>, s.V, a, st);
+    case 8: return launch_few<8, 4>(ce_skinny_kernel<float, 8, 4>, s.V, a, st);
+    default: return launch_few<16, 2>(ce_skinny_kernel<float, 16, 2>, s.V, a, st);
   }
-  return launch_few(ce_skinny_kernel<T, 2, 2>, 2, 2, a.H, a.V, a, st);
 }
-template <typename T>
-cudaError_t launch_skinny_grad(const SkinnyGradArgs& a, cudaStream_t st) {
+cudaError_t launch_skinny_grad(const CeShape& s, const SkinnyGradArgs& a, cudaStream_t st) {
+  const bool f = s.dtype == MOE_F32;
   const int64_t have = std::min<int64_t>(a.vcols, a.V - a.v0);
-  if (a.T <= 1) return launch_few(ce_skinny_grad_kernel<T, 1, 2>, 2, 1, a.H, have, a, st);
-  if constexpr (sizeof(T) == 4) {
-    if (a.T > 2) return launch_few(ce_skinny_grad_kernel<T, 4, 4>, 4, 4, a.H, have, a, st);
+  switch (skinny_group(s)) {
+    case 1:
+      return launch_few<1, 2>(f ? ce_skinny_grad_kernel<float, 1, 2> : ce_skinny_grad_kernel<bf16, 1, 2>, have, a, st);
+    case 2:
+      return launch_few<2, 2>(f ? ce_skinny_grad_kernel<float, 2, 2> : ce_skinny_grad_kernel<bf16, 2, 2>, have, a, st);
+    case 4: return launch_few<4, 4>(ce_skinny_grad_kernel<float, 4, 4>, have, a, st);
+    case 8: return launch_few<8, 4>(ce_skinny_grad_kernel<float, 8, 4>, have, a, st);
+    default: return launch_few<16, 2>(ce_skinny_grad_kernel<float, 16, 2>, have, a, st);
   }
-  return launch_few(ce_skinny_grad_kernel<T, 2, 2>, 2, 2, a.H, have, a, st);
 }
 
-// The few-row kernel against the tensor cores' tiles (which do the work of 256 rows
-// whatever T is), us at H = 2048, V = 50257 and H = 7168, V = 32768:
-//   bf16  T = 1: 38 / 64, 79 / 120   T = 2: 48 / 64, 99 / 120   T = 4: 59 / 64, 135 / 120
-//   fp32  T = 1: 71 / 485, 149 / 1124                           T = 4: 83 / 485, 209 / 1124
-// (fp32 W goes through its planes first): two rows in bf16, four in fp32.
+// The few-row kernels against the tensor cores' tiles (which do the work of 256 rows
+// whatever T is, fp32 after turning W into planes).  Loss, us, few-row / tiles:
+//   H, V            bf16  T = 1    2         fp32  T = 1     4         8         16        32        48
+//   2048, 50257     38 / 64   48 / 64        70 / 412  77 / 412  105 / 413 160 / 412 286 / 414 416 / 412
+//   1024, 32001                              28 / 152  33 / 153   51 / 153  73 / 152 124 / 152 172 / 153
+//   7168, 32768     79 / 120  99 / 120      148 / 915 204 / 915  330 / 917 586 / 916 (groups of 4)
+// and with the gradient, fp32:
+//   2048, 50257                             660       698       757 / 1154 863 / 1156 1128 / 1156 1397 / 1155
+//   1024, 32001                             247       267       301 / 429  356 / 434   470 / 434   574 / 437
+//   7168, 32768                            1601      1946      2330 / 2645 3151 / 2647
+// bf16 takes four rows in 59 us against 64, at H = 7168 135 against 120.  So two rows in
+// bf16, in fp32 two groups of as many rows as a block holds.
 bool skinny_ok(const CeShape& s) {
-  const int64_t most = s.dtype == MOE_F32 ? kSkinnyRows : 2;
-  return s.T >= 1 && s.T <= most && (size_t)(s.T <= 2 ? s.T : 4) * s.H * 4 <= (size_t)kSkinnySmem;
+  if (s.T < 1 || s.T > (s.dtype == MOE_F32 ? kSkinnyRows : 2)) return false;
+  const int r = skinny_group(s);
+  return s.T <= 2 * r && (size_t)r * s.H * 4 <= (size_t)kSkinnySmem;
 }
 
 cudaError_t run_prep(const CeShape& s, const CeLayout& L, char* ws, PrepArgs& p, cudaStream_t st) {
@@ -776,7 +829,7 @@ extern "C" moe_status moe_linear_ce_forward(const moe_ce_shape* shape, const voi
     k.zt = reinterpret_cast<float*>(b + L.zt);
     k.flags = reinterpret_cast<uint32_t*>(b);
     k.ticket = reinterpret_cast<int32_t*>(b) + 8;
-    CHECK_CUDA(s.dtype == MOE_F32 ? launch_skinny<float>(k, st) : launch_skinny<bf16>(k, st));
+    CHECK_CUDA(launch_skinny(s, k, st));
     return MOE_OK;
   }
   PrepArgs p = {};
@@ -883,7 +936,7 @@ extern "C" moe_status moe_linear_ce_backward(const moe_ce_shape* shape, const vo
       k.plane = L.rows_pad;
       k.d_ld = L.piece;
       k.d = reinterpret_cast<bf16*>(b + L.d);
-      CHECK_CUDA(s.dtype == MOE_F32 ? launch_skinny_grad<float>(k, st) : launch_skinny_grad<bf16>(k, st));
+      CHECK_CUDA(launch_skinny_grad(s, k, st));
     } else {
       LogitsArgs a = {};
       a.planes = s.planes;

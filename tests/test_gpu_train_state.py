@@ -119,13 +119,13 @@ def test_fp32_row_and_feature_of_x_far_above_the_rest(T, value):
     assert float((dw[:, keep].double() - want).norm()) <= gt * float(want.norm())
 
 
-@pytest.mark.parametrize("T", [1, 2, 3, 4, 5])
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 8, 9, 16, 17])
 def test_fp32_few_rows_over_several_pieces(T):
-    """Up to four rows have kernels of their own in both directions; w's planes take
-    more than one piece here; one of the tokens does not count."""
-    H, V = 4096, 30001
+    """Few rows have kernels of their own in both directions (up to 16 at this size);
+    w's planes take more than one piece here; one of the tokens does not count."""
+    H, V = 4096, 40001
     x, w, t, dl = make(T, H, V, 37)
-    t[T - 1] = 29999
+    t[T - 1] = 39999
     if T > 1:
         t[0] = IGNORE
         x[0] = math.nan
@@ -139,6 +139,32 @@ def test_fp32_few_rows_over_several_pieces(T):
     assert float((dw.double() - want).norm()) <= gt * float(want.norm())
     if T > 1:
         assert (dx[0] == 0).all()
+
+
+@pytest.mark.parametrize("H,T", [(520, 7), (520, 12), (520, 16), (520, 17), (520, 31), (520, 32), (520, 33),
+                                 (4000, 15), (4000, 17), (8200, 6), (8200, 8), (8200, 9), (14080, 3), (14088, 3)])
+def test_fp32_rows_in_groups(H, T):
+    """Rows that fill one or two groups of the few-row kernels (16, 8 or 4 rows, by H)
+    or miss them by one; a third of the tokens do not count and hold anything."""
+    V = 777
+    x, w, t, dl = make(T, H, V, 38)
+    skip = torch.arange(T, device="cuda") % 3 == 1
+    t[skip] = IGNORE
+    x[skip] = math.inf
+    rows = (~skip).nonzero().flatten()
+    d, dx, dw, xd, wd, gt = compare(x, w, t, dl, torch.arange(V, device="cuda"), rows)
+    want = d @ wd
+    assert float((dx[rows].double() - want).norm()) <= gt * float(want.norm())
+    want = d.t() @ xd
+    assert float((dw.double() - want).norm()) <= gt * float(want.norm())
+    assert (dx[skip] == 0).all()
+    for reduction in ("sum", "mean"):
+        op = m.LinearCrossEntropy(T, H, V, dtype=FP, reduction=reduction, ignore_index=IGNORE)
+        got = float(op.forward(x, w, t))
+        z = xd @ wd.t()
+        each = torch.logsumexp(z, 1) - z.gather(1, t[rows].long()[:, None])[:, 0]
+        ref = float(each.sum() if reduction == "sum" else each.mean())
+        assert abs(got - ref) <= gt * abs(ref)
 
 
 def test_fp32_gradient_of_rare_columns():

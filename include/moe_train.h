@@ -111,8 +111,10 @@ moe_status moe_router_backward(const moe_shape *shape, const void *x, const void
  *   norm = sqrt(sum over all tensors and elements of g^2)
  *   coef = min(1, max_norm / (norm + 1e-6));  1 when norm is not finite
  *   dst = g * coef, rounded once to dst's type
- * A norm that is not finite thus leaves the gradients as they are, and the
- * caller, who has the norm, skips the step.  Squares are added in fp32 in
+ * A norm that is not finite (an infinity or NaN among the gradients) thus leaves
+ * them as they are, and the caller, who has the norm, skips the step; one beyond
+ * fp32 clips and reads as infinity.  No two destinations may overlap, nor a
+ * destination another tensor's source.  Squares are added in fp32 in
  * groups and in fp64 across them, in an order that depends on the list alone; a
  * group whose fp32 sum leaves the safe range is added again, scaled.
  * ------------------------------------------------------------------------- */

@@ -175,7 +175,7 @@ def _p(t: Optional[torch.Tensor]):
 
 
 # The current stream's handle without the Stream object that torch.cuda makes around
-# it (6 us of a small call); not part of torch's public interface, so it may be absent.
+# it (3 us of a small call); not part of torch's public interface, so it may be absent.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 

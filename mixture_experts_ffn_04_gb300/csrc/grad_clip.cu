@@ -5,10 +5,10 @@
 //
 // Bound by HBM: every gradient is read for the norm before the first can be
 // scaled, then read again and written.  The list is cut into chunks of
-// kChunk elements that never span two tensors (a table in the workspace, so one
-// launch covers any list).  The norm pass goes through the chunks upwards and
-// the scaling pass downwards: what the norm pass read last is still in L2 when
-// the scaling pass starts.  604 M bf16 values: norm 175 us (6.9 TB/s), scaling 350
+// kChunkMin to kChunkMax elements that never span two tensors (a table in the
+// workspace, so one launch covers any list).  The norm pass goes through the chunks
+// upwards and the scaling pass downwards: what the norm pass read last is still in L2
+// when the scaling pass starts.  604 M bf16 values: norm 175 us (6.9 TB/s), scaling 350
 // (6.9); 200 M values in 1500 tensors at odd offsets 91 (6.2) and 171 (6.6).
 //
 // Each chunk's squares are added in fp32 (at most 64 in a row in each of
@@ -16,7 +16,7 @@
 // chunks in fp64 in chunk order (no atomics on the sums, so the norm is the same
 // in every run).  A chunk whose fp32 sum overflowed, or is small enough for
 // squares to have underflowed, is added again with its values scaled by a power
-// of two.
+// of two; a chunk of zeros is among them (200 M bf16 zeros: norm 73 us, else 65).
 #include <algorithm>
 #include <cmath>
 

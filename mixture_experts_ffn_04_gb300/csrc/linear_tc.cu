@@ -32,9 +32,9 @@
 // fp32 operands come in three bf16 planes (train.h): a tile's k-loop runs over the
 // six plane products whose weight is above 2^-24, smallest first.
 //
-// Measured under a full clock: statistics 1.71 PFLOP/s (T = 4096, H = 2048, V =
-// 131072), the logit gradient 1.76, the gradient products 1.87, against 1.91 for the
-// library's matrix product; back to back under the power cap 1.56-1.6 against 1.73.
+// Measured under a full clock (T = 4096, H = 2048, V = 131072): statistics 1.67
+// PFLOP/s, the logit gradient 1.63, the gradient products 1.83, against 1.91 for the
+// library's matrix product; back to back under the power cap 1.5-1.55 against 1.73.
 // What bounds them is the MMA rate and the cap; tiles with few k-blocks (dW of few
 // rows, dX of a router) are bound by their output.
 //
@@ -600,8 +600,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int n0 = t.nt * BN;
         // Line by line, not by cp.async.bulk.prefetch.L2: with that, one row an
         // instruction, this warp of one block once in some hundred launches did not
-        // come back from it, and the launch never ended (found by progress counters
-        // in host memory; 380,000 launches of this form ran through).
+        // come back from it, and the launch never ended.  Its addresses and sizes were
+        // multiples of 16 inside the matrix and the wait before it is bounded: the
+        // code does not show why, so the instruction is not used.
         const int lines = (min(BN, a.hidden - n0) * esz + 127) / 128;
         for (int r = lane; r < BMC; r += 32) {
           const int64_t row = (int64_t)t.mt * BM + (int64_t)rank * BMC + r;

@@ -36,7 +36,8 @@ extern "C" {
  * bf16 planes each (all 24 mantissa bits, any finite magnitude; an infinite element
  * may give NaN where fp32 arithmetic gives an infinity), fp32 sums; statistics in
  * fp32; the gradient of the logits is rounded to bf16 (fp32: to three planes) as the
- * operand of the two gradient products; dx and dw are rounded once.
+ * operand of the two gradient products (before the total's gradient and the mean's
+ * divisor, which scale the products in fp32); dx and dw are rounded once.
  * ------------------------------------------------------------------------- */
 typedef enum { MOE_CE_NONE = 0, MOE_CE_SUM = 1, MOE_CE_MEAN = 2 } moe_ce_reduction;
 

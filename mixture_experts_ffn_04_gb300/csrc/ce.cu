@@ -130,7 +130,7 @@ CeLayout layout_ce(const CeShape& s) {
   const size_t T = (size_t)L.rows_pad;
   L.flags = take(256);   // status word; the few-row kernel's ticket at +32
   L.skinny = take(s.T <= kSkinnyRows ? (size_t)tc_sm_count() * kSkinnyPerSm * s.T * 8 : 0);
-  L.meta = take(256);   // rows that count, the merge's ticket
+  L.meta = take(256);   // rows that count, the merge's ticket, the gradients' scale
   L.ctr = take((size_t)L.nctr * 4);
   L.count = take(kPackBlocks * 4);
   L.rowmap = take(T * 4);
@@ -162,6 +162,7 @@ struct PrepArgs {
   int64_t x_ld, plane;
   bf16* xc;
   int32_t *nrows, *ticket, *ctr, *rowmap, *inv, *tgt;
+  float* scale;   // of the gradients, for the backward
   int64_t nctr;
   uint32_t* flags;
   // forward: zero the outputs of tokens that do not count
@@ -238,6 +239,14 @@ __global__ void __launch_bounds__(kPackTile) ce_prep_kernel(const PrepArgs a) {
     if (threadIdx.x == 0) {
       *a.nrows = s_total;
       *a.ticket = 0;
+      // One factor of every token's gradient stays out of the logit gradient, where
+      // its rounding to bf16 would be the same relative error in every entry.
+      float g = 1.0f;
+      if (a.g && a.reduction != MOE_CE_NONE) {
+        if (a.dloss) g = a.dloss[0];
+        if (a.reduction == MOE_CE_MEAN && s_total > 0) g /= (float)s_total;
+      }
+      *a.scale = g;
     }
     for (int64_t i = threadIdx.x; i < a.nctr; i += blockDim.x) a.ctr[i] = 0;
   }
@@ -269,13 +278,7 @@ __global__ void __launch_bounds__(kPackTile) ce_prep_kernel(const PrepArgs a) {
         a.rowmap[pos] = (int32_t)mine;
         a.tgt[pos] = t;
         if (a.g) {
-          float g = 1.0f;
-          if (a.reduction == MOE_CE_NONE) g = a.dloss[mine];
-          else {
-            if (a.dloss) g = a.dloss[0];
-            if (a.reduction == MOE_CE_MEAN) g /= (float)s_total;
-          }
-          a.g[pos] = g;
+          a.g[pos] = a.reduction == MOE_CE_NONE ? a.dloss[mine] : 1.0f;
           a.rowstat_c[pos] = a.rowstat[mine];
         }
       } else {
@@ -743,6 +746,7 @@ cudaError_t run_prep(const CeShape& s, const CeLayout& L, char* ws, PrepArgs& p,
   p.xc = reinterpret_cast<bf16*>(ws + L.xc);
   p.nrows = reinterpret_cast<int32_t*>(ws + L.meta);
   p.ticket = p.nrows + 1;
+  p.scale = reinterpret_cast<float*>(p.nrows + 2);
   p.ctr = reinterpret_cast<int32_t*>(ws + L.ctr);
   p.nctr = L.nctr;
   p.rowmap = reinterpret_cast<int32_t*>(ws + L.rowmap);
@@ -978,6 +982,7 @@ extern "C" moe_status moe_linear_ce_backward(const moe_ce_shape* shape, const vo
     q.w_ld = o.ld;
     q.w_plane = o.plane;
     q.w_rows = o.rows;
+    q.scale = p.scale;
     q.hidden = s.H;
     q.v0 = v0;
     q.w_v0 = o.v0;

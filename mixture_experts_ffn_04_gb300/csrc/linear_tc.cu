@@ -110,6 +110,7 @@ struct Args {
   int64_t rows_pad;
   const float4* rowstat;
   const float* g;
+  const float* scale;   // of dX and dW
   int ks_dx, ks_dw, out_f32;
   float* dx_part;
   int accumulate;
@@ -723,6 +724,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (acc == 0) aph ^= 1u;
       }
       if (!ok) break;
+      if (KIND == kGrad && a.scale != nullptr) {
+        const float scale = *a.scale;
+#pragma unroll
+        for (int j = 0; j < BN / 2; ++j) f[j] *= scale;
+      }
       if (KIND == kStats) {
         // maximum of the row over this half of the tile and the sum of e^(z - maximum).
         // The difference is taken before the factor log2 e: a half tile of masked
@@ -1171,7 +1177,8 @@ cudaError_t launch_linear_grad(const LinearGradArgs& a, cudaStream_t st) {
   t.wide_dx = a.hidden * (a.out_f32 ? 4 : 2) % 32 == 0 && aligned32(a.dx);
   t.want_dx = a.dx_part != nullptr || a.dx != nullptr;
   t.want_dw = a.dw_part != nullptr || a.dw != nullptr;
-  if (a.dx_add && a.rowmap) return cudaErrorInvalidValue;
+  t.scale = a.scale;
+  if (a.dx_add && (a.rowmap || a.scale)) return cudaErrorInvalidValue;
   if ((t.want_dx && t.ks_dx > 1 && !a.dx_part) || (t.want_dw && t.ks_dw > 1 && !a.dw_part))
     return cudaErrorInvalidValue;
   const int64_t nth = (a.hidden + BN - 1) / BN;

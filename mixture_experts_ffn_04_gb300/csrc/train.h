@@ -138,6 +138,7 @@ struct LinearGradArgs {
   int64_t x_rows;
   const void* w;           // bf16 [planes * w_plane, w_ld]
   int64_t w_ld, w_plane, w_rows;
+  const float* scale;      // device: factor of dx and dw, or NULL (not with dx_add)
   int hidden;
   int64_t v0, w_v0, vcols, vocab;
   const int32_t* nrows;    // device count, or NULL: rows_bound

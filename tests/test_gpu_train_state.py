@@ -256,6 +256,30 @@ def test_huge_logits(T, value, dtype):
 
 
 # ---------------------------------------------------------------------------
+# the objective's gradient
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("T", [2, 64, 300])
+@pytest.mark.parametrize("up", [1 + 2.0 ** -8, 1 / 129.0, 3.0e-30, 65504.0 * 3])
+def test_bf16_gradients_follow_the_objectives_gradient(T, up):
+    """One gradient of the reduced loss scales every entry: the same factor must not be
+    rounded to bf16 in each of them.  Against the gradients at 1, projected on them, the
+    factor is off by the results' own roundings (at most 2^-8 each, independent) alone:
+    6 sigma of their mean."""
+    H, V = 256, 3000
+    x, w, t, _ = make(T, H, V, 42)
+    x, w = x.bfloat16(), w.bfloat16()
+    op = m.LinearCrossEntropy(T, H, V, reduction="sum", ignore_index=IGNORE)
+    op.forward(x, w, t)
+    one = [g.double() for g in op.backward(x, w, t)]
+    got = op.backward(x, w, t, torch.tensor([up], device="cuda"))
+    factor = float(torch.tensor(up, dtype=FP))
+    for a, b in zip(got, one):
+        ratio = float((a.double() * b).sum() / (b * b).sum()) / factor
+        weight = float((b ** 4).sum().sqrt() / (b * b).sum())   # of independent errors
+        assert abs(ratio - 1) <= 6 * 2.0 ** -8 * weight + 4 * F, (ratio, weight)
+
+
+# ---------------------------------------------------------------------------
 # one workspace for several shapes and operators
 # ---------------------------------------------------------------------------
 def router_shape(T, H, E, k, dtype=BF):

@@ -35,8 +35,8 @@ extern "C" {
  * Precision: bf16 inputs on the tensor cores with fp32 sums; fp32 inputs as three
  * bf16 planes each (all 24 mantissa bits, any finite magnitude; an infinite element
  * may give NaN where fp32 arithmetic gives an infinity), fp32 sums; statistics in
- * fp32; the gradient of the logits is rounded to bf16 (fp32: to three planes) as the
- * operand of the two gradient products (before the total's gradient and the mean's
+ * fp32; the gradient of the logits is rounded to bf16 (up to 32 tokens to two planes,
+ * fp32 to three) as the operand of the two gradient products (before the total's gradient and the mean's
  * divisor, which scale the products in fp32); dx and dw are rounded once.
  * ------------------------------------------------------------------------- */
 typedef enum { MOE_CE_NONE = 0, MOE_CE_SUM = 1, MOE_CE_MEAN = 2 } moe_ce_reduction;

@@ -38,6 +38,13 @@ namespace {
 // us, 128 5613, 256 5525, 512 5478, all in one (1 GiB) 5446: each piece costs a launch
 // pair's tail, and larger ones only memory.
 constexpr int64_t kDlogitBytes = 512ll << 20;
+// Tokens up to which a bf16 call keeps the logit gradient in two bf16 planes.  Its
+// rounding to one adds the result's own error once more where it averages out (1.45
+// times the error with weights per token, at 64 rows and at 1000), but up to 2.1 times
+// at one row, 1.7 at 16, 1.6 at 32, where few large entries carry a result; the second
+// plane costs a quarter of such a backward (H = 2048, V = 50257, 16 rows 165 us against
+// 203), and as much as a third from 256 rows on (389 rows 250 against 363).
+constexpr int kTwoPlaneRows = 32;
 // Planes of one piece of an fp32 W.  T = 64, H = 2048, V = 50257: pieces of 512 MiB
 // (two of them, four rounds of tiles) 494 us the loss and 1337 with the gradient, of 768
 // (one, three rounds) 417 and 1158.
@@ -51,7 +58,7 @@ constexpr int kSkinnyRows = 32, kSkinnyPerSm = 4, kSkinnySmem = 220 * 1024;
 
 struct CeShape {
   int64_t T, x_ld, w_ld;
-  int H, V, dtype, reduction, ignore, esize, planes;
+  int H, V, dtype, reduction, ignore, esize, planes, d_planes;
 };
 
 moe_status decode_ce(const moe_ce_shape* s, CeShape* o, const char** why) {
@@ -95,6 +102,7 @@ moe_status decode_ce(const moe_ce_shape* s, CeShape* o, const char** why) {
   o->ignore = s->ignore_index;
   o->esize = s->dtype == MOE_F32 ? 4 : 2;
   o->planes = s->dtype == MOE_F32 ? kPlanesF32 : 1;
+  o->d_planes = s->dtype == MOE_F32 ? kPlanesF32 : s->tokens <= kTwoPlaneRows ? 2 : 1;
   return MOE_OK;
 }
 
@@ -110,7 +118,7 @@ CeLayout layout_ce(const CeShape& s) {
   CeLayout L;
   L.rows_pad = std::max<int64_t>(256, (s.T + 255) / 256 * 256);
   const int64_t vpad = ((int64_t)s.V + 255) / 256 * 256;
-  int64_t piece = kDlogitBytes / (L.rows_pad * 2 * s.planes) / 256 * 256;
+  int64_t piece = kDlogitBytes / (L.rows_pad * 2 * s.d_planes) / 256 * 256;
   if (s.planes > 1) piece = std::min(piece, kPlaneBytes / ((int64_t)s.H * 2 * s.planes) / 256 * 256);
   piece = std::max<int64_t>(piece, 256);
   L.npieces = (vpad + piece - 1) / piece;
@@ -146,7 +154,7 @@ CeLayout layout_ce(const CeShape& s) {
   L.stats = take((size_t)(vpad / 128) * T * 8);
   const size_t fwd_end = off;
   off = base;   // the backward's buffers take the forward statistics' place
-  L.d = take((size_t)s.planes * T * L.piece * 2);
+  L.d = take((size_t)s.d_planes * T * L.piece * 2);
   L.dx_part = take(L.dx_direct ? 0 : (size_t)L.split.dx * T * s.H * 4);
   L.dw_part = take(L.dw_direct ? 0 : (size_t)L.split.dw * L.piece * s.H * 4);
   L.total = std::max(off, fwd_end);
@@ -932,7 +940,7 @@ extern "C" moe_status moe_linear_ce_backward(const moe_ce_shape* shape, const vo
       k.H = s.H;
       k.V = s.V;
       k.ignore = s.ignore;
-      k.planes = s.planes;
+      k.planes = s.d_planes;
       k.rowstat = p.rowstat;
       k.g = p.g;
       k.v0 = v0;
@@ -963,6 +971,7 @@ extern "C" moe_status moe_linear_ce_backward(const moe_ce_shape* shape, const vo
       a.flags = p.flags;
       a.rows_pad = L.rows_pad;
       a.gradient = true;
+      a.d_planes = s.d_planes;
       a.rowstat = p.rowstat_c;
       a.g = p.g;
       a.d = b + L.d;
@@ -970,7 +979,7 @@ extern "C" moe_status moe_linear_ce_backward(const moe_ce_shape* shape, const vo
       CHECK_CUDA(launch_linear_logits(a, st));
     }
     LinearGradArgs q = {};
-    q.planes = s.planes;
+    q.planes = s.d_planes == 2 ? kPlanesD2 : s.planes;
     q.d = b + L.d;
     q.d_ld = L.piece;
     q.d_plane = L.rows_pad;

@@ -97,7 +97,7 @@ constexpr uint32_t IDESC_A_MN = 1u << 15, IDESC_B_MN = 1u << 16;
 enum Kind { kStats = 0, kDlogit = 1, kGrad = 2, kProduct = 3 };
 
 struct Args {
-  int hidden, planes;
+  int hidden, planes, d_planes;
   int64_t v0, w_v0, vcols, vocab;
   const int32_t* nrows;
   int64_t rows_bound;
@@ -782,14 +782,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
 #pragma unroll
         for (int c = 0; c < BN / 2; c += 64) {
-          for (int pl = 0; pl < a.planes; ++pl) {
+          for (int pl = 0; pl < a.d_planes; ++pl) {
             stage_free(lane);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               float q[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                q[e] = pl + 1 < a.planes ? take_plane(f[c + 8 * j + e]) : f[c + 8 * j + e];
+                q[e] = pl + 1 < a.d_planes ? take_plane(f[c + 8 * j + e]) : f[c + 8 * j + e];
               put_piece(stage, lane, j, pack16(q, (const bf16*)nullptr));
             }
             stage_out(&tmOx, stage, lane, t.nt * BN + c_lo + c, (int)(pl * a.d_plane + row0), false);
@@ -1100,7 +1100,8 @@ cudaError_t launch_linear_logits(const LogitsArgs& a, cudaStream_t st) {
   const int64_t tiles = ((a.rows_bound + BM - 1) / BM) * ((a.vcols + BN - 1) / BN);
   if (!a.gradient) return launch<kStats>(mX, mW, mX, mX, mX, mX, mX, t, tiles, st);
   CUtensorMap mO;
-  if (!map_out(&mO, a.d, a.planes * a.rows_pad, a.d_ld, false)) return cudaErrorInvalidValue;
+  t.d_planes = a.d_planes;
+  if (!map_out(&mO, a.d, a.d_planes * a.rows_pad, a.d_ld, false)) return cudaErrorInvalidValue;
   return launch<kDlogit>(mX, mW, mX, mX, mO, mO, mO, t, tiles, st);
 }
 

@@ -82,6 +82,7 @@ LinearSplit linear_grad_split(int64_t rows, int64_t vocab, int hidden);
 
 struct LogitsArgs {
   int planes;              // 1: bf16 operands, kPlanesF32: fp32 in planes
+  int d_planes;            // of d: 1 or 2, or kPlanesF32
   const void* x;           // bf16 [planes * x_plane, x_ld], rows of `hidden`
   int64_t x_ld, x_plane;
   const void* w;           // bf16 [planes * w_plane, w_ld]
@@ -103,7 +104,7 @@ struct LogitsArgs {
   float* zt;
   int64_t rows_pad;
   // gradient (gradient == true): d = g e^(z - M) / S, at the target -g R / S, in bf16
-  // planes [planes * rows_pad, d_ld], zeros past the rows (to the tile) and
+  // planes [d_planes * rows_pad, d_ld], zeros past the rows (to the tile) and
   // past the vocabulary
   bool gradient;
   const float4* rowstat;   // (M, S, R, -) of the compacted rows

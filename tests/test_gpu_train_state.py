@@ -279,6 +279,26 @@ def test_bf16_gradients_follow_the_objectives_gradient(T, up):
         assert abs(ratio - 1) <= 6 * 2.0 ** -8 * weight + 4 * F, (ratio, weight)
 
 
+@pytest.mark.parametrize("T", [1, 2, 3, 8, 31, 32])
+def test_bf16_gradients_of_few_rows(T):
+    """Up to 32 tokens the logit gradient keeps 16 bits: beside the results' rounding
+    (of the exact result itself) only 2^-16 of it and the logits' error are left."""
+    H, V = 264, 1500
+    x, w, t, dl = make(T, H, V, 43)
+    x, w = x.bfloat16(), w.bfloat16()
+    op = m.LinearCrossEntropy(T, H, V, reduction="none", ignore_index=IGNORE)
+    op.forward(x, w, t)
+    dx, dw = op.backward(x, w, t, dl)
+    xd, wd = x.double(), w.double()
+    z = xd @ wd.t()
+    d = (torch.softmax(z, 1) - torch.nn.functional.one_hot(t.long(), V)) * dl.double()[:, None]
+    zb = 8 * math.sqrt(H) * F * float(xd.norm(dim=1).max() * wd.norm(dim=1).max()) + 16 * F * float(z.abs().max())
+    for got, want in ((dx, d @ wd), (dw, d.t() @ xd)):
+        own = float((want.bfloat16().double() - want).norm())
+        left = (4 * zb + 2.0 ** -16 + 16 * F) * float(want.norm())
+        assert float((got.double() - want).norm()) <= 1.05 * own + left
+
+
 # ---------------------------------------------------------------------------
 # one workspace for several shapes and operators
 # ---------------------------------------------------------------------------

@@ -619,6 +619,7 @@ def moe_grad_clip_workspace_bytes(tensors) -> int:
 
 def moe_grad_clip_plan(tensors, ws, stream=None) -> MoEGradPlan:
     plan = MoEGradPlan()
+    _on_device(ws)
     _check(lib().moe_grad_clip_plan(tensors, len(tensors), ctypes.byref(plan), _p(ws), _nbytes(ws),
                                     _stream(stream)), "moe_grad_clip_plan")
     return plan

@@ -119,3 +119,13 @@ def test_the_current_stream_without_torch_internals(m, monkeypatch):
     monkeypatch.setattr(m, "_raw_stream", lambda device: 100 + device)
     assert m._stream(None) == 105
     assert m._stream(17) == 17
+
+
+def test_a_plan_needs_device_memory(m):
+    table = (m.MoEGradTensor * 1)()
+    table[0].src, table[0].numel, table[0].src_dtype, table[0].dst_dtype = 256, 100, m.MOE_F32, m.MOE_F32
+    ws = torch.zeros(m.moe_grad_clip_workspace_bytes(table) + 256, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="workspace must be a CUDA tensor"):
+        m.moe_grad_clip_plan(table, ws, stream=0)
+    with pytest.raises(ValueError, match="workspace must be a CUDA tensor"):
+        m.moe_grad_clip_plan(table, None, stream=0)

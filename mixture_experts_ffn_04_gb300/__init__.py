@@ -13,7 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -26,6 +26,7 @@ MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE = 0, 1, 2, 3
 MOE_ERR_CUDA, MOE_ERR_DEVICE_ROUTE, MOE_ERR_TIMEOUT, MOE_ERR_ROWS = 4, 5, 6, 7
 MOE_ERR_GATHER = 8
 MOE_ERR_TARGET = 9
+MOE_ERR_TOKEN = 10
 MOE_F32, MOE_BF16 = 0, 1
 STAGES = ("residual_setup", "route", "permute", "gate_up", "down", "shared", "combine")
 
@@ -82,6 +83,43 @@ class MoEGradPlan(ctypes.Structure):
                 ("chunk_elems", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class MoEEmbedShape(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("hidden", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("padding_idx", ctypes.c_int32),
+                ("scale", ctypes.c_double), ("w_stride", ctypes.c_int64)]
+
+
+class MoEBlockNormShape(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("hidden", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("gate", ctypes.c_int32), ("unit_offset", ctypes.c_int32),
+                ("residual_scale", ctypes.c_double), ("eps", ctypes.c_double)]
+
+
+MOE_ORTH_MAX_STEPS = 16
+
+
+class MoEOrthCoefs(ctypes.Structure):
+    _fields_ = [("steps", ctypes.c_int32), ("reserved", ctypes.c_int32), ("eps", ctypes.c_double),
+                ("coef", (ctypes.c_double * 3) * MOE_ORTH_MAX_STEPS)]
+
+
+class MoEOrthShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class MoEMuonTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("momentum", ctypes.c_void_p),
+                ("batch", ctypes.c_int64), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
+                ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32)]
+
+
+class MoEMuonConfig(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("momentum", ctypes.c_double),
+                ("weight_decay", ctypes.c_double), ("nesterov", ctypes.c_int32),
+                ("scale", ctypes.c_int32), ("coefs", MoEOrthCoefs)]
+
+
 class MoERouteInfo(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "topk_idx", "topk_w", "gate", "counts", "offsets", "scatter_index", "row_token",
@@ -103,6 +141,8 @@ def lib():
     P, S, i32, i64, u32, sz = (ctypes.c_void_p, ctypes.POINTER(MoEShape), ctypes.c_int32,
                                ctypes.c_int64, ctypes.c_uint32, ctypes.c_size_t)
     C = ctypes.POINTER(MoECeShape)
+    M, N = ctypes.POINTER(MoEEmbedShape), ctypes.POINTER(MoEBlockNormShape)
+    O, K = ctypes.POINTER(MoEOrthShape), ctypes.POINTER(MoEOrthCoefs)
     sig = {
         "moe_topk_pack": (u32, [i32, i32]),
         "moe_topk_unpack": (i32, [u32, ctypes.POINTER(i32), ctypes.POINTER(i32)]),
@@ -154,6 +194,17 @@ def lib():
         "moe_grad_clip_workspace_bytes": (sz, [P, i64]),
         "moe_grad_clip_plan": (i32, [P, i64, ctypes.POINTER(MoEGradPlan), P, sz, P]),
         "moe_grad_clip": (i32, [ctypes.POINTER(MoEGradPlan), ctypes.c_double, P, P, sz, P]),
+        # operators between the layer and the rest of a model (moe_model.h)
+        "moe_embed_workspace_bytes": (sz, [M]),
+        "moe_embed_forward": (i32, [M, P, P, P, P, sz, P]),
+        "moe_embed_backward": (i32, [M, P, P, P, P, P, sz, P]),
+        "moe_block_norm_workspace_bytes": (sz, [N]),
+        "moe_block_norm_forward": (i32, [N] + [P] * 9),
+        "moe_block_norm_backward": (i32, [N] + [P] * 14 + [sz, P]),
+        "moe_orthogonalize_workspace_bytes": (sz, [O, K]),
+        "moe_orthogonalize": (i32, [O, K, P, P, P, sz, P]),
+        "moe_muon_workspace_bytes": (sz, [P, i64, ctypes.POINTER(MoEMuonConfig)]),
+        "moe_muon_step": (i32, [P, i64, ctypes.POINTER(MoEMuonConfig), P, sz, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -633,6 +684,149 @@ def moe_grad_clip(plan: MoEGradPlan, max_norm: float, norm, ws, stream=None):
 
 
 # ---------------------------------------------------------------------------
+# embedding, block norms, orthogonalised update (moe_model.h), name for name
+# ---------------------------------------------------------------------------
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN = 0, 1, 2
+MOE_MUON_SCALE_NONE, MOE_MUON_SCALE_SPECTRAL, MOE_MUON_SCALE_RMS = 0, 1, 2
+
+
+def _here(ws: torch.Tensor, **tensors):
+    """_on_device, and that device is the current one: the launch goes to a stream of
+    the current device."""
+    _on_device(ws, **tensors)
+    if torch.cuda.current_device() != ws.get_device():
+        raise ValueError("the tensors are on %s, the current device is cuda:%d"
+                         % (ws.device, torch.cuda.current_device()))
+
+
+def _maybe(t, n, dtype, name):
+    return None if t is None else _vec(t, n, dtype, name)
+
+
+def _act(shape):
+    return torch.float32 if shape.dtype == MOE_F32 else torch.bfloat16
+
+
+def moe_embed_workspace_bytes(shape: MoEEmbedShape) -> int:
+    return int(lib().moe_embed_workspace_bytes(ctypes.byref(shape)))
+
+
+def moe_embed_forward(shape: MoEEmbedShape, w, ids, y, ws, stream=None):
+    """w may be rows of a wider buffer (the stride goes into the shape)."""
+    dt, T, H = _act(shape), shape.tokens, shape.hidden
+    wp, shape.w_stride = _rows(w, shape.vocab, H, dt, "w")
+    args = (_vec(ids, T, torch.int32, "ids"), _vec(y, T * H, dt, "y"))
+    _here(ws, w=w, ids=ids, y=y)
+    _check(lib().moe_embed_forward(ctypes.byref(shape), wp, *args, _p(ws), _nbytes(ws),
+                                   _stream(stream)), "moe_embed_forward")
+
+
+def moe_embed_backward(shape: MoEEmbedShape, ids, dy, dw_add, dw, ws, stream=None):
+    dt, T, H, V = _act(shape), shape.tokens, shape.hidden, shape.vocab
+    args = (_vec(ids, T, torch.int32, "ids"), _vec(dy, T * H, dt, "dy"),
+            _maybe(dw_add, V * H, dt, "dw_add"), _vec(dw, V * H, dt, "dw"))
+    _here(ws, ids=ids, dy=dy, dw_add=dw_add, dw=dw)
+    _check(lib().moe_embed_backward(ctypes.byref(shape), *args, _p(ws), _nbytes(ws),
+                                    _stream(stream)), "moe_embed_backward")
+
+
+def moe_block_norm_workspace_bytes(shape: MoEBlockNormShape) -> int:
+    return int(lib().moe_block_norm_workspace_bytes(ctypes.byref(shape)))
+
+
+def _gate(shape, gate, name):
+    if shape.gate == MOE_GATE_TOKEN:
+        return _maybe(gate, shape.tokens, torch.float32, name)
+    return _maybe(gate, shape.hidden, _act(shape), name)
+
+
+def moe_block_norm_forward(shape: MoEBlockNormShape, x, y, w_post, gate, w_pre, s, h, rstd,
+                           stream=None):
+    dt, n, H = _act(shape), shape.tokens * shape.hidden, shape.hidden
+    args = (_vec(x, n, dt, "x"), _maybe(y, n, dt, "y"), _maybe(w_post, H, dt, "w_post"),
+            _gate(shape, gate, "gate"), _maybe(w_pre, H, dt, "w_pre"), _maybe(s, n, dt, "s"),
+            _maybe(h, n, dt, "h"), _maybe(rstd, 2 * shape.tokens, torch.float32, "rstd"))
+    _here(x, y=y, w_post=w_post, gate=gate, w_pre=w_pre, s=s, h=h, rstd=rstd)
+    _check(lib().moe_block_norm_forward(ctypes.byref(shape), *args, _stream(stream)),
+           "moe_block_norm_forward")
+
+
+def moe_block_norm_backward(shape: MoEBlockNormShape, ds, dh, x, y, w_post, gate, w_pre, rstd, dx,
+                            dy, dw_post, dgate, dw_pre, ws, stream=None):
+    dt, n, H = _act(shape), shape.tokens * shape.hidden, shape.hidden
+    args = (_maybe(ds, n, dt, "ds"), _maybe(dh, n, dt, "dh"), _vec(x, n, dt, "x"),
+            _maybe(y, n, dt, "y"), _maybe(w_post, H, dt, "w_post"), _gate(shape, gate, "gate"),
+            _maybe(w_pre, H, dt, "w_pre"), _vec(rstd, 2 * shape.tokens, torch.float32, "rstd"),
+            _maybe(dx, n, dt, "dx"), _maybe(dy, n, dt, "dy"), _maybe(dw_post, H, dt, "dw_post"),
+            _gate(shape, dgate, "dgate"), _maybe(dw_pre, H, dt, "dw_pre"))
+    _here(ws, ds=ds, dh=dh, x=x, y=y, w_post=w_post, gate=gate, w_pre=w_pre, rstd=rstd, dx=dx, dy=dy,
+          dw_post=dw_post, dgate=dgate, dw_pre=dw_pre)
+    _check(lib().moe_block_norm_backward(ctypes.byref(shape), *args, _p(ws), _nbytes(ws),
+                                         _stream(stream)), "moe_block_norm_backward")
+
+
+def orth_coefs(coefficients=(3.4445, -4.7750, 2.0315), steps: int = 5, eps: float = 1e-7) -> MoEOrthCoefs:
+    """MoEOrthCoefs of one (a, b, c) for every step, or of a sequence of them, one a
+    step (steps is then its length)."""
+    each = list(coefficients)
+    if each and not hasattr(each[0], "__len__"):
+        each = [each] * steps
+    if not 1 <= len(each) <= MOE_ORTH_MAX_STEPS or any(len(t) != 3 for t in each):
+        raise ValueError("coefficients must be (a, b, c) with 1 to %d steps, or as many triples"
+                         % MOE_ORTH_MAX_STEPS)
+    c = MoEOrthCoefs()
+    c.steps, c.eps = len(each), eps
+    for i, t in enumerate(each):
+        for j in range(3):
+            c.coef[i][j] = t[j]
+    return c
+
+
+def moe_orthogonalize_workspace_bytes(shape: MoEOrthShape, coefs: MoEOrthCoefs) -> int:
+    return int(lib().moe_orthogonalize_workspace_bytes(ctypes.byref(shape), ctypes.byref(coefs)))
+
+
+def moe_orthogonalize(shape: MoEOrthShape, coefs: MoEOrthCoefs, x, out, ws, stream=None):
+    dt, n = _act(shape), shape.batch * shape.rows * shape.cols
+    args = (_vec(x, n, dt, "x"), _vec(out, n, dt, "out"))
+    _here(ws, x=x, out=out)
+    _check(lib().moe_orthogonalize(ctypes.byref(shape), ctypes.byref(coefs), *args, _p(ws),
+                                   _nbytes(ws), _stream(stream)), "moe_orthogonalize")
+
+
+def muon_tensors(params, grads, momenta):
+    """MoEMuonTensor array over parameters [..., rows, cols] (the leading dimensions
+    are a batch of matrices), their gradients and fp32 momenta."""
+    params, grads, momenta = list(params), list(grads), list(momenta)
+    if not len(params) == len(grads) == len(momenta):
+        raise ValueError("every parameter needs one gradient and one momentum")
+    arr = (MoEMuonTensor * len(params))()
+    for e, w, g, v in zip(arr, params, grads, momenta):
+        if w.dim() < 2 or g.shape != w.shape or v.shape != w.shape or v.dtype != torch.float32:
+            raise ValueError("a parameter must be a matrix or a batch of them, its gradient and fp32 "
+                             "momentum of the same shape, got %s, %s and %s %s"
+                             % (tuple(w.shape), tuple(g.shape), tuple(v.shape), v.dtype))
+        for t in (w, g, v):
+            if not t.is_cuda or t.device != params[0].device:
+                raise ValueError("parameters, gradients and momenta must be on one CUDA device")
+        e.param, e.grad, e.momentum = _p(w), _p(g), _p(v)
+        e.rows, e.cols = w.shape[-2], w.shape[-1]
+        e.batch = w.numel() // max(1, w.shape[-2] * w.shape[-1])
+        e.param_dtype, e.grad_dtype = _dtype_code(w.dtype), _dtype_code(g.dtype)
+    return arr
+
+
+def moe_muon_workspace_bytes(tensors, config: MoEMuonConfig) -> int:
+    return int(lib().moe_muon_workspace_bytes(tensors, len(tensors), ctypes.byref(config)))
+
+
+def moe_muon_step(tensors, config: MoEMuonConfig, ws, stream=None):
+    _here(ws)
+    _check(lib().moe_muon_step(tensors, len(tensors), ctypes.byref(config), _p(ws), _nbytes(ws),
+                               _stream(stream)), "moe_muon_step")
+
+
+# ---------------------------------------------------------------------------
 # conveniences over the ABI (allocation through torch, nothing else)
 # ---------------------------------------------------------------------------
 def shape_for(wl, T: Optional[int] = None) -> MoEShape:
@@ -833,6 +1027,156 @@ class GradClip:
             norm = _empty(stream, 1, torch.float32, self.ws.device)
         moe_grad_clip(self.plan, max_norm, norm, self.ws, stream)
         return norm
+
+    def device_status(self, stream=None):
+        return moe_get_device_status(self.ws, stream)
+
+
+class TokenEmbedding:
+    """Rows of a table looked up by token id, times a scale, and the table's
+    gradient: shape and a workspace over caller tensors.  w [vocab, hidden] may be rows
+    of a wider buffer; ids is int32 [tokens].  Tokens of padding_idx get no gradient, an id
+    out of range a zero row and a bit of the device status.  Streams as in
+    LinearCrossEntropy."""
+
+    def __init__(self, tokens: int, hidden: int, vocab: int, dtype=torch.bfloat16, scale: float = 1.0,
+                 padding_idx: Optional[int] = None, device="cuda"):
+        s = MoEEmbedShape()
+        s.tokens, s.hidden, s.vocab, s.dtype = tokens, hidden, vocab, _dtype_code(dtype)
+        s.padding_idx, s.scale = -1 if padding_idx is None else padding_idx, scale
+        self.shape, self.dtype = s, dtype
+        self.ws = _alloc_ws(moe_embed_workspace_bytes(s), device, None, "TokenEmbedding")
+
+    def forward(self, w, ids, y=None, stream=None):
+        """y [tokens, hidden]."""
+        if y is None:
+            y = _empty(stream, (self.shape.tokens, self.shape.hidden), w.dtype, w.device)
+        moe_embed_forward(self.shape, w, ids, y, self.ws, stream)
+        return y
+
+    def backward(self, ids, dy, dw_add=None, dw=None, stream=None):
+        """dw [vocab, hidden], plus dw_add where given (the gradient of a classifier
+        that shares the table); dw_add may be dw: only rows with tokens are touched."""
+        if dw is None:
+            dw = _empty(stream, (self.shape.vocab, self.shape.hidden), dy.dtype, dy.device)
+        moe_embed_backward(self.shape, ids, dy, dw_add, dw, self.ws, stream)
+        return dw
+
+    def device_status(self, stream=None):
+        return moe_get_device_status(self.ws, stream)
+
+
+class BlockGrads(NamedTuple):
+    """What BlockNorm.backward computes; None where the input is."""
+    dx: torch.Tensor
+    dy: Optional[torch.Tensor]
+    dw_post: Optional[torch.Tensor]
+    dgate: Optional[torch.Tensor]
+    dw_pre: Optional[torch.Tensor]
+
+
+class BlockNorm:
+    """The norms before and after a block with its gate and the residual, in one pass:
+
+        s = residual_scale * x + gate * RMSNorm(y; w_post),  h = RMSNorm(s; w_pre)
+
+    gate: None, "channel" ([hidden] in dtype) or "token" ([tokens] fp32); unit_offset:
+    the weights count from 1.  Without y (the norm before the first block) s is
+    residual_scale * x, without w_pre there is no h, without w_post y is taken as it is.
+    Streams as in LinearCrossEntropy."""
+
+    def __init__(self, tokens: int, hidden: int, dtype=torch.bfloat16, gate: Optional[str] = None,
+                 residual_scale: float = 1.0, eps: float = 1e-6, unit_offset: bool = False,
+                 device="cuda"):
+        s = MoEBlockNormShape()
+        s.tokens, s.hidden, s.dtype = tokens, hidden, _dtype_code(dtype)
+        s.gate = {None: MOE_GATE_NONE, "none": MOE_GATE_NONE, "channel": MOE_GATE_CHANNEL,
+                  "token": MOE_GATE_TOKEN}[gate]
+        s.residual_scale, s.eps, s.unit_offset = residual_scale, eps, int(unit_offset)
+        self.shape, self.dtype = s, dtype
+        self.ws = _alloc_ws(moe_block_norm_workspace_bytes(s), device, None, "BlockNorm")
+        self.rstd = torch.zeros((tokens, 2), dtype=torch.float32, device=device)
+
+    def forward(self, x, y=None, w_post=None, gate=None, w_pre=None, s=None, h=None, stream=None):
+        """(s, h); self.rstd is what the backward needs."""
+        if s is None:
+            s = _empty(stream, x.shape, x.dtype, x.device)
+        if h is None and w_pre is not None:
+            h = _empty(stream, x.shape, x.dtype, x.device)
+        moe_block_norm_forward(self.shape, x, y, w_post, gate, w_pre, s, h, self.rstd, stream)
+        return s, h
+
+    def backward(self, ds, dh, x, y=None, w_post=None, gate=None, w_pre=None, dx=None, dy=None,
+                 dw_post=None, dgate=None, dw_pre=None, stream=None) -> BlockGrads:
+        """Gradients after a forward with the same inputs, given ds (of s, or None for
+        zeros) and dh (of h)."""
+        def like(out, t):
+            return _empty(stream, t.shape, t.dtype, t.device) if out is None and t is not None else out
+
+        d = BlockGrads(like(dx, x), like(dy, y), like(dw_post, w_post), like(dgate, gate),
+                       like(dw_pre, w_pre))
+        moe_block_norm_backward(self.shape, ds, dh, x, y, w_post, gate, w_pre, self.rstd, *d, self.ws,
+                                stream)
+        return d
+
+    def device_status(self, stream=None):
+        return moe_get_device_status(self.ws, stream)
+
+
+class Orthogonalize:
+    """A batch of matrices with their singular values taken towards 1 by `steps`
+    Newton-Schulz products: shape, coefficients and a workspace over caller tensors.
+    coefficients: (a, b, c), or one triple a step.  Streams as in LinearCrossEntropy."""
+
+    def __init__(self, batch: int, rows: int, cols: int, dtype=torch.bfloat16,
+                 coefficients=(3.4445, -4.7750, 2.0315), steps: int = 5, eps: float = 1e-7,
+                 device="cuda"):
+        s = MoEOrthShape()
+        s.batch, s.rows, s.cols, s.dtype = batch, rows, cols, _dtype_code(dtype)
+        self.shape, self.coefs = s, orth_coefs(coefficients, steps, eps)
+        self.ws = _alloc_ws(moe_orthogonalize_workspace_bytes(s, self.coefs), device, None, "Orthogonalize")
+
+    def forward(self, x, out=None, stream=None):
+        """out [batch, rows, cols]; may be x."""
+        if out is None:
+            out = _empty(stream, x.shape, x.dtype, x.device)
+        moe_orthogonalize(self.shape, self.coefs, x, out, self.ws, stream)
+        return out
+
+    def device_status(self, stream=None):
+        return moe_get_device_status(self.ws, stream)
+
+
+class Muon:
+    """Momentum and orthogonalised update of a list of weight matrices (each [..., rows,
+    cols], the leading dimensions a batch of matrices), in place.  scale: "none",
+    "spectral" (sqrt(max(1, rows / cols))) or "rms" (0.2 sqrt(max(rows, cols))).  The
+    tensors must stay where they are; momenta (fp32) are made here unless given.
+    Streams as in LinearCrossEntropy."""
+
+    def __init__(self, params, grads, momenta=None, lr: float = 0.02, momentum: float = 0.95,
+                 nesterov: bool = True, weight_decay: float = 0.0, scale: str = "spectral",
+                 coefficients=(3.4445, -4.7750, 2.0315), steps: int = 5, eps: float = 1e-7):
+        self.params, self.grads = list(params), list(grads)
+        if not self.params:
+            raise ValueError("the list of parameters is empty")
+        if momenta is None:
+            momenta = [torch.zeros(p.shape, dtype=torch.float32, device=p.device) for p in self.params]
+        self.momenta = list(momenta)
+        self.tensors = muon_tensors(self.params, self.grads, self.momenta)
+        c = MoEMuonConfig()
+        c.lr, c.momentum, c.weight_decay, c.nesterov = lr, momentum, weight_decay, int(nesterov)
+        c.scale = {"none": MOE_MUON_SCALE_NONE, "spectral": MOE_MUON_SCALE_SPECTRAL,
+                   "rms": MOE_MUON_SCALE_RMS}[scale]
+        c.coefs = orth_coefs(coefficients, steps, eps)
+        self.config = c
+        self.ws = _alloc_ws(moe_muon_workspace_bytes(self.tensors, c), self.params[0].device, None, "Muon")
+
+    def step(self, lr: Optional[float] = None, stream=None):
+        """One update; lr stays what it was last set to."""
+        if lr is not None:
+            self.config.lr = lr
+        moe_muon_step(self.tensors, self.config, self.ws, stream)
 
     def device_status(self, stream=None):
         return moe_get_device_status(self.ws, stream)

@@ -18,6 +18,7 @@ enum : uint32_t {
   kFlagTimeout = 1u << 2,  // a bounded pipeline wait ran out
   kFlagGather = 1u << 3,   // a gathered row's token outside [0, tokens)
   kFlagTarget = 1u << 4,   // a target outside [0, vocab) that is not ignore_index
+  kFlagToken = 1u << 5,    // a token id outside [0, vocab)
 };
 
 typedef __nv_bfloat16 bf16;

@@ -125,49 +125,6 @@ struct Args {
   int chunk;   // k-blocks the tensor cores add up before the fp32 registers do
 };
 
-// Cluster-scope wait that lets the hardware suspend the thread (bounded like
-// wait2): a spinning warp takes issue slots and, under the power cap, clock.
-__device__ __forceinline__ bool wait_cl(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  auto ready = [&]() {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-  };
-  if (ready()) return true;
-  const long long t0 = clock64();
-  while (true) {
-    if (ready()) return true;
-    if (*abort_flag) return false;
-    if (clock64() - t0 > kWaitCycles) {
-      *abort_flag = 1;
-      return false;
-    }
-  }
-}
-
-// Arrival without a memory fence: for barriers that only say "this slot or
-// accumulator has been read".  A releasing arrival waits for the thread's own
-// global stores, which here are the previous tile's output.
-__device__ __forceinline__ void arrive_relaxed(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
-__device__ __forceinline__ uint64_t mn_desc(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(BOX_BYTES >> 4) << 16;   // next 64 columns
-  d |= (uint64_t)(1024 >> 4) << 32;        // next 8 k-rows
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
-
 // Plane products in ascending weight: (0,2) (2,0) (1,1) (0,1) (1,0) (0,0).
 __device__ __forceinline__ void plane_pair(int planes, int i, int& pa, int& pb) {
   if (planes == 1) { pa = pb = 0; return; }
@@ -271,20 +228,7 @@ __device__ __forceinline__ float pick(float a, float b, int i, int j) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Output goes through a warp's staging slice (32 rows of 128 bytes, 128-byte
-// swizzle: conflict-free 16-byte pieces) and out by TMA, one box a slice: with a
-// lane storing its own row instead, every instruction touches 32 lines, and a
-// 256 x 256 bf16 tile took the SM about 6000 clocks.  add: the box is added to
-// what is there (fp32).
-__device__ __forceinline__ void put_piece(uint32_t stage, int lane, int j, uint4 v) {
-  const uint32_t at = stage + lane * 128 + ((j ^ (lane & 7)) << 4);
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-               : "memory");
-}
-__device__ __forceinline__ void stage_free(int lane) {
-  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-  __syncwarp();
-}
+// A warp's slice (tc_pair.cuh) out as one box; add: it is added to what is there (fp32).
 __device__ __forceinline__ void stage_out(const CUtensorMap* map, uint32_t stage, int lane, int col, int row,
                                           bool add) {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -302,17 +246,6 @@ __device__ __forceinline__ void stage_out(const CUtensorMap* map, uint32_t stage
                    : "memory");
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   }
-}
-
-// A piece of the warp's slice back: 16 bytes j of this lane's row.
-__device__ __forceinline__ uint4 get_piece(uint32_t stage, int lane, int j) {
-  const uint32_t at = stage + lane * 128 + ((j ^ (lane & 7)) << 4);
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(at)
-               : "memory");
-  return v;
 }
 
 // Rows of dX that go to their tokens are stored by the lane that owns the row, in

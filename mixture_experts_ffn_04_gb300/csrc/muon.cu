@@ -1,0 +1,672 @@
+// muon.cu -- orthogonalised update of weight matrices (include/moe_model.h): the
+// momentum, the matrices' norms, the fp16 planes that the products of orth_tc.cu
+// read, and the update of the parameters.
+//
+// Tensors with the same smaller and larger side and the same precision form a
+// bucket, whose matrices go through the products together, at most so many at a time
+// as kScratch bytes of scratch hold.  A matrix is laid out with its smaller side as
+// rows (one with more rows than columns is transposed on the way in and out), so the
+// products see one shape.
+//
+// Bound by HBM: a bf16 parameter reads gradient and momentum twice (for the norm, then
+// for the scaled planes), writes the momentum, and passes once more for the update.
+#include <algorithm>
+#include <cmath>
+
+#include "../../include/moe_model.h"
+#include "common.cuh"
+#include "internal.h"
+#include "orth.h"
+#include "train.h"
+
+namespace moe {
+namespace muon {
+
+constexpr int kSegs = 16;                       // tensors a launch carries in its arguments
+constexpr int64_t kScratch = 3ll << 30;         // bytes of one round's matrices
+constexpr int64_t kMaxRound = 16384;            // matrices of a round
+constexpr int kPart = 8192;                     // elements of a partial sum of squares
+constexpr int kTile = 64;
+
+// Matrices of one tensor that take part in a round: `count` from its matrix
+// `first`, the round's matrices `at` and on.
+struct Seg {
+  void* param;        // also the output of the matrices alone
+  const void* grad;
+  float* momentum;    // NULL: u is grad itself
+  int64_t first;
+  int32_t at, count;
+  int32_t rows, cols, pdtype, gdtype;
+  float size;         // lr * size of the update
+};
+
+struct Round {
+  Seg seg[kSegs];
+  int32_t segs, batch;
+  int32_t m, n, ldx, parts;   // of a matrix: sides, row length in scratch, partial sums
+  float beta, rest, keep;     // momentum, 1 - momentum; 1 - lr * weight_decay
+  int32_t nesterov, update;   // update: param = keep param - size X, else out = X
+  double eps;
+  double* sums;               // [batch][parts]
+  __half* x;                  // [2][batch][m][ldx]
+};
+
+__device__ __forceinline__ const Seg& seg_of(const Round& r, int b) {
+  int s = 0;
+  while (s + 1 < r.segs && r.seg[s + 1].at <= b) ++s;
+  return r.seg[s];
+}
+
+// 8 consecutive elements of a row or of the whole matrix, as floats; `n` of them
+// exist.  vec: 16-byte aligned and all there.
+__device__ __forceinline__ void read8(const void* p, int dtype, int64_t at, int n, bool vec, float* f) {
+  if (dtype == MOE_F32) {
+    const float* q = static_cast<const float*>(p) + at;
+    if (vec) {
+      unpack16(reinterpret_cast<const uint4*>(q)[0], f, (const float*)nullptr);
+      unpack16(reinterpret_cast<const uint4*>(q)[1], f + 4, (const float*)nullptr);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = e < n ? q[e] : 0.0f;
+    }
+  } else {
+    const bf16* q = static_cast<const bf16*>(p) + at;
+    if (vec) {
+      unpack16(reinterpret_cast<const uint4*>(q)[0], f, (const bf16*)nullptr);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = e < n ? __bfloat162float(q[e]) : 0.0f;
+    }
+  }
+}
+__device__ __forceinline__ void write8(void* p, int dtype, int64_t at, int n, bool vec, const float* f) {
+  if (dtype == MOE_F32) {
+    float* q = static_cast<float*>(p) + at;
+    if (vec) {
+      reinterpret_cast<uint4*>(q)[0] = pack16(f, (const float*)nullptr);
+      reinterpret_cast<uint4*>(q)[1] = pack16(f + 4, (const float*)nullptr);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < n) q[e] = f[e];
+    }
+  } else {
+    bf16* q = static_cast<bf16*>(p) + at;
+    if (vec) {
+      *reinterpret_cast<uint4*>(q) = pack16(f, (const bf16*)nullptr);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < n) q[e] = __float2bfloat16_rn(f[e]);
+    }
+  }
+}
+__device__ __forceinline__ bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// The direction's element from a gradient's and the new momentum's.
+__device__ __forceinline__ float direction(const Round& r, float g, float v) {
+  return r.nesterov ? fmaf(r.beta, v, r.rest * g) : v;
+}
+
+// Momentum, and the sum of u^2 over kPart elements of a matrix: in fp32 over a warp's
+// elements, in fp64 beyond.  A warp whose sum overflowed, or is small enough for
+// squares to have underflowed, adds again with its values scaled by a power of two.
+__global__ void __launch_bounds__(256) momentum_kernel(const __grid_constant__ Round r) {
+  __shared__ double sh[8];
+  pdl_trigger();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t tasks = (int64_t)r.batch * r.parts;
+  for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
+    const int b = (int)(task / r.parts), part = (int)(task - (int64_t)b * r.parts);
+    const Seg& s = seg_of(r, b);
+    const int64_t each = (int64_t)s.rows * s.cols;
+    const int64_t base = (s.first + (b - s.at)) * each;      // the matrix in its tensor
+    const bool ok = each % 8 == 0 && aligned(s.grad) && aligned(s.momentum);
+    float u[kPart / 256 / 8][8];
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kPart / 256 / 8; ++k) {
+      const int64_t at = (int64_t)part * kPart + (k * 256 + threadIdx.x) * 8;
+      const int n = at >= each ? 0 : (each - at < 8 ? (int)(each - at) : 8);
+      float g[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u[k][e] = 0.0f;
+      if (n > 0) {
+        read8(s.grad, s.gdtype, base + at, n, ok, g);
+        if (s.momentum != nullptr) {
+          float v[8];
+          read8(s.momentum, MOE_F32, base + at, n, ok, v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            v[e] = fmaf(r.beta, v[e], r.rest * g[e]);
+            u[k][e] = e < n ? direction(r, g[e], v[e]) : 0.0f;
+          }
+          write8(s.momentum, MOE_F32, base + at, n, ok, v);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) u[k][e] = g[e];
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = fmaf(u[k][e], u[k][e], sum);
+    }
+    auto all = [](float v) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      return v;
+    };
+    auto squares = [&](float scale) {
+      float t = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kPart / 256 / 8; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float v = u[k][e] * scale;
+          t = fmaf(v, v, t);
+        }
+      return (double)all(t);
+    };
+    double total = (double)all(sum);
+    if (!(total >= 1e-28)) total = squares(0x1p80f) * 0x1p-160;
+    else if (!(total <= 1e38)) total = squares(0x1p-96f) * 0x1p192;
+    __syncthreads();
+    if (lane == 0) sh[warp] = total;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      double t = 0.0;
+      for (int w = 0; w < 8; ++w) t += sh[w];
+      r.sums[task] = t;
+    }
+  }
+}
+
+// Two factors whose product is 2^kOrthX / (norm + eps): one would leave fp32 for
+// norms far from 1.
+__device__ __forceinline__ float2 scale_of(double sum, double eps) {
+  const double norm = sqrt(sum);
+  if (!isfinite(norm)) return make_float2(__int_as_float(0x7fc00000), 1.0f);
+  if (norm == 0.0) return make_float2(0.0f, 0.0f);
+  int e;
+  const double f = frexp(norm + eps, &e);      // norm + eps = f 2^e
+  const int h = -e / 2;
+  return make_float2(ldexpf(1.0f, h), (float)ldexp(1.0 / f, kOrthX - e - h));
+}
+
+__device__ __forceinline__ void split8(const float* f, uint4& hi, uint4& lo) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 a = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+    const float2 v = __half22float2(a);
+    const __half2 c = __floats2half2_rn(f[2 * i] - v.x, f[2 * i + 1] - v.y);
+    h[i] = *reinterpret_cast<const uint32_t*>(&a);
+    l[i] = *reinterpret_cast<const uint32_t*>(&c);
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+struct TileAt {
+  int b, r0, c0;   // matrix of the round; first row and column of the tile in its tensor
+};
+__device__ __forceinline__ TileAt tile_at(const Round& r, int64_t task, const Seg*& s) {
+  // tiles of kTile x kTile over the larger and smaller side, whichever way round
+  const int tm = (r.m + kTile - 1) / kTile, tn = (r.n + kTile - 1) / kTile;
+  TileAt t;
+  t.b = (int)(task / ((int64_t)tm * tn));
+  const int l = (int)(task - (int64_t)t.b * tm * tn);
+  s = &seg_of(r, t.b);
+  const int tc = s->rows <= s->cols ? tn : tm;   // tiles along a row of the tensor
+  t.r0 = l / tc * kTile;
+  t.c0 = l % tc * kTile;
+  return t;
+}
+
+// u / (norm + eps) in two fp16 planes, its smaller side as rows.
+__global__ void __launch_bounds__(256) planes_kernel(const __grid_constant__ Round r) {
+  __shared__ float sh[kTile][kTile + 1];
+  __shared__ double part[8];
+  __shared__ float2 factor;
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x;
+  const int64_t tiles = (int64_t)((r.m + kTile - 1) / kTile) * ((r.n + kTile - 1) / kTile);
+  const int64_t plane = (int64_t)r.batch * r.m * r.ldx;
+  int last = -1;
+  // a block takes neighbouring tiles, so that a matrix's norm is added up once
+  const int64_t all = tiles * r.batch, each = (all + gridDim.x - 1) / gridDim.x;
+  const int64_t end = min(all, (blockIdx.x + 1) * each);
+  for (int64_t task = blockIdx.x * each; task < end; ++task) {
+    const Seg* s;
+    const TileAt t = tile_at(r, task, s);
+    if (t.b != last) {
+      last = t.b;
+      double v = 0.0;
+      for (int i = tid; i < r.parts; i += 256) v += __ldcg(r.sums + (int64_t)t.b * r.parts + i);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      __syncthreads();
+      if ((tid & 31) == 0) part[tid >> 5] = v;
+      __syncthreads();
+      if (tid == 0) {
+        double w = 0.0;
+        for (int i = 0; i < 8; ++i) w += part[i];
+        factor = scale_of(w, r.eps);
+      }
+      __syncthreads();
+    }
+    const float2 q = factor;
+    const bool tall = s->rows > s->cols;
+    const int64_t base = (s->first + (t.b - s->at)) * (int64_t)s->rows * s->cols;
+    const bool ok = s->cols % 8 == 0 && aligned(s->grad) && aligned(s->momentum);
+    __half* x = r.x + (int64_t)t.b * r.m * r.ldx;
+    if (tall) __syncthreads();   // the last tile's readers are done
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int lr = k * 32 + tid / 8, lc = tid % 8 * 8;
+      const int row = t.r0 + lr, col = t.c0 + lc;
+      const int n = row >= s->rows || col >= s->cols ? 0 : min(8, s->cols - col);
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = 0.0f;
+      if (n > 0) {
+        const int64_t at = base + (int64_t)row * s->cols + col;
+        read8(s->grad, s->gdtype, at, n, ok, f);
+        if (s->momentum != nullptr) {
+          float v[8];
+          read8(s->momentum, MOE_F32, at, n, ok, v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = direction(r, f[e], v[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = e < n ? f[e] * q.x * q.y : 0.0f;
+        if (!tall) {
+          uint4 hi, lo;
+          split8(f, hi, lo);
+          *reinterpret_cast<uint4*>(x + (int64_t)row * r.ldx + col) = hi;
+          *reinterpret_cast<uint4*>(x + plane + (int64_t)row * r.ldx + col) = lo;
+        }
+      }
+      if (tall) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sh[lr][lc + e] = f[e];
+      }
+    }
+    if (!tall) continue;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int lr = k * 32 + tid / 8, lc = tid % 8 * 8;   // of the transposed tile
+      const int row = t.c0 + lr, col = t.r0 + lc;
+      if (row >= r.m || col >= r.n) continue;
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = sh[lc + e][lr];
+      uint4 hi, lo;
+      split8(f, hi, lo);
+      *reinterpret_cast<uint4*>(x + (int64_t)row * r.ldx + col) = hi;
+      *reinterpret_cast<uint4*>(x + plane + (int64_t)row * r.ldx + col) = lo;
+    }
+  }
+}
+
+// param = keep param - size X, or out = X, from the two planes.
+__global__ void __launch_bounds__(256) update_kernel(const __grid_constant__ Round r) {
+  __shared__ float sh[kTile][kTile + 1];
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x;
+  const int64_t all = (int64_t)((r.m + kTile - 1) / kTile) * ((r.n + kTile - 1) / kTile) * r.batch;
+  const int64_t plane = (int64_t)r.batch * r.m * r.ldx;
+  for (int64_t task = blockIdx.x; task < all; task += gridDim.x) {
+    const Seg* s;
+    const TileAt t = tile_at(r, task, s);
+    const bool tall = s->rows > s->cols;
+    const int64_t base = (s->first + (t.b - s->at)) * (int64_t)s->rows * s->cols;
+    const bool ok = s->cols % 8 == 0 && aligned(s->param);
+    const __half* x = r.x + (int64_t)t.b * r.m * r.ldx;
+    auto load = [&](int row, int col, float* f) {
+      const uint4 hi = *reinterpret_cast<const uint4*>(x + (int64_t)row * r.ldx + col);
+      const uint4 lo = *reinterpret_cast<const uint4*>(x + plane + (int64_t)row * r.ldx + col);
+      const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&l[i]));
+        f[2 * i] = (a.x + b.x) * ldexpf(1.0f, -kOrthX);
+        f[2 * i + 1] = (a.y + b.y) * ldexpf(1.0f, -kOrthX);
+      }
+    };
+    if (tall) {
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int lr = k * 32 + tid / 8, lc = tid % 8 * 8;
+        const int row = t.c0 + lr, col = t.r0 + lc;
+        if (row < r.m && col < r.n) {
+          float f[8];
+          load(row, col, f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sh[lc + e][lr] = f[e];
+        }
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int lr = k * 32 + tid / 8, lc = tid % 8 * 8;
+      const int row = t.r0 + lr, col = t.c0 + lc;
+      const int n = row >= s->rows || col >= s->cols ? 0 : min(8, s->cols - col);
+      if (n <= 0) continue;
+      const int64_t at = base + (int64_t)row * s->cols + col;
+      float f[8];
+      if (tall) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = e < n ? sh[lr][lc + e] : 0.0f;
+      } else {
+        load(row, col, f);
+      }
+      if (r.update) {
+        float w[8];
+        read8(s->param, s->pdtype, at, n, ok, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = fmaf(-s->size, f[e], r.keep * w[e]);
+      }
+      write8(s->param, s->pdtype, at, n, ok, f);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+struct Bucket {
+  int m, n, planes;
+  int64_t batch;
+  int ldx, lda, parts;
+  int64_t each;    // scratch bytes of a matrix
+  int64_t round;   // matrices at a time
+};
+
+Bucket bucket_of(int m, int n, int planes, int64_t batch) {
+  Bucket b = {};
+  b.m = m;
+  b.n = n;
+  b.planes = planes;
+  b.batch = batch;
+  // rows on 128-byte boundaries where they are long enough for it
+  auto pad = [](int v) { return v >= 64 ? (v + 63) / 64 * 64 : (v + 7) / 8 * 8; };
+  b.ldx = pad(n);
+  b.lda = pad(m);
+  b.parts = (int)(((int64_t)m * n + kPart - 1) / kPart);
+  b.each = 4ll * m * b.ldx * 2 + 2ll * planes * m * b.lda * 2 + 8ll * b.parts;
+  b.round = std::max<int64_t>(1, std::min<int64_t>(batch, std::min<int64_t>(kMaxRound, kScratch / b.each)));
+  return b;
+}
+
+struct RoundLayout {
+  size_t sums, x[2], a, b, total;
+};
+RoundLayout layout_of(const Bucket& q) {
+  RoundLayout L;
+  size_t off = 256;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += (bytes + 255) & ~(size_t)255;
+    return at;
+  };
+  L.sums = take((size_t)q.round * q.parts * 8);
+  for (int i = 0; i < 2; ++i) L.x[i] = take((size_t)q.round * 4 * q.m * q.ldx);
+  L.a = take((size_t)q.round * q.planes * q.m * q.lda * 2);
+  L.b = take((size_t)q.round * q.planes * q.m * q.lda * 2);
+  L.total = off;
+  return L;
+}
+
+const char* check_coefs(const moe_orth_coefs& c) {
+  if (c.steps < 1 || c.steps > MOE_ORTH_MAX_STEPS) return "steps must be in [1, MOE_ORTH_MAX_STEPS]";
+  if (!(c.eps >= 0.0) || !std::isfinite(c.eps)) return "eps must be finite and >= 0";
+  if (c.reserved != 0) return "reserved must be 0";
+  double top = 1.0;   // of the singular values before the step
+  for (int i = 0; i < c.steps; ++i) {
+    const double a = c.coef[i][0], b = c.coef[i][1], d = c.coef[i][2];
+    if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(d)) return "coefficients must be finite";
+    // extremes of a s + b s^3 + d s^5 and of b s^2 + d s^4 over [0, top]
+    double x = 0.0, y = 0.0;
+    auto look = [&](double s2) {
+      if (!(s2 > 0.0) || s2 > top * top) return;
+      const double s = std::sqrt(s2);
+      x = std::max(x, std::fabs(s * (a + s2 * (b + s2 * d))));
+      y = std::max(y, std::fabs(s2 * (b + s2 * d)));
+    };
+    look(top * top);
+    if (d != 0.0) {
+      look(-b / (2.0 * d));
+      const double disc = 9.0 * b * b - 20.0 * a * d;
+      if (disc >= 0.0) {
+        look((-3.0 * b + std::sqrt(disc)) / (10.0 * d));
+        look((-3.0 * b - std::sqrt(disc)) / (10.0 * d));
+      }
+    } else if (b != 0.0) {
+      look(-a / (3.0 * b));
+    }
+    if (!(x <= kOrthMaxX)) return "a step's coefficients take singular values past 3.5";
+    if (!(y <= kOrthMaxB)) return "a step's b s^2 + c s^4 passes 100";
+    top = x;
+  }
+  return nullptr;
+}
+
+const char* check_sides(int64_t batch, int32_t rows, int32_t cols) {
+  if (batch < 0 || batch > (1 << 24)) return "batch must be in [0, 2^24]";
+  if (rows < 1 || cols < 1 || rows > 65536 || cols > 65536) return "rows and cols must be in [1, 65536]";
+  return nullptr;
+}
+
+// One round: the products of the matrices in r's segments.
+cudaError_t run_round(Round& r, const Bucket& q, const RoundLayout& L, char* ws, const moe_orth_coefs& c,
+                      cudaStream_t st) {
+  r.m = q.m;
+  r.n = q.n;
+  r.ldx = q.ldx;
+  r.parts = q.parts;
+  r.eps = c.eps;
+  r.sums = reinterpret_cast<double*>(ws + L.sums);
+  r.x = reinterpret_cast<__half*>(ws + L.x[0]);
+  const int64_t sms = tc_sm_count(), tiles = (int64_t)((q.m + kTile - 1) / kTile) * ((q.n + kTile - 1) / kTile) * r.batch;
+  cudaError_t e = launch_after(momentum_kernel, (unsigned)std::min<int64_t>((int64_t)r.batch * q.parts, 16 * sms), 256, 0,
+                               st, 1, r);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = (unsigned)std::min<int64_t>(tiles, 16 * sms);
+  e = launch_after(planes_kernel, grid, 256, 0, st, 1, r);
+  if (e != cudaSuccess) return e;
+  OrthBatch t = {};
+  t.batch = r.batch;
+  t.m = q.m;
+  t.n = q.n;
+  t.ldx = q.ldx;
+  t.lda = q.lda;
+  t.planes = q.planes;
+  t.x[0] = ws + L.x[0];
+  t.x[1] = ws + L.x[1];
+  t.a = ws + L.a;
+  t.b = ws + L.b;
+  t.flags = reinterpret_cast<uint32_t*>(ws);
+  e = launch_orth_steps(t, c.steps, c.coef, st);
+  if (e != cudaSuccess) return e;
+  r.x = reinterpret_cast<__half*>(ws + L.x[c.steps & 1]);
+  return launch_after(update_kernel, grid, 256, 0, st, 1, r);
+}
+
+moe_status check_list(const moe_muon_tensor* t, int64_t n, const moe_muon_config* c, const char** why) {
+  *why = nullptr;
+  if (n < 0 || n > 65536 || (n > 0 && !t)) *why = "tensors must be an array of 0 to 65536 entries";
+  else if (!c) *why = "config is NULL";
+  else *why = check_coefs(c->coefs);
+  if (*why) return MOE_ERR_INVALID_ARG;
+  if (!std::isfinite(c->lr) || !std::isfinite(c->weight_decay) || !(c->momentum >= 0.0 && c->momentum < 1.0))
+    *why = "lr and weight_decay must be finite, momentum in [0, 1)";
+  else if (c->nesterov != 0 && c->nesterov != 1) *why = "nesterov must be 0 or 1";
+  else if (c->scale < MOE_MUON_SCALE_NONE || c->scale > MOE_MUON_SCALE_RMS) *why = "scale must be a moe_muon_scale";
+  if (*why) return MOE_ERR_INVALID_ARG;
+  for (int64_t i = 0; i < n; ++i) {
+    for (int32_t d : {t[i].param_dtype, t[i].grad_dtype})
+      if (d != MOE_F32 && d != MOE_BF16) {
+        *why = "dtypes must be MOE_F32 or MOE_BF16";
+        return MOE_ERR_UNSUPPORTED;
+      }
+    *why = check_sides(t[i].batch, t[i].rows, t[i].cols);
+    if (*why) return MOE_ERR_INVALID_ARG;
+    if (t[i].batch == 0) continue;
+    if (!t[i].param || !t[i].grad || !t[i].momentum) *why = "param, grad and momentum must be non-NULL";
+    else if ((uintptr_t)t[i].param % (t[i].param_dtype == MOE_F32 ? 4 : 2) ||
+             (uintptr_t)t[i].grad % (t[i].grad_dtype == MOE_F32 ? 4 : 2) || (uintptr_t)t[i].momentum % 4)
+      *why = "param, grad and momentum must be aligned to their elements";
+    if (*why) return MOE_ERR_INVALID_ARG;
+  }
+  return MOE_OK;
+}
+
+struct Key {
+  int m, n, planes;
+};
+Key key_of(const moe_muon_tensor& t) {
+  return {std::min(t.rows, t.cols), std::max(t.rows, t.cols), t.param_dtype == MOE_F32 ? 2 : 1};
+}
+bool same(const Key& a, const Key& b) { return a.m == b.m && a.n == b.n && a.planes == b.planes; }
+
+// Calls f(bucket, its first tensor) for every bucket, in the order of first tensors.
+template <class F>
+moe_status each_bucket(const moe_muon_tensor* t, int64_t n, F f) {
+  for (int64_t i = 0; i < n; ++i) {
+    const Key k = key_of(t[i]);
+    bool seen = false;
+    for (int64_t j = 0; j < i && !seen; ++j) seen = same(key_of(t[j]), k);
+    if (seen) continue;
+    int64_t batch = 0;
+    for (int64_t j = i; j < n; ++j)
+      if (same(key_of(t[j]), k)) batch += t[j].batch;
+    if (batch == 0) continue;
+    const moe_status st = f(bucket_of(k.m, k.n, k.planes, batch), i);
+    if (st != MOE_OK) return st;
+  }
+  return MOE_OK;
+}
+
+float size_of(const moe_muon_config& c, const moe_muon_tensor& t) {
+  double s = 1.0;
+  if (c.scale == MOE_MUON_SCALE_SPECTRAL) s = std::sqrt(std::max(1.0, (double)t.rows / t.cols));
+  if (c.scale == MOE_MUON_SCALE_RMS) s = 0.2 * std::sqrt((double)std::max(t.rows, t.cols));
+  return (float)(c.lr * s);
+}
+
+moe_status check_shape(const moe_orth_shape* s, const moe_orth_coefs* c, const char** why) {
+  *why = nullptr;
+  if (!s || !c) *why = "shape and coefs must be non-NULL";
+  else if (s->dtype != MOE_F32 && s->dtype != MOE_BF16) {
+    *why = "dtype must be MOE_F32 or MOE_BF16";
+    return MOE_ERR_UNSUPPORTED;
+  } else if (s->reserved != 0) *why = "reserved must be 0";
+  else *why = check_sides(s->batch, s->rows, s->cols);
+  if (!*why) *why = check_coefs(*c);
+  return *why ? MOE_ERR_INVALID_ARG : MOE_OK;
+}
+Bucket bucket_of(const moe_orth_shape& s) {
+  return bucket_of(std::min(s.rows, s.cols), std::max(s.rows, s.cols), s.dtype == MOE_F32 ? 2 : 1, s.batch);
+}
+
+}  // namespace muon
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" size_t moe_orthogonalize_workspace_bytes(const moe_orth_shape* shape, const moe_orth_coefs* coefs) {
+  const char* why;
+  const moe_status st = muon::check_shape(shape, coefs, &why);
+  if (st != MOE_OK) {
+    fail(st, why);
+    return 0;
+  }
+  return muon::layout_of(muon::bucket_of(*shape)).total;
+}
+
+extern "C" moe_status moe_orthogonalize(const moe_orth_shape* shape, const moe_orth_coefs* coefs, const void* x,
+                                        void* out, void* ws, size_t ws_bytes, void* stream) {
+  reset_launch_count();
+  const char* why;
+  moe_status st = muon::check_shape(shape, coefs, &why);
+  if (st != MOE_OK) return fail(st, why);
+  if (shape->batch > 0 && (!x || !out)) return fail(MOE_ERR_INVALID_ARG, "x and out must be non-NULL");
+  const size_t esz = shape->dtype == MOE_F32 ? 4 : 2;
+  if ((uintptr_t)x % esz || (uintptr_t)out % esz) return fail(MOE_ERR_INVALID_ARG, "x and out must be aligned to their elements");
+  const muon::Bucket q = muon::bucket_of(*shape);
+  const muon::RoundLayout L = muon::layout_of(q);
+  st = check_ws(ws, ws_bytes, L.total);
+  if (st != MOE_OK) return st;
+  for (int64_t at = 0; at < shape->batch; at += q.round) {
+    muon::Round r = {};
+    r.batch = (int32_t)std::min<int64_t>(q.round, shape->batch - at);
+    r.segs = 1;
+    r.seg[0] = {out, x, nullptr, at, 0, r.batch, shape->rows, shape->cols, shape->dtype, shape->dtype, 0.0f};
+    CHECK_CUDA(muon::run_round(r, q, L, static_cast<char*>(ws), *coefs, (cudaStream_t)stream));
+  }
+  return MOE_OK;
+}
+
+extern "C" size_t moe_muon_workspace_bytes(const moe_muon_tensor* tensors, int64_t n, const moe_muon_config* config) {
+  const char* why;
+  const moe_status st = muon::check_list(tensors, n, config, &why);
+  if (st != MOE_OK) {
+    fail(st, why);
+    return 0;
+  }
+  size_t need = 256;
+  muon::each_bucket(tensors, n, [&](const muon::Bucket& q, int64_t) {
+    need = std::max(need, muon::layout_of(q).total);
+    return MOE_OK;
+  });
+  return need;
+}
+
+extern "C" moe_status moe_muon_step(const moe_muon_tensor* tensors, int64_t n, const moe_muon_config* config, void* ws,
+                                    size_t ws_bytes, void* stream) {
+  reset_launch_count();
+  const char* why;
+  moe_status st = muon::check_list(tensors, n, config, &why);
+  if (st != MOE_OK) return fail(st, why);
+  st = check_ws(ws, ws_bytes, moe_muon_workspace_bytes(tensors, n, config));
+  if (st != MOE_OK) return st;
+  return muon::each_bucket(tensors, n, [&](const muon::Bucket& q, int64_t i) -> moe_status {
+    const muon::RoundLayout L = muon::layout_of(q);
+    const muon::Key k = muon::key_of(tensors[i]);
+    muon::Round r = {};
+    auto flush = [&]() -> moe_status {
+      if (r.batch == 0) return MOE_OK;
+      CHECK_CUDA(muon::run_round(r, q, L, static_cast<char*>(ws), config->coefs, (cudaStream_t)stream));
+      r = {};
+      return MOE_OK;
+    };
+    for (int64_t j = i; j < n; ++j) {
+      const moe_muon_tensor& t = tensors[j];
+      if (!muon::same(muon::key_of(t), k)) continue;
+      for (int64_t at = 0; at < t.batch;) {
+        if (r.segs == muon::kSegs || r.batch == q.round) {
+          const moe_status e = flush();
+          if (e != MOE_OK) return e;
+        }
+        const int32_t m = (int32_t)std::min<int64_t>(t.batch - at, q.round - r.batch);
+        r.seg[r.segs++] = {t.param, t.grad, t.momentum, at, r.batch, m, t.rows, t.cols, t.param_dtype, t.grad_dtype,
+                           muon::size_of(*config, t)};
+        r.batch += m;
+        r.update = 1;
+        r.nesterov = config->nesterov;
+        r.beta = (float)config->momentum;
+        r.rest = (float)(1.0 - config->momentum);
+        r.keep = (float)(1.0 - config->lr * config->weight_decay);
+        at += m;
+      }
+    }
+    return flush();
+  });
+}

@@ -19,6 +19,7 @@
 #include "../../include/moe_model.h"
 #include "common.cuh"
 #include "internal.h"
+#include "tcgen05.cuh"
 #include "train.h"
 
 namespace moe {
@@ -200,6 +201,248 @@ __global__ void __launch_bounds__(1024) norm_forward_kernel(int64_t rows, int H,
   }
 }
 
+
+// ---------------------------------------------------------------------------
+// Many rows: each team of threads (a row's threads, or a warp with several short
+// rows) is fed by bulk copies into a ring of its own, kRing steps deep, so that the
+// next rows are under way while this one's sums wait on each other; the weights
+// stand in shared memory.  Held in registers without the ring, a row's loads, two
+// row sums and stores followed one another: the forward at T = 4096, H = 2816 took 39 us,
+// the backward at T = 8192, H = 7168 340.
+// ---------------------------------------------------------------------------
+struct RingShape {
+  int G;        // threads of a team (whole warps)
+  int Gs, R;    // threads of a row, rows a step: R > 1 within a warp
+  int NG;       // teams of a block
+  int vpt, depth;
+  int smem;
+  int per_sm;   // blocks
+};
+
+constexpr int kBarBytes = 512;   // barriers of all teams, 16-byte rows after them
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+// Waits for a phase, about two seconds at most.
+__device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity) {
+  if (tc::mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!tc::mbar_try_wait(bar, parity))
+    if (clock64() - t0 > tc::kWaitCycles) return false;
+  return true;
+}
+
+// After a wait that ran out: every copy that was started had a wait of its own, but
+// this one's may still come.  A thousand times its latency, then the block may end.
+__device__ __forceinline__ void ring_drain() {
+  const long long t0 = clock64();
+  while (clock64() - t0 < (1 << 21)) {}
+}
+
+// What a team knows of its place.
+struct Team {
+  int g, tt, row, lane;      // team, thread in it, row of the step, thread in the row
+  int G, Gs;
+  __device__ __forceinline__ explicit Team(const RingShape& q) : G(q.G), Gs(q.Gs) {
+    g = threadIdx.x / G;
+    tt = threadIdx.x - g * G;
+    row = tt / Gs;
+    lane = tt - row * Gs;
+  }
+  __device__ __forceinline__ void sync() const {
+    if (G == 32) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(G) : "memory");
+  }
+  // Sums over a row's threads; red: [2][N][warps] of the team.
+  template <int N>
+  __device__ __forceinline__ void sum(float (&v)[N], float* red, int& slot) const {
+    const int span = Gs < 32 ? Gs : 32;
+    for (int o = span >> 1; o; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    if (Gs <= 32) return;
+    float* r = red + slot * N * 32;
+    if ((tt & 31) == 0)
+#pragma unroll
+      for (int i = 0; i < N; ++i) r[i * 32 + (tt >> 5)] = v[i];
+    sync();
+    const int lane32 = tt & 31, warps = G >> 5;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = lane32 < warps ? r[i * 32 + lane32] : 0.0f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    slot ^= 1;
+  }
+};
+
+// What y and s are multiplied by, to shared memory in fp32: w1 = (w_post + o) g of a
+// channel gate, w2 = w_pre + o (opened and combined once instead of in every row).
+template <typename T>
+__device__ __forceinline__ void stage_weights(float* w1, float* w2, const T* w_post, const T* gate, const T* w_pre,
+                                              float off, int H) {
+  for (int c = threadIdx.x; c < H; c += blockDim.x) {
+    const float g = gate ? to_f(gate[c]) : 1.0f;
+    w1[c] = (w_post ? to_f(w_post[c]) + off : 1.0f) * g;
+    w2[c] = w_pre ? to_f(w_pre[c]) + off : 0.0f;
+  }
+}
+__device__ __forceinline__ void open8f(const float* p, float* f) {
+  unpack16(reinterpret_cast<const uint4*>(p)[0], f, (const float*)nullptr);
+  unpack16(reinterpret_cast<const uint4*>(p)[1], f + 4, (const float*)nullptr);
+}
+
+// A team's rows: `steps` steps of R rows, NG * R rows apart, through its ring.
+template <int STREAMS>
+struct Feed {
+  const char* src[STREAMS];   // NULL: not loaded
+  int64_t rows, first;        // rows in all; the team's first
+  int64_t step;               // rows between a team's steps
+  int R, row_bytes, depth;
+  uint32_t ring, bars;        // of the team
+
+  __device__ __forceinline__ void init(int64_t all, int bytes, const RingShape& q, int steps, const Team& m,
+                                       unsigned char* smem, unsigned char* rings) {
+    rows = all;
+    R = q.R;
+    first = ((int64_t)blockIdx.x * steps * q.NG + m.g) * R;
+    step = (int64_t)q.NG * R;
+    row_bytes = bytes;
+    depth = q.depth;
+    ring = tc::smem_u32(rings) + (uint32_t)(m.g * depth * STREAMS * R * row_bytes);
+    bars = tc::smem_u32(smem) + 8u * m.g * depth;
+    if (m.tt == 0) {
+      for (int i = 0; i < depth; ++i) tc::mbar_init(bars + 8u * i, 1);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+  }
+  __device__ __forceinline__ int64_t row_of(int i) const { return first + i * step; }
+  __device__ __forceinline__ bool wait(int i) const { return ring_wait(bars + 8u * (i % depth), (uint32_t)(i / depth) & 1u); }
+  __device__ __forceinline__ const unsigned char* at(const unsigned char* rings, const Team& m, int i) const {
+    return rings + (size_t)(m.g * depth + i % depth) * STREAMS * R * row_bytes;
+  }
+  // Called by one thread of the team.
+  __device__ __forceinline__ void load(int i, int steps) const {
+    if (i >= steps) return;
+    const int64_t r = row_of(i);
+    if (r >= rows) return;
+    const int n = rows - r < R ? (int)(rows - r) : R;
+    const uint32_t bytes = (uint32_t)n * row_bytes, bar = bars + 8u * (i % depth);
+    const uint32_t to = ring + (uint32_t)(i % depth) * STREAMS * R * row_bytes;
+    uint32_t all = 0;
+#pragma unroll
+    for (int k = 0; k < STREAMS; ++k) all += src[k] ? bytes : 0u;
+    tc::mbar_expect_tx(bar, all);
+#pragma unroll
+    for (int k = 0; k < STREAMS; ++k)
+      if (src[k]) bulk_load(to + k * R * row_bytes, src[k] + r * row_bytes, bytes, bar);
+  }
+  __device__ __forceinline__ void start(int steps) const {
+    for (int i = 0; i < depth - 1; ++i) load(i, steps);
+  }
+};
+
+template <typename T, int VPT>
+__global__ void __launch_bounds__(1024, 1) norm_forward_ring_kernel(
+    int64_t rows, int H, const RingShape q, int steps, int kind, float off, float res, float eps, const T* x,
+    const T* __restrict__ y, const T* __restrict__ w_post, const void* __restrict__ gate, const T* __restrict__ w_pre,
+    T* s, T* __restrict__ h, float2* __restrict__ rstd) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ float red_all[16][2 * 32];
+  float* w1 = reinterpret_cast<float*>(smem + kBarBytes);
+  float* w2 = w1 + H;
+  unsigned char* ring = reinterpret_cast<unsigned char*>(w2 + H);
+  const Team m(q);
+  float* red = red_all[m.g];
+  Feed<2> f;
+  f.init(rows, H * (int)sizeof(T), q, steps, m, smem, ring);
+  f.src[0] = reinterpret_cast<const char*>(x);
+  f.src[1] = reinterpret_cast<const char*>(y);
+  pdl_trigger();
+  pdl_wait();
+  if (m.tt == 0) f.start(steps);
+  stage_weights<T>(w1, w2, w_post, kind == MOE_GATE_CHANNEL ? static_cast<const T*>(gate) : nullptr, w_pre, off, H);
+  __syncthreads();
+  const float inv_h = 1.0f / (float)H;
+  int slot = 0;
+  bool fed = true;
+  for (int i = 0; i < steps; ++i) {
+    const int64_t base = f.row_of(i);
+    if (base >= rows) break;
+    fed = fed && f.wait(i);
+    m.sync();                                     // the step before is behind every thread
+    if (m.tt == 0) f.load(i + q.depth - 1, steps);   // into its slot
+    const int64_t t = base + m.row;
+    const bool on = t < rows;
+    const T* bx = reinterpret_cast<const T*>(f.at(ring, m, i)) + (size_t)m.row * H;
+    const T* by = bx + (size_t)q.R * H;
+    float gt = 1.0f;
+    if (kind == MOE_GATE_TOKEN && on) gt = static_cast<const float*>(gate)[t];
+    float v[VPT][8];
+    float sum[1] = {0.0f};
+    float r1 = 1.0f;
+    if (w_post) {
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        const int c = (m.lane + k * q.Gs) * 8;
+        if (!on || c >= H) continue;
+        float fy[8];
+        open8<T>(load8<T>(by + c), fy);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[0] = fmaf(fy[e], fy[e], sum[0]);
+      }
+      m.sum<1>(sum, red, slot);
+      r1 = 1.0f / sqrtf(sum[0] * inv_h + eps);
+      sum[0] = 0.0f;
+    }
+    if (!fed) r1 = __int_as_float(0x7fc00000);   // a copy that never came
+    const float rg = r1 * gt, rx = fed ? res : r1;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int c = (m.lane + k * q.Gs) * 8;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[k][e] = 0.0f;
+      if (!on || c >= H) continue;
+      open8<T>(load8<T>(bx + c), v[k]);
+      if (y) {
+        float fy[8], w[8];
+        open8<T>(load8<T>(by + c), fy);
+        open8f(w1 + c, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[k][e] = fmaf(rx, v[k][e], rg * (fy[e] * w[e]));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[k][e] *= rx;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[0] = fmaf(v[k][e], v[k][e], sum[0]);
+      if (s) store8<T>(s + t * H + c, v[k]);
+    }
+    float r2 = 0.0f;
+    if (w_pre) {
+      m.sum<1>(sum, red, slot);
+      r2 = 1.0f / sqrtf(sum[0] * inv_h + eps);
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        const int c = (m.lane + k * q.Gs) * 8;
+        if (!on || c >= H) continue;
+        float w[8];
+        open8f(w2 + c, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[k][e] *= r2 * w[e];
+        store8<T>(h + t * H + c, v[k]);
+      }
+    }
+    if (rstd && on && m.lane == 0) rstd[t] = make_float2(w_post ? r1 : 0.0f, r2);
+  }
+  if (!fed) ring_drain();
+}
+
 struct BwdArgs {
   int64_t rows;
   int H, G, NG, kind, flushes;
@@ -208,7 +451,7 @@ struct BwdArgs {
   const float2* rstd;
   void *dx, *dy;
   float* dgate;      // of a token gate
-  float* part;       // [flushes][blocks][NG][3][H], or NULL
+  float* part;       // [flushes][blocks][NG][2][H] (rings: [blocks][2][H]), or NULL
 };
 
 template <typename T, int VPT>
@@ -230,7 +473,7 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : 512) norm_backward_kernel(co
   T* dx = static_cast<T*>(a.dx);
   T* dy = static_cast<T*>(a.dy);
   Eight<T> wp[VPT], wg[VPT], wq[VPT];
-  float s_post[VPT][8], s_gate[VPT][8], s_pre[VPT][8];
+  float s_e[VPT][8], s_pre[VPT][8];   // of g D yn (g of the token) and dh sn
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     const int c = (lane + v * G) * 8;
@@ -239,21 +482,20 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : 512) norm_backward_kernel(co
     wg[v] = live && a.kind == MOE_GATE_CHANNEL ? load8<T>(static_cast<const T*>(a.gate) + c) : zero8<T>();
     wq[v] = live && w_pre ? load8<T>(w_pre + c) : zero8<T>();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s_post[v][e] = s_gate[v][e] = s_pre[v][e] = 0.0f;
+    for (int e = 0; e < 8; ++e) s_e[v][e] = s_pre[v][e] = 0.0f;
   }
   int count = 0, flush = 0;
   auto put_sums = [&]() {
-    float* p = a.part + (((int64_t)flush * gridDim.x + blockIdx.x) * a.NG + g) * 3 * H;
+    float* p = a.part + (((int64_t)flush * gridDim.x + blockIdx.x) * a.NG + g) * 2 * H;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int c = (lane + v * G) * 8;
       if (c < H) {
-        store8<float>(p + c, s_post[v]);
-        store8<float>(p + H + c, s_gate[v]);
-        store8<float>(p + 2 * H + c, s_pre[v]);
+        store8<float>(p + c, s_e[v]);
+        store8<float>(p + H + c, s_pre[v]);
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s_post[v][e] = s_gate[v][e] = s_pre[v][e] = 0.0f;
+      for (int e = 0; e < 8; ++e) s_e[v][e] = s_pre[v][e] = 0.0f;
     }
     ++flush;
     count = 0;
@@ -346,8 +588,7 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : 512) norm_backward_kernel(co
         const float wv = w_post ? w[e] + a.off : 1.0f;
         const float gv = a.kind == MOE_GATE_CHANNEL ? gg[e] : gt;
         const float du = D[v][e] * gv, dyn = D[v][e] * yn;
-        s_post[v][e] = fmaf(du, yn, s_post[v][e]);
-        s_gate[v][e] = fmaf(dyn, wv, s_gate[v][e]);
+        s_e[v][e] = fmaf(gt, dyn, s_e[v][e]);
         c1[0] = fmaf(du * wv, yn, c1[0]);
         c1[1] = fmaf(dyn, wv, c1[1]);
         D[v][e] = du * wv;
@@ -376,39 +617,212 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : 512) norm_backward_kernel(co
     while (flush < a.flushes) put_sums();   // a group with fewer rows adds zeros
 }
 
-// The groups' column sums, added in order: eight warps take a part of them each.
-constexpr int kJoinWarps = 8;
+
+// ds is needed once, in the middle, and comes straight to registers; x, y and dh by
+// the ring.  One vector a thread, so that many warps share the arithmetic (25 fp32
+// operations an element; two vectors or two rows a thread were latency-bound at 14
+// warps an SM: 255 and 374 us at T = 8192, H = 7168).
+template <typename T, int VPT>
+__global__ void __launch_bounds__(VPT == 1 ? 896 : 512, 1) norm_backward_ring_kernel(const BwdArgs a, const RingShape q,
+                                                                                     int steps) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ float red_all[16][2 * 32];
+  const int H = a.H;
+  float* w1 = reinterpret_cast<float*>(smem + kBarBytes);
+  float* w2 = w1 + H;
+  unsigned char* ring = reinterpret_cast<unsigned char*>(w2 + H);
+  const Team m(q);
+  float* red = red_all[m.g];
+  const T* ds = static_cast<const T*>(a.ds);
+  const bool with_y = a.y != nullptr, pre = a.w_pre != nullptr, post = a.w_post != nullptr;
+  Feed<3> f;
+  f.init(a.rows, H * (int)sizeof(T), q, steps, m, smem, ring);
+  f.src[0] = static_cast<const char*>(pre ? a.x : nullptr);
+  f.src[1] = static_cast<const char*>(a.y);
+  f.src[2] = static_cast<const char*>(a.dh);
+  T* dx = static_cast<T*>(a.dx);
+  T* dy = static_cast<T*>(a.dy);
+  pdl_trigger();
+  pdl_wait();
+  const bool feeds = pre || with_y;   // else there is nothing to wait for
+  if (m.tt == 0 && feeds) f.start(steps);
+  stage_weights<T>(w1, w2, static_cast<const T*>(a.w_post),
+                   a.kind == MOE_GATE_CHANNEL ? static_cast<const T*>(a.gate) : nullptr, static_cast<const T*>(a.w_pre),
+                   a.off, H);
+  __syncthreads();
+  const float inv_h = 1.0f / (float)H;
+  int slot = 0;
+  bool fed = true;
+  float c_e[VPT][8], c_pre[VPT][8];   // the columns' sums over this team's rows
+#pragma unroll
+  for (int k = 0; k < VPT; ++k)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c_e[k][e] = c_pre[k][e] = 0.0f;
+  for (int i = 0; i < steps; ++i) {
+    const int64_t base = f.row_of(i);
+    if (base >= a.rows) break;
+    const int64_t t = base + m.row;
+    const bool on = t < a.rows;
+    Eight<T> us[VPT];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int c = (m.lane + k * q.Gs) * 8;
+      us[k] = on && c < H && ds ? load8<T>(ds + t * H + c) : zero8<T>();
+    }
+    float2 r = on ? a.rstd[t] : make_float2(0.0f, 0.0f);
+    const float gt = on && a.kind == MOE_GATE_TOKEN ? static_cast<const float*>(a.gate)[t] : 1.0f;
+    if (!post) r.x = 1.0f;
+    if (feeds) fed = fed && f.wait(i);
+    m.sync();                                                 // the step before is behind every thread
+    if (m.tt == 0 && feeds) f.load(i + q.depth - 1, steps);   // into its slot
+    if (!fed) r.x = r.y = __int_as_float(0x7fc00000);         // a copy that never came
+    const T* bx = reinterpret_cast<const T*>(f.at(ring, m, i)) + (size_t)m.row * H;
+    const T *by = bx + (size_t)q.R * H, *bh = by + (size_t)q.R * H;
+    float D[VPT][8];
+    if (pre) {
+      float c2[1] = {0.0f};
+      const float rx = a.res * r.y, ry = gt * r.x * r.y;
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        const int c = (m.lane + k * q.Gs) * 8;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) D[k][e] = 0.0f;
+        if (!on || c >= H) continue;
+        float fv[8], w[8];
+        open8<T>(load8<T>(bx + c), D[k]);
+        if (with_y) {
+          open8<T>(load8<T>(by + c), fv);
+          open8f(w1 + c, w);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) D[k][e] = fmaf(rx, D[k][e], ry * (fv[e] * w[e]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) D[k][e] *= rx;
+        }
+        open8<T>(load8<T>(bh + c), fv);
+        open8f(w2 + c, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          c_pre[k][e] = fmaf(fv[e], D[k][e], c_pre[k][e]);
+          c2[0] = fmaf(fv[e] * w[e], D[k][e], c2[0]);   // D is sn until the sum is there
+        }
+      }
+      m.sum<1>(c2, red, slot);
+      const float mean = -c2[0] * inv_h;
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        const int c = (m.lane + k * q.Gs) * 8;
+        if (!on || c >= H) continue;
+        float fv[8], w[8];
+        open8<T>(load8<T>(bh + c), fv);
+        open8f(w2 + c, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) D[k][e] = fmaf(D[k][e], mean, fv[e] * w[e]);
+        open8<T>(us[k], fv);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) D[k][e] = fmaf(r.y, D[k][e], fv[e]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) open8<T>(us[k], D[k]);
+    }
+    // D, and the block's side: the row sum of D yn w1, which is the token gate's
+    // gradient too
+    float c1[1] = {0.0f};
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int c = (m.lane + k * q.Gs) * 8;
+      if (!on || c >= H) continue;
+      if (dx) {
+        float o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = a.res * D[k][e];
+        store8<T>(dx + t * H + c, o);
+      }
+      if (!with_y) continue;
+      float fy[8], w[8];
+      open8<T>(load8<T>(by + c), fy);
+      open8f(w1 + c, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float dyn = D[k][e] * (fy[e] * r.x);
+        c_e[k][e] = fmaf(gt, dyn, c_e[k][e]);
+        c1[0] = fmaf(dyn, w[e], c1[0]);
+        D[k][e] *= w[e];
+      }
+    }
+    if (!with_y) continue;
+    if (post || a.dgate) m.sum<1>(c1, red, slot);
+    if (a.dgate && on && m.lane == 0) a.dgate[t] = c1[0];
+    if (!dy) continue;
+    const float mine = gt * r.x, back = -r.x * mine * (c1[0] * inv_h);
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int c = (m.lane + k * q.Gs) * 8;
+      if (!on || c >= H) continue;
+      float fy[8];
+      open8<T>(load8<T>(by + c), fy);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) D[k][e] = post ? fmaf(fy[e], back, mine * D[k][e]) : mine * D[k][e];
+      store8<T>(dy + t * H + c, D[k]);
+    }
+  }
+  if (!fed) ring_drain();
+  if (!a.part) return;
+  // The rows' sums of the block in the ring, which no copy fills any more: a thread's
+  // columns lie at its own row of its team, then added in that order.
+  __syncthreads();
+  float* sums = reinterpret_cast<float*>(ring);     // [NG][R][2][H]
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) {
+    const int c = (m.lane + k * q.Gs) * 8;
+    if (c >= H) continue;
+    float* p = sums + (size_t)(m.g * q.R + m.row) * 2 * H + c;
+    store8<float>(p, c_e[k]);
+    store8<float>(p + H, c_pre[k]);
+  }
+  __syncthreads();
+  float* out = a.part + (int64_t)blockIdx.x * 2 * H;
+  for (int c = threadIdx.x * 4; c < 2 * H; c += blockDim.x * 4) {
+    float4 v = *reinterpret_cast<const float4*>(sums + c);
+    for (int n = 1; n < q.NG * q.R; ++n) {
+      const float4 u = *reinterpret_cast<const float4*>(sums + (size_t)n * 2 * H + c);
+      v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+    }
+    *reinterpret_cast<float4*>(out + c) = v;
+  }
+}
+
+// The blocks' column sums, added in order: sixteen warps take a part of them each.
+// With E = sum_t D yn (times the token's gate): dw_post = gate E, dgate = (w_post + o) E.
+constexpr int kJoinWarps = 16;
 template <typename T>
 __global__ void __launch_bounds__(32 * kJoinWarps) norm_columns_kernel(const float* __restrict__ part, int64_t n, int H,
+                                                                       const T* __restrict__ w_post,
+                                                                       const T* __restrict__ gate, float off,
                                                                        T* dw_post, T* dgate, T* dw_pre) {
-  __shared__ float4 sh[kJoinWarps][32];
+  __shared__ float sh[kJoinWarps][32];
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c = (blockIdx.x * 32 + lane) * 4;
+  const int c = blockIdx.x * 32 + lane, col = c < H ? c : c - H;
+  const bool live = c < 2 * H && (c < H ? dw_post != nullptr || dgate != nullptr : dw_pre != nullptr);
   const int64_t each = (n + kJoinWarps - 1) / kJoinWarps, hi = min(n, (warp + 1) * each);
-  float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (c < 3 * H) {
+  float f = 0.0f;
+  if (live) {
 #pragma unroll 8
-    for (int64_t i = warp * each; i < hi; ++i) {
-      const float4 u = __ldcg(reinterpret_cast<const float4*>(part + i * 3 * H + c));
-      f.x += u.x; f.y += u.y; f.z += u.z; f.w += u.w;
-    }
+    for (int64_t i = warp * each; i < hi; ++i) f += __ldcg(part + i * 2 * H + c);
   }
   sh[warp][lane] = f;
   __syncthreads();
-  if (warp != 0 || c >= 3 * H) return;
-  for (int w = 1; w < kJoinWarps; ++w) {
-    const float4 u = sh[w][lane];
-    f.x += u.x; f.y += u.y; f.z += u.z; f.w += u.w;
+  if (warp != 0 || !live) return;
+  for (int w = 1; w < kJoinWarps; ++w) f += sh[w][lane];
+  if (c >= H) {
+    dw_pre[col] = from_f<T>(f);
+    return;
   }
-  const int which = c / H, col = c - which * H;
-  T* out = which == 0 ? dw_post : which == 1 ? dgate : dw_pre;
-  if (out == nullptr) return;
-  out[col] = from_f<T>(f.x);
-  out[col + 1] = from_f<T>(f.y);
-  out[col + 2] = from_f<T>(f.z);
-  out[col + 3] = from_f<T>(f.w);
+  if (dw_post) dw_post[col] = from_f<T>(gate ? f * to_f(gate[col]) : f);
+  if (dgate) dgate[col] = from_f<T>(w_post ? f * (to_f(w_post[col]) + off) : f);
 }
 
 // ---------------------------------------------------------------------------
@@ -436,30 +850,100 @@ moe_status decode(const moe_block_norm_shape* s, NShape* o, const char** why) {
   return MOE_OK;
 }
 
-// The same on every device, so that a workspace's size and the sums do not depend on it.
+// Rings for rows of H columns, `streams` of them in and two fp32 weight vectors beside
+// them, one vector of 8 columns a thread up to `wide` vectors, at most `threads`
+// threads of an SM (two vectors: threads2): as many teams as fit with two steps or more in
+// their rings, then the deepest rings.  depth 0: none fits.
+constexpr int kSmemBlock = 227 * 1024, kSmemSm = 228 * 1024;   // 1 KB of the latter goes with each block
+constexpr int kStatic = 4096;                                   // what the kernels declare besides
+RingShape ring_shape(int H, int esize, int streams, int wide, int threads, int threads2) {
+  RingShape q = {};
+  const int vecs = H / 8;
+  if (vecs <= 32) {
+    q.vpt = 1;
+    q.Gs = 4;
+    while (q.Gs < vecs) q.Gs *= 2;
+    q.G = 32;
+    q.R = 32 / q.Gs;
+  } else {
+    q.vpt = vecs <= wide ? 1 : 2;
+    q.Gs = q.G = ((vecs + q.vpt - 1) / q.vpt + 31) / 32 * 32;
+    q.R = 1;
+  }
+  const int most_threads = q.vpt == 1 ? threads : threads2;
+  const int row = H * esize, weights = kBarBytes + 2 * H * 4;
+  const int step = streams * q.R * row;
+  int best = 0;
+  for (int b = 1; b <= 8; ++b)
+    for (int ng = 1; ng <= 15 && b * ng * q.G <= most_threads; ++ng) {
+      const int most = std::min(kSmemSm / b - 1024, kSmemBlock) - kStatic;
+      const int depth = std::min(4, std::max(0, most - weights) / (ng * step));
+      const int smem = std::max(weights + ng * depth * step, weights + ng * q.R * 2 * H * 4);
+      if (depth < 2 || smem > most) continue;
+      const int score = ng * b * 8 + depth;
+      if (score <= best) continue;
+      best = score;
+      q.NG = ng;
+      q.depth = depth;
+      q.smem = smem;
+      q.per_sm = b;
+    }
+  return q;
+}
+
+// The backward's work split, the same on every device, so that a workspace's size
+// and the sums do not depend on it.  Rows in rings, at most kFlush a team; else (a row
+// too wide for them, or so few rows that a block has one) as they come.
 struct Split {
-  Geometry g;
+  RingShape q;
+  int steps;       // of a team
+  Geometry g;      // without rings
   int64_t blocks;
   int flushes;
 };
 Split split_of(const NShape& s) {
-  Split p;
+  Split p = {};
+  p.q = ring_shape(s.H, s.esize, 3, 896, 896, 512);
+  if (p.q.depth > 0) {
+    const int64_t per = (int64_t)p.q.NG * p.q.R;   // rows of a block's step
+    const int64_t resident = 152ll * p.q.per_sm;
+    const int64_t rows = (s.T + per - 1) / per;
+    const int64_t waves = std::max<int64_t>(1, (rows + resident * kFlush - 1) / (resident * kFlush));
+    p.steps = (int)std::max<int64_t>(1, (rows + resident * waves - 1) / (resident * waves));
+    p.blocks = std::max<int64_t>(1, (rows + p.steps - 1) / p.steps);
+    return p;
+  }
   p.g = geometry(s.H, 256);
   const int threads = p.g.G * p.g.NG;
-  const int per_sm = threads > 512 ? 1 : 512 / threads > 0 ? 1024 / threads / 2 + 1 : 1;
+  const int per_sm = threads > 512 ? 1 : 1024 / threads / 2 + 1;
   p.blocks = std::min<int64_t>((s.T + p.g.NG - 1) / p.g.NG, 152ll * std::max(1, per_sm));
   if (p.blocks < 1) p.blocks = 1;
   const int64_t rows = (s.T + p.blocks * p.g.NG - 1) / (p.blocks * p.g.NG);   // of a group
   p.flushes = (int)std::max<int64_t>(1, (rows + kFlush - 1) / kFlush);
   return p;
 }
-size_t part_bytes(const NShape& s, const Split& p) {
-  return (size_t)p.flushes * p.blocks * p.g.NG * 3 * s.H * 4;
-}
+int64_t parts_of(const Split& p) { return p.q.depth > 0 ? p.blocks : (int64_t)p.flushes * p.blocks * p.g.NG; }
+size_t part_bytes(const NShape& s, const Split& p) { return (size_t)parts_of(p) * 2 * s.H * 4; }
 
 template <typename T>
 cudaError_t forward(const NShape& s, const void* x, const void* y, const void* w_post, const void* gate,
                     const void* w_pre, void* so, void* h, float* rstd, cudaStream_t st) {
+  const RingShape q = ring_shape(s.H, s.esize, 2, 64, 1024, 1024);
+  const int64_t per = (int64_t)q.NG * q.R, rows = (s.T + std::max<int64_t>(per, 1) - 1) / std::max<int64_t>(per, 1);
+  const int64_t resident = (int64_t)tc_sm_count() * q.per_sm;
+  if (q.depth > 0 && rows > 2 * resident) {
+    const int steps = (int)((rows + resident - 1) / resident);
+    const unsigned grid = (unsigned)((rows + steps - 1) / steps);
+    auto go = [&](auto kernel) {
+      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBlock - kStatic);
+      if (e != cudaSuccess) return e;
+      return launch_after(kernel, grid, (unsigned)(q.G * q.NG), q.smem, st, 1, s.T, s.H, q, steps, s.gate, s.off, s.res,
+                          s.eps, static_cast<const T*>(x), static_cast<const T*>(y), static_cast<const T*>(w_post), gate,
+                          static_cast<const T*>(w_pre), static_cast<T*>(so), static_cast<T*>(h),
+                          reinterpret_cast<float2*>(rstd));
+    };
+    return q.vpt == 1 ? go(norm_forward_ring_kernel<T, 1>) : go(norm_forward_ring_kernel<T, 2>);
+  }
   const Geometry g = geometry(s.H, 512);
   const unsigned threads = (unsigned)(g.G * g.NG);
   const int64_t need = (s.T + g.NG - 1) / g.NG, cap = (int64_t)tc_sm_count() * std::max(1u, 2048 / threads);
@@ -476,16 +960,30 @@ cudaError_t forward(const NShape& s, const void* x, const void* y, const void* w
 }
 
 template <typename T>
-cudaError_t backward(const NShape& s, const Split& p, const BwdArgs& a, void* dw_post, void* dgate, void* dw_pre,
+cudaError_t backward(const NShape& s, const Split& p, BwdArgs a, void* dw_post, void* dgate, void* dw_pre,
                      cudaStream_t st) {
-  const unsigned threads = (unsigned)(p.g.G * p.g.NG);
-  auto go = [&](auto kernel) { return launch_after(kernel, (unsigned)p.blocks, threads, 0, st, 1, a); };
-  cudaError_t e = p.g.vpt == 1 ? go(norm_backward_kernel<T, 1>)
-                  : p.g.vpt == 2 ? go(norm_backward_kernel<T, 2>) : go(norm_backward_kernel<T, 4>);
+  cudaError_t e;
+  if (p.q.depth > 0) {
+    auto go = [&](auto kernel) {
+      const cudaError_t f = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBlock - kStatic);
+      if (f != cudaSuccess) return f;
+      return launch_after(kernel, (unsigned)p.blocks, (unsigned)(p.q.G * p.q.NG), p.q.smem, st, 1, a, p.q, p.steps);
+    };
+    e = p.q.vpt == 1 ? go(norm_backward_ring_kernel<T, 1>) : go(norm_backward_ring_kernel<T, 2>);
+  } else {
+    const unsigned threads = (unsigned)(p.g.G * p.g.NG);
+    a.G = p.g.G;
+    a.NG = p.g.NG;
+    a.flushes = p.flushes;
+    auto go = [&](auto kernel) { return launch_after(kernel, (unsigned)p.blocks, threads, 0, st, 1, a); };
+    e = p.g.vpt == 1 ? go(norm_backward_kernel<T, 1>)
+        : p.g.vpt == 2 ? go(norm_backward_kernel<T, 2>) : go(norm_backward_kernel<T, 4>);
+  }
   if (e != cudaSuccess || !a.part) return e;
-  return launch_after(norm_columns_kernel<T>, (unsigned)((3 * s.H + 127) / 128), 32 * kJoinWarps, 0, st, 1,
-                      (const float*)a.part, (int64_t)p.flushes * p.blocks * p.g.NG, s.H, static_cast<T*>(dw_post),
-                      static_cast<T*>(dgate), static_cast<T*>(dw_pre));
+  return launch_after(norm_columns_kernel<T>, (unsigned)((2 * s.H + 31) / 32), 32 * kJoinWarps, 0, st, 1,
+                      (const float*)a.part, parts_of(p), s.H, static_cast<const T*>(a.w_post),
+                      a.kind == MOE_GATE_CHANNEL ? static_cast<const T*>(a.gate) : nullptr, a.off,
+                      static_cast<T*>(dw_post), static_cast<T*>(dgate), static_cast<T*>(dw_pre));
 }
 
 // What both directions ask of the inputs.
@@ -572,10 +1070,7 @@ extern "C" moe_status moe_block_norm_backward(const moe_block_norm_shape* shape,
   bn::BwdArgs a = {};
   a.rows = s.T;
   a.H = s.H;
-  a.G = p.g.G;
-  a.NG = p.g.NG;
   a.kind = s.gate;
-  a.flushes = p.flushes;
   a.off = s.off;
   a.res = s.res;
   a.ds = ds;

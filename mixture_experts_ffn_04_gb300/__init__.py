@@ -690,21 +690,37 @@ MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN = 0, 1, 2
 MOE_MUON_SCALE_NONE, MOE_MUON_SCALE_SPECTRAL, MOE_MUON_SCALE_RMS = 0, 1, 2
 
 
-def _here(ws: torch.Tensor, **tensors):
-    """_on_device, and that device is the current one: the launch goes to a stream of
-    the current device."""
-    _on_device(ws, **tensors)
-    if torch.cuda.current_device() != ws.get_device():
+def _device(t: torch.Tensor) -> int:
+    """The device of a call's workspace (or first tensor): a CUDA device, and the
+    current one, to whose stream the launch goes."""
+    if t is None or not t.is_cuda:
+        raise ValueError("the workspace and the tensors must be CUDA tensors, got %s"
+                         % (t if t is None else t.device))
+    at = t.get_device()
+    if at != torch.cuda.current_device():
         raise ValueError("the tensors are on %s, the current device is cuda:%d"
-                         % (ws.device, torch.cuda.current_device()))
+                         % (t.device, torch.cuda.current_device()))
+    return at
 
 
-def _maybe(t, n, dtype, name):
-    return None if t is None else _vec(t, n, dtype, name)
+def _arg(t, n: int, dtype, at: int, name: str, none: bool = True):
+    """Address of n contiguous elements on device `at` (all checks of an argument in one
+    place: a small call is as long as its host side)."""
+    if t is None:
+        if none:
+            return None
+        raise ValueError("%s must be a tensor" % name)
+    if t.dtype != dtype or t.numel() != n:
+        raise ValueError("%s must hold %d elements of %s, got %s %s" % (name, n, dtype, tuple(t.shape),
+                                                                        t.dtype))
+    if t.get_device() != at:
+        raise ValueError("%s is on %s, the workspace on cuda:%d" % (name, t.device, at))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
 
 
-def _act(shape):
-    return torch.float32 if shape.dtype == MOE_F32 else torch.bfloat16
+_ACT = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16}
 
 
 def moe_embed_workspace_bytes(shape: MoEEmbedShape) -> int:
@@ -713,56 +729,58 @@ def moe_embed_workspace_bytes(shape: MoEEmbedShape) -> int:
 
 def moe_embed_forward(shape: MoEEmbedShape, w, ids, y, ws, stream=None):
     """w may be rows of a wider buffer (the stride goes into the shape)."""
-    dt, T, H = _act(shape), shape.tokens, shape.hidden
+    at, dt, T, H = _device(ws), _ACT[shape.dtype], shape.tokens, shape.hidden
     wp, shape.w_stride = _rows(w, shape.vocab, H, dt, "w")
-    args = (_vec(ids, T, torch.int32, "ids"), _vec(y, T * H, dt, "y"))
-    _here(ws, w=w, ids=ids, y=y)
-    _check(lib().moe_embed_forward(ctypes.byref(shape), wp, *args, _p(ws), _nbytes(ws),
-                                   _stream(stream)), "moe_embed_forward")
+    if w.get_device() != at:
+        raise ValueError("w is on %s, the workspace on cuda:%d" % (w.device, at))
+    st = lib().moe_embed_forward(ctypes.byref(shape), wp, _arg(ids, T, torch.int32, at, "ids", False),
+                                 _arg(y, T * H, dt, at, "y", False), ws.data_ptr(), _nbytes(ws), _stream(stream))
+    if st:
+        _check(st, "moe_embed_forward")
 
 
 def moe_embed_backward(shape: MoEEmbedShape, ids, dy, dw_add, dw, ws, stream=None):
-    dt, T, H, V = _act(shape), shape.tokens, shape.hidden, shape.vocab
-    args = (_vec(ids, T, torch.int32, "ids"), _vec(dy, T * H, dt, "dy"),
-            _maybe(dw_add, V * H, dt, "dw_add"), _vec(dw, V * H, dt, "dw"))
-    _here(ws, ids=ids, dy=dy, dw_add=dw_add, dw=dw)
-    _check(lib().moe_embed_backward(ctypes.byref(shape), *args, _p(ws), _nbytes(ws),
-                                    _stream(stream)), "moe_embed_backward")
+    at, dt, T = _device(ws), _ACT[shape.dtype], shape.tokens
+    n, all_ = T * shape.hidden, shape.vocab * shape.hidden
+    st = lib().moe_embed_backward(ctypes.byref(shape), _arg(ids, T, torch.int32, at, "ids", False),
+                                  _arg(dy, n, dt, at, "dy", False), _arg(dw_add, all_, dt, at, "dw_add"),
+                                  _arg(dw, all_, dt, at, "dw", False), ws.data_ptr(), _nbytes(ws), _stream(stream))
+    if st:
+        _check(st, "moe_embed_backward")
 
 
 def moe_block_norm_workspace_bytes(shape: MoEBlockNormShape) -> int:
     return int(lib().moe_block_norm_workspace_bytes(ctypes.byref(shape)))
 
 
-def _gate(shape, gate, name):
-    if shape.gate == MOE_GATE_TOKEN:
-        return _maybe(gate, shape.tokens, torch.float32, name)
-    return _maybe(gate, shape.hidden, _act(shape), name)
-
-
 def moe_block_norm_forward(shape: MoEBlockNormShape, x, y, w_post, gate, w_pre, s, h, rstd,
                            stream=None):
-    dt, n, H = _act(shape), shape.tokens * shape.hidden, shape.hidden
-    args = (_vec(x, n, dt, "x"), _maybe(y, n, dt, "y"), _maybe(w_post, H, dt, "w_post"),
-            _gate(shape, gate, "gate"), _maybe(w_pre, H, dt, "w_pre"), _maybe(s, n, dt, "s"),
-            _maybe(h, n, dt, "h"), _maybe(rstd, 2 * shape.tokens, torch.float32, "rstd"))
-    _here(x, y=y, w_post=w_post, gate=gate, w_pre=w_pre, s=s, h=h, rstd=rstd)
-    _check(lib().moe_block_norm_forward(ctypes.byref(shape), *args, _stream(stream)),
-           "moe_block_norm_forward")
+    at, dt, T, H = _device(x), _ACT[shape.dtype], shape.tokens, shape.hidden
+    n, token = T * H, shape.gate == MOE_GATE_TOKEN
+    st = lib().moe_block_norm_forward(
+        ctypes.byref(shape), _arg(x, n, dt, at, "x", False), _arg(y, n, dt, at, "y"),
+        _arg(w_post, H, dt, at, "w_post"),
+        _arg(gate, T if token else H, torch.float32 if token else dt, at, "gate"),
+        _arg(w_pre, H, dt, at, "w_pre"), _arg(s, n, dt, at, "s"), _arg(h, n, dt, at, "h"),
+        _arg(rstd, 2 * T, torch.float32, at, "rstd"), _stream(stream))
+    if st:
+        _check(st, "moe_block_norm_forward")
 
 
 def moe_block_norm_backward(shape: MoEBlockNormShape, ds, dh, x, y, w_post, gate, w_pre, rstd, dx,
                             dy, dw_post, dgate, dw_pre, ws, stream=None):
-    dt, n, H = _act(shape), shape.tokens * shape.hidden, shape.hidden
-    args = (_maybe(ds, n, dt, "ds"), _maybe(dh, n, dt, "dh"), _vec(x, n, dt, "x"),
-            _maybe(y, n, dt, "y"), _maybe(w_post, H, dt, "w_post"), _gate(shape, gate, "gate"),
-            _maybe(w_pre, H, dt, "w_pre"), _vec(rstd, 2 * shape.tokens, torch.float32, "rstd"),
-            _maybe(dx, n, dt, "dx"), _maybe(dy, n, dt, "dy"), _maybe(dw_post, H, dt, "dw_post"),
-            _gate(shape, dgate, "dgate"), _maybe(dw_pre, H, dt, "dw_pre"))
-    _here(ws, ds=ds, dh=dh, x=x, y=y, w_post=w_post, gate=gate, w_pre=w_pre, rstd=rstd, dx=dx, dy=dy,
-          dw_post=dw_post, dgate=dgate, dw_pre=dw_pre)
-    _check(lib().moe_block_norm_backward(ctypes.byref(shape), *args, _p(ws), _nbytes(ws),
-                                         _stream(stream)), "moe_block_norm_backward")
+    at, dt, T, H = _device(ws), _ACT[shape.dtype], shape.tokens, shape.hidden
+    n, token = T * H, shape.gate == MOE_GATE_TOKEN
+    gn, gd = (T, torch.float32) if token else (H, dt)
+    st = lib().moe_block_norm_backward(
+        ctypes.byref(shape), _arg(ds, n, dt, at, "ds"), _arg(dh, n, dt, at, "dh"),
+        _arg(x, n, dt, at, "x", False), _arg(y, n, dt, at, "y"), _arg(w_post, H, dt, at, "w_post"),
+        _arg(gate, gn, gd, at, "gate"), _arg(w_pre, H, dt, at, "w_pre"),
+        _arg(rstd, 2 * T, torch.float32, at, "rstd", False), _arg(dx, n, dt, at, "dx"),
+        _arg(dy, n, dt, at, "dy"), _arg(dw_post, H, dt, at, "dw_post"), _arg(dgate, gn, gd, at, "dgate"),
+        _arg(dw_pre, H, dt, at, "dw_pre"), ws.data_ptr(), _nbytes(ws), _stream(stream))
+    if st:
+        _check(st, "moe_block_norm_backward")
 
 
 def orth_coefs(coefficients=(3.4445, -4.7750, 2.0315), steps: int = 5, eps: float = 1e-7) -> MoEOrthCoefs:
@@ -787,11 +805,12 @@ def moe_orthogonalize_workspace_bytes(shape: MoEOrthShape, coefs: MoEOrthCoefs) 
 
 
 def moe_orthogonalize(shape: MoEOrthShape, coefs: MoEOrthCoefs, x, out, ws, stream=None):
-    dt, n = _act(shape), shape.batch * shape.rows * shape.cols
-    args = (_vec(x, n, dt, "x"), _vec(out, n, dt, "out"))
-    _here(ws, x=x, out=out)
-    _check(lib().moe_orthogonalize(ctypes.byref(shape), ctypes.byref(coefs), *args, _p(ws),
-                                   _nbytes(ws), _stream(stream)), "moe_orthogonalize")
+    at, dt, n = _device(ws), _ACT[shape.dtype], shape.batch * shape.rows * shape.cols
+    st = lib().moe_orthogonalize(ctypes.byref(shape), ctypes.byref(coefs), _arg(x, n, dt, at, "x", False),
+                                 _arg(out, n, dt, at, "out", False), ws.data_ptr(), _nbytes(ws),
+                                 _stream(stream))
+    if st:
+        _check(st, "moe_orthogonalize")
 
 
 def muon_tensors(params, grads, momenta):
@@ -821,7 +840,7 @@ def moe_muon_workspace_bytes(tensors, config: MoEMuonConfig) -> int:
 
 
 def moe_muon_step(tensors, config: MoEMuonConfig, ws, stream=None):
-    _here(ws)
+    _device(ws)
     _check(lib().moe_muon_step(tensors, len(tensors), ctypes.byref(config), _p(ws), _nbytes(ws),
                                _stream(stream)), "moe_muon_step")
 
@@ -913,6 +932,14 @@ def _empty(stream, shape, dtype, device):
         stream = torch.cuda.ExternalStream(stream)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _like(stream, t):
+    """_empty of t's shape and type (a tensor's own method on the current stream: a
+    microsecond less)."""
+    if stream is None and t.is_contiguous():
+        return torch.empty_like(t)
+    return _empty(stream, t.shape, t.dtype, t.device)
 
 
 def _alloc_ws(n: int, device, stream, where: str):
@@ -1050,7 +1077,7 @@ class TokenEmbedding:
     def forward(self, w, ids, y=None, stream=None):
         """y [tokens, hidden]."""
         if y is None:
-            y = _empty(stream, (self.shape.tokens, self.shape.hidden), w.dtype, w.device)
+            y = _empty(stream, (self.shape.tokens, self.shape.hidden), self.dtype, w.device)
         moe_embed_forward(self.shape, w, ids, y, self.ws, stream)
         return y
 
@@ -1058,7 +1085,7 @@ class TokenEmbedding:
         """dw [vocab, hidden], plus dw_add where given (the gradient of a classifier
         that shares the table); dw_add may be dw: only rows with tokens are touched."""
         if dw is None:
-            dw = _empty(stream, (self.shape.vocab, self.shape.hidden), dy.dtype, dy.device)
+            dw = _empty(stream, (self.shape.vocab, self.shape.hidden), self.dtype, dy.device)
         moe_embed_backward(self.shape, ids, dy, dw_add, dw, self.ws, stream)
         return dw
 
@@ -1100,9 +1127,9 @@ class BlockNorm:
     def forward(self, x, y=None, w_post=None, gate=None, w_pre=None, s=None, h=None, stream=None):
         """(s, h); self.rstd is what the backward needs."""
         if s is None:
-            s = _empty(stream, x.shape, x.dtype, x.device)
+            s = _like(stream, x)
         if h is None and w_pre is not None:
-            h = _empty(stream, x.shape, x.dtype, x.device)
+            h = _like(stream, x)
         moe_block_norm_forward(self.shape, x, y, w_post, gate, w_pre, s, h, self.rstd, stream)
         return s, h
 
@@ -1111,7 +1138,7 @@ class BlockNorm:
         """Gradients after a forward with the same inputs, given ds (of s, or None for
         zeros) and dh (of h)."""
         def like(out, t):
-            return _empty(stream, t.shape, t.dtype, t.device) if out is None and t is not None else out
+            return _like(stream, t) if out is None and t is not None else out
 
         d = BlockGrads(like(dx, x), like(dy, y), like(dw_post, w_post), like(dgate, gate),
                        like(dw_pre, w_pre))
@@ -1139,7 +1166,7 @@ class Orthogonalize:
     def forward(self, x, out=None, stream=None):
         """out [batch, rows, cols]; may be x."""
         if out is None:
-            out = _empty(stream, x.shape, x.dtype, x.device)
+            out = _like(stream, x)
         moe_orthogonalize(self.shape, self.coefs, x, out, self.ws, stream)
         return out
 

@@ -934,8 +934,9 @@ cudaError_t forward(const NShape& s, const void* x, const void* y, const void* w
   if (q.depth > 0 && rows > 2 * resident) {
     const int steps = (int)((rows + resident - 1) / resident);
     const unsigned grid = (unsigned)((rows + steps - 1) / steps);
+    static std::atomic<uint64_t> done[2];
     auto go = [&](auto kernel) {
-      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBlock - kStatic);
+      const cudaError_t e = allow_smem(kernel, kSmemBlock - kStatic, done[q.vpt - 1]);
       if (e != cudaSuccess) return e;
       return launch_after(kernel, grid, (unsigned)(q.G * q.NG), q.smem, st, 1, s.T, s.H, q, steps, s.gate, s.off, s.res,
                           s.eps, static_cast<const T*>(x), static_cast<const T*>(y), static_cast<const T*>(w_post), gate,
@@ -964,8 +965,9 @@ cudaError_t backward(const NShape& s, const Split& p, BwdArgs a, void* dw_post, 
                      cudaStream_t st) {
   cudaError_t e;
   if (p.q.depth > 0) {
+    static std::atomic<uint64_t> done[2];
     auto go = [&](auto kernel) {
-      const cudaError_t f = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBlock - kStatic);
+      const cudaError_t f = allow_smem(kernel, kSmemBlock - kStatic, done[p.q.vpt - 1]);
       if (f != cudaSuccess) return f;
       return launch_after(kernel, (unsigned)p.blocks, (unsigned)(p.q.G * p.q.NG), p.q.smem, st, 1, a, p.q, p.steps);
     };

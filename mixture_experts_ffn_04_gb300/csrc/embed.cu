@@ -7,7 +7,7 @@
 // vocabulary entry.
 //
 // Gradient: the tokens are sorted by id (stable, so a row's tokens stay in
-// order), the sorted list is cut into chunks of equal length, and one warp walks a
+// order; up to kSmallT by counting, more by radix passes), the sorted list is cut into chunks of equal length, and one warp walks a
 // chunk over 256 columns with its sum in fp32 registers: a row whose tokens lie
 // inside the chunk is written at once, a row that crosses a chunk's border leaves
 // a partial sum.  A second launch adds those up in chunk order.  So a frequent
@@ -28,10 +28,11 @@
 namespace moe {
 namespace emb {
 
-constexpr int kSmallT = 8192;       // tokens that one block sorts in shared memory
+constexpr int kSmallT = 16384;      // tokens whose places are counted, not sorted
 constexpr int kMaxBits = 9;         // of a radix digit
 constexpr int kMaxBins = 1 << kMaxBits;
-constexpr int kSmallWarps = 32, kTileWarps = 16;
+constexpr int kTileWarps = 16, kTileMin = 1024;
+static_assert(32 * kTileWarps == kMaxBins, "a thread a digit");
 constexpr int kMaxTiles = 256;      // blocks of a radix pass
 
 struct EShape {
@@ -99,11 +100,11 @@ __global__ void __launch_bounds__(kLookThreads) embed_kernel(const T* __restrict
 }
 
 // ---------------------------------------------------------------------------
-// sorting the tokens by id: least significant digit first, stable
+// sorting the tokens by id, stable
 // ---------------------------------------------------------------------------
 
-// One warp counts (or places) 32 items at a time in order: the lanes with the same
-// digit find each other, the lowest of them keeps the warp's counter.
+// Radix passes: one warp counts (or places) 32 items at a time in order: the lanes with
+// the same digit find each other, the lowest of them keeps the warp's counter.
 __device__ __forceinline__ void count_digit(uint32_t* cnt, uint32_t digit, bool live) {
   const uint32_t all = __ballot_sync(0xffffffffu, live);
   if (live) {
@@ -126,106 +127,60 @@ __device__ __forceinline__ uint32_t place_digit(uint32_t* cnt, uint32_t digit, b
   return at;
 }
 
-// cnt[warps][bins] counts -> the position of each warp's first item of a digit,
-// counted from the block's first; base[digit] (shared) is added where given, else
-// the exclusive sum over the smaller digits.  Every thread of the block calls it.
-template <int WARPS>
-__device__ __forceinline__ void scan_digits(uint32_t* cnt, int bins, const uint32_t* base, uint32_t* total,
-                                            uint32_t* sums) {
-  const int tid = threadIdx.x;
-  for (int d = tid; d < bins; d += 32 * WARPS) {
-    uint32_t run = 0;
-    for (int w = 0; w < WARPS; ++w) {
-      const uint32_t v = cnt[w * bins + d];
-      cnt[w * bins + d] = run;
-      run += v;
-    }
-    total[d] = run;
-  }
-  __syncthreads();
-  if (base == nullptr) {
-    // exclusive scan of the totals by the first warp, 16 digits a lane
-    if (tid < 32) {
-      const int each = (bins + 31) / 32;
-      uint32_t run = 0;
-      for (int i = 0; i < each; ++i)
-        if (tid * each + i < bins) run += total[tid * each + i];
-      uint32_t incl = run;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (tid >= o) incl += v;
-      }
-      run = incl - run;
-      for (int i = 0; i < each; ++i)
-        if (tid * each + i < bins) {
-          sums[tid * each + i] = run;
-          run += total[tid * each + i];
-        }
-    }
-    __syncthreads();
-    base = sums;
-  }
-  for (int i = tid; i < WARPS * bins; i += 32 * WARPS) cnt[i] += base[i % bins];
-  __syncthreads();
+// Marks a row as having tokens.  Frequent rows are marked thousands of times: the
+// word is read first.
+__device__ __forceinline__ void mark(uint32_t* present, uint32_t row) {
+  const uint32_t bit = 1u << (row & 31);
+  if (!(__ldcg(present + (row >> 5)) & bit)) atomicOr(present + (row >> 5), bit);
 }
 
-// Up to kSmallT tokens in one block; also marks the rows that have tokens.
-__global__ void __launch_bounds__(32 * kSmallWarps) sort_small_kernel(const int32_t* __restrict__ ids, int T,
-                                                                      int V, int pad, int passes, int bits,
-                                                                      uint32_t* __restrict__ keys,
-                                                                      int32_t* __restrict__ toks,
-                                                                      uint32_t* present, uint32_t* flags) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  const int bins = 1 << bits;
-  uint32_t* cnt = reinterpret_cast<uint32_t*>(smem);           // [warps][bins]
-  uint32_t* total = cnt + kSmallWarps * bins;                  // [bins]
-  uint32_t* sums = total + bins;                               // [bins]
-  uint32_t* key = sums + bins;                                 // [2][T]
-  uint16_t* tok = reinterpret_cast<uint16_t*>(key + 2 * T);    // [2][T]
+// Up to kSmallT tokens: a token's place is the number of tokens before it in the
+// sorted order, T comparisons each (T = 4096: 17 M over all SMs, 1.5 us of a launch;
+// one block with a radix sort in shared memory took 26).  A block finds the places of
+// 32 tokens, a lane each; its warps take a part of every kRankKeys keys.
+constexpr int kRankWarps = 8, kRankKeys = 4096;
+__global__ void __launch_bounds__(32 * kRankWarps) rank_kernel(const int32_t* __restrict__ ids, int T, int V, int pad,
+                                                               uint32_t* __restrict__ keys,
+                                                               int32_t* __restrict__ toks, uint32_t* present,
+                                                               uint32_t* flags) {
+  __shared__ __align__(16) uint32_t key[kRankKeys];
+  __shared__ uint32_t part[kRankWarps][32];
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per = ((T + 32 * kSmallWarps - 1) / (32 * kSmallWarps)) * 32;   // items of a warp
-  const int lo = min(T, warp * per), hi = min(T, lo + per);
-  for (int i = threadIdx.x; i < T; i += 32 * kSmallWarps) {
-    const int id = ids[i];
-    if ((uint32_t)id >= (uint32_t)V) set_flag(flags, kFlagToken);
-    const uint32_t k = key_of(id, V, pad);
-    key[i] = k;
-    tok[i] = (uint16_t)i;
-    if (present != nullptr && k < (uint32_t)V) atomicOr(present + (k >> 5), 1u << (k & 31));
-  }
-  __syncthreads();
-  for (int p = 0; p < passes; ++p) {
-    const uint32_t* ka = key + (p & 1) * T;
-    const uint16_t* ta = tok + (p & 1) * T;
-    uint32_t* kb = key + ((p & 1) ^ 1) * T;
-    uint16_t* tb = tok + ((p & 1) ^ 1) * T;
-    uint32_t* mine = cnt + warp * bins;
-    for (int d = lane; d < bins; d += 32) mine[d] = 0;
-    __syncwarp();
-    for (int i = lo; i < hi; i += 32) {
-      const bool live = i + lane < hi;
-      count_digit(mine, live ? (ka[i + lane] >> (p * bits)) & (bins - 1) : 0u, live);
-    }
+  const int first = blockIdx.x * 32, t = first + lane;
+  const int id = t < T ? ids[t] : 0;
+  const uint32_t mine = t < T ? key_of(id, V, pad) : 0u;
+  uint32_t n = 0;
+  for (int base = 0; base < T; base += kRankKeys) {
     __syncthreads();
-    scan_digits<kSmallWarps>(cnt, bins, nullptr, total, sums);
-    for (int i = lo; i < hi; i += 32) {
-      const bool live = i + lane < hi;
-      const uint32_t k = live ? ka[i + lane] : 0u;
-      const uint32_t at = place_digit(mine, (k >> (p * bits)) & (bins - 1), live);
-      if (live) {
-        kb[at] = k;
-        tb[at] = ta[i + lane];
+    for (int i = threadIdx.x; i < kRankKeys; i += 32 * kRankWarps)
+      key[i] = base + i < T ? key_of(ids[base + i], V, pad) : ~0u;    // ~0: before no token
+    __syncthreads();
+    constexpr int each = kRankKeys / kRankWarps;
+    const int lo = warp * each, hi = min(lo + each, T - base);
+    // four keys a step; those before the block's tokens count when equal, those behind
+    // them do not (first is a multiple of 32, so a step lies on one side of it or in it)
+    for (int i = lo; i < hi; i += 4) {
+      const uint4 k = *reinterpret_cast<const uint4*>(key + i);
+      const int at = base + i;
+      if (at + 4 <= first || at >= first + 32) {
+        const uint32_t lim = mine + (at < first ? 1u : 0u);
+        n += (k.x < lim) + (k.y < lim) + (k.z < lim) + (k.w < lim);
+      } else {
+        n += (k.x < mine + (at < t)) + (k.y < mine + (at + 1 < t)) + (k.z < mine + (at + 2 < t)) +
+             (k.w < mine + (at + 3 < t));
       }
     }
-    __syncthreads();
   }
-  for (int i = threadIdx.x; i < T; i += 32 * kSmallWarps) {
-    keys[i] = key[(passes & 1) * T + i];
-    toks[i] = tok[(passes & 1) * T + i];
-  }
+  part[warp][lane] = n;
+  __syncthreads();
+  if (warp != 0 || t >= T) return;
+  for (int w = 1; w < kRankWarps; ++w) n += part[w][lane];
+  keys[n] = mine;
+  toks[n] = t;
+  if ((uint32_t)id >= (uint32_t)V) set_flag(flags, kFlagToken);
+  if (present != nullptr && mine < (uint32_t)V) mark(present, mine);
 }
 
 // More tokens: each pass cuts the list into at most kMaxTiles tiles of `tile`
@@ -244,7 +199,7 @@ __global__ void __launch_bounds__(512) hist_kernel(const int32_t* __restrict__ i
     if ((uint32_t)id >= (uint32_t)V) set_flag(flags, kFlagToken);
     const uint32_t k = key_of(id, V, pad);
     atomicAdd(cnt + (k & (bins - 1)), 1u);
-    if (present != nullptr && k < (uint32_t)V) atomicOr(present + (k >> 5), 1u << (k & 31));
+    if (present != nullptr && k < (uint32_t)V) mark(present, k);
   }
   __syncthreads();
   for (int d = threadIdx.x; d < bins; d += 512) hist[(int64_t)blockIdx.x * bins + d] = cnt[d];
@@ -257,42 +212,32 @@ __global__ void __launch_bounds__(32 * kTileWarps) scatter_kernel(
     int64_t tile, int V, int pad, int pass, int bits, const uint32_t* __restrict__ hist, uint32_t* next,
     uint32_t* __restrict__ kout, int32_t* __restrict__ tout) {
   __shared__ uint32_t cnt[kTileWarps * kMaxBins];
-  __shared__ uint32_t base[kMaxBins], total[kMaxBins], sums[kMaxBins];
+  __shared__ uint32_t sums[kTileWarps];
   pdl_trigger();
   pdl_wait();
   const int bins = 1 << bits, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // where this tile's items of each digit start: all items of smaller digits,
-  // then the earlier tiles' items of this one
-  for (int d = threadIdx.x; d < bins; d += 32 * kTileWarps) {
-    uint32_t before = 0, all = 0;
+  // where this tile's items of a digit (a thread's each) start: all items of smaller
+  // digits, then the earlier tiles' items of this one
+  uint32_t before = 0, all = 0;
+  const int digit = threadIdx.x;
+  if (digit < bins) {
+#pragma unroll 16
     for (unsigned b = 0; b < gridDim.x; ++b) {
-      const uint32_t v = __ldcg(hist + (int64_t)b * bins + d);
-      if (b < blockIdx.x) before += v;
+      const uint32_t v = __ldcg(hist + (int64_t)b * bins + digit);
+      before += b < blockIdx.x ? v : 0u;
       all += v;
     }
-    base[d] = before;
-    total[d] = all;
   }
-  __syncthreads();
-  if (warp == 0) {
-    const int each = (bins + 31) / 32;
-    uint32_t run = 0;
-    for (int i = 0; i < each; ++i)
-      if (lane * each + i < bins) run += total[lane * each + i];
-    uint32_t incl = run;
+  uint32_t incl = all;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    run = incl - run;
-    for (int i = 0; i < each; ++i)
-      if (lane * each + i < bins) {
-        base[lane * each + i] += run;
-        run += total[lane * each + i];
-      }
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
   }
+  if (lane == 31) sums[warp] = incl;
   __syncthreads();
+  uint32_t start = before + incl - all;
+  for (int w = 0; w < warp; ++w) start += sums[w];
   const int64_t t0 = blockIdx.x * tile, t1 = min(T, t0 + tile), per = tile / kTileWarps;
   const int64_t lo = min(t1, t0 + warp * per), hi = min(t1, lo + per);
   uint32_t* mine = cnt + warp * bins;
@@ -305,7 +250,15 @@ __global__ void __launch_bounds__(32 * kTileWarps) scatter_kernel(
     count_digit(mine, live ? (key_at(i + lane) >> shift) & (bins - 1) : 0u, live);
   }
   __syncthreads();
-  scan_digits<kTileWarps>(cnt, bins, base, total, sums);
+  if (digit < bins) {
+#pragma unroll
+    for (int w = 0; w < kTileWarps; ++w) {
+      const uint32_t v = cnt[w * bins + digit];
+      cnt[w * bins + digit] = start;
+      start += v;
+    }
+  }
+  __syncthreads();
   for (int64_t i = lo; i < hi; i += 32) {
     const bool live = i + lane < hi;
     const uint32_t k = live ? key_at(i + lane) : 0u;
@@ -469,8 +422,7 @@ __global__ void __launch_bounds__(32 * kSumWarps) join_kernel(const SumArgs a, c
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t c = blockIdx.x / a.slabs;
-  const int col = (int)(blockIdx.x - c * a.slabs) * 256 + lane * 8;
+  const int64_t c = blockIdx.x;
   const int64_t p0 = c * a.chunk, p1 = p0 + a.chunk;
   if (p1 >= a.T) return;
   const uint32_t row = a.keys[p1];
@@ -485,30 +437,33 @@ __global__ void __launch_bounds__(32 * kSumWarps) join_kernel(const SumArgs a, c
     n += m < 0 ? 32 : m;
     if (m >= 0) break;
   }
-  const bool live = col < a.H;
-  const int64_t each = (n + kSumWarps - 1) / kSumWarps;
-  float f[8];
+  const int64_t each = (n + kSumWarps - 1) / kSumWarps, hi = min(n, (warp + 1) * each);
+  for (int slab = blockIdx.y; slab < a.slabs; slab += gridDim.y) {
+    const int col = slab * 256 + lane * 8;
+    const bool live = col < a.H;
+    float f[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = 0.0f;
-  if (live) {
-    auto take = [&](const float* p) {
-      const float4 u = __ldcg(reinterpret_cast<const float4*>(p)), v = __ldcg(reinterpret_cast<const float4*>(p) + 1);
-      f[0] += u.x; f[1] += u.y; f[2] += u.z; f[3] += u.w;
-      f[4] += v.x; f[5] += v.y; f[6] += v.z; f[7] += v.w;
-    };
-    if (warp == 0) take(a.right + c * a.H + col);
-    const int64_t hi = min(n, (warp + 1) * each);
+    for (int e = 0; e < 8; ++e) f[e] = 0.0f;
+    if (live) {
+      auto take = [&](const float* p) {
+        const float4 u = __ldcg(reinterpret_cast<const float4*>(p)), v = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+        f[0] += u.x; f[1] += u.y; f[2] += u.z; f[3] += u.w;
+        f[4] += v.x; f[5] += v.y; f[6] += v.z; f[7] += v.w;
+      };
+      if (warp == 0) take(a.right + c * a.H + col);
 #pragma unroll 4
-    for (int64_t i = warp * each; i < hi; ++i) take(a.left + (c + 1 + i) * a.H + col);
-  }
+      for (int64_t i = warp * each; i < hi; ++i) take(a.left + (c + 1 + i) * a.H + col);
+    }
+    __syncthreads();
 #pragma unroll
-  for (int e = 0; e < 8; ++e) part[warp][lane * 8 + e] = f[e];
-  __syncthreads();
-  if (warp == 0 && live) {
-    for (int w = 1; w < kSumWarps; ++w)
+    for (int e = 0; e < 8; ++e) part[warp][lane * 8 + e] = f[e];
+    __syncthreads();
+    if (warp == 0 && live) {
+      for (int w = 1; w < kSumWarps; ++w)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] += part[w][lane * 8 + e];
-    write8<T>(f, a.scale, add, dw, (int64_t)row * a.H + col);
+        for (int e = 0; e < 8; ++e) f[e] += part[w][lane * 8 + e];
+      write8<T>(f, a.scale, add, dw, (int64_t)row * a.H + col);
+    }
   }
 }
 
@@ -563,7 +518,8 @@ Layout layout_of(const EShape& s) {
   while (chunk < 256 && (s.T + chunk - 1) / chunk * L.slabs > 16 * 152) chunk *= 2;
   L.chunk = (int)chunk;
   L.chunks = (s.T + chunk - 1) / chunk;
-  L.tile = std::max<int64_t>(2048, ((s.T + kMaxTiles - 1) / kMaxTiles + 2047) / 2048 * 2048);
+  L.tile = ((s.T + kMaxTiles - 1) / kMaxTiles + kTileMin - 1) / kTileMin * kTileMin;
+  if (L.tile < kTileMin) L.tile = kTileMin;
   L.tiles = (s.T + L.tile - 1) / L.tile;
   const bool small = s.T <= kSmallT;
   L.flags = take(256);
@@ -581,8 +537,22 @@ Layout layout_of(const EShape& s) {
   return L;
 }
 
-constexpr int small_smem(int T, int bits) {
-  return (kSmallWarps + 2) * (1 << bits) * 4 + T * 2 * 6;
+template <typename T>
+cudaError_t launch_join(const SumArgs& a, const T* add, T* dw, cudaStream_t st) {
+  // most chunks have no row to join: one check for a chunk's slabs, up to four at once
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)a.chunks, (unsigned)std::min(a.slabs, 4));
+  cfg.blockDim = dim3(32 * kSumWarps);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, join_kernel<T>, a, add, dw);
+  if (e != cudaSuccess) return e;
+  count_launch();
+  return cudaGetLastError();
 }
 
 template <typename T>
@@ -596,11 +566,9 @@ moe_status backward(const EShape& s, const Layout& L, char* b, const int32_t* id
   int at = 0;    // where the sorted list is
   if (s.T > kSmallT || fill) CHECK_CUDA(cudaMemsetAsync(b + L.present, 0, L.zero_end - L.present, st));
   if (s.T > 0 && s.T <= kSmallT) {
-    const int bytes = small_smem((int)s.T, L.dig.bits);
-    CHECK_CUDA(cudaFuncSetAttribute(sort_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, small_smem(kSmallT, kMaxBits)));
-    CHECK_CUDA(launch_after(sort_small_kernel, 1, 32 * kSmallWarps, bytes, st, 1, ids, (int)s.T, s.V, s.pad, L.dig.passes,
-                            L.dig.bits, reinterpret_cast<uint32_t*>(b + L.keys[0]),
-                            reinterpret_cast<int32_t*>(b + L.toks[0]), present, flags));
+    CHECK_CUDA(launch_after(rank_kernel, (unsigned)((s.T + 31) / 32), 32 * kRankWarps, 0, st, 1, ids, (int)s.T, s.V, s.pad,
+                            reinterpret_cast<uint32_t*>(b + L.keys[0]), reinterpret_cast<int32_t*>(b + L.toks[0]),
+                            present, flags));
   } else if (s.T > 0) {
     CHECK_CUDA(launch_after(hist_kernel, (unsigned)L.tiles, 512, 0, st, 1, ids, s.T, L.tile, s.V, s.pad, 1 << L.dig.bits,
                             hist, present, flags));
@@ -636,8 +604,7 @@ moe_status backward(const EShape& s, const Layout& L, char* b, const int32_t* id
     CHECK_CUDA(launch_after(sum_kernel<T>, (unsigned)(a.acc_blocks + fill_blocks), 32 * kSumWarps, 0, st, 1, a,
                             static_cast<const T*>(dy), static_cast<const T*>(add), static_cast<T*>(dw)));
   if (L.chunks > 1)
-    CHECK_CUDA(launch_after(join_kernel<T>, (unsigned)(L.chunks * L.slabs), 32 * kSumWarps, 0, st, 1, a,
-                            static_cast<const T*>(add), static_cast<T*>(dw)));
+    CHECK_CUDA(launch_join<T>(a, static_cast<const T*>(add), static_cast<T*>(dw), st));
   return MOE_OK;
 }
 

@@ -3,6 +3,7 @@
 // small kernels around them.
 #pragma once
 
+#include <atomic>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -43,6 +44,19 @@ cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned block, si
   if (e != cudaSuccess) return e;
   count_launch();
   return cudaGetLastError();
+}
+
+// Lets a kernel have `bytes` of dynamic shared memory, once a device (done: a bit each).
+template <typename K>
+cudaError_t allow_smem(K* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 #endif
 

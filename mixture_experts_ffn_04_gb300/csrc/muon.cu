@@ -48,7 +48,8 @@ struct Round {
   int32_t nesterov, update;   // update: param = keep param - size X, else out = X
   double eps;
   double* sums;               // [batch][parts]
-  __half* x;                  // [2][batch][m][ldx]
+  int32_t planes;             // of X: two of fp16, or one and 8-bit parts (orth.h)
+  __half* x;                  // [planes][batch][m][ldx], the 8-bit parts behind
 };
 
 __device__ __forceinline__ const Seg& seg_of(const Round& r, int b) {
@@ -193,19 +194,64 @@ __device__ __forceinline__ float2 scale_of(double sum, double eps) {
   return make_float2(ldexpf(1.0f, h), (float)ldexp(1.0 / f, kOrthX - e - h));
 }
 
-__device__ __forceinline__ void split8(const float* f, uint4& hi, uint4& lo) {
-  uint32_t h[4], l[4];
+// 8 values to X, from `at` elements of the round's first plane.
+__device__ __forceinline__ void put8(const Round& r, int64_t at, const float* f) {
+  uint32_t h[4];
+  float lead[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const __half2 a = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
     const float2 v = __half22float2(a);
-    const __half2 c = __floats2half2_rn(f[2 * i] - v.x, f[2 * i + 1] - v.y);
+    lead[2 * i] = v.x;
+    lead[2 * i + 1] = v.y;
     h[i] = *reinterpret_cast<const uint32_t*>(&a);
-    l[i] = *reinterpret_cast<const uint32_t*>(&c);
   }
-  hi = make_uint4(h[0], h[1], h[2], h[3]);
-  lo = make_uint4(l[0], l[1], l[2], l[3]);
+  *reinterpret_cast<uint4*>(r.x + at) = make_uint4(h[0], h[1], h[2], h[3]);
+  const int64_t plane = (int64_t)r.batch * r.m * r.ldx;
+  if (r.planes == 2) {
+    uint32_t l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 c = __floats2half2_rn(f[2 * i] - lead[2 * i], f[2 * i + 1] - lead[2 * i + 1]);
+      l[i] = *reinterpret_cast<const uint32_t*>(&c);
+    }
+    *reinterpret_cast<uint4*>(r.x + plane + at) = make_uint4(l[0], l[1], l[2], l[3]);
+  } else {
+    uint32_t l[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) l[i / 4] |= (uint32_t)(orth_low_part(f[i], lead[i]) & 255) << (i % 4 * 8);
+    *reinterpret_cast<uint2*>(reinterpret_cast<char*>(r.x + plane) + at) = make_uint2(l[0], l[1]);
+  }
 }
+__device__ __forceinline__ void get8(const Round& r, int64_t at, float* f) {
+  const uint4 hi = *reinterpret_cast<const uint4*>(r.x + at);
+  const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    f[2 * i] = a.x;
+    f[2 * i + 1] = a.y;
+  }
+  const int64_t plane = (int64_t)r.batch * r.m * r.ldx;
+  if (r.planes == 2) {
+    const uint4 lo = *reinterpret_cast<const uint4*>(r.x + plane + at);
+    const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&l[i]));
+      f[2 * i] += b.x;
+      f[2 * i + 1] += b.y;
+    }
+  } else {
+    const uint2 lo = *reinterpret_cast<const uint2*>(reinterpret_cast<const char*>(r.x + plane) + at);
+    const uint32_t l[2] = {lo.x, lo.y};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = orth_with_low(f[i], (int)(int8_t)((l[i / 4] >> (i % 4 * 8)) & 255u));
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] *= 0x1p-13f;
+}
+static_assert(kOrthX == 13, "get8's factor");
 
 struct TileAt {
   int b, r0, c0;   // matrix of the round; first row and column of the tile in its tensor
@@ -223,7 +269,7 @@ __device__ __forceinline__ TileAt tile_at(const Round& r, int64_t task, const Se
   return t;
 }
 
-// u / (norm + eps) in two fp16 planes, its smaller side as rows.
+// u / (norm + eps) as X is held, its smaller side as rows.
 __global__ void __launch_bounds__(256) planes_kernel(const __grid_constant__ Round r) {
   __shared__ float sh[kTile][kTile + 1];
   __shared__ double part[8];
@@ -232,7 +278,6 @@ __global__ void __launch_bounds__(256) planes_kernel(const __grid_constant__ Rou
   pdl_wait();
   const int tid = threadIdx.x;
   const int64_t tiles = (int64_t)((r.m + kTile - 1) / kTile) * ((r.n + kTile - 1) / kTile);
-  const int64_t plane = (int64_t)r.batch * r.m * r.ldx;
   int last = -1;
   // a block takes neighbouring tiles, so that a matrix's norm is added up once
   const int64_t all = tiles * r.batch, each = (all + gridDim.x - 1) / gridDim.x;
@@ -260,7 +305,7 @@ __global__ void __launch_bounds__(256) planes_kernel(const __grid_constant__ Rou
     const bool tall = s->rows > s->cols;
     const int64_t base = (s->first + (t.b - s->at)) * (int64_t)s->rows * s->cols;
     const bool ok = s->cols % 8 == 0 && aligned(s->grad) && aligned(s->momentum);
-    __half* x = r.x + (int64_t)t.b * r.m * r.ldx;
+    const int64_t x = (int64_t)t.b * r.m * r.ldx;   // of the matrix in the planes
     if (tall) __syncthreads();   // the last tile's readers are done
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -281,12 +326,7 @@ __global__ void __launch_bounds__(256) planes_kernel(const __grid_constant__ Rou
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = e < n ? f[e] * q.x * q.y : 0.0f;
-        if (!tall) {
-          uint4 hi, lo;
-          split8(f, hi, lo);
-          *reinterpret_cast<uint4*>(x + (int64_t)row * r.ldx + col) = hi;
-          *reinterpret_cast<uint4*>(x + plane + (int64_t)row * r.ldx + col) = lo;
-        }
+        if (!tall) put8(r, x + (int64_t)row * r.ldx + col, f);
       }
       if (tall) {
 #pragma unroll
@@ -303,41 +343,25 @@ __global__ void __launch_bounds__(256) planes_kernel(const __grid_constant__ Rou
       float f[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = sh[lc + e][lr];
-      uint4 hi, lo;
-      split8(f, hi, lo);
-      *reinterpret_cast<uint4*>(x + (int64_t)row * r.ldx + col) = hi;
-      *reinterpret_cast<uint4*>(x + plane + (int64_t)row * r.ldx + col) = lo;
+      put8(r, x + (int64_t)row * r.ldx + col, f);
     }
   }
 }
 
-// param = keep param - size X, or out = X, from the two planes.
+// param = keep param - size X, or out = X.
 __global__ void __launch_bounds__(256) update_kernel(const __grid_constant__ Round r) {
   __shared__ float sh[kTile][kTile + 1];
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x;
   const int64_t all = (int64_t)((r.m + kTile - 1) / kTile) * ((r.n + kTile - 1) / kTile) * r.batch;
-  const int64_t plane = (int64_t)r.batch * r.m * r.ldx;
   for (int64_t task = blockIdx.x; task < all; task += gridDim.x) {
     const Seg* s;
     const TileAt t = tile_at(r, task, s);
     const bool tall = s->rows > s->cols;
     const int64_t base = (s->first + (t.b - s->at)) * (int64_t)s->rows * s->cols;
     const bool ok = s->cols % 8 == 0 && aligned(s->param);
-    const __half* x = r.x + (int64_t)t.b * r.m * r.ldx;
-    auto load = [&](int row, int col, float* f) {
-      const uint4 hi = *reinterpret_cast<const uint4*>(x + (int64_t)row * r.ldx + col);
-      const uint4 lo = *reinterpret_cast<const uint4*>(x + plane + (int64_t)row * r.ldx + col);
-      const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&l[i]));
-        f[2 * i] = (a.x + b.x) * ldexpf(1.0f, -kOrthX);
-        f[2 * i + 1] = (a.y + b.y) * ldexpf(1.0f, -kOrthX);
-      }
-    };
+    const int64_t x = (int64_t)t.b * r.m * r.ldx;
     if (tall) {
       __syncthreads();
 #pragma unroll
@@ -346,7 +370,7 @@ __global__ void __launch_bounds__(256) update_kernel(const __grid_constant__ Rou
         const int row = t.c0 + lr, col = t.r0 + lc;
         if (row < r.m && col < r.n) {
           float f[8];
-          load(row, col, f);
+          get8(r, x + (int64_t)row * r.ldx + col, f);
 #pragma unroll
           for (int e = 0; e < 8; ++e) sh[lc + e][lr] = f[e];
         }
@@ -365,7 +389,7 @@ __global__ void __launch_bounds__(256) update_kernel(const __grid_constant__ Rou
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = e < n ? sh[lr][lc + e] : 0.0f;
       } else {
-        load(row, col, f);
+        get8(r, x + (int64_t)row * r.ldx + col, f);
       }
       if (r.update) {
         float w[8];
@@ -389,6 +413,9 @@ struct Bucket {
   int64_t round;   // matrices at a time
 };
 
+// Bytes of one X: two fp16 planes, or one and the 8-bit parts.
+int64_t x_bytes(const Bucket& b) { return (int64_t)b.m * b.ldx * (b.planes == 2 ? 4 : 3); }
+
 Bucket bucket_of(int m, int n, int planes, int64_t batch) {
   Bucket b = {};
   b.m = m;
@@ -396,11 +423,11 @@ Bucket bucket_of(int m, int n, int planes, int64_t batch) {
   b.planes = planes;
   b.batch = batch;
   // rows on 128-byte boundaries where they are long enough for it
-  auto pad = [](int v) { return v >= 64 ? (v + 63) / 64 * 64 : (v + 7) / 8 * 8; };
+  auto pad = [](int v) { return v >= 64 ? (v + 63) / 64 * 64 : (v + 15) / 16 * 16; };
   b.ldx = pad(n);
   b.lda = pad(m);
   b.parts = (int)(((int64_t)m * n + kPart - 1) / kPart);
-  b.each = 4ll * m * b.ldx * 2 + 2ll * planes * m * b.lda * 2 + 8ll * b.parts;
+  b.each = 2 * x_bytes(b) + 2ll * planes * m * b.lda * 2 + 8ll * b.parts;
   b.round = std::max<int64_t>(1, std::min<int64_t>(batch, std::min<int64_t>(kMaxRound, kScratch / b.each)));
   return b;
 }
@@ -417,7 +444,7 @@ RoundLayout layout_of(const Bucket& q) {
     return at;
   };
   L.sums = take((size_t)q.round * q.parts * 8);
-  for (int i = 0; i < 2; ++i) L.x[i] = take((size_t)q.round * 4 * q.m * q.ldx);
+  for (int i = 0; i < 2; ++i) L.x[i] = take((size_t)q.round * x_bytes(q));
   L.a = take((size_t)q.round * q.planes * q.m * q.lda * 2);
   L.b = take((size_t)q.round * q.planes * q.m * q.lda * 2);
   L.total = off;
@@ -471,6 +498,7 @@ cudaError_t run_round(Round& r, const Bucket& q, const RoundLayout& L, char* ws,
   r.n = q.n;
   r.ldx = q.ldx;
   r.parts = q.parts;
+  r.planes = q.planes;
   r.eps = c.eps;
   r.sums = reinterpret_cast<double*>(ws + L.sums);
   r.x = reinterpret_cast<__half*>(ws + L.x[0]);

@@ -7,14 +7,15 @@
 
 namespace moe {
 
-// A matrix is held as one or two fp16 planes of its values times a power of two:
-// the leading 11 bits, and the next 11.  X [m, n] with m <= n, its singular values at
-// most 3.5; A = X X^T; B = b A + c A A, at most 100.
+// A matrix is held as fp16 planes of its values times a power of two: the leading 11
+// bits, and the next 11; X of bf16 matrices as one plane and an 8-bit part, the next 8 bits.
+// X [m, n] with m <= n, its singular values at most 3.5; A = X X^T; B = b A + c A A, at most
+// 100.
 constexpr int kOrthX = 13, kOrthA = 11, kOrthB = 9;
 constexpr double kOrthMaxX = 3.5, kOrthMaxB = 100.0;
 
-// A batch in scratch.  x[0], x[1]: two planes each, [2][batch][m][ldx]; a, b: `planes`
-// planes, [planes][batch][m][lda]; rows start on 16-byte boundaries.
+// A batch in scratch.  x[0], x[1]: [planes][batch][m][ldx] each, with one plane the 8-bit
+// parts [batch][m][ldx] behind it; a, b: [planes][batch][m][lda]; ldx and lda multiples of 16.
 struct OrthBatch {
   int64_t batch;
   int m, n, ldx, lda;
@@ -24,6 +25,23 @@ struct OrthBatch {
   void* b;
   uint32_t* flags;
 };
+
+#ifdef __CUDACC__
+// The 8-bit part of f whose leading fp16 plane is h (as fp32): how far f's bit pattern
+// is from h's, in steps of 32 of at most 4096 either way (half of h's last bit), so h
+// and the part hold 19 bits.  Integer steps at full rate: with a part in units of h's
+// last bit, through float-integer conversions at a quarter of it, the epilogue took longer
+// than the products.  Below fp16's normal range the part stops at its limit, closer to f
+// than h alone.
+__device__ __forceinline__ int orth_low_part(float f, float h) {
+  const int d = __float_as_int(f) - __float_as_int(h);
+  return (d < -4096 ? -4096 : (d > 4095 ? 4095 : d)) >> 5;
+}
+// low: sign-extended
+__device__ __forceinline__ float orth_with_low(float h, int low) {
+  return __int_as_float(__float_as_int(h) + low * 32 + 16);
+}
+#endif
 
 // `steps` times X <- a X + (b A + c A A) X with (a, b, c) = coef[i], from x[0]; the
 // last X is in x[steps & 1].

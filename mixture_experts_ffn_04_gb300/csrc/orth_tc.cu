@@ -16,13 +16,15 @@
 // the same plane as A A: with b A exact instead 2.8e-3).  fp32 matrices take three
 // products of two planes each, smallest first: 5.7e-7 (fp32 products: 7.2e-6).
 //
-// A pair of SMs computes 256 x 256 tiles over 64-wide k-blocks through six 32 KB
+// A pair of SMs computes 256 x 256 tiles over 64-wide k-blocks through four 32 KB
 // stages.  The sums of a tile leave TMEM in chunks of k-blocks (the tensor cores cut
 // the accumulator off at each K = 16 step) into fp32 registers, which start from the
 // addend a X or b A, read while the tile's products run.
 //
 // Roles in each CTA: warp 0 TMA producer, warp 1 TMEM and (even CTA) the MMA
-// issuer, warps 4-11 epilogue, two a 32-lane TMEM quarter.  Tiles are dealt out in a
+// issuer, warps 4-19 epilogue, four a 32-lane TMEM quarter (with two, whose 128 columns a
+// thread had two warps a scheduler to hide behind, a 256 x 256 tile of kApply took
+// 8.3 us, three times its products).  Tiles are dealt out in a
 // fixed order (all have the same K).  Every wait on an mbarrier is bounded, and a CTA
 // that gives up waits, with a limit, for its copies and MMAs in flight.
 #include <atomic>
@@ -46,22 +48,24 @@ namespace orth {
 using namespace tc;
 
 constexpr int BM = 256, BN = 256, BMC = BM / 2, BNC = BN / 2, BK = 64;
-constexpr int S = 6;
+constexpr int S = 4;
 constexpr int A_BYTES = BMC * BK * 2, B_BYTES = BNC * BK * 2;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int BOX_BYTES = 64 * BK * 2;
 constexpr int RING_BYTES = S * STAGE_BYTES;
-constexpr int EPI_WARPS = 8;
+constexpr int EPI_WARPS = 16, EPI_COLS = 64;   // a warp: 32 rows, 64 columns
 constexpr int THREADS = 32 * (4 + EPI_WARPS);
-// 168 registers a thread at launch; 56 + 2 * 224 <= 3 * 168 (three groups of 4 warps)
-constexpr int ROLE_REGS = 56, EPI_REGS = 224;
-static_assert(ROLE_REGS + 2 * EPI_REGS <= 3 * 168, "register pool of the launch");
+// 96 registers a thread at launch; 56 + 4 * 104 <= 5 * 96 (five groups of 4 warps)
+constexpr int ROLE_REGS = 56, EPI_REGS = 104;
+static_assert(ROLE_REGS + 4 * EPI_REGS <= 5 * 96, "register pool of the launch");
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int BAR_BYTES = 256;
-constexpr int STAGE_WARP = 4096;   // staging of an epilogue warp: 32 rows of 128 bytes
+constexpr int BAR_BYTES = 512;
+// staging of an epilogue warp: 32 rows of 64 fp16 values (128-byte swizzle), and of 64
+// 8-bit parts (64-byte swizzle)
+constexpr int HALF_BYTES = 4096, LOW_BYTES = 2048, STAGE_WARP = HALF_BYTES + LOW_BYTES;
 constexpr int SMEM_BYTES = 1024 + RING_BYTES + EPI_WARPS * STAGE_WARP + BAR_BYTES;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget of one CTA");
-static_assert((2 * S + 5 + EPI_WARPS) * 8 + 8 <= BAR_BYTES, "barrier area");
+static_assert((2 * S + 5 + 2 * EPI_WARPS) * 8 + 8 <= BAR_BYTES, "barrier area");
 constexpr long long kDrainCycles = 1 << 21;
 constexpr int kChunkExact = 8, kChunkHalf = 64;   // k-blocks: two planes, one plane
 
@@ -77,8 +81,9 @@ struct Args {
   int kb;                 // k-blocks
   int mt, nt, per;        // row tiles, column tiles, tiles a matrix
   float add_scale, mul;   // result = add_scale * addend + mul * product
-  int out_planes;         // 1 or 2
-  int add_planes;         // of the addend: 0, 1 or 2
+  const char* add;        // the addend's leading plane, rows ld bytes apart: for the L2
+  const char* add_low;    // its second plane, or 8-bit parts
+  int64_t add_ld, low_ld;
   uint32_t* flags;
 };
 
@@ -129,21 +134,31 @@ __device__ __forceinline__ void box_out(const CUtensorMap* map, uint32_t stage, 
   }
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
+}
+
+// How X' and the addend are held: kOne: one fp16 plane (A, B); kTwo: two; kLow: one
+// and the 8-bit part (X of bf16 matrices).
+enum Form { kOne = 0, kTwo = 1, kLow = 2 };
+
 // Maps are 3-D, {columns, rows, plane * batch + matrix}.  mA, mB: operand boxes
 // (128 x 64; kApply's B operand 64 x 64 in its stored layout); mAdd, mOut: 32 rows of
-// 64 columns; mT: 64 rows of 32 columns, for the transposed tile.
-template <int KIND>
-__global__ void __launch_bounds__(THREADS, 1)
-    orth_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB,
-                const __grid_constant__ CUtensorMap mAdd, const __grid_constant__ CUtensorMap mOut,
-                const __grid_constant__ CUtensorMap mT, const Args a) {
+// 64 columns; mAddLow, mOutLow: 32 rows of 64 8-bit parts; mT: 64 rows of 32 columns, for the
+// transposed tile.
+struct Maps {
+  CUtensorMap A, B, Add, AddLow, Out, OutLow, T;
+};
+
+template <int KIND, int FORM>
+__global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant__ Maps maps, const Args a) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   unsigned char* s_out = smem + RING_BYTES;
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_out + EPI_WARPS * STAGE_WARP);
-  // bars: full[S] empty[S] tfull[2] tempty[2] final addend[EPI_WARPS]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5 + EPI_WARPS);
+  // bars: full[S] empty[S] tfull[2] tempty[2] final addend[2 * EPI_WARPS]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5 + 2 * EPI_WARPS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   pdl_trigger();
@@ -168,7 +183,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(tempty(b), 2 * EPI_WARPS);
     }
     mbar_init(final_bar, 1);
-    for (int w = 0; w < EPI_WARPS; ++w) mbar_init(addend(w), 1);
+    for (int w = 0; w < 2 * EPI_WARPS; ++w) mbar_init(addend(w), 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -209,12 +224,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!wait_cl(empty(s), ph ^ 1u, abort_flag)) { ok = false; break; }
             const uint32_t sa = ring + s * STAGE_BYTES, sb = sa + A_BYTES, fb = full0 + 8u * s;
             if (leader) mbar_expect_tx(full(s), 2 * STAGE_BYTES);
-            tma_load_3d_pair(sa, &mA, k, arow, za, fb);
+            tma_load_3d_pair(sa, &maps.A, k, arow, za, fb);
             if (KIND == kApply) {
-              tma_load_3d_pair(sb, &mB, bcol, k, zb, fb);
-              tma_load_3d_pair(sb + BOX_BYTES, &mB, bcol + 64, k, zb, fb);
+              tma_load_3d_pair(sb, &maps.B, bcol, k, zb, fb);
+              tma_load_3d_pair(sb + BOX_BYTES, &maps.B, bcol + 64, k, zb, fb);
             } else {
-              tma_load_3d_pair(sb, &mB, k, bcol, zb, fb);
+              tma_load_3d_pair(sb, &maps.B, k, bcol, zb, fb);
             }
             ++issued;
             if (++s == S) { s = 0; ph ^= 1u; }
@@ -268,42 +283,93 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
   } else {
-    // ---------------- epilogue (warps 4..11, both CTAs) ----------------
+    // ---------------- epilogue (warps 4..19, both CTAs) ----------------
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
     const int q = warp & 3;                 // TMEM lanes 32q .. 32q+31
-    const int c_lo = (warp - 4) / 4 * (BN / 2);
-    const uint32_t stage = smem_u32(s_out + (warp - 4) * STAGE_WARP);
+    const int c_lo = (warp - 4) / 4 * EPI_COLS;
+    const uint32_t half = smem_u32(s_out + (warp - 4) * STAGE_WARP), lows = half + HALF_BYTES;
+    const uint32_t half_bar = addend(2 * (warp - 4)), low_bar = addend(2 * (warp - 4) + 1);
     const int width = KIND == kApply ? a.n : a.m;
     int acc = 0;
-    uint32_t aph = 0, add_ph = 0;
+    uint32_t aph = 0, half_ph = 0, low_ph = 0;
     bool ok = true;
+    // lane 0 waits for a box, the others' reads come after it
+    auto landed = [&](uint32_t bar, uint32_t& ph) {
+      int w = 1;
+      if (lane == 0) {
+        w = wait_cl(bar, ph, abort_flag) ? 1 : 0;
+        // given up (perhaps for another warp's wait): the box still lands first
+        if (!w) wait2_quiet(bar, ph);
+      }
+      ph ^= 1u;
+      ok = __shfl_sync(0xffffffffu, w, 0) && ok;
+      __syncwarp();   // (the exchange alone orders no memory)
+    };
+    auto ask = [&](uint32_t to, const CUtensorMap* map, int col, int row, int z, uint32_t bar, uint32_t bytes) {
+      if (lane != 0) return;
+      mbar_expect_tx(bar, bytes);
+      tma_load_3d(to, map, col, row, z, bar);
+    };
+    // 16 bytes j of this lane's 64-byte row of 8-bit parts
+    auto low_at = [&](int j) { return lows + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4); };
     for (uint32_t t = first; ok && t < total; t += step) {
       const Tile d = decode<KIND>(a, t);
       const int row0 = d.i * BM + (int)rank * BMC + q * 32, n0 = d.j * BN + c_lo;
-      float f[BN / 2];
+      const bool live = row0 < a.m && n0 < width;
+      float f[EPI_COLS];
 #pragma unroll
-      for (int j = 0; j < BN / 2; ++j) f[j] = 0.0f;
-      if (KIND != kGram && row0 < a.m) {
-        // start from the addend: boxes through the staging slice
+      for (int j = 0; j < EPI_COLS; ++j) f[j] = 0.0f;
+      if (KIND != kGram && live) {
+        // start from the addend
+        stage_free(lane);
+        ask(half, &maps.Add, n0, row0, d.b, half_bar, HALF_BYTES);
+        if (FORM == kLow) {
+          ask(lows, &maps.AddLow, n0, row0, d.b, low_bar, LOW_BYTES);
+          landed(half_bar, half_ph);
+          landed(low_bar, low_ph);
 #pragma unroll
-        for (int c = 0; c < BN / 2; c += 64) {
-          if (n0 + c >= width) continue;
-          for (int p = 0; p < a.add_planes && ok; ++p) {
-            stage_free(lane);
-            int w = 1;
-            if (lane == 0) {
-              mbar_expect_tx(addend(warp - 4), STAGE_WARP);
-              tma_load_3d(stage, &mAdd, n0 + c, row0, p * a.batch + d.b, addend(warp - 4));
-              w = wait_cl(addend(warp - 4), add_ph, abort_flag) ? 1 : 0;
-              // given up (perhaps for another warp's wait): the box still lands first
-              if (!w) wait2_quiet(addend(warp - 4), add_ph);
+          for (int j = 0; j < 4; ++j) {
+            uint4 l;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(l.x), "=r"(l.y), "=r"(l.z), "=r"(l.w)
+                         : "r"(low_at(j))
+                         : "memory");
+            const uint32_t low[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint4 v = get_piece(half, lane, 2 * j + h);
+              const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w4[e]));
+                const int at = 8 * h + 2 * e;    // of the 16 parts
+                const uint32_t q2 = low[at / 4] >> (at % 4 * 8);
+                f[16 * j + at] = a.add_scale * orth_with_low(x.x, (int)(int8_t)(q2 & 255u));
+                f[16 * j + at + 1] = a.add_scale * orth_with_low(x.y, (int)(int8_t)((q2 >> 8) & 255u));
+              }
             }
-            add_ph ^= 1u;
-            ok = __shfl_sync(0xffffffffu, w, 0);
-            if (!ok) break;
+          }
+        } else {
+          landed(half_bar, half_ph);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) add_halves(f + c + 8 * j, get_piece(stage, lane, j), a.add_scale);
+          for (int j = 0; j < 8; ++j) add_halves(f + 8 * j, get_piece(half, lane, j), a.add_scale);
+          if (FORM == kTwo) {
             __syncwarp();
+            ask(half, &maps.Add, n0, row0, a.batch + d.b, half_bar, HALF_BYTES);
+            landed(half_bar, half_ph);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) add_halves(f + 8 * j, get_piece(half, lane, j), a.add_scale);
+          }
+        }
+        __syncwarp();
+        // the next tile's addend to the L2 while this one is worked on
+        if (t + step < total) {
+          const Tile e = decode<KIND>(a, t + step);
+          const int row = e.i * BM + (int)rank * BMC + q * 32 + lane, col = e.j * BN + c_lo;
+          if (row < a.m && col < width) {
+            prefetch_l2(a.add + ((int64_t)e.b * a.m + row) * a.add_ld + 2 * col);
+            if (FORM != kOne)
+              prefetch_l2(a.add_low + ((int64_t)e.b * a.m + row) * a.low_ld + (FORM == kTwo ? 2 : 1) * col);
           }
         }
       }
@@ -317,16 +383,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_after();
         const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)acc * BN + c_lo;
 #pragma unroll
-        for (int c = 0; c < BN / 2; c += 64) {
-          uint32_t r0[32], r1[32];
-          tmem_ld32(taddr + c, r0);
-          tmem_ld32(taddr + c + 32, r1);
+        for (int c = 0; c < EPI_COLS; c += 16) {
+          uint32_t r[16];
+          tmem_ld16(taddr + c, r);
           tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            f[c + j] = fmaf(a.mul, __uint_as_float(r0[j]), f[c + j]);
-            f[c + 32 + j] = fmaf(a.mul, __uint_as_float(r1[j]), f[c + 32 + j]);
-          }
+          for (int j = 0; j < 16; ++j) f[c + j] = fmaf(a.mul, __uint_as_float(r[j]), f[c + j]);
         }
         tc_fence_before();
         __syncwarp();
@@ -335,38 +397,65 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (acc == 0) aph ^= 1u;
       }
       if (!ok) break;
-      if (row0 >= a.m) continue;
+      if (!live) continue;
       const bool mirror = KIND != kApply && d.i != d.j;
 #pragma unroll
-      for (int c = 0; c < BN / 2; c += 64) {
-        if (n0 + c >= width) continue;
-        for (int p = 0; p < a.out_planes; ++p) {
-          const int z = p * a.batch + d.b;
-          stage_free(lane);
+      for (int p = 0; p < (FORM == kTwo ? 2 : 1); ++p) {
+        const int z = p * a.batch + d.b;
+        stage_free(lane);
+        if (FORM == kLow) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t l[4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t w4[4];
+              int low[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float* v = f + 16 * j + 8 * h + 2 * e;
+                w4[e] = pack_half2(v[0], v[1]);
+                const float2 lead = __half22float2(*reinterpret_cast<const __half2*>(&w4[e]));
+                low[2 * e] = orth_low_part(v[0], lead.x);
+                low[2 * e + 1] = orth_low_part(v[1], lead.y);
+              }
+              put_piece(half, lane, 2 * j + h, make_uint4(w4[0], w4[1], w4[2], w4[3]));
+              // the low bytes of four words
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                l[2 * h + e] = __byte_perm(__byte_perm(low[4 * e], low[4 * e + 1], 0x0040),
+                                           __byte_perm(low[4 * e + 2], low[4 * e + 3], 0x0040), 0x5410);
+            }
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(low_at(j)), "r"(l[0]), "r"(l[1]), "r"(l[2]),
+                         "r"(l[3])
+                         : "memory");
+          }
+          box_out(&maps.OutLow, lows, lane, n0, row0, z);
+        } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float* v = f + c + 8 * j;
-            put_piece(stage, lane, j, make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]),
-                                                 pack_half2(v[4], v[5]), pack_half2(v[6], v[7])));
+            const float* v = f + 8 * j;
+            put_piece(half, lane, j, make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]), pack_half2(v[4], v[5]),
+                                                pack_half2(v[6], v[7])));
           }
-          box_out(&mOut, stage, lane, n0 + c, row0, z);
-          if (mirror) {
-            // the transposed box: 64 rows (this warp's columns) of 32 values
-            stage_free(lane);
+        }
+        box_out(&maps.Out, half, lane, n0, row0, z);
+        if (mirror) {
+          // the transposed box: 64 rows (this warp's columns) of 32 values
+          stage_free(lane);
 #pragma unroll
-            for (int j = 0; j < 64; ++j) {
-              const __half h = __float2half_rn(f[c + j]);
-              asm volatile("st.shared.u16 [%0], %1;" ::"r"(stage + j * 64 + lane * 2),
-                           "h"(*reinterpret_cast<const unsigned short*>(&h))
-                           : "memory");
-            }
-            box_out(&mT, stage, lane, row0, n0 + c, z);
+          for (int j = 0; j < EPI_COLS; ++j) {
+            const __half h = __float2half_rn(f[j]);
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(half + j * 64 + lane * 2),
+                         "h"(*reinterpret_cast<const unsigned short*>(&h))
+                         : "memory");
           }
-          if (p + 1 < a.out_planes) {
-            // what the leading plane leaves
+          box_out(&maps.T, half, lane, row0, n0, z);
+        }
+        if (FORM == kTwo && p == 0) {
+          // what the leading plane leaves
 #pragma unroll
-            for (int j = 0; j < 64; ++j) f[c + j] -= __half2float(__float2half_rn(f[c + j]));
-          }
+          for (int j = 0; j < EPI_COLS; ++j) f[j] -= __half2float(__float2half_rn(f[j]));
         }
       }
     }
@@ -391,17 +480,17 @@ __global__ void __launch_bounds__(THREADS, 1)
 // host side
 // ---------------------------------------------------------------------------
 
-// [planes * batch] matrices [rows, cols] of fp16, rows ld elements apart.
+// `count` matrices [rows, cols] of fp16 (or bytes), rows ld elements apart.
 static bool map3(CUtensorMap* m, const void* ptr, int64_t count, int rows, int cols, int ld, int box_cols, int box_rows,
-                 bool swizzle) {
+                 CUtensorMapSwizzle swizzle, int esize = 2) {
   cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)count};
-  cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * 2 * (cuuint64_t)rows};
+  cuuint64_t strides[2] = {(cuuint64_t)ld * esize, (cuuint64_t)ld * esize * (cuuint64_t)rows};
   cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
   cuuint32_t es[3] = {1, 1, 1};
   return encode_fn() != nullptr &&
-         encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, es,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+         encode_fn()(m, esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
+                     const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 static std::atomic<int> g_clusters[64];
@@ -414,8 +503,9 @@ static cudaError_t prepare_device(int* clusters) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (g_clusters[dev] == 0) {
-    const void* fn[3] = {(const void*)orth_kernel<kGram>, (const void*)orth_kernel<kPoly>,
-                         (const void*)orth_kernel<kApply>};
+    const void* fn[6] = {(const void*)orth_kernel<kGram, kOne>,  (const void*)orth_kernel<kGram, kTwo>,
+                         (const void*)orth_kernel<kPoly, kOne>,  (const void*)orth_kernel<kPoly, kTwo>,
+                         (const void*)orth_kernel<kApply, kLow>, (const void*)orth_kernel<kApply, kTwo>};
     int least = 1 << 30;
     for (const void* f : fn) {
       e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
@@ -441,9 +531,8 @@ static cudaError_t prepare_device(int* clusters) {
   return *clusters > 0 ? cudaSuccess : cudaErrorNotSupported;
 }
 
-template <int KIND>
-static cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorMap& mAdd, const CUtensorMap& mOut,
-                          const CUtensorMap& mT, const Args& t, cudaStream_t st) {
+template <int KIND, int FORM>
+static cudaError_t launch(const Maps& maps, const Args& t, cudaStream_t st) {
   int mc = 0;
   cudaError_t e = prepare_device(&mc);
   if (e != cudaSuccess) return e;
@@ -451,7 +540,7 @@ static cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const CU
   if (tiles <= 0) return cudaSuccess;
   if (tiles >= (1ll << 31)) return cudaErrorInvalidValue;
   const unsigned pairs = (unsigned)(tiles < mc ? tiles : mc);
-  return launch_after(orth_kernel<KIND>, 2 * pairs, THREADS, SMEM_BYTES, st, 2, mA, mB, mAdd, mOut, mT, t);
+  return launch_after(orth_kernel<KIND, FORM>, 2 * pairs, THREADS, SMEM_BYTES, st, 2, maps, t);
 }
 
 }  // namespace orth
@@ -459,16 +548,38 @@ static cudaError_t launch(const CUtensorMap& mA, const CUtensorMap& mB, const CU
 cudaError_t launch_orth_steps(const OrthBatch& t, int steps, const double (*coef)[3], cudaStream_t st) {
   using namespace orth;
   const int64_t B = t.batch, all = B * t.planes;
-  CUtensorMap xk[2], xmn[2], xio[2], ak, aio, at, bk, bio, bt;
-  for (int i = 0; i < 2; ++i)
-    if (!map3(&xk[i], t.x[i], 2 * B, t.m, t.n, t.ldx, 64, 128, true) ||
-        !map3(&xmn[i], t.x[i], 2 * B, t.m, t.n, t.ldx, 64, 64, true) ||
-        !map3(&xio[i], t.x[i], 2 * B, t.m, t.n, t.ldx, 64, 32, true))
-      return cudaErrorInvalidValue;
-  if (!map3(&ak, t.a, all, t.m, t.m, t.lda, 64, 128, true) || !map3(&aio, t.a, all, t.m, t.m, t.lda, 64, 32, true) ||
-      !map3(&at, t.a, all, t.m, t.m, t.lda, 32, 64, false) || !map3(&bk, t.b, all, t.m, t.m, t.lda, 64, 128, true) ||
-      !map3(&bio, t.b, all, t.m, t.m, t.lda, 64, 32, true) || !map3(&bt, t.b, all, t.m, t.m, t.lda, 32, 64, false))
+  const bool two = t.planes == 2;
+  // the three products' maps, those of X for either buffer as the source
+  Maps gram[2], poly, apply[2];
+  CUtensorMap ak, aio;
+  if (!map3(&ak, t.a, all, t.m, t.m, t.lda, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) || !map3(&aio, t.a, all, t.m, t.m, t.lda, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !map3(&gram[0].T, t.a, all, t.m, t.m, t.lda, 32, 64, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !map3(&apply[0].A, t.b, all, t.m, t.m, t.lda, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !map3(&poly.Out, t.b, all, t.m, t.m, t.lda, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !map3(&poly.T, t.b, all, t.m, t.m, t.lda, 32, 64, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
+  poly.A = poly.B = ak;
+  poly.Add = poly.AddLow = aio;
+  poly.OutLow = poly.Out;
+  for (int i = 0; i < 2; ++i) {
+    // planes of X: two of fp16, or one and the 8-bit parts behind it
+    const int64_t planes = (two ? 2 : 1) * B;
+    char* low = static_cast<char*>(t.x[i]) + B * t.m * (int64_t)t.ldx * 2;
+    if (!map3(&gram[i].A, t.x[i], planes, t.m, t.n, t.ldx, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !map3(&apply[i].B, t.x[i], planes, t.m, t.n, t.ldx, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !map3(&apply[i].Add, t.x[i], planes, t.m, t.n, t.ldx, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !map3(&apply[i].AddLow, low, B, t.m, t.n, t.ldx, 64, 32, CU_TENSOR_MAP_SWIZZLE_64B, 1))
+      return cudaErrorInvalidValue;
+    gram[i].B = gram[i].Add = gram[i].AddLow = gram[i].A;
+    gram[i].Out = gram[i].OutLow = aio;
+    gram[i].T = gram[0].T;
+    apply[i].A = apply[0].A;
+    apply[i].T = poly.T;
+  }
+  for (int i = 0; i < 2; ++i) {
+    apply[i].Out = apply[i ^ 1].Add;
+    apply[i].OutLow = apply[i ^ 1].AddLow;
+  }
   Args g = {};
   g.m = t.m;
   g.n = t.n;
@@ -482,23 +593,27 @@ cudaError_t launch_orth_steps(const OrthBatch& t, int steps, const double (*coef
     // A = X X^T
     g.kb = (t.n + BK - 1) / BK;
     g.per = g.mt * (g.mt + 1) / 2;
-    g.out_planes = t.planes;
     g.mul = ldexpf(1.0f, kOrthA - 2 * kOrthX);
-    cudaError_t e = launch<kGram>(xk[from], xk[from], xk[from], aio, at, g, st);
+    cudaError_t e = two ? launch<kGram, kTwo>(gram[from], g, st) : launch<kGram, kOne>(gram[from], g, st);
     if (e != cudaSuccess) return e;
     // B = b A + c A A, the polynomial in the planes that the product reads
     g.kb = (t.m + BK - 1) / BK;
-    g.add_planes = t.planes;
     g.add_scale = ldexpf((float)coef[i][1], kOrthB - kOrthA);
     g.mul = ldexpf((float)coef[i][2], kOrthB - 2 * kOrthA);
-    e = launch<kPoly>(ak, ak, aio, bio, bt, g, st);
+    g.add_ld = g.low_ld = (int64_t)t.lda * 2;
+    g.add = static_cast<const char*>(t.a);
+    g.add_low = g.add + B * t.m * g.add_ld;
+    e = two ? launch<kPoly, kTwo>(poly, g, st) : launch<kPoly, kOne>(poly, g, st);
     if (e != cudaSuccess) return e;
     // X' = a X + B X
     g.per = g.mt * g.nt;
-    g.out_planes = g.add_planes = 2;
     g.add_scale = (float)coef[i][0];
     g.mul = ldexpf(1.0f, -kOrthB);
-    e = launch<kApply>(bk, xmn[from], xio[from], xio[from ^ 1], xio[from ^ 1], g, st);
+    g.add_ld = (int64_t)t.ldx * 2;
+    g.low_ld = two ? g.add_ld : t.ldx;
+    g.add = static_cast<const char*>(t.x[from]);
+    g.add_low = g.add + B * t.m * g.add_ld;
+    e = two ? launch<kApply, kTwo>(apply[from], g, st) : launch<kApply, kLow>(apply[from], g, st);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -217,9 +217,11 @@ __device__ __forceinline__ void put8(const Round& r, int64_t at, const float* f)
     }
     *reinterpret_cast<uint4*>(r.x + plane + at) = make_uint4(l[0], l[1], l[2], l[3]);
   } else {
-    uint32_t l[2] = {0, 0};
+    uint32_t l[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) l[i / 4] |= (uint32_t)(orth_low_part(f[i], lead[i]) & 255) << (i % 4 * 8);
+    for (int i = 0; i < 2; ++i)
+      l[i] = orth_low_pack(orth_low_steps(f[4 * i], lead[4 * i]), orth_low_steps(f[4 * i + 1], lead[4 * i + 1]),
+                           orth_low_steps(f[4 * i + 2], lead[4 * i + 2]), orth_low_steps(f[4 * i + 3], lead[4 * i + 3]));
     *reinterpret_cast<uint2*>(reinterpret_cast<char*>(r.x + plane) + at) = make_uint2(l[0], l[1]);
   }
 }
@@ -422,10 +424,8 @@ Bucket bucket_of(int m, int n, int planes, int64_t batch) {
   b.n = n;
   b.planes = planes;
   b.batch = batch;
-  // rows on 128-byte boundaries where they are long enough for it
-  auto pad = [](int v) { return v >= 64 ? (v + 63) / 64 * 64 : (v + 15) / 16 * 16; };
-  b.ldx = pad(n);
-  b.lda = pad(m);
+  b.ldx = (n + 127) / 128 * 128;
+  b.lda = (m + 63) / 64 * 64;
   b.parts = (int)(((int64_t)m * n + kPart - 1) / kPart);
   b.each = 2 * x_bytes(b) + 2ll * planes * m * b.lda * 2 + 8ll * b.parts;
   b.round = std::max<int64_t>(1, std::min<int64_t>(batch, std::min<int64_t>(kMaxRound, kScratch / b.each)));

@@ -15,7 +15,8 @@ constexpr int kOrthX = 13, kOrthA = 11, kOrthB = 9;
 constexpr double kOrthMaxX = 3.5, kOrthMaxB = 100.0;
 
 // A batch in scratch.  x[0], x[1]: [planes][batch][m][ldx] each, with one plane the 8-bit
-// parts [batch][m][ldx] behind it; a, b: [planes][batch][m][lda]; ldx and lda multiples of 16.
+// parts [batch][m][ldx] behind it; a, b: [planes][batch][m][lda]; ldx a multiple of 128, lda of
+// 64 (columns past m and n, up to there, are written, and read only into themselves).
 struct OrthBatch {
   int64_t batch;
   int m, n, ldx, lda;
@@ -33,13 +34,22 @@ struct OrthBatch {
 // last bit, through float-integer conversions at a quarter of it, the epilogue took longer
 // than the products.  Below fp16's normal range the part stops at its limit, closer to f
 // than h alone.
-__device__ __forceinline__ int orth_low_part(float f, float h) {
-  const int d = __float_as_int(f) - __float_as_int(h);
-  return (d < -4096 ? -4096 : (d > 4095 ? 4095 : d)) >> 5;
+__device__ __forceinline__ int orth_low_steps(float f, float h) {
+  return (__float_as_int(f) - __float_as_int(h) + 16) >> 5;
+}
+// Four parts, each at its limit where it passes 8 bits, in one word, the first lowest.
+__device__ __forceinline__ uint32_t orth_low_pack(int a, int b, int c, int d) {
+  uint32_t r;
+  asm("{\n\t.reg .b32 t;\n\t"
+      "cvt.pack.sat.s8.s32.b32 t, %4, %3, 0;\n\t"
+      "cvt.pack.sat.s8.s32.b32 %0, %2, %1, t;\n\t}\n"
+      : "=r"(r)
+      : "r"(a), "r"(b), "r"(c), "r"(d));
+  return r;
 }
 // low: sign-extended
 __device__ __forceinline__ float orth_with_low(float h, int low) {
-  return __int_as_float(__float_as_int(h) + low * 32 + 16);
+  return __int_as_float(__float_as_int(h) + low * 32);
 }
 #endif
 

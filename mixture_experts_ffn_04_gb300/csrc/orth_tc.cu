@@ -16,17 +16,21 @@
 // the same plane as A A: with b A exact instead 2.8e-3).  fp32 matrices take three
 // products of two planes each, smallest first: 5.7e-7 (fp32 products: 7.2e-6).
 //
-// A pair of SMs computes 256 x 256 tiles over 64-wide k-blocks through four 32 KB
-// stages.  The sums of a tile leave TMEM in chunks of k-blocks (the tensor cores cut
-// the accumulator off at each K = 16 step) into fp32 registers, which start from the
-// addend a X or b A, read while the tile's products run.
+// A pair of SMs computes 256 x 256 tiles over 64-wide k-blocks through six 32 KB
+// stages.  Addend and result go between registers and memory as whole 128-byte rows, turned
+// in a 4 KB slice of each epilogue warp between that layout and the one of TMEM (a lane a
+// row), the addend asked for a tile ahead.  By TMA boxes both stood in the TMA queue behind
+// the operands of more than a tile: at m = 704, whose tiles have 11 k-blocks, 2800 of a
+// tile's 14000 clocks went by waiting for the addend, 2000 issuing the result; by the
+// lane that owns the row, 32 bytes at a time, each instruction took 32 lines (340 us for 96
+// matrices 704 x 2816 against 312).
 //
 // Roles in each CTA: warp 0 TMA producer, warp 1 TMEM and (even CTA) the MMA
-// issuer, warps 4-19 epilogue, four a 32-lane TMEM quarter (with two, whose 128 columns a
-// thread had two warps a scheduler to hide behind, a 256 x 256 tile of kApply took
-// 8.3 us, three times its products).  Tiles are dealt out in a
-// fixed order (all have the same K).  Every wait on an mbarrier is bounded, and a CTA
-// that gives up waits, with a limit, for its copies and MMAs in flight.
+// issuer, warps 4-11 epilogue, two a 32-lane TMEM quarter.  Tiles are dealt out in a
+// fixed order (all have the same K).  The sums of fp32 matrices leave TMEM in chunks of
+// k-blocks, added in fp32 registers (the tensor cores cut the accumulator off at each K = 16
+// step); with operands of 11 bits it would not show.  Every wait on an mbarrier is bounded,
+// and a CTA that gives up waits, with a limit, for its copies and MMAs in flight.
 #include <atomic>
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -48,26 +52,24 @@ namespace orth {
 using namespace tc;
 
 constexpr int BM = 256, BN = 256, BMC = BM / 2, BNC = BN / 2, BK = 64;
-constexpr int S = 4;
+constexpr int S = 6;
 constexpr int A_BYTES = BMC * BK * 2, B_BYTES = BNC * BK * 2;
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int BOX_BYTES = 64 * BK * 2;
 constexpr int RING_BYTES = S * STAGE_BYTES;
-constexpr int EPI_WARPS = 16, EPI_COLS = 64;   // a warp: 32 rows, 64 columns
+constexpr int EPI_WARPS = 8, EPI_COLS = 128;   // a warp: 32 rows, 128 columns
 constexpr int THREADS = 32 * (4 + EPI_WARPS);
-// 96 registers a thread at launch; 56 + 4 * 104 <= 5 * 96 (five groups of 4 warps)
-constexpr int ROLE_REGS = 56, EPI_REGS = 104;
-static_assert(ROLE_REGS + 4 * EPI_REGS <= 5 * 96, "register pool of the launch");
+// 168 registers a thread at launch; 56 + 2 * 224 <= 3 * 168 (three groups of 4 warps)
+constexpr int ROLE_REGS = 56, EPI_REGS = 224;
+static_assert(ROLE_REGS + 2 * EPI_REGS <= 3 * 168, "register pool of the launch");
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int BAR_BYTES = 512;
-// staging of an epilogue warp: 32 rows of 64 fp16 values (128-byte swizzle), and of 64
-// 8-bit parts (64-byte swizzle)
-constexpr int HALF_BYTES = 4096, LOW_BYTES = 2048, STAGE_WARP = HALF_BYTES + LOW_BYTES;
+constexpr int BAR_BYTES = 256;
+constexpr int STAGE_WARP = 4096;   // an epilogue warp's slice: 32 rows of 128 bytes
 constexpr int SMEM_BYTES = 1024 + RING_BYTES + EPI_WARPS * STAGE_WARP + BAR_BYTES;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget of one CTA");
-static_assert((2 * S + 5 + 2 * EPI_WARPS) * 8 + 8 <= BAR_BYTES, "barrier area");
+static_assert((2 * S + 5) * 8 + 8 <= BAR_BYTES, "barrier area");
 constexpr long long kDrainCycles = 1 << 21;
-constexpr int kChunkExact = 8, kChunkHalf = 64;   // k-blocks: two planes, one plane
+constexpr int kChunkExact = 8;   // k-blocks of 64
 
 // kind::f16: D fp32, A and B fp16, M = 256 over the pair, N = 256.
 constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
@@ -81,9 +83,11 @@ struct Args {
   int kb;                 // k-blocks
   int mt, nt, per;        // row tiles, column tiles, tiles a matrix
   float add_scale, mul;   // result = add_scale * addend + mul * product
-  const char* add;        // the addend's leading plane, rows ld bytes apart: for the L2
-  const char* add_low;    // its second plane, or 8-bit parts
-  int64_t add_ld, low_ld;
+  const char* add;        // the addend's leading plane, rows add_ld bytes apart
+  const char* add_low;    // its second plane, or its 8-bit parts
+  char* out;              // the result, the same
+  char* out_low;
+  int64_t add_ld, low_ld; // of the addend and the result, bytes
   uint32_t* flags;
 };
 
@@ -113,41 +117,82 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   const __half2 p = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&p);
 }
-__device__ __forceinline__ void add_halves(float* f, uint4 v, float scale) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// 32 rows of 128 bytes, ld bytes apart, as a warp moves them: lane l has 16 bytes l % 8
+// of rows l / 8, + 4, .. + 28; rows from `rows` on are not there.
+struct Block {
+  uint4 v[8];
+};
+__device__ __forceinline__ void load_block(Block& b, const char* p, int64_t ld, int rows, int lane) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-    f[2 * i] = fmaf(scale, h.x, f[2 * i]);
-    f[2 * i + 1] = fmaf(scale, h.y, f[2 * i + 1]);
+  for (int i = 0; i < 8; ++i) {
+    const int r = 4 * i + (lane >> 3);
+    b.v[i] = r < rows ? *reinterpret_cast<const uint4*>(p + r * ld + (lane & 7) * 16) : make_uint4(0, 0, 0, 0);
   }
 }
-__device__ __forceinline__ void box_out(const CUtensorMap* map, uint32_t stage, int lane, int col, int row, int z) {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  __syncwarp();
-  if (lane == 0) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(col), "r"(row), "r"(z), "r"(stage)
+// The block to and from a slice (put_piece's layout: piece j of row r at j ^ (r & 7)).
+__device__ __forceinline__ uint32_t block_at(uint32_t stage, int lane, int i) {
+  const int r = 4 * i + (lane >> 3);
+  return stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
+}
+__device__ __forceinline__ void block_to_slice(const Block& b, uint32_t stage, int lane) {
+  __syncwarp();   // what the slice held has been read
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(block_at(stage, lane, i)), "r"(b.v[i].x), "r"(b.v[i].y),
+                 "r"(b.v[i].z), "r"(b.v[i].w)
                  : "memory");
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-  }
+  __syncwarp();
 }
-
-__device__ __forceinline__ void prefetch_l2(const void* p) {
-  asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
+__device__ __forceinline__ uint4 load_piece(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void slice_to_rows(uint32_t stage, char* p, int64_t ld, int rows, int lane) {
+  __syncwarp();   // every lane's pieces are in the slice
+  Block b;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b.v[i] = load_piece(block_at(stage, lane, i));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = 4 * i + (lane >> 3);
+    if (r < rows) *reinterpret_cast<uint4*>(p + r * ld + (lane & 7) * 16) = b.v[i];
+  }
+  __syncwarp();
+}
+// The transposed image of 64 columns: value j of this lane's row goes to row j of 64 bytes
+// (w: pairs of columns), then rows `cols` of them at p, whole (their ends may be padding).
+__device__ __forceinline__ void mirror_rows(uint32_t stage, const uint32_t (&w)[32], char* p, int64_t ld, int cols,
+                                            int lane) {
+  __syncwarp();   // what the slice held has been read
+#pragma unroll
+  for (int j = 0; j < 64; ++j)
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(stage + j * 64 + lane * 2),
+                 "h"((unsigned short)(w[j / 2] >> (j % 2 * 16)))
+                 : "memory");
+  __syncwarp();
+  Block b;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b.v[i] = load_piece(stage + (8 * i + (lane >> 2)) * 64 + (lane & 3) * 16);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = 8 * i + (lane >> 2);
+    if (r < cols) *reinterpret_cast<uint4*>(p + r * ld + (lane & 3) * 16) = b.v[i];
+  }
+  __syncwarp();
 }
 
 // How X' and the addend are held: kOne: one fp16 plane (A, B); kTwo: two; kLow: one
 // and the 8-bit part (X of bf16 matrices).
 enum Form { kOne = 0, kTwo = 1, kLow = 2 };
 
-// Maps are 3-D, {columns, rows, plane * batch + matrix}.  mA, mB: operand boxes
-// (128 x 64; kApply's B operand 64 x 64 in its stored layout); mAdd, mOut: 32 rows of
-// 64 columns; mAddLow, mOutLow: 32 rows of 64 8-bit parts; mT: 64 rows of 32 columns, for the
-// transposed tile.
+// Operand maps are 3-D, {columns, rows, plane * batch + matrix}: boxes of 64 columns by
+// 128 rows, kApply's B operand 64 by 64 in its stored layout.
 struct Maps {
-  CUtensorMap A, B, Add, AddLow, Out, OutLow, T;
+  CUtensorMap A, B;
 };
 
 template <int KIND, int FORM>
@@ -157,8 +202,8 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   unsigned char* s_out = smem + RING_BYTES;
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_out + EPI_WARPS * STAGE_WARP);
-  // bars: full[S] empty[S] tfull[2] tempty[2] final addend[2 * EPI_WARPS]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5 + 2 * EPI_WARPS);
+  // bars: full[S] empty[S] tfull[2] tempty[2] final
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   pdl_trigger();
@@ -171,7 +216,6 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
   auto tfull = [&](int b) { return smem_u32(&bars[2 * S + b]); };
   auto tempty = [&](int b) { return smem_u32(&bars[2 * S + 2 + b]); };
   const uint32_t final_bar = smem_u32(&bars[2 * S + 4]);
-  auto addend = [&](int w) { return smem_u32(&bars[2 * S + 5 + w]); };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -183,7 +227,6 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
       mbar_init(tempty(b), 2 * EPI_WARPS);
     }
     mbar_init(final_bar, 1);
-    for (int w = 0; w < 2 * EPI_WARPS; ++w) mbar_init(addend(w), 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -202,8 +245,8 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
   pdl_wait();
   const uint32_t total = (uint32_t)a.per * (uint32_t)a.batch, first = blockIdx.x >> 1, step = gridDim.x >> 1;
   const int nprod = a.planes == 2 ? 3 : 1;
-  const int chunk = a.planes == 2 ? kChunkExact : kChunkHalf;
   const int steps = a.kb * nprod;   // k-blocks of a tile
+  const int chunk = FORM == kTwo ? kChunkExact : steps;
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(ROLE_REGS));
@@ -287,181 +330,227 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
     const int q = warp & 3;                 // TMEM lanes 32q .. 32q+31
     const int c_lo = (warp - 4) / 4 * EPI_COLS;
-    const uint32_t half = smem_u32(s_out + (warp - 4) * STAGE_WARP), lows = half + HALF_BYTES;
-    const uint32_t half_bar = addend(2 * (warp - 4)), low_bar = addend(2 * (warp - 4) + 1);
+    const uint32_t stage = smem_u32(s_out + (warp - 4) * STAGE_WARP);
     const int width = KIND == kApply ? a.n : a.m;
     int acc = 0;
-    uint32_t aph = 0, half_ph = 0, low_ph = 0;
+    uint32_t aph = 0;
     bool ok = true;
-    // lane 0 waits for a box, the others' reads come after it
-    auto landed = [&](uint32_t bar, uint32_t& ph) {
+    auto wait_acc = [&]() {
       int w = 1;
-      if (lane == 0) {
-        w = wait_cl(bar, ph, abort_flag) ? 1 : 0;
-        // given up (perhaps for another warp's wait): the box still lands first
-        if (!w) wait2_quiet(bar, ph);
-      }
-      ph ^= 1u;
-      ok = __shfl_sync(0xffffffffu, w, 0) && ok;
-      __syncwarp();   // (the exchange alone orders no memory)
+      if (lane == 0) w = wait_cl(tfull(acc), aph, abort_flag) ? 1 : 0;
+      ok = __shfl_sync(0xffffffffu, w, 0);
+      if (ok) tc_fence_after();
+      return ok;
     };
-    auto ask = [&](uint32_t to, const CUtensorMap* map, int col, int row, int z, uint32_t bar, uint32_t bytes) {
-      if (lane != 0) return;
-      mbar_expect_tx(bar, bytes);
-      tma_load_3d(to, map, col, row, z, bar);
+    auto free_acc = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_relaxed(map_to_rank(tempty(acc), 0));
+      acc ^= 1;
+      if (acc == 0) aph ^= 1u;
     };
-    // 16 bytes j of this lane's 64-byte row of 8-bit parts
-    auto low_at = [&](int j) { return lows + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4); };
-    for (uint32_t t = first; ok && t < total; t += step) {
-      const Tile d = decode<KIND>(a, t);
-      const int row0 = d.i * BM + (int)rank * BMC + q * 32, n0 = d.j * BN + c_lo;
-      const bool live = row0 < a.m && n0 < width;
-      float f[EPI_COLS];
-#pragma unroll
-      for (int j = 0; j < EPI_COLS; ++j) f[j] = 0.0f;
-      if (KIND != kGram && live) {
-        // start from the addend
-        stage_free(lane);
-        ask(half, &maps.Add, n0, row0, d.b, half_bar, HALF_BYTES);
-        if (FORM == kLow) {
-          ask(lows, &maps.AddLow, n0, row0, d.b, low_bar, LOW_BYTES);
-          landed(half_bar, half_ph);
-          landed(low_bar, low_ph);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint4 l;
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(l.x), "=r"(l.y), "=r"(l.z), "=r"(l.w)
-                         : "r"(low_at(j))
-                         : "memory");
-            const uint32_t low[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint4 v = get_piece(half, lane, 2 * j + h);
-              const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w4[e]));
-                const int at = 8 * h + 2 * e;    // of the 16 parts
-                const uint32_t q2 = low[at / 4] >> (at % 4 * 8);
-                f[16 * j + at] = a.add_scale * orth_with_low(x.x, (int)(int8_t)(q2 & 255u));
-                f[16 * j + at + 1] = a.add_scale * orth_with_low(x.y, (int)(int8_t)((q2 >> 8) & 255u));
-              }
-            }
-          }
-        } else {
-          landed(half_bar, half_ph);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) add_halves(f + 8 * j, get_piece(half, lane, j), a.add_scale);
-          if (FORM == kTwo) {
-            __syncwarp();
-            ask(half, &maps.Add, n0, row0, a.batch + d.b, half_bar, HALF_BYTES);
-            landed(half_bar, half_ph);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) add_halves(f + 8 * j, get_piece(half, lane, j), a.add_scale);
-          }
-        }
-        __syncwarp();
-        // the next tile's addend to the L2 while this one is worked on
+    auto tmem_at = [&]() { return tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)acc * BN + c_lo; };
+    // a tile's part of this warp: its first row (of all matrices' rows) and column, and how
+    // many rows there are; columns past the width go to the rows' padding
+    struct Part {
+      int64_t row;
+      int n0, rows, r0;
+    };
+    auto part_of = [&](const Tile& d) {
+      Part p;
+      p.r0 = d.i * BM + (int)rank * BMC + q * 32;
+      p.row = (int64_t)d.b * a.m + p.r0;
+      p.n0 = d.j * BN + c_lo;
+      p.rows = p.n0 < width ? min(32, a.m - p.r0) : 0;
+      return p;
+    };
+    // the mirror image of 64 columns from `col`
+    auto mirror = [&](char* out, const Tile& d, const Part& p, int col, const uint32_t (&w)[32]) {
+      mirror_rows(stage, w, out + ((int64_t)d.b * a.m + col) * a.add_ld + 2 * p.r0, a.add_ld, a.m - col, lane);
+    };
+    if constexpr (FORM != kTwo) {
+      // One sum a tile, 16 columns at a time from TMEM through the slice.  A block of the
+      // addend is asked for as soon as the tile before has put its own into the slice.
+      Block hi[2], lo;
+      auto ask_hi = [&](const Part& p, int h) {
+        if (KIND != kGram)
+          load_block(hi[h], a.add + p.row * a.add_ld + 2 * (p.n0 + 64 * h), a.add_ld, p.n0 + 64 * h < width ? p.rows : 0,
+                     lane);
+      };
+      auto ask_lo = [&](const Part& p) {
+        if (FORM == kLow) load_block(lo, a.add_low + p.row * a.low_ld + p.n0, a.low_ld, p.rows, lane);
+      };
+      Tile d = decode<KIND>(a, first), dn = d;
+      Part p = part_of(d), pn = p;
+      ask_lo(p);
+      ask_hi(p, 0);
+      ask_hi(p, 1);
+      for (uint32_t t = first; t < total; t += step, d = dn, p = pn) {
         if (t + step < total) {
-          const Tile e = decode<KIND>(a, t + step);
-          const int row = e.i * BM + (int)rank * BMC + q * 32 + lane, col = e.j * BN + c_lo;
-          if (row < a.m && col < width) {
-            prefetch_l2(a.add + ((int64_t)e.b * a.m + row) * a.add_ld + 2 * col);
-            if (FORM != kOne)
-              prefetch_l2(a.add_low + ((int64_t)e.b * a.m + row) * a.low_ld + (FORM == kTwo ? 2 : 1) * col);
-          }
-        }
-      }
-      if (!ok) break;
-#pragma unroll 1
-      for (int i0 = 0; i0 < steps; i0 += chunk) {
-        int w = 1;
-        if (lane == 0) w = wait_cl(tfull(acc), aph, abort_flag) ? 1 : 0;
-        ok = __shfl_sync(0xffffffffu, w, 0);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)acc * BN + c_lo;
-#pragma unroll
-        for (int c = 0; c < EPI_COLS; c += 16) {
-          uint32_t r[16];
-          tmem_ld16(taddr + c, r);
-          tmem_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 16; ++j) f[c + j] = fmaf(a.mul, __uint_as_float(r[j]), f[c + j]);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_relaxed(map_to_rank(tempty(acc), 0));
-        acc ^= 1;
-        if (acc == 0) aph ^= 1u;
-      }
-      if (!ok) break;
-      if (!live) continue;
-      const bool mirror = KIND != kApply && d.i != d.j;
-#pragma unroll
-      for (int p = 0; p < (FORM == kTwo ? 2 : 1); ++p) {
-        const int z = p * a.batch + d.b;
-        stage_free(lane);
-        if (FORM == kLow) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t l[4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t w4[4];
-              int low[8];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float* v = f + 16 * j + 8 * h + 2 * e;
-                w4[e] = pack_half2(v[0], v[1]);
-                const float2 lead = __half22float2(*reinterpret_cast<const __half2*>(&w4[e]));
-                low[2 * e] = orth_low_part(v[0], lead.x);
-                low[2 * e + 1] = orth_low_part(v[1], lead.y);
-              }
-              put_piece(half, lane, 2 * j + h, make_uint4(w4[0], w4[1], w4[2], w4[3]));
-              // the low bytes of four words
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                l[2 * h + e] = __byte_perm(__byte_perm(low[4 * e], low[4 * e + 1], 0x0040),
-                                           __byte_perm(low[4 * e + 2], low[4 * e + 3], 0x0040), 0x5410);
-            }
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(low_at(j)), "r"(l[0]), "r"(l[1]), "r"(l[2]),
-                         "r"(l[3])
-                         : "memory");
-          }
-          box_out(&maps.OutLow, lows, lane, n0, row0, z);
+          dn = decode<KIND>(a, t + step);
+          pn = part_of(dn);
         } else {
+          pn.rows = 0;     // nothing more to ask for
+        }
+        uint32_t low[FORM == kLow ? 32 : 1];     // this lane's 128 8-bit parts
+        if (FORM == kLow) {
+          block_to_slice(lo, stage, lane);
+          ask_lo(pn);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float* v = f + 8 * j;
-            put_piece(half, lane, j, make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]), pack_half2(v[4], v[5]),
-                                                pack_half2(v[6], v[7])));
+            const uint4 v = get_piece(stage, lane, j);
+            low[4 * j] = v.x;
+            low[4 * j + 1] = v.y;
+            low[4 * j + 2] = v.z;
+            low[4 * j + 3] = v.w;
           }
         }
-        box_out(&maps.Out, half, lane, n0, row0, z);
-        if (mirror) {
-          // the transposed box: 64 rows (this warp's columns) of 32 values
-          stage_free(lane);
+        if (!wait_acc()) break;
+        const uint32_t taddr = tmem_at();
+        uint32_t r[2][16];
+        tmem_ld16(taddr, r[0]);
 #pragma unroll
-          for (int j = 0; j < EPI_COLS; ++j) {
-            const __half h = __float2half_rn(f[j]);
-            asm volatile("st.shared.u16 [%0], %1;" ::"r"(half + j * 64 + lane * 2),
-                         "h"(*reinterpret_cast<const unsigned short*>(&h))
-                         : "memory");
+        for (int h = 0; h < 2; ++h) {
+          if (KIND != kGram) {
+            block_to_slice(hi[h], stage, lane);
+            ask_hi(pn, h);
           }
-          box_out(&maps.T, half, lane, row0, n0, z);
-        }
-        if (FORM == kTwo && p == 0) {
-          // what the leading plane leaves
+          uint32_t w[32];      // 64 columns, packed
 #pragma unroll
-          for (int j = 0; j < EPI_COLS; ++j) f[j] -= __half2float(__float2half_rn(f[j]));
+          for (int c = 0; c < 4; ++c) {
+            const int k = 4 * h + c;
+            tmem_wait_ld();
+            if (k < 7) tmem_ld16(taddr + 16 * (k + 1), r[(k + 1) & 1]);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {       // 8 columns: a piece
+              int steps8[8];
+              uint4 add = make_uint4(0, 0, 0, 0);
+              if (KIND != kGram) add = get_piece(stage, lane, 2 * c + g);
+              const uint32_t h4[4] = {add.x, add.y, add.z, add.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float f0 = a.mul * __uint_as_float(r[k & 1][8 * g + 2 * e]);
+                float f1 = a.mul * __uint_as_float(r[k & 1][8 * g + 2 * e + 1]);
+                if (KIND != kGram) {
+                  float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h4[e]));
+                  if (FORM == kLow) {
+                    const uint32_t q2 = low[16 * h + 4 * c + 2 * g + e / 2] >> (e % 2 * 16);
+                    x.x = orth_with_low(x.x, (int)(int8_t)(q2 & 255u));
+                    x.y = orth_with_low(x.y, (int)(int8_t)((q2 >> 8) & 255u));
+                  }
+                  f0 = fmaf(a.add_scale, x.x, f0);
+                  f1 = fmaf(a.add_scale, x.y, f1);
+                }
+                const uint32_t v = pack_half2(f0, f1);
+                w[8 * c + 4 * g + e] = v;
+                if (FORM == kLow) {
+                  const float2 lead = __half22float2(*reinterpret_cast<const __half2*>(&v));
+                  steps8[2 * e] = orth_low_steps(f0, lead.x);
+                  steps8[2 * e + 1] = orth_low_steps(f1, lead.y);
+                }
+              }
+              const uint32_t* v = w + 8 * c + 4 * g;
+              put_piece(stage, lane, 2 * c + g, make_uint4(v[0], v[1], v[2], v[3]));
+              if (FORM == kLow) {
+                // the parts replace the addend's
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  low[16 * h + 4 * c + 2 * g + e] =
+                      orth_low_pack(steps8[4 * e], steps8[4 * e + 1], steps8[4 * e + 2], steps8[4 * e + 3]);
+              }
+            }
+          }
+          if (h == 1) free_acc();
+          const int col = p.n0 + 64 * h, rows = col < width ? p.rows : 0;
+          slice_to_rows(stage, a.out + p.row * a.add_ld + 2 * col, a.add_ld, rows, lane);
+          if (KIND != kApply && d.i != d.j && rows > 0) mirror(a.out, d, p, col, w);
+        }
+        if (FORM == kLow) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            put_piece(stage, lane, j, make_uint4(low[4 * j], low[4 * j + 1], low[4 * j + 2], low[4 * j + 3]));
+          slice_to_rows(stage, a.out_low + p.row * a.low_ld + p.n0, a.low_ld, p.rows, lane);
+        }
+      }
+    } else {
+      for (uint32_t t = first; ok && t < total; t += step) {
+        const Tile d = decode<KIND>(a, t);
+        const Part p = part_of(d);
+        float f[EPI_COLS];
+#pragma unroll
+        for (int j = 0; j < EPI_COLS; ++j) f[j] = 0.0f;
+        if (KIND != kGram && p.rows > 0) {
+          // start from the addend's two planes
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int rows = p.n0 + 64 * h < width ? p.rows : 0;
+            Block b[2];
+            load_block(b[0], a.add + p.row * a.add_ld + 2 * (p.n0 + 64 * h), a.add_ld, rows, lane);
+            load_block(b[1], a.add_low + p.row * a.add_ld + 2 * (p.n0 + 64 * h), a.add_ld, rows, lane);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              block_to_slice(b[k], stage, lane);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const uint4 v = get_piece(stage, lane, j);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+                  float* g = f + 64 * h + 8 * j + 2 * e;
+                  g[0] = fmaf(a.add_scale, x.x, g[0]);
+                  g[1] = fmaf(a.add_scale, x.y, g[1]);
+                }
+              }
+            }
+          }
+        }
+#pragma unroll 1
+        for (int i0 = 0; i0 < steps; i0 += chunk) {
+          if (!wait_acc()) break;
+          const uint32_t taddr = tmem_at();
+#pragma unroll
+          for (int c = 0; c < EPI_COLS; c += 32) {
+            uint32_t r[32];
+            tmem_ld32(taddr + c, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) f[c + j] = fmaf(a.mul, __uint_as_float(r[j]), f[c + j]);
+          }
+          free_acc();
+        }
+        if (!ok) break;
+        if (p.rows <= 0) continue;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int col = p.n0 + 64 * h;
+          if (col >= width) continue;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            char* out = k == 0 ? a.out : a.out_low;
+            uint32_t w[32];
+            __syncwarp();   // what the slice held has been read
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float* g = f + 64 * h + 8 * j + 2 * e;
+                w[4 * j + e] = pack_half2(g[0], g[1]);
+                if (k == 0) {
+                  // what the leading plane leaves
+                  const float2 lead = __half22float2(*reinterpret_cast<const __half2*>(&w[4 * j + e]));
+                  g[0] -= lead.x;
+                  g[1] -= lead.y;
+                }
+              }
+              put_piece(stage, lane, j, make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
+            }
+            slice_to_rows(stage, out + p.row * a.add_ld + 2 * col, a.add_ld, p.rows, lane);
+            if (KIND != kApply && d.i != d.j) mirror(out, d, p, col, w);
+          }
         }
       }
     }
-    // the staging slices and what left them outlive the block's last tile
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-    __syncwarp();
   }
 
   __syncwarp();     // the barriers below are for whole warps: roles end lane by lane
@@ -480,17 +569,16 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
 // host side
 // ---------------------------------------------------------------------------
 
-// `count` matrices [rows, cols] of fp16 (or bytes), rows ld elements apart.
-static bool map3(CUtensorMap* m, const void* ptr, int64_t count, int rows, int cols, int ld, int box_cols, int box_rows,
-                 CUtensorMapSwizzle swizzle, int esize = 2) {
+// `count` matrices [rows, cols] of fp16, rows ld elements apart; 128-byte swizzle.
+static bool map3(CUtensorMap* m, const void* ptr, int64_t count, int rows, int cols, int ld, int box_cols, int box_rows) {
   cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)count};
-  cuuint64_t strides[2] = {(cuuint64_t)ld * esize, (cuuint64_t)ld * esize * (cuuint64_t)rows};
+  cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * 2 * (cuuint64_t)rows};
   cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
   cuuint32_t es[3] = {1, 1, 1};
   return encode_fn() != nullptr &&
-         encode_fn()(m, esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
-                     const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+         encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, es,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 static std::atomic<int> g_clusters[64];
@@ -551,34 +639,18 @@ cudaError_t launch_orth_steps(const OrthBatch& t, int steps, const double (*coef
   const bool two = t.planes == 2;
   // the three products' maps, those of X for either buffer as the source
   Maps gram[2], poly, apply[2];
-  CUtensorMap ak, aio;
-  if (!map3(&ak, t.a, all, t.m, t.m, t.lda, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) || !map3(&aio, t.a, all, t.m, t.m, t.lda, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !map3(&gram[0].T, t.a, all, t.m, t.m, t.lda, 32, 64, CU_TENSOR_MAP_SWIZZLE_NONE) ||
-      !map3(&apply[0].A, t.b, all, t.m, t.m, t.lda, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !map3(&poly.Out, t.b, all, t.m, t.m, t.lda, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !map3(&poly.T, t.b, all, t.m, t.m, t.lda, 32, 64, CU_TENSOR_MAP_SWIZZLE_NONE))
+  CUtensorMap bk;
+  if (!map3(&poly.A, t.a, all, t.m, t.m, t.lda, 64, 128) || !map3(&bk, t.b, all, t.m, t.m, t.lda, 64, 128))
     return cudaErrorInvalidValue;
-  poly.A = poly.B = ak;
-  poly.Add = poly.AddLow = aio;
-  poly.OutLow = poly.Out;
+  poly.B = poly.A;
   for (int i = 0; i < 2; ++i) {
-    // planes of X: two of fp16, or one and the 8-bit parts behind it
+    // planes of X: two of fp16, or one with the 8-bit parts behind it
     const int64_t planes = (two ? 2 : 1) * B;
-    char* low = static_cast<char*>(t.x[i]) + B * t.m * (int64_t)t.ldx * 2;
-    if (!map3(&gram[i].A, t.x[i], planes, t.m, t.n, t.ldx, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !map3(&apply[i].B, t.x[i], planes, t.m, t.n, t.ldx, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !map3(&apply[i].Add, t.x[i], planes, t.m, t.n, t.ldx, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !map3(&apply[i].AddLow, low, B, t.m, t.n, t.ldx, 64, 32, CU_TENSOR_MAP_SWIZZLE_64B, 1))
+    if (!map3(&gram[i].A, t.x[i], planes, t.m, t.n, t.ldx, 64, 128) ||
+        !map3(&apply[i].B, t.x[i], planes, t.m, t.n, t.ldx, 64, 64))
       return cudaErrorInvalidValue;
-    gram[i].B = gram[i].Add = gram[i].AddLow = gram[i].A;
-    gram[i].Out = gram[i].OutLow = aio;
-    gram[i].T = gram[0].T;
-    apply[i].A = apply[0].A;
-    apply[i].T = poly.T;
-  }
-  for (int i = 0; i < 2; ++i) {
-    apply[i].Out = apply[i ^ 1].Add;
-    apply[i].OutLow = apply[i ^ 1].AddLow;
+    gram[i].B = gram[i].A;
+    apply[i].A = bk;
   }
   Args g = {};
   g.m = t.m;
@@ -588,32 +660,40 @@ cudaError_t launch_orth_steps(const OrthBatch& t, int steps, const double (*coef
   g.flags = t.flags;
   g.mt = (t.m + BM - 1) / BM;
   g.nt = (t.n + BN - 1) / BN;
+  const int64_t rows = B * t.m, a_ld = (int64_t)t.lda * 2, x_ld = (int64_t)t.ldx * 2;
+  char *pa = static_cast<char*>(t.a), *pb = static_cast<char*>(t.b);
   for (int i = 0; i < steps; ++i) {
-    const int from = i & 1;
+    char *from = static_cast<char*>(t.x[i & 1]), *to = static_cast<char*>(t.x[(i & 1) ^ 1]);
     // A = X X^T
     g.kb = (t.n + BK - 1) / BK;
     g.per = g.mt * (g.mt + 1) / 2;
     g.mul = ldexpf(1.0f, kOrthA - 2 * kOrthX);
-    cudaError_t e = two ? launch<kGram, kTwo>(gram[from], g, st) : launch<kGram, kOne>(gram[from], g, st);
+    g.add_ld = g.low_ld = a_ld;
+    g.out = pa;
+    g.out_low = pa + rows * a_ld;
+    cudaError_t e = two ? launch<kGram, kTwo>(gram[i & 1], g, st) : launch<kGram, kOne>(gram[i & 1], g, st);
     if (e != cudaSuccess) return e;
     // B = b A + c A A, the polynomial in the planes that the product reads
     g.kb = (t.m + BK - 1) / BK;
     g.add_scale = ldexpf((float)coef[i][1], kOrthB - kOrthA);
     g.mul = ldexpf((float)coef[i][2], kOrthB - 2 * kOrthA);
-    g.add_ld = g.low_ld = (int64_t)t.lda * 2;
-    g.add = static_cast<const char*>(t.a);
-    g.add_low = g.add + B * t.m * g.add_ld;
+    g.add = pa;
+    g.add_low = pa + rows * a_ld;
+    g.out = pb;
+    g.out_low = pb + rows * a_ld;
     e = two ? launch<kPoly, kTwo>(poly, g, st) : launch<kPoly, kOne>(poly, g, st);
     if (e != cudaSuccess) return e;
     // X' = a X + B X
     g.per = g.mt * g.nt;
     g.add_scale = (float)coef[i][0];
     g.mul = ldexpf(1.0f, -kOrthB);
-    g.add_ld = (int64_t)t.ldx * 2;
-    g.low_ld = two ? g.add_ld : t.ldx;
-    g.add = static_cast<const char*>(t.x[from]);
-    g.add_low = g.add + B * t.m * g.add_ld;
-    e = two ? launch<kApply, kTwo>(apply[from], g, st) : launch<kApply, kLow>(apply[from], g, st);
+    g.add_ld = x_ld;
+    g.low_ld = t.ldx;
+    g.add = from;
+    g.add_low = from + rows * x_ld;
+    g.out = to;
+    g.out_low = to + rows * x_ld;
+    e = two ? launch<kApply, kTwo>(apply[i & 1], g, st) : launch<kApply, kLow>(apply[i & 1], g, st);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -16,98 +16,12 @@
 #include "../../include/moe_model.h"
 #include "common.cuh"
 #include "internal.h"
+#include "muon.cuh"
 #include "orth.h"
 #include "train.h"
 
 namespace moe {
 namespace muon {
-
-constexpr int kSegs = 16;                       // tensors a launch carries in its arguments
-constexpr int64_t kScratch = 3ll << 30;         // bytes of one round's matrices
-constexpr int64_t kMaxRound = 16384;            // matrices of a round
-constexpr int kPart = 8192;                     // elements of a partial sum of squares
-constexpr int kTile = 64;
-
-// Matrices of one tensor that take part in a round: `count` from its matrix
-// `first`, the round's matrices `at` and on.
-struct Seg {
-  void* param;        // also the output of the matrices alone
-  const void* grad;
-  float* momentum;    // NULL: u is grad itself
-  int64_t first;
-  int32_t at, count;
-  int32_t rows, cols, pdtype, gdtype;
-  float size;         // lr * size of the update
-};
-
-struct Round {
-  Seg seg[kSegs];
-  int32_t segs, batch;
-  int32_t m, n, ldx, parts;   // of a matrix: sides, row length in scratch, partial sums
-  float beta, rest, keep;     // momentum, 1 - momentum; 1 - lr * weight_decay
-  int32_t nesterov, update;   // update: param = keep param - size X, else out = X
-  double eps;
-  double* sums;               // [batch][parts]
-  int32_t planes;             // of X: two of fp16, or one and 8-bit parts (orth.h)
-  __half* x;                  // [planes][batch][m][ldx], the 8-bit parts behind
-};
-
-__device__ __forceinline__ const Seg& seg_of(const Round& r, int b) {
-  int s = 0;
-  while (s + 1 < r.segs && r.seg[s + 1].at <= b) ++s;
-  return r.seg[s];
-}
-
-// 8 consecutive elements of a row or of the whole matrix, as floats; `n` of them
-// exist.  vec: 16-byte aligned and all there.
-__device__ __forceinline__ void read8(const void* p, int dtype, int64_t at, int n, bool vec, float* f) {
-  if (dtype == MOE_F32) {
-    const float* q = static_cast<const float*>(p) + at;
-    if (vec) {
-      unpack16(reinterpret_cast<const uint4*>(q)[0], f, (const float*)nullptr);
-      unpack16(reinterpret_cast<const uint4*>(q)[1], f + 4, (const float*)nullptr);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = e < n ? q[e] : 0.0f;
-    }
-  } else {
-    const bf16* q = static_cast<const bf16*>(p) + at;
-    if (vec) {
-      unpack16(reinterpret_cast<const uint4*>(q)[0], f, (const bf16*)nullptr);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = e < n ? __bfloat162float(q[e]) : 0.0f;
-    }
-  }
-}
-__device__ __forceinline__ void write8(void* p, int dtype, int64_t at, int n, bool vec, const float* f) {
-  if (dtype == MOE_F32) {
-    float* q = static_cast<float*>(p) + at;
-    if (vec) {
-      reinterpret_cast<uint4*>(q)[0] = pack16(f, (const float*)nullptr);
-      reinterpret_cast<uint4*>(q)[1] = pack16(f + 4, (const float*)nullptr);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e < n) q[e] = f[e];
-    }
-  } else {
-    bf16* q = static_cast<bf16*>(p) + at;
-    if (vec) {
-      *reinterpret_cast<uint4*>(q) = pack16(f, (const bf16*)nullptr);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e < n) q[e] = __float2bfloat16_rn(f[e]);
-    }
-  }
-}
-__device__ __forceinline__ bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-// The direction's element from a gradient's and the new momentum's.
-__device__ __forceinline__ float direction(const Round& r, float g, float v) {
-  return r.nesterov ? fmaf(r.beta, v, r.rest * g) : v;
-}
 
 // Momentum, and the sum of u^2 over kPart elements of a matrix: in fp32 over a warp's
 // elements, in fp64 beyond.  A warp whose sum overflowed, or is small enough for
@@ -180,18 +94,6 @@ __global__ void __launch_bounds__(256) momentum_kernel(const __grid_constant__ R
       r.sums[task] = t;
     }
   }
-}
-
-// Two factors whose product is 2^kOrthX / (norm + eps): one would leave fp32 for
-// norms far from 1.
-__device__ __forceinline__ float2 scale_of(double sum, double eps) {
-  const double norm = sqrt(sum);
-  if (!isfinite(norm)) return make_float2(__int_as_float(0x7fc00000), 1.0f);
-  if (norm == 0.0) return make_float2(0.0f, 0.0f);
-  int e;
-  const double f = frexp(norm + eps, &e);      // norm + eps = f 2^e
-  const int h = -e / 2;
-  return make_float2(ldexpf(1.0f, h), (float)ldexp(1.0 / f, kOrthX - e - h));
 }
 
 // 8 values to X, from `at` elements of the round's first plane.
@@ -427,7 +329,8 @@ Bucket bucket_of(int m, int n, int planes, int64_t batch) {
   b.ldx = (n + 127) / 128 * 128;
   b.lda = (m + 63) / 64 * 64;
   b.parts = (int)(((int64_t)m * n + kPart - 1) / kPart);
-  b.each = 2 * x_bytes(b) + 2ll * planes * m * b.lda * 2 + 8ll * b.parts;
+  const bool small = muon_small_fits(m, n, planes);   // needs none
+  b.each = small ? 1 : 2 * x_bytes(b) + 2ll * planes * m * b.lda * 2 + 8ll * b.parts;
   b.round = std::max<int64_t>(1, std::min<int64_t>(batch, std::min<int64_t>(kMaxRound, kScratch / b.each)));
   return b;
 }
@@ -436,8 +339,10 @@ struct RoundLayout {
   size_t sums, x[2], a, b, total;
 };
 RoundLayout layout_of(const Bucket& q) {
-  RoundLayout L;
+  RoundLayout L = {};
   size_t off = 256;
+  L.total = off;
+  if (muon_small_fits(q.m, q.n, q.planes)) return L;
   auto take = [&](size_t bytes) {
     const size_t at = off;
     off += (bytes + 255) & ~(size_t)255;
@@ -491,7 +396,7 @@ const char* check_sides(int64_t batch, int32_t rows, int32_t cols) {
   return nullptr;
 }
 
-// One round: the products of the matrices in r's segments.
+// One round: the update of the matrices in r's segments.
 cudaError_t run_round(Round& r, const Bucket& q, const RoundLayout& L, char* ws, const moe_orth_coefs& c,
                       cudaStream_t st) {
   r.m = q.m;
@@ -500,6 +405,8 @@ cudaError_t run_round(Round& r, const Bucket& q, const RoundLayout& L, char* ws,
   r.parts = q.parts;
   r.planes = q.planes;
   r.eps = c.eps;
+  if (muon_small_fits(q.m, q.n, q.planes))
+    return launch_muon_small(r, q.planes, c.steps, c.coef, reinterpret_cast<uint32_t*>(ws), st);
   r.sums = reinterpret_cast<double*>(ws + L.sums);
   r.x = reinterpret_cast<__half*>(ws + L.x[0]);
   const int64_t sms = tc_sm_count(), tiles = (int64_t)((q.m + kTile - 1) / kTile) * ((q.n + kTile - 1) / kTile) * r.batch;

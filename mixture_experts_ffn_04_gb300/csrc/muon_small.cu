@@ -1,0 +1,520 @@
+// muon_small.cu -- the orthogonalised update of matrices whose smaller side is at most
+// 128, in one launch: a cluster of up to 16 CTAs holds a matrix from gradient to
+// parameter.
+//
+// X [m, n], m <= 128, is split by columns: a CTA has 256 of them (fp32 matrices: 128), in
+// fp32 in the registers of its threads, laid out as TMEM is (a lane a row), and as
+// fp16 planes in shared memory for the tensor cores (tcgen05, 128 x 128 and 128 x 256
+// products).  A step is
+//   P = X_slab X_slab^T in each CTA, summed over the cluster through distributed shared
+//       memory (each CTA adds up its share of the rows, in rank order, and hands it to all):  A
+//   B = b A + c A A in each CTA,   X_slab <- a X_slab + B X_slab
+// with the operand precision of the general path (one fp16 plane, or three products of two
+// planes), and X itself in fp32.
+//
+// Bound by latency: two cluster barriers and three short chains of products a step.  A
+// 128 x 2048 matrix through the general path's 18 launches took 155 us.
+#include <algorithm>
+#include <atomic>
+
+#include "../../include/moe_model.h"
+#include "common.cuh"
+#include "internal.h"
+#include "muon.cuh"
+#include "orth.h"
+#include "tc_pair.cuh"
+#include "tcgen05.cuh"
+#include "train.h"
+
+namespace moe {
+namespace muon {
+
+using namespace tc;
+
+constexpr int kSide = 128;
+constexpr int kThreads = 256;
+constexpr int kMaxCluster = 16;
+constexpr int kSquare = kSide * kSide * 2;              // an fp16 plane of A or B
+constexpr int kPartial = kSide * kSide * 4;             // P, then the planes of B
+__host__ __device__ constexpr int slab_of(int planes) { return planes == 2 ? 128 : 256; }
+__host__ __device__ constexpr int x_bytes_of(int planes) { return planes * kSide * slab_of(planes) * 2; }
+constexpr int smem_of(int planes) { return 1024 + x_bytes_of(planes) + kPartial + planes * kSquare + 256; }
+static_assert(smem_of(1) <= 232448 && smem_of(2) <= 232448, "shared memory budget of one CTA");
+static_assert(2 * kSquare <= kPartial, "B's planes take P's place");
+
+struct Coefs {
+  int32_t steps;
+  float c[MOE_ORTH_MAX_STEPS][3];
+};
+
+// An operand of 64-column blocks [128 rows][128 bytes], 128-byte swizzle: 16 bytes j of
+// row r of block b.
+__device__ __forceinline__ uint32_t op_at(uint32_t base, int b, int r, int j) {
+  return base + b * (kSide * 128) + r * 128 + ((j ^ (r & 7)) << 4);
+}
+// The same blocks as an MN-major operand: 64 columns a block, the next 16384 bytes on.
+__device__ __forceinline__ uint64_t block_mn_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)((kSide * 128) >> 4) << 16;   // next 64 columns
+  d |= (uint64_t)(1024 >> 4) << 32;            // next 8 k-rows
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+__host__ __device__ constexpr uint32_t idesc_of(int n, bool b_mn) {
+  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kSide >> 4) << 24) | (b_mn ? 1u << 16 : 0u);
+}
+
+__device__ __forceinline__ void st4(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 ld4(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void st4_cluster(uint32_t at, uint4 v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ float4 ld4_cluster(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+// 8 values as planes of fp16.
+template <int PLANES>
+__device__ __forceinline__ void halves8(const float* f, uint4 (&out)[PLANES]) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 a = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+    h[i] = *reinterpret_cast<const uint32_t*>(&a);
+    if (PLANES == 2) {
+      const float2 v = __half22float2(a);
+      const __half2 b = __floats2half2_rn(f[2 * i] - v.x, f[2 * i + 1] - v.y);
+      l[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+  }
+  out[0] = make_uint4(h[0], h[1], h[2], h[3]);
+  if (PLANES == 2) out[PLANES - 1] = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// The staging square: [128][128] floats, a row's columns turned by its number, so that a
+// warp's rows of one column lie in different banks.
+__device__ __forceinline__ float* square_at(float* s, int r, int c) { return s + r * kSide + (c ^ (r & 31)); }
+
+template <int PLANES>
+__global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constant__ Round r,
+                                                            const __grid_constant__ Coefs k, int cols_of, int ctas,
+                                                            uint32_t* flags) {
+  constexpr int SLAB = slab_of(PLANES), MINE = SLAB / 2, XP = kSide * SLAB * 2;   // XP: a plane of X
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  float* part = reinterpret_cast<float*>(smem + x_bytes_of(PLANES));
+  unsigned char* s_a = smem + x_bytes_of(PLANES) + kPartial;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_a + PLANES * kSquare);
+  double* sums = reinterpret_cast<double*>(bars + 2);          // [8] of the warps, [8] the CTA's
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sums + 10);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  pdl_trigger();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = ctas > 1 ? (int)cluster_rank() : 0;
+  const uint32_t xs = smem_u32(smem), ps = smem_u32(part), as = smem_u32(s_a), bar = smem_u32(bars);
+  if (tid == 0) {
+    mbar_init(bar, 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    proxy_fence();
+  }
+  if (warp == 0) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t d_gram = tmem, d_poly = tmem + 128, d_apply = tmem + 256;
+  pdl_wait();
+
+  const int b = (int)blockIdx.x / ctas;
+  const Seg& s = seg_of(r, b);
+  const bool tall = s.rows > s.cols;
+  const int64_t base = (s.first + (b - s.at)) * (int64_t)s.rows * s.cols;
+  const int col0 = rank * cols_of, cols = max(0, min(cols_of, r.n - col0));   // of this CTA
+  const bool ok8 = s.cols % 8 == 0 && aligned(s.grad) && aligned(s.momentum) && aligned(s.param);
+  // 8 elements of the square of columns 128 h .. as memory has them: `line` (a row of X,
+  // or a column where it is tall) and 8 places from `place`; n of them exist
+  struct Piece {
+    int64_t at;
+    int line, place, n;
+  };
+  auto piece = [&](int h, int it) {
+    Piece p;
+    p.line = it * 16 + tid / 16;
+    p.place = tid % 16 * 8;
+    const int c = 128 * h + (tall ? p.line : p.place), row = tall ? p.place : p.line;
+    if (tall) {
+      p.n = c < cols ? min(8, r.m - row) : 0;
+      p.at = base + (int64_t)(col0 + c) * s.cols + row;
+    } else {
+      p.n = row < r.m ? min(8, cols - c) : 0;
+      p.at = base + (int64_t)row * s.cols + col0 + c;
+    }
+    return p;
+  };
+  auto place_of = [&](const Piece& p, int e) {
+    return tall ? square_at(part, p.place + e, p.line) : square_at(part, p.line, p.place + e);
+  };
+  const int row = 32 * (warp & 3) + lane, half = warp >> 2;   // this thread's row; its MINE columns
+  float x[MINE];
+  double square = 0.0;
+#pragma unroll
+  for (int h = 0; h < SLAB / 128; ++h) {
+    float u[8][8];
+    float sum = 0.0f;
+#pragma unroll
+    for (int it = 0; it < 8; ++it) {
+      const Piece p = piece(h, it);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u[it][e] = 0.0f;
+      if (p.n > 0) {
+        const bool v8 = ok8 && p.n == 8;
+        float g[8];
+        read8(s.grad, s.gdtype, p.at, p.n, v8, g);
+        if (s.momentum != nullptr) {
+          float v[8];
+          read8(s.momentum, MOE_F32, p.at, p.n, v8, v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            v[e] = fmaf(r.beta, v[e], r.rest * g[e]);
+            u[it][e] = e < p.n ? direction(r, g[e], v[e]) : 0.0f;
+          }
+          write8(s.momentum, MOE_F32, p.at, p.n, v8, v);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) u[it][e] = e < p.n ? g[e] : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        sum = fmaf(u[it][e], u[it][e], sum);
+        *place_of(p, e) = u[it][e];
+      }
+    }
+    // squares as in the general path: in fp32 over a warp, scaled where they leave the
+    // range, in fp64 beyond
+    auto over = [](float v) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      return v;
+    };
+    auto squares = [&](float scale) {
+      float t = 0.0f;
+#pragma unroll
+      for (int it = 0; it < 8; ++it)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float v = u[it][e] * scale;
+          t = fmaf(v, v, t);
+        }
+      return (double)over(t);
+    };
+    double total = (double)over(sum);
+    if (!(total >= 1e-28)) total = squares(0x1p80f) * 0x1p-160;
+    else if (!(total <= 1e38)) total = squares(0x1p-96f) * 0x1p192;
+    square += total;
+    __syncthreads();
+    if (SLAB == 128 || half == h)
+#pragma unroll
+      for (int j = 0; j < MINE; ++j) x[j] = *square_at(part, row, (SLAB == 128 ? half * MINE : 0) + j);
+    __syncthreads();
+  }
+  if (lane == 0) sums[warp] = square;
+  __syncthreads();
+  if (tid == 0) {
+    double t = 0.0;
+    for (int w = 0; w < 8; ++w) t += sums[w];
+    sums[8] = t;
+  }
+  if (ctas > 1) cluster_sync();
+  else __syncthreads();
+  {
+    double t = 0.0;
+    for (int q = 0; q < ctas; ++q) {
+      double v;
+      asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(map_to_rank(smem_u32(sums + 8), (uint32_t)q)) : "memory");
+      t += v;
+    }
+    const float2 f = scale_of(t, r.eps);
+#pragma unroll
+    for (int j = 0; j < MINE; ++j) x[j] = x[j] * f.x * f.y;
+  }
+
+  bool good = true;
+  uint32_t phase = 0;
+  // Products issued by one thread, waited for by all.
+  auto multiply = [&](auto issue) {
+    proxy_fence();          // this thread's writes of operands
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0) {
+      tc_fence_after();
+      issue();
+      tc_commit(bar);
+    }
+    if (!mbar_wait(bar, phase & 1u, abort_flag)) good = false;
+    phase ^= 1u;
+    tc_fence_after();
+  };
+  auto put_x = [&]() {
+#pragma unroll
+    for (int j = 0; j < MINE / 8; ++j) {
+      uint4 v[PLANES];
+      halves8<PLANES>(x + 8 * j, v);
+      const int c = half * MINE / 8 + j;
+#pragma unroll
+      for (int p = 0; p < PLANES; ++p) st4(op_at(xs + p * XP, c / 8, row, c % 8), v[p]);
+    }
+  };
+  // the products of planes above 2^-22, smallest first
+  constexpr int PRODUCTS = PLANES == 2 ? 3 : 1;
+  auto plane_a = [](int i) { return PRODUCTS == 3 && i == 0 ? 1 : 0; };
+  auto plane_b = [](int i) { return PRODUCTS == 3 && i == 1 ? 1 : 0; };
+  const int blocks = (cols + 63) / 64;       // of X with columns
+  put_x();
+  for (int step = 0; step < k.steps; ++step) {
+    const float ca = k.c[step][0], cb = k.c[step][1], cc = k.c[step][2];
+    // P = X X^T over this CTA's columns
+    multiply([&]() {
+      uint32_t more = 0;
+      for (int i = 0; i < PRODUCTS; ++i)
+        for (int q = 0; q < blocks * 4; ++q, more = 1) {
+          const uint32_t at = xs + (q / 4) * (kSide * 128) + (q % 4) * 32;
+          tc_mma(d_gram, sw128_desc(at + plane_a(i) * XP), sw128_desc(at + plane_b(i) * XP), idesc_of(128, false), more);
+        }
+    });
+    // row `row`, 64 columns, to the partial square in units of 16 bytes (turned by the row)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t v[16];
+      tmem_ld16(d_gram + ((uint32_t)(32 * (warp & 3)) << 16) + half * 64 + 16 * c, v);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int unit = half * 16 + 4 * c + j;
+        const uint4 w = blocks > 0 ? make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]) : make_uint4(0, 0, 0, 0);
+        st4(ps + row * 512 + ((unit ^ (row & 31)) << 4), w);
+      }
+    }
+    if (ctas > 1) cluster_sync();
+    else __syncthreads();
+    // this CTA's rows of A: the partial squares in rank order, to every CTA
+    {
+      const int share = (kSide + ctas - 1) / ctas, r0 = rank * share, r1 = min(kSide, r0 + share);
+      for (int it = r0 * 16 + tid; it < r1 * 16; it += kThreads) {
+        const int rr = it / 16, j = it % 16;       // 8 columns from 8 j
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = 0.0f;
+        for (int q = 0; q < ctas; ++q) {
+          const uint32_t from = map_to_rank(ps, (uint32_t)q) + rr * 512;
+          const float4 u = ld4_cluster(from + (((2 * j) ^ (rr & 31)) << 4)), v = ld4_cluster(from + (((2 * j + 1) ^ (rr & 31)) << 4));
+          f[0] += u.x; f[1] += u.y; f[2] += u.z; f[3] += u.w;
+          f[4] += v.x; f[5] += v.y; f[6] += v.z; f[7] += v.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] *= 0x1p-15f;    // 2^(kOrthA - 2 kOrthX)
+        uint4 v[PLANES];
+        halves8<PLANES>(f, v);
+        for (int q = 0; q < ctas; ++q)
+#pragma unroll
+          for (int p = 0; p < PLANES; ++p)
+            st4_cluster(op_at(map_to_rank(as, (uint32_t)q) + p * kSquare, j / 8, rr, j % 8), v[p]);
+      }
+      proxy_fence();
+    }
+    if (ctas > 1) cluster_sync();
+    else __syncthreads();
+    // B = b A + c A A
+    multiply([&]() {
+      uint32_t more = 0;
+      for (int i = 0; i < PRODUCTS; ++i)
+        for (int q = 0; q < 8; ++q, more = 1) {
+          const uint32_t at = as + (q / 4) * (kSide * 128) + (q % 4) * 32;
+          tc_mma(d_poly, sw128_desc(at + plane_a(i) * kSquare), sw128_desc(at + plane_b(i) * kSquare), idesc_of(128, false), more);
+        }
+    });
+    const float kb = cb * 0.25f, kc = cc * 0x1p-13f;     // 2^(kOrthB - kOrthA), 2^(kOrthB - 2 kOrthA)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t v[16];
+      tmem_ld16(d_poly + ((uint32_t)(32 * (warp & 3)) << 16) + half * 64 + 16 * c, v);
+      tmem_wait_ld();
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int j = half * 8 + 2 * c + g;
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = 0.0f;
+#pragma unroll
+        for (int p = PLANES - 1; p >= 0; --p) {
+          const uint4 h = ld4(op_at(as + p * kSquare, j / 8, row, j % 8));
+          const uint32_t w[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+            f[2 * e] += y.x;
+            f[2 * e + 1] += y.y;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = fmaf(kc, __uint_as_float(v[8 * g + e]), kb * f[e]);
+        uint4 o[PLANES];
+        halves8<PLANES>(f, o);
+#pragma unroll
+        for (int p = 0; p < PLANES; ++p) st4(op_at(ps + p * kSquare, j / 8, row, j % 8), o[p]);
+      }
+    }
+    // X = a X + B X
+    multiply([&]() {
+      uint32_t more = 0;
+      for (int i = 0; i < PRODUCTS; ++i)
+        for (int q = 0; q < 8; ++q, more = 1)
+          tc_mma(d_apply, sw128_desc(ps + plane_a(i) * kSquare + (q / 4) * (kSide * 128) + (q % 4) * 32),
+                 block_mn_desc(xs + plane_b(i) * XP + q * 2048), idesc_of(SLAB, true), more);
+    });
+#pragma unroll
+    for (int c = 0; c < MINE / 16; ++c) {
+      uint32_t v[16];
+      tmem_ld16(d_apply + ((uint32_t)(32 * (warp & 3)) << 16) + half * MINE + 16 * c, v);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[16 * c + e] = fmaf(0x1p-9f, __uint_as_float(v[e]), ca * x[16 * c + e]);
+    }
+    if (step + 1 < k.steps) put_x();
+  }
+  static_assert(kOrthX == 13 && kOrthA == 11 && kOrthB == 9, "the powers of two above");
+
+  // the update, through the square again
+#pragma unroll
+  for (int h = 0; h < SLAB / 128; ++h) {
+    __syncthreads();
+    if (SLAB == 128 || half == h)
+#pragma unroll
+      for (int j = 0; j < MINE; ++j) *square_at(part, row, (SLAB == 128 ? half * MINE : 0) + j) = x[j] * 0x1p-13f;
+    __syncthreads();
+#pragma unroll
+    for (int it = 0; it < 8; ++it) {
+      const Piece p = piece(h, it);
+      if (p.n <= 0) continue;
+      const bool v8 = ok8 && p.n == 8;
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = *place_of(p, e);
+      if (r.update) {
+        float w[8];
+        read8(s.param, s.pdtype, p.at, p.n, v8, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = fmaf(-s.size, f[e], r.keep * w[e]);
+      }
+      write8(s.param, s.pdtype, p.at, p.n, v8, f);
+    }
+  }
+  if (!good) {
+    // a product that never ended: long enough for it to be over before TMEM goes
+    const long long t0 = clock64();
+    while (clock64() - t0 < (1 << 21)) {}
+    if (lane == 0) set_flag(flags, kFlagTimeout);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (ctas > 1) cluster_sync();   // no CTA leaves while its shared memory may be read
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// CTAs of a matrix: a power of two.
+static int ctas_of(int n, int planes) {
+  int c = 1;
+  while (c * slab_of(planes) < n) c *= 2;
+  return c;
+}
+
+static std::atomic<int> g_most[2][64];   // CTAs of the largest cluster that runs, + 1
+
+// Shared memory and cluster sizes of this device, found out once.
+static cudaError_t prepare(int planes, int* most) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::atomic<int>& slot = g_most[planes - 1][dev];
+  if (slot == 0) {
+    const void* f = planes == 2 ? (const void*)small_kernel<2> : (const void*)small_kernel<1>;
+    e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(planes));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    int found = 1;
+    for (int c = kMaxCluster; c > 1 && found == 1; c /= 2) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = c;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.gridDim = dim3(c);
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = smem_of(planes);
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int n = 0;
+      e = cudaOccupancyMaxActiveClusters(&n, f, &cfg);
+      if (e != cudaSuccess) return e;
+      if (n > 0) found = c;
+    }
+    slot = found + 1;
+  }
+  *most = slot.load() - 1;
+  return cudaSuccess;
+}
+
+}  // namespace muon
+
+bool muon_small_fits(int m, int n, int planes) {
+  return m <= muon::kSide && muon::ctas_of(n, planes) <= muon::kMaxCluster;
+}
+
+cudaError_t launch_muon_small(const muon::Round& r, int planes, int steps, const double (*coef)[3], uint32_t* flags,
+                              cudaStream_t st) {
+  using namespace muon;
+  int most = 0;
+  cudaError_t e = prepare(planes, &most);
+  if (e != cudaSuccess) return e;
+  const int ctas = ctas_of(r.n, planes);
+  if (ctas > most) return cudaErrorNotSupported;
+  const int cols = ((r.n + ctas - 1) / ctas + 7) / 8 * 8;   // of a CTA
+  Coefs k = {};
+  k.steps = steps;
+  for (int i = 0; i < steps; ++i)
+    for (int j = 0; j < 3; ++j) k.c[i][j] = (float)coef[i][j];
+  const unsigned grid = (unsigned)(r.batch * ctas);
+  if (planes == 2)
+    return launch_after(small_kernel<2>, grid, kThreads, smem_of(2), st, (unsigned)ctas, r, k, cols, ctas, flags);
+  return launch_after(small_kernel<1>, grid, kThreads, smem_of(1), st, (unsigned)ctas, r, k, cols, ctas, flags);
+}
+
+}  // namespace moe

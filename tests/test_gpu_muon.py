@@ -3,8 +3,8 @@
 Bounds (derived).  The result of the polynomial's steps has no useful closed error
 bound (an error may grow by 4 a step), so the bound is the error that the
 documented roundings give on the same input: `modelled` runs the steps in float64
-with X in two fp16 parts, the operands of every product in one (bf16 matrices) or two
-(fp32), and every product's entry off by up to 2^-19 downwards: the tensor cores cut
+with X in two fp16 parts (bf16 matrices: 19 bits), the operands of every product in one
+part (bf16 matrices) or two (fp32), and every product's entry off by up to 2^-19 downwards: the tensor cores cut
 the fp32 accumulator at each K = 16 step, by at most 2^-23 of it (a bit of 24), 32
 steps of a chunk lose up to half of each, the chunks are added in fp32.  Two draws of such
 errors differ by sqrt 2 of one; 2.5 times the modelled error covers that and the
@@ -43,7 +43,11 @@ def modelled(u, planes, coefs=(COEFS,) * 5, eps=1e-7):
     def parts(v, power):
         v = (v * 2.0 ** power).float()
         hi = v.half()
-        return hi.double() / 2.0 ** power, (v - hi.float()).half().double() / 2.0 ** power
+        low = (v - hi.float()).half().double()
+        if planes == 1:
+            unit = 2.0 ** (torch.floor(torch.log2(hi.double().abs().clamp_min(2.0 ** -14))) - 18)
+            low = torch.round((v.double() - hi.double()) / unit) * unit
+        return hi.double() / 2.0 ** power, low / 2.0 ** power
 
     def product(p, q):
         r = p[0] @ q[0] if planes == 1 else p[0] @ q[0] + p[0] @ q[1] + p[1] @ q[0]
@@ -81,7 +85,9 @@ def draw(shape, dt, seed=0, rank=None):
 
 
 SHAPES = [(1, 1, 1), (1, 1, 9), (2, 9, 1), (3, 7, 5), (2, 16, 16), (5, 8, 64), (1, 64, 200), (2, 129, 70),
-          (1, 128, 2048), (1, 257, 300), (4, 100, 513), (3, 513, 100), (2, 256, 256), (2, 777, 1001), (1, 1030, 520)]
+          (1, 128, 2048), (1, 257, 300), (4, 100, 513), (3, 513, 100), (2, 256, 256), (2, 777, 1001), (1, 1030, 520),
+          # one side at most 128: a cluster a matrix up to a length, more of them than run at once, beyond it
+          (40, 128, 1000), (2, 2047, 127), (1, 4096, 100), (2, 33, 4097), (1, 9001, 64), (300, 24, 40), (2, 129, 4000)]
 
 
 @pytest.mark.parametrize("shape", SHAPES)
@@ -178,9 +184,9 @@ def check_step(m, params, grads, nesterov, decay, scale, lr=0.05, beta=0.9):
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("nesterov,decay,scale", [(True, 0.1, "spectral"), (False, 0.0, "rms"), (True, 0.0, "none")])
 def test_step_of_a_layer(m, dt, nesterov, decay, scale):
-    """gate, up and down of one layer share their launches; a router and a 2-D matrix
+    """gate, up and down of one layer share their launches; a router and 2-D matrices
     have their own."""
-    shapes = [(4, 72, 136), (4, 72, 136), (4, 136, 72), (10, 136), (200, 33)]
+    shapes = [(4, 72, 136), (4, 72, 136), (4, 136, 72), (10, 136), (200, 33), (3, 140, 264), (3, 264, 140), (131, 131)]
     params = [torch.randn(s, device="cuda").to(dt) for s in shapes]
     grads = [torch.randn(s, device="cuda").to(dt) for s in shapes]
     check_step(m, params, grads, nesterov, decay, scale)
@@ -188,14 +194,18 @@ def test_step_of_a_layer(m, dt, nesterov, decay, scale):
 
 def test_step_of_mixed_types_and_odd_addresses(m):
     """Gradients of the other type; views at odd element offsets."""
-    flat = torch.randn(20000, device="cuda")
-    half = torch.randn(20000, device="cuda").bfloat16()
-    params = [flat[1:1 + 40 * 60].view(40, 60), half[3:3 + 2 * 31 * 17].view(2, 31, 17), flat[5001:5001 + 17 * 31].view(17, 31)]
-    grads = [half[7001:7001 + 2400].view(40, 60), flat[9003:9003 + 1054].view(2, 31, 17), half[12001:12001 + 527].view(17, 31)]
+    N = 200000
+    flat = torch.randn(N, device="cuda")
+    half = torch.randn(N, device="cuda").bfloat16()
+    params = [flat[1:1 + 40 * 60].view(40, 60), half[3:3 + 2 * 31 * 17].view(2, 31, 17), flat[5001:5001 + 17 * 31].view(17, 31),
+              half[20001:20001 + 130 * 151].view(130, 151), flat[60003:60003 + 150 * 133].view(150, 133)]
+    grads = [half[7001:7001 + 2400].view(40, 60), flat[9003:9003 + 1054].view(2, 31, 17), half[12001:12001 + 527].view(17, 31),
+             flat[100001:100001 + 130 * 151].view(130, 151), half[150003:150003 + 150 * 133].view(150, 133)]
     guard = flat.clone(), half.clone()
     check_step(m, params, grads, True, 0.01, "spectral")
-    for now, was, used in ((flat, guard[0], [(1, 2401), (5001, 5528)]), (half, guard[1], [(3, 1057)])):
-        keep = torch.ones(20000, dtype=torch.bool, device="cuda")
+    for now, was, used in ((flat, guard[0], [(1, 2401), (5001, 5528), (60003, 60003 + 150 * 133)]),
+                           (half, guard[1], [(3, 1057), (20001, 20001 + 130 * 151)])):
+        keep = torch.ones(N, dtype=torch.bool, device="cuda")
         for lo, hi in used:
             keep[lo:hi] = False
         assert torch.equal(now[keep], was[keep])

@@ -97,15 +97,22 @@ __device__ __forceinline__ float direction(const Round& r, float g, float v) {
 }
 
 // Two factors whose product is 2^kOrthX / (norm + eps): one would leave fp32 for
-// norms far from 1.
+// norms far from 1.  The square root and the quotient in fp32 (a common factor of the matrix,
+// within 2^-23), the range in the exponents: fp64 roots and divisions take thousands of clocks
+// here.
 __device__ __forceinline__ float2 scale_of(double sum, double eps) {
-  const double norm = sqrt(sum);
-  if (!isfinite(norm)) return make_float2(__int_as_float(0x7fc00000), 1.0f);
-  if (norm == 0.0) return make_float2(0.0f, 0.0f);
+  if (!isfinite(sum)) return make_float2(__int_as_float(0x7fc00000), 1.0f);
+  if (sum == 0.0) return make_float2(0.0f, 0.0f);
   int e;
-  const double f = frexp(norm + eps, &e);      // norm + eps = f 2^e
-  const int h = -e / 2;
-  return make_float2(ldexpf(1.0f, h), (float)ldexp(1.0 / f, kOrthX - e - h));
+  double m = frexp(sum, &e);                   // sum = m 2^e, made even
+  if (e & 1) {
+    m *= 0.5;
+    ++e;
+  }
+  int q;
+  const double f = frexp(ldexp((double)sqrtf((float)m), e / 2) + eps, &q);      // norm + eps = f 2^q
+  const int h = -q / 2;
+  return make_float2(ldexpf(1.0f, h), ldexpf(1.0f / (float)f, kOrthX - q - h));
 }
 
 }  // namespace muon

@@ -32,7 +32,7 @@ namespace muon {
 using namespace tc;
 
 constexpr int kSide = 128;
-constexpr int kThreads = 256;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kSquare = kSide * kSide * 2;              // an fp16 plane of A or B
 constexpr int kPartial = kSide * kSide * 4;             // P, then the planes of B
@@ -77,9 +77,8 @@ __device__ __forceinline__ uint4 ld4(uint32_t at) {
                : "memory");
   return v;
 }
-__device__ __forceinline__ void st4_cluster(uint32_t at, uint4 v) {
-  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-               : "memory");
+__device__ __forceinline__ void st2_cluster(uint32_t at, uint32_t x, uint32_t y) {
+  asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(x), "r"(y) : "memory");
 }
 __device__ __forceinline__ float4 ld4_cluster(uint32_t at) {
   float4 v;
@@ -109,29 +108,55 @@ __device__ __forceinline__ void halves8(const float* f, uint4 (&out)[PLANES]) {
   if (PLANES == 2) out[PLANES - 1] = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
-// The staging square: [128][128] floats, a row's columns turned by its number, so that a
-// warp's rows of one column lie in different banks.
-__device__ __forceinline__ float* square_at(float* s, int r, int c) { return s + r * kSide + (c ^ (r & 31)); }
+// The staging square: [128][columns] floats, whose columns change places by the row and by
+// themselves, so that neither a warp's 32 rows of one column meet in a bank, nor its columns 8
+// apart of one row, nor its rows 8 apart of one column.
+__device__ __forceinline__ int row_turn(int r) { return (r & 31) ^ ((r >> 5) & 3); }
+__device__ __forceinline__ int col_turn(int c) { return c ^ ((c >> 5) & 7); }
+template <int COLS>
+__device__ __forceinline__ float* square_at(float* s, int r, int c) { return s + r * COLS + (col_turn(c) ^ row_turn(r)); }
+
+// Eight elements that lie side by side in memory: of row `line` of X from column `place`,
+// or, where X is the transposed matrix, of column `line` from row `place` (a multiple of 8).
+// Their places in the square, e = 0 .. 7, without the turns worked out for each.
+template <int COLS, bool TALL>
+struct Places {
+  float* p;
+  int turn;
+  __device__ __forceinline__ Places(float* s, int line, int place) {
+    if (TALL) {
+      p = s + place * COLS;
+      turn = col_turn(line) ^ row_turn(place);       // row_turn(place + e) = row_turn(place) ^ e
+    } else {
+      turn = col_turn(place) ^ row_turn(line);       // col_turn(place + e) = col_turn(place) ^ e
+      p = s + line * COLS;
+    }
+  }
+  __device__ __forceinline__ float& operator[](int e) const { return TALL ? p[e * COLS + (turn ^ e)] : p[turn ^ e]; }
+};
 
 template <int PLANES>
 __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constant__ Round r,
                                                             const __grid_constant__ Coefs k, int cols_of, int ctas,
                                                             uint32_t* flags) {
-  constexpr int SLAB = slab_of(PLANES), MINE = SLAB / 2, XP = kSide * SLAB * 2;   // XP: a plane of X
+  constexpr int SLAB = slab_of(PLANES), MINE = SLAB / 4, XP = kSide * SLAB * 2;   // XP: a plane of X
+  static_assert(kSide * SLAB * 4 <= x_bytes_of(PLANES) + kPartial, "the staging square lies over X's planes and P");
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  float* part = reinterpret_cast<float*>(smem + x_bytes_of(PLANES));
-  unsigned char* s_a = smem + x_bytes_of(PLANES) + kPartial;
+  float* square = reinterpret_cast<float*>(smem);
+  unsigned char* s_p = smem + x_bytes_of(PLANES);
+  unsigned char* s_a = s_p + kPartial;
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_a + PLANES * kSquare);
-  double* sums = reinterpret_cast<double*>(bars + 2);          // [8] of the warps, [8] the CTA's
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sums + 10);
+  double* sums = reinterpret_cast<double*>(bars + 2);          // of the warps, then the CTA's
+  float2* factor = reinterpret_cast<float2*>(sums + kWarps + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(factor + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = ctas > 1 ? (int)cluster_rank() : 0;
-  const uint32_t xs = smem_u32(smem), ps = smem_u32(part), as = smem_u32(s_a), bar = smem_u32(bars);
+  const uint32_t xs = smem_u32(smem), ps = smem_u32(s_p), as = smem_u32(s_a), bar = smem_u32(bars);
   if (tid == 0) {
     mbar_init(bar, 1);
     *abort_flag = 0;
@@ -142,6 +167,8 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
+  // A's rows and columns past m stay zero
+  for (int i = tid; i < PLANES * kSquare / 16; i += kThreads) st4(as + 16 * i, make_uint4(0, 0, 0, 0));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -155,110 +182,172 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
   const int64_t base = (s.first + (b - s.at)) * (int64_t)s.rows * s.cols;
   const int col0 = rank * cols_of, cols = max(0, min(cols_of, r.n - col0));   // of this CTA
   const bool ok8 = s.cols % 8 == 0 && aligned(s.grad) && aligned(s.momentum) && aligned(s.param);
-  // 8 elements of the square of columns 128 h .. as memory has them: `line` (a row of X,
-  // or a column where it is tall) and 8 places from `place`; n of them exist
+  // 8 elements of this CTA's columns as memory has them: `line` (a row of X, or a column
+  // where it is tall) and 8 places from `place`; n of them exist
   struct Piece {
     int64_t at;
     int line, place, n;
   };
-  auto piece = [&](int h, int it) {
+  constexpr int PIECES = kSide * SLAB / 8 / kThreads, BATCH = 4;
+  auto piece = [&](int it) {
     Piece p;
-    p.line = it * 16 + tid / 16;
-    p.place = tid % 16 * 8;
-    const int c = 128 * h + (tall ? p.line : p.place), row = tall ? p.place : p.line;
+    const int i = it * kThreads + tid;
     if (tall) {
-      p.n = c < cols ? min(8, r.m - row) : 0;
-      p.at = base + (int64_t)(col0 + c) * s.cols + row;
+      p.line = i / 16;
+      p.place = i % 16 * 8;
+      p.n = p.line < cols ? min(8, r.m - p.place) : 0;
+      p.at = base + (int64_t)(col0 + p.line) * s.cols + p.place;
     } else {
-      p.n = row < r.m ? min(8, cols - c) : 0;
-      p.at = base + (int64_t)row * s.cols + col0 + c;
+      p.line = i / (SLAB / 8);
+      p.place = i % (SLAB / 8) * 8;
+      p.n = p.line < r.m ? min(8, cols - p.place) : 0;
+      p.at = base + (int64_t)p.line * s.cols + col0 + p.place;
     }
     return p;
   };
-  auto place_of = [&](const Piece& p, int e) {
-    return tall ? square_at(part, p.place + e, p.line) : square_at(part, p.line, p.place + e);
+  auto to_square = [&](const Piece& p, const float* f) {
+    if (tall) {
+      const Places<SLAB, true> at(square, p.line, p.place);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) at[e] = f[e];
+    } else {
+      const Places<SLAB, false> at(square, p.line, p.place);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) at[e] = f[e];
+    }
   };
-  const int row = 32 * (warp & 3) + lane, half = warp >> 2;   // this thread's row; its MINE columns
+  auto from_square = [&](const Piece& p, float* f) {
+    if (tall) {
+      const Places<SLAB, true> at(square, p.line, p.place);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = at[e];
+    } else {
+      const Places<SLAB, false> at(square, p.line, p.place);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = at[e];
+    }
+  };
+  const int row = 32 * (warp & 3) + lane, part = warp >> 2;   // this thread's row, and MINE columns of it
   float x[MINE];
-  double square = 0.0;
+  float sum = 0.0f;
+  // where pieces are whole (or not there) and on 16-byte boundaries, a batch's reads go out
+  // together, before anything looks at their values
+  const bool small_g = s.gdtype == MOE_BF16, moves = s.momentum != nullptr;
+#pragma unroll 1
+  for (int i0 = 0; i0 < PIECES; i0 += BATCH) {
+    float g[BATCH][8], v[BATCH][8];
+    if (ok8) {
+      uint4 a[BATCH][2], c[BATCH][2];
 #pragma unroll
-  for (int h = 0; h < SLAB / 128; ++h) {
-    float u[8][8];
-    float sum = 0.0f;
-#pragma unroll
-    for (int it = 0; it < 8; ++it) {
-      const Piece p = piece(h, it);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) u[it][e] = 0.0f;
-      if (p.n > 0) {
-        const bool v8 = ok8 && p.n == 8;
-        float g[8];
-        read8(s.grad, s.gdtype, p.at, p.n, v8, g);
-        if (s.momentum != nullptr) {
-          float v[8];
-          read8(s.momentum, MOE_F32, p.at, p.n, v8, v);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            v[e] = fmaf(r.beta, v[e], r.rest * g[e]);
-            u[it][e] = e < p.n ? direction(r, g[e], v[e]) : 0.0f;
+      for (int i = 0; i < BATCH; ++i) {
+        const Piece p = piece(i0 + i);
+        a[i][0] = a[i][1] = c[i][0] = c[i][1] = make_uint4(0, 0, 0, 0);
+        if (p.n > 0) {
+          const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(s.grad) + p.at * (small_g ? 2 : 4));
+          a[i][0] = q[0];
+          if (!small_g) a[i][1] = q[1];
+          if (moves) {
+            c[i][0] = reinterpret_cast<const uint4*>(s.momentum + p.at)[0];
+            c[i][1] = reinterpret_cast<const uint4*>(s.momentum + p.at)[1];
           }
-          write8(s.momentum, MOE_F32, p.at, p.n, v8, v);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) u[it][e] = e < p.n ? g[e] : 0.0f;
         }
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        sum = fmaf(u[it][e], u[it][e], sum);
-        *place_of(p, e) = u[it][e];
+      for (int i = 0; i < BATCH; ++i) {
+        if (small_g) {
+          unpack16(a[i][0], g[i], (const bf16*)nullptr);
+        } else {
+          unpack16(a[i][0], g[i], (const float*)nullptr);
+          unpack16(a[i][1], g[i] + 4, (const float*)nullptr);
+        }
+        unpack16(c[i][0], v[i], (const float*)nullptr);
+        unpack16(c[i][1], v[i] + 4, (const float*)nullptr);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const Piece p = piece(i0 + i);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[i][e] = v[i][e] = 0.0f;
+        if (p.n > 0) {
+          read8(s.grad, s.gdtype, p.at, p.n, false, g[i]);
+          if (moves) read8(s.momentum, MOE_F32, p.at, p.n, false, v[i]);
+        }
       }
     }
-    // squares as in the general path: in fp32 over a warp, scaled where they leave the
-    // range, in fp64 beyond
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const Piece p = piece(i0 + i);    // (what is not there was read as zeros)
+      if (moves) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          v[i][e] = fmaf(r.beta, v[i][e], r.rest * g[i][e]);
+          g[i][e] = direction(r, g[i][e], v[i][e]);
+        }
+        if (p.n > 0) write8(s.momentum, MOE_F32, p.at, p.n, ok8, v[i]);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = fmaf(g[i][e], g[i][e], sum);
+      to_square(p, g[i]);
+    }
+  }
+  // squares as in the general path: in fp32 over a warp's elements, once more and scaled
+  // where they leave the range, in fp64 beyond
+  {
     auto over = [](float v) {
 #pragma unroll
       for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
       return v;
     };
-    auto squares = [&](float scale) {
+    auto scaled = [&](float scale) {
       float t = 0.0f;
-#pragma unroll
-      for (int it = 0; it < 8; ++it)
+      for (int i = 0; i < PIECES; ++i) {
+        float f[8];
+        from_square(piece(i), f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float v = u[it][e] * scale;
+          const float v = f[e] * scale;
           t = fmaf(v, v, t);
         }
-      return (double)over(t);
+      }
+      return over(t);
     };
-    double total = (double)over(sum);
-    if (!(total >= 1e-28)) total = squares(0x1p80f) * 0x1p-160;
-    else if (!(total <= 1e38)) total = squares(0x1p-96f) * 0x1p192;
-    square += total;
-    __syncthreads();
-    if (SLAB == 128 || half == h)
-#pragma unroll
-      for (int j = 0; j < MINE; ++j) x[j] = *square_at(part, row, (SLAB == 128 ? half * MINE : 0) + j);
-    __syncthreads();
+    float total = over(sum);
+    double unit = 1.0;
+    if (!(total >= 1e-28f)) {
+      total = scaled(0x1p80f);
+      unit = 0x1p-160;
+    } else if (!(total <= 1e38f)) {
+      total = scaled(0x1p-96f);
+      unit = 0x1p192;
+    }
+    if (lane == 0) sums[warp] = (double)total * unit;
   }
-  if (lane == 0) sums[warp] = square;
   __syncthreads();
-  if (tid == 0) {
-    double t = 0.0;
-    for (int w = 0; w < 8; ++w) t += sums[w];
-    sums[8] = t;
+#pragma unroll
+  for (int j = 0; j < MINE; ++j) x[j] = *square_at<SLAB>(square, row, part * MINE + j);
+  if (warp == 0) {
+    double t = lane < kWarps ? sums[lane] : 0.0;
+#pragma unroll
+    for (int o = kWarps / 2; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if (lane == 0) sums[kWarps] = t;
   }
   if (ctas > 1) cluster_sync();
   else __syncthreads();
-  {
+  if (warp == 0) {
     double t = 0.0;
-    for (int q = 0; q < ctas; ++q) {
-      double v;
-      asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(map_to_rank(smem_u32(sums + 8), (uint32_t)q)) : "memory");
-      t += v;
-    }
-    const float2 f = scale_of(t, r.eps);
+    if (lane < ctas)
+      asm volatile("ld.shared::cluster.f64 %0, [%1];"
+                   : "=d"(t)
+                   : "r"(map_to_rank(smem_u32(sums + kWarps), (uint32_t)lane))
+                   : "memory");
+#pragma unroll
+    for (int o = kMaxCluster / 2; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if (lane == 0) *factor = scale_of(t, r.eps);
+  }
+  __syncthreads();
+  {
+    const float2 f = *factor;
 #pragma unroll
     for (int j = 0; j < MINE; ++j) x[j] = x[j] * f.x * f.y;
   }
@@ -284,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
     for (int j = 0; j < MINE / 8; ++j) {
       uint4 v[PLANES];
       halves8<PLANES>(x + 8 * j, v);
-      const int c = half * MINE / 8 + j;
+      const int c = part * MINE / 8 + j;
 #pragma unroll
       for (int p = 0; p < PLANES; ++p) st4(op_at(xs + p * XP, c / 8, row, c % 8), v[p]);
     }
@@ -306,43 +395,64 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
           tc_mma(d_gram, sw128_desc(at + plane_a(i) * XP), sw128_desc(at + plane_b(i) * XP), idesc_of(128, false), more);
         }
     });
-    // row `row`, 64 columns, to the partial square in units of 16 bytes (turned by the row)
+    // row `row`, 32 columns, to the partial square in units of 16 bytes (turned by the row)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < 2; ++c) {
       uint32_t v[16];
-      tmem_ld16(d_gram + ((uint32_t)(32 * (warp & 3)) << 16) + half * 64 + 16 * c, v);
+      tmem_ld16(d_gram + ((uint32_t)(32 * (warp & 3)) << 16) + part * 32 + 16 * c, v);
       tmem_wait_ld();
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int unit = half * 16 + 4 * c + j;
+        const int unit = part * 8 + 4 * c + j;
         const uint4 w = blocks > 0 ? make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]) : make_uint4(0, 0, 0, 0);
         st4(ps + row * 512 + ((unit ^ (row & 31)) << 4), w);
       }
     }
     if (ctas > 1) cluster_sync();
     else __syncthreads();
-    // this CTA's rows of A: the partial squares in rank order, to every CTA
+    // This CTA's rows of A: the partial squares in rank order, to every CTA.  What goes
+    // between SMs takes the longest of a step (some 14 bytes a clock into an SM); with the units
+    // that reach the diagonal alone, and the other side filled in by each CTA, it took as long.
     {
-      const int share = (kSide + ctas - 1) / ctas, r0 = rank * share, r1 = min(kSide, r0 + share);
-      for (int it = r0 * 16 + tid; it < r1 * 16; it += kThreads) {
-        const int rr = it / 16, j = it % 16;       // 8 columns from 8 j
-        float f[8];
+      const int share = (kSide + ctas - 1) / ctas, r0 = rank * share, r1 = min(r.m, r0 + share);
+      for (int it = tid; it < (r1 - r0) * 32; it += kThreads) {
+        const int rr = r0 + it / 32, unit = it % 32;       // 4 columns
+        const uint32_t from = ps + rr * 512 + ((unit ^ (rr & 31)) << 4);
+        float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (ctas == 1) {
+          const uint4 u = ld4(from);
+          f[0] = __uint_as_float(u.x);
+          f[1] = __uint_as_float(u.y);
+          f[2] = __uint_as_float(u.z);
+          f[3] = __uint_as_float(u.w);
+        } else {
+          for (int q0 = 0; q0 < ctas; q0 += 8) {
+            float4 u[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = 0.0f;
-        for (int q = 0; q < ctas; ++q) {
-          const uint32_t from = map_to_rank(ps, (uint32_t)q) + rr * 512;
-          const float4 u = ld4_cluster(from + (((2 * j) ^ (rr & 31)) << 4)), v = ld4_cluster(from + (((2 * j + 1) ^ (rr & 31)) << 4));
-          f[0] += u.x; f[1] += u.y; f[2] += u.z; f[3] += u.w;
-          f[4] += v.x; f[5] += v.y; f[6] += v.z; f[7] += v.w;
+            for (int q = 0; q < 8; ++q)
+              u[q] = q0 + q < ctas ? ld4_cluster(map_to_rank(from, (uint32_t)(q0 + q))) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              f[0] += u[q].x; f[1] += u[q].y; f[2] += u[q].z; f[3] += u[q].w;
+            }
+          }
         }
+        uint32_t h[2], l[2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= 0x1p-15f;    // 2^(kOrthA - 2 kOrthX)
-        uint4 v[PLANES];
-        halves8<PLANES>(f, v);
-        for (int q = 0; q < ctas; ++q)
-#pragma unroll
-          for (int p = 0; p < PLANES; ++p)
-            st4_cluster(op_at(map_to_rank(as, (uint32_t)q) + p * kSquare, j / 8, rr, j % 8), v[p]);
+        for (int e = 0; e < 2; ++e) {
+          const float f0 = f[2 * e] * 0x1p-15f, f1 = f[2 * e + 1] * 0x1p-15f;    // 2^(kOrthA - 2 kOrthX)
+          const __half2 a = __floats2half2_rn(f0, f1);
+          const float2 lead = __half22float2(a);
+          const __half2 c = __floats2half2_rn(f0 - lead.x, f1 - lead.y);
+          h[e] = *reinterpret_cast<const uint32_t*>(&a);
+          l[e] = *reinterpret_cast<const uint32_t*>(&c);
+        }
+        const uint32_t to = op_at(as, unit / 16, rr, unit % 16 / 2) + (unit & 1) * 8;
+        for (int q = 0; q < ctas; ++q) {
+          const uint32_t at = map_to_rank(to, (uint32_t)q);
+          st2_cluster(at, h[0], h[1]);
+          if (PLANES == 2) st2_cluster(at + kSquare, l[0], l[1]);
+        }
       }
       proxy_fence();
     }
@@ -359,13 +469,13 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
     });
     const float kb = cb * 0.25f, kc = cc * 0x1p-13f;     // 2^(kOrthB - kOrthA), 2^(kOrthB - 2 kOrthA)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < 2; ++c) {
       uint32_t v[16];
-      tmem_ld16(d_poly + ((uint32_t)(32 * (warp & 3)) << 16) + half * 64 + 16 * c, v);
+      tmem_ld16(d_poly + ((uint32_t)(32 * (warp & 3)) << 16) + part * 32 + 16 * c, v);
       tmem_wait_ld();
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        const int j = half * 8 + 2 * c + g;
+        const int j = part * 4 + 2 * c + g;
         float f[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = 0.0f;
@@ -399,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
 #pragma unroll
     for (int c = 0; c < MINE / 16; ++c) {
       uint32_t v[16];
-      tmem_ld16(d_apply + ((uint32_t)(32 * (warp & 3)) << 16) + half * MINE + 16 * c, v);
+      tmem_ld16(d_apply + ((uint32_t)(32 * (warp & 3)) << 16) + part * MINE + 16 * c, v);
       tmem_wait_ld();
 #pragma unroll
       for (int e = 0; e < 16; ++e) x[16 * c + e] = fmaf(0x1p-9f, __uint_as_float(v[e]), ca * x[16 * c + e]);
@@ -408,29 +518,55 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
   }
   static_assert(kOrthX == 13 && kOrthA == 11 && kOrthB == 9, "the powers of two above");
 
-  // the update, through the square again
+  // the update, through the square again (the last product has read X's planes)
+  __syncthreads();
 #pragma unroll
-  for (int h = 0; h < SLAB / 128; ++h) {
-    __syncthreads();
-    if (SLAB == 128 || half == h)
+  for (int j = 0; j < MINE; ++j) *square_at<SLAB>(square, row, part * MINE + j) = x[j] * 0x1p-13f;
+  __syncthreads();
+#pragma unroll 1
+  for (int i0 = 0; i0 < PIECES; i0 += BATCH) {
+    float w[BATCH][8];
+    if (ok8) {
+      const bool small_w = s.pdtype == MOE_BF16;
+      uint4 a[BATCH][2];
 #pragma unroll
-      for (int j = 0; j < MINE; ++j) *square_at(part, row, (SLAB == 128 ? half * MINE : 0) + j) = x[j] * 0x1p-13f;
-    __syncthreads();
-#pragma unroll
-    for (int it = 0; it < 8; ++it) {
-      const Piece p = piece(h, it);
-      if (p.n <= 0) continue;
-      const bool v8 = ok8 && p.n == 8;
-      float f[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = *place_of(p, e);
-      if (r.update) {
-        float w[8];
-        read8(s.param, s.pdtype, p.at, p.n, v8, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = fmaf(-s.size, f[e], r.keep * w[e]);
+      for (int i = 0; i < BATCH; ++i) {
+        const Piece p = piece(i0 + i);
+        a[i][0] = a[i][1] = make_uint4(0, 0, 0, 0);
+        if (p.n > 0 && r.update) {
+          const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(s.param) + p.at * (small_w ? 2 : 4));
+          a[i][0] = q[0];
+          if (!small_w) a[i][1] = q[1];
+        }
       }
-      write8(s.param, s.pdtype, p.at, p.n, v8, f);
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        if (small_w) {
+          unpack16(a[i][0], w[i], (const bf16*)nullptr);
+        } else {
+          unpack16(a[i][0], w[i], (const float*)nullptr);
+          unpack16(a[i][1], w[i] + 4, (const float*)nullptr);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const Piece p = piece(i0 + i);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[i][e] = 0.0f;
+        if (p.n > 0 && r.update) read8(s.param, s.pdtype, p.at, p.n, false, w[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const Piece p = piece(i0 + i);
+      if (p.n <= 0) continue;
+      float f[8];
+      from_square(p, f);
+      if (r.update)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = fmaf(-s.size, f[e], r.keep * w[i][e]);
+      write8(s.param, s.pdtype, p.at, p.n, ok8, f);
     }
   }
   if (!good) {

@@ -127,6 +127,7 @@ __device__ __forceinline__ void put8(const Round& r, int64_t at, const float* f)
     *reinterpret_cast<uint2*>(reinterpret_cast<char*>(r.x + plane) + at) = make_uint2(l[0], l[1]);
   }
 }
+// 8 values of the last X (which has no 8-bit parts: no step is left to need them).
 __device__ __forceinline__ void get8(const Round& r, int64_t at, float* f) {
   const uint4 hi = *reinterpret_cast<const uint4*>(r.x + at);
   const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w};
@@ -146,11 +147,6 @@ __device__ __forceinline__ void get8(const Round& r, int64_t at, float* f) {
       f[2 * i] += b.x;
       f[2 * i + 1] += b.y;
     }
-  } else {
-    const uint2 lo = *reinterpret_cast<const uint2*>(reinterpret_cast<const char*>(r.x + plane) + at);
-    const uint32_t l[2] = {lo.x, lo.y};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = orth_with_low(f[i], (int)(int8_t)((l[i / 4] >> (i % 4 * 8)) & 255u));
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) f[i] *= 0x1p-13f;

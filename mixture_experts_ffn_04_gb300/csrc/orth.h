@@ -54,7 +54,7 @@ __device__ __forceinline__ float orth_with_low(float h, int low) {
 #endif
 
 // `steps` times X <- a X + (b A + c A A) X with (a, b, c) = coef[i], from x[0]; the
-// last X is in x[steps & 1].
+// last X is in x[steps & 1], of bf16 matrices without 8-bit parts.
 cudaError_t launch_orth_steps(const OrthBatch& t, int steps, const double (*coef)[3], cudaStream_t st);
 
 }  // namespace moe

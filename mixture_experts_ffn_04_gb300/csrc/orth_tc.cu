@@ -14,10 +14,11 @@
 // matrix of rank 10 with a floor of 1e-2 (bf16 operands throughout: 0.29), in two planes
 // 3.0e-4; normal entries 1.6e-3 (the polynomial in the rounded A, which b A takes from
 // the same plane as A A: with b A exact instead 2.8e-3).  fp32 matrices take three
-// products of two planes each, smallest first: 5.7e-7 (fp32 products: 7.2e-6).
+// products of two planes each, smallest first: 5.7e-7 (fp32 products: 7.2e-6), from stages with
+// both planes of both operands.
 //
 // A pair of SMs computes 256 x 256 tiles over 64-wide k-blocks through six 32 KB
-// stages.  Addend and result go between registers and memory as whole 128-byte rows, turned
+// stages (three of 64 KB).  Addend and result go between registers and memory as whole 128-byte rows, turned
 // in a 4 KB slice of each epilogue warp between that layout and the one of TMEM (a lane a
 // row), the addend asked for a tile ahead.  By TMA boxes both stood in the TMA queue behind
 // the operands of more than a tile: at m = 704, whose tiles have 11 k-blocks, 2800 of a
@@ -32,6 +33,7 @@
 // step); with operands of 11 bits it would not show.  Every wait on an mbarrier is bounded,
 // and a CTA that gives up waits, with a limit, for its copies and MMAs in flight.
 #include <atomic>
+#include <cmath>
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -52,11 +54,10 @@ namespace orth {
 using namespace tc;
 
 constexpr int BM = 256, BN = 256, BMC = BM / 2, BNC = BN / 2, BK = 64;
-constexpr int S = 6;
-constexpr int A_BYTES = BMC * BK * 2, B_BYTES = BNC * BK * 2;
-constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int A_BYTES = BMC * BK * 2, B_BYTES = BNC * BK * 2;   // of a plane
 constexpr int BOX_BYTES = 64 * BK * 2;
-constexpr int RING_BYTES = S * STAGE_BYTES;
+constexpr int RING_BYTES = 6 * (A_BYTES + B_BYTES);              // six stages of a plane, three of two
+constexpr int MAX_STAGES = 6;
 constexpr int EPI_WARPS = 8, EPI_COLS = 128;   // a warp: 32 rows, 128 columns
 constexpr int THREADS = 32 * (4 + EPI_WARPS);
 // 168 registers a thread at launch; 56 + 2 * 224 <= 3 * 168 (three groups of 4 warps)
@@ -67,9 +68,9 @@ constexpr int BAR_BYTES = 256;
 constexpr int STAGE_WARP = 4096;   // an epilogue warp's slice: 32 rows of 128 bytes
 constexpr int SMEM_BYTES = 1024 + RING_BYTES + EPI_WARPS * STAGE_WARP + BAR_BYTES;
 static_assert(SMEM_BYTES <= 232448, "shared memory budget of one CTA");
-static_assert((2 * S + 5) * 8 + 8 <= BAR_BYTES, "barrier area");
+static_assert((2 * MAX_STAGES + 5) * 8 + 8 <= BAR_BYTES, "barrier area");
 constexpr long long kDrainCycles = 1 << 21;
-constexpr int kChunkExact = 8;   // k-blocks of 64
+constexpr int kChunkExact = 3;   // k-blocks of 64, three products each
 
 // kind::f16: D fp32, A and B fp16, M = 256 over the pair, N = 256.
 constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
@@ -94,24 +95,50 @@ struct Args {
 struct Tile {
   int b, i, j;
 };
+// A pair's tiles: every `step`th of all matrices' tiles, from its own.  Divisions by the
+// number of tiles of a matrix are done once.
 template <int KIND>
-__device__ __forceinline__ Tile decode(const Args& a, uint32_t t) {
-  Tile r;
-  r.b = (int)(t / (uint32_t)a.per);
-  uint32_t l = t - (uint32_t)r.b * (uint32_t)a.per;
-  if (KIND == kApply) {
-    r.j = (int)(l / (uint32_t)a.mt);
-    r.i = (int)(l - (uint32_t)r.j * (uint32_t)a.mt);
-  } else {
-    // row i of the lower triangle starts at i (i + 1) / 2
-    int i = (int)((sqrtf(8.0f * (float)l + 1.0f) - 1.0f) * 0.5f);
-    while ((uint32_t)i * (i + 1) / 2 > l) --i;
-    while ((uint32_t)(i + 1) * (i + 2) / 2 <= l) ++i;
-    r.i = i;
-    r.j = (int)(l - (uint32_t)i * (i + 1) / 2);
+struct Walk {
+  uint32_t t, l, b;             // tile; place in its matrix; matrix
+  uint32_t step, step_l, step_b;
+  float inv;                    // of the row tiles
+  __device__ __forceinline__ Walk(const Args& a, uint32_t first, uint32_t step_) : t(first), step(step_) {
+    b = first / (uint32_t)a.per;
+    l = first - b * (uint32_t)a.per;
+    step_b = step_ / (uint32_t)a.per;
+    step_l = step_ - step_b * (uint32_t)a.per;
+    inv = 1.0f / (float)a.mt;
   }
-  return r;
-}
+  __device__ __forceinline__ void next(const Args& a) {
+    t += step;
+    l += step_l;
+    b += step_b;
+    if (l >= (uint32_t)a.per) {
+      l -= (uint32_t)a.per;
+      ++b;
+    }
+  }
+  __device__ __forceinline__ Tile tile(const Args& a) const {
+    Tile r;
+    r.b = (int)b;
+    if (KIND == kApply) {
+      int j = (int)((float)l * inv);      // within one of l / mt
+      int i = (int)l - j * a.mt;
+      if (i < 0) { --j; i += a.mt; }
+      if (i >= a.mt) { ++j; i -= a.mt; }
+      r.i = i;
+      r.j = j;
+    } else {
+      // row i of the lower triangle starts at i (i + 1) / 2
+      int i = (int)((sqrtf(8.0f * (float)l + 1.0f) - 1.0f) * 0.5f);
+      while ((uint32_t)i * (i + 1) / 2 > l) --i;
+      while ((uint32_t)(i + 1) * (i + 2) / 2 <= l) ++i;
+      r.i = i;
+      r.j = (int)(l - (uint32_t)i * (i + 1) / 2);
+    }
+    return r;
+  }
+};
 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   const __half2 p = __floats2half2_rn(lo, hi);
@@ -185,9 +212,9 @@ __device__ __forceinline__ void mirror_rows(uint32_t stage, const uint32_t (&w)[
   __syncwarp();
 }
 
-// How X' and the addend are held: kOne: one fp16 plane (A, B); kTwo: two; kLow: one
-// and the 8-bit part (X of bf16 matrices).
-enum Form { kOne = 0, kTwo = 1, kLow = 2 };
+// How addend and result are held: kOne: one fp16 plane; kTwo: two; kLow: one and the 8-bit
+// part (X of bf16 matrices); kLowIn: the addend so, the result in one plane.
+enum Form { kOne = 0, kTwo = 1, kLow = 2, kLowIn = 3 };
 
 // Operand maps are 3-D, {columns, rows, plane * batch + matrix}: boxes of 64 columns by
 // 128 rows, kApply's B operand 64 by 64 in its stored layout.
@@ -197,6 +224,9 @@ struct Maps {
 
 template <int KIND, int FORM>
 __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant__ Maps maps, const Args a) {
+  // two planes: a stage has both of both operands, for the three products
+  constexpr int PL = FORM == kTwo ? 2 : 1, S = MAX_STAGES / PL, STAGE_BYTES = PL * (A_BYTES + B_BYTES);
+  constexpr bool LOW_IN = FORM == kLow || FORM == kLowIn, LOW_OUT = FORM == kLow;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -244,8 +274,7 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
   const uint32_t tmem_base = *tmem_slot;
   pdl_wait();
   const uint32_t total = (uint32_t)a.per * (uint32_t)a.batch, first = blockIdx.x >> 1, step = gridDim.x >> 1;
-  const int nprod = a.planes == 2 ? 3 : 1;
-  const int steps = a.kb * nprod;   // k-blocks of a tile
+  const int steps = a.kb;   // k-blocks of a tile
   const int chunk = FORM == kTwo ? kChunkExact : steps;
 
   if (warp < 4) {
@@ -256,27 +285,26 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
       uint32_t ph = 0, issued = 0;
       bool ok = true;
       const uint32_t full0 = map_to_rank(full(0), 0);   // the even CTA's "full" barriers
-      for (uint32_t t = first; ok && t < total; t += step) {
-        const Tile q = decode<KIND>(a, t);
+      for (Walk<KIND> walk(a, first, step); ok && walk.t < total; walk.next(a)) {
+        const Tile q = walk.tile(a);
         const int arow = q.i * BM + (int)rank * BMC, bcol = q.j * BN + (int)rank * BNC;
-        for (int p = 0; p < nprod && ok; ++p) {
-          // the products of planes (1, 0), (0, 1), (0, 0)
-          const int pa = nprod == 3 && p == 0, pb = nprod == 3 && p == 1;
-          const int za = pa * a.batch + q.b, zb = pb * a.batch + q.b;
-          for (int k = 0; k < a.kb * BK; k += BK) {
-            if (!wait_cl(empty(s), ph ^ 1u, abort_flag)) { ok = false; break; }
-            const uint32_t sa = ring + s * STAGE_BYTES, sb = sa + A_BYTES, fb = full0 + 8u * s;
-            if (leader) mbar_expect_tx(full(s), 2 * STAGE_BYTES);
-            tma_load_3d_pair(sa, &maps.A, k, arow, za, fb);
+        for (int k = 0; k < a.kb * BK; k += BK) {
+          if (!wait_cl(empty(s), ph ^ 1u, abort_flag)) { ok = false; break; }
+          const uint32_t sa = ring + s * STAGE_BYTES, sb = sa + PL * A_BYTES, fb = full0 + 8u * s;
+          if (leader) mbar_expect_tx(full(s), 2 * STAGE_BYTES);
+#pragma unroll
+          for (int p = 0; p < PL; ++p) {
+            const int z = p * a.batch + q.b;
+            tma_load_3d_pair(sa + p * A_BYTES, &maps.A, k, arow, z, fb);
             if (KIND == kApply) {
-              tma_load_3d_pair(sb, &maps.B, bcol, k, zb, fb);
-              tma_load_3d_pair(sb + BOX_BYTES, &maps.B, bcol + 64, k, zb, fb);
+              tma_load_3d_pair(sb + p * B_BYTES, &maps.B, bcol, k, z, fb);
+              tma_load_3d_pair(sb + p * B_BYTES + BOX_BYTES, &maps.B, bcol + 64, k, z, fb);
             } else {
-              tma_load_3d_pair(sb, &maps.B, k, bcol, zb, fb);
+              tma_load_3d_pair(sb + p * B_BYTES, &maps.B, k, bcol, z, fb);
             }
-            ++issued;
-            if (++s == S) { s = 0; ph ^= 1u; }
           }
+          ++issued;
+          if (++s == S) { s = 0; ph ^= 1u; }
         }
       }
       if (*abort_flag) {
@@ -305,11 +333,16 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
           for (int i = i0; i < i1; ++i) {
             if (!wait_cl(full(s), ph, abort_flag)) { ok = false; break; }
             tc_fence_after();
-            const uint32_t sa = ring + s * STAGE_BYTES, sb = sa + A_BYTES;
+            const uint32_t sa = ring + s * STAGE_BYTES, sb = sa + PL * A_BYTES;
+            // two planes: (1, 0), (0, 1), (0, 0)
 #pragma unroll
-            for (int kk = 0; kk < BK / 16; ++kk) {
-              const uint64_t bd = KIND == kApply ? mn_desc(sb + kk * 2048) : sw128_desc(sb + kk * 32);
-              mma2(d, sw128_desc(sa + kk * 32), bd, idesc, (i != i0 || kk != 0) ? 1u : 0u);
+            for (int p = 0; p < (PL == 2 ? 3 : 1); ++p) {
+              const uint32_t oa = sa + (PL == 2 && p == 0 ? A_BYTES : 0), ob = sb + (PL == 2 && p == 1 ? B_BYTES : 0);
+#pragma unroll
+              for (int kk = 0; kk < BK / 16; ++kk) {
+                const uint64_t bd = KIND == kApply ? mn_desc(ob + kk * 2048) : sw128_desc(ob + kk * 32);
+                mma2(d, sw128_desc(oa + kk * 32), bd, idesc, (i != i0 || p != 0 || kk != 0) ? 1u : 0u);
+              }
             }
             commit2_both(empty(s));
             if (++s == S) { s = 0; ph ^= 1u; }
@@ -378,22 +411,24 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
                      lane);
       };
       auto ask_lo = [&](const Part& p) {
-        if (FORM == kLow) load_block(lo, a.add_low + p.row * a.low_ld + p.n0, a.low_ld, p.rows, lane);
+        if (LOW_IN) load_block(lo, a.add_low + p.row * a.low_ld + p.n0, a.low_ld, p.rows, lane);
       };
-      Tile d = decode<KIND>(a, first), dn = d;
+      Walk<KIND> walk(a, first, step);
+      Tile d = walk.tile(a), dn = d;
       Part p = part_of(d), pn = p;
       ask_lo(p);
       ask_hi(p, 0);
       ask_hi(p, 1);
       for (uint32_t t = first; t < total; t += step, d = dn, p = pn) {
-        if (t + step < total) {
-          dn = decode<KIND>(a, t + step);
+        walk.next(a);
+        if (walk.t < total) {
+          dn = walk.tile(a);
           pn = part_of(dn);
         } else {
           pn.rows = 0;     // nothing more to ask for
         }
-        uint32_t low[FORM == kLow ? 32 : 1];     // this lane's 128 8-bit parts
-        if (FORM == kLow) {
+        uint32_t low[LOW_IN ? 32 : 1];     // this lane's 128 8-bit parts
+        if (LOW_IN) {
           block_to_slice(lo, stage, lane);
           ask_lo(pn);
 #pragma unroll
@@ -433,7 +468,7 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
                 float f1 = a.mul * __uint_as_float(r[k & 1][8 * g + 2 * e + 1]);
                 if (KIND != kGram) {
                   float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h4[e]));
-                  if (FORM == kLow) {
+                  if (LOW_IN) {
                     const uint32_t q2 = low[16 * h + 4 * c + 2 * g + e / 2] >> (e % 2 * 16);
                     x.x = orth_with_low(x.x, (int)(int8_t)(q2 & 255u));
                     x.y = orth_with_low(x.y, (int)(int8_t)((q2 >> 8) & 255u));
@@ -443,7 +478,7 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
                 }
                 const uint32_t v = pack_half2(f0, f1);
                 w[8 * c + 4 * g + e] = v;
-                if (FORM == kLow) {
+                if (LOW_OUT) {
                   const float2 lead = __half22float2(*reinterpret_cast<const __half2*>(&v));
                   steps8[2 * e] = orth_low_steps(f0, lead.x);
                   steps8[2 * e + 1] = orth_low_steps(f1, lead.y);
@@ -451,7 +486,7 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
               }
               const uint32_t* v = w + 8 * c + 4 * g;
               put_piece(stage, lane, 2 * c + g, make_uint4(v[0], v[1], v[2], v[3]));
-              if (FORM == kLow) {
+              if (LOW_OUT) {
                 // the parts replace the addend's
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
@@ -465,7 +500,7 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
           slice_to_rows(stage, a.out + p.row * a.add_ld + 2 * col, a.add_ld, rows, lane);
           if (KIND != kApply && d.i != d.j && rows > 0) mirror(a.out, d, p, col, w);
         }
-        if (FORM == kLow) {
+        if (LOW_OUT) {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             put_piece(stage, lane, j, make_uint4(low[4 * j], low[4 * j + 1], low[4 * j + 2], low[4 * j + 3]));
@@ -473,8 +508,8 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
         }
       }
     } else {
-      for (uint32_t t = first; ok && t < total; t += step) {
-        const Tile d = decode<KIND>(a, t);
+      for (Walk<KIND> walk(a, first, step); ok && walk.t < total; walk.next(a)) {
+        const Tile d = walk.tile(a);
         const Part p = part_of(d);
         float f[EPI_COLS];
 #pragma unroll
@@ -591,9 +626,10 @@ static cudaError_t prepare_device(int* clusters) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (g_clusters[dev] == 0) {
-    const void* fn[6] = {(const void*)orth_kernel<kGram, kOne>,  (const void*)orth_kernel<kGram, kTwo>,
+    const void* fn[8] = {(const void*)orth_kernel<kGram, kOne>,  (const void*)orth_kernel<kGram, kTwo>,
                          (const void*)orth_kernel<kPoly, kOne>,  (const void*)orth_kernel<kPoly, kTwo>,
-                         (const void*)orth_kernel<kApply, kLow>, (const void*)orth_kernel<kApply, kTwo>};
+                         (const void*)orth_kernel<kApply, kLow>, (const void*)orth_kernel<kApply, kLowIn>,
+                         (const void*)orth_kernel<kApply, kOne>, (const void*)orth_kernel<kApply, kTwo>};
     int least = 1 << 30;
     for (const void* f : fn) {
       e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
@@ -662,6 +698,7 @@ cudaError_t launch_orth_steps(const OrthBatch& t, int steps, const double (*coef
   g.nt = (t.n + BN - 1) / BN;
   const int64_t rows = B * t.m, a_ld = (int64_t)t.lda * 2, x_ld = (int64_t)t.ldx * 2;
   char *pa = static_cast<char*>(t.a), *pb = static_cast<char*>(t.b);
+  bool low = true;     // x[0] has its 8-bit parts
   for (int i = 0; i < steps; ++i) {
     char *from = static_cast<char*>(t.x[i & 1]), *to = static_cast<char*>(t.x[(i & 1) ^ 1]);
     // A = X X^T
@@ -693,8 +730,18 @@ cudaError_t launch_orth_steps(const OrthBatch& t, int steps, const double (*coef
     g.add_low = from + rows * x_ld;
     g.out = to;
     g.out_low = to + rows * x_ld;
-    e = two ? launch<kApply, kTwo>(apply[i & 1], g, st) : launch<kApply, kLow>(apply[i & 1], g, st);
+    // What the steps to come multiply an error outside X's rows and columns by: up to 4, 11
+    // bits do (simulated as above, the last two X without their parts: 1.6e-3 again for
+    // normal entries, rank 16 1.0e-3 instead of 4.3e-4; the last three: rank 16 2.5e-3).
+    double grows = 1.0;
+    for (int k = i + 1; k < steps; ++k) grows *= fabs(coef[k][0]);
+    const bool keep = grows > 4.0;
+    if (two) e = launch<kApply, kTwo>(apply[i & 1], g, st);
+    else if (keep && low) e = launch<kApply, kLow>(apply[i & 1], g, st);
+    else if (low) e = launch<kApply, kLowIn>(apply[i & 1], g, st);
+    else e = launch<kApply, kOne>(apply[i & 1], g, st);
     if (e != cudaSuccess) return e;
+    low = low && keep;
   }
   return cudaSuccess;
 }

@@ -38,34 +38,58 @@ __global__ void __launch_bounds__(256) momentum_kernel(const __grid_constant__ R
     const int64_t each = (int64_t)s.rows * s.cols;
     const int64_t base = (s.first + (b - s.at)) * each;      // the matrix in its tensor
     const bool ok = each % 8 == 0 && aligned(s.grad) && aligned(s.momentum);
-    float u[kPart / 256 / 8][8];
+    constexpr int PIECES = kPart / 256 / 8;
+    float u[PIECES][8];
     float sum = 0.0f;
+    auto at_of = [&](int k) { return (int64_t)part * kPart + (k * 256 + threadIdx.x) * 8; };
+    if (ok) {
+      Raw8 g[PIECES], v[PIECES];
 #pragma unroll
-    for (int k = 0; k < kPart / 256 / 8; ++k) {
-      const int64_t at = (int64_t)part * kPart + (k * 256 + threadIdx.x) * 8;
-      const int n = at >= each ? 0 : (each - at < 8 ? (int)(each - at) : 8);
-      float g[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) u[k][e] = 0.0f;
-      if (n > 0) {
-        read8(s.grad, s.gdtype, base + at, n, ok, g);
-        if (s.momentum != nullptr) {
-          float v[8];
-          read8(s.momentum, MOE_F32, base + at, n, ok, v);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            v[e] = fmaf(r.beta, v[e], r.rest * g[e]);
-            u[k][e] = e < n ? direction(r, g[e], v[e]) : 0.0f;
-          }
-          write8(s.momentum, MOE_F32, base + at, n, ok, v);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) u[k][e] = g[e];
-        }
+      for (int k = 0; k < PIECES; ++k) {
+        const int64_t at = at_of(k);
+        g[k] = load_raw(s.grad, s.gdtype, base + at, at < each);
+        v[k] = load_raw(s.momentum, MOE_F32, base + at, at < each && s.momentum != nullptr);
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum = fmaf(u[k][e], u[k][e], sum);
+      for (int k = 0; k < PIECES; ++k) {
+        const int64_t at = at_of(k);
+        open_raw(g[k], s.gdtype, u[k]);
+        if (s.momentum != nullptr) {
+          float m[8];
+          open_raw(v[k], MOE_F32, m);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            m[e] = fmaf(r.beta, m[e], r.rest * u[k][e]);
+            u[k][e] = direction(r, u[k][e], m[e]);
+          }
+          if (at < each) write8(s.momentum, MOE_F32, base + at, 8, true, m);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < PIECES; ++k) {
+        const int64_t at = at_of(k);
+        const int n = at >= each ? 0 : (each - at < 8 ? (int)(each - at) : 8);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[k][e] = 0.0f;
+        if (n <= 0) continue;
+        read8(s.grad, s.gdtype, base + at, n, false, u[k]);
+        if (s.momentum != nullptr) {
+          float m[8];
+          read8(s.momentum, MOE_F32, base + at, n, false, m);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            m[e] = fmaf(r.beta, m[e], r.rest * u[k][e]);
+            u[k][e] = e < n ? direction(r, u[k][e], m[e]) : 0.0f;
+          }
+          write8(s.momentum, MOE_F32, base + at, n, false, m);
+        }
+      }
     }
+#pragma unroll
+    for (int k = 0; k < PIECES; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = fmaf(u[k][e], u[k][e], sum);
     auto all = [](float v) {
 #pragma unroll
       for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -207,30 +231,42 @@ __global__ void __launch_bounds__(256) planes_kernel(const __grid_constant__ Rou
     const bool ok = s->cols % 8 == 0 && aligned(s->grad) && aligned(s->momentum);
     const int64_t x = (int64_t)t.b * r.m * r.ldx;   // of the matrix in the planes
     if (tall) __syncthreads();   // the last tile's readers are done
+    Raw8 g[2], v[2];
+    if (ok)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int row = t.r0 + k * 32 + tid / 8, col = t.c0 + tid % 8 * 8;
+        const bool there = row < s->rows && col < s->cols;
+        const int64_t at = base + (int64_t)row * s->cols + col;
+        g[k] = load_raw(s->grad, s->gdtype, at, there);
+        v[k] = load_raw(s->momentum, MOE_F32, at, there && s->momentum != nullptr);
+      }
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int lr = k * 32 + tid / 8, lc = tid % 8 * 8;
       const int row = t.r0 + lr, col = t.c0 + lc;
       const int n = row >= s->rows || col >= s->cols ? 0 : min(8, s->cols - col);
-      float f[8];
+      float f[8], m[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = 0.0f;
-      if (n > 0) {
+      for (int e = 0; e < 8; ++e) f[e] = m[e] = 0.0f;
+      if (ok) {
+        open_raw(g[k], s->gdtype, f);
+        open_raw(v[k], MOE_F32, m);
+      } else if (n > 0) {
         const int64_t at = base + (int64_t)row * s->cols + col;
-        read8(s->grad, s->gdtype, at, n, ok, f);
-        if (s->momentum != nullptr) {
-          float v[8];
-          read8(s->momentum, MOE_F32, at, n, ok, v);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = direction(r, f[e], v[e]);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = e < n ? f[e] * q.x * q.y : 0.0f;
-        if (!tall) put8(r, x + (int64_t)row * r.ldx + col, f);
+        read8(s->grad, s->gdtype, at, n, false, f);
+        if (s->momentum != nullptr) read8(s->momentum, MOE_F32, at, n, false, m);
       }
-      if (tall) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sh[lr][lc + e] = f[e];
+      for (int e = 0; e < 8; ++e) {
+        if (s->momentum != nullptr) f[e] = direction(r, f[e], m[e]);
+        f[e] = f[e] * q.x * q.y;
+      }
+      if (!tall) {
+        if (n > 0) put8(r, x + (int64_t)row * r.ldx + col, f);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sh[lr][lc + e] = e < n ? f[e] : 0.0f;
       }
     }
     if (!tall) continue;
@@ -260,23 +296,29 @@ __global__ void __launch_bounds__(256) update_kernel(const __grid_constant__ Rou
     const TileAt t = tile_at(r, task, s);
     const bool tall = s->rows > s->cols;
     const int64_t base = (s->first + (t.b - s->at)) * (int64_t)s->rows * s->cols;
-    const bool ok = s->cols % 8 == 0 && aligned(s->param);
+    const bool ok = s->cols % 8 == 0 && aligned(s->param);   // pieces are whole and on 16-byte boundaries
     const int64_t x = (int64_t)t.b * r.m * r.ldx;
-    if (tall) {
-      __syncthreads();
+    // everything that is read first
+    Raw8 w[2];
+    float f[2][8];
+    if (r.update && ok)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int lr = k * 32 + tid / 8, lc = tid % 8 * 8;
-        const int row = t.c0 + lr, col = t.r0 + lc;
-        if (row < r.m && col < r.n) {
-          float f[8];
-          get8(r, x + (int64_t)row * r.ldx + col, f);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) sh[lc + e][lr] = f[e];
-        }
+        const int row = t.r0 + k * 32 + tid / 8, col = t.c0 + tid % 8 * 8;
+        w[k] = load_raw(s->param, s->pdtype, base + (int64_t)row * s->cols + col, row < s->rows && col < s->cols);
       }
-      __syncthreads();
+    if (tall) __syncthreads();   // the last tile's readers are done
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int lr = k * 32 + tid / 8, lc = tid % 8 * 8;
+      const int row = (tall ? t.c0 : t.r0) + lr, col = (tall ? t.r0 : t.c0) + lc;
+      if (row >= r.m || col >= r.n) continue;
+      get8(r, x + (int64_t)row * r.ldx + col, f[k]);
+      if (tall)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sh[lc + e][lr] = f[k][e];
     }
+    if (tall) __syncthreads();
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int lr = k * 32 + tid / 8, lc = tid % 8 * 8;
@@ -284,20 +326,18 @@ __global__ void __launch_bounds__(256) update_kernel(const __grid_constant__ Rou
       const int n = row >= s->rows || col >= s->cols ? 0 : min(8, s->cols - col);
       if (n <= 0) continue;
       const int64_t at = base + (int64_t)row * s->cols + col;
-      float f[8];
       if (tall) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = e < n ? sh[lr][lc + e] : 0.0f;
-      } else {
-        get8(r, x + (int64_t)row * r.ldx + col, f);
+        for (int e = 0; e < 8; ++e) f[k][e] = e < n ? sh[lr][lc + e] : 0.0f;
       }
       if (r.update) {
-        float w[8];
-        read8(s->param, s->pdtype, at, n, ok, w);
+        float p[8];
+        if (ok) open_raw(w[k], s->pdtype, p);
+        else read8(s->param, s->pdtype, at, n, false, p);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = fmaf(-s->size, f[e], r.keep * w[e]);
+        for (int e = 0; e < 8; ++e) f[k][e] = fmaf(-s->size, f[k][e], r.keep * p[e]);
       }
-      write8(s->param, s->pdtype, at, n, ok, f);
+      write8(s->param, s->pdtype, at, n, ok, f[k]);
     }
   }
 }

@@ -67,6 +67,29 @@ __device__ __forceinline__ void read8(const void* p, int dtype, int64_t at, int 
     }
   }
 }
+// 8 whole elements on a 16-byte boundary as memory has them, and as floats: several reads go
+// out before the first value is looked at.
+struct Raw8 {
+  uint4 v[2];
+};
+__device__ __forceinline__ Raw8 load_raw(const void* p, int dtype, int64_t at, bool there) {
+  Raw8 r;
+  r.v[0] = r.v[1] = make_uint4(0, 0, 0, 0);
+  if (there) {
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + at * (dtype == MOE_F32 ? 4 : 2));
+    r.v[0] = q[0];
+    if (dtype == MOE_F32) r.v[1] = q[1];
+  }
+  return r;
+}
+__device__ __forceinline__ void open_raw(const Raw8& r, int dtype, float* f) {
+  if (dtype == MOE_F32) {
+    unpack16(r.v[0], f, (const float*)nullptr);
+    unpack16(r.v[1], f + 4, (const float*)nullptr);
+  } else {
+    unpack16(r.v[0], f, (const bf16*)nullptr);
+  }
+}
 __device__ __forceinline__ void write8(void* p, int dtype, int64_t at, int n, bool vec, const float* f) {
   if (dtype == MOE_F32) {
     float* q = static_cast<float*>(p) + at;

@@ -256,64 +256,67 @@ struct Team {
     if (G == 32) __syncwarp();
     else asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(G) : "memory");
   }
-  // Sums over a row's threads; red: [2][N][warps] of the team.
-  template <int N>
-  __device__ __forceinline__ void sum(float (&v)[N], float* red, int& slot) const {
+  // Sums over a row's threads; red: two values a warp of the block, 32 apart.
+  __device__ __forceinline__ float sum(float v, float* red, int& slot) const {
     const int span = Gs < 32 ? Gs : 32;
-    for (int o = span >> 1; o; o >>= 1)
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-    if (Gs <= 32) return;
-    float* r = red + slot * N * 32;
-    if ((tt & 31) == 0)
-#pragma unroll
-      for (int i = 0; i < N; ++i) r[i * 32 + (tt >> 5)] = v[i];
-    sync();
+    for (int o = span >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (Gs <= 32) return v;
     const int lane32 = tt & 31, warps = G >> 5;
+    float* r = red + slot * 32 + g * warps;
+    if (lane32 == 0) r[tt >> 5] = v;
+    sync();
+    v = lane32 < warps ? r[lane32] : 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = lane32 < warps ? r[i * 32 + lane32] : 0.0f;
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     slot ^= 1;
+    return v;
   }
 };
 
 // What y and s are multiplied by, to shared memory in fp32: w1 = (w_post + o) g of a
-// channel gate, w2 = w_pre + o (opened and combined once instead of in every row).
+// channel gate, w2 = w_pre + o (opened and combined once instead of in every row).  Of
+// each eight columns the first four stand in the first half and the others in the second:
+// a thread's eight side by side would put two of every eight lanes in the same banks.
 template <typename T>
 __device__ __forceinline__ void stage_weights(float* w1, float* w2, const T* w_post, const T* gate, const T* w_pre,
                                               float off, int H) {
-  for (int c = threadIdx.x; c < H; c += blockDim.x) {
-    const float g = gate ? to_f(gate[c]) : 1.0f;
-    w1[c] = (w_post ? to_f(w_post[c]) + off : 1.0f) * g;
-    w2[c] = w_pre ? to_f(w_pre[c]) + off : 0.0f;
+  for (int c = threadIdx.x * 8; c < H; c += blockDim.x * 8) {
+    float a[8], g[8], b[8];
+    open8<T>(w_post ? load8<T>(w_post + c) : zero8<T>(), a);
+    open8<T>(gate ? load8<T>(gate + c) : zero8<T>(), g);
+    open8<T>(w_pre ? load8<T>(w_pre + c) : zero8<T>(), b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int to = (e >> 2) * (H >> 1) + (c >> 1) + (e & 3);
+      w1[to] = (w_post ? a[e] + off : 1.0f) * (gate ? g[e] : 1.0f);
+      w2[to] = w_pre ? b[e] + off : 0.0f;
+    }
   }
 }
-__device__ __forceinline__ void open8f(const float* p, float* f) {
-  unpack16(reinterpret_cast<const uint4*>(p)[0], f, (const float*)nullptr);
-  unpack16(reinterpret_cast<const uint4*>(p)[1], f + 4, (const float*)nullptr);
-}
-
 // A team's rows: `steps` steps of R rows, NG * R rows apart, through its ring.
 template <int STREAMS>
 struct Feed {
   const char* src[STREAMS];   // NULL: not loaded
-  int64_t rows, first;        // rows in all; the team's first
-  int64_t step;               // rows between a team's steps
+  int rows, first;            // rows in all; the team's first
+  int step;                   // rows between a team's steps
   int R, row_bytes, depth;
   uint32_t ring, bars;        // of the team
+  const unsigned char* rows_at;   // the team's ring
+  int at;                     // the slot that is read, its wait's parity; kept from step to
+  uint32_t parity;            // step, since a division a step was a tenth of the instructions
 
   __device__ __forceinline__ void init(int64_t all, int bytes, const RingShape& q, int steps, const Team& m,
                                        unsigned char* smem, unsigned char* rings) {
-    rows = all;
+    rows = (int)all;
     R = q.R;
-    first = ((int64_t)blockIdx.x * steps * q.NG + m.g) * R;
-    step = (int64_t)q.NG * R;
+    first = ((int)blockIdx.x * steps * q.NG + m.g) * R;
+    step = q.NG * R;
     row_bytes = bytes;
     depth = q.depth;
-    ring = tc::smem_u32(rings) + (uint32_t)(m.g * depth * STREAMS * R * row_bytes);
+    rows_at = rings + (size_t)m.g * depth * STREAMS * R * row_bytes;
+    ring = tc::smem_u32(rows_at);
+    at = 0;
+    parity = 0;
     bars = tc::smem_u32(smem) + 8u * m.g * depth;
     if (m.tt == 0) {
       for (int i = 0; i < depth; ++i) tc::mbar_init(bars + 8u * i, 1);
@@ -321,31 +324,87 @@ struct Feed {
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
   }
-  __device__ __forceinline__ int64_t row_of(int i) const { return first + i * step; }
-  __device__ __forceinline__ bool wait(int i) const { return ring_wait(bars + 8u * (i % depth), (uint32_t)(i / depth) & 1u); }
-  __device__ __forceinline__ const unsigned char* at(const unsigned char* rings, const Team& m, int i) const {
-    return rings + (size_t)(m.g * depth + i % depth) * STREAMS * R * row_bytes;
+  __device__ __forceinline__ bool wait() const { return ring_wait(bars + 8u * at, parity); }
+  __device__ __forceinline__ const unsigned char* here() const { return rows_at + at * STREAMS * R * row_bytes; }
+  __device__ __forceinline__ void next() {
+    if (++at == depth) {
+      at = 0;
+      parity ^= 1u;
+    }
   }
   // Called by one thread of the team.
-  __device__ __forceinline__ void load(int i, int steps) const {
+  __device__ __forceinline__ void load(int i, int steps, int to_slot) const {
     if (i >= steps) return;
-    const int64_t r = row_of(i);
+    const int r = first + i * step;
     if (r >= rows) return;
-    const int n = rows - r < R ? (int)(rows - r) : R;
-    const uint32_t bytes = (uint32_t)n * row_bytes, bar = bars + 8u * (i % depth);
-    const uint32_t to = ring + (uint32_t)(i % depth) * STREAMS * R * row_bytes;
+    const int n = min(rows - r, R);
+    const uint32_t bytes = (uint32_t)n * row_bytes, bar = bars + 8u * to_slot;
+    const uint32_t to = ring + (uint32_t)to_slot * STREAMS * R * row_bytes;
     uint32_t all = 0;
 #pragma unroll
     for (int k = 0; k < STREAMS; ++k) all += src[k] ? bytes : 0u;
     tc::mbar_expect_tx(bar, all);
 #pragma unroll
     for (int k = 0; k < STREAMS; ++k)
-      if (src[k]) bulk_load(to + k * R * row_bytes, src[k] + r * row_bytes, bytes, bar);
+      if (src[k]) bulk_load(to + k * R * row_bytes, src[k] + (int64_t)r * row_bytes, bytes, bar);
   }
   __device__ __forceinline__ void start(int steps) const {
-    for (int i = 0; i < depth - 1; ++i) load(i, steps);
+    for (int i = 0; i < depth - 1; ++i) load(i, steps, i);
   }
+  // Into the slot of the step before `i`, which every thread has left.
+  __device__ __forceinline__ void refill(int i, int steps) const { load(i + depth - 1, steps, (at ? at : depth) - 1); }
 };
+
+// Pairs of fp32: one instruction multiplies and adds two, each rounded as alone.  What
+// bounds the kernels below, once the ring hides the memory, is the instructions they issue.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+// Eight columns as four pairs.
+struct Pairs {
+  float2 p[4];
+};
+template <typename T>
+__device__ __forceinline__ Pairs open_pairs(const Eight<T>& r) {
+  float f[8];
+  open8<T>(r, f);
+  Pairs o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o.p[i] = make_float2(f[2 * i], f[2 * i + 1]);
+  return o;
+}
+// Of the staged weights, w the address of the thread's first four, `half` floats between
+// the halves.
+__device__ __forceinline__ Pairs weight_pairs(const float* w, int half) {
+  const float4 a = *reinterpret_cast<const float4*>(w), b = *reinterpret_cast<const float4*>(w + half);
+  Pairs o;
+  o.p[0] = make_float2(a.x, a.y);
+  o.p[1] = make_float2(a.z, a.w);
+  o.p[2] = make_float2(b.x, b.y);
+  o.p[3] = make_float2(b.z, b.w);
+  return o;
+}
+template <typename T>
+__device__ __forceinline__ void store_pairs(T* to, const Pairs& v) {
+  const float f[8] = {v.p[0].x, v.p[0].y, v.p[1].x, v.p[1].y, v.p[2].x, v.p[2].y, v.p[3].x, v.p[3].y};
+  store8<T>(to, f);
+}
 
 template <typename T, int VPT>
 __global__ void __launch_bounds__(1024, 1) norm_forward_ring_kernel(
@@ -353,12 +412,13 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_ring_kernel(
     const T* __restrict__ y, const T* __restrict__ w_post, const void* __restrict__ gate, const T* __restrict__ w_pre,
     T* s, T* __restrict__ h, float2* __restrict__ rstd) {
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ float red_all[16][2 * 32];
+  __shared__ float red[2 * 32];
+  __shared__ volatile int lost;
+  if (threadIdx.x == 0) lost = 0;
   float* w1 = reinterpret_cast<float*>(smem + kBarBytes);
   float* w2 = w1 + H;
   unsigned char* ring = reinterpret_cast<unsigned char*>(w2 + H);
   const Team m(q);
-  float* red = red_all[m.g];
   Feed<2> f;
   f.init(rows, H * (int)sizeof(T), q, steps, m, smem, ring);
   f.src[0] = reinterpret_cast<const char*>(x);
@@ -369,73 +429,63 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_ring_kernel(
   stage_weights<T>(w1, w2, w_post, kind == MOE_GATE_CHANNEL ? static_cast<const T*>(gate) : nullptr, w_pre, off, H);
   __syncthreads();
   const float inv_h = 1.0f / (float)H;
+  const int half = H >> 1, span = q.Gs * 8, c0 = m.lane * 8;
   int slot = 0;
   bool fed = true;
-  for (int i = 0; i < steps; ++i) {
-    const int64_t base = f.row_of(i);
-    if (base >= rows) break;
-    fed = fed && f.wait(i);
-    m.sync();                                     // the step before is behind every thread
-    if (m.tt == 0) f.load(i + q.depth - 1, steps);   // into its slot
-    const int64_t t = base + m.row;
+  int t = f.first + m.row;             // the row
+  int64_t to = (int64_t)t * H + c0;    // the thread's first column in it
+  for (int i = 0; i < steps && t - m.row < rows; ++i, t += f.step, to += (int64_t)f.step * H, f.next()) {
+    if (m.tt < 32 && !f.wait()) lost = 1;   // the barrier hands it on to the team
+    m.sync();                               // the step before is behind every thread
+    fed = !lost;
+    if (m.tt == 0) f.refill(i, steps);      // into its slot
     const bool on = t < rows;
-    const T* bx = reinterpret_cast<const T*>(f.at(ring, m, i)) + (size_t)m.row * H;
+    const T* bx = reinterpret_cast<const T*>(f.here()) + (size_t)m.row * H + c0;
     const T* by = bx + (size_t)q.R * H;
     float gt = 1.0f;
     if (kind == MOE_GATE_TOKEN && on) gt = static_cast<const float*>(gate)[t];
-    float v[VPT][8];
-    float sum[1] = {0.0f};
+    Pairs v[VPT];
     float r1 = 1.0f;
     if (w_post) {
+      float2 sq = both(0.0f);
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
-        const int c = (m.lane + k * q.Gs) * 8;
-        if (!on || c >= H) continue;
-        float fy[8];
-        open8<T>(load8<T>(by + c), fy);
+        if (!on || c0 + k * span >= H) continue;
+        const Pairs fy = open_pairs<T>(load8<T>(by + k * span));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum[0] = fmaf(fy[e], fy[e], sum[0]);
+        for (int e = 0; e < 4; ++e) sq = fma2(fy.p[e], fy.p[e], sq);
       }
-      m.sum<1>(sum, red, slot);
-      r1 = 1.0f / sqrtf(sum[0] * inv_h + eps);
-      sum[0] = 0.0f;
+      r1 = 1.0f / sqrtf(m.sum(sq.x + sq.y, red, slot) * inv_h + eps);
     }
     if (!fed) r1 = __int_as_float(0x7fc00000);   // a copy that never came
-    const float rg = r1 * gt, rx = fed ? res : r1;
+    const float2 rg = both(r1 * gt), rx = both(fed ? res : r1);
+    float2 sq = both(0.0f);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const int c = (m.lane + k * q.Gs) * 8;
+      if (!on || c0 + k * span >= H) continue;
+      v[k] = open_pairs<T>(load8<T>(bx + k * span));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[k][e] = 0.0f;
-      if (!on || c >= H) continue;
-      open8<T>(load8<T>(bx + c), v[k]);
+      for (int e = 0; e < 4; ++e) v[k].p[e] = mul2(rx, v[k].p[e]);
       if (y) {
-        float fy[8], w[8];
-        open8<T>(load8<T>(by + c), fy);
-        open8f(w1 + c, w);
+        const Pairs fy = open_pairs<T>(load8<T>(by + k * span));
+        const Pairs w = weight_pairs(w1 + ((c0 + k * span) >> 1), half);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[k][e] = fmaf(rx, v[k][e], rg * (fy[e] * w[e]));
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[k][e] *= rx;
+        for (int e = 0; e < 4; ++e) v[k].p[e] = fma2(rg, mul2(fy.p[e], w.p[e]), v[k].p[e]);
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum[0] = fmaf(v[k][e], v[k][e], sum[0]);
-      if (s) store8<T>(s + t * H + c, v[k]);
+      for (int e = 0; e < 4; ++e) sq = fma2(v[k].p[e], v[k].p[e], sq);
+      if (s) store_pairs<T>(s + to + k * span, v[k]);
     }
     float r2 = 0.0f;
     if (w_pre) {
-      m.sum<1>(sum, red, slot);
-      r2 = 1.0f / sqrtf(sum[0] * inv_h + eps);
+      r2 = 1.0f / sqrtf(m.sum(sq.x + sq.y, red, slot) * inv_h + eps);
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
-        const int c = (m.lane + k * q.Gs) * 8;
-        if (!on || c >= H) continue;
-        float w[8];
-        open8f(w2 + c, w);
+        if (!on || c0 + k * span >= H) continue;
+        const Pairs w = weight_pairs(w2 + ((c0 + k * span) >> 1), half);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[k][e] *= r2 * w[e];
-        store8<T>(h + t * H + c, v[k]);
+        for (int e = 0; e < 4; ++e) v[k].p[e] = mul2(v[k].p[e], mul2(both(r2), w.p[e]));
+        store_pairs<T>(h + to + k * span, v[k]);
       }
     }
     if (rstd && on && m.lane == 0) rstd[t] = make_float2(w_post ? r1 : 0.0f, r2);
@@ -618,33 +668,33 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : 512) norm_backward_kernel(co
 }
 
 
-// ds is needed once, in the middle, and comes straight to registers; x, y and dh by
-// the ring.  One vector a thread, so that many warps share the arithmetic (25 fp32
+// One vector a thread, so that many warps share the arithmetic (25 fp32
 // operations an element; two vectors or two rows a thread were latency-bound at 14
 // warps an SM: 255 and 374 us at T = 8192, H = 7168).
 template <typename T, int VPT>
 __global__ void __launch_bounds__(VPT == 1 ? 896 : 512, 1) norm_backward_ring_kernel(const BwdArgs a, const RingShape q,
                                                                                      int steps) {
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ float red_all[16][2 * 32];
+  __shared__ float red[2 * 32];
+  __shared__ volatile int lost;
+  if (threadIdx.x == 0) lost = 0;
   const int H = a.H;
   float* w1 = reinterpret_cast<float*>(smem + kBarBytes);
   float* w2 = w1 + H;
   unsigned char* ring = reinterpret_cast<unsigned char*>(w2 + H);
   const Team m(q);
-  float* red = red_all[m.g];
-  const T* ds = static_cast<const T*>(a.ds);
   const bool with_y = a.y != nullptr, pre = a.w_pre != nullptr, post = a.w_post != nullptr;
-  Feed<3> f;
+  Feed<4> f;
   f.init(a.rows, H * (int)sizeof(T), q, steps, m, smem, ring);
   f.src[0] = static_cast<const char*>(pre ? a.x : nullptr);
   f.src[1] = static_cast<const char*>(a.y);
   f.src[2] = static_cast<const char*>(a.dh);
+  f.src[3] = static_cast<const char*>(a.ds);
   T* dx = static_cast<T*>(a.dx);
   T* dy = static_cast<T*>(a.dy);
   pdl_trigger();
   pdl_wait();
-  const bool feeds = pre || with_y;   // else there is nothing to wait for
+  const bool feeds = pre || with_y || a.ds;   // else there is nothing to wait for
   if (m.tt == 0 && feeds) f.start(steps);
   stage_weights<T>(w1, w2, static_cast<const T*>(a.w_post),
                    a.kind == MOE_GATE_CHANNEL ? static_cast<const T*>(a.gate) : nullptr, static_cast<const T*>(a.w_pre),
@@ -653,118 +703,115 @@ __global__ void __launch_bounds__(VPT == 1 ? 896 : 512, 1) norm_backward_ring_ke
   const float inv_h = 1.0f / (float)H;
   int slot = 0;
   bool fed = true;
-  float c_e[VPT][8], c_pre[VPT][8];   // the columns' sums over this team's rows
+  Pairs c_e[VPT], c_pre[VPT];   // the columns' sums over this team's rows
 #pragma unroll
   for (int k = 0; k < VPT; ++k)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) c_e[k][e] = c_pre[k][e] = 0.0f;
-  for (int i = 0; i < steps; ++i) {
-    const int64_t base = f.row_of(i);
-    if (base >= a.rows) break;
-    const int64_t t = base + m.row;
+    for (int e = 0; e < 4; ++e) c_e[k].p[e] = c_pre[k].p[e] = both(0.0f);
+  const int half = H >> 1, span = q.Gs * 8, c0 = m.lane * 8;
+  int t = f.first + m.row;             // the row
+  int64_t to = (int64_t)t * H + c0;    // the thread's first column in it
+  float2 r_next = make_float2(0.0f, 0.0f);        // a step ahead
+  float gate_next = 1.0f;
+  auto ask = [&](int row) {
+    if (row >= a.rows) return;
+    r_next = a.rstd[row];
+    if (a.kind == MOE_GATE_TOKEN) gate_next = static_cast<const float*>(a.gate)[row];
+  };
+  ask(t);
+  for (int i = 0; i < steps && t - m.row < a.rows; ++i, t += f.step, to += (int64_t)f.step * H, f.next()) {
     const bool on = t < a.rows;
-    Eight<T> us[VPT];
-#pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-      const int c = (m.lane + k * q.Gs) * 8;
-      us[k] = on && c < H && ds ? load8<T>(ds + t * H + c) : zero8<T>();
-    }
-    float2 r = on ? a.rstd[t] : make_float2(0.0f, 0.0f);
-    const float gt = on && a.kind == MOE_GATE_TOKEN ? static_cast<const float*>(a.gate)[t] : 1.0f;
+    float2 r = r_next;
+    const float gt = gate_next;
+    ask(t + f.step);
     if (!post) r.x = 1.0f;
-    if (feeds) fed = fed && f.wait(i);
-    m.sync();                                                 // the step before is behind every thread
-    if (m.tt == 0 && feeds) f.load(i + q.depth - 1, steps);   // into its slot
-    if (!fed) r.x = r.y = __int_as_float(0x7fc00000);         // a copy that never came
-    const T* bx = reinterpret_cast<const T*>(f.at(ring, m, i)) + (size_t)m.row * H;
-    const T *by = bx + (size_t)q.R * H, *bh = by + (size_t)q.R * H;
-    float D[VPT][8];
+    if (m.tt < 32 && feeds && !f.wait()) lost = 1;      // the barrier hands it on to the team
+    m.sync();                                           // the step before is behind every thread
+    fed = !lost;
+    if (m.tt == 0 && feeds) f.refill(i, steps);         // into its slot
+    if (!fed) r.x = r.y = __int_as_float(0x7fc00000);   // a copy that never came
+    const T* bx = reinterpret_cast<const T*>(f.here()) + (size_t)m.row * H + c0;
+    const T *by = bx + (size_t)q.R * H, *bh = by + (size_t)q.R * H, *bs = bh + (size_t)q.R * H;
+    Pairs D[VPT];
     if (pre) {
-      float c2[1] = {0.0f};
-      const float rx = a.res * r.y, ry = gt * r.x * r.y;
+      float2 sum = both(0.0f);
+      const float2 rx = both(a.res * r.y), ry = both(gt * r.x * r.y);
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
-        const int c = (m.lane + k * q.Gs) * 8;
+        if (!on || c0 + k * span >= H) continue;
+        D[k] = open_pairs<T>(load8<T>(bx + k * span));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) D[k][e] = 0.0f;
-        if (!on || c >= H) continue;
-        float fv[8], w[8];
-        open8<T>(load8<T>(bx + c), D[k]);
+        for (int e = 0; e < 4; ++e) D[k].p[e] = mul2(rx, D[k].p[e]);
         if (with_y) {
-          open8<T>(load8<T>(by + c), fv);
-          open8f(w1 + c, w);
+          const Pairs fy = open_pairs<T>(load8<T>(by + k * span));
+          const Pairs w = weight_pairs(w1 + ((c0 + k * span) >> 1), half);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) D[k][e] = fmaf(rx, D[k][e], ry * (fv[e] * w[e]));
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) D[k][e] *= rx;
+          for (int e = 0; e < 4; ++e) D[k].p[e] = fma2(ry, mul2(fy.p[e], w.p[e]), D[k].p[e]);
         }
-        open8<T>(load8<T>(bh + c), fv);
-        open8f(w2 + c, w);
+        const Pairs fh = open_pairs<T>(load8<T>(bh + k * span));
+        const Pairs w = weight_pairs(w2 + ((c0 + k * span) >> 1), half);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          c_pre[k][e] = fmaf(fv[e], D[k][e], c_pre[k][e]);
-          c2[0] = fmaf(fv[e] * w[e], D[k][e], c2[0]);   // D is sn until the sum is there
+        for (int e = 0; e < 4; ++e) {
+          c_pre[k].p[e] = fma2(fh.p[e], D[k].p[e], c_pre[k].p[e]);
+          const float2 b = mul2(fh.p[e], w.p[e]);
+          sum = fma2(b, D[k].p[e], sum);   // D is sn until the sum is there
         }
       }
-      m.sum<1>(c2, red, slot);
-      const float mean = -c2[0] * inv_h;
+      const float2 mean = both(-m.sum(sum.x + sum.y, red, slot) * inv_h), ry2 = both(r.y);
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
-        const int c = (m.lane + k * q.Gs) * 8;
-        if (!on || c >= H) continue;
-        float fv[8], w[8];
-        open8<T>(load8<T>(bh + c), fv);
-        open8f(w2 + c, w);
+        if (!on || c0 + k * span >= H) continue;
+        const Pairs fs = open_pairs<T>(a.ds ? load8<T>(bs + k * span) : zero8<T>()), fh = open_pairs<T>(load8<T>(bh + k * span));
+        const Pairs w = weight_pairs(w2 + ((c0 + k * span) >> 1), half);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) D[k][e] = fmaf(D[k][e], mean, fv[e] * w[e]);
-        open8<T>(us[k], fv);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) D[k][e] = fmaf(r.y, D[k][e], fv[e]);
+        for (int e = 0; e < 4; ++e)
+          D[k].p[e] = fma2(ry2, fma2(D[k].p[e], mean, mul2(fh.p[e], w.p[e])), fs.p[e]);
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < VPT; ++k) open8<T>(us[k], D[k]);
+      for (int k = 0; k < VPT; ++k)
+        D[k] = open_pairs<T>(on && c0 + k * span < H && a.ds ? load8<T>(bs + k * span) : zero8<T>());
     }
     // D, and the block's side: the row sum of D yn w1, which is the token gate's
     // gradient too
-    float c1[1] = {0.0f};
+    float2 sum = both(0.0f);
+    const float2 ge = both(gt * r.x);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const int c = (m.lane + k * q.Gs) * 8;
-      if (!on || c >= H) continue;
+      if (!on || c0 + k * span >= H) continue;
       if (dx) {
-        float o[8];
+        Pairs o;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = a.res * D[k][e];
-        store8<T>(dx + t * H + c, o);
+        for (int e = 0; e < 4; ++e) o.p[e] = mul2(both(a.res), D[k].p[e]);
+        store_pairs<T>(dx + to + k * span, o);
       }
       if (!with_y) continue;
-      float fy[8], w[8];
-      open8<T>(load8<T>(by + c), fy);
-      open8f(w1 + c, w);
+      const Pairs fy = open_pairs<T>(load8<T>(by + k * span));
+      const Pairs w = weight_pairs(w1 + ((c0 + k * span) >> 1), half);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float dyn = D[k][e] * (fy[e] * r.x);
-        c_e[k][e] = fmaf(gt, dyn, c_e[k][e]);
-        c1[0] = fmaf(dyn, w[e], c1[0]);
-        D[k][e] *= w[e];
+      for (int e = 0; e < 4; ++e) {
+        c_e[k].p[e] = fma2(mul2(D[k].p[e], ge), fy.p[e], c_e[k].p[e]);
+        D[k].p[e] = mul2(D[k].p[e], w.p[e]);
+        sum = fma2(D[k].p[e], fy.p[e], sum);
       }
     }
     if (!with_y) continue;
-    if (post || a.dgate) m.sum<1>(c1, red, slot);
-    if (a.dgate && on && m.lane == 0) a.dgate[t] = c1[0];
+    float c1 = (sum.x + sum.y) * r.x;
+    if (post || a.dgate) c1 = m.sum(c1, red, slot);
+    if (a.dgate && on && m.lane == 0) a.dgate[t] = c1;
     if (!dy) continue;
-    const float mine = gt * r.x, back = -r.x * mine * (c1[0] * inv_h);
+    const float2 mine = both(gt * r.x), back = both(post ? -r.x * (gt * r.x) * (c1 * inv_h) : 0.0f);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const int c = (m.lane + k * q.Gs) * 8;
-      if (!on || c >= H) continue;
-      float fy[8];
-      open8<T>(load8<T>(by + c), fy);
+      if (!on || c0 + k * span >= H) continue;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) D[k][e] = post ? fmaf(fy[e], back, mine * D[k][e]) : mine * D[k][e];
-      store8<T>(dy + t * H + c, D[k]);
+      for (int e = 0; e < 4; ++e) D[k].p[e] = mul2(mine, D[k].p[e]);
+      if (post) {
+        const Pairs fy = open_pairs<T>(load8<T>(by + k * span));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) D[k].p[e] = fma2(fy.p[e], back, D[k].p[e]);
+      }
+      store_pairs<T>(dy + to + k * span, D[k]);
     }
   }
   if (!fed) ring_drain();
@@ -778,8 +825,8 @@ __global__ void __launch_bounds__(VPT == 1 ? 896 : 512, 1) norm_backward_ring_ke
     const int c = (m.lane + k * q.Gs) * 8;
     if (c >= H) continue;
     float* p = sums + (size_t)(m.g * q.R + m.row) * 2 * H + c;
-    store8<float>(p, c_e[k]);
-    store8<float>(p + H, c_pre[k]);
+    store_pairs<float>(p, c_e[k]);
+    store_pairs<float>(p + H, c_pre[k]);
   }
   __syncthreads();
   float* out = a.part + (int64_t)blockIdx.x * 2 * H;
@@ -855,7 +902,7 @@ moe_status decode(const moe_block_norm_shape* s, NShape* o, const char** why) {
 // threads of an SM (two vectors: threads2): as many teams as fit with two steps or more in
 // their rings, then the deepest rings.  depth 0: none fits.
 constexpr int kSmemBlock = 227 * 1024, kSmemSm = 228 * 1024;   // 1 KB of the latter goes with each block
-constexpr int kStatic = 4096;                                   // what the kernels declare besides
+constexpr int kStatic = 512;                                    // what the kernels declare besides
 RingShape ring_shape(int H, int esize, int streams, int wide, int threads, int threads2) {
   RingShape q = {};
   const int vecs = H / 8;
@@ -903,7 +950,7 @@ struct Split {
 };
 Split split_of(const NShape& s) {
   Split p = {};
-  p.q = ring_shape(s.H, s.esize, 3, 896, 896, 512);
+  p.q = ring_shape(s.H, s.esize, 4, 896, 896, 512);
   if (p.q.depth > 0) {
     const int64_t per = (int64_t)p.q.NG * p.q.R;   // rows of a block's step
     const int64_t resident = 152ll * p.q.per_sm;

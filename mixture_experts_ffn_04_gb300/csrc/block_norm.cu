@@ -3,9 +3,11 @@
 //
 //   u = y r1 (w_post + o),  s = residual_scale x + g u,  h = s r2 (w_pre + o)
 //
-// Bound by HBM: the forward reads two rows a token and writes two, the backward
-// reads four and writes two (s is not read back: from x and y it costs a few
-// FMAs, and it has not been rounded).  A group of threads holds a whole row in
+// The forward reads two rows a token and writes two, the backward reads four and
+// writes two (s is not read back: from x and y it costs a few FMAs, and it has not been
+// rounded).  At 8192 rows of 7168 columns in bf16 that takes 84 us (470 MB, 5.6 TB/s: 82 % of
+// the rate of a copy) and 154 us (705 MB, 4.6 TB/s: 67 %), by the rings below; few rows are
+// bound by latency (one row of 7168: 4.5 us on the device).  A group of threads holds a whole row in
 // registers, eight columns and their multiples a thread, so that both norms of the
 // forward, and both row sums of the backward, come from one read.  Sums in fp32.
 //
@@ -207,8 +209,9 @@ __global__ void __launch_bounds__(1024) norm_forward_kernel(int64_t rows, int H,
 // rows) is fed by bulk copies into a ring of its own, kRing steps deep, so that the
 // next rows are under way while this one's sums wait on each other; the weights
 // stand in shared memory.  Held in registers without the ring, a row's loads, two
-// row sums and stores followed one another: the forward at T = 4096, H = 2816 took 39 us,
-// the backward at T = 8192, H = 7168 340.
+// row sums and stores followed one another: the forward at T = 4096, H = 2816 took 39 us
+// against 25, the backward at T = 8192, H = 7168 340 against 160.  x in registers a step
+// ahead instead of by the ring: 104 us against 84 at 8192 x 7168 forward.
 // ---------------------------------------------------------------------------
 struct RingShape {
   int G;        // threads of a team (whole warps)
@@ -668,9 +671,12 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : 512) norm_backward_kernel(co
 }
 
 
-// One vector a thread, so that many warps share the arithmetic (25 fp32
-// operations an element; two vectors or two rows a thread were latency-bound at 14
-// warps an SM: 255 and 374 us at T = 8192, H = 7168).
+// Two vectors a thread in
+// 14 warps halve the instructions of the row sums, waits and addresses for each element: 160
+// us at 8192 x 7168 against 172 with one vector in 28 warps.  Nothing may spill: beside rings
+// that leave the L1 no room a spilled register is an access of L2 (72 registers with a few
+// spills: 195 to 270 us).  One barrier a row instead of three, by finishing dy a step later,
+// took as long.
 template <typename T, int VPT>
 __global__ void __launch_bounds__(VPT == 1 ? 896 : 512, 1) norm_backward_ring_kernel(const BwdArgs a, const RingShape q,
                                                                                      int steps) {
@@ -950,7 +956,7 @@ struct Split {
 };
 Split split_of(const NShape& s) {
   Split p = {};
-  p.q = ring_shape(s.H, s.esize, 4, 896, 896, 512);
+  p.q = ring_shape(s.H, s.esize, 4, 64, 896, 512);
   if (p.q.depth > 0) {
     const int64_t per = (int64_t)p.q.NG * p.q.R;   // rows of a block's step
     const int64_t resident = 152ll * p.q.per_sm;

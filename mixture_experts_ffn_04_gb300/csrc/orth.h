@@ -10,13 +10,14 @@ namespace moe {
 // A matrix is held as fp16 planes of its values times a power of two: the leading 11
 // bits, and the next 11; X of bf16 matrices as one plane and an 8-bit part, the next 8 bits.
 // X [m, n] with m <= n, its singular values at most 3.5; A = X X^T; B = b A + c A A, at most
-// 100.
-constexpr int kOrthX = 13, kOrthA = 11, kOrthB = 9;
-constexpr double kOrthMaxX = 3.5, kOrthMaxB = 100.0;
+// 100; R of two steps in one (below), at most 200.
+constexpr int kOrthX = 13, kOrthA = 11, kOrthB = 9, kOrthR = 8;
+constexpr double kOrthMaxX = 3.5, kOrthMaxB = 100.0, kOrthMaxR = 200.0;
 
 // A batch in scratch.  x[0], x[1]: [planes][batch][m][ldx] each, with one plane the 8-bit
-// parts [batch][m][ldx] behind it; a, b: [planes][batch][m][lda]; ldx a multiple of 128, lda of
+// parts [batch][m][ldx] behind it; a, b, c: [planes][batch][m][lda]; ldx a multiple of 128, lda of
 // 64 (columns past m and n, up to there, are written, and read only into themselves).
+// c: NULL, or (one plane) the first two steps go in one where steps follow them.
 struct OrthBatch {
   int64_t batch;
   int m, n, ldx, lda;
@@ -24,6 +25,7 @@ struct OrthBatch {
   void* x[2];
   void* a;
   void* b;
+  void* c;
   uint32_t* flags;
 };
 
@@ -54,7 +56,7 @@ __device__ __forceinline__ float orth_with_low(float h, int low) {
 #endif
 
 // `steps` times X <- a X + (b A + c A A) X with (a, b, c) = coef[i], from x[0]; the
-// last X is in x[steps & 1], of bf16 matrices without 8-bit parts.
-cudaError_t launch_orth_steps(const OrthBatch& t, int steps, const double (*coef)[3], cudaStream_t st);
+// last X is in x[*last], of bf16 matrices without 8-bit parts.
+cudaError_t launch_orth_steps(const OrthBatch& t, int steps, const double (*coef)[3], int* last, cudaStream_t st);
 
 }  // namespace moe

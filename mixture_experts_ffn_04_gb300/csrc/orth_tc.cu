@@ -6,6 +6,15 @@
 // A and B are symmetric: only the tiles on and below the diagonal are computed,
 // and each is written twice, the second time transposed.
 //
+// The first two steps of wide bf16 matrices are one: with B = b A + c A A of the first,
+//   C = a A + B A,  A' = a C + B C (= X' X'^T),  B' = b' A' + c' A' A',
+//   R = a B' + a' B + B' B,  X'' = a a' X + R X
+// (polynomials in A commute), three products of K = m more in place of a kGram and a
+// kApply, which is the slowest (2652 us against 2894 for 96 matrices 704 x 2816).
+// a a' X stays apart, so that X keeps its 19 bits; simulated as below no less precise
+// (normal entries 1.6e-3, rank 16 4.5e-4).  A later pair rounds R closer to the result
+// (2.6e-3 with the third and fourth step in one too): not taken.
+//
 // Operands are the leading fp16 planes of X, A and B (11 bits); a X takes both planes
 // of X, and X' is kept in both.  That matters more than the precision of the
 // products: an error in X outside its row and column space grows by a in every
@@ -86,6 +95,8 @@ struct Args {
   float add_scale, mul;   // result = add_scale * addend + mul * product
   const char* add;        // the addend's leading plane, rows add_ld bytes apart
   const char* add_low;    // its second plane, or its 8-bit parts
+  const char* add2;       // kOneTwice: the second addend
+  float add2_scale;
   char* out;              // the result, the same
   char* out_low;
   int64_t add_ld, low_ld; // of the addend and the result, bytes
@@ -213,8 +224,9 @@ __device__ __forceinline__ void mirror_rows(uint32_t stage, const uint32_t (&w)[
 }
 
 // How addend and result are held: kOne: one fp16 plane; kTwo: two; kLow: one and the 8-bit
-// part (X of bf16 matrices); kLowIn: the addend so, the result in one plane.
-enum Form { kOne = 0, kTwo = 1, kLow = 2, kLowIn = 3 };
+// part (X of bf16 matrices); kLowIn: the addend so, the result in one plane; kOneTwice: kOne
+// with two addends.
+enum Form { kOne = 0, kTwo = 1, kLow = 2, kLowIn = 3, kOneTwice = 4 };
 
 // Operand maps are 3-D, {columns, rows, plane * batch + matrix}: boxes of 64 columns by
 // 128 rows, kApply's B operand 64 by 64 in its stored layout.
@@ -410,6 +422,12 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
           load_block(hi[h], a.add + p.row * a.add_ld + 2 * (p.n0 + 64 * h), a.add_ld, p.n0 + 64 * h < width ? p.rows : 0,
                      lane);
       };
+      Block more[FORM == kOneTwice ? 2 : 1];
+      auto ask_more = [&](const Part& p, int h) {
+        if (FORM == kOneTwice)
+          load_block(more[h], a.add2 + p.row * a.add_ld + 2 * (p.n0 + 64 * h), a.add_ld,
+                     p.n0 + 64 * h < width ? p.rows : 0, lane);
+      };
       auto ask_lo = [&](const Part& p) {
         if (LOW_IN) load_block(lo, a.add_low + p.row * a.low_ld + p.n0, a.low_ld, p.rows, lane);
       };
@@ -419,6 +437,10 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
       ask_lo(p);
       ask_hi(p, 0);
       ask_hi(p, 1);
+      if (FORM == kOneTwice) {
+        ask_more(p, 0);
+        ask_more(p, 1);
+      }
       for (uint32_t t = first; t < total; t += step, d = dn, p = pn) {
         walk.next(a);
         if (walk.t < total) {
@@ -446,6 +468,19 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
         tmem_ld16(taddr, r[0]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+          uint32_t second[FORM == kOneTwice ? 32 : 1];   // this lane's part of the second addend
+          if (FORM == kOneTwice) {
+            block_to_slice(more[h], stage, lane);
+            ask_more(pn, h);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint4 v = get_piece(stage, lane, j);
+              second[4 * j] = v.x;
+              second[4 * j + 1] = v.y;
+              second[4 * j + 2] = v.z;
+              second[4 * j + 3] = v.w;
+            }
+          }
           if (KIND != kGram) {
             block_to_slice(hi[h], stage, lane);
             ask_hi(pn, h);
@@ -475,6 +510,11 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
                   }
                   f0 = fmaf(a.add_scale, x.x, f0);
                   f1 = fmaf(a.add_scale, x.y, f1);
+                }
+                if (FORM == kOneTwice) {
+                  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&second[8 * c + 4 * g + e]));
+                  f0 = fmaf(a.add2_scale, x.x, f0);
+                  f1 = fmaf(a.add2_scale, x.y, f1);
                 }
                 const uint32_t v = pack_half2(f0, f1);
                 w[8 * c + 4 * g + e] = v;
@@ -626,7 +666,8 @@ static cudaError_t prepare_device(int* clusters) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (g_clusters[dev] == 0) {
-    const void* fn[8] = {(const void*)orth_kernel<kGram, kOne>,  (const void*)orth_kernel<kGram, kTwo>,
+    const void* fn[] = {(const void*)orth_kernel<kPoly, kOneTwice>,
+                         (const void*)orth_kernel<kGram, kOne>,  (const void*)orth_kernel<kGram, kTwo>,
                          (const void*)orth_kernel<kPoly, kOne>,  (const void*)orth_kernel<kPoly, kTwo>,
                          (const void*)orth_kernel<kApply, kLow>, (const void*)orth_kernel<kApply, kLowIn>,
                          (const void*)orth_kernel<kApply, kOne>, (const void*)orth_kernel<kApply, kTwo>};
@@ -669,24 +710,24 @@ static cudaError_t launch(const Maps& maps, const Args& t, cudaStream_t st) {
 
 }  // namespace orth
 
-cudaError_t launch_orth_steps(const OrthBatch& t, int steps, const double (*coef)[3], cudaStream_t st) {
+cudaError_t launch_orth_steps(const OrthBatch& t, int steps, const double (*coef)[3], int* last, cudaStream_t st) {
   using namespace orth;
   const int64_t B = t.batch, all = B * t.planes;
   const bool two = t.planes == 2;
-  // the three products' maps, those of X for either buffer as the source
-  Maps gram[2], poly, apply[2];
-  CUtensorMap bk;
-  if (!map3(&poly.A, t.a, all, t.m, t.m, t.lda, 64, 128) || !map3(&bk, t.b, all, t.m, t.m, t.lda, 64, 128))
+  // the products' maps, those of X for either buffer as the source
+  CUtensorMap of_a, of_b, of_c;
+  Maps gram[2];
+  CUtensorMap apply_x[2];
+  if (!map3(&of_a, t.a, all, t.m, t.m, t.lda, 64, 128) || !map3(&of_b, t.b, all, t.m, t.m, t.lda, 64, 128) ||
+      !map3(&of_c, t.c ? t.c : t.a, all, t.m, t.m, t.lda, 64, 128))
     return cudaErrorInvalidValue;
-  poly.B = poly.A;
   for (int i = 0; i < 2; ++i) {
     // planes of X: two of fp16, or one with the 8-bit parts behind it
     const int64_t planes = (two ? 2 : 1) * B;
     if (!map3(&gram[i].A, t.x[i], planes, t.m, t.n, t.ldx, 64, 128) ||
-        !map3(&apply[i].B, t.x[i], planes, t.m, t.n, t.ldx, 64, 64))
+        !map3(&apply_x[i], t.x[i], planes, t.m, t.n, t.ldx, 64, 64))
       return cudaErrorInvalidValue;
     gram[i].B = gram[i].A;
-    apply[i].A = bk;
   }
   Args g = {};
   g.m = t.m;
@@ -697,10 +738,30 @@ cudaError_t launch_orth_steps(const OrthBatch& t, int steps, const double (*coef
   g.mt = (t.m + BM - 1) / BM;
   g.nt = (t.n + BN - 1) / BN;
   const int64_t rows = B * t.m, a_ld = (int64_t)t.lda * 2, x_ld = (int64_t)t.ldx * 2;
-  char *pa = static_cast<char*>(t.a), *pb = static_cast<char*>(t.b);
+  char *pa = static_cast<char*>(t.a), *pb = static_cast<char*>(t.b), *pc = static_cast<char*>(t.c);
+  // out = add_scale add (+ add2_scale add2) + mul P Q, symmetric, the scales with the powers of two
+  auto poly = [&](const CUtensorMap& P, const CUtensorMap& Q, double mul, const char* add, double add_scale,
+                  const char* add2, double add2_scale, char* out) {
+    const Maps maps = {P, Q};
+    g.kb = (t.m + BK - 1) / BK;
+    g.per = g.mt * (g.mt + 1) / 2;
+    g.mul = (float)mul;
+    g.add_scale = (float)add_scale;
+    g.add = add;
+    g.add_low = add + rows * a_ld;
+    g.add2 = add2;
+    g.add2_scale = (float)add2_scale;
+    g.add_ld = g.low_ld = a_ld;
+    g.out = out;
+    g.out_low = out + rows * a_ld;
+    if (two) return launch<kPoly, kTwo>(maps, g, st);
+    return add2 ? launch<kPoly, kOneTwice>(maps, g, st) : launch<kPoly, kOne>(maps, g, st);
+  };
+  auto two_to = [](int e) { return std::ldexp(1.0, e); };
   bool low = true;     // x[0] has its 8-bit parts
-  for (int i = 0; i < steps; ++i) {
-    char *from = static_cast<char*>(t.x[i & 1]), *to = static_cast<char*>(t.x[(i & 1) ^ 1]);
+  int at = 0;          // the buffer that X is in
+  for (int i = 0; i < steps; at ^= 1) {
+    char *from = static_cast<char*>(t.x[at]), *to = static_cast<char*>(t.x[at ^ 1]);
     // A = X X^T
     g.kb = (t.n + BK - 1) / BK;
     g.per = g.mt * (g.mt + 1) / 2;
@@ -708,22 +769,30 @@ cudaError_t launch_orth_steps(const OrthBatch& t, int steps, const double (*coef
     g.add_ld = g.low_ld = a_ld;
     g.out = pa;
     g.out_low = pa + rows * a_ld;
-    cudaError_t e = two ? launch<kGram, kTwo>(gram[i & 1], g, st) : launch<kGram, kOne>(gram[i & 1], g, st);
+    cudaError_t e = two ? launch<kGram, kTwo>(gram[at], g, st) : launch<kGram, kOne>(gram[at], g, st);
     if (e != cudaSuccess) return e;
     // B = b A + c A A, the polynomial in the planes that the product reads
-    g.kb = (t.m + BK - 1) / BK;
-    g.add_scale = ldexpf((float)coef[i][1], kOrthB - kOrthA);
-    g.mul = ldexpf((float)coef[i][2], kOrthB - 2 * kOrthA);
-    g.add = pa;
-    g.add_low = pa + rows * a_ld;
-    g.out = pb;
-    g.out_low = pb + rows * a_ld;
-    e = two ? launch<kPoly, kTwo>(poly, g, st) : launch<kPoly, kOne>(poly, g, st);
+    const double *c0 = coef[i], *c1 = coef[i + 1 < steps ? i + 1 : i];
+    e = poly(of_a, of_a, c0[2] * two_to(kOrthB - 2 * kOrthA), pa, c0[1] * two_to(kOrthB - kOrthA), nullptr, 0.0, pb);
+    const bool pair = t.c && i == 0 && steps > 2;
+    if (pair) {
+      // C, A', B', R to c, a, c, a
+      if (e == cudaSuccess) e = poly(of_b, of_a, two_to(-kOrthB), pa, c0[0], nullptr, 0.0, pc);
+      if (e == cudaSuccess) e = poly(of_b, of_c, two_to(-kOrthB), pc, c0[0], nullptr, 0.0, pa);
+      if (e == cudaSuccess)
+        e = poly(of_a, of_a, c1[2] * two_to(kOrthB - 2 * kOrthA), pa, c1[1] * two_to(kOrthB - kOrthA), nullptr, 0.0, pc);
+      if (e == cudaSuccess)
+        e = poly(of_c, of_b, two_to(kOrthR - 2 * kOrthB), pc, c0[0] * two_to(kOrthR - kOrthB), pb,
+                 c1[0] * two_to(kOrthR - kOrthB), pa);
+    }
     if (e != cudaSuccess) return e;
-    // X' = a X + B X
+    i += pair ? 2 : 1;
+    // X' = a X + B X, or a a' X + R X
+    const Maps apply = {pair ? of_a : of_b, apply_x[at]};
+    g.kb = (t.m + BK - 1) / BK;
     g.per = g.mt * g.nt;
-    g.add_scale = (float)coef[i][0];
-    g.mul = ldexpf(1.0f, -kOrthB);
+    g.add_scale = (float)(pair ? c0[0] * c1[0] : c0[0]);
+    g.mul = ldexpf(1.0f, pair ? -kOrthR : -kOrthB);
     g.add_ld = x_ld;
     g.low_ld = t.ldx;
     g.add = from;
@@ -734,15 +803,16 @@ cudaError_t launch_orth_steps(const OrthBatch& t, int steps, const double (*coef
     // bits do (simulated as above, the last two X without their parts: 1.6e-3 again for
     // normal entries, rank 16 1.0e-3 instead of 4.3e-4; the last three: rank 16 2.5e-3).
     double grows = 1.0;
-    for (int k = i + 1; k < steps; ++k) grows *= fabs(coef[k][0]);
+    for (int k = i; k < steps; ++k) grows *= fabs(coef[k][0]);
     const bool keep = grows > 4.0;
-    if (two) e = launch<kApply, kTwo>(apply[i & 1], g, st);
-    else if (keep && low) e = launch<kApply, kLow>(apply[i & 1], g, st);
-    else if (low) e = launch<kApply, kLowIn>(apply[i & 1], g, st);
-    else e = launch<kApply, kOne>(apply[i & 1], g, st);
+    if (two) e = launch<kApply, kTwo>(apply, g, st);
+    else if (keep && low) e = launch<kApply, kLow>(apply, g, st);
+    else if (low) e = launch<kApply, kLowIn>(apply, g, st);
+    else e = launch<kApply, kOne>(apply, g, st);
     if (e != cudaSuccess) return e;
     low = low && keep;
   }
+  *last = at;
   return cudaSuccess;
 }
 

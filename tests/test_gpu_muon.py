@@ -146,6 +146,32 @@ def test_steps_of_their_own(m):
     close(m.Orthogonalize(2, 90, 150, coefficients=(1.5, -0.5, 0.0), steps=1).forward(u), u, coefs[:1])
 
 
+WIDE = [(1, 129, 258), (3, 200, 400), (2, 130, 1000), (1, 2050, 300), (5, 256, 512)]
+
+
+@pytest.mark.parametrize("shape", WIDE)
+@pytest.mark.parametrize("rank", [None, 1, 16])
+def test_first_two_steps_in_one(m, shape, rank):
+    """bf16 matrices at least twice as wide as high (or the reverse); the default steps, three
+    of them, and two, which stay apart."""
+    u = draw(shape, torch.bfloat16, seed=sum(shape), rank=rank)
+    for steps in (5, 3, 2):
+        op = m.Orthogonalize(*shape, steps=steps)
+        got = op.forward(u)
+        close(got, u, (COEFS,) * steps)
+        assert torch.equal(op.forward(u), got)
+        assert op.device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("third", [(0.3, 0.0, 0.0), (0.9, -0.02, 0.0)])
+def test_two_steps_too_large_for_one(m, third):
+    """3.5 T5(s), then 3.5 T5(s / 3.5): (b A + c A A) of both and their product pass 200 together."""
+    coefs = ((17.5, -70.0, 56.0), (5.0, -20.0 / 12.25, 16.0 / 12.25 ** 2), third)
+    coefs = tuple(tuple(0.99 * v for v in c) for c in coefs)
+    u = draw((2, 150, 310), torch.bfloat16, seed=5)
+    close(m.Orthogonalize(2, 150, 310, coefficients=coefs).forward(u), u, coefs)
+
+
 def reference_step(w, g, v, lr, beta, nesterov, decay, scale):
     v2 = beta * v.double() + (1.0 - beta) * g.double()
     u = beta * v2 + (1.0 - beta) * g.double() if nesterov else v2

@@ -11,6 +11,7 @@ fallback: if ``libmoe.so`` is missing or fails to load, every call raises.
 """
 from __future__ import annotations
 
+import bisect
 import ctypes
 import os
 from typing import NamedTuple, Optional
@@ -832,6 +833,16 @@ def muon_tensors(params, grads, momenta):
         e.rows, e.cols = w.shape[-2], w.shape[-1]
         e.batch = w.numel() // max(1, w.shape[-2] * w.shape[-1])
         e.param_dtype, e.grad_dtype = _dtype_code(w.dtype), _dtype_code(g.dtype)
+    # what a step writes is written once, and read as nothing else
+    span = lambda t: (t.data_ptr(), t.data_ptr() + t.numel() * t.element_size())
+    written = sorted(span(t) for t in params + momenta if t.numel())
+    ends = [hi for _, hi in written]
+    if any(hi > lo for hi, (lo, _) in zip(ends, written[1:])):
+        raise ValueError("no two parameters and momenta may overlap")
+    for lo, hi in (span(g) for g in grads if g.numel()):
+        i = bisect.bisect_right(ends, lo)   # the first that ends behind the gradient's start
+        if i < len(written) and written[i][0] < hi:
+            raise ValueError("a gradient must not overlap a parameter or a momentum")
     return arr
 
 
@@ -1200,7 +1211,8 @@ class Muon:
         self.ws = _alloc_ws(moe_muon_workspace_bytes(self.tensors, c), self.params[0].device, None, "Muon")
 
     def step(self, lr: Optional[float] = None, stream=None):
-        """One update; lr stays what it was last set to."""
+        """One update; lr stays what it was last set to (a captured step keeps the lr that it
+        was captured with)."""
         if lr is not None:
             self.config.lr = lr
         moe_muon_step(self.tensors, self.config, self.ws, stream)

@@ -236,3 +236,43 @@ def test_stream_and_graph(m):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(p, q) for p, q in zip(out, want))
+
+
+MANY = [  # rows enough for several steps of every ring, in both directions
+    (5000, 1024, "bf16", "channel", True, True, True, 0, 1.0), (4001, 1000, "f32", "token", True, True, True, 1, 0.5),
+    (3001, 2816, "bf16", None, True, True, True, 1, 1.0), (3001, 512, "f32", "token", False, True, True, 0, 1.0),
+    (4000, 520, "bf16", "channel", True, False, True, 0, 1.0), (6001, 264, "bf16", None, False, True, False, 0, 2.0),
+    (3000, 640, "f32", "channel", False, False, True, 0, 1.0), (9001, 136, "bf16", "token", True, True, True, 0, 1.0),
+    (2000, 7168, "bf16", "channel", True, True, True, 0, 1.0), (1500, 7168, "f32", None, True, True, True, 0, 1.0)]
+
+
+@pytest.mark.parametrize("T,H,dtype,gate,post,pre,with_y,offset,res", MANY)
+def test_many_rows(m, T, H, dtype, gate, post, pre, with_y, offset, res):
+    test_forward_and_gradients(m, T, H, dtype, gate, post, pre, with_y, offset, res)
+
+
+@pytest.mark.parametrize("T,H,dt", [(6000, 512, torch.bfloat16), (4001, 72, torch.float32), (3000, 4096, torch.bfloat16)])
+def test_many_rows_in_place(m, T, H, dt):
+    a = inputs(T, H, dt, "token", True, True, True)
+    op = m.BlockNorm(T, H, dtype=dt, gate="token")
+    kw = {k: a[k] for k in ("w_post", "gate", "w_pre")}
+    s, h = op.forward(a["x"], a["y"], **kw)
+    full = op.backward(a["ds"], a["dh"], a["x"], a["y"], **kw)
+    ds, y = a["ds"].clone(), a["y"].clone()
+    got = op.backward(ds, a["dh"], a["x"], y, **kw, dx=ds, dy=y)
+    assert all(torch.equal(p, q) for p, q in zip(got, full))
+    x = a["x"].clone()
+    again = op.forward(x, a["y"], **kw, s=x)
+    assert torch.equal(again[0], s) and torch.equal(again[1], h)
+    zero = op.backward(torch.zeros_like(a["ds"]), a["dh"], a["x"], a["y"], **kw)
+    none = op.backward(None, a["dh"], a["x"], a["y"], **kw)
+    assert all(torch.equal(p, q) for p, q in zip(none, zero))
+    # a bad row stays in its row (what is summed over rows apart)
+    a["y"][T // 3, 3], a["x"][T // 2, 5] = float("nan"), float("inf")
+    s2, h2 = op.forward(a["x"], a["y"], **kw)
+    d = op.backward(a["ds"], a["dh"], a["x"], a["y"], **kw)
+    ok = torch.ones(T, dtype=torch.bool, device="cuda")
+    ok[[T // 3, T // 2]] = False
+    assert torch.equal(s2[ok], s[ok]) and torch.equal(h2[ok], h[ok])
+    assert torch.equal(d.dx[ok], full.dx[ok]) and torch.equal(d.dy[ok], full.dy[ok])
+    assert torch.equal(d.dgate[ok], full.dgate[ok])

@@ -264,3 +264,34 @@ def test_step_in_a_graph_and_on_a_stream(m):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(one, three) and torch.equal(a.momenta[0], c.momenta[0])
+
+
+def test_a_list_that_meets_itself_is_refused(m):
+    z = lambda *n: torch.zeros(n, device="cuda", dtype=torch.float32)
+    w, g, v = z(4, 160, 160), z(4, 160, 160), z(4, 160, 160)
+    with pytest.raises(ValueError, match="no two"):
+        m.Muon([w, w], [g, g.clone()], [v, v.clone()])
+    with pytest.raises(ValueError, match="no two"):
+        m.Muon([w, w[3:]], [g, g[:1]], [v, z(1, 160, 160)])
+    with pytest.raises(ValueError, match="no two"):
+        m.Muon([w[:2], w[2:]], [g[:2], g[2:]], [v[:2], v[1:3]])
+    with pytest.raises(ValueError, match="gradient"):
+        m.Muon([w], [w], [v])
+    with pytest.raises(ValueError, match="gradient"):
+        m.Muon([w[:1], w[1:2]], [g[:1], w[1:2]], [v[:1], v[1:2]])
+    # side by side, and one gradient for two
+    m.Muon([w[:2], w[2:]], [g[:2], g[:2]], [v[:2], v[2:]]).step()
+
+
+@pytest.mark.parametrize("shape", [(5, 160, 400), (5, 400, 160)])
+def test_bad_wide_matrices_stay_alone(m, shape):
+    u = draw(shape, torch.bfloat16, seed=9)
+    op = m.Orthogonalize(*shape)
+    clean = op.forward(u)
+    u[1] = 0.0
+    u[2, 5, 5] = float("nan")
+    u[4, 6, 7] = float("-inf")
+    got = op.forward(u)
+    assert float(got[1].abs().max()) == 0.0
+    assert bool(got[2].isnan().all()) and bool(got[4].isnan().all())
+    assert torch.equal(got[0], clean[0]) and torch.equal(got[3], clean[3])

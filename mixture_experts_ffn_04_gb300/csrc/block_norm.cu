@@ -358,27 +358,8 @@ struct Feed {
   __device__ __forceinline__ void refill(int i, int steps) const { load(i + depth - 1, steps, (at ? at : depth) - 1); }
 };
 
-// Pairs of fp32: one instruction multiplies and adds two, each rounded as alone.  What
-// bounds the kernels below, once the ring hides the memory, is the instructions they issue.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{.reg .b64 a, b, c, d;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{.reg .b64 a, b, d;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+// What bounds the kernels below, once the ring hides the memory, is the instructions they
+// issue: fp32 arithmetic in pairs.
 // Eight columns as four pairs.
 struct Pairs {
   float2 p[4];

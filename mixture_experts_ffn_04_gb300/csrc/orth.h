@@ -49,9 +49,9 @@ __device__ __forceinline__ uint32_t orth_low_pack(int a, int b, int c, int d) {
       : "r"(a), "r"(b), "r"(c), "r"(d));
   return r;
 }
-// low: sign-extended
-__device__ __forceinline__ float orth_with_low(float h, int low) {
-  return __int_as_float(__float_as_int(h) + low * 32);
+// h and its part, byte `at` of `low`: one dot product of four bytes with 32 at that byte.
+__device__ __forceinline__ float orth_with_low(float h, uint32_t low, int at) {
+  return __int_as_float(__dp4a((int)low, 32 << (8 * at), __float_as_int(h)));
 }
 #endif
 

@@ -29,7 +29,7 @@
 // A pair of SMs computes 256 x 256 tiles over 64-wide k-blocks through six 32 KB
 // stages (three of 64 KB).  Addend and result go between registers and memory as whole 128-byte rows, turned
 // in a 4 KB slice of each epilogue warp between that layout and the one of TMEM (a lane a
-// row), the addend asked for a tile ahead.  By TMA boxes both stood in the TMA queue behind
+// row), the addend asked for half a tile ahead.  By TMA boxes both stood in the TMA queue behind
 // the operands of more than a tile: at m = 704, whose tiles have 11 k-blocks, 2800 of a
 // tile's 14000 clocks went by waiting for the addend, 2000 issuing the result; by the
 // lane that owns the row, 32 bytes at a time, each instruction took 32 lines (340 us for 96
@@ -161,16 +161,19 @@ struct Block {
   uint4 v[8];
 };
 __device__ __forceinline__ void load_block(Block& b, const char* p, int64_t ld, int rows, int lane) {
+  const char* at = p + (lane >> 3) * ld + (lane & 7) * 16;
+  const int there = rows - (lane >> 3);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = 4 * i + (lane >> 3);
-    b.v[i] = r < rows ? *reinterpret_cast<const uint4*>(p + r * ld + (lane & 7) * 16) : make_uint4(0, 0, 0, 0);
-  }
+  for (int i = 0; i < 8; ++i, at += 4 * ld)
+    b.v[i] = 4 * i < there ? *reinterpret_cast<const uint4*>(at) : make_uint4(0, 0, 0, 0);
 }
-// The block to and from a slice (put_piece's layout: piece j of row r at j ^ (r & 7)).
+// The block to and from a slice (put_piece's layout: piece j of row r at j ^ (r & 7)): where
+// this lane's part of rows 0 .. 3 stands; of rows 4 i on it is 512 i behind, with bit 2 of the
+// piece turned for odd i (a slice starts at a multiple of 128).
 __device__ __forceinline__ uint32_t block_at(uint32_t stage, int lane, int i) {
-  const int r = 4 * i + (lane >> 3);
-  return stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4);
+  const int r = lane >> 3;
+  const uint32_t at = stage + r * 128 + (((lane & 7) ^ r) << 4);
+  return (i & 1 ? at ^ 64u : at) + 512 * i;
 }
 __device__ __forceinline__ void block_to_slice(const Block& b, uint32_t stage, int lane) {
   __syncwarp();   // what the slice held has been read
@@ -194,11 +197,11 @@ __device__ __forceinline__ void slice_to_rows(uint32_t stage, char* p, int64_t l
   Block b;
 #pragma unroll
   for (int i = 0; i < 8; ++i) b.v[i] = load_piece(block_at(stage, lane, i));
+  char* at = p + (lane >> 3) * ld + (lane & 7) * 16;
+  const int there = rows - (lane >> 3);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int r = 4 * i + (lane >> 3);
-    if (r < rows) *reinterpret_cast<uint4*>(p + r * ld + (lane & 7) * 16) = b.v[i];
-  }
+  for (int i = 0; i < 8; ++i, at += 4 * ld)
+    if (4 * i < there) *reinterpret_cast<uint4*>(at) = b.v[i];
   __syncwarp();
 }
 // The transposed image of 64 columns: value j of this lane's row goes to row j of 64 bytes
@@ -415,17 +418,18 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
     };
     if constexpr (FORM != kTwo) {
       // One sum a tile, 16 columns at a time from TMEM through the slice.  A block of the
-      // addend is asked for as soon as the tile before has put its own into the slice.
-      Block hi[2], lo;
+      // addend is asked for as soon as the one before has gone into the slice: half a tile
+      // ahead, the 8-bit parts a tile (more would not fit into the registers).
+      Block hi, lo;
       auto ask_hi = [&](const Part& p, int h) {
         if (KIND != kGram)
-          load_block(hi[h], a.add + p.row * a.add_ld + 2 * (p.n0 + 64 * h), a.add_ld, p.n0 + 64 * h < width ? p.rows : 0,
+          load_block(hi, a.add + p.row * a.add_ld + 2 * (p.n0 + 64 * h), a.add_ld, p.n0 + 64 * h < width ? p.rows : 0,
                      lane);
       };
-      Block more[FORM == kOneTwice ? 2 : 1];
+      Block more;
       auto ask_more = [&](const Part& p, int h) {
         if (FORM == kOneTwice)
-          load_block(more[h], a.add2 + p.row * a.add_ld + 2 * (p.n0 + 64 * h), a.add_ld,
+          load_block(more, a.add2 + p.row * a.add_ld + 2 * (p.n0 + 64 * h), a.add_ld,
                      p.n0 + 64 * h < width ? p.rows : 0, lane);
       };
       auto ask_lo = [&](const Part& p) {
@@ -436,11 +440,7 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
       Part p = part_of(d), pn = p;
       ask_lo(p);
       ask_hi(p, 0);
-      ask_hi(p, 1);
-      if (FORM == kOneTwice) {
-        ask_more(p, 0);
-        ask_more(p, 1);
-      }
+      ask_more(p, 0);
       for (uint32_t t = first; t < total; t += step, d = dn, p = pn) {
         walk.next(a);
         if (walk.t < total) {
@@ -470,8 +470,8 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
         for (int h = 0; h < 2; ++h) {
           uint32_t second[FORM == kOneTwice ? 32 : 1];   // this lane's part of the second addend
           if (FORM == kOneTwice) {
-            block_to_slice(more[h], stage, lane);
-            ask_more(pn, h);
+            block_to_slice(more, stage, lane);
+            ask_more(h ? pn : p, h ^ 1);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const uint4 v = get_piece(stage, lane, j);
@@ -482,8 +482,8 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
             }
           }
           if (KIND != kGram) {
-            block_to_slice(hi[h], stage, lane);
-            ask_hi(pn, h);
+            block_to_slice(hi, stage, lane);
+            ask_hi(h ? pn : p, h ^ 1);
           }
           uint32_t w[32];      // 64 columns, packed
 #pragma unroll
@@ -499,29 +499,27 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
               const uint32_t h4[4] = {add.x, add.y, add.z, add.w};
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                float f0 = a.mul * __uint_as_float(r[k & 1][8 * g + 2 * e]);
-                float f1 = a.mul * __uint_as_float(r[k & 1][8 * g + 2 * e + 1]);
+                float2 f = mul2(both(a.mul), make_float2(__uint_as_float(r[k & 1][8 * g + 2 * e]),
+                                                         __uint_as_float(r[k & 1][8 * g + 2 * e + 1])));
                 if (KIND != kGram) {
                   float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h4[e]));
                   if (LOW_IN) {
-                    const uint32_t q2 = low[16 * h + 4 * c + 2 * g + e / 2] >> (e % 2 * 16);
-                    x.x = orth_with_low(x.x, (int)(int8_t)(q2 & 255u));
-                    x.y = orth_with_low(x.y, (int)(int8_t)((q2 >> 8) & 255u));
+                    const uint32_t part = low[16 * h + 4 * c + 2 * g + e / 2];
+                    x.x = orth_with_low(x.x, part, e % 2 * 2);
+                    x.y = orth_with_low(x.y, part, e % 2 * 2 + 1);
                   }
-                  f0 = fmaf(a.add_scale, x.x, f0);
-                  f1 = fmaf(a.add_scale, x.y, f1);
+                  f = fma2(both(a.add_scale), x, f);
                 }
                 if (FORM == kOneTwice) {
                   const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&second[8 * c + 4 * g + e]));
-                  f0 = fmaf(a.add2_scale, x.x, f0);
-                  f1 = fmaf(a.add2_scale, x.y, f1);
+                  f = fma2(both(a.add2_scale), x, f);
                 }
-                const uint32_t v = pack_half2(f0, f1);
+                const uint32_t v = pack_half2(f.x, f.y);
                 w[8 * c + 4 * g + e] = v;
                 if (LOW_OUT) {
                   const float2 lead = __half22float2(*reinterpret_cast<const __half2*>(&v));
-                  steps8[2 * e] = orth_low_steps(f0, lead.x);
-                  steps8[2 * e + 1] = orth_low_steps(f1, lead.y);
+                  steps8[2 * e] = orth_low_steps(f.x, lead.x);
+                  steps8[2 * e + 1] = orth_low_steps(f.y, lead.y);
                 }
               }
               const uint32_t* v = w + 8 * c + 4 * g;

@@ -117,10 +117,14 @@ moe_status moe_block_norm_backward(const moe_block_norm_shape *shape, const void
  * leaves the singular vectors.  A matrix of zeros stays zero; one with an
  * infinity or NaN becomes NaN, others in the batch do not see it.
  *
- * Precision: X is held in two fp16 parts (22 bits) under a fixed power of two,
- * which the bound below keeps in range.  bf16 matrices take one tensor-core
- * product of the leading parts (11 bits; a_i X_i uses both), fp32 matrices the
- * three products above 2^-22; sums in fp32.
+ * Precision: X is held under a fixed power of two, which the bounds below keep in
+ * range.  bf16 matrices: one tensor-core product of fp16 operands (11 bits), while
+ * a_i X_i takes X's 19 bits (an error outside X's row and column space grows by a_i
+ * in every step); an X whose later steps grow such an error by 4 or less keeps 11.
+ * Where n >= 2 m the first two of three or more steps are taken as one polynomial in
+ * A (its coefficients allowing).  fp32 matrices: X in two fp16 parts (22 bits), the
+ * three products above 2^-22.  A smaller side of at most 128 (up to a length): X in
+ * fp32 between the steps.  Sums in fp32.
  * ------------------------------------------------------------------------- */
 #define MOE_ORTH_MAX_STEPS 16
 

@@ -9,7 +9,10 @@
 // products see one shape.
 //
 // Bound by HBM: a bf16 parameter reads gradient and momentum twice (for the norm, then
-// for the scaled planes), writes the momentum, and passes once more for the update.
+// for the scaled planes), writes the momentum, and passes once more for the update.  Of 96
+// matrices 704 x 2816, a third of them transposed, the momentum takes 285 us (6.7 TB/s), the
+// planes 320 (5.4), the update 239 (4.8).  Tiles of 64 x 128 instead of 64 x 64: planes 317,
+// update 359 (two blocks an SM instead of four).
 #include <algorithm>
 #include <cmath>
 

@@ -35,6 +35,12 @@
 // lane that owns the row, 32 bytes at a time, each instruction took 32 lines (340 us for 96
 // matrices 704 x 2816 against 312).
 //
+// At 704 x 2816 (96 matrices): kGram 126 us, kPoly 49 to 54 (with two addends 65), kApply 260
+// with both 8-bit parts, 217 and 193 without; 2.46 ms for five steps, 0.47 of the tensor cores' measured
+// rate by the formula's flops.  kGram is bound by the products (a k-block of a pair takes 650 clocks, what
+// 256 x 256 x 64 takes at the peak), kApply and kPoly by their epilogues: with 11 k-blocks a tile's
+// products take 7100 clocks, kApply's epilogue 9000 to 12000.
+//
 // Roles in each CTA: warp 0 TMA producer, warp 1 TMEM and (even CTA) the MMA
 // issuer, warps 4-11 epilogue, two a 32-lane TMEM quarter.  Tiles are dealt out in a
 // fixed order (all have the same K).  The sums of fp32 matrices leave TMEM in chunks of

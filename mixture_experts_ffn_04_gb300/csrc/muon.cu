@@ -380,7 +380,7 @@ Bucket bucket_of(int m, int n, int planes, int64_t batch) {
 }
 
 struct RoundLayout {
-  size_t sums, x[2], a, b, c, total;
+  size_t sums, x[2], a, b, c, parts, total;
 };
 RoundLayout layout_of(const Bucket& q) {
   RoundLayout L = {};
@@ -397,6 +397,7 @@ RoundLayout layout_of(const Bucket& q) {
   L.a = take((size_t)q.round * q.planes * q.m * q.lda * 2);
   L.b = take((size_t)q.round * q.planes * q.m * q.lda * 2);
   L.c = take(q.pair ? (size_t)q.round * q.planes * q.m * q.lda * 2 : 0);
+  L.parts = take(orth_parts_bytes(q.round, q.m, q.n, q.planes));
   L.total = off;
   return L;
 }
@@ -488,6 +489,7 @@ cudaError_t run_round(Round& r, const Bucket& q, const RoundLayout& L, char* ws,
   t.a = ws + L.a;
   t.b = ws + L.b;
   t.c = q.pair && pair_fits(c) ? ws + L.c : nullptr;
+  t.parts = reinterpret_cast<float*>(ws + L.parts);
   t.flags = reinterpret_cast<uint32_t*>(ws);
   int last = 0;
   e = launch_orth_steps(t, c.steps, c.coef, &last, st);

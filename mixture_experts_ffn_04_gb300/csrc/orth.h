@@ -17,7 +17,8 @@ constexpr double kOrthMaxX = 3.5, kOrthMaxB = 100.0, kOrthMaxR = 200.0;
 // A batch in scratch.  x[0], x[1]: [planes][batch][m][ldx] each, with one plane the 8-bit
 // parts [batch][m][ldx] behind it; a, b, c: [planes][batch][m][lda]; ldx a multiple of 128, lda of
 // 64 (columns past m and n, up to there, are written, and read only into themselves).
-// c: NULL, or (one plane) the first two steps go in one where steps follow them.
+// c: NULL, or (one plane) the first two steps go in one where steps follow them.  parts: of
+// orth_parts_bytes.
 struct OrthBatch {
   int64_t batch;
   int m, n, ldx, lda;
@@ -26,6 +27,7 @@ struct OrthBatch {
   void* a;
   void* b;
   void* c;
+  float* parts;
   uint32_t* flags;
 };
 
@@ -54,6 +56,12 @@ __device__ __forceinline__ float orth_with_low(float h, uint32_t low, int at) {
   return __int_as_float(__dp4a((int)low, 32 << (8 * at), __float_as_int(h)));
 }
 #endif
+
+// Pieces that the sums of A = X X^T are cut into along n, where the tiles of `batch` matrices
+// leave most of the GPU without one (1: whole); bytes of their partial sums for any batch of
+// at most `most` (0: whole).
+int orth_split(int64_t batch, int m, int n, int planes);
+size_t orth_parts_bytes(int64_t most, int m, int n, int planes);
 
 // `steps` times X <- a X + (b A + c A A) X with (a, b, c) = coef[i], from x[0]; the
 // last X is in x[*last], of bf16 matrices without 8-bit parts.

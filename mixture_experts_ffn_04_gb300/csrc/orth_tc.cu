@@ -26,6 +26,10 @@
 // products of two planes each, smallest first: 5.7e-7 (fp32 products: 7.2e-6), from stages with
 // both planes of both operands.
 //
+// Few matrices with a long side (fewer tiles of A than half of the pairs of SMs) have kGram's
+// sums cut into pieces along n, fp32 partial tiles that join_kernel adds in order (2 matrices 731
+// x 8026 in fp32, 12 tiles: 1065 us for five steps whole, 725 in pieces).
+//
 // A pair of SMs computes 256 x 256 tiles over 64-wide k-blocks through six 32 KB
 // stages (three of 64 KB).  Addend and result go between registers and memory as whole 128-byte rows, turned
 // in a 4 KB slice of each epilogue warp between that layout and the one of TMEM (a lane a
@@ -47,6 +51,7 @@
 // k-blocks, added in fp32 registers (the tensor cores cut the accumulator off at each K = 16
 // step); with operands of 11 bits it would not show.  Every wait on an mbarrier is bounded,
 // and a CTA that gives up waits, with a limit, for its copies and MMAs in flight.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cuda.h>
@@ -101,6 +106,8 @@ struct Args {
   float add_scale, mul;   // result = add_scale * addend + mul * product
   const char* add;        // the addend's leading plane, rows add_ld bytes apart
   const char* add_low;    // its second plane, or its 8-bit parts
+  int split;              // kGram: pieces of a tile's sum, neighbours in the tiles' order
+  float* parts;           // [tiles][split][256][256] of them
   const char* add2;       // kOneTwice: the second addend
   float add2_scale;
   char* out;              // the result, the same
@@ -110,11 +117,11 @@ struct Args {
 };
 
 struct Tile {
-  int b, i, j;
+  int b, i, j, piece;
 };
 // A pair's tiles: every `step`th of all matrices' tiles, from its own.  Divisions by the
 // number of tiles of a matrix are done once.
-template <int KIND>
+template <int KIND, bool SPLIT = false>
 struct Walk {
   uint32_t t, l, b;             // tile; place in its matrix; matrix
   uint32_t step, step_l, step_b;
@@ -138,6 +145,7 @@ struct Walk {
   __device__ __forceinline__ Tile tile(const Args& a) const {
     Tile r;
     r.b = (int)b;
+    r.piece = 0;
     if (KIND == kApply) {
       int j = (int)((float)l * inv);      // within one of l / mt
       int i = (int)l - j * a.mt;
@@ -146,6 +154,12 @@ struct Walk {
       r.i = i;
       r.j = j;
     } else {
+      uint32_t l = this->l;
+      if (SPLIT) {
+        const uint32_t whole = l / (uint32_t)a.split;
+        r.piece = (int)(l - whole * (uint32_t)a.split);
+        l = whole;
+      }
       // row i of the lower triangle starts at i (i + 1) / 2
       int i = (int)((sqrtf(8.0f * (float)l + 1.0f) - 1.0f) * 0.5f);
       while ((uint32_t)i * (i + 1) / 2 > l) --i;
@@ -243,7 +257,8 @@ struct Maps {
   CUtensorMap A, B;
 };
 
-template <int KIND, int FORM>
+// SPLIT: kGram's sums in pieces, which go to a.parts.
+template <int KIND, int FORM, bool SPLIT = false>
 __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant__ Maps maps, const Args a) {
   // two planes: a stage has both of both operands, for the three products
   constexpr int PL = FORM == kTwo ? 2 : 1, S = MAX_STAGES / PL, STAGE_BYTES = PL * (A_BYTES + B_BYTES);
@@ -306,10 +321,12 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
       uint32_t ph = 0, issued = 0;
       bool ok = true;
       const uint32_t full0 = map_to_rank(full(0), 0);   // the even CTA's "full" barriers
-      for (Walk<KIND> walk(a, first, step); ok && walk.t < total; walk.next(a)) {
+      for (Walk<KIND, SPLIT> walk(a, first, step); ok && walk.t < total; walk.next(a)) {
         const Tile q = walk.tile(a);
         const int arow = q.i * BM + (int)rank * BMC, bcol = q.j * BN + (int)rank * BNC;
-        for (int k = 0; k < a.kb * BK; k += BK) {
+        // (a piece's last k-blocks may lie past n: zeros)
+        const int k0 = SPLIT ? q.piece * a.kb * BK : 0;
+        for (int k = k0; k < k0 + a.kb * BK; k += BK) {
           if (!wait_cl(empty(s), ph ^ 1u, abort_flag)) { ok = false; break; }
           const uint32_t sa = ring + s * STAGE_BYTES, sb = sa + PL * A_BYTES, fb = full0 + 8u * s;
           if (leader) mbar_expect_tx(full(s), 2 * STAGE_BYTES);
@@ -422,7 +439,27 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
     auto mirror = [&](char* out, const Tile& d, const Part& p, int col, const uint32_t (&w)[32]) {
       mirror_rows(stage, w, out + ((int64_t)d.b * a.m + col) * a.add_ld + 2 * p.r0, a.add_ld, a.m - col, lane);
     };
-    if constexpr (FORM != kTwo) {
+    // a lane's row of a partial tile
+    auto part_row = [&](uint32_t t) {
+      return a.parts + ((size_t)t * BM + (int)rank * BMC + q * 32 + lane) * BN + c_lo;
+    };
+    if constexpr (SPLIT && FORM == kOne) {
+      for (uint32_t t = first; t < total; t += step) {
+        if (!wait_acc()) break;
+        float4* to = reinterpret_cast<float4*>(part_row(t));
+#pragma unroll
+        for (int c = 0; c < EPI_COLS / 32; ++c) {
+          uint32_t r[32];
+          tmem_ld32(tmem_at() + 32 * c, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            to[8 * c + j] = make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
+                                        __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3]));
+        }
+        free_acc();
+      }
+    } else if constexpr (FORM != kTwo) {
       // One sum a tile, 16 columns at a time from TMEM through the slice.  A block of the
       // addend is asked for as soon as the one before has gone into the slice: half a tile
       // ahead, the 8-bit parts a tile (more would not fit into the registers).
@@ -552,7 +589,7 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
         }
       }
     } else {
-      for (Walk<KIND> walk(a, first, step); ok && walk.t < total; walk.next(a)) {
+      for (Walk<KIND, SPLIT> walk(a, first, step); ok && walk.t < total; walk.next(a)) {
         const Tile d = walk.tile(a);
         const Part p = part_of(d);
         float f[EPI_COLS];
@@ -586,6 +623,7 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
         }
 #pragma unroll 1
         for (int i0 = 0; i0 < steps; i0 += chunk) {
+          const float mul = SPLIT ? 1.0f : a.mul;   // the parts are bare sums
           if (!wait_acc()) break;
           const uint32_t taddr = tmem_at();
 #pragma unroll
@@ -594,11 +632,17 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
             tmem_ld32(taddr + c, r);
             tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) f[c + j] = fmaf(a.mul, __uint_as_float(r[j]), f[c + j]);
+            for (int j = 0; j < 32; ++j) f[c + j] = fmaf(mul, __uint_as_float(r[j]), f[c + j]);
           }
           free_acc();
         }
         if (!ok) break;
+        if constexpr (SPLIT) {
+          float4* to = reinterpret_cast<float4*>(part_row(walk.t));
+#pragma unroll
+          for (int j = 0; j < EPI_COLS / 4; ++j) to[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+          continue;
+        }
         if (p.rows <= 0) continue;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -644,6 +688,56 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
   if (threadIdx.x == 0 && *abort_flag) set_flag(a.flags, kFlagTimeout);
 }
 
+// A tile of A from its pieces, added in order, to the planes and below the diagonal to its
+// mirror image: 32 x 32 elements a block, four a thread.
+template <int PLANES>
+__global__ void __launch_bounds__(256) join_kernel(const Args a, int lda) {
+  __shared__ float sh[32][33];
+  pdl_trigger();
+  pdl_wait();
+  Args whole = a;
+  whole.split = 1;
+  whole.per = a.per / a.split;
+  const uint32_t t = blockIdx.x >> 6;
+  const Tile d = Walk<kPoly>(whole, t, 1).tile(whole);
+  const int r0 = (blockIdx.x >> 3 & 7) * 32, c0 = (blockIdx.x & 7) * 32;
+  const int row0 = d.i * BM + r0, col0 = d.j * BN + c0;
+  if (row0 >= a.m || col0 >= a.m) return;
+  const int r = threadIdx.x >> 3, c = (threadIdx.x & 7) * 4;
+  const float* p = a.parts + (size_t)t * a.split * BM * BN + (size_t)(r0 + r) * BN + c0 + c;
+  float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int s = 0; s < a.split; ++s) {
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(p + (size_t)s * BM * BN));
+    f[0] += v.x;
+    f[1] += v.y;
+    f[2] += v.z;
+    f[3] += v.w;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) f[e] *= a.mul;
+  auto put = [&](int row, int col) {     // columns past m go to the rows' padding
+    if (row >= a.m || col >= lda) return;
+    const int64_t at = ((int64_t)d.b * a.m + row) * a.add_ld + 2 * col;
+    const uint32_t h[2] = {pack_half2(f[0], f[1]), pack_half2(f[2], f[3])};
+    *reinterpret_cast<uint2*>(a.out + at) = make_uint2(h[0], h[1]);
+    if (PLANES == 2) {
+      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h[0]));
+      const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&h[1]));
+      *reinterpret_cast<uint2*>(a.out_low + at) =
+          make_uint2(pack_half2(f[0] - x.x, f[1] - x.y), pack_half2(f[2] - y.x, f[3] - y.y));
+    }
+  };
+  put(row0 + r, col0 + c);
+  if (d.i == d.j) return;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sh[r][c + e] = f[e];
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < 4; ++e) f[e] = sh[c + e][r];
+  put(col0 + r, row0 + c);
+}
+
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
@@ -670,7 +764,8 @@ static cudaError_t prepare_device(int* clusters) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (g_clusters[dev] == 0) {
-    const void* fn[] = {(const void*)orth_kernel<kPoly, kOneTwice>,
+    const void* fn[] = {(const void*)orth_kernel<kPoly, kOneTwice>, (const void*)orth_kernel<kGram, kOne, true>,
+                         (const void*)orth_kernel<kGram, kTwo, true>,
                          (const void*)orth_kernel<kGram, kOne>,  (const void*)orth_kernel<kGram, kTwo>,
                          (const void*)orth_kernel<kPoly, kOne>,  (const void*)orth_kernel<kPoly, kTwo>,
                          (const void*)orth_kernel<kApply, kLow>, (const void*)orth_kernel<kApply, kLowIn>,
@@ -700,7 +795,7 @@ static cudaError_t prepare_device(int* clusters) {
   return *clusters > 0 ? cudaSuccess : cudaErrorNotSupported;
 }
 
-template <int KIND, int FORM>
+template <int KIND, int FORM, bool SPLIT = false>
 static cudaError_t launch(const Maps& maps, const Args& t, cudaStream_t st) {
   int mc = 0;
   cudaError_t e = prepare_device(&mc);
@@ -709,10 +804,36 @@ static cudaError_t launch(const Maps& maps, const Args& t, cudaStream_t st) {
   if (tiles <= 0) return cudaSuccess;
   if (tiles >= (1ll << 31)) return cudaErrorInvalidValue;
   const unsigned pairs = (unsigned)(tiles < mc ? tiles : mc);
-  return launch_after(orth_kernel<KIND, FORM>, 2 * pairs, THREADS, SMEM_BYTES, st, 2, maps, t);
+  return launch_after(orth_kernel<KIND, FORM, SPLIT>, 2 * pairs, THREADS, SMEM_BYTES, st, 2, maps, t);
 }
 
+static int gram_tiles(int m) {
+  const int mt = (m + BM - 1) / BM;
+  return mt * (mt + 1) / 2;
+}
 }  // namespace orth
+
+// As many pieces as fill the pairs, of at least 8 k-blocks of 64, where the whole sum is long
+// enough to pay for the partial tiles and their join: five steps with and without, 1 x 300 x 2200
+// in fp32 264 us against 345, 4 x 55 x 3670 242 against 390, 2 x 731 x 8026 725 against 1065
+// (bf16 395 against 465); bf16 1 x 704 x 2816 236 against 242, 1 x 300 x 1100 187 against 170,
+// fp32 3 x 777 x 1001 388 against 390.
+int orth_split(int64_t batch, int m, int n, int planes) {
+  using namespace orth;
+  constexpr int kPairs = 76, kLeast = 8, kLong = 48;   // fixed, so that the sums do not depend on the device
+  const int64_t tiles = batch * gram_tiles(m), kb = (n + BK - 1) / BK;
+  if (tiles <= 0 || 2 * tiles > kPairs || planes * kb < kLong) return 1;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(kPairs / tiles, kb / kLeast));
+}
+size_t orth_parts_bytes(int64_t most, int m, int n, int planes) {
+  int64_t tiles = 0;
+  for (int64_t b = 1; b <= most; ++b) {
+    const int split = orth_split(b, m, n, planes);
+    if (split > 1) tiles = std::max<int64_t>(tiles, b * orth::gram_tiles(m) * split);
+    else break;   // nor does any larger batch
+  }
+  return (size_t)tiles * orth::BM * orth::BN * 4;
+}
 
 cudaError_t launch_orth_steps(const OrthBatch& t, int steps, const double (*coef)[3], int* last, cudaStream_t st) {
   using namespace orth;
@@ -761,19 +882,29 @@ cudaError_t launch_orth_steps(const OrthBatch& t, int steps, const double (*coef
     if (two) return launch<kPoly, kTwo>(maps, g, st);
     return add2 ? launch<kPoly, kOneTwice>(maps, g, st) : launch<kPoly, kOne>(maps, g, st);
   };
+  const int split = t.parts ? orth_split(B, t.m, t.n, t.planes) : 1;
+  g.parts = t.parts;
   auto two_to = [](int e) { return std::ldexp(1.0, e); };
   bool low = true;     // x[0] has its 8-bit parts
   int at = 0;          // the buffer that X is in
   for (int i = 0; i < steps; at ^= 1) {
     char *from = static_cast<char*>(t.x[at]), *to = static_cast<char*>(t.x[at ^ 1]);
     // A = X X^T
-    g.kb = (t.n + BK - 1) / BK;
-    g.per = g.mt * (g.mt + 1) / 2;
+    g.split = split;
+    g.kb = ((t.n + BK - 1) / BK + split - 1) / split;
+    g.per = gram_tiles(t.m) * split;
     g.mul = ldexpf(1.0f, kOrthA - 2 * kOrthX);
     g.add_ld = g.low_ld = a_ld;
     g.out = pa;
     g.out_low = pa + rows * a_ld;
-    cudaError_t e = two ? launch<kGram, kTwo>(gram[at], g, st) : launch<kGram, kOne>(gram[at], g, st);
+    cudaError_t e;
+    if (split > 1) e = two ? launch<kGram, kTwo, true>(gram[at], g, st) : launch<kGram, kOne, true>(gram[at], g, st);
+    else e = two ? launch<kGram, kTwo>(gram[at], g, st) : launch<kGram, kOne>(gram[at], g, st);
+    if (e == cudaSuccess && split > 1) {
+      const unsigned blocks = (unsigned)(B * gram_tiles(t.m) * 64);
+      e = two ? launch_after(join_kernel<2>, blocks, 256, 0, st, 1, g, t.lda)
+              : launch_after(join_kernel<1>, blocks, 256, 0, st, 1, g, t.lda);
+    }
     if (e != cudaSuccess) return e;
     // B = b A + c A A, the polynomial in the planes that the product reads
     const double *c0 = coef[i], *c1 = coef[i + 1 < steps ? i + 1 : i];

@@ -295,3 +295,30 @@ def test_bad_wide_matrices_stay_alone(m, shape):
     assert float(got[1].abs().max()) == 0.0
     assert bool(got[2].isnan().all()) and bool(got[4].isnan().all())
     assert torch.equal(got[0], clean[0]) and torch.equal(got[3], clean[3])
+
+
+# few matrices with a long side: A's sums in pieces
+LONG = [(1, 129, 4100), (2, 300, 2500), (1, 700, 5000), (6, 260, 1030), (1, 9000, 140), (37, 130, 1100), (1, 1030, 1100)]
+
+
+@pytest.mark.parametrize("shape", LONG)
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_long_sides(m, shape, dt):
+    u = draw(shape, dt, seed=sum(shape))
+    op = m.Orthogonalize(*shape, dtype=dt)
+    got = op.forward(u)
+    close(got, u)
+    assert torch.equal(op.forward(u), got)
+    # the workspace of a call of another batch in between
+    two = m.Orthogonalize(*shape, dtype=dt)
+    two.forward(-u)
+    assert torch.equal(two.forward(u), got) and two.device_status() == (0, 0)
+
+
+def test_long_sides_in_a_list(m):
+    """More tensors than a launch carries: rounds of different sizes."""
+    gs = [draw((1, 200, 1200) if i % 2 else (1, 1200, 200), torch.float32, seed=i) for i in range(19)]
+    ps = [torch.zeros_like(g) for g in gs]
+    m.Muon(ps, gs, lr=0.1, momentum=0.0, nesterov=False, scale="none").step()
+    for p, g in zip(ps, gs):
+        close(p / -0.1, g)   # of zeros: two more roundings of the direction

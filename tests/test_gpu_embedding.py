@@ -181,3 +181,20 @@ def test_one_workspace_for_many_shapes_a_stream_and_a_graph(m):
     torch.cuda.synchronize()
     assert torch.equal(y, w[ids.long()])
     close_rows(dw, ids, dy, 5000, 1.0, None, None)
+
+
+FEW = [  # around the number of tokens that need no sorted list
+    (64, 5, 264, "few", "bf16", 1.0, None, "in"), (64, 1, 2048, "one", "f32", 0.5, None, None),
+    (63, 1000, 7168, "skewed", "bf16", 1.0, 0, "out"), (65, 1000, 520, "skewed", "bf16", 1.0, 0, "out"),
+    (40, 33, 8, "any", "f32", 3.0, 7, "in"), (64, 70001, 40, "any", "bf16", 1.0, None, None),
+    (2, 2, 16, "one", "f32", 1.0, None, "out"), (33, 9, 1288, "one", "bf16", 1.0, 4, "out")]
+
+
+@pytest.mark.parametrize("T,V,H,kind,dtype,scale,pad,add", FEW)
+def test_few_tokens(m, T, V, H, kind, dtype, scale, pad, add):
+    test_lookup_and_gradient(m, T, V, H, kind, dtype, scale, pad, add)
+
+
+@pytest.mark.parametrize("T", [5, 64, 65])
+def test_few_tokens_out_of_range(m, T):
+    test_ids_out_of_range(m, T)

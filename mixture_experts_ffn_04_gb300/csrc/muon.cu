@@ -11,8 +11,8 @@
 // Bound by HBM: a bf16 parameter reads gradient and momentum twice (for the norm, then
 // for the scaled planes), writes the momentum, and passes once more for the update.  Of 96
 // matrices 704 x 2816, a third of them transposed, the momentum takes 285 us (6.7 TB/s), the
-// planes 320 (5.4), the update 239 (4.8).  Tiles of 64 x 128 instead of 64 x 64: planes 317,
-// update 359 (two blocks an SM instead of four).
+// planes 282 (6.1; with three blocks an SM instead of four 320), the update 239 (4.8).  Tiles of 64 x 128 instead of 64 x 64: planes 317,
+// update 359 (two blocks an SM).
 #include <algorithm>
 #include <cmath>
 
@@ -123,7 +123,13 @@ __global__ void __launch_bounds__(256) momentum_kernel(const __grid_constant__ R
   }
 }
 
+// ALL16: gradients and parameters are bf16 in every segment, which leaves registers for more
+// blocks an SM.
+template <bool ALL16>
+__device__ __forceinline__ int type_of(int dtype) { return ALL16 ? (int)MOE_BF16 : dtype; }
+
 // 8 values to X, from `at` elements of the round's first plane.
+template <bool ALL16>
 __device__ __forceinline__ void put8(const Round& r, int64_t at, const float* f) {
   uint32_t h[4];
   float lead[8];
@@ -137,7 +143,7 @@ __device__ __forceinline__ void put8(const Round& r, int64_t at, const float* f)
   }
   *reinterpret_cast<uint4*>(r.x + at) = make_uint4(h[0], h[1], h[2], h[3]);
   const int64_t plane = (int64_t)r.batch * r.m * r.ldx;
-  if (r.planes == 2) {
+  if (!ALL16 && r.planes == 2) {
     uint32_t l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -155,6 +161,7 @@ __device__ __forceinline__ void put8(const Round& r, int64_t at, const float* f)
   }
 }
 // 8 values of the last X (which has no 8-bit parts: no step is left to need them).
+template <bool ALL16>
 __device__ __forceinline__ void get8(const Round& r, int64_t at, float* f) {
   const uint4 hi = *reinterpret_cast<const uint4*>(r.x + at);
   const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w};
@@ -165,7 +172,7 @@ __device__ __forceinline__ void get8(const Round& r, int64_t at, float* f) {
     f[2 * i + 1] = a.y;
   }
   const int64_t plane = (int64_t)r.batch * r.m * r.ldx;
-  if (r.planes == 2) {
+  if (!ALL16 && r.planes == 2) {
     const uint4 lo = *reinterpret_cast<const uint4*>(r.x + plane + at);
     const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w};
 #pragma unroll
@@ -197,7 +204,8 @@ __device__ __forceinline__ TileAt tile_at(const Round& r, int64_t task, const Se
 }
 
 // u / (norm + eps) as X is held, its smaller side as rows.
-__global__ void __launch_bounds__(256) planes_kernel(const __grid_constant__ Round r) {
+template <bool ALL16>
+__global__ void __launch_bounds__(256, ALL16 ? 4 : 3) planes_kernel(const __grid_constant__ Round r) {
   __shared__ float sh[kTile][kTile + 1];
   __shared__ double part[8];
   __shared__ float2 factor;
@@ -241,7 +249,7 @@ __global__ void __launch_bounds__(256) planes_kernel(const __grid_constant__ Rou
         const int row = t.r0 + k * 32 + tid / 8, col = t.c0 + tid % 8 * 8;
         const bool there = row < s->rows && col < s->cols;
         const int64_t at = base + (int64_t)row * s->cols + col;
-        g[k] = load_raw(s->grad, s->gdtype, at, there);
+        g[k] = load_raw(s->grad, type_of<ALL16>(s->gdtype), at, there);
         v[k] = load_raw(s->momentum, MOE_F32, at, there && s->momentum != nullptr);
       }
 #pragma unroll
@@ -253,11 +261,11 @@ __global__ void __launch_bounds__(256) planes_kernel(const __grid_constant__ Rou
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = m[e] = 0.0f;
       if (ok) {
-        open_raw(g[k], s->gdtype, f);
+        open_raw(g[k], type_of<ALL16>(s->gdtype), f);
         open_raw(v[k], MOE_F32, m);
       } else if (n > 0) {
         const int64_t at = base + (int64_t)row * s->cols + col;
-        read8(s->grad, s->gdtype, at, n, false, f);
+        read8(s->grad, type_of<ALL16>(s->gdtype), at, n, false, f);
         if (s->momentum != nullptr) read8(s->momentum, MOE_F32, at, n, false, m);
       }
 #pragma unroll
@@ -266,7 +274,7 @@ __global__ void __launch_bounds__(256) planes_kernel(const __grid_constant__ Rou
         f[e] = f[e] * q.x * q.y;
       }
       if (!tall) {
-        if (n > 0) put8(r, x + (int64_t)row * r.ldx + col, f);
+        if (n > 0) put8<ALL16>(r, x + (int64_t)row * r.ldx + col, f);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) sh[lr][lc + e] = e < n ? f[e] : 0.0f;
@@ -282,12 +290,13 @@ __global__ void __launch_bounds__(256) planes_kernel(const __grid_constant__ Rou
       float f[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = sh[lc + e][lr];
-      put8(r, x + (int64_t)row * r.ldx + col, f);
+      put8<ALL16>(r, x + (int64_t)row * r.ldx + col, f);
     }
   }
 }
 
 // param = keep param - size X, or out = X.
+template <bool ALL16>
 __global__ void __launch_bounds__(256) update_kernel(const __grid_constant__ Round r) {
   __shared__ float sh[kTile][kTile + 1];
   pdl_trigger();
@@ -308,7 +317,7 @@ __global__ void __launch_bounds__(256) update_kernel(const __grid_constant__ Rou
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int row = t.r0 + k * 32 + tid / 8, col = t.c0 + tid % 8 * 8;
-        w[k] = load_raw(s->param, s->pdtype, base + (int64_t)row * s->cols + col, row < s->rows && col < s->cols);
+        w[k] = load_raw(s->param, type_of<ALL16>(s->pdtype), base + (int64_t)row * s->cols + col, row < s->rows && col < s->cols);
       }
     if (tall) __syncthreads();   // the last tile's readers are done
 #pragma unroll
@@ -316,7 +325,7 @@ __global__ void __launch_bounds__(256) update_kernel(const __grid_constant__ Rou
       const int lr = k * 32 + tid / 8, lc = tid % 8 * 8;
       const int row = (tall ? t.c0 : t.r0) + lr, col = (tall ? t.r0 : t.c0) + lc;
       if (row >= r.m || col >= r.n) continue;
-      get8(r, x + (int64_t)row * r.ldx + col, f[k]);
+      get8<ALL16>(r, x + (int64_t)row * r.ldx + col, f[k]);
       if (tall)
 #pragma unroll
         for (int e = 0; e < 8; ++e) sh[lc + e][lr] = f[k][e];
@@ -335,12 +344,12 @@ __global__ void __launch_bounds__(256) update_kernel(const __grid_constant__ Rou
       }
       if (r.update) {
         float p[8];
-        if (ok) open_raw(w[k], s->pdtype, p);
-        else read8(s->param, s->pdtype, at, n, false, p);
+        if (ok) open_raw(w[k], type_of<ALL16>(s->pdtype), p);
+        else read8(s->param, type_of<ALL16>(s->pdtype), at, n, false, p);
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[k][e] = fmaf(-s->size, f[k][e], r.keep * p[e]);
       }
-      write8(s->param, s->pdtype, at, n, ok, f[k]);
+      write8(s->param, type_of<ALL16>(s->pdtype), at, n, ok, f[k]);
     }
   }
 }
@@ -475,7 +484,9 @@ cudaError_t run_round(Round& r, const Bucket& q, const RoundLayout& L, char* ws,
                                st, 1, r);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)std::min<int64_t>(tiles, 16 * sms);
-  e = launch_after(planes_kernel, grid, 256, 0, st, 1, r);
+  bool all16 = true;
+  for (int i = 0; i < r.segs; ++i) all16 = all16 && r.seg[i].pdtype == MOE_BF16 && r.seg[i].gdtype == MOE_BF16;
+  e = all16 ? launch_after(planes_kernel<true>, grid, 256, 0, st, 1, r) : launch_after(planes_kernel<false>, grid, 256, 0, st, 1, r);
   if (e != cudaSuccess) return e;
   OrthBatch t = {};
   t.batch = r.batch;
@@ -495,7 +506,8 @@ cudaError_t run_round(Round& r, const Bucket& q, const RoundLayout& L, char* ws,
   e = launch_orth_steps(t, c.steps, c.coef, &last, st);
   if (e != cudaSuccess) return e;
   r.x = reinterpret_cast<__half*>(ws + L.x[last]);
-  return launch_after(update_kernel, grid, 256, 0, st, 1, r);
+  return all16 ? launch_after(update_kernel<true>, grid, 256, 0, st, 1, r)
+               : launch_after(update_kernel<false>, grid, 256, 0, st, 1, r);
 }
 
 moe_status check_list(const moe_muon_tensor* t, int64_t n, const moe_muon_config* c, const char** why) {

@@ -30,7 +30,7 @@
 // sums cut into pieces along n, fp32 partial tiles that join_kernel adds in order (2 matrices 731
 // x 8026 in fp32, 12 tiles: 1065 us for five steps whole, 725 in pieces).
 //
-// A pair of SMs computes 256 x 256 tiles over 64-wide k-blocks through six 32 KB
+// A pair of SMs computes 256 x 256 tiles (256 x 128 where there are few) over 64-wide k-blocks through six 32 KB
 // stages (three of 64 KB).  Addend and result go between registers and memory as whole 128-byte rows, turned
 // in a 4 KB slice of each epilogue warp between that layout and the one of TMEM (a lane a
 // row), the addend asked for half a tile ahead.  By TMA boxes both stood in the TMA queue behind
@@ -78,7 +78,7 @@ constexpr int A_BYTES = BMC * BK * 2, B_BYTES = BNC * BK * 2;   // of a plane
 constexpr int BOX_BYTES = 64 * BK * 2;
 constexpr int RING_BYTES = 6 * (A_BYTES + B_BYTES);              // six stages of a plane, three of two
 constexpr int MAX_STAGES = 6;
-constexpr int EPI_WARPS = 8, EPI_COLS = 128;   // a warp: 32 rows, 128 columns
+constexpr int EPI_WARPS = 8;   // a warp: 32 rows, half of the columns
 constexpr int THREADS = 32 * (4 + EPI_WARPS);
 // 168 registers a thread at launch; 56 + 2 * 224 <= 3 * 168 (three groups of 4 warps)
 constexpr int ROLE_REGS = 56, EPI_REGS = 224;
@@ -92,8 +92,8 @@ static_assert((2 * MAX_STAGES + 5) * 8 + 8 <= BAR_BYTES, "barrier area");
 constexpr long long kDrainCycles = 1 << 21;
 constexpr int kChunkExact = 3;   // k-blocks of 64, three products each
 
-// kind::f16: D fp32, A and B fp16, M = 256 over the pair, N = 256.
-constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+// kind::f16: D fp32, A and B fp16, M = 256 over the pair, N = n.
+__host__ __device__ constexpr uint32_t idesc_of(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(BM >> 4) << 24); }
 constexpr uint32_t IDESC_B_MN = 1u << 16;
 
 enum Kind { kGram = 0, kPoly = 1, kApply = 2 };
@@ -121,7 +121,8 @@ struct Tile {
 };
 // A pair's tiles: every `step`th of all matrices' tiles, from its own.  Divisions by the
 // number of tiles of a matrix are done once.
-template <int KIND, bool SPLIT = false>
+// NARROW: each tile of kGram and kPoly as two of 128 columns.
+template <int KIND, bool SPLIT = false, bool NARROW = false>
 struct Walk {
   uint32_t t, l, b;             // tile; place in its matrix; matrix
   uint32_t step, step_l, step_b;
@@ -160,12 +161,15 @@ struct Walk {
         r.piece = (int)(l - whole * (uint32_t)a.split);
         l = whole;
       }
+      const uint32_t side = l & 1u;
+      if (NARROW) l >>= 1;
       // row i of the lower triangle starts at i (i + 1) / 2
       int i = (int)((sqrtf(8.0f * (float)l + 1.0f) - 1.0f) * 0.5f);
       while ((uint32_t)i * (i + 1) / 2 > l) --i;
       while ((uint32_t)(i + 1) * (i + 2) / 2 <= l) ++i;
       r.i = i;
       r.j = (int)(l - (uint32_t)i * (i + 1) / 2);
+      if (NARROW) r.j = 2 * r.j + (int)side;
     }
     return r;
   }
@@ -257,9 +261,12 @@ struct Maps {
   CUtensorMap A, B;
 };
 
-// SPLIT: kGram's sums in pieces, which go to a.parts.
-template <int KIND, int FORM, bool SPLIT = false>
+// SPLIT: kGram's sums in pieces, which go to a.parts.  NB: columns of a tile.
+template <int KIND, int FORM, bool SPLIT = false, int NB = 256>
 __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant__ Maps maps, const Args a) {
+  constexpr int BN = NB, BNC = BN / 2, B_BYTES = BNC * BK * 2, EPI_COLS = BN / 2;
+  constexpr bool NARROW = NB == 128;
+  static_assert(!NARROW || (KIND != kApply && !SPLIT), "kGram and kPoly alone have tiles of 128 columns");
   // two planes: a stage has both of both operands, for the three products
   constexpr int PL = FORM == kTwo ? 2 : 1, S = MAX_STAGES / PL, STAGE_BYTES = PL * (A_BYTES + B_BYTES);
   constexpr bool LOW_IN = FORM == kLow || FORM == kLowIn, LOW_OUT = FORM == kLow;
@@ -321,7 +328,7 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
       uint32_t ph = 0, issued = 0;
       bool ok = true;
       const uint32_t full0 = map_to_rank(full(0), 0);   // the even CTA's "full" barriers
-      for (Walk<KIND, SPLIT> walk(a, first, step); ok && walk.t < total; walk.next(a)) {
+      for (Walk<KIND, SPLIT, NARROW> walk(a, first, step); ok && walk.t < total; walk.next(a)) {
         const Tile q = walk.tile(a);
         const int arow = q.i * BM + (int)rank * BMC, bcol = q.j * BN + (int)rank * BNC;
         // (a piece's last k-blocks may lie past n: zeros)
@@ -361,7 +368,7 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
       int s = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
       bool ok = true;
-      const uint32_t idesc = IDESC | (KIND == kApply ? IDESC_B_MN : 0u);
+      const uint32_t idesc = idesc_of(BN) | (KIND == kApply ? IDESC_B_MN : 0u);
       for (uint32_t t = first; ok && t < total; t += step) {
         for (int i0 = 0; i0 < steps && ok; i0 += chunk) {
           const int i1 = min(steps, i0 + chunk);
@@ -435,6 +442,7 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
       p.rows = p.n0 < width ? min(32, a.m - p.r0) : 0;
       return p;
     };
+    auto block_col = [&](const Tile& d) { return NARROW ? d.j >> 1 : d.j; };   // of 256 columns
     // the mirror image of 64 columns from `col`
     auto mirror = [&](char* out, const Tile& d, const Part& p, int col, const uint32_t (&w)[32]) {
       mirror_rows(stage, w, out + ((int64_t)d.b * a.m + col) * a.add_ld + 2 * p.r0, a.add_ld, a.m - col, lane);
@@ -478,7 +486,7 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
       auto ask_lo = [&](const Part& p) {
         if (LOW_IN) load_block(lo, a.add_low + p.row * a.low_ld + p.n0, a.low_ld, p.rows, lane);
       };
-      Walk<KIND> walk(a, first, step);
+      Walk<KIND, SPLIT, NARROW> walk(a, first, step);
       Tile d = walk.tile(a), dn = d;
       Part p = part_of(d), pn = p;
       ask_lo(p);
@@ -510,11 +518,12 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
         uint32_t r[2][16];
         tmem_ld16(taddr, r[0]);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < EPI_COLS / 64; ++h) {
           uint32_t second[FORM == kOneTwice ? 32 : 1];   // this lane's part of the second addend
           if (FORM == kOneTwice) {
             block_to_slice(more, stage, lane);
-            ask_more(h ? pn : p, h ^ 1);
+            if (NARROW) ask_more(pn, 0);
+            else ask_more(h ? pn : p, h ^ 1);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const uint4 v = get_piece(stage, lane, j);
@@ -526,14 +535,15 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
           }
           if (KIND != kGram) {
             block_to_slice(hi, stage, lane);
-            ask_hi(h ? pn : p, h ^ 1);
+            if (NARROW) ask_hi(pn, 0);
+            else ask_hi(h ? pn : p, h ^ 1);
           }
           uint32_t w[32];      // 64 columns, packed
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const int k = 4 * h + c;
             tmem_wait_ld();
-            if (k < 7) tmem_ld16(taddr + 16 * (k + 1), r[(k + 1) & 1]);
+            if (k < EPI_COLS / 16 - 1) tmem_ld16(taddr + 16 * (k + 1), r[(k + 1) & 1]);
 #pragma unroll
             for (int g = 0; g < 2; ++g) {       // 8 columns: a piece
               int steps8[8];
@@ -576,10 +586,10 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
               }
             }
           }
-          if (h == 1) free_acc();
+          if (h == EPI_COLS / 64 - 1) free_acc();
           const int col = p.n0 + 64 * h, rows = col < width ? p.rows : 0;
           slice_to_rows(stage, a.out + p.row * a.add_ld + 2 * col, a.add_ld, rows, lane);
-          if (KIND != kApply && d.i != d.j && rows > 0) mirror(a.out, d, p, col, w);
+          if (KIND != kApply && d.i != block_col(d) && rows > 0) mirror(a.out, d, p, col, w);
         }
         if (LOW_OUT) {
 #pragma unroll
@@ -589,7 +599,7 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
         }
       }
     } else {
-      for (Walk<KIND, SPLIT> walk(a, first, step); ok && walk.t < total; walk.next(a)) {
+      for (Walk<KIND, SPLIT, NARROW> walk(a, first, step); ok && walk.t < total; walk.next(a)) {
         const Tile d = walk.tile(a);
         const Part p = part_of(d);
         float f[EPI_COLS];
@@ -598,7 +608,7 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
         if (KIND != kGram && p.rows > 0) {
           // start from the addend's two planes
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < EPI_COLS / 64; ++h) {
             const int rows = p.n0 + 64 * h < width ? p.rows : 0;
             Block b[2];
             load_block(b[0], a.add + p.row * a.add_ld + 2 * (p.n0 + 64 * h), a.add_ld, rows, lane);
@@ -645,7 +655,7 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
         }
         if (p.rows <= 0) continue;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < EPI_COLS / 64; ++h) {
           const int col = p.n0 + 64 * h;
           if (col >= width) continue;
 #pragma unroll
@@ -669,7 +679,7 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
               put_piece(stage, lane, j, make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
             }
             slice_to_rows(stage, out + p.row * a.add_ld + 2 * col, a.add_ld, p.rows, lane);
-            if (KIND != kApply && d.i != d.j) mirror(out, d, p, col, w);
+            if (KIND != kApply && d.i != block_col(d)) mirror(out, d, p, col, w);
           }
         }
       }
@@ -766,6 +776,9 @@ static cudaError_t prepare_device(int* clusters) {
   if (g_clusters[dev] == 0) {
     const void* fn[] = {(const void*)orth_kernel<kPoly, kOneTwice>, (const void*)orth_kernel<kGram, kOne, true>,
                          (const void*)orth_kernel<kGram, kTwo, true>,
+                         (const void*)orth_kernel<kGram, kOne, false, 128>, (const void*)orth_kernel<kGram, kTwo, false, 128>,
+                         (const void*)orth_kernel<kPoly, kOne, false, 128>, (const void*)orth_kernel<kPoly, kTwo, false, 128>,
+                         (const void*)orth_kernel<kPoly, kOneTwice, false, 128>,
                          (const void*)orth_kernel<kGram, kOne>,  (const void*)orth_kernel<kGram, kTwo>,
                          (const void*)orth_kernel<kPoly, kOne>,  (const void*)orth_kernel<kPoly, kTwo>,
                          (const void*)orth_kernel<kApply, kLow>, (const void*)orth_kernel<kApply, kLowIn>,
@@ -795,7 +808,7 @@ static cudaError_t prepare_device(int* clusters) {
   return *clusters > 0 ? cudaSuccess : cudaErrorNotSupported;
 }
 
-template <int KIND, int FORM, bool SPLIT = false>
+template <int KIND, int FORM, bool SPLIT = false, int NB = 256>
 static cudaError_t launch(const Maps& maps, const Args& t, cudaStream_t st) {
   int mc = 0;
   cudaError_t e = prepare_device(&mc);
@@ -804,7 +817,7 @@ static cudaError_t launch(const Maps& maps, const Args& t, cudaStream_t st) {
   if (tiles <= 0) return cudaSuccess;
   if (tiles >= (1ll << 31)) return cudaErrorInvalidValue;
   const unsigned pairs = (unsigned)(tiles < mc ? tiles : mc);
-  return launch_after(orth_kernel<KIND, FORM, SPLIT>, 2 * pairs, THREADS, SMEM_BYTES, st, 2, maps, t);
+  return launch_after(orth_kernel<KIND, FORM, SPLIT, NB>, 2 * pairs, THREADS, SMEM_BYTES, st, 2, maps, t);
 }
 
 static int gram_tiles(int m) {
@@ -839,12 +852,21 @@ cudaError_t launch_orth_steps(const OrthBatch& t, int steps, const double (*coef
   using namespace orth;
   const int64_t B = t.batch, all = B * t.planes;
   const bool two = t.planes == 2;
+  const int split = t.parts ? orth_split(B, t.m, t.n, t.planes) : 1;
   // the products' maps, those of X for either buffer as the source
   CUtensorMap of_a, of_b, of_c;
+  // Tiles of 128 columns for kGram and kPoly where those of 256 leave half of the pairs idle: five
+  // steps with and without, 3 x 777 x 1001 in fp32 307 us against 369, bf16 1 x 704 x 2816 189
+  // against 222, 1 x 2048 x 7168 465 against 488, 37 x 200 x 300 (37 tiles) 132 against 142
+  const bool narrow = 2 * B * gram_tiles(t.m) <= 76;
+  const int b_rows = narrow ? 64 : 128;
+  CUtensorMap as_b[3];   // a, b and c as the second operand
   Maps gram[2];
   CUtensorMap apply_x[2];
   if (!map3(&of_a, t.a, all, t.m, t.m, t.lda, 64, 128) || !map3(&of_b, t.b, all, t.m, t.m, t.lda, 64, 128) ||
-      !map3(&of_c, t.c ? t.c : t.a, all, t.m, t.m, t.lda, 64, 128))
+      !map3(&of_c, t.c ? t.c : t.a, all, t.m, t.m, t.lda, 64, 128) ||
+      !map3(&as_b[0], t.a, all, t.m, t.m, t.lda, 64, b_rows) || !map3(&as_b[1], t.b, all, t.m, t.m, t.lda, 64, b_rows) ||
+      !map3(&as_b[2], t.c ? t.c : t.a, all, t.m, t.m, t.lda, 64, b_rows))
     return cudaErrorInvalidValue;
   for (int i = 0; i < 2; ++i) {
     // planes of X: two of fp16, or one with the 8-bit parts behind it
@@ -853,6 +875,7 @@ cudaError_t launch_orth_steps(const OrthBatch& t, int steps, const double (*coef
         !map3(&apply_x[i], t.x[i], planes, t.m, t.n, t.ldx, 64, 64))
       return cudaErrorInvalidValue;
     gram[i].B = gram[i].A;
+    if (narrow && split == 1 && !map3(&gram[i].B, t.x[i], planes, t.m, t.n, t.ldx, 64, b_rows)) return cudaErrorInvalidValue;
   }
   Args g = {};
   g.m = t.m;
@@ -869,7 +892,7 @@ cudaError_t launch_orth_steps(const OrthBatch& t, int steps, const double (*coef
                   const char* add2, double add2_scale, char* out) {
     const Maps maps = {P, Q};
     g.kb = (t.m + BK - 1) / BK;
-    g.per = g.mt * (g.mt + 1) / 2;
+    g.per = gram_tiles(t.m) * (narrow ? 2 : 1);
     g.mul = (float)mul;
     g.add_scale = (float)add_scale;
     g.add = add;
@@ -879,10 +902,13 @@ cudaError_t launch_orth_steps(const OrthBatch& t, int steps, const double (*coef
     g.add_ld = g.low_ld = a_ld;
     g.out = out;
     g.out_low = out + rows * a_ld;
+    if (narrow) {
+      if (two) return launch<kPoly, kTwo, false, 128>(maps, g, st);
+      return add2 ? launch<kPoly, kOneTwice, false, 128>(maps, g, st) : launch<kPoly, kOne, false, 128>(maps, g, st);
+    }
     if (two) return launch<kPoly, kTwo>(maps, g, st);
     return add2 ? launch<kPoly, kOneTwice>(maps, g, st) : launch<kPoly, kOne>(maps, g, st);
   };
-  const int split = t.parts ? orth_split(B, t.m, t.n, t.planes) : 1;
   g.parts = t.parts;
   auto two_to = [](int e) { return std::ldexp(1.0, e); };
   bool low = true;     // x[0] has its 8-bit parts
@@ -892,13 +918,15 @@ cudaError_t launch_orth_steps(const OrthBatch& t, int steps, const double (*coef
     // A = X X^T
     g.split = split;
     g.kb = ((t.n + BK - 1) / BK + split - 1) / split;
-    g.per = gram_tiles(t.m) * split;
+    g.per = gram_tiles(t.m) * (split > 1 ? split : narrow ? 2 : 1);
     g.mul = ldexpf(1.0f, kOrthA - 2 * kOrthX);
     g.add_ld = g.low_ld = a_ld;
     g.out = pa;
     g.out_low = pa + rows * a_ld;
     cudaError_t e;
     if (split > 1) e = two ? launch<kGram, kTwo, true>(gram[at], g, st) : launch<kGram, kOne, true>(gram[at], g, st);
+    else if (narrow)
+      e = two ? launch<kGram, kTwo, false, 128>(gram[at], g, st) : launch<kGram, kOne, false, 128>(gram[at], g, st);
     else e = two ? launch<kGram, kTwo>(gram[at], g, st) : launch<kGram, kOne>(gram[at], g, st);
     if (e == cudaSuccess && split > 1) {
       const unsigned blocks = (unsigned)(B * gram_tiles(t.m) * 64);
@@ -908,16 +936,16 @@ cudaError_t launch_orth_steps(const OrthBatch& t, int steps, const double (*coef
     if (e != cudaSuccess) return e;
     // B = b A + c A A, the polynomial in the planes that the product reads
     const double *c0 = coef[i], *c1 = coef[i + 1 < steps ? i + 1 : i];
-    e = poly(of_a, of_a, c0[2] * two_to(kOrthB - 2 * kOrthA), pa, c0[1] * two_to(kOrthB - kOrthA), nullptr, 0.0, pb);
+    e = poly(of_a, as_b[0], c0[2] * two_to(kOrthB - 2 * kOrthA), pa, c0[1] * two_to(kOrthB - kOrthA), nullptr, 0.0, pb);
     const bool pair = t.c && i == 0 && steps > 2;
     if (pair) {
       // C, A', B', R to c, a, c, a
-      if (e == cudaSuccess) e = poly(of_b, of_a, two_to(-kOrthB), pa, c0[0], nullptr, 0.0, pc);
-      if (e == cudaSuccess) e = poly(of_b, of_c, two_to(-kOrthB), pc, c0[0], nullptr, 0.0, pa);
+      if (e == cudaSuccess) e = poly(of_b, as_b[0], two_to(-kOrthB), pa, c0[0], nullptr, 0.0, pc);
+      if (e == cudaSuccess) e = poly(of_b, as_b[2], two_to(-kOrthB), pc, c0[0], nullptr, 0.0, pa);
       if (e == cudaSuccess)
-        e = poly(of_a, of_a, c1[2] * two_to(kOrthB - 2 * kOrthA), pa, c1[1] * two_to(kOrthB - kOrthA), nullptr, 0.0, pc);
+        e = poly(of_a, as_b[0], c1[2] * two_to(kOrthB - 2 * kOrthA), pa, c1[1] * two_to(kOrthB - kOrthA), nullptr, 0.0, pc);
       if (e == cudaSuccess)
-        e = poly(of_c, of_b, two_to(kOrthR - 2 * kOrthB), pc, c0[0] * two_to(kOrthR - kOrthB), pb,
+        e = poly(of_c, as_b[1], two_to(kOrthR - 2 * kOrthB), pc, c0[0] * two_to(kOrthR - kOrthB), pb,
                  c1[0] * two_to(kOrthR - kOrthB), pa);
     }
     if (e != cudaSuccess) return e;

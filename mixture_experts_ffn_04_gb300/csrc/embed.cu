@@ -191,18 +191,23 @@ __global__ void __launch_bounds__(32 * kRankWarps) rank_kernel(const int32_t* __
 __global__ void __launch_bounds__(512) hist_kernel(const int32_t* __restrict__ ids, int64_t T, int64_t tile,
                                                    int V, int pad, int bins, uint32_t* __restrict__ hist,
                                                    uint32_t* present, uint32_t* flags) {
-  __shared__ uint32_t cnt[kMaxBins];
+  constexpr int kSeen = 1024;
+  __shared__ uint32_t cnt[kMaxBins], seen[kSeen];
   pdl_trigger();
   pdl_wait();
   for (int d = threadIdx.x; d < bins; d += 512) cnt[d] = 0;
+  for (int d = threadIdx.x; d < kSeen; d += 512) seen[d] = ~0u;
   __syncthreads();
   const int64_t lo = blockIdx.x * tile, hi = min(T, lo + tile);
+  // A frequent row is marked by few threads of a block (a warp's equal keys once, and not
+  // again while its key stands in `seen`): thousands of atomics on one word are a queue.
   for (int64_t i = lo + threadIdx.x; i < hi; i += 512) {
     const int id = ids[i];
     if ((uint32_t)id >= (uint32_t)V) set_flag(flags, kFlagToken);
-    const uint32_t k = key_of(id, V, pad);
-    atomicAdd(cnt + (k & (bins - 1)), 1u);
-    if (present != nullptr && k < (uint32_t)V) mark(present, k);
+    const uint32_t k = key_of(id, V, pad), same = __match_any_sync(__activemask(), k);
+    if ((__ffs(same) - 1) != (int)(threadIdx.x & 31)) continue;
+    atomicAdd(cnt + (k & (bins - 1)), (uint32_t)__popc(same));
+    if (present != nullptr && k < (uint32_t)V && atomicExch(seen + (k & (kSeen - 1)), k) != k) mark(present, k);
   }
   __syncthreads();
   for (int d = threadIdx.x; d < bins; d += 512) hist[(int64_t)blockIdx.x * bins + d] = cnt[d];

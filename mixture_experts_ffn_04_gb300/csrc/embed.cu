@@ -6,8 +6,8 @@
 // columns in bf16 27 us; frequent rows come from L2), the gradient reads a row a token and writes
 // (and, with dw_add elsewhere, reads) one a vocabulary entry: 4096 tokens, 131072 x 2048 in bf16 with
 // dw_add 191 us, of them 167 for the sums and the rows without tokens (1.09 GB, 6.5 TB/s);
-// 60001 tokens, 32001 x 1000 in fp32 119 us, of them 72 for the sums (368 MB, 5.1 TB/s) and
-// 43 for the sort's three launches.
+// 60001 tokens, 32001 x 1000 in fp32 113 us, of them 63 for the sums (368 MB, 5.8 TB/s) and
+// 39 for the sort's three launches.
 //
 // Gradient: the tokens are sorted by id (stable, so a row's tokens stay in
 // order; up to kSmallT by counting, more by radix passes), the sorted list is cut into chunks of equal length, and one warp walks a
@@ -582,10 +582,10 @@ Layout layout_of(const EShape& s) {
   };
   L.dig = digits_for(s.V);
   L.slabs = (s.H + 255) / 256;
-  // Chunks long enough for at most some 16 warps an SM (a border costs a row of
-  // fp32 written and read), at least 8 tokens, at most 256
-  int64_t chunk = 8;
-  while (chunk < 256 && (s.T + chunk - 1) / chunk * L.slabs > 16 * 152) chunk *= 2;
+  // Chunks for some 16 warps an SM, which are all there at once (a border costs a row of fp32
+  // written and read), of 8 to 256 tokens.  60001 tokens, 32001 x 1000 in fp32: 113 us with the
+  // sort, in powers of two 123, for 24 warps an SM 131; 30000, 50257 x 2048 in bf16 150, 166, 147
+  const int64_t chunk = std::min<int64_t>(256, std::max<int64_t>(8, (s.T * L.slabs / (16 * 152) + 7) / 8 * 8));
   L.chunk = (int)chunk;
   L.chunks = (s.T + chunk - 1) / chunk;
   L.tile = ((s.T + kMaxTiles - 1) / kMaxTiles + kTileMin - 1) / kTileMin * kTileMin;

@@ -11,8 +11,9 @@
 // Bound by HBM: a bf16 parameter reads gradient and momentum twice (for the norm, then
 // for the scaled planes), writes the momentum, and passes once more for the update.  Of 96
 // matrices 704 x 2816, a third of them transposed, the momentum takes 285 us (6.7 TB/s), the
-// planes 282 (6.1; with three blocks an SM instead of four 320), the update 239 (4.8).  Tiles of 64 x 128 instead of 64 x 64: planes 317,
-// update 359 (two blocks an SM).
+// planes 282 (6.1; with three blocks an SM instead of four 320), the update 199 (5.7;
+// with the second piece of X read after the first was opened 239).  Tiles of 64 x 128 instead
+// of 64 x 64: planes 317, update 359 (two blocks an SM).
 #include <algorithm>
 #include <cmath>
 
@@ -160,32 +161,37 @@ __device__ __forceinline__ void put8(const Round& r, int64_t at, const float* f)
     *reinterpret_cast<uint2*>(reinterpret_cast<char*>(r.x + plane) + at) = make_uint2(l[0], l[1]);
   }
 }
-// 8 values of the last X (which has no 8-bit parts: no step is left to need them).
+// 8 values of the last X (which has no 8-bit parts: no step is left to need them), as they
+// stand, and as floats.
+struct RawX {
+  uint4 hi, lo;
+};
 template <bool ALL16>
-__device__ __forceinline__ void get8(const Round& r, int64_t at, float* f) {
-  const uint4 hi = *reinterpret_cast<const uint4*>(r.x + at);
-  const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w};
+__device__ __forceinline__ RawX load_x(const Round& r, int64_t at, bool there) {
+  RawX x;
+  x.hi = x.lo = make_uint4(0, 0, 0, 0);
+  if (there) {
+    x.hi = *reinterpret_cast<const uint4*>(r.x + at);
+    if (!ALL16 && r.planes == 2) x.lo = *reinterpret_cast<const uint4*>(r.x + (int64_t)r.batch * r.m * r.ldx + at);
+  }
+  return x;
+}
+template <bool ALL16>
+__device__ __forceinline__ void open_x(const RawX& x, float* f) {
+  const uint32_t h[4] = {x.hi.x, x.hi.y, x.hi.z, x.hi.w}, l[4] = {x.lo.x, x.lo.y, x.lo.z, x.lo.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-    f[2 * i] = a.x;
-    f[2 * i + 1] = a.y;
-  }
-  const int64_t plane = (int64_t)r.batch * r.m * r.ldx;
-  if (!ALL16 && r.planes == 2) {
-    const uint4 lo = *reinterpret_cast<const uint4*>(r.x + plane + at);
-    const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    if (!ALL16) {
       const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&l[i]));
-      f[2 * i] += b.x;
-      f[2 * i + 1] += b.y;
+      a.x += b.x;
+      a.y += b.y;
     }
+    f[2 * i] = a.x * 0x1p-13f;
+    f[2 * i + 1] = a.y * 0x1p-13f;
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] *= 0x1p-13f;
 }
-static_assert(kOrthX == 13, "get8's factor");
+static_assert(kOrthX == 13, "open_x's factor");
 
 struct TileAt {
   int b, r0, c0;   // matrix of the round; first row and column of the tile in its tensor
@@ -303,7 +309,8 @@ __global__ void __launch_bounds__(256) update_kernel(const __grid_constant__ Rou
   pdl_wait();
   const int tid = threadIdx.x;
   const int64_t all = (int64_t)((r.m + kTile - 1) / kTile) * ((r.n + kTile - 1) / kTile) * r.batch;
-  for (int64_t task = blockIdx.x; task < all; task += gridDim.x) {
+  const int64_t each = (all + gridDim.x - 1) / gridDim.x, end = min(all, (blockIdx.x + 1) * each);
+  for (int64_t task = blockIdx.x * each; task < end; ++task) {
     const Seg* s;
     const TileAt t = tile_at(r, task, s);
     const bool tall = s->rows > s->cols;
@@ -319,13 +326,17 @@ __global__ void __launch_bounds__(256) update_kernel(const __grid_constant__ Rou
         const int row = t.r0 + k * 32 + tid / 8, col = t.c0 + tid % 8 * 8;
         w[k] = load_raw(s->param, type_of<ALL16>(s->pdtype), base + (int64_t)row * s->cols + col, row < s->rows && col < s->cols);
       }
+    RawX raw[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int row = (tall ? t.c0 : t.r0) + k * 32 + tid / 8, col = (tall ? t.r0 : t.c0) + tid % 8 * 8;
+      raw[k] = load_x<ALL16>(r, x + (int64_t)row * r.ldx + col, row < r.m && col < r.n);
+    }
     if (tall) __syncthreads();   // the last tile's readers are done
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int lr = k * 32 + tid / 8, lc = tid % 8 * 8;
-      const int row = (tall ? t.c0 : t.r0) + lr, col = (tall ? t.r0 : t.c0) + lc;
-      if (row >= r.m || col >= r.n) continue;
-      get8<ALL16>(r, x + (int64_t)row * r.ldx + col, f[k]);
+      open_x<ALL16>(raw[k], f[k]);
       if (tall)
 #pragma unroll
         for (int e = 0; e < 8; ++e) sh[lc + e][lr] = f[k][e];

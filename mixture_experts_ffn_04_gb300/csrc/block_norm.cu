@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(1024) norm_forward_kernel(int64_t rows, int H,
 
 // ---------------------------------------------------------------------------
 // Many rows: each team of threads (a row's threads, or a warp with several short
-// rows) is fed by bulk copies into a ring of its own, kRing steps deep, so that the
+// rows) is fed by bulk copies into a ring of its own, two steps deep, so that the
 // next rows are under way while this one's sums wait on each other; the weights
 // stand in shared memory.  Held in registers without the ring, a row's loads, two
 // row sums and stores followed one another: the forward at T = 4096, H = 2816 took 39 us
@@ -886,8 +886,9 @@ moe_status decode(const moe_block_norm_shape* s, NShape* o, const char** why) {
 
 // Rings for rows of H columns, `streams` of them in and two fp32 weight vectors beside
 // them, one vector of 8 columns a thread up to `wide` vectors, at most `threads`
-// threads of an SM (two vectors: threads2): as many teams as fit with two steps or more in
-// their rings, then the deepest rings.  depth 0: none fits.
+// threads of an SM (two vectors: threads2): as many teams as fit with two steps in their
+// rings (three or four steps took as long or longer to start: the forward at 4096 x 2816 25 us
+// with two, 27 with three).  depth 0: none fits.
 constexpr int kSmemBlock = 227 * 1024, kSmemSm = 228 * 1024;   // 1 KB of the latter goes with each block
 constexpr int kStatic = 512;                                    // what the kernels declare besides
 RingShape ring_shape(int H, int esize, int streams, int wide, int threads, int threads2) {
@@ -911,7 +912,7 @@ RingShape ring_shape(int H, int esize, int streams, int wide, int threads, int t
   for (int b = 1; b <= 8; ++b)
     for (int ng = 1; ng <= 15 && b * ng * q.G <= most_threads; ++ng) {
       const int most = std::min(kSmemSm / b - 1024, kSmemBlock) - kStatic;
-      const int depth = std::min(4, std::max(0, most - weights) / (ng * step));
+      const int depth = std::min(2, std::max(0, most - weights) / (ng * step));
       const int smem = std::max(weights + ng * depth * step, weights + ng * q.R * 2 * H * 4);
       if (depth < 2 || smem > most) continue;
       const int score = ng * b * 8 + depth;

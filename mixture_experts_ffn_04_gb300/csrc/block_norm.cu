@@ -5,9 +5,11 @@
 //
 // The forward reads two rows a token and writes two, the backward reads four and
 // writes two (s is not read back: from x and y it costs a few FMAs, and it has not been
-// rounded).  At 8192 rows of 7168 columns in bf16 that takes 84 us (470 MB, 5.6 TB/s: 82 % of
-// the rate of a copy) and 154 us (705 MB, 4.6 TB/s: 67 %), by the rings below; few rows are
-// bound by latency (one row of 7168: 4.5 us on the device).  A group of threads holds a whole row in
+// rounded).  At 8192 rows of 7168 columns in bf16 that takes 80 us (470 MB, 5.9 TB/s: 87 % of
+// the rate of a copy) and 146 us (705 MB, 4.8 TB/s: 71 %), by the rings below; few rows are
+// bound by latency (one row of 2048: 4.5 us on the device).  1 / sqrt by rsqrtf, within two
+// units of fp32's last place: exactly rounded root and quotient, in every thread for its row,
+// cost 4 % of the forward.  A group of threads holds a whole row in
 // registers, eight columns and their multiples a thread, so that both norms of the
 // forward, and both row sums of the backward, come from one read.  Sums in fp32.
 //
@@ -156,7 +158,7 @@ __global__ void __launch_bounds__(1024) norm_forward_kernel(int64_t rows, int H,
         for (int e = 0; e < 8; ++e) sum[0] = fmaf(f[e], f[e], sum[0]);
       }
       row_sum<1>(sum, G, red, slot);
-      r1 = 1.0f / sqrtf(sum[0] * inv_h + eps);
+      r1 = rsqrtf(sum[0] * inv_h + eps);
     }
     float f[VPT][8];
     float sum[1] = {0.0f};
@@ -184,7 +186,7 @@ __global__ void __launch_bounds__(1024) norm_forward_kernel(int64_t rows, int H,
     float r2 = 0.0f;
     if (w_pre) {
       row_sum<1>(sum, G, red, slot);
-      r2 = 1.0f / sqrtf(sum[0] * inv_h + eps);
+      r2 = rsqrtf(sum[0] * inv_h + eps);
     }
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
@@ -261,9 +263,13 @@ struct Team {
   }
   // Sums over a row's threads; red: two values a warp of the block, 32 apart.
   __device__ __forceinline__ float sum(float v, float* red, int& slot) const {
-    const int span = Gs < 32 ? Gs : 32;
-    for (int o = span >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (Gs <= 32) return v;
+    if (Gs < 32) {
+      for (int o = Gs >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      return v;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (Gs == 32) return v;
     const int lane32 = tt & 31, warps = G >> 5;
     float* r = red + slot * 32 + g * warps;
     if (lane32 == 0) r[tt >> 5] = v;
@@ -439,7 +445,7 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_ring_kernel(
 #pragma unroll
         for (int e = 0; e < 4; ++e) sq = fma2(fy.p[e], fy.p[e], sq);
       }
-      r1 = 1.0f / sqrtf(m.sum(sq.x + sq.y, red, slot) * inv_h + eps);
+      r1 = rsqrtf(m.sum(sq.x + sq.y, red, slot) * inv_h + eps);
     }
     if (!fed) r1 = __int_as_float(0x7fc00000);   // a copy that never came
     const float2 rg = both(r1 * gt), rx = both(fed ? res : r1);
@@ -462,7 +468,7 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_ring_kernel(
     }
     float r2 = 0.0f;
     if (w_pre) {
-      r2 = 1.0f / sqrtf(m.sum(sq.x + sq.y, red, slot) * inv_h + eps);
+      r2 = rsqrtf(m.sum(sq.x + sq.y, red, slot) * inv_h + eps);
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
         if (!on || c0 + k * span >= H) continue;

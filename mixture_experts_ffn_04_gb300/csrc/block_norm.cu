@@ -6,7 +6,7 @@
 // The forward reads two rows a token and writes two, the backward reads four and
 // writes two (s is not read back: from x and y it costs a few FMAs, and it has not been
 // rounded).  At 8192 rows of 7168 columns in bf16 that takes 80 us (470 MB, 5.9 TB/s: 87 % of
-// the rate of a copy) and 146 us (705 MB, 4.8 TB/s: 71 %), by the rings below; few rows are
+// the rate of a copy) and 143 us (705 MB, 4.9 TB/s: 73 %), by the rings below; few rows are
 // bound by latency (one row of 2048: 4.5 us on the device).  1 / sqrt by rsqrtf, within two
 // units of fp32's last place: exactly rounded root and quotient, in every thread for its row,
 // cost 4 % of the forward.  A group of threads holds a whole row in
@@ -430,6 +430,9 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_ring_kernel(
     fed = !lost;
     if (m.tt == 0) f.refill(i, steps);      // into its slot
     const bool on = t < rows;
+    bool live[VPT];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) live[k] = on && c0 + k * span < H;
     const T* bx = reinterpret_cast<const T*>(f.here()) + (size_t)m.row * H + c0;
     const T* by = bx + (size_t)q.R * H;
     float gt = 1.0f;
@@ -440,7 +443,7 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_ring_kernel(
       float2 sq = both(0.0f);
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
-        if (!on || c0 + k * span >= H) continue;
+        if (!live[k]) continue;
         const Pairs fy = open_pairs<T>(load8<T>(by + k * span));
 #pragma unroll
         for (int e = 0; e < 4; ++e) sq = fma2(fy.p[e], fy.p[e], sq);
@@ -452,7 +455,7 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_ring_kernel(
     float2 sq = both(0.0f);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      if (!on || c0 + k * span >= H) continue;
+      if (!live[k]) continue;
       v[k] = open_pairs<T>(load8<T>(bx + k * span));
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[k].p[e] = mul2(rx, v[k].p[e]);
@@ -471,7 +474,7 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_ring_kernel(
       r2 = rsqrtf(m.sum(sq.x + sq.y, red, slot) * inv_h + eps);
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
-        if (!on || c0 + k * span >= H) continue;
+        if (!live[k]) continue;
         const Pairs w = weight_pairs(w2 + ((c0 + k * span) >> 1), half);
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[k].p[e] = mul2(v[k].p[e], mul2(both(r2), w.p[e]));
@@ -714,6 +717,9 @@ __global__ void __launch_bounds__(VPT == 1 ? 896 : 512, 1) norm_backward_ring_ke
   ask(t);
   for (int i = 0; i < steps && t - m.row < a.rows; ++i, t += f.step, to += (int64_t)f.step * H, f.next()) {
     const bool on = t < a.rows;
+    bool live[VPT];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) live[k] = on && c0 + k * span < H;
     float2 r = r_next;
     const float gt = gate_next;
     ask(t + f.step);
@@ -731,7 +737,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 896 : 512, 1) norm_backward_ring_ke
       const float2 rx = both(a.res * r.y), ry = both(gt * r.x * r.y);
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
-        if (!on || c0 + k * span >= H) continue;
+        if (!live[k]) continue;
         D[k] = open_pairs<T>(load8<T>(bx + k * span));
 #pragma unroll
         for (int e = 0; e < 4; ++e) D[k].p[e] = mul2(rx, D[k].p[e]);
@@ -753,7 +759,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 896 : 512, 1) norm_backward_ring_ke
       const float2 mean = both(-m.sum(sum.x + sum.y, red, slot) * inv_h), ry2 = both(r.y);
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
-        if (!on || c0 + k * span >= H) continue;
+        if (!live[k]) continue;
         const Pairs fs = open_pairs<T>(a.ds ? load8<T>(bs + k * span) : zero8<T>()), fh = open_pairs<T>(load8<T>(bh + k * span));
         const Pairs w = weight_pairs(w2 + ((c0 + k * span) >> 1), half);
 #pragma unroll
@@ -771,7 +777,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 896 : 512, 1) norm_backward_ring_ke
     const float2 ge = both(gt * r.x);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      if (!on || c0 + k * span >= H) continue;
+      if (!live[k]) continue;
       if (dx) {
         Pairs o;
 #pragma unroll
@@ -796,7 +802,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 896 : 512, 1) norm_backward_ring_ke
     const float2 mine = both(gt * r.x), back = both(post ? -r.x * (gt * r.x) * (c1 * inv_h) : 0.0f);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      if (!on || c0 + k * span >= H) continue;
+      if (!live[k]) continue;
 #pragma unroll
       for (int e = 0; e < 4; ++e) D[k].p[e] = mul2(mine, D[k].p[e]);
       if (post) {

@@ -56,6 +56,7 @@
 #include <cmath>
 #include <cuda.h>
 #include <cudaTypedefs.h>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -121,7 +122,7 @@ struct Tile {
 };
 // A pair's tiles: every `step`th of all matrices' tiles, from its own.  Divisions by the
 // number of tiles of a matrix are done once.
-// NARROW: each tile of kGram and kPoly as two of 128 columns.
+// NARROW: tiles of 128 columns, two to each whole one of kGram and kPoly.
 template <int KIND, bool SPLIT = false, bool NARROW = false>
 struct Walk {
   uint32_t t, l, b;             // tile; place in its matrix; matrix
@@ -228,6 +229,40 @@ __device__ __forceinline__ void slice_to_rows(uint32_t stage, char* p, int64_t l
     if (4 * i < there) *reinterpret_cast<uint4*>(at) = b.v[i];
   __syncwarp();
 }
+// The same with rows of 64 bytes, half of a slice's (the 8-bit parts of 64 columns): lane l has
+// 16 bytes l % 4 of rows l / 4, + 8, + 16, + 24.
+__device__ __forceinline__ uint32_t half_at(uint32_t stage, int lane, int i) {
+  const int r = 8 * i + (lane >> 2);
+  return stage + r * 128 + (((lane & 3) ^ (r & 7)) << 4);
+}
+__device__ __forceinline__ void load_half(Block& b, const char* p, int64_t ld, int rows, int lane) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2);
+    b.v[i] = r < rows ? *reinterpret_cast<const uint4*>(p + r * ld + (lane & 3) * 16) : make_uint4(0, 0, 0, 0);
+  }
+}
+__device__ __forceinline__ void half_to_slice(const Block& b, uint32_t stage, int lane) {
+  __syncwarp();   // what the slice held has been read
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(half_at(stage, lane, i)), "r"(b.v[i].x), "r"(b.v[i].y),
+                 "r"(b.v[i].z), "r"(b.v[i].w)
+                 : "memory");
+  __syncwarp();
+}
+__device__ __forceinline__ void half_to_rows(uint32_t stage, char* p, int64_t ld, int rows, int lane) {
+  __syncwarp();   // every lane's pieces are in the slice
+  uint4 v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = load_piece(half_at(stage, lane, i));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2);
+    if (r < rows) *reinterpret_cast<uint4*>(p + r * ld + (lane & 3) * 16) = v[i];
+  }
+  __syncwarp();
+}
 // The transposed image of 64 columns: value j of this lane's row goes to row j of 64 bytes
 // (w: pairs of columns), then rows `cols` of them at p, whole (their ends may be padding).
 __device__ __forceinline__ void mirror_rows(uint32_t stage, const uint32_t (&w)[32], char* p, int64_t ld, int cols,
@@ -266,7 +301,7 @@ template <int KIND, int FORM, bool SPLIT = false, int NB = 256>
 __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant__ Maps maps, const Args a) {
   constexpr int BN = NB, BNC = BN / 2, B_BYTES = BNC * BK * 2, EPI_COLS = BN / 2;
   constexpr bool NARROW = NB == 128;
-  static_assert(!NARROW || (KIND != kApply && !SPLIT), "kGram and kPoly alone have tiles of 128 columns");
+  static_assert(!NARROW || !SPLIT, "pieces of a sum are whole tiles");
   // two planes: a stage has both of both operands, for the three products
   constexpr int PL = FORM == kTwo ? 2 : 1, S = MAX_STAGES / PL, STAGE_BYTES = PL * (A_BYTES + B_BYTES);
   constexpr bool LOW_IN = FORM == kLow || FORM == kLowIn, LOW_OUT = FORM == kLow;
@@ -343,7 +378,7 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
             tma_load_3d_pair(sa + p * A_BYTES, &maps.A, k, arow, z, fb);
             if (KIND == kApply) {
               tma_load_3d_pair(sb + p * B_BYTES, &maps.B, bcol, k, z, fb);
-              tma_load_3d_pair(sb + p * B_BYTES + BOX_BYTES, &maps.B, bcol + 64, k, z, fb);
+              if (!NARROW) tma_load_3d_pair(sb + p * B_BYTES + BOX_BYTES, &maps.B, bcol + 64, k, z, fb);
             } else {
               tma_load_3d_pair(sb + p * B_BYTES, &maps.B, k, bcol, z, fb);
             }
@@ -484,7 +519,10 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
                      p.n0 + 64 * h < width ? p.rows : 0, lane);
       };
       auto ask_lo = [&](const Part& p) {
-        if (LOW_IN) load_block(lo, a.add_low + p.row * a.low_ld + p.n0, a.low_ld, p.rows, lane);
+        if (!LOW_IN) return;
+        const char* at = a.add_low + p.row * a.low_ld + p.n0;
+        if (NARROW) load_half(lo, at, a.low_ld, p.rows, lane);
+        else load_block(lo, at, a.low_ld, p.rows, lane);
       };
       Walk<KIND, SPLIT, NARROW> walk(a, first, step);
       Tile d = walk.tile(a), dn = d;
@@ -500,12 +538,13 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
         } else {
           pn.rows = 0;     // nothing more to ask for
         }
-        uint32_t low[LOW_IN ? 32 : 1];     // this lane's 128 8-bit parts
+        uint32_t low[LOW_IN ? EPI_COLS / 4 : 1];     // this lane's 8-bit parts
         if (LOW_IN) {
-          block_to_slice(lo, stage, lane);
+          if (NARROW) half_to_slice(lo, stage, lane);
+          else block_to_slice(lo, stage, lane);
           ask_lo(pn);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < EPI_COLS / 16; ++j) {
             const uint4 v = get_piece(stage, lane, j);
             low[4 * j] = v.x;
             low[4 * j + 1] = v.y;
@@ -593,9 +632,11 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
         }
         if (LOW_OUT) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
+          for (int j = 0; j < EPI_COLS / 16; ++j)
             put_piece(stage, lane, j, make_uint4(low[4 * j], low[4 * j + 1], low[4 * j + 2], low[4 * j + 3]));
-          slice_to_rows(stage, a.out_low + p.row * a.low_ld + p.n0, a.low_ld, p.rows, lane);
+          char* to = a.out_low + p.row * a.low_ld + p.n0;
+          if (NARROW) half_to_rows(stage, to, a.low_ld, p.rows, lane);
+          else slice_to_rows(stage, to, a.low_ld, p.rows, lane);
         }
       }
     } else {
@@ -779,6 +820,8 @@ static cudaError_t prepare_device(int* clusters) {
                          (const void*)orth_kernel<kGram, kOne, false, 128>, (const void*)orth_kernel<kGram, kTwo, false, 128>,
                          (const void*)orth_kernel<kPoly, kOne, false, 128>, (const void*)orth_kernel<kPoly, kTwo, false, 128>,
                          (const void*)orth_kernel<kPoly, kOneTwice, false, 128>,
+                         (const void*)orth_kernel<kApply, kOne, false, 128>, (const void*)orth_kernel<kApply, kTwo, false, 128>,
+                         (const void*)orth_kernel<kApply, kLow, false, 128>, (const void*)orth_kernel<kApply, kLowIn, false, 128>,
                          (const void*)orth_kernel<kGram, kOne>,  (const void*)orth_kernel<kGram, kTwo>,
                          (const void*)orth_kernel<kPoly, kOne>,  (const void*)orth_kernel<kPoly, kTwo>,
                          (const void*)orth_kernel<kApply, kLow>, (const void*)orth_kernel<kApply, kLowIn>,
@@ -910,6 +953,9 @@ cudaError_t launch_orth_steps(const OrthBatch& t, int steps, const double (*coef
     return add2 ? launch<kPoly, kOneTwice>(maps, g, st) : launch<kPoly, kOne>(maps, g, st);
   };
   g.parts = t.parts;
+  // kApply's by the same rule: 1 x 704 x 2816 bf16 181 us against 190, 1 x 1024 x 1024 155 against
+  // 168, fp32 265 against 300
+  const bool narrow_x = 2 * B * g.mt * g.nt <= 76;
   auto two_to = [](int e) { return std::ldexp(1.0, e); };
   bool low = true;     // x[0] has its 8-bit parts
   int at = 0;          // the buffer that X is in
@@ -953,7 +999,7 @@ cudaError_t launch_orth_steps(const OrthBatch& t, int steps, const double (*coef
     // X' = a X + B X, or a a' X + R X
     const Maps apply = {pair ? of_a : of_b, apply_x[at]};
     g.kb = (t.m + BK - 1) / BK;
-    g.per = g.mt * g.nt;
+    g.per = g.mt * (narrow_x ? (t.n + 127) / 128 : g.nt);
     g.add_scale = (float)(pair ? c0[0] * c1[0] : c0[0]);
     g.mul = ldexpf(1.0f, pair ? -kOrthR : -kOrthB);
     g.add_ld = x_ld;
@@ -968,10 +1014,14 @@ cudaError_t launch_orth_steps(const OrthBatch& t, int steps, const double (*coef
     double grows = 1.0;
     for (int k = i; k < steps; ++k) grows *= fabs(coef[k][0]);
     const bool keep = grows > 4.0;
-    if (two) e = launch<kApply, kTwo>(apply, g, st);
-    else if (keep && low) e = launch<kApply, kLow>(apply, g, st);
-    else if (low) e = launch<kApply, kLowIn>(apply, g, st);
-    else e = launch<kApply, kOne>(apply, g, st);
+    auto product = [&](auto columns) {
+      constexpr int NB = decltype(columns)::value;
+      if (two) return launch<kApply, kTwo, false, NB>(apply, g, st);
+      if (keep && low) return launch<kApply, kLow, false, NB>(apply, g, st);
+      if (low) return launch<kApply, kLowIn, false, NB>(apply, g, st);
+      return launch<kApply, kOne, false, NB>(apply, g, st);
+    };
+    e = narrow_x ? product(std::integral_constant<int, 128>()) : product(std::integral_constant<int, 256>());
     if (e != cudaSuccess) return e;
     low = low && keep;
   }

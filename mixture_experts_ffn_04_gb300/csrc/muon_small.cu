@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     proxy_fence();
   }
+  __syncwarp();
   if (warp == 0) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
@@ -226,6 +227,12 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = at[e];
     }
+  };
+  // All threads of the matrix (the cluster barrier is for whole warps).
+  auto meet = [&]() {
+    __syncwarp();
+    if (ctas > 1) cluster_sync();
+    else __syncthreads();
   };
   const int row = 32 * (warp & 3) + lane, part = warp >> 2;   // this thread's row, and MINE columns of it
   float x[MINE];
@@ -332,8 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
     for (int o = kWarps / 2; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
     if (lane == 0) sums[kWarps] = t;
   }
-  if (ctas > 1) cluster_sync();
-  else __syncthreads();
+  meet();
   if (warp == 0) {
     double t = 0.0;
     if (lane < ctas)
@@ -352,7 +358,6 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
     for (int j = 0; j < MINE; ++j) x[j] = x[j] * f.x * f.y;
   }
 
-  bool good = true;
   uint32_t phase = 0;
   // Products issued by one thread, waited for by all.
   auto multiply = [&](auto issue) {
@@ -364,8 +369,9 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
       issue();
       tc_commit(bar);
     }
-    if (!mbar_wait(bar, phase & 1u, abort_flag)) good = false;
+    mbar_wait(bar, phase & 1u, abort_flag);
     phase ^= 1u;
+    __syncwarp();           // each lane polls its own way out; what follows is for whole warps
     tc_fence_after();
   };
   auto put_x = [&]() {
@@ -408,8 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
         st4(ps + row * 512 + ((unit ^ (row & 31)) << 4), w);
       }
     }
-    if (ctas > 1) cluster_sync();
-    else __syncthreads();
+    meet();
     // This CTA's rows of A: the partial squares in rank order, to every CTA.  What goes
     // between SMs takes the longest of a step (some 14 bytes a clock into an SM); with the units
     // that reach the diagonal alone, and the other side filled in by each CTA, it took as long.
@@ -456,8 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
       }
       proxy_fence();
     }
-    if (ctas > 1) cluster_sync();
-    else __syncthreads();
+    meet();
     // B = b A + c A A
     multiply([&]() {
       uint32_t more = 0;
@@ -569,15 +573,15 @@ __global__ void __launch_bounds__(kThreads, 1) small_kernel(const __grid_constan
       write8(s.param, s.pdtype, p.at, p.n, ok8, f);
     }
   }
-  if (!good) {
+  if (*abort_flag) {
     // a product that never ended: long enough for it to be over before TMEM goes
     const long long t0 = clock64();
     while (clock64() - t0 < (1 << 21)) {}
-    if (lane == 0) set_flag(flags, kFlagTimeout);
   }
   tc_fence_before();
   __syncthreads();
-  if (ctas > 1) cluster_sync();   // no CTA leaves while its shared memory may be read
+  if (tid == 0 && *abort_flag) set_flag(flags, kFlagTimeout);
+  meet();   // no CTA leaves while its shared memory may be read
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);

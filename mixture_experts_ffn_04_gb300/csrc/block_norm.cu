@@ -257,9 +257,10 @@ struct Team {
     row = tt / Gs;
     lane = tt - row * Gs;
   }
+  // (Its warps have to be whole: lanes come from loops of their own, a wait or one lane's store.)
   __device__ __forceinline__ void sync() const {
-    if (G == 32) __syncwarp();
-    else asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(G) : "memory");
+    __syncwarp();
+    if (G > 32) asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(G) : "memory");
   }
   // Sums over a row's threads; red: two values a warp of the block, 32 apart.
   __device__ __forceinline__ float sum(float v, float* red, int& slot) const {

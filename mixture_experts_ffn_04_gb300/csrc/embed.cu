@@ -201,13 +201,16 @@ __global__ void __launch_bounds__(512) hist_kernel(const int32_t* __restrict__ i
   const int64_t lo = blockIdx.x * tile, hi = min(T, lo + tile);
   // A frequent row is marked by few threads of a block (a warp's equal keys once, and not
   // again while its key stands in `seen`): thousands of atomics on one word are a queue.
-  for (int64_t i = lo + threadIdx.x; i < hi; i += 512) {
-    const int id = ids[i];
+  // Whole warps go round (those past the end with the key ~0, which no token has).
+  for (int64_t i = lo + threadIdx.x; i - (threadIdx.x & 31) < hi; i += 512) {
+    const int id = i < hi ? ids[i] : 0;
     if ((uint32_t)id >= (uint32_t)V) set_flag(flags, kFlagToken);
-    const uint32_t k = key_of(id, V, pad), same = __match_any_sync(__activemask(), k);
-    if ((__ffs(same) - 1) != (int)(threadIdx.x & 31)) continue;
-    atomicAdd(cnt + (k & (bins - 1)), (uint32_t)__popc(same));
-    if (present != nullptr && k < (uint32_t)V && atomicExch(seen + (k & (kSeen - 1)), k) != k) mark(present, k);
+    const uint32_t k = i < hi ? key_of(id, V, pad) : ~0u, same = __match_any_sync(0xffffffffu, k);
+    if (k != ~0u && (__ffs(same) - 1) == (int)(threadIdx.x & 31)) {
+      atomicAdd(cnt + (k & (bins - 1)), (uint32_t)__popc(same));
+      if (present != nullptr && k < (uint32_t)V && atomicExch(seen + (k & (kSeen - 1)), k) != k) mark(present, k);
+    }
+    __syncwarp();
   }
   __syncthreads();
   for (int d = threadIdx.x; d < bins; d += 512) hist[(int64_t)blockIdx.x * bins + d] = cnt[d];

@@ -120,7 +120,8 @@ moe_status moe_block_norm_backward(const moe_block_norm_shape *shape, const void
  * Precision: X is held under a fixed power of two, which the bounds below keep in
  * range.  bf16 matrices: one tensor-core product of fp16 operands (11 bits), while
  * a_i X_i takes X's 19 bits (an error outside X's row and column space grows by a_i
- * in every step); an X whose later steps grow such an error by 4 or less keeps 11.
+ * in every step); an X keeps 11 where the steps after it, and after any later X, grow such
+ * an error by 4 or less.
  * Where n >= 2 m the first two of three or more steps are taken as one polynomial in
  * A (its coefficients allowing).  fp32 matrices: X in two fp16 parts (22 bits), the
  * three products above 2^-22.  A smaller side of at most 128 (up to a length): X in

@@ -1010,20 +1010,26 @@ cudaError_t launch_orth_steps(const OrthBatch& t, int steps, const double (*coef
     g.out_low = to + rows * x_ld;
     // What the steps to come multiply an error outside X's rows and columns by: up to 4, 11
     // bits do (simulated as above, the last two X without their parts: 1.6e-3 again for
-    // normal entries, rank 16 1.0e-3 instead of 4.3e-4; the last three: rank 16 2.5e-3).
-    double grows = 1.0;
-    for (int k = i; k < steps; ++k) grows *= fabs(coef[k][0]);
-    const bool keep = grows > 4.0;
+    // normal entries, rank 16 1.0e-3 instead of 4.3e-4; the last three: rank 16 2.5e-3).  A
+    // later X that needs its parts takes them from this one's, so the most of any of them
+    // counts (a = 3.44, 3.44, 0.005, then 3.44 five times: rank 4 1.0e-3, by this X's factor
+    // alone 7.0e-2).
+    double grows = 1.0, most = 1.0;
+    for (int k = steps - 1; k >= i; --k) {
+      grows *= fabs(coef[k][0]);
+      most = std::max(most, grows);
+    }
+    const bool keep = most > 4.0;
     auto product = [&](auto columns) {
       constexpr int NB = decltype(columns)::value;
       if (two) return launch<kApply, kTwo, false, NB>(apply, g, st);
-      if (keep && low) return launch<kApply, kLow, false, NB>(apply, g, st);
+      if (keep) return launch<kApply, kLow, false, NB>(apply, g, st);   // (low: most only falls)
       if (low) return launch<kApply, kLowIn, false, NB>(apply, g, st);
       return launch<kApply, kOne, false, NB>(apply, g, st);
     };
     e = narrow_x ? product(std::integral_constant<int, 128>()) : product(std::integral_constant<int, 256>());
     if (e != cudaSuccess) return e;
-    low = low && keep;
+    low = keep;
   }
   *last = at;
   return cudaSuccess;

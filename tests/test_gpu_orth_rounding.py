@@ -1,0 +1,102 @@
+"""How far directions of bf16 matrices are off, against a model that rounds where the
+kernels round.
+
+The model (float64 between its roundings): X in one fp16 part of 11 bits and 8 more, or
+in the 11 alone where the steps to come (those after any later X too) grow an error
+outside X's row and column space by 4 or less; A, B, C and R in one fp16 part each, at
+their powers of two; the first two of three or more steps as one polynomial where a matrix is
+at least twice as wide as high; the result rounded to bf16.  What the kernels differ in is the
+order of fp32 sums, by some 2^-19 of a sum against roundings of 2^-12 on average: single
+roundings fall the other way, and the error's norm, over some 10^4 entries and more, moves by
+a few percent.  1.25 times the model's error is the bound; 1.5 for matrices of low rank, whose error
+is as large as the few directions that it happens to meet.
+"""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+S = (3.4445, -4.7750, 2.0315)
+# takes singular values near one to one another's range, and an error beside them nearly away
+DIP = (0.005, 1.0, -0.3)
+
+
+@pytest.fixture(scope="module")
+def m():
+    import mixture_experts_ffn_04_gb300 as m
+    return m
+
+
+def part(v, power):
+    return (v * 2.0 ** power).float().half().double() / 2.0 ** power
+
+
+def part19(v):
+    s = (v * 2.0 ** 13).float()
+    h = s.half().double()
+    unit = 2.0 ** (torch.floor(torch.log2(h.abs().clamp_min(2.0 ** -14))) - 18)
+    return (h + torch.round((s.double() - h) / unit) * unit) / 2.0 ** 13
+
+
+def normed(u):
+    x = u.double().mT if u.shape[-2] > u.shape[-1] else u.double()
+    return x / (torch.linalg.matrix_norm(x, keepdim=True) + 1e-7)
+
+
+def exact(u, coefs):
+    x = normed(u)
+    for a, b, c in coefs:
+        p = x @ x.mT
+        x = a * x + (b * p + c * (p @ p)) @ x
+    return x.mT if u.shape[-2] > u.shape[-1] else x
+
+
+def rounded(u, coefs):
+    x = part19(normed(u))
+    pair, i = x.shape[-1] >= 2 * x.shape[-2] and len(coefs) > 2, 0
+    while i < len(coefs):
+        (a, b, c), h = coefs[i], part(x, 13)
+        A = part(h @ h.mT, 11)
+        B = part(b * A + c * (A @ A), 9)
+        if pair and i == 0:
+            d, e, f = coefs[1]
+            C = part(a * A + B @ A, 11)
+            A = part(a * C + B @ C, 11)
+            D = part(e * A + f * (A @ A), 9)
+            x = a * d * x + part(a * D + d * B + D @ B, 8) @ h
+            i = 2
+        else:
+            x = a * x + B @ h
+            i += 1
+        grows = most = 1.0
+        for k in range(len(coefs) - 1, i - 1, -1):
+            grows *= abs(coefs[k][0])
+            most = max(most, grows)
+        x = part19(x) if most > 4.0 else part(x, 13)
+    x = x.mT if u.shape[-2] > u.shape[-1] else x
+    return x.to(torch.bfloat16)
+
+
+def draw(shape, rank=None, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    b, r, c = shape
+    if rank is None:
+        return torch.randn(shape, generator=g, device="cuda").bfloat16()
+    return (torch.randn((b, r, rank), generator=g, device="cuda")
+            @ torch.randn((b, rank, c), generator=g, device="cuda")).bfloat16()
+
+
+def off(got, want):
+    return torch.linalg.matrix_norm(got.double() - want) / torch.linalg.matrix_norm(want)
+
+
+@pytest.mark.parametrize("steps", [3, 5])
+@pytest.mark.parametrize("shape", [(2, 200, 330), (2, 150, 400), (2, 400, 150), (1, 1030, 520)])
+@pytest.mark.parametrize("rank", [1, 4, None])
+def test_a_small_coefficient_between_large_ones(m, shape, rank, steps):
+    """The X before the small one needs no second part, those after it do."""
+    coefs = (S, S, DIP) + (S,) * steps
+    u = draw(shape, rank, seed=sum(shape) + steps)
+    got = m.Orthogonalize(*shape, coefficients=coefs).forward(u)
+    want = exact(u, coefs)
+    bound = (1.25 if rank is None else 1.5) * off(rounded(u, coefs), want)
+    assert bool((off(got, want) <= bound).all()), (off(got, want) / bound).tolist()

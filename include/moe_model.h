@@ -66,6 +66,9 @@ moe_status moe_embed_backward(const moe_embed_shape *shape, const int32_t *ids, 
  * token.  x is the residual stream, y the block's output (NULL: only the norm
  * before the next block), s the new residual stream, h the next block's input,
  * computed from s before its rounding.  All in fp32, each output rounded once.
+ * Rows are copied ahead under a bounded wait: where one never comes, the rows its block
+ * had left become NaN, and the backward sets MOE_ERR_TIMEOUT (the forward, which has no
+ * workspace, has no other sign).
  * ------------------------------------------------------------------------- */
 typedef enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 } moe_gate_kind;
 

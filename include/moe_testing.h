@@ -64,6 +64,12 @@ moe_status moe_testing_router_logits(const moe_shape *shape, const void *x, cons
  * and no bit is set.  Needs the workspace's status word only. */
 moe_status moe_testing_wait_probe(void *ws, int64_t max_cycles, int32_t arrive, void *stream);
 
+/* How many SM clocks the block norms' rings wait for a row's copies: negative or
+ * above 4e9 = 4e9, about 2 s (default); 0 = they give up at once, the path of a copy that
+ * never comes (the copies do come, and are waited for apart before a block ends).
+ * Applies to later calls from any thread; returns the previous setting. */
+int64_t moe_testing_set_norm_wait(int64_t max_cycles);
+
 #ifdef __cplusplus
 }
 #endif

@@ -18,9 +18,11 @@
 // most kFlush of them in one sum), go to the workspace, and a second kernel adds
 // the groups' sums in a fixed order.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "../../include/moe_model.h"
+#include "../../include/moe_testing.h"
 #include "common.cuh"
 #include "internal.h"
 #include "tcgen05.cuh"
@@ -222,6 +224,7 @@ struct RingShape {
   int vpt, depth;
   int smem;
   int per_sm;   // blocks
+  long long limit;   // clocks of a wait
 };
 
 constexpr int kBarBytes = 512;   // barriers of all teams, 16-byte rows after them
@@ -231,20 +234,21 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
 }
-// Waits for a phase, about two seconds at most.
-__device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity) {
-  if (tc::mbar_try_wait(bar, parity)) return true;
-  const long long t0 = clock64();
-  while (!tc::mbar_try_wait(bar, parity))
-    if (clock64() - t0 > tc::kWaitCycles) return false;
-  return true;
-}
-
-// After a wait that ran out: every copy that was started had a wait of its own, but
-// this one's may still come.  A thousand times its latency, then the block may end.
-__device__ __forceinline__ void ring_drain() {
-  const long long t0 = clock64();
-  while (clock64() - t0 < (1 << 21)) {}
+// Waits for a phase, `limit` clocks at most (0: gives up at once).  A copy that has not come by
+// then may still do so: a thousand times its latency, so that it is not in flight when its
+// slot is used for something else or the block ends.
+__device__ __forceinline__ bool ring_wait(uint32_t bar, uint32_t parity, long long limit) {
+  long long t0;
+  if (limit > 0) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    t0 = clock64();
+    do {
+      if (tc::mbar_try_wait(bar, parity)) return true;
+    } while (clock64() - t0 <= limit);
+  }
+  t0 = clock64();
+  while (clock64() - t0 < (1 << 21) && !tc::mbar_try_wait(bar, parity)) {}
+  return false;
 }
 
 // What a team knows of its place.
@@ -310,6 +314,7 @@ struct Feed {
   int rows, first;            // rows in all; the team's first
   int step;                   // rows between a team's steps
   int R, row_bytes, depth;
+  long long limit;
   uint32_t ring, bars;        // of the team
   const unsigned char* rows_at;   // the team's ring
   int at;                     // the slot that is read, its wait's parity; kept from step to
@@ -323,6 +328,7 @@ struct Feed {
     step = q.NG * R;
     row_bytes = bytes;
     depth = q.depth;
+    limit = q.limit;
     rows_at = rings + (size_t)m.g * depth * STREAMS * R * row_bytes;
     ring = tc::smem_u32(rows_at);
     at = 0;
@@ -334,7 +340,7 @@ struct Feed {
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
   }
-  __device__ __forceinline__ bool wait() const { return ring_wait(bars + 8u * at, parity); }
+  __device__ __forceinline__ bool wait() const { return ring_wait(bars + 8u * at, parity, limit); }
   __device__ __forceinline__ const unsigned char* here() const { return rows_at + at * STREAMS * R * row_bytes; }
   __device__ __forceinline__ void next() {
     if (++at == depth) {
@@ -404,7 +410,7 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_ring_kernel(
     T* s, T* __restrict__ h, float2* __restrict__ rstd) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float red[2 * 32];
-  __shared__ volatile int lost;
+  __shared__ volatile int lost;   // a copy of the block never came
   if (threadIdx.x == 0) lost = 0;
   float* w1 = reinterpret_cast<float*>(smem + kBarBytes);
   float* w2 = w1 + H;
@@ -422,14 +428,17 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_ring_kernel(
   const float inv_h = 1.0f / (float)H;
   const int half = H >> 1, span = q.Gs * 8, c0 = m.lane * 8;
   int slot = 0;
-  bool fed = true;
+  bool fed = true, came = true;        // the copies: the block's, this thread's (the polling warp's)
   int t = f.first + m.row;             // the row
   int64_t to = (int64_t)t * H + c0;    // the thread's first column in it
   for (int i = 0; i < steps && t - m.row < rows; ++i, t += f.step, to += (int64_t)f.step * H, f.next()) {
-    if (m.tt < 32 && !f.wait()) lost = 1;   // the barrier hands it on to the team
-    m.sync();                               // the step before is behind every thread
+    if (m.tt < 32) {
+      came = came && f.wait();
+      if (!came) lost = 1;                      // the barrier hands it on to the team
+    }
+    m.sync();                                   // the step before is behind every thread
+    if (m.tt == 0 && came) f.refill(i, steps);  // into its slot
     fed = !lost;
-    if (m.tt == 0) f.refill(i, steps);      // into its slot
     const bool on = t < rows;
     bool live[VPT];
 #pragma unroll
@@ -451,7 +460,7 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_ring_kernel(
       }
       r1 = rsqrtf(m.sum(sq.x + sq.y, red, slot) * inv_h + eps);
     }
-    if (!fed) r1 = __int_as_float(0x7fc00000);   // a copy that never came
+    if (!fed) r1 = __int_as_float(0x7fc00000);
     const float2 rg = both(r1 * gt), rx = both(fed ? res : r1);
     float2 sq = both(0.0f);
 #pragma unroll
@@ -484,7 +493,6 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_ring_kernel(
     }
     if (rstd && on && m.lane == 0) rstd[t] = make_float2(w_post ? r1 : 0.0f, r2);
   }
-  if (!fed) ring_drain();
 }
 
 struct BwdArgs {
@@ -496,6 +504,7 @@ struct BwdArgs {
   void *dx, *dy;
   float* dgate;      // of a token gate
   float* part;       // [flushes][blocks][NG][2][H] (rings: [blocks][2][H]), or NULL
+  uint32_t* flags;
 };
 
 template <typename T, int VPT>
@@ -673,7 +682,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 896 : 512, 1) norm_backward_ring_ke
                                                                                      int steps) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ float red[2 * 32];
-  __shared__ volatile int lost;
+  __shared__ volatile int lost;   // a copy of the block never came
   if (threadIdx.x == 0) lost = 0;
   const int H = a.H;
   float* w1 = reinterpret_cast<float*>(smem + kBarBytes);
@@ -699,7 +708,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 896 : 512, 1) norm_backward_ring_ke
   __syncthreads();
   const float inv_h = 1.0f / (float)H;
   int slot = 0;
-  bool fed = true;
+  bool fed = true, came = true;   // the copies: the block's, this thread's (the polling warp's)
   Pairs c_e[VPT], c_pre[VPT];   // the columns' sums over this team's rows
 #pragma unroll
   for (int k = 0; k < VPT; ++k)
@@ -725,11 +734,14 @@ __global__ void __launch_bounds__(VPT == 1 ? 896 : 512, 1) norm_backward_ring_ke
     const float gt = gate_next;
     ask(t + f.step);
     if (!post) r.x = 1.0f;
-    if (m.tt < 32 && feeds && !f.wait()) lost = 1;      // the barrier hands it on to the team
-    m.sync();                                           // the step before is behind every thread
+    if (m.tt < 32 && feeds) {
+      came = came && f.wait();
+      if (!came) lost = 1;                               // the barrier hands it on to the team
+    }
+    m.sync();                                            // the step before is behind every thread
+    if (m.tt == 0 && feeds && came) f.refill(i, steps);  // into its slot
     fed = !lost;
-    if (m.tt == 0 && feeds) f.refill(i, steps);         // into its slot
-    if (!fed) r.x = r.y = __int_as_float(0x7fc00000);   // a copy that never came
+    if (!fed) r.x = r.y = __int_as_float(0x7fc00000);
     const T* bx = reinterpret_cast<const T*>(f.here()) + (size_t)m.row * H + c0;
     const T *by = bx + (size_t)q.R * H, *bh = by + (size_t)q.R * H, *bs = bh + (size_t)q.R * H;
     Pairs D[VPT];
@@ -782,7 +794,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 896 : 512, 1) norm_backward_ring_ke
       if (dx) {
         Pairs o;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o.p[e] = mul2(both(a.res), D[k].p[e]);
+        for (int e = 0; e < 4; ++e) o.p[e] = mul2(both(fed ? a.res : r.x), D[k].p[e]);
         store_pairs<T>(dx + to + k * span, o);
       }
       if (!with_y) continue;
@@ -814,7 +826,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 896 : 512, 1) norm_backward_ring_ke
       store_pairs<T>(dy + to + k * span, D[k]);
     }
   }
-  if (!fed) ring_drain();
+  if (!fed && m.tt == 0) set_flag(a.flags, kFlagTimeout);
   if (!a.part) return;
   // The rows' sums of the block in the ring, which no copy fills any more: a thread's
   // columns lie at its own row of its team, then added in that order.
@@ -973,10 +985,17 @@ Split split_of(const NShape& s) {
 int64_t parts_of(const Split& p) { return p.q.depth > 0 ? p.blocks : (int64_t)p.flushes * p.blocks * p.g.NG; }
 size_t part_bytes(const NShape& s, const Split& p) { return (size_t)parts_of(p) * 2 * s.H * 4; }
 
+std::atomic<int64_t> g_wait{-1};   // moe_testing_set_norm_wait
+long long wait_limit() {
+  const int64_t v = g_wait.load(std::memory_order_relaxed);
+  return v < 0 || v > tc::kWaitCycles ? tc::kWaitCycles : v;
+}
+
 template <typename T>
 cudaError_t forward(const NShape& s, const void* x, const void* y, const void* w_post, const void* gate,
                     const void* w_pre, void* so, void* h, float* rstd, cudaStream_t st) {
-  const RingShape q = ring_shape(s.H, s.esize, 2, 64, 1024, 1024);
+  RingShape q = ring_shape(s.H, s.esize, 2, 64, 1024, 1024);
+  q.limit = wait_limit();
   const int64_t per = (int64_t)q.NG * q.R, rows = (s.T + std::max<int64_t>(per, 1) - 1) / std::max<int64_t>(per, 1);
   const int64_t resident = (int64_t)tc_sm_count() * q.per_sm;
   if (q.depth > 0 && rows > 2 * resident) {
@@ -1014,10 +1033,12 @@ cudaError_t backward(const NShape& s, const Split& p, BwdArgs a, void* dw_post, 
   cudaError_t e;
   if (p.q.depth > 0) {
     static std::atomic<uint64_t> done[2];
+    RingShape q = p.q;
+    q.limit = wait_limit();
     auto go = [&](auto kernel) {
       const cudaError_t f = allow_smem(kernel, kSmemBlock - kStatic, done[p.q.vpt - 1]);
       if (f != cudaSuccess) return f;
-      return launch_after(kernel, (unsigned)p.blocks, (unsigned)(p.q.G * p.q.NG), p.q.smem, st, 1, a, p.q, p.steps);
+      return launch_after(kernel, (unsigned)p.blocks, (unsigned)(p.q.G * p.q.NG), p.q.smem, st, 1, a, q, p.steps);
     };
     e = p.q.vpt == 1 ? go(norm_backward_ring_kernel<T, 1>) : go(norm_backward_ring_kernel<T, 2>);
   } else {
@@ -1134,6 +1155,7 @@ extern "C" moe_status moe_block_norm_backward(const moe_block_norm_shape* shape,
   a.dx = dx;
   a.dy = dy;
   a.dgate = channel ? nullptr : static_cast<float*>(dgate);
+  a.flags = static_cast<uint32_t*>(ws);
   // without tokens the columns' sums are zeros, written like any others
   if (dw_post || dw_pre || (channel && dgate)) a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + 256);
   if (s.T == 0 && !a.part) return MOE_OK;
@@ -1141,4 +1163,8 @@ extern "C" moe_status moe_block_norm_backward(const moe_block_norm_shape* shape,
   CHECK_CUDA(s.dtype == MOE_F32 ? bn::backward<float>(s, p, a, dw_post, dcol, dw_pre, (cudaStream_t)stream)
                                 : bn::backward<bf16>(s, p, a, dw_post, dcol, dw_pre, (cudaStream_t)stream));
   return MOE_OK;
+}
+
+extern "C" int64_t moe_testing_set_norm_wait(int64_t max_cycles) {
+  return bn::g_wait.exchange(max_cycles < 0 ? -1 : max_cycles);
 }

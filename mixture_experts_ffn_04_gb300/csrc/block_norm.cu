@@ -1063,7 +1063,8 @@ moe_status check_inputs(const NShape& s, const void* x, const void* y, const voi
   if (!x && s.T > 0) return fail(MOE_ERR_INVALID_ARG, "x must be non-NULL");
   if (!y && (w_post || s.gate != MOE_GATE_NONE) && s.T > 0)
     return fail(MOE_ERR_INVALID_ARG, "w_post and a gate need y");
-  if ((s.gate != MOE_GATE_NONE) != (gate != nullptr))
+  const bool empty_gate = s.gate == MOE_GATE_TOKEN && s.T == 0;   // an array of none has no address
+  if ((s.gate != MOE_GATE_NONE) != (gate != nullptr || empty_gate))
     return fail(MOE_ERR_INVALID_ARG, "gate must be given iff the shape has one");
   if (!aligned16(x) || !aligned16(y) || !aligned16(w_post) || !aligned16(w_pre) ||
       (s.gate == MOE_GATE_CHANNEL && !aligned16(gate)))
@@ -1127,7 +1128,7 @@ extern "C" moe_status moe_block_norm_backward(const moe_block_norm_shape* shape,
   if (!rstd && s.T > 0) return fail(MOE_ERR_INVALID_ARG, "rstd must be non-NULL");
   if ((dy && !y && s.T > 0) || (dw_post && !w_post) || (dgate && !gate) || (dw_pre && !w_pre))
     return fail(MOE_ERR_INVALID_ARG, "a gradient's input must be non-NULL");
-  if (!dx && !dy && !dw_post && !dgate && !dw_pre) return fail(MOE_ERR_INVALID_ARG, "no gradient is asked for");
+  if (!dx && !dy && !dw_post && !dgate && !dw_pre && s.T > 0) return fail(MOE_ERR_INVALID_ARG, "no gradient is asked for");
   if (!aligned16(ds) || !aligned16(dh) || !aligned16(dx) || !aligned16(dy))
     return fail(MOE_ERR_INVALID_ARG, "ds, dh, dx and dy must be 16-byte aligned");
   if (((uintptr_t)dw_post | (uintptr_t)dw_pre | (uintptr_t)dgate) & (uintptr_t)(s.esize - 1) ||

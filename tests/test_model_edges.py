@@ -1,0 +1,46 @@
+"""Calls at the edges of what the embedding and the block norms allow, as far as the host
+answers them: no GPU needed."""
+import ctypes
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def m():
+    import mixture_experts_ffn_04_gb300 as m
+    from mixture_experts_ffn_04_gb300 import build
+    build.build()
+    m.lib()
+    return m
+
+
+def norm_shape(m, **kw):
+    s = m.MoEBlockNormShape()
+    s.tokens, s.hidden, s.dtype, s.residual_scale, s.eps = 64, 256, m.MOE_BF16, 1.0, 1e-6
+    for k, v in kw.items():
+        setattr(s, k, v)
+    return s
+
+
+def test_norms_of_no_tokens(m):
+    """Arrays of no tokens have no address; a gate for each of them is one."""
+    f, b = m.lib().moe_block_norm_forward, m.lib().moe_block_norm_backward
+    s = norm_shape(m, tokens=0, gate=m.MOE_GATE_TOKEN)
+    n = m.moe_block_norm_workspace_bytes(s)
+    assert n > 0
+    assert f(ctypes.byref(s), None, None, 16, None, 16, None, None, None, None) == m.MOE_OK, m.moe_last_error()
+    # nothing but gradients of no tokens
+    assert b(ctypes.byref(s), None, None, None, None, 16, None, 16, None, None, None, None, None, None, 256, n,
+             None) == m.MOE_OK, m.moe_last_error()
+    plain = norm_shape(m, tokens=0)
+    assert b(ctypes.byref(plain), None, None, None, None, None, None, None, None, None, None, None, None, None, 256, n,
+             None) == m.MOE_OK, m.moe_last_error()
+    # a gate for each channel has its addresses all the same, and so has one for each of some tokens
+    for kw in (dict(tokens=0, gate=m.MOE_GATE_CHANNEL), dict(gate=m.MOE_GATE_TOKEN)):
+        s = norm_shape(m, **kw)
+        assert f(ctypes.byref(s), 16, 16, 16, None, 16, 16, 16, 16, None) == m.MOE_ERR_INVALID_ARG
+        assert "gate" in m.moe_last_error()
+    s = norm_shape(m)
+    assert b(ctypes.byref(s), 16, 16, 16, 16, 16, None, 16, 16, None, None, None, None, None, 256, 1 << 40,
+             None) == m.MOE_ERR_INVALID_ARG
+    assert "no gradient" in m.moe_last_error()

@@ -734,9 +734,12 @@ def moe_embed_workspace_bytes(shape: MoEEmbedShape) -> int:
 
 
 def moe_embed_forward(shape: MoEEmbedShape, w, ids, y, ws, stream=None):
-    """w may be rows of a wider buffer (the stride goes into the shape)."""
+    """w may be rows of a wider buffer (its stride goes into a copy of the shape)."""
     at, dt, T, H = _device(ws), _ACT[shape.dtype], shape.tokens, shape.hidden
-    wp, shape.w_stride = _rows(w, shape.vocab, H, dt, "w")
+    wp, ld = _rows(w, shape.vocab, H, dt, "w")
+    if (shape.w_stride or H) != ld:
+        shape = MoEEmbedShape.from_buffer_copy(shape)
+        shape.w_stride = ld
     if w.get_device() != at:
         raise ValueError("w is on %s, the workspace on cuda:%d" % (w.device, at))
     st = lib().moe_embed_forward(ctypes.byref(shape), wp, _arg(ids, T, torch.int32, at, "ids", False),

@@ -44,3 +44,20 @@ def test_norms_of_no_tokens(m):
     assert b(ctypes.byref(s), 16, 16, 16, 16, 16, None, 16, 16, None, None, None, None, None, 256, 1 << 40,
              None) == m.MOE_ERR_INVALID_ARG
     assert "no gradient" in m.moe_last_error()
+
+
+def test_a_refused_table_leaves_the_shape_as_it_was(m, monkeypatch):
+    """The row stride of a table belongs to its call: the calls after a refused one, and the
+    gradient, which reads no table, go on."""
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(m, "_device", lambda t: -1)     # host tensors
+    s = m.MoEEmbedShape()
+    s.tokens, s.hidden, s.vocab, s.dtype, s.padding_idx, s.scale = 6, 16, 10, m.MOE_F32, -1, 1.0
+    n = m.moe_embed_workspace_bytes(s)
+    ids, y, ws = torch.zeros(6, dtype=torch.int32), torch.zeros(6, 16), torch.zeros(n, dtype=torch.uint8)
+    with pytest.raises(m.MoEError, match="w_stride"):
+        m.moe_embed_forward(s, torch.zeros(10, 20)[:, :16], ids, y, ws, stream=0)
+    assert s.w_stride == 0 and m.moe_embed_workspace_bytes(s) == n
+    with pytest.raises(ValueError, match="ids"):
+        m.moe_embed_forward(s, torch.zeros(10, 24)[:, :16], ids[:5], y, ws, stream=0)
+    assert s.w_stride == 0

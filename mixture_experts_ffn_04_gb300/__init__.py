@@ -1129,7 +1129,10 @@ class BlockNorm:
     gate: None, "channel" ([hidden] in dtype) or "token" ([tokens] fp32); unit_offset:
     the weights count from 1.  Without y (the norm before the first block) s is
     residual_scale * x, without w_pre there is no h, without w_post y is taken as it is.
-    Streams as in LinearCrossEntropy."""
+    self.rstd holds the norms of the last forward, which the backward needs: an object
+    serves one place of a model, or several whose callers keep an rstd ([tokens, 2] fp32) for
+    each and give it to both calls.  The status is the backward's; a forward whose rows never came
+    shows it by NaN.  Streams as in LinearCrossEntropy."""
 
     def __init__(self, tokens: int, hidden: int, dtype=torch.bfloat16, gate: Optional[str] = None,
                  residual_scale: float = 1.0, eps: float = 1e-6, unit_offset: bool = False,
@@ -1143,26 +1146,27 @@ class BlockNorm:
         self.ws = _alloc_ws(moe_block_norm_workspace_bytes(s), device, None, "BlockNorm")
         self.rstd = torch.zeros((tokens, 2), dtype=torch.float32, device=device)
 
-    def forward(self, x, y=None, w_post=None, gate=None, w_pre=None, s=None, h=None, stream=None):
-        """(s, h); self.rstd is what the backward needs."""
+    def forward(self, x, y=None, w_post=None, gate=None, w_pre=None, s=None, h=None, stream=None, rstd=None):
+        """(s, h); rstd (self.rstd unless given) is what the backward needs."""
         if s is None:
             s = _like(stream, x)
         if h is None and w_pre is not None:
             h = _like(stream, x)
-        moe_block_norm_forward(self.shape, x, y, w_post, gate, w_pre, s, h, self.rstd, stream)
+        moe_block_norm_forward(self.shape, x, y, w_post, gate, w_pre, s, h,
+                               self.rstd if rstd is None else rstd, stream)
         return s, h
 
     def backward(self, ds, dh, x, y=None, w_post=None, gate=None, w_pre=None, dx=None, dy=None,
-                 dw_post=None, dgate=None, dw_pre=None, stream=None) -> BlockGrads:
-        """Gradients after a forward with the same inputs, given ds (of s, or None for
-        zeros) and dh (of h)."""
+                 dw_post=None, dgate=None, dw_pre=None, stream=None, rstd=None) -> BlockGrads:
+        """Gradients after a forward with the same inputs (the last one, or the one that was
+        given this rstd), given ds (of s, or None for zeros) and dh (of h)."""
         def like(out, t):
             return _like(stream, t) if out is None and t is not None else out
 
         d = BlockGrads(like(dx, x), like(dy, y), like(dw_post, w_post), like(dgate, gate),
                        like(dw_pre, w_pre))
-        moe_block_norm_backward(self.shape, ds, dh, x, y, w_post, gate, w_pre, self.rstd, *d, self.ws,
-                                stream)
+        moe_block_norm_backward(self.shape, ds, dh, x, y, w_post, gate, w_pre,
+                                self.rstd if rstd is None else rstd, *d, self.ws, stream)
         return d
 
     def device_status(self, stream=None):

@@ -19,6 +19,7 @@
 // the groups' sums in a fixed order.
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 
 #include "../../include/moe_model.h"
@@ -747,7 +748,11 @@ __global__ void __launch_bounds__(VPT == 1 ? 896 : 512, 1) norm_backward_ring_ke
     Pairs D[VPT];
     if (pre) {
       float2 sum = both(0.0f);
-      const float2 rx = both(a.res * r.y), ry = both(gt * r.x * r.y);
+      // under an eps near fp32's smallest the product of both norms of a row of zeros leaves
+      // the range, and infinity times its zeros would be NaN
+      float r12 = gt * r.x * r.y;
+      r12 = r12 > FLT_MAX ? FLT_MAX : r12 < -FLT_MAX ? -FLT_MAX : r12;
+      const float2 rx = both(a.res * r.y), ry = both(r12);
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
         if (!live[k]) continue;
@@ -812,7 +817,7 @@ __global__ void __launch_bounds__(VPT == 1 ? 896 : 512, 1) norm_backward_ring_ke
     if (post || a.dgate) c1 = m.sum(c1, red, slot);
     if (a.dgate && on && m.lane == 0) a.dgate[t] = c1;
     if (!dy) continue;
-    const float2 mine = both(gt * r.x), back = both(post ? -r.x * (gt * r.x) * (c1 * inv_h) : 0.0f);
+    const float2 mine = both(gt * r.x), back = both(post ? -(c1 * (inv_h * r.x)) * (gt * r.x) : 0.0f);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       if (!live[k]) continue;

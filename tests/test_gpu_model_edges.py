@@ -46,3 +46,37 @@ def test_one_object_for_two_layers(T, H, dt):
         assert torch.equal(p, q)
     with pytest.raises(ValueError, match="rstd"):
         one.forward(layers[0][0], **layers[0][1], rstd=rstd[0][:1])
+
+
+@pytest.mark.parametrize("gate", [None, "token", "channel"])
+@pytest.mark.parametrize("T,H,dt", [(40, 256, torch.float32), (40, 2816, torch.bfloat16), (9, 8200, torch.float32)])
+def test_rows_of_zeros_under_a_tiny_eps(T, H, dt, gate):
+    """1 / sqrt(eps) of both norms is a number of fp32, their product is not: nothing of a row of
+    zeros reaches the sums over rows, and dx, dy are ds, dh times what the formula says."""
+    eps = 1e-42
+    g = torch.Generator(device="cuda").manual_seed(H)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").to(dt)
+    z, w, ds = torch.zeros((T, H), device="cuda", dtype=dt), r(H), r(T, H)
+    k = {None: None, "channel": r(H), "token": torch.rand(T, generator=g, device="cuda")}[gate]
+    op = m.BlockNorm(T, H, dtype=dt, gate=gate, eps=eps)
+    s, h = op.forward(z, z, w_post=w, gate=k, w_pre=w)
+    assert float(s.abs().max()) == float(h.abs().max()) == 0.0
+    d = op.backward(ds, torch.zeros_like(ds), z, z, w_post=w, gate=k, w_pre=w)
+    for t in (d.dw_post, d.dw_pre, d.dgate):
+        assert t is None or float(t.abs().max()) == 0.0
+    assert torch.equal(d.dx, ds)
+    # dy = g ds w_post / sqrt(eps): four roundings of fp32 and the reciprocal root's two units, then the type's.
+    # eps is a subnormal of fp32 here: what it is rounded to counts
+    root = float(torch.tensor(eps, dtype=torch.float32).double()) ** -0.5
+    gain = 1.0 if k is None else (k.double() if gate == "channel" else k.double()[:, None])
+    want = gain * ds.double() * w.double() * root
+    tol = torch.finfo(dt).eps / 2 + 8 * 2.0 ** -24
+    assert bool(((d.dy.double() - want).abs() <= tol * want.abs()).all())
+    # rows of values beside them
+    x = r(T, H)
+    x[::2] = 0.0
+    s, h = op.forward(x, x, w_post=w, gate=k, w_pre=w)
+    d = op.backward(torch.zeros_like(ds), ds, x, x, w_post=w, gate=k, w_pre=w)
+    for t in (s, h, d.dw_pre):
+        assert bool(torch.isfinite(t).all())
+    assert float(h[::2].abs().max()) == 0.0

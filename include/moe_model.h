@@ -31,7 +31,7 @@ extern "C" {
  * ------------------------------------------------------------------------- */
 typedef struct {
   int64_t tokens;       /* T >= 0, at most 2^28 */
-  int32_t hidden;       /* H, a positive multiple of 8 */
+  int32_t hidden;       /* H, a positive multiple of 8, at most 2^28 */
   int32_t vocab;        /* V >= 1, at most 2^30 */
   int32_t dtype;        /* moe_dtype of w, y, dy, dw_add, dw */
   int32_t padding_idx;  /* -1 or in [0, vocab) */

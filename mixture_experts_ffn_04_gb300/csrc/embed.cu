@@ -549,6 +549,7 @@ moe_status decode(const moe_embed_shape* s, EShape* o, const char** why) {
   if (s->dtype != MOE_F32 && s->dtype != MOE_BF16) { *why = "dtype must be MOE_F32 or MOE_BF16"; return MOE_ERR_UNSUPPORTED; }
   if (s->tokens < 0 || s->tokens > (1ll << 28)) { *why = "tokens must be in [0, 2^28]"; return MOE_ERR_INVALID_ARG; }
   if (s->hidden <= 0 || s->hidden % 8) { *why = "hidden must be a positive multiple of 8"; return MOE_ERR_INVALID_ARG; }
+  if (s->hidden > (1 << 28)) { *why = "hidden must be at most 2^28"; return MOE_ERR_INVALID_ARG; }
   if (s->vocab < 1 || s->vocab > (1 << 30)) { *why = "vocab must be in [1, 2^30]"; return MOE_ERR_INVALID_ARG; }
   if (s->padding_idx < -1 || s->padding_idx >= s->vocab) { *why = "padding_idx must be -1 or in [0, vocab)"; return MOE_ERR_INVALID_ARG; }
   if (!std::isfinite(s->scale) || !std::isfinite((float)s->scale)) { *why = "scale must be finite in fp32"; return MOE_ERR_INVALID_ARG; }

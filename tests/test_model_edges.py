@@ -61,3 +61,17 @@ def test_a_refused_table_leaves_the_shape_as_it_was(m, monkeypatch):
     with pytest.raises(ValueError, match="ids"):
         m.moe_embed_forward(s, torch.zeros(10, 24)[:, :16], ids[:5], y, ws, stream=0)
     assert s.w_stride == 0
+
+
+def test_rows_past_31_bits_of_bytes_are_refused(m):
+    """A lookup of rows of 2 GiB counted their pieces in 32 bits."""
+    for dtype in (m.MOE_F32, m.MOE_BF16):
+        s = m.MoEEmbedShape()
+        s.tokens, s.vocab, s.dtype, s.padding_idx, s.scale = 1, 1, dtype, -1, 1.0
+        s.hidden = 1 << 28
+        assert m.moe_embed_workspace_bytes(s) > 0
+        s.hidden = (1 << 28) + 8
+        assert m.moe_embed_workspace_bytes(s) == 0 and "hidden" in m.moe_last_error()
+        for call in (m.lib().moe_embed_forward, m.lib().moe_embed_backward):
+            a = (16, 16, 16) if call is m.lib().moe_embed_forward else (16, 16, None, 16)
+            assert call(ctypes.byref(s), *a, 256, 1 << 60, None) == m.MOE_ERR_INVALID_ARG

@@ -30,7 +30,7 @@ extern "C" {
  * sums), each output rounded once.
  * ------------------------------------------------------------------------- */
 typedef struct {
-  int64_t tokens;       /* T >= 0, at most 2^28 */
+  int64_t tokens;       /* T >= 0, at most 2^28; T H below 2^47 */
   int32_t hidden;       /* H, a positive multiple of 8, at most 2^28 */
   int32_t vocab;        /* V >= 1, at most 2^30 */
   int32_t dtype;        /* moe_dtype of w, y, dy, dw_add, dw */

@@ -543,6 +543,14 @@ __global__ void __launch_bounds__(32 * kSumWarps) join_kernel(const SumArgs a, c
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
+// Chunks for some 16 warps an SM, which are all there at once (a border costs a row of fp32
+// written and read), of 8 to 256 tokens.  60001 tokens, 32001 x 1000 in fp32: 113 us with the
+// sort, in powers of two 123, for 24 warps an SM 131; 30000, 50257 x 2048 in bf16 150, 166, 147
+int64_t chunk_of(int64_t T, int slabs) {
+  return std::min<int64_t>(256, std::max<int64_t>(8, (T * slabs / (16 * 152) + 7) / 8 * 8));
+}
+int slabs_of(int H) { return (H + 255) / 256; }
+
 moe_status decode(const moe_embed_shape* s, EShape* o, const char** why) {
   *why = "";
   if (!s) { *why = "shape is NULL"; return MOE_ERR_INVALID_ARG; }
@@ -556,6 +564,12 @@ moe_status decode(const moe_embed_shape* s, EShape* o, const char** why) {
   if (s->w_stride != 0 && (s->w_stride < s->hidden || s->w_stride % 8)) {
     *why = "w_stride must be 0, or at least hidden and a multiple of 8";
     return MOE_ERR_INVALID_ARG;
+  }
+  const int slabs = slabs_of(s->hidden);
+  const int64_t chunk = chunk_of(s->tokens, slabs);
+  if ((s->tokens + chunk - 1) / chunk * slabs > 0x7fffffff) {    // warps of the gradient's sums
+    *why = "tokens times hidden is too large";
+    return MOE_ERR_UNSUPPORTED;
   }
   o->T = s->tokens;
   o->H = s->hidden;
@@ -585,11 +599,8 @@ Layout layout_of(const EShape& s) {
     return at;
   };
   L.dig = digits_for(s.V);
-  L.slabs = (s.H + 255) / 256;
-  // Chunks for some 16 warps an SM, which are all there at once (a border costs a row of fp32
-  // written and read), of 8 to 256 tokens.  60001 tokens, 32001 x 1000 in fp32: 113 us with the
-  // sort, in powers of two 123, for 24 warps an SM 131; 30000, 50257 x 2048 in bf16 150, 166, 147
-  const int64_t chunk = std::min<int64_t>(256, std::max<int64_t>(8, (s.T * L.slabs / (16 * 152) + 7) / 8 * 8));
+  L.slabs = slabs_of(s.H);
+  const int64_t chunk = chunk_of(s.T, L.slabs);
   L.chunk = (int)chunk;
   L.chunks = (s.T + chunk - 1) / chunk;
   L.tile = ((s.T + kMaxTiles - 1) / kMaxTiles + kTileMin - 1) / kTileMin * kTileMin;
@@ -679,8 +690,6 @@ moe_status backward(const EShape& s, const Layout& L, char* b, const int32_t* id
   a.right = reinterpret_cast<float*>(b + L.right);
   a.acc_blocks = (L.chunks * L.slabs + kSumWarps - 1) / kSumWarps;
   a.present = present;
-  if (a.acc_blocks + fill_blocks > 0x7fffffff || L.chunks * L.slabs > 0x7fffffff)
-    return fail(MOE_ERR_UNSUPPORTED, "tokens times hidden is too large");
   if (a.acc_blocks + fill_blocks > 0)
     CHECK_CUDA(launch_after(sum_kernel<T>, (unsigned)(a.acc_blocks + fill_blocks), 32 * kSumWarps, 0, st, 1, a,
                             static_cast<const T*>(dy), static_cast<const T*>(add), static_cast<T*>(dw)));

@@ -75,3 +75,14 @@ def test_rows_past_31_bits_of_bytes_are_refused(m):
         for call in (m.lib().moe_embed_forward, m.lib().moe_embed_backward):
             a = (16, 16, 16) if call is m.lib().moe_embed_forward else (16, 16, None, 16)
             assert call(ctypes.byref(s), *a, 256, 1 << 60, None) == m.MOE_ERR_INVALID_ARG
+
+
+def test_too_much_gradient_is_refused_before_anything_runs(m):
+    """2^32 pieces of sums: refused with the shape, not after the sort has been launched."""
+    s = m.MoEEmbedShape()
+    s.tokens, s.hidden, s.vocab, s.dtype, s.padding_idx, s.scale = 1 << 28, 1 << 20, 10, m.MOE_BF16, -1, 1.0
+    assert m.moe_embed_workspace_bytes(s) == 0 and "tokens times hidden" in m.moe_last_error()
+    st = m.lib().moe_embed_backward(ctypes.byref(s), 16, 16, None, 16, 256, 1 << 62, None)
+    assert st == m.MOE_ERR_UNSUPPORTED and "tokens times hidden" in m.moe_last_error()
+    s.hidden = 1 << 18
+    assert m.moe_embed_workspace_bytes(s) > 0

@@ -77,7 +77,7 @@ __device__ __forceinline__ void store8(T* p, const float* f) {
 struct Geometry {
   int G, NG, vpt;
 };
-Geometry geometry(int H, int wide) {
+Geometry geometry(int H) {
   const int vecs = H / 8;
   Geometry g;
   if (vecs <= 32) {
@@ -85,7 +85,7 @@ Geometry geometry(int H, int wide) {
     g.G = 4;
     while (g.G < vecs) g.G *= 2;
   } else {
-    g.vpt = vecs <= wide ? 1 : (vecs <= 1024 ? 2 : 4);
+    g.vpt = vecs <= 512 ? 1 : (vecs <= 1024 ? 2 : 4);
     g.G = ((vecs + g.vpt - 1) / g.vpt + 31) / 32 * 32;
   }
   g.NG = std::max(1, 256 / g.G);
@@ -498,24 +498,25 @@ __global__ void __launch_bounds__(1024, 1) norm_forward_ring_kernel(
 
 struct BwdArgs {
   int64_t rows;
-  int H, G, NG, kind, flushes;
+  int H, kind, flushes;
   float off, res;
   const void *ds, *dh, *x, *y, *w_post, *gate, *w_pre;
   const float2* rstd;
   void *dx, *dy;
   float* dgate;      // of a token gate
-  float* part;       // [flushes][blocks][NG][2][H] (rings: [blocks][2][H]), or NULL
+  float* part;       // [flushes][blocks][2][H] (rings: [blocks][2][H]), or NULL
   uint32_t* flags;
 };
 
+// Rows too wide for a ring of two (fp32 from H = 5792, bf16 from 8200): a block a row, held in
+// registers.
 template <typename T, int VPT>
 __global__ void __launch_bounds__(VPT == 4 ? 1024 : 512) norm_backward_kernel(const BwdArgs a) {
   __shared__ float red[2][1][kMaxWarps];
   __shared__ float red2[2][2][kMaxWarps];
   pdl_trigger();
   pdl_wait();
-  const int G = a.G, H = a.H;
-  const int g = threadIdx.x / G, lane = threadIdx.x - g * G;
+  const int G = blockDim.x, H = a.H, lane = threadIdx.x;
   int slot = 0, slot2 = 0;
   const float inv_h = 1.0f / (float)H;
   const T* w_post = static_cast<const T*>(a.w_post);
@@ -540,7 +541,7 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : 512) norm_backward_kernel(co
   }
   int count = 0, flush = 0;
   auto put_sums = [&]() {
-    float* p = a.part + (((int64_t)flush * gridDim.x + blockIdx.x) * a.NG + g) * 2 * H;
+    float* p = a.part + ((int64_t)flush * gridDim.x + blockIdx.x) * 2 * H;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int c = (lane + v * G) * 8;
@@ -554,24 +555,21 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : 512) norm_backward_kernel(co
     ++flush;
     count = 0;
   };
-  for (int64_t base = (int64_t)blockIdx.x * a.NG; base < a.rows; base += (int64_t)gridDim.x * a.NG) {
-    const int64_t t = base + g;
-    const bool on = t < a.rows;
+  for (int64_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
     Eight<T> ux[VPT], uy[VPT], us[VPT], uh[VPT];
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int c = (lane + v * G) * 8;
-      const bool live = on && c < H;
+      const bool live = c < H;
       ux[v] = live && w_pre ? load8<T>(x + t * H + c) : zero8<T>();
       uy[v] = live && y ? load8<T>(y + t * H + c) : zero8<T>();
       us[v] = live && ds ? load8<T>(ds + t * H + c) : zero8<T>();
       uh[v] = live && w_pre ? load8<T>(dh + t * H + c) : zero8<T>();
     }
-    float2 r = make_float2(0.0f, 0.0f);
-    if (on) r = a.rstd[t];
+    float2 r = a.rstd[t];
     if (!w_post) r.x = 1.0f;
     float gt = 1.0f;
-    if (a.kind == MOE_GATE_TOKEN && on) gt = static_cast<const float*>(a.gate)[t];
+    if (a.kind == MOE_GATE_TOKEN) gt = static_cast<const float*>(a.gate)[t];
     // D: first the row sum of dh w_pre sn
     float D[VPT][8];
     float c2[1] = {0.0f};
@@ -620,7 +618,7 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : 512) norm_backward_kernel(co
         for (int e = 0; e < 8; ++e) D[v][e] = fs[e];
       }
       const int c = (lane + v * G) * 8;
-      if (dx && on && c < H) {
+      if (dx && c < H) {
         float o[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = a.res * D[v][e];
@@ -649,13 +647,13 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : 512) norm_backward_kernel(co
       }
     }
     row_sum<2>(c1, G, red2, slot2);
-    if (a.dgate && on && lane == 0) a.dgate[t] = c1[1];
+    if (a.dgate && lane == 0) a.dgate[t] = c1[1];
     c1[0] *= inv_h;
     if (dy) {
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
         const int c = (lane + v * G) * 8;
-        if (!on || c >= H) continue;
+        if (c >= H) continue;
         if (w_post) {
           float fy[8];
           open8<T>(uy[v], fy);
@@ -668,7 +666,7 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : 512) norm_backward_kernel(co
     if (a.part && ++count == kFlush) put_sums();
   }
   if (a.part)
-    while (flush < a.flushes) put_sums();   // a group with fewer rows adds zeros
+    while (flush < a.flushes) put_sums();   // a block with fewer rows adds zeros
 }
 
 
@@ -701,7 +699,9 @@ __global__ void __launch_bounds__(VPT == 1 ? 896 : 512, 1) norm_backward_ring_ke
   T* dy = static_cast<T*>(a.dy);
   pdl_trigger();
   pdl_wait();
-  const bool feeds = pre || with_y || a.ds;   // else there is nothing to wait for
+  // (false without tokens alone, which need no ds or dh; with the conditions on it the compiler's
+  // order of the loop is the better one: 8192 x 7168 142 us, without them 144)
+  const bool feeds = pre || with_y || a.ds;
   if (m.tt == 0 && feeds) f.start(steps);
   stage_weights<T>(w1, w2, static_cast<const T*>(a.w_post),
                    a.kind == MOE_GATE_CHANNEL ? static_cast<const T*>(a.gate) : nullptr, static_cast<const T*>(a.w_pre),
@@ -957,12 +957,12 @@ RingShape ring_shape(int H, int esize, int streams, int wide, int threads, int t
 }
 
 // The backward's work split, the same on every device, so that a workspace's size
-// and the sums do not depend on it.  Rows in rings, at most kFlush a team; else (a row
-// too wide for them, or so few rows that a block has one) as they come.
+// and the sums do not depend on it.  Rows in rings, at most kFlush a team; those too wide for
+// one, a block each, as they come.
 struct Split {
   RingShape q;
   int steps;       // of a team
-  Geometry g;      // without rings
+  int G, vpt;      // without rings: threads, vectors of each
   int64_t blocks;
   int flushes;
 };
@@ -978,16 +978,14 @@ Split split_of(const NShape& s) {
     p.blocks = std::max<int64_t>(1, (rows + p.steps - 1) / p.steps);
     return p;
   }
-  p.g = geometry(s.H, 256);
-  const int threads = p.g.G * p.g.NG;
-  const int per_sm = threads > 512 ? 1 : 1024 / threads / 2 + 1;
-  p.blocks = std::min<int64_t>((s.T + p.g.NG - 1) / p.g.NG, 152ll * std::max(1, per_sm));
-  if (p.blocks < 1) p.blocks = 1;
-  const int64_t rows = (s.T + p.blocks * p.g.NG - 1) / (p.blocks * p.g.NG);   // of a group
-  p.flushes = (int)std::max<int64_t>(1, (rows + kFlush - 1) / kFlush);
+  const int vecs = s.H / 8;
+  p.vpt = s.dtype == MOE_F32 && vecs <= 1024 ? 2 : 4;
+  p.G = ((vecs + p.vpt - 1) / p.vpt + 31) / 32 * 32;
+  p.blocks = std::max<int64_t>(1, std::min<int64_t>(s.T, p.G > 512 ? 152 : 2 * 152));
+  p.flushes = (int)std::max<int64_t>(1, ((s.T + p.blocks - 1) / p.blocks + kFlush - 1) / kFlush);
   return p;
 }
-int64_t parts_of(const Split& p) { return p.q.depth > 0 ? p.blocks : (int64_t)p.flushes * p.blocks * p.g.NG; }
+int64_t parts_of(const Split& p) { return p.q.depth > 0 ? p.blocks : (int64_t)p.flushes * p.blocks; }
 size_t part_bytes(const NShape& s, const Split& p) { return (size_t)parts_of(p) * 2 * s.H * 4; }
 
 std::atomic<int64_t> g_wait{-1};   // moe_testing_set_norm_wait
@@ -1017,7 +1015,7 @@ cudaError_t forward(const NShape& s, const void* x, const void* y, const void* w
     };
     return q.vpt == 1 ? go(norm_forward_ring_kernel<T, 1>) : go(norm_forward_ring_kernel<T, 2>);
   }
-  const Geometry g = geometry(s.H, 512);
+  const Geometry g = geometry(s.H);
   const unsigned threads = (unsigned)(g.G * g.NG);
   const int64_t need = (s.T + g.NG - 1) / g.NG, cap = (int64_t)tc_sm_count() * std::max(1u, 2048 / threads);
   const unsigned grid = (unsigned)std::min(need, cap);
@@ -1047,13 +1045,10 @@ cudaError_t backward(const NShape& s, const Split& p, BwdArgs a, void* dw_post, 
     };
     e = p.q.vpt == 1 ? go(norm_backward_ring_kernel<T, 1>) : go(norm_backward_ring_kernel<T, 2>);
   } else {
-    const unsigned threads = (unsigned)(p.g.G * p.g.NG);
-    a.G = p.g.G;
-    a.NG = p.g.NG;
     a.flushes = p.flushes;
-    auto go = [&](auto kernel) { return launch_after(kernel, (unsigned)p.blocks, threads, 0, st, 1, a); };
-    e = p.g.vpt == 1 ? go(norm_backward_kernel<T, 1>)
-        : p.g.vpt == 2 ? go(norm_backward_kernel<T, 2>) : go(norm_backward_kernel<T, 4>);
+    auto go = [&](auto kernel) { return launch_after(kernel, (unsigned)p.blocks, (unsigned)p.G, 0, st, 1, a); };
+    if constexpr (sizeof(T) == 4) e = p.vpt == 2 ? go(norm_backward_kernel<T, 2>) : go(norm_backward_kernel<T, 4>);
+    else e = go(norm_backward_kernel<T, 4>);
   }
   if (e != cudaSuccess || !a.part) return e;
   return launch_after(norm_columns_kernel<T>, (unsigned)((2 * s.H + 31) / 32), 32 * kJoinWarps, 0, st, 1,

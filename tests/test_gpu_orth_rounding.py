@@ -100,3 +100,23 @@ def test_a_small_coefficient_between_large_ones(m, shape, rank, steps):
     want = exact(u, coefs)
     bound = (1.25 if rank is None else 1.5) * off(rounded(u, coefs), want)
     assert bool((off(got, want) <= bound).all()), (off(got, want) / bound).tolist()
+
+
+SHAPES = [(2, 200, 330), (3, 150, 400), (2, 400, 150), (1, 704, 2816), (1, 1030, 520), (1, 1024, 1024)]
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("rank", [None, 16])
+def test_five_steps(m, shape, rank):
+    """The default steps, against the model and in absolute terms.  Before its last rounding the
+    model is off by at most 1.85e-3 of the norm for normal entries over these shapes, by
+    1.1e-3 for rank 16; that rounding is uniform within half a step, 2^-9 to 2^-8 of a value,
+    so at most 2^-8 / sqrt(3) = 2.26e-3 of the norm.  Together 2.92e-3 and 2.51e-3, and a few
+    percent for the sums' order."""
+    u = draw(shape, rank, seed=sum(shape))
+    got = m.Orthogonalize(*shape).forward(u)
+    coefs = (S,) * 5
+    want = exact(u, coefs)
+    err = off(got, want)
+    assert bool((err <= (1.25 if rank is None else 1.5) * off(rounded(u, coefs), want)).all())
+    assert float(err.max()) <= (3.0e-3 if rank is None else 2.6e-3), err.tolist()

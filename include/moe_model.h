@@ -66,6 +66,9 @@ moe_status moe_embed_backward(const moe_embed_shape *shape, const int32_t *ids, 
  * token.  x is the residual stream, y the block's output (NULL: only the norm
  * before the next block), s the new residual stream, h the next block's input,
  * computed from s before its rounding.  All in fp32, each output rounded once.
+ * (moe_residual_setup of moe.h is the norm before a block too, to 2^-44 before its
+ * rounding: what decides near ties of a router as the exact norm would is that one; here an
+ * h may be the type's neighbouring value, and the routes those of the h that is fed.)
  * Rows are copied ahead under a bounded wait: where one never comes, the rows its block
  * had left become NaN, and the backward sets MOE_ERR_TIMEOUT (the forward, which has no
  * workspace, has no other sign).
@@ -128,7 +131,12 @@ moe_status moe_block_norm_backward(const moe_block_norm_shape *shape, const void
  * Where n >= 2 m the first two of three or more steps are taken as one polynomial in
  * A (its coefficients allowing).  fp32 matrices: X in two fp16 parts (22 bits), the
  * three products above 2^-22.  A smaller side of at most 128 (up to a length): X in
- * fp32 between the steps.  Sums in fp32.
+ * fp32 between the steps.  Sums in fp32.  So a returned bf16 direction is some 2.3e-3 of its
+ * norm off (its own rounding 1.7e-3 of it), an fp32 one 1e-6 to 5e-6.  Under the fixed power of
+ * two entries of X below 2^-27 (fp32 matrices: 2^-16) have fewer bits and below 2^-38 none:
+ * those of matrices far smaller than eps, and after steps that shrink singular values so far.
+ * Matrices with a smaller side of at most 128 take clusters of up to 16 CTAs; where a
+ * device or a part of one cannot hold those, the call returns MOE_ERR_CUDA.
  * ------------------------------------------------------------------------- */
 #define MOE_ORTH_MAX_STEPS 16
 
@@ -162,7 +170,8 @@ moe_status moe_orthogonalize(const moe_orth_shape *shape, const moe_orth_coefs *
  * size: 1 (MOE_MUON_SCALE_NONE), sqrt(max(1, rows / cols)) (_SPECTRAL) or
  * 0.2 sqrt(max(rows, cols)) (_RMS).  Each [rows, cols] matrix of a batch is
  * orthogonalised by itself; tensors whose smaller and larger sides agree share
- * their launches, whichever way round they are. */
+ * their launches, whichever way round they are.  The parameter's type decides the
+ * precision of its direction, whatever its gradient's is. */
 typedef enum { MOE_MUON_SCALE_NONE = 0, MOE_MUON_SCALE_SPECTRAL = 1, MOE_MUON_SCALE_RMS = 2 } moe_muon_scale;
 
 typedef struct {

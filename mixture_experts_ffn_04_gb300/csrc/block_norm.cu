@@ -5,8 +5,8 @@
 //
 // The forward reads two rows a token and writes two, the backward reads four and
 // writes two (s is not read back: from x and y it costs a few FMAs, and it has not been
-// rounded).  At 8192 rows of 7168 columns in bf16 that takes 80 us (470 MB, 5.9 TB/s: 87 % of
-// the rate of a copy) and 143 us (705 MB, 4.9 TB/s: 73 %), by the rings below; few rows are
+// rounded).  At 8192 rows of 7168 columns in bf16 that takes 74 us (470 MB, 6.4 TB/s: 94 % of
+// the rate of a copy) and 142 us (705 MB, 5.0 TB/s: 73 %), by the rings below; few rows are
 // bound by latency (one row of 2048: 4.5 us on the device).  1 / sqrt by rsqrtf, within two
 // units of fp32's last place: exactly rounded root and quotient, in every thread for its row,
 // cost 4 % of the forward.  A group of threads holds a whole row in
@@ -215,8 +215,8 @@ __global__ void __launch_bounds__(1024) norm_forward_kernel(int64_t rows, int H,
 // next rows are under way while this one's sums wait on each other; the weights
 // stand in shared memory.  Held in registers without the ring, a row's loads, two
 // row sums and stores followed one another: the forward at T = 4096, H = 2816 took 39 us
-// against 25, the backward at T = 8192, H = 7168 340 against 160.  x in registers a step
-// ahead instead of by the ring: 104 us against 84 at 8192 x 7168 forward.
+// (by the ring 25 then, 18 now), the backward at T = 8192, H = 7168 340 (160 then, 142 now).  x in
+// registers a step ahead instead of by the ring: 104 us at 8192 x 7168 forward (84 then, 74 now).
 // ---------------------------------------------------------------------------
 struct RingShape {
   int G;        // threads of a team (whole warps)
@@ -508,8 +508,10 @@ struct BwdArgs {
   uint32_t* flags;
 };
 
-// Rows too wide for a ring of two (fp32 from H = 5792, bf16 from 8200): a block a row, held in
-// registers.
+// Rows too wide for a ring of two steps beside the weights (fp32 from H = 5792, bf16 from 8200): a
+// block a row, held in registers, of which there are too few (four vectors a thread: 32, the rest
+// in local memory).  4096 rows: fp32 of 5784 columns by the ring 101 us, of 5792 185, of 7168 213; bf16
+// of 8192 by the ring 78 us, of 8200 947, of 16384 1214.
 template <typename T, int VPT>
 __global__ void __launch_bounds__(VPT == 4 ? 1024 : 512) norm_backward_kernel(const BwdArgs a) {
   __shared__ float red[2][1][kMaxWarps];
@@ -670,12 +672,11 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : 512) norm_backward_kernel(co
 }
 
 
-// Two vectors a thread in
-// 14 warps halve the instructions of the row sums, waits and addresses for each element: 160
-// us at 8192 x 7168 against 172 with one vector in 28 warps.  Nothing may spill: beside rings
-// that leave the L1 no room a spilled register is an access of L2 (72 registers with a few
-// spills: 195 to 270 us).  One barrier a row instead of three, by finishing dy a step later,
-// took as long.
+// Two vectors a thread in 14 warps halve the instructions of the row sums, waits and
+// addresses for each element: at 8192 x 7168 160 us when it was measured (142 now) against 172 with
+// one vector in 28 warps.  Nothing may spill: beside rings that leave the L1 no room a spilled
+// register is an access of L2 (72 registers with a few spills: 195 to 270 us).  One barrier a row
+// instead of three, by finishing dy a step later, took as long.
 template <typename T, int VPT>
 __global__ void __launch_bounds__(VPT == 1 ? 896 : 512, 1) norm_backward_ring_kernel(const BwdArgs a, const RingShape q,
                                                                                      int steps) {
@@ -917,8 +918,8 @@ moe_status decode(const moe_block_norm_shape* s, NShape* o, const char** why) {
 // Rings for rows of H columns, `streams` of them in and two fp32 weight vectors beside
 // them, one vector of 8 columns a thread up to `wide` vectors, at most `threads`
 // threads of an SM (two vectors: threads2): as many teams as fit with two steps in their
-// rings (three or four steps took as long or longer to start: the forward at 4096 x 2816 25 us
-// with two, 27 with three).  depth 0: none fits.
+// rings (three or four steps took as long or longer to start: the forward at 4096 x 2816 with
+// three 27 us, with two 25 then and 18 now).  depth 0: none fits.
 constexpr int kSmemBlock = 227 * 1024, kSmemSm = 228 * 1024;   // 1 KB of the latter goes with each block
 constexpr int kStatic = 512;                                    // what the kernels declare besides
 RingShape ring_shape(int H, int esize, int streams, int wide, int threads, int threads2) {

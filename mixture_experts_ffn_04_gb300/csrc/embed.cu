@@ -3,7 +3,7 @@
 //   y_t = scale w[id_t],   dw_v = dw_add_v + scale sum_{t : id_t = v} dy_t
 //
 // Both are bound by HBM: a lookup reads and writes a row a token (8192 tokens of 7168
-// columns in bf16 27 us; frequent rows come from L2), the gradient reads a row a token and writes
+// columns in bf16 29 us; frequent rows come from L2), the gradient reads a row a token and writes
 // (and, with dw_add elsewhere, reads) one a vocabulary entry: 4096 tokens, 131072 x 2048 in bf16 with
 // dw_add 191 us, of them 167 for the sums and the rows without tokens (1.09 GB, 6.5 TB/s);
 // 60001 tokens, 32001 x 1000 in fp32 113 us, of them 63 for the sums (368 MB, 5.8 TB/s) and

@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant_
       }
     }
   } else {
-    // ---------------- epilogue (warps 4..19, both CTAs) ----------------
+    // ---------------- epilogue (warps 4..11, both CTAs) ----------------
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(EPI_REGS));
     const int q = warp & 3;                 // TMEM lanes 32q .. 32q+31
     const int c_lo = (warp - 4) / 4 * EPI_COLS;

@@ -80,3 +80,27 @@ def test_rows_of_zeros_under_a_tiny_eps(T, H, dt, gate):
     for t in (s, h, d.dw_pre):
         assert bool(torch.isfinite(t).all())
     assert float(h[::2].abs().max()) == 0.0
+
+
+@pytest.mark.parametrize("T,V,H", [(300000, 5, 16), (60001, 300, 256), (9000, 40, 64), (64, 1, 264), (64, 3, 8)])
+def test_infinities_and_overflow_of_a_gradient_stay(T, V, H):
+    """An infinite term gives an infinite sum, one of each sign or a NaN give NaN, and finite terms whose
+    sum leaves the range its infinity; the other columns are as they were."""
+    g = torch.Generator(device="cuda").manual_seed(T + 1)
+    ids = torch.randint(0, V, (T,), generator=g, device="cuda", dtype=torch.int32)
+    dy = torch.rand((T, H), generator=g, device="cuda")
+    op = m.TokenEmbedding(T, H, V, dtype=torch.float32)
+    clean = op.backward(ids, dy)
+    row = int(ids[T // 2])
+    mine = (ids == row).nonzero()[:, 0]
+    dy[mine[len(mine) // 2], 1] = float("inf")
+    dy[mine[0], 2], dy[mine[-1], 2] = float("inf"), float("-inf")
+    dy[mine[-1], 3] = float("nan")
+    dy[mine, 4] = 3e38
+    got = op.backward(ids, dy)
+    several = len(mine) > 1
+    assert float(got[row, 1]) == float("inf") and bool(got[row, 3].isnan())
+    assert bool(got[row, 2].isnan()) if several else float(got[row, 2]) == float("-inf")
+    assert float(got[row, 4]) == (float("inf") if several else float(torch.tensor(3e38)))
+    clean[row, 1:5] = got[row, 1:5] = 0.0
+    assert torch.equal(got, clean)
